@@ -72,7 +72,7 @@ def draw(rng):
     if op.startswith("norm"):
         W = _log_int(rng, 16, 12000)
         R = _log_int(rng, 1, max(2, min(600000, 60_000_000 // W)))
-        if flag():
+        if flag() or W > 8000:
             W = -(-W // 8) * 8
         return dict(op=op, xdtype=rng.choice([dtype, "f32"]), dtype=dtype, R=R, W=W, rms=flag(), bias=flag(), gate=flag())
     G = rng.choice([1, 2, 4, 8])
