@@ -1,7 +1,7 @@
 /*
  * ssd.h -- C ABI of libssd.so, the gfx950 (MI355X) Mamba-2 SSD mixer core.
  *
- * Nine operations, each a few HIP kernel launches on the caller's stream:
+ * Fourteen operations, each a few HIP kernel launches on the caller's stream:
  *
  *   ssd_conv_fwd        causal depthwise conv (k = 4) + SiLU over the
  *                       [x | B | C] columns, and dt = softplus(dt_raw + dt_bias)
@@ -20,6 +20,11 @@
  *   ssd_chunk_scan_bwd  backward (VJP) of the scan for a zero-state prefill
  *   ssd_conv_bwd        backward of the conv prologue
  *   ssd_mixer_bwd       backward of conv + scan, recomputing the forward
+ *   ssd_delta_scan_fwd  the gated delta rule over a sequence, in chunks of 64
+ *   ssd_delta_step      one decode token of the gated delta rule per sequence
+ *   ssd_delta_scan_bwd  backward (VJP) of ssd_delta_scan_fwd
+ *   ssd_norm_fwd        layer or RMS norm of rows, with weight, bias and gate
+ *   ssd_norm_bwd        backward of ssd_norm_fwd, with the weights' reductions
  *
  * The operation (per batch row b and head h, token t, head h in group
  * g = h / (H/G)):
@@ -541,6 +546,104 @@ int ssd_mixer_bwd(int B, int L, int H, int P, int N, int G, int K, int chunk, in
 /* Bytes of workspace of ssd_mixer_bwd: the recomputed conv output (T) and dt,
  * the conv output's gradient (fp32), and the two backward calls' scratch. */
 size_t ssd_mixer_bwd_workspace_size(int B, int L, int H, int P, int N, int G, int dtype);
+
+/*
+ * The gated delta rule (ssd_delta_scan_fwd, ssd_delta_step,
+ * ssd_delta_scan_bwd) -- the other linear recurrence of hybrid language
+ * models, in the scan's conventions: per batch row b and head h (group
+ * g = h / (H/G)), with the state S_t [P][N]
+ *     a_t = exp(dt_t * A_h)
+ *     u_t = beta_t * (v_t - a_t * S_{t-1} k_t)
+ *     S_t = a_t * S_{t-1} + u_t k_t^T
+ *     y_t = scale * S_t q_t                              (S_t after token t)
+ * Its layer needs no other prologue: ssd_conv_fwd over [v | k | q] columns
+ * gives v, k, q and dt, and ssd_norm_fwd over y ends it.
+ *
+ *   q, k    T   [B][L][G*N] group-major, v T [B][L][H*P] head-major, row
+ *               strides in elements as in ssd_chunk_scan_fwd (column slices
+ *               of one ssd_conv_fwd output are fine)
+ *   dt      f32 [B][L][H], dt_softplus, dt_bias, A as in ssd_chunk_scan_fwd
+ *   beta    f32 [B][L][H]  row stride beta_row_stride; beta_sigmoid = 0: as
+ *               it is; 1: beta := sigmoid(beta)
+ *   scale   of the output (N^-0.5 is the usual choice)
+ *   qk_norm 1: every q and k row of N entries is first divided by
+ *               sqrt(sum of its squares + 1e-6); 0: taken as it is
+ *   doc_ids i32 [B][L] or NULL: a new document starts from a zero state, as
+ *               in ssd_chunk_scan_fwd
+ *   state   f32 [B][H][P][N]
+ *   y       T   [B][L][H*P], rounded once to T (the norm and the projection
+ *               behind it read T; the scan's y stays fp32 because its gate
+ *               and skip come first)
+ * All sums, decays and the state are held in fp32 or wider; bf16 inputs enter
+ * the products as they are, fp32 intermediates as bf16 pairs (hi + lo), fp32
+ * inputs on the fp32 MFMA.  Supported: P in {64, 128}, N in {32, 64, 128},
+ * chunk = 64, G divides H.  beta in [0, 2) with unit k keeps the recurrence
+ * stable; other values are computed as they are.
+ */
+
+/*
+ * ssd_delta_step -- one token for each of B sequences: the recurrence above
+ * at L = 1, the state read and updated in place.  It continues
+ * ssd_delta_scan_fwd's final_state as it is.
+ *   q, k    T   [B][G*N]   v, y T [B][H*P]   row strides in elements
+ *   dt, beta f32 [B][H]    row strides in elements
+ *   state   f32 [B][H][P][N]
+ * Deterministic and batch-invariant up to the choice of rows a thread takes,
+ * which changes no sum.
+ */
+int ssd_delta_step(int B, int H, int P, int N, int G, int dtype,
+                   const void *q, int64_t q_row_stride,
+                   const void *k, int64_t k_row_stride,
+                   const void *v, int64_t v_row_stride,
+                   const float *dt, int64_t dt_row_stride, int dt_softplus, const float *dt_bias,
+                   const float *A,
+                   const float *beta, int64_t beta_row_stride, int beta_sigmoid,
+                   float scale, int qk_norm,
+                   float *state, void *y, int64_t y_row_stride, void *stream);
+
+/*
+ * ssd_norm_fwd -- the norm of R rows of W columns:
+ *     rms = 0:  n = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
+ *     rms = 1:  n = x / sqrt(mean(x^2) + eps)
+ *     y = (n * weight + bias) * silu(z)
+ *   x       f32 or bf16 (x_dtype) [R][W], row stride x_row_stride
+ *   weight, bias  f32 [W] or NULL (1 and 0)
+ *   z       T   [R][W] or NULL (no gate)
+ *   y       T   [R][W] (dtype); must not be x or z
+ * The mixer's norm(y * silu(z)) is this without z on the scan's fp32 y; a
+ * gated norm of every head by itself is R = B*L*H rows of W = P columns.
+ * 1 <= W <= 16384; a W above 8192 needs 16-byte aligned bases and row strides
+ * and W % 8 == 0 (SSD_ERR_ALIGNMENT).  Otherwise any alignment of the element
+ * type will do; rows that meet those conditions are read in 16-byte pieces.
+ * Statistics are fp32, the variance from the centred row.
+ */
+int ssd_norm_fwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
+                 const void *x, int64_t x_row_stride, const float *weight, const float *bias,
+                 const void *z, int64_t z_row_stride,
+                 void *y, int64_t y_row_stride, void *stream);
+
+/*
+ * ssd_norm_bwd -- backward of ssd_norm_fwd: with g = grad_y * silu(z),
+ *     dweight = sum_rows g n,  dbias = sum_rows g,  dz = grad_y (n weight + bias) silu'(z)
+ *     dx = (g weight - mean(g weight) - n mean(g weight n)) / sqrt(...)   (rms: no mean(g weight))
+ * The statistics are computed again from x.
+ *   grad_y  T   [R][W];  dx x_dtype [R][W];  dz T [R][W] or NULL (only with z)
+ *   dweight, dbias  f32 [W] or NULL.  Their sums over the rows are taken in a
+ *               fixed order (deterministic) through the workspace:
+ *               ssd_norm_bwd_workspace_size() bytes, 16-byte aligned,
+ *               required where dweight or dbias is given.
+ * R = 0 writes zero dweight and dbias.
+ */
+int ssd_norm_bwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
+                 const void *x, int64_t x_row_stride, const float *weight, const float *bias,
+                 const void *z, int64_t z_row_stride,
+                 const void *grad_y, int64_t grad_y_row_stride,
+                 void *dx, int64_t dx_row_stride, float *dweight, float *dbias,
+                 void *dz, int64_t dz_row_stride,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of ssd_norm_bwd: one fp32 row pair for every workgroup. */
+size_t ssd_norm_bwd_workspace_size(int64_t R, int W);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,11 @@ The entry points mirror the C ABI in include/ssd.h one to one:
     ssd_chunk_scan_bwd  backward (VJP) of the scan for a zero-state prefill
     ssd_conv_bwd        backward of the conv prologue
     ssd_mixer_bwd       backward of conv + scan
+    ssd_delta_scan_fwd  the gated delta rule over a sequence (chunks of 64)
+    ssd_delta_step      one decode token of the gated delta rule per sequence
+    ssd_delta_scan_bwd  backward (VJP) of the gated delta rule
+    ssd_norm_fwd        layer or RMS norm of rows, with weight, bias and a silu gate
+    ssd_norm_bwd        its backward, with the weights' reductions
 
 This module only marshals torch tensors (device pointers, row strides, the
 current HIP stream) into the library; every step of the computation runs in
@@ -30,6 +35,7 @@ __all__ = ["load", "ssd_conv_fwd", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_sta
            "ssd_s6_scan_fwd", "ssd_chunk_scan_workspace_size", "ssd_mixer_workspace_size", "ssd_s6_workspace_size",
            "ssd_chunk_scan_bwd", "ssd_conv_bwd", "ssd_mixer_bwd", "ssd_chunk_scan_bwd_workspace_size",
            "ssd_conv_bwd_workspace_size", "ssd_mixer_bwd_workspace_size",
+           "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
            "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_ACT_SILU", "SSD_ACT_NONE"]
 
 # SSD_LIBRARY names another build of the same library (the host-sanitized one the ABI checks use)
@@ -100,6 +106,17 @@ def load() -> ctypes.CDLL:
     for nm in ("ssd_chunk_scan_bwd_workspace_size", "ssd_conv_bwd_workspace_size", "ssd_mixer_bwd_workspace_size"):
         getattr(lib, nm).restype = SZ
         getattr(lib, nm).argtypes = [I, I, I, I, I, I, I]
+    F = ctypes.c_float
+    # q, k, v, dt (softplus, bias), A, beta (sigmoid), scale, qk_norm: the shared head of the delta calls
+    delta = [P, I64, P, I64, P, I64, P, I64, I, P, P, P, I64, I, F, I]
+    lib.ssd_delta_step.restype = I
+    lib.ssd_delta_step.argtypes = [I, I, I, I, I, I, *delta, P, P, I64, P]
+    lib.ssd_norm_fwd.restype = I
+    lib.ssd_norm_fwd.argtypes = [I64, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P]
+    lib.ssd_norm_bwd.restype = I
+    lib.ssd_norm_bwd.argtypes = [I64, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P, I64, P, P, P, I64, P, SZ, P]
+    lib.ssd_norm_bwd_workspace_size.restype = SZ
+    lib.ssd_norm_bwd_workspace_size.argtypes = [I64, I]
     lib.ssd_s6_workspace_size.restype = SZ
     lib.ssd_s6_workspace_size.argtypes = [I, I, I, I, I]
     _lib = lib
@@ -554,3 +571,145 @@ def ssd_mixer_bwd(xbc_raw, dt_raw, conv_w, A, grad_y, *, H, P, N, G, K=4, conv_b
         ws.numel() * ws.element_size(), _stream(stream))
     _check(st)
     return {k: v for k, v in g.items() if v is not None}
+
+
+# ---- the gated delta rule and the row norm.  These calls run on the inputs' own GPU, whichever is current.
+class _Call:
+    """The device and the tensor checks of one call: every tensor has to be on `x`'s GPU."""
+
+    __slots__ = ("dev", "index")
+
+    def __init__(self, x, name):
+        _ptr(x, name)
+        self.dev = x.device
+        self.index = x.device.index
+
+    def ptr(self, t, name, dtype=None):
+        if t is None:
+            return None
+        p = _ptr(t, name, dtype)
+        if t.device != self.dev:
+            raise ValueError(f"{name}: on {t.device}, expected {self.dev} as the first input")
+        return p
+
+    def vec(self, t, name, dtype, shape):
+        _contig(t, name, shape)
+        return self.ptr(t, name, dtype)
+
+    def rows(self, t, name, dtype, shape):
+        """(pointer, row stride) of a tensor of `shape`, its rows a uniform number of elements apart."""
+        if t is None:
+            return None, 0
+        p = self.ptr(t, name, dtype)
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+        if t.is_contiguous():
+            return p, shape[-1]
+        if t.stride(-1) != 1 and shape[-1] > 1:
+            raise ValueError(f"{name}: the innermost dimension must be contiguous")
+        # the row index runs over the leading dimensions: those of more than one entry must nest
+        rs, step = None, 1
+        for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+            if n == 1:
+                continue
+            if rs is None:
+                rs = st
+            elif st != rs * step:
+                raise ValueError(f"{name}: batch rows must be L * row_stride elements apart")
+            step *= n
+        # a single row: any stride that holds it and keeps the alignment
+        return p, (-(-shape[-1] // 8) * 8 if rs is None else rs)
+
+    def run(self, fn, args, stream):
+        """fn(*args, stream) on the tensors' device."""
+        if stream is not None:
+            stream = _stream(stream)
+        elif self.index == torch.cuda.current_device():
+            stream = torch.cuda.current_stream().cuda_stream
+        if self.index == torch.cuda.current_device():
+            _check(fn(*args, stream))
+            return
+        with torch.cuda.device(self.dev):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream))
+
+
+def _delta_head(c, lead, T, q, k, v, dt, A, beta, H, P, N, G, scale, qk_norm, dt_softplus, dt_bias, beta_sigmoid):
+    """The arguments that the delta calls share; lead: the dimensions before the columns, (B, L) or (B,)."""
+    qp, qs = c.rows(q, "q", T, lead + (G * N,))
+    kp, ks = c.rows(k, "k", T, lead + (G * N,))
+    vp, vs = c.rows(v, "v", T, lead + (H * P,))
+    dp, ds = c.rows(dt, "dt", torch.float32, lead + (H,))
+    bp, bs = c.rows(beta, "beta", torch.float32, lead + (H,))
+    return [qp, qs, kp, ks, vp, vs, dp, ds, int(bool(dt_softplus)), c.vec(dt_bias, "dt_bias", torch.float32, (H,)),
+            c.vec(A, "A", torch.float32, (H,)), bp, bs, int(bool(beta_sigmoid)),
+            N ** -0.5 if scale is None else float(scale), int(bool(qk_norm))]
+
+
+def ssd_delta_step(q, k, v, dt, A, beta, state, *, H, P, N, G, scale=None, qk_norm=False, dt_softplus=False,
+                   dt_bias=None, beta_sigmoid=False, y=None, stream=None):
+    """One token of the gated delta rule.  q, k [B, G*N], v [B, H*P] (one dtype), dt, beta [B, H] fp32, A [H] fp32;
+    state [B, H, P, N] fp32 is updated in place.  scale: N^-0.5 if None.  Returns y [B, H*P] in q's dtype."""
+    lib = load()
+    c = _Call(q, "q")
+    dtype = _dtype_code(q, "q")
+    B, T = q.shape[0], q.dtype
+    head = _delta_head(c, (B,), T, q, k, v, dt, A, beta, H, P, N, G, scale, qk_norm, dt_softplus, dt_bias, beta_sigmoid)
+    if y is None:
+        y = torch.empty((B, H * P), dtype=T, device=c.dev)
+    yp, ys = c.rows(y, "y", T, (B, H * P))
+    c.run(lib.ssd_delta_step, (B, H, P, N, G, dtype, *head, c.vec(state, "state", torch.float32, (B, H, P, N)), yp, ys),
+          stream)
+    return y
+
+
+def ssd_norm_fwd(x, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, out_dtype=None, y=None, stream=None):
+    """Norm of x's rows (its last dimension), times weight plus bias, times silu(z).  x fp32 or bf16; weight, bias
+    fp32 [W]; z in the output's dtype, which is y's, else out_dtype, else z's, else x's.  Returns y."""
+    lib = load()
+    c = _Call(x, "x")
+    shape, W = x.shape, x.shape[-1]
+    T = y.dtype if y is not None else out_dtype or (x.dtype if z is None else z.dtype)
+    if y is None:
+        y = torch.empty(shape, dtype=T, device=c.dev)
+    xp, xs = c.rows(x, "x", None, shape)
+    zp, zs = c.rows(z, "z", T, shape)
+    yp, ys = c.rows(y, "y", T, shape)
+    c.run(lib.ssd_norm_fwd, (x.numel() // W if W else 0, W, _dtype_code(x, "x"), _dtype_code(y, "y"), int(bool(rms)),
+                             float(eps), xp, xs, c.vec(weight, "weight", torch.float32, (W,)),
+                             c.vec(bias, "bias", torch.float32, (W,)), zp, zs, yp, ys), stream)
+    return y
+
+
+def ssd_norm_bwd_workspace_size(R, W) -> int:
+    return int(load().ssd_norm_bwd_workspace_size(R, W))
+
+
+def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, workspace=None, stream=None):
+    """Backward of ssd_norm_fwd; grad_y (and z) in the output's dtype.  Returns a dict: x in x's dtype, weight and
+    bias fp32 [W] and z in z's dtype, where those inputs are given.  A workspace is allocated here when none is
+    passed."""
+    lib = load()
+    c = _Call(x, "x")
+    shape, W, T = x.shape, x.shape[-1], grad_y.dtype
+    R = x.numel() // W if W else 0
+    f32 = dict(dtype=torch.float32, device=c.dev)
+    g = {"x": torch.empty(shape, dtype=x.dtype, device=c.dev)}
+    if weight is not None:
+        g["weight"] = torch.empty(W, **f32)
+    if bias is not None:
+        g["bias"] = torch.empty(W, **f32)
+    if z is not None:
+        g["z"] = torch.empty(shape, dtype=T, device=c.dev)
+    ws, nb = None, 0
+    if weight is not None or bias is not None:
+        ws = _ws(workspace, ssd_norm_bwd_workspace_size(R, W), c.dev)
+        nb = ws.numel() * ws.element_size()
+    xp, xs = c.rows(x, "x", None, shape)
+    zp, zs = c.rows(z, "z", T, shape)
+    gp, gs = c.rows(grad_y, "grad_y", T, shape)
+    out = lambda n: g[n].data_ptr() if n in g else None  # noqa: E731
+    c.run(lib.ssd_norm_bwd, (R, W, _dtype_code(x, "x"), _dtype_code(grad_y, "grad_y"), int(bool(rms)), float(eps), xp,
+                             xs, c.vec(weight, "weight", torch.float32, (W,)), c.vec(bias, "bias", torch.float32, (W,)),
+                             zp, zs, gp, gs, out("x"), W, out("weight"), out("bias"), out("z"), W,
+                             c.ptr(ws, "workspace"), nb), stream)
+    return g

@@ -964,4 +964,200 @@ int ssd_step(int B, int H, int P, int N, int G, int K, int dtype,
     return hip_status(fn, ssd::launch_step(a, static_cast<hipStream_t>(stream)));
 }
 
+// ---- the gated delta rule: sizes and arguments that its three calls share
+static int check_delta(const char* fn, ssd::DeltaArgs& a, bool work) {
+    if (a.dtype != SSD_F32 && a.dtype != SSD_BF16)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: dtype=%d is not supported (only SSD_F32=0 and SSD_BF16=1; "
+                    "fp16, fp64 and other types are refused, not converted)", fn, a.dtype);
+    if (a.B < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: B=%d must be >= 0", fn, a.B);
+    if (a.L < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: L=%d must be >= 0", fn, a.L);
+    if (a.L > kMaxL) return fail(SSD_ERR_BAD_SHAPE, "%s: L=%d is above the %d tokens a row may hold", fn, a.L, kMaxL);
+    if (a.H <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: H=%d must be > 0", fn, a.H);
+    if (a.G <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: G=%d must be > 0", fn, a.G);
+    if (a.H % a.G != 0) return fail(SSD_ERR_BAD_SHAPE, "%s: H=%d is not divisible by G=%d", fn, a.H, a.G);
+    if (a.P != 64 && a.P != 128)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: P=%d is not supported (head dim must be 64 or 128)", fn, a.P);
+    if (a.N != 32 && a.N != 64 && a.N != 128)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: N=%d is not supported (state dim must be 32, 64 or 128)", fn, a.N);
+    // the grids: a workgroup for every chunk of every head, and up to 16 for a head's step
+    const long long units = (long long)a.B * a.H * std::max(16LL, ((long long)a.L + 63) / 64);
+    if (units > 0x7fffffffLL)
+        return fail(SSD_ERR_BAD_SHAPE, "%s: B*H*max(16, L/64)=%lld is too large", fn, units);
+    if (a.dt_softplus != 0 && a.dt_softplus != 1)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: dt_softplus=%d must be 0 or 1", fn, a.dt_softplus);
+    if (a.beta_sigmoid != 0 && a.beta_sigmoid != 1)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: beta_sigmoid=%d must be 0 or 1", fn, a.beta_sigmoid);
+    if (a.qk_norm != 0 && a.qk_norm != 1)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: qk_norm=%d must be 0 or 1", fn, a.qk_norm);
+    const int es = esize(a.dtype);
+    const int64_t HP = (int64_t)a.H * a.P, GN = (int64_t)a.G * a.N;
+    TRY(check_tensor(fn, "q", a.q, a.q_stride, GN, es, work));
+    TRY(check_tensor(fn, "k", a.k, a.k_stride, GN, es, work));
+    TRY(check_tensor(fn, "v", a.v, a.v_stride, HP, es, work));
+    if (work) {
+        if (!a.dt) return fail(SSD_ERR_NULL_ARG, "%s: dt is NULL", fn);
+        if (!a.beta) return fail(SSD_ERR_NULL_ARG, "%s: beta is NULL", fn);
+        if (a.dt_stride < a.H || a.beta_stride < a.H)
+            return fail(SSD_ERR_BAD_SHAPE, "%s: dt / beta row strides (%lld, %lld) are smaller than H=%d", fn,
+                        (long long)a.dt_stride, (long long)a.beta_stride, a.H);
+        if (a.q_stride > (1 << 22) || a.k_stride > (1 << 22) || a.v_stride > (1 << 22) || a.y_stride > (1 << 22) ||
+            a.dt_stride > (1 << 22) || a.beta_stride > (1 << 22))
+            return fail(SSD_ERR_BAD_SHAPE, "%s: row strides above 4194304 elements are not supported", fn);
+    }
+    TRY(check_ptr(fn, "dt", a.dt, false, false));
+    TRY(check_ptr(fn, "beta", a.beta, false, false));
+    TRY(check_ptr(fn, "dt_bias", a.dt_bias, false, false));
+    TRY(check_ptr(fn, "A", a.A, a.B > 0, false));
+    TRY(check_ptr(fn, "doc_ids", a.doc, false, false));
+    TRY(check_ptr(fn, "lengths", a.lengths, false, false));
+    return SSD_OK;
+}
+
+static ssd::DeltaArgs delta_args(int B, int L, int H, int P, int N, int G, int dtype, const void* q, int64_t q_stride,
+                                 const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* dt,
+                                 int64_t dt_stride, int dt_softplus, const float* dt_bias, const float* A,
+                                 const float* beta, int64_t beta_stride, int beta_sigmoid, float scale, int qk_norm) {
+    ssd::DeltaArgs a{};
+    a.B = B; a.L = L; a.H = H; a.P = P; a.N = N; a.G = G; a.dtype = dtype;
+    a.q = q; a.q_stride = q_stride;
+    a.k = k; a.k_stride = k_stride;
+    a.v = v; a.v_stride = v_stride;
+    a.dt = dt; a.dt_stride = dt_stride;
+    a.dt_softplus = dt_softplus; a.dt_bias = dt_softplus ? dt_bias : nullptr;
+    a.A = A;
+    a.beta = beta; a.beta_stride = beta_stride;
+    a.beta_sigmoid = beta_sigmoid; a.scale = scale; a.qk_norm = qk_norm;
+    return a;
+}
+
+int ssd_delta_step(int B, int H, int P, int N, int G, int dtype,
+                   const void* q, int64_t q_row_stride,
+                   const void* k, int64_t k_row_stride,
+                   const void* v, int64_t v_row_stride,
+                   const float* dt, int64_t dt_row_stride, int dt_softplus, const float* dt_bias,
+                   const float* A,
+                   const float* beta, int64_t beta_row_stride, int beta_sigmoid,
+                   float scale, int qk_norm,
+                   float* state, void* y, int64_t y_row_stride, void* stream) {
+    const char* fn = "ssd_delta_step";
+    ssd::DeltaArgs a = delta_args(B, 1, H, P, N, G, dtype, q, q_row_stride, k, k_row_stride, v, v_row_stride, dt,
+                                  dt_row_stride, dt_softplus, dt_bias, A, beta, beta_row_stride, beta_sigmoid, scale,
+                                  qk_norm);
+    a.final_state = state;
+    a.y = y; a.y_stride = y_row_stride;
+    const bool work = B > 0;
+    TRY(check_delta(fn, a, work));
+    TRY(check_tensor(fn, "y", y, y_row_stride, (int64_t)H * P, esize(dtype), work));
+    TRY(check_ptr(fn, "state", state, work, true));
+    if (!work) return ok();
+    if (y == state || y == v || y == q || y == k)
+        return fail(SSD_ERR_BAD_SHAPE, "%s: y must not alias an input or the state", fn);
+    return hip_status(fn, ssd::launch_delta_step(a, static_cast<hipStream_t>(stream)));
+}
+
+// ---- the row norm
+static int check_norm(const char* fn, ssd::NormArgs& a, bool bwd) {
+    for (int d : {a.x_dtype, a.dtype})
+        if (d != SSD_F32 && d != SSD_BF16)
+            return fail(SSD_ERR_UNSUPPORTED, "%s: dtype=%d is not supported (only SSD_F32=0 and SSD_BF16=1; "
+                        "fp16, fp64 and other types are refused, not converted)", fn, d);
+    if (a.R < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: R=%lld must be >= 0", fn, (long long)a.R);
+    if (a.R > 0x7fffffffLL) return fail(SSD_ERR_BAD_SHAPE, "%s: R=%lld is too large", fn, (long long)a.R);
+    if (a.W <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: W=%d must be > 0", fn, a.W);
+    if (a.W > 16384) return fail(SSD_ERR_UNSUPPORTED, "%s: W=%d is not supported (at most 16384 columns)", fn, a.W);
+    if (a.rms != 0 && a.rms != 1) return fail(SSD_ERR_UNSUPPORTED, "%s: rms=%d must be 0 or 1", fn, a.rms);
+    if (!(a.eps >= 0.0f)) return fail(SSD_ERR_UNSUPPORTED, "%s: eps=%g must be >= 0", fn, (double)a.eps);
+    const bool work = a.R > 0;
+    const int xe = esize(a.x_dtype), te = esize(a.dtype);
+    a.vec = a.W % 8 == 0;
+    struct Row { const char* name; const void* p; int64_t stride; int es; bool required; };
+    const Row rows[] = {
+        {"x", a.x, a.x_stride, xe, work}, {"z", a.z, a.z_stride, te, false}, {"y", a.y, a.y_stride, te, work && !bwd},
+        {"grad_y", a.gy, a.gy_stride, te, work && bwd}, {"dx", a.dx, a.dx_stride, xe, work && bwd},
+        {"dz", a.dz, a.dz_stride, te, false}};
+    for (const Row& r : rows) {
+        if (!r.p) {
+            if (r.required) return fail(SSD_ERR_NULL_ARG, "%s: %s is NULL", fn, r.name);
+            continue;
+        }
+        if (r.stride < a.W)
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is smaller than the row width %d", fn, r.name,
+                        (long long)r.stride, a.W);
+        if (r.stride > (1 << 22))
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is above 4194304 elements", fn, r.name,
+                        (long long)r.stride);
+        if (reinterpret_cast<uintptr_t>(r.p) % r.es)
+            return fail(SSD_ERR_ALIGNMENT, "%s: %s=%p is not aligned to its elements", fn, r.name, r.p);
+        if (!aligned16(r.p) || r.stride * r.es % 16) a.vec = 0;
+    }
+    if (!a.vec && a.W > 8192)
+        return fail(SSD_ERR_ALIGNMENT, "%s: W=%d above 8192 needs W %% 8 == 0 and 16-byte aligned rows", fn, a.W);
+    TRY(check_ptr(fn, "weight", a.w, false, false));
+    TRY(check_ptr(fn, "bias", a.b, false, false));
+    return SSD_OK;
+}
+
+int ssd_norm_fwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
+                 const void* x, int64_t x_row_stride, const float* weight, const float* bias,
+                 const void* z, int64_t z_row_stride,
+                 void* y, int64_t y_row_stride, void* stream) {
+    const char* fn = "ssd_norm_fwd";
+    ssd::NormArgs a{};
+    a.R = R; a.W = W; a.x_dtype = x_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
+    a.x = x; a.x_stride = x_row_stride;
+    a.w = weight; a.b = bias;
+    a.z = z; a.z_stride = z_row_stride;
+    a.y = y; a.y_stride = y_row_stride;
+    TRY(check_norm(fn, a, false));
+    if (R == 0) return ok();
+    if (y == x || y == z) return fail(SSD_ERR_BAD_SHAPE, "%s: y must not alias x or z", fn);
+    return hip_status(fn, ssd::launch_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_norm_bwd_workspace_size(int64_t R, int W) {
+    if (R <= 0 || W <= 0) return 0;
+    return ssd::norm_bwd_workspace_bytes(R, W);
+}
+
+int ssd_norm_bwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
+                 const void* x, int64_t x_row_stride, const float* weight, const float* bias,
+                 const void* z, int64_t z_row_stride,
+                 const void* grad_y, int64_t grad_y_row_stride,
+                 void* dx, int64_t dx_row_stride, float* dweight, float* dbias,
+                 void* dz, int64_t dz_row_stride,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssd_norm_bwd";
+    ssd::NormArgs a{};
+    a.R = R; a.W = W; a.x_dtype = x_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
+    a.x = x; a.x_stride = x_row_stride;
+    a.w = weight; a.b = bias;
+    a.z = z; a.z_stride = z_row_stride;
+    a.gy = grad_y; a.gy_stride = grad_y_row_stride;
+    a.dx = dx; a.dx_stride = dx_row_stride;
+    a.dz = dz; a.dz_stride = dz_row_stride;
+    a.dw = dweight; a.db = dbias;
+    TRY(check_norm(fn, a, true));
+    if (dz && !z) return fail(SSD_ERR_NULL_ARG, "%s: dz is given but z is NULL", fn);
+    TRY(check_ptr(fn, "dweight", dweight, false, false));
+    TRY(check_ptr(fn, "dbias", dbias, false, false));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (R == 0) {
+        TRY(hip_status(fn, ssd::launch_zero_f32(dweight, (size_t)W, s)));
+        TRY(hip_status(fn, ssd::launch_zero_f32(dbias, (size_t)W, s)));
+        return ok();
+    }
+    if (dx == x || dx == grad_y || dx == z || (dz && (dz == x || dz == grad_y || dz == z || dz == dx)))
+        return fail(SSD_ERR_BAD_SHAPE, "%s: dx and dz must not alias an input or each other", fn);
+    if (dweight || dbias) {
+        const size_t need = ssd_norm_bwd_workspace_size(R, W);
+        if (!workspace || workspace_bytes < need)
+            return fail(SSD_ERR_WORKSPACE, "%s: workspace_bytes=%zu is smaller than the required %zu", fn,
+                        workspace ? workspace_bytes : (size_t)0, need);
+        if (!aligned16(workspace))
+            return fail(SSD_ERR_ALIGNMENT, "%s: workspace=%p is not 16-byte aligned", fn, workspace);
+        a.part = static_cast<float*>(workspace);
+    }
+    return hip_status(fn, ssd::launch_norm(a, s));
+}
+
 }  // extern "C"

@@ -9,6 +9,7 @@
 namespace ssd {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kQkEps = 1e-6f;    // under the root of the delta rule's q and k normalisation
 
 // ---------------------------------------------------------------- bf16
 // bf16 is the top half of an fp32 bit pattern.  Widening is exact (a shift);
@@ -100,6 +101,32 @@ __device__ __forceinline__ void wave_segscan(float& v, int f, int& s) {
     segscan_step<0x118, 0xF>(v, f, s);
     segscan_step<0x142, 0xA>(v, f, s);
     segscan_step<0x143, 0xC>(v, f, s);
+}
+
+// ---------------------------------------------------------------- lane-group sums
+template <int CTRL>
+__device__ __forceinline__ float dpp_plus(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+// Every lane of an aligned group of W lanes (a power of two, 4..64) ends with
+// the group's sum: DPP moves within 16 lanes; across them the gfx950 row and
+// half swaps, which leave (own, other) rows in the two results.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+    static_assert(W >= 4 && W <= 64 && (W & (W - 1)) == 0, "group width");
+    v = dpp_plus<0xB1>(v);                    // quad_perm [1,0,3,2]
+    v = dpp_plus<0x4E>(v);                    // quad_perm [2,3,0,1]
+    if (W >= 8) v = dpp_plus<0x141>(v);       // row_half_mirror
+    if (W >= 16) v = dpp_plus<0x140>(v);      // row_mirror
+    if (W >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if (W >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return v;
 }
 
 // ---------------------------------------------------------------- split operands

@@ -132,6 +132,43 @@ struct ConvBwdArgs {
     float* part;                           // [B * ntc][C][5] per-chunk partial sums of dw and dbias
 };
 
+// Row norm over R rows of W columns (forward: gy = null).
+struct NormArgs {
+    int64_t R;
+    int W, x_dtype, dtype, rms;
+    int vec;                               // rows start on 16-byte boundaries and W % 8 == 0
+    float eps;
+    const void* x; int64_t x_stride;       // x_dtype
+    const float* w; const float* b;        // [W] or null
+    const void* z; int64_t z_stride;       // dtype, or null
+    void* y; int64_t y_stride;             // dtype
+    // backward
+    const void* gy; int64_t gy_stride;     // dtype
+    void* dx; int64_t dx_stride;           // x_dtype
+    void* dz; int64_t dz_stride;           // dtype, or null
+    float* dw; float* db;                  // [W] or null
+    float* part;                           // [workgroups][2][W], null when neither dw nor db is asked for
+};
+// workgroups of the two passes at most: 8 and 4 of 256 threads on every CU
+constexpr int kNormGrid = 2048, kNormBwdGrid = 1024;
+
+// Gated delta rule.  Head h reads group h / (H / G) of q and k.
+struct DeltaArgs {
+    int B, L, H, P, N, G, dtype;
+    const void* q; int64_t q_stride;       // [B][L][G*N] (dtype)
+    const void* k; int64_t k_stride;
+    const void* v; int64_t v_stride;       // [B][L][H*P] (dtype)
+    const float* dt; int64_t dt_stride;    // [B][L][H]
+    int dt_softplus; const float* dt_bias;
+    const float* A;
+    const float* beta; int64_t beta_stride;
+    int beta_sigmoid, qk_norm;
+    float scale;
+    const int32_t* doc; const int32_t* lengths;
+    const float* init_state; float* final_state;   // [B][H][P][N]; the step updates final_state in place
+    void* y; int64_t y_stride;             // [B][L][H*P] (dtype)
+};
+
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_scan(const ScanArgs& a, hipStream_t stream);
 // Sequence split chosen for these sizes (1 = none) and its superchunk length.
@@ -165,6 +202,9 @@ size_t conv_bwd_workspace_bytes(int B, int L, int C);
 // Zero fill of n floats by a kernel (no memset node).
 hipError_t launch_zero_f32(float* p, size_t n, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t stream);
+hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+size_t norm_bwd_workspace_bytes(int64_t R, int W);
 void s6_split(int B, int L, int D, int& K, int& S);
 size_t s6_workspace_bytes(int B, int L, int D, int N);
 
