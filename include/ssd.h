@@ -582,6 +582,45 @@ size_t ssd_mixer_bwd_workspace_size(int B, int L, int H, int P, int N, int G, in
  */
 
 /*
+ * ssd_delta_scan_fwd -- the recurrence over [B][L] tokens, in chunks of 64.
+ *
+ *   lengths i32 [B] or NULL: row b is real at t < lengths[b] (read on the
+ *               device, clamped to [0, L]).  y is exactly 0 behind it, and the
+ *               state stops there: final_state is the state after lengths[b]
+ *               tokens.  Inputs behind it are not used, NaN and Inf included.
+ *   init_state  f32 [B][H][P][N] or NULL (zero)
+ *   final_state f32 [B][H][P][N] or NULL; may equal init_state (in place)
+ *   y       T   [B][L][H*P]  row stride y_row_stride; must not overlap inputs
+ *   workspace, workspace_bytes: required, at least
+ *               ssd_delta_scan_workspace_size() bytes, 16-byte aligned,
+ *               caller-owned, not shared by concurrent calls
+ * Within a chunk, with G_t the running sum of dt A and M_tj = exp(G_t - G_j),
+ *     T = (I + strictly_lower(beta_t M_tj k_t.k_j))^-1
+ *     U = T (beta (V - e^G K S)),  Y = scale (e^G Q S + (M o Q K^T) U),
+ *     S' = e^{G_C} S + (e^{G_C - G} K)^T U
+ * A first launch computes T and M o Q K^T of all chunks; a second passes the
+ * state from chunk to chunk, held on chip.  Chunks are counted from t = 0, so
+ * a prefill split at a multiple of 64 tokens with the state carried is
+ * bitwise identical to one call.  L = 0 copies the state through.
+ */
+int ssd_delta_scan_fwd(int B, int L, int H, int P, int N, int G, int chunk, int dtype,
+                       const void *q, int64_t q_row_stride,
+                       const void *k, int64_t k_row_stride,
+                       const void *v, int64_t v_row_stride,
+                       const float *dt, int64_t dt_row_stride, int dt_softplus, const float *dt_bias,
+                       const float *A,
+                       const float *beta, int64_t beta_row_stride, int beta_sigmoid,
+                       float scale, int qk_norm,
+                       const int32_t *doc_ids, const int32_t *lengths,
+                       const float *init_state, float *final_state,
+                       void *y, int64_t y_row_stride,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of ssd_delta_scan_fwd: T, M o Q K^T and the decays of
+ * every chunk and head. */
+size_t ssd_delta_scan_workspace_size(int B, int L, int H, int P, int N, int G, int dtype);
+
+/*
  * ssd_delta_step -- one token for each of B sequences: the recurrence above
  * at L = 1, the state read and updated in place.  It continues
  * ssd_delta_scan_fwd's final_state as it is.
@@ -602,22 +641,23 @@ int ssd_delta_step(int B, int H, int P, int N, int G, int dtype,
                    float *state, void *y, int64_t y_row_stride, void *stream);
 
 /*
- * ssd_norm_fwd -- the norm of R rows of W columns:
+ * ssd_norm_fwd -- the norm of R rows of `groups` times W columns, every group
+ * of W columns by itself (groups = 1: the whole row; groups = H, W = P: every
+ * head of a token's row):
  *     rms = 0:  n = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
  *     rms = 1:  n = x / sqrt(mean(x^2) + eps)
  *     y = (n * weight + bias) * silu(z)
- *   x       f32 or bf16 (x_dtype) [R][W], row stride x_row_stride
- *   weight, bias  f32 [W] or NULL (1 and 0)
- *   z       T   [R][W] or NULL (no gate)
- *   y       T   [R][W] (dtype); must not be x or z
- * The mixer's norm(y * silu(z)) is this without z on the scan's fp32 y; a
- * gated norm of every head by itself is R = B*L*H rows of W = P columns.
+ *   x       f32 or bf16 (x_dtype) [R][groups*W], row stride x_row_stride
+ *   weight, bias  f32 [W] or NULL (1 and 0), the same for every group
+ *   z       T   [R][groups*W] or NULL (no gate)
+ *   y       T   [R][groups*W] (dtype); must not be x or z
+ * The mixer's norm(y * silu(z)) is this without z on the scan's fp32 y.
  * 1 <= W <= 16384; a W above 8192 needs 16-byte aligned bases and row strides
  * and W % 8 == 0 (SSD_ERR_ALIGNMENT).  Otherwise any alignment of the element
  * type will do; rows that meet those conditions are read in 16-byte pieces.
  * Statistics are fp32, the variance from the centred row.
  */
-int ssd_norm_fwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
+int ssd_norm_fwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, float eps,
                  const void *x, int64_t x_row_stride, const float *weight, const float *bias,
                  const void *z, int64_t z_row_stride,
                  void *y, int64_t y_row_stride, void *stream);
@@ -627,14 +667,15 @@ int ssd_norm_fwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
  *     dweight = sum_rows g n,  dbias = sum_rows g,  dz = grad_y (n weight + bias) silu'(z)
  *     dx = (g weight - mean(g weight) - n mean(g weight n)) / sqrt(...)   (rms: no mean(g weight))
  * The statistics are computed again from x.
- *   grad_y  T   [R][W];  dx x_dtype [R][W];  dz T [R][W] or NULL (only with z)
- *   dweight, dbias  f32 [W] or NULL.  Their sums over the rows are taken in a
+ *   grad_y  T   [R][groups*W];  dx x_dtype and dz T of the same shape; dz NULL
+ *               or given with z
+ *   dweight, dbias  f32 [W] or NULL.  Their sums over the rows and groups are taken in a
  *               fixed order (deterministic) through the workspace:
  *               ssd_norm_bwd_workspace_size() bytes, 16-byte aligned,
  *               required where dweight or dbias is given.
  * R = 0 writes zero dweight and dbias.
  */
-int ssd_norm_bwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
+int ssd_norm_bwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, float eps,
                  const void *x, int64_t x_row_stride, const float *weight, const float *bias,
                  const void *z, int64_t z_row_stride,
                  const void *grad_y, int64_t grad_y_row_stride,
@@ -643,7 +684,7 @@ int ssd_norm_bwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
                  void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace of ssd_norm_bwd: one fp32 row pair for every workgroup. */
-size_t ssd_norm_bwd_workspace_size(int64_t R, int W);
+size_t ssd_norm_bwd_workspace_size(int64_t R, int groups, int W);
 
 #ifdef __cplusplus
 }

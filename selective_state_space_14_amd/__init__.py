@@ -35,7 +35,7 @@ __all__ = ["load", "ssd_conv_fwd", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_sta
            "ssd_s6_scan_fwd", "ssd_chunk_scan_workspace_size", "ssd_mixer_workspace_size", "ssd_s6_workspace_size",
            "ssd_chunk_scan_bwd", "ssd_conv_bwd", "ssd_mixer_bwd", "ssd_chunk_scan_bwd_workspace_size",
            "ssd_conv_bwd_workspace_size", "ssd_mixer_bwd_workspace_size",
-           "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
+           "ssd_delta_scan_fwd", "ssd_delta_scan_workspace_size", "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
            "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_ACT_SILU", "SSD_ACT_NONE"]
 
 # SSD_LIBRARY names another build of the same library (the host-sanitized one the ABI checks use)
@@ -109,14 +109,18 @@ def load() -> ctypes.CDLL:
     F = ctypes.c_float
     # q, k, v, dt (softplus, bias), A, beta (sigmoid), scale, qk_norm: the shared head of the delta calls
     delta = [P, I64, P, I64, P, I64, P, I64, I, P, P, P, I64, I, F, I]
+    lib.ssd_delta_scan_fwd.restype = I
+    lib.ssd_delta_scan_fwd.argtypes = [I, I, I, I, I, I, I, I, *delta, P, P, P, P, P, I64, P, SZ, P]
+    lib.ssd_delta_scan_workspace_size.restype = SZ
+    lib.ssd_delta_scan_workspace_size.argtypes = [I, I, I, I, I, I, I]
     lib.ssd_delta_step.restype = I
     lib.ssd_delta_step.argtypes = [I, I, I, I, I, I, *delta, P, P, I64, P]
     lib.ssd_norm_fwd.restype = I
-    lib.ssd_norm_fwd.argtypes = [I64, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P]
+    lib.ssd_norm_fwd.argtypes = [I64, I, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P]
     lib.ssd_norm_bwd.restype = I
-    lib.ssd_norm_bwd.argtypes = [I64, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P, I64, P, P, P, I64, P, SZ, P]
+    lib.ssd_norm_bwd.argtypes = [I64, I, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P, I64, P, P, P, I64, P, SZ, P]
     lib.ssd_norm_bwd_workspace_size.restype = SZ
-    lib.ssd_norm_bwd_workspace_size.argtypes = [I64, I]
+    lib.ssd_norm_bwd_workspace_size.argtypes = [I64, I, I]
     lib.ssd_s6_workspace_size.restype = SZ
     lib.ssd_s6_workspace_size.argtypes = [I, I, I, I, I]
     _lib = lib
@@ -645,6 +649,34 @@ def _delta_head(c, lead, T, q, k, v, dt, A, beta, H, P, N, G, scale, qk_norm, dt
             N ** -0.5 if scale is None else float(scale), int(bool(qk_norm))]
 
 
+def ssd_delta_scan_workspace_size(B, L, H, P, N, G, dtype=SSD_BF16) -> int:
+    return int(load().ssd_delta_scan_workspace_size(B, L, H, P, N, G, dtype))
+
+
+def ssd_delta_scan_fwd(q, k, v, dt, A, beta, *, H, P, N, G, scale=None, qk_norm=False, dt_softplus=False, dt_bias=None,
+                       beta_sigmoid=False, doc_ids=None, lengths=None, init_state=None, final_state=None, y=None,
+                       chunk=64, workspace=None, stream=None):
+    """The gated delta rule.  q, k [B, L, G*N], v [B, L, H*P] (one dtype), dt, beta [B, L, H] fp32, A [H] fp32.
+    scale: N^-0.5 if None.  Returns y [B, L, H*P] in q's dtype (and writes final_state [B, H, P, N] if given).  A
+    workspace is allocated here when none is passed."""
+    lib = load()
+    c = _Call(q, "q")
+    dtype = _dtype_code(q, "q")
+    B, L, T = q.shape[0], q.shape[1], q.dtype
+    head = _delta_head(c, (B, L), T, q, k, v, dt, A, beta, H, P, N, G, scale, qk_norm, dt_softplus, dt_bias, beta_sigmoid)
+    if y is None:
+        y = torch.empty((B, L, H * P), dtype=T, device=c.dev)
+    yp, ys = c.rows(y, "y", T, (B, L, H * P))
+    ws = _ws(workspace, ssd_delta_scan_workspace_size(B, L, H, P, N, G, dtype), c.dev)
+    state = (B, H, P, N)
+    c.run(lib.ssd_delta_scan_fwd,
+          (B, L, H, P, N, G, chunk, dtype, *head, c.vec(doc_ids, "doc_ids", torch.int32, (B, L)),
+           c.vec(lengths, "lengths", torch.int32, (B,)), c.vec(init_state, "init_state", torch.float32, state),
+           c.vec(final_state, "final_state", torch.float32, state), yp, ys, c.ptr(ws, "workspace"),
+           ws.numel() * ws.element_size()), stream)
+    return y
+
+
 def ssd_delta_step(q, k, v, dt, A, beta, state, *, H, P, N, G, scale=None, qk_norm=False, dt_softplus=False,
                    dt_bias=None, beta_sigmoid=False, y=None, stream=None):
     """One token of the gated delta rule.  q, k [B, G*N], v [B, H*P] (one dtype), dt, beta [B, H] fp32, A [H] fp32;
@@ -662,26 +694,45 @@ def ssd_delta_step(q, k, v, dt, A, beta, state, *, H, P, N, G, scale=None, qk_no
     return y
 
 
+def _norm_groups(c, shape, tensors):
+    """(rows, groups, strides by name) of norm operands: the last dimension is a group; where some operand's rows are not
+    a uniform distance apart, the dimension before it holds the groups of a row (the heads of a token's row)."""
+    W = shape[-1]
+    n = 1
+    for s in shape[:-1]:
+        n *= s
+    try:
+        return n, 1, {name: c.rows(t, name, dtype, shape) for name, (t, dtype) in tensors.items()}
+    except ValueError:
+        if len(shape) < 3 or any(t is not None and (t.shape != shape or t.stride(-2) != W) for t, _ in tensors.values()):
+            raise
+    g = shape[-2]
+    flat = shape[:-2] + (g * W,)
+    return n // g, g, {name: c.rows(None if t is None else t.flatten(-2), name, dtype, flat)
+                       for name, (t, dtype) in tensors.items()}
+
+
 def ssd_norm_fwd(x, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, out_dtype=None, y=None, stream=None):
-    """Norm of x's rows (its last dimension), times weight plus bias, times silu(z).  x fp32 or bf16; weight, bias
-    fp32 [W]; z in the output's dtype, which is y's, else out_dtype, else z's, else x's.  Returns y."""
+    """Norm of x's last dimension, times weight plus bias, times silu(z).  x [..., W] fp32 or bf16, its rows a uniform
+    distance apart, or [..., heads, W] with the heads of a row side by side; weight, bias fp32 [W]; z in the output's
+    dtype, which is y's, else out_dtype, else z's, else x's.  Returns y."""
     lib = load()
     c = _Call(x, "x")
     shape, W = x.shape, x.shape[-1]
     T = y.dtype if y is not None else out_dtype or (x.dtype if z is None else z.dtype)
     if y is None:
         y = torch.empty(shape, dtype=T, device=c.dev)
-    xp, xs = c.rows(x, "x", None, shape)
-    zp, zs = c.rows(z, "z", T, shape)
-    yp, ys = c.rows(y, "y", T, shape)
-    c.run(lib.ssd_norm_fwd, (x.numel() // W if W else 0, W, _dtype_code(x, "x"), _dtype_code(y, "y"), int(bool(rms)),
-                             float(eps), xp, xs, c.vec(weight, "weight", torch.float32, (W,)),
-                             c.vec(bias, "bias", torch.float32, (W,)), zp, zs, yp, ys), stream)
+    if x.numel() == 0:
+        return y
+    R, groups, at = _norm_groups(c, shape, {"x": (x, None), "z": (z, T), "y": (y, T)})
+    c.run(lib.ssd_norm_fwd, (R, groups, W, _dtype_code(x, "x"), _dtype_code(y, "y"), int(bool(rms)), float(eps), *at["x"],
+                             c.vec(weight, "weight", torch.float32, (W,)), c.vec(bias, "bias", torch.float32, (W,)),
+                             *at["z"], *at["y"]), stream)
     return y
 
 
-def ssd_norm_bwd_workspace_size(R, W) -> int:
-    return int(load().ssd_norm_bwd_workspace_size(R, W))
+def ssd_norm_bwd_workspace_size(R, groups, W) -> int:
+    return int(load().ssd_norm_bwd_workspace_size(R, groups, W))
 
 
 def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, workspace=None, stream=None):
@@ -691,7 +742,6 @@ def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e
     lib = load()
     c = _Call(x, "x")
     shape, W, T = x.shape, x.shape[-1], grad_y.dtype
-    R = x.numel() // W if W else 0
     f32 = dict(dtype=torch.float32, device=c.dev)
     g = {"x": torch.empty(shape, dtype=x.dtype, device=c.dev)}
     if weight is not None:
@@ -700,16 +750,15 @@ def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e
         g["bias"] = torch.empty(W, **f32)
     if z is not None:
         g["z"] = torch.empty(shape, dtype=T, device=c.dev)
+    R, groups, at = _norm_groups(c, shape, {"x": (x, None), "z": (z, T), "grad_y": (grad_y, T), "dx": (g["x"], None),
+                                            "dz": (g.get("z"), T)})
     ws, nb = None, 0
     if weight is not None or bias is not None:
-        ws = _ws(workspace, ssd_norm_bwd_workspace_size(R, W), c.dev)
+        ws = _ws(workspace, ssd_norm_bwd_workspace_size(R, groups, W), c.dev)
         nb = ws.numel() * ws.element_size()
-    xp, xs = c.rows(x, "x", None, shape)
-    zp, zs = c.rows(z, "z", T, shape)
-    gp, gs = c.rows(grad_y, "grad_y", T, shape)
     out = lambda n: g[n].data_ptr() if n in g else None  # noqa: E731
-    c.run(lib.ssd_norm_bwd, (R, W, _dtype_code(x, "x"), _dtype_code(grad_y, "grad_y"), int(bool(rms)), float(eps), xp,
-                             xs, c.vec(weight, "weight", torch.float32, (W,)), c.vec(bias, "bias", torch.float32, (W,)),
-                             zp, zs, gp, gs, out("x"), W, out("weight"), out("bias"), out("z"), W,
-                             c.ptr(ws, "workspace"), nb), stream)
+    c.run(lib.ssd_norm_bwd, (R, groups, W, _dtype_code(x, "x"), _dtype_code(grad_y, "grad_y"), int(bool(rms)), float(eps),
+                             *at["x"], c.vec(weight, "weight", torch.float32, (W,)),
+                             c.vec(bias, "bias", torch.float32, (W,)), *at["z"], *at["grad_y"], *at["dx"], out("weight"),
+                             out("bias"), *at["dz"], c.ptr(ws, "workspace"), nb), stream)
     return g

@@ -1030,6 +1030,53 @@ static ssd::DeltaArgs delta_args(int B, int L, int H, int P, int N, int G, int d
     return a;
 }
 
+size_t ssd_delta_scan_workspace_size(int B, int L, int H, int P, int N, int G, int dtype) {
+    if (B <= 0 || L <= 0 || H <= 0 || P <= 0 || N <= 0 || G <= 0) return 0;
+    return ssd::delta_fwd_workspace_bytes(B, L, H, dtype);
+}
+
+int ssd_delta_scan_fwd(int B, int L, int H, int P, int N, int G, int chunk, int dtype,
+                       const void* q, int64_t q_row_stride,
+                       const void* k, int64_t k_row_stride,
+                       const void* v, int64_t v_row_stride,
+                       const float* dt, int64_t dt_row_stride, int dt_softplus, const float* dt_bias,
+                       const float* A,
+                       const float* beta, int64_t beta_row_stride, int beta_sigmoid,
+                       float scale, int qk_norm,
+                       const int32_t* doc_ids, const int32_t* lengths,
+                       const float* init_state, float* final_state,
+                       void* y, int64_t y_row_stride,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssd_delta_scan_fwd";
+    ssd::DeltaArgs a = delta_args(B, L, H, P, N, G, dtype, q, q_row_stride, k, k_row_stride, v, v_row_stride, dt,
+                                  dt_row_stride, dt_softplus, dt_bias, A, beta, beta_row_stride, beta_sigmoid, scale,
+                                  qk_norm);
+    a.doc = doc_ids; a.lengths = lengths;
+    a.init_state = init_state; a.final_state = final_state;
+    a.y = y; a.y_stride = y_row_stride;
+    const bool work = B > 0 && L > 0;
+    TRY(check_delta(fn, a, work));
+    if (chunk != 64) return fail(SSD_ERR_UNSUPPORTED, "%s: chunk=%d is not supported (must be 64)", fn, chunk);
+    TRY(check_tensor(fn, "y", y, y_row_stride, (int64_t)H * P, esize(dtype), work));
+    TRY(check_ptr(fn, "init_state", init_state, false, true));
+    TRY(check_ptr(fn, "final_state", final_state, false, true));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!work) {
+        if (final_state && B > 0)
+            return hip_status(fn, ssd::launch_copy16(init_state, final_state, (size_t)B * H * P * N * 4 / 16, s));
+        return ok();
+    }
+    if (y == final_state || y == init_state || y == v || y == q || y == k)
+        return fail(SSD_ERR_BAD_SHAPE, "%s: y must not alias an input or the state", fn);
+    const size_t need = ssd_delta_scan_workspace_size(B, L, H, P, N, G, dtype);
+    if (!workspace || workspace_bytes < need)
+        return fail(SSD_ERR_WORKSPACE, "%s: workspace_bytes=%zu is smaller than the required %zu", fn,
+                    workspace ? workspace_bytes : (size_t)0, need);
+    if (!aligned16(workspace))
+        return fail(SSD_ERR_ALIGNMENT, "%s: workspace=%p is not 16-byte aligned", fn, workspace);
+    return hip_status(fn, ssd::launch_delta_fwd(a, workspace, s));
+}
+
 int ssd_delta_step(int B, int H, int P, int N, int G, int dtype,
                    const void* q, int64_t q_row_stride,
                    const void* k, int64_t k_row_stride,
@@ -1062,7 +1109,9 @@ static int check_norm(const char* fn, ssd::NormArgs& a, bool bwd) {
             return fail(SSD_ERR_UNSUPPORTED, "%s: dtype=%d is not supported (only SSD_F32=0 and SSD_BF16=1; "
                         "fp16, fp64 and other types are refused, not converted)", fn, d);
     if (a.R < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: R=%lld must be >= 0", fn, (long long)a.R);
-    if (a.R > 0x7fffffffLL) return fail(SSD_ERR_BAD_SHAPE, "%s: R=%lld is too large", fn, (long long)a.R);
+    if (a.groups <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: groups=%d must be > 0", fn, a.groups);
+    if (a.R > 0x7fffffffLL / a.groups)
+        return fail(SSD_ERR_BAD_SHAPE, "%s: R=%lld rows of %d groups are too many", fn, (long long)a.R, a.groups);
     if (a.W <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: W=%d must be > 0", fn, a.W);
     if (a.W > 16384) return fail(SSD_ERR_UNSUPPORTED, "%s: W=%d is not supported (at most 16384 columns)", fn, a.W);
     if (a.rms != 0 && a.rms != 1) return fail(SSD_ERR_UNSUPPORTED, "%s: rms=%d must be 0 or 1", fn, a.rms);
@@ -1080,9 +1129,9 @@ static int check_norm(const char* fn, ssd::NormArgs& a, bool bwd) {
             if (r.required) return fail(SSD_ERR_NULL_ARG, "%s: %s is NULL", fn, r.name);
             continue;
         }
-        if (r.stride < a.W)
-            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is smaller than the row width %d", fn, r.name,
-                        (long long)r.stride, a.W);
+        if (r.stride < (int64_t)a.groups * a.W)
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is smaller than the row width %lld", fn, r.name,
+                        (long long)r.stride, (long long)a.groups * a.W);
         if (r.stride > (1 << 22))
             return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is above 4194304 elements", fn, r.name,
                         (long long)r.stride);
@@ -1097,13 +1146,13 @@ static int check_norm(const char* fn, ssd::NormArgs& a, bool bwd) {
     return SSD_OK;
 }
 
-int ssd_norm_fwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
+int ssd_norm_fwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, float eps,
                  const void* x, int64_t x_row_stride, const float* weight, const float* bias,
                  const void* z, int64_t z_row_stride,
                  void* y, int64_t y_row_stride, void* stream) {
     const char* fn = "ssd_norm_fwd";
     ssd::NormArgs a{};
-    a.R = R; a.W = W; a.x_dtype = x_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
+    a.R = R; a.groups = groups; a.W = W; a.x_dtype = x_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
     a.x = x; a.x_stride = x_row_stride;
     a.w = weight; a.b = bias;
     a.z = z; a.z_stride = z_row_stride;
@@ -1111,15 +1160,16 @@ int ssd_norm_fwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
     TRY(check_norm(fn, a, false));
     if (R == 0) return ok();
     if (y == x || y == z) return fail(SSD_ERR_BAD_SHAPE, "%s: y must not alias x or z", fn);
+    a.R *= groups;   // the kernels count groups
     return hip_status(fn, ssd::launch_norm(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t ssd_norm_bwd_workspace_size(int64_t R, int W) {
-    if (R <= 0 || W <= 0) return 0;
-    return ssd::norm_bwd_workspace_bytes(R, W);
+size_t ssd_norm_bwd_workspace_size(int64_t R, int groups, int W) {
+    if (R <= 0 || groups <= 0 || W <= 0) return 0;
+    return ssd::norm_bwd_workspace_bytes(R * groups, W);
 }
 
-int ssd_norm_bwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
+int ssd_norm_bwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, float eps,
                  const void* x, int64_t x_row_stride, const float* weight, const float* bias,
                  const void* z, int64_t z_row_stride,
                  const void* grad_y, int64_t grad_y_row_stride,
@@ -1128,7 +1178,7 @@ int ssd_norm_bwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
                  void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "ssd_norm_bwd";
     ssd::NormArgs a{};
-    a.R = R; a.W = W; a.x_dtype = x_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
+    a.R = R; a.groups = groups; a.W = W; a.x_dtype = x_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
     a.x = x; a.x_stride = x_row_stride;
     a.w = weight; a.b = bias;
     a.z = z; a.z_stride = z_row_stride;
@@ -1149,7 +1199,7 @@ int ssd_norm_bwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
     if (dx == x || dx == grad_y || dx == z || (dz && (dz == x || dz == grad_y || dz == z || dz == dx)))
         return fail(SSD_ERR_BAD_SHAPE, "%s: dx and dz must not alias an input or each other", fn);
     if (dweight || dbias) {
-        const size_t need = ssd_norm_bwd_workspace_size(R, W);
+        const size_t need = ssd_norm_bwd_workspace_size(R, groups, W);
         if (!workspace || workspace_bytes < need)
             return fail(SSD_ERR_WORKSPACE, "%s: workspace_bytes=%zu is smaller than the required %zu", fn,
                         workspace ? workspace_bytes : (size_t)0, need);
@@ -1157,6 +1207,7 @@ int ssd_norm_bwd(int64_t R, int W, int x_dtype, int dtype, int rms, float eps,
             return fail(SSD_ERR_ALIGNMENT, "%s: workspace=%p is not 16-byte aligned", fn, workspace);
         a.part = static_cast<float*>(workspace);
     }
+    a.R *= groups;
     return hip_status(fn, ssd::launch_norm(a, s));
 }
 

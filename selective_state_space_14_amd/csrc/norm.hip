@@ -151,6 +151,17 @@ __device__ __forceinline__ void load_params(const float* w, const float* b, cons
     }
 }
 
+// group r as row `row` of memory and the columns before it; r < 2^31
+__device__ __forceinline__ void locate(const NormArgs& a, int64_t r, int64_t& row, int& col) {
+    row = r;
+    col = 0;
+    if (a.groups > 1) {
+        const uint32_t o = (uint32_t)r / (uint32_t)a.groups;
+        row = o;
+        col = (int)((uint32_t)r - o * (uint32_t)a.groups) * a.W;
+    }
+}
+
 template <typename X, typename T, int TPR, int NV, int VEC>
 __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_kernel(NormArgs a) {
     using SH = Shape<TPR, NV, VEC>;
@@ -166,8 +177,10 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_k
     const T* zp = static_cast<const T*>(a.z);
     T* yp = static_cast<T*>(a.y);
     for (int64_t r0 = (int64_t)blockIdx.x * SH::rows; r0 < a.R; r0 += (int64_t)gridDim.x * SH::rows) {
-        const int64_t r = r0 + sub;
-        const bool live = r < a.R;                  // TPR > 64: rows = 1, uniform
+        const bool live = r0 + sub < a.R;           // TPR > 64: rows = 1, uniform
+        int64_t r;
+        int col;
+        locate(a, r0 + sub, r, col);
         float x[NV][VEC], z[NV][VEC];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -175,8 +188,8 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_k
 #pragma unroll
             for (int e = 0; e < VEC; ++e) x[j][e] = z[j][e] = 0.0f;
             if (live && on[j]) {
-                ldv<VEC>(xp + r * a.x_stride + c, x[j]);
-                if (zp) ldv<VEC>(zp + r * a.z_stride + c, z[j]);
+                ldv<VEC>(xp + r * a.x_stride + col + c, x[j]);
+                if (zp) ldv<VEC>(zp + r * a.z_stride + col + c, z[j]);
             }
         }
         to_hat<TPR, NV, VEC>(x, on, a.W, a.rms, a.eps, red, turn);
@@ -189,7 +202,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_k
                 y[e] = fmaf(x[j][e], wv[j][e], bv[j][e]);
                 if (zp) y[e] *= silu_f(z[j][e]);
             }
-            if (live && on[j]) stv<VEC>(yp + r * a.y_stride + c, y);
+            if (live && on[j]) stv<VEC>(yp + r * a.y_stride + col + c, y);
         }
     }
 }
@@ -224,8 +237,10 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
     T* dzp = static_cast<T*>(a.dz);
     const float inv = 1.0f / (float)a.W;
     for (int64_t r0 = (int64_t)blockIdx.x * SH::rows; r0 < a.R; r0 += (int64_t)gridDim.x * SH::rows) {
-        const int64_t r = r0 + sub;
-        const bool live = r < a.R;
+        const bool live = r0 + sub < a.R;
+        int64_t r;
+        int col;
+        locate(a, r0 + sub, r, col);
         float x[NV][VEC], z[NV][VEC], g[NV][VEC];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -233,9 +248,9 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
 #pragma unroll
             for (int e = 0; e < VEC; ++e) x[j][e] = z[j][e] = g[j][e] = 0.0f;
             if (live && on[j]) {
-                ldv<VEC>(xp + r * a.x_stride + c, x[j]);
-                ldv<VEC>(gp + r * a.gy_stride + c, g[j]);
-                if (zp) ldv<VEC>(zp + r * a.z_stride + c, z[j]);
+                ldv<VEC>(xp + r * a.x_stride + col + c, x[j]);
+                ldv<VEC>(gp + r * a.gy_stride + col + c, g[j]);
+                if (zp) ldv<VEC>(zp + r * a.z_stride + col + c, z[j]);
             }
         }
         const float rstd = to_hat<TPR, NV, VEC>(x, on, a.W, a.rms, a.eps, red, turn);
@@ -253,7 +268,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
                     d[e] = g[j][e] * n * s * fmaf(z[j][e], 1.0f - s, 1.0f);
                     g[j][e] *= z[j][e] * s;
                 }
-                if (dzp && live && on[j]) stv<VEC>(dzp + r * a.dz_stride + c, d);
+                if (dzp && live && on[j]) stv<VEC>(dzp + r * a.dz_stride + col + c, d);
             }
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
@@ -278,7 +293,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             float d[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) d[e] = rstd * (g[j][e] - m1 - x[j][e] * m2);
-            if (live && on[j]) stv<VEC>(dxp + r * a.dx_stride + c, d);
+            if (live && on[j]) stv<VEC>(dxp + r * a.dx_stride + col + c, d);
         }
     }
     // the workgroup's sums: [block][2][W], rows of the workgroup added in order

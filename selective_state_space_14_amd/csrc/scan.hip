@@ -2006,6 +2006,8 @@ hipError_t launch_scan_t(const ScanArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+hipError_t prepare_launch(const void* fn, size_t lds) { return prepare_kernel(fn, lds, false); }
+
 // Sequence split.  fp32: enough (b, h, superchunk) units to give every CU
 // several workgroups, with superchunks of at least 8 chunks.  bf16: the K
 // (at most 8) that minimises the critical path in chunk steps -- rounds of

@@ -132,10 +132,11 @@ struct ConvBwdArgs {
     float* part;                           // [B * ntc][C][5] per-chunk partial sums of dw and dbias
 };
 
-// Row norm over R rows of W columns (forward: gy = null).
+// Row norm over R groups of W columns, `groups` of them side by side in a row
+// of memory (forward: gy = null).
 struct NormArgs {
     int64_t R;
-    int W, x_dtype, dtype, rms;
+    int groups, W, x_dtype, dtype, rms;
     int vec;                               // rows start on 16-byte boundaries and W % 8 == 0
     float eps;
     const void* x; int64_t x_stride;       // x_dtype
@@ -202,6 +203,11 @@ size_t conv_bwd_workspace_bytes(int B, int L, int C);
 // Zero fill of n floats by a kernel (no memset node).
 hipError_t launch_zero_f32(float* p, size_t n, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t stream);
+// Raises a kernel's dynamic-LDS cap to `lds` on the current device before its
+// first launch there; once per (kernel, device), thread-safe.
+hipError_t prepare_launch(const void* fn, size_t lds);
+size_t delta_fwd_workspace_bytes(int B, int L, int H, int dtype);
+hipError_t launch_delta_fwd(const DeltaArgs& a, void* ws, hipStream_t stream);
 hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 size_t norm_bwd_workspace_bytes(int64_t R, int W);

@@ -98,6 +98,28 @@ def test_norm_strided_rows(gpu_lib):
     assert torch.equal(y3.view(24, 96), want)
 
 
+def test_norm_of_heads_in_wider_rows(gpu_lib):
+    """Every head by itself where x, z and grad_y are column slices of wider token rows: the bits of contiguous heads."""
+    ssd, (B, L, H, P) = gpu_lib, (2, 9, 4, 64)
+    d = up(make(B * L * H, P, "bf16", "bf16", gate=True))
+    heads = {n: d[n].view(B, L, H, P) for n in ("x", "z", "gy")}
+    want = ssd.ssd_norm_fwd(d["x"], d["weight"], bias=d["bias"], z=d["z"])
+    wg = ssd.ssd_norm_bwd(d["x"], d["gy"], d["weight"], bias=d["bias"], z=d["z"])
+    for pad in (16, 3):
+        wide = torch.zeros(3, B, L, H * P + pad, dtype=torch.bfloat16, device=DEV)
+        views = {}
+        for j, n in enumerate(heads):
+            wide[j, ..., :H * P] = heads[n].flatten(-2)
+            views[n] = wide[j, ..., :H * P].unflatten(-1, (H, P))
+        y = ssd.ssd_norm_fwd(views["x"], d["weight"], bias=d["bias"], z=views["z"])
+        torch.testing.assert_close(y.view(-1, P).float(), want.float(), rtol=2 ** -7, atol=2 ** -12)
+        assert pad == 3 or torch.equal(y.view(-1, P), want)
+        g = ssd.ssd_norm_bwd(views["x"], views["gy"], d["weight"], bias=d["bias"], z=views["z"])
+        assert pad == 3 or all(torch.equal(g[n].view(wg[n].shape), wg[n]) for n in wg)
+    with pytest.raises(ValueError):
+        ssd.ssd_norm_fwd(views["x"].transpose(1, 2), d["weight"])
+
+
 def test_norm_nan_and_inf_stay_in_their_row(gpu_lib):
     d = make(20, 256, "f32", "f32")
     d["x"][3, 5], d["x"][11, 0] = float("nan"), float("inf")
@@ -178,7 +200,7 @@ def test_norm_on_a_side_stream_and_captured(gpu_lib):
     """A captured forward and backward, replayed with new inputs in the same memory between eager calls."""
     ssd = gpu_lib
     d = up(make(300, 264, "bf16", "bf16", gate=True))
-    ws = torch.empty(ssd.ssd_norm_bwd_workspace_size(300, 264), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(ssd.ssd_norm_bwd_workspace_size(300, 1, 264), dtype=torch.uint8, device=DEV)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
