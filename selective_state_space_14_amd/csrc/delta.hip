@@ -13,12 +13,11 @@ namespace {
 using namespace delta;
 
 // ============================================================ prep
-// One wave a unit; four heads of a chunk, which mostly share q and k, in a
-// workgroup, without a barrier between them.  A row of k is an operand of
-// k k^T from either side, so the chunk's k is loaded once, straight into
-// fragments (a lane takes 8 consecutive entries of a row: 64-byte pieces of
-// memory; which K index an element stands for does not matter while both
-// operands agree).
+// One wave a unit, two to a workgroup, without a barrier between them.  A row
+// of k is an operand of k k^T from either side, so the chunk's k is loaded
+// once, straight into fragments (a lane takes 8 consecutive entries of a row:
+// 64-byte pieces of memory; which K index an element stands for does not
+// matter while both operands agree).
 //
 // The inverse is taken of I + L^T, whose accumulator tiles [j][t] are T's
 // operand fragments as they come: the four diagonal 16 x 16 blocks by back
@@ -28,13 +27,27 @@ using namespace delta;
 // (I - L)(I + L^2)..., never forms a power of L, whose entries can reach 1e8
 // where keys point the same way and would cancel.
 //
-// The running sum of dt A is taken in fp64 and kept as two floats: decays
-// within a chunk are differences of sums that can reach -12800 (a token's
-// dt A is taken as at least -200: e^-200 is 0 in fp32 either way).
-constexpr int kLtStride = C + 4;
+// The running sum of dt A is taken in fp64: within a chunk decays are
+// differences of sums that can reach -12800 (a token's dt A is taken as at
+// least -200: e^-200 is 0 in fp32 either way).  Between two 16-token blocks a
+// decay is the product of one to the later block's first token and one from
+// it, both from a table of 16 exponentials a token; inside a block it is taken
+// from the sum held as two floats.
+//
+// What the scan needs of T depends on it (Prep): the bf16 forward multiplies X
+// by T only to get U scaled for the state, diag(e^{G_C - G}) T diag(beta), and
+// Att T diag(beta) for y, so those two products are formed here, where all
+// chunks run at once, and not in the chain of the scan.
+constexpr int kLtRow = 20;                           // floats of an L^T tile's row: 16-byte reads of 16 rows hit all banks
+constexpr int kPrepWaves = 2;
+enum Prep {
+    kPrepScaled = 0,               // bf16 forward: diag(kout) T diag(beta) (split), Att T diag(beta) (rounded)
+    kPrepPlain = 1,                // fp32 forward: T, Att
+    kPrepBwd = 2,                  // backward: T, its transpose, Att's transposed product's operand (all split)
+};
 
 struct PrepOut {
-    unsigned char *T, *TT, *att;   // per unit: T, its transpose (backward), Att (forward: lower; backward: upper, split)
+    unsigned char *T, *TT, *att;   // per unit, as above
     float* scal;                   // [u][kScal][C]
     float* across;                 // [u]
 };
@@ -44,9 +57,8 @@ struct Rows;                       // 8 consecutive entries of a row
 template <>
 struct Rows<uint16_t> {
     Frag f;
-    __device__ __forceinline__ void load(const uint16_t* p, bool on) {
-        f.u = on ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-    }
+    __device__ __forceinline__ void load(const uint16_t* p) { f.u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void clear() { f.u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ float sq() const {
         float s = 0.0f;
 #pragma unroll
@@ -61,13 +73,11 @@ struct Rows<uint16_t> {
 template <>
 struct Rows<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float* p, bool on) {
-        a = b = make_float4(0, 0, 0, 0);
-        if (on) {
-            a = *reinterpret_cast<const float4*>(p);
-            b = *reinterpret_cast<const float4*>(p + 4);
-        }
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
     }
+    __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
     __device__ __forceinline__ float sq() const {
         return a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w + b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
     }
@@ -82,35 +92,46 @@ __device__ __forceinline__ double shfl_up_f64(double v, int d) {
     return __longlong_as_double(((long long)hi << 32) | (unsigned)lo);
 }
 
-template <typename T, int N, bool BWD>
-__global__ __launch_bounds__(256) void ssd_delta_prep_kernel(DeltaArgs a, PrepOut o, int nc) {
+template <typename T, int N, int PM>
+__global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaArgs a, PrepOut o, int nc) {
     constexpr bool F32 = std::is_same<T, float>::value;
     constexpr int KS = N / 32;
-    __shared__ float lt_s[4][C][kLtStride];
-    __shared__ float tok_s[4][6][C];
-    enum { kGhi, kGlo, kSeg, kB, kRk, kRq };
+    __shared__ __align__(16) float lt_s[kPrepWaves][10 * 16 * kLtRow];
+    enum { kGhi, kGlo, kSeg, kB, kRk, kRq, kF, kOut, kE, kTok = kE + 3 };
+    __shared__ __align__(16) float tok_s[kPrepWaves][kTok][C];
 
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, q = lane / 16, i = lane % 16;
-    const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+    const int64_t id = (int64_t)blockIdx.x * kPrepWaves + wave;
     if (id >= (int64_t)a.B * nc * a.H) return;
     const int h = (int)(id % a.H), c = (int)(id / a.H % nc), b = (int)(id / a.H / nc);
     const int t0 = c * C, n_on = min(C, row_len(a, b) - t0);
     if (n_on <= 0) return;
     const size_t u = ((size_t)b * a.H + h) * nc + c;
     const int g = h / (a.H / a.G);
-    float(*lt)[kLtStride] = lt_s[wave];
+    float* lt = lt_s[wave];
     float(*tok)[C] = tok_s[wave];
+    // tile (n, m), n <= m, of an upper triangular matrix: rows j of block n, columns t of block m
+    auto ltp = [&](int n, int m, int r, int col) { return lt + (tile_id(m, n) * 16 + r) * kLtRow + col; };
+    auto lt4 = [&](int n, int m) { return *reinterpret_cast<const float4*>(ltp(n, m, i, 4 * q)); };
 
-    // ---- k's rows as fragments, and their norms
+    // ---- k's rows as fragments
     const T* kp = static_cast<const T*>(a.k) + ((size_t)b * a.L + t0) * a.k_stride + (size_t)g * N + 8 * q;
     const T* qp = static_cast<const T*>(a.q) + ((size_t)b * a.L + t0) * a.q_stride + (size_t)g * N + 8 * q;
-    Rows<T> kf[4][KS];
+    // row t = 16 m + i of a tile; rows past the sequence read its last one and become zeros
+    auto load_rows = [&](Rows<T>(&f)[KS], const T* p, int64_t stride, int m) {
+        const T* at = p + min(16 * m + i, n_on - 1) * stride;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int t = 16 * m + i;
+        for (int s = 0; s < KS; ++s) f[s].load(at + 32 * s);
+        if (n_on < C && 16 * m + i >= n_on) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) kf[m][s].load(kp + (size_t)t * a.k_stride + 32 * s, t < n_on);
-    }
+            for (int s = 0; s < KS; ++s) f[s].clear();
+        }
+    };
+    Rows<T> kf[4][KS], qf[4][KS];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) load_rows(kf[m], kp, a.k_stride, m);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) load_rows(qf[m], qp, a.q_stride, m);
 
     // ---- the token's scalars, one token a lane
     const bool on = lane < n_on;
@@ -129,10 +150,14 @@ __global__ __launch_bounds__(256) void ssd_delta_prep_kernel(DeltaArgs a, PrepOu
         if (lane >= d) G += up;
     }
     G *= 1.4426950408889634074;                      // log2 e
+    auto of_lane = [&](int l) {
+        const long long v = __double_as_longlong(G);
+        return __longlong_as_double(((long long)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32) |
+                                    (unsigned)__builtin_amdgcn_readlane((int)v, l));
+    };
     const uint64_t starts = __ballot(start);
     const int seg = __popcll(starts & (~0ull >> (63 - lane))), last = __popcll(starts);
-    const double Gc = __longlong_as_double(((long long)__builtin_amdgcn_readlane((int)(__double_as_longlong(G) >> 32), 63) << 32) |
-                                           (unsigned)__builtin_amdgcn_readlane((int)__double_as_longlong(G), 63));
+    const double Gc = of_lane(63);
     const float into = seg == 0 ? fast_exp2((float)G) : 0.0f;
     const float out = seg == last ? fast_exp2((float)(Gc - G)) : 0.0f;
     const float ghi = (float)G;
@@ -140,117 +165,116 @@ __global__ __launch_bounds__(256) void ssd_delta_prep_kernel(DeltaArgs a, PrepOu
     tok[kGlo][lane] = (float)(G - (double)ghi);
     tok[kSeg][lane] = (float)seg;
     tok[kB][lane] = beta;
+    {
+        float f = 0.0f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const double ref = of_lane(16 * m);
+            const int rseg = __popcll(starts & (~0ull >> (63 - 16 * m)));
+            if (lane / 16 == m && seg == rseg) f = fast_exp2((float)(G - ref));
+            if (m > 0) tok[kE + m - 1][lane] = lane < 16 * m && seg == rseg ? fast_exp2((float)(ref - G)) : 0.0f;
+        }
+        tok[kF][lane] = f;
+    }
+    float rq[4];                                     // of column t = 16 m + i, with the output's scale
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        float s = 0.0f;
+        float s = 0.0f, z = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) s += kf[m][k].sq();
+        for (int k = 0; k < KS; ++k) {
+            s += kf[m][k].sq();
+            z += qf[m][k].sq();
+        }
         s = rows_sum(s);
-        if (q == 0) tok[kRk][16 * m + i] = a.qk_norm ? 1.0f / sqrtf(s + kQkEps) : 1.0f;
+        z = rows_sum(z);
+        rq[m] = (a.qk_norm ? __builtin_amdgcn_rsqf(z + kQkEps) : 1.0f) * a.scale;
+        if (q == 0) {
+            tok[kRk][16 * m + i] = a.qk_norm ? __builtin_amdgcn_rsqf(s + kQkEps) : 1.0f;
+            tok[kRq][16 * m + i] = rq[m];
+        }
+    }
+    lds_wait();
+    auto row4 = [&](int what, int n) { return v4(*reinterpret_cast<const float4*>(&tok[what][16 * n + 4 * q])); };
+    auto col1 = [&](int what, int m) { return tok[what][16 * m + i]; };
+    // the table's decays with k_j's norm
+    f32x4 rk4[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        rk4[n] = row4(kRk, n);
+#pragma unroll
+        for (int m = n + 1; m < 4; ++m) {
+            const f32x4 e = row4(kE + m - 1, n) * rk4[n];
+            if (i == 0) *reinterpret_cast<float4*>(&tok[kE + m - 1][16 * n + 4 * q]) = f4(e);
+        }
     }
     lds_wait();
 
-    // ---- L^T, tile by tile, into LDS; column quantities of t = 16 m + i
-    float chi[4], clo[4], cseg[4], cb[4];
+    // ---- L^T and Att^T, tile by tile: row j = 16 n + 4 q + r, column t = 16 m + i.  L^T goes to LDS, Att^T stays in
+    // registers (the backward's Att, whose transpose is wanted, leaves at once)
+    f32x4 at[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        chi[m] = tok[kGhi][16 * m + i];
-        clo[m] = tok[kGlo][16 * m + i];
-        cseg[m] = tok[kSeg][16 * m + i];
-        cb[m] = tok[kB][16 * m + i] * tok[kRk][16 * m + i];
-    }
-    // decay from j = 16 n + 4 q + r to t = 16 m + i, 0 where it does not apply
-    auto decay = [&](int n, int m, int r, float4 jh, float4 jl, float4 js, bool diag) {
-        const float h4[4] = {jh.x, jh.y, jh.z, jh.w}, l4[4] = {jl.x, jl.y, jl.z, jl.w}, s4[4] = {js.x, js.y, js.z, js.w};
-        const bool use = s4[r] == cseg[m] && (n < m || (diag ? 4 * q + r <= i : 4 * q + r < i));
-        return use ? fast_exp2((chi[m] - h4[r]) + (clo[m] - l4[r])) : 0.0f;
-    };
-    auto row4 = [&](int what, int n) { return *reinterpret_cast<const float4*>(&tok[what][16 * n + 4 * q]); };
+        const float ct = col1(kF, m), cb = col1(kB, m) * col1(kRk, m);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const float4 jh = row4(kGhi, n), jl = row4(kGlo, n), js = row4(kSeg, n), jr = row4(kRk, n);
-        const float r4[4] = {jr.x, jr.y, jr.z, jr.w};
+        for (int n = 0; n <= m; ++n) {
+            f32x4 l = kZero4, d;
 #pragma unroll
-        for (int m = n; m < 4; ++m) {
-            f32x4 acc = kZero4;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) acc = Rows<T>::mul(acc, kf[n][s], kf[m][s]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                lt[16 * n + 4 * q + r][16 * m + i] = acc[r] * (cb[m] * r4[r]) * decay(n, m, r, jh, jl, js, false);
-        }
-    }
-
-    // ---- Att: a row tile of q at a time
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        Rows<T> qf[KS];
-        const int t = 16 * m + i;
-        float s2 = 0.0f;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            qf[s].load(qp + (size_t)t * a.q_stride + 32 * s, t < n_on);
-            s2 += qf[s].sq();
-        }
-        s2 = rows_sum(s2);
-        const float rq = (a.qk_norm ? 1.0f / sqrtf(s2 + kQkEps) : 1.0f) * a.scale;   // of column t
-        if (q == 0) tok[kRq][t] = rq;
-        if constexpr (!BWD) {
-            f32x4 at[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                at[n] = kZero4;
-                if (n > m) continue;
-                f32x4 acc = kZero4;
-#pragma unroll
-                for (int s = 0; s < KS; ++s) acc = Rows<T>::mul(acc, kf[n][s], qf[s]);
-                const float4 jh = row4(kGhi, n), jl = row4(kGlo, n), js = row4(kSeg, n), jr = row4(kRk, n);
-                const float r4[4] = {jr.x, jr.y, jr.z, jr.w};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) at[n][r] = acc[r] * (rq * r4[r]) * decay(n, m, r, jh, jl, js, true);
-            }
-            unsigned char* dst = o.att + u * Bytes<F32>::att + lane * 16;
-            if constexpr (F32) {
-#pragma unroll
-                for (int n = 0; n <= m; ++n) *reinterpret_cast<float4*>(dst + tile_id(m, n) * 1024) = f4(at[n]);
+            for (int s = 0; s < KS; ++s) l = Rows<T>::mul(l, kf[n][s], kf[m][s]);
+            if (n < m) {
+                d = row4(kE + m - 1, n) * ct;
             } else {
+                const f32x4 h4 = row4(kGhi, n), l4 = row4(kGlo, n), s4 = row4(kSeg, n);
+                const float th = col1(kGhi, m), tl = col1(kGlo, m), ts = col1(kSeg, m);
 #pragma unroll
-                for (int s = 0; s < m / 2 + 1; ++s)
-                    *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 1024) = round2(at[2 * s], at[2 * s + 1]).u;
+                for (int r = 0; r < 4; ++r) d[r] = fast_exp2(s4[r] == ts && 4 * q + r <= i ? (th - h4[r]) + (tl - l4[r]) : -INFINITY);
+                d *= rk4[n];
             }
-        } else {
-            // rows t = 16 m + 4 q + r, column j = 16 n + i: the transposed product's operand
-            lds_wait();
-            const float4 th = row4(kGhi, m), tl = row4(kGlo, m), ts = row4(kSeg, m), tr = row4(kRq, m);
-            const float h4[4] = {th.x, th.y, th.z, th.w}, l4[4] = {tl.x, tl.y, tl.z, tl.w};
-            const float s4[4] = {ts.x, ts.y, ts.z, ts.w}, r4[4] = {tr.x, tr.y, tr.z, tr.w};
-            unsigned char* dst = o.att + u * Bytes<F32>::split + lane * 16;
+            l *= d * cb;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) *ltp(n, m, 4 * q + r, i) = n == m && 4 * q + r == i ? 0.0f : l[r];
+            if constexpr (PM != kPrepBwd) {
+                at[n][m] = kZero4;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) at[n][m] = Rows<T>::mul(at[n][m], kf[n][s], qf[m][s]);
+                at[n][m] *= d * rq[m];
+            }
+        }
+    }
+    if constexpr (PM == kPrepBwd) {
+        unsigned char* da = o.att + u * Bytes<F32>::split + lane * 16;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            // rows t = 16 m + 4 q + r, column j = 16 n + i
+            const f32x4 r4 = row4(kRq, m);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 f32x4 acc = kZero4;
                 if (n <= m) {
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) acc = Rows<T>::mul(acc, qf[s], kf[n][s]);
-                    const float rk = tok[kRk][16 * n + i];
+                    for (int s = 0; s < KS; ++s) acc = Rows<T>::mul(acc, qf[m][s], kf[n][s]);
+                    if (n < m) {
+                        acc *= r4 * row4(kF, m) * col1(kE + m - 1, n);
+                    } else {
+                        acc *= r4 * col1(kRk, n);
+                        const f32x4 h4 = row4(kGhi, m), l4 = row4(kGlo, m), s4 = row4(kSeg, m);
+                        const float jh = col1(kGhi, n), jl = col1(kGlo, n), js = col1(kSeg, n);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool use = s4[r] == cseg[n] && (n < m || i <= 4 * q + r);
-                        acc[r] = use ? acc[r] * (rk * r4[r]) * fast_exp2((h4[r] - chi[n]) + (l4[r] - clo[n])) : 0.0f;
+                        for (int r = 0; r < 4; ++r)
+                            acc[r] *= fast_exp2(s4[r] == js && i <= 4 * q + r ? (h4[r] - jh) + (l4[r] - jl) : -INFINITY);
                     }
                 }
                 if constexpr (F32) {
-                    if (n <= m) *reinterpret_cast<float4*>(dst + tile_id(m, n) * 1024) = f4(acc);
+                    if (n <= m) *reinterpret_cast<float4*>(da + tile_id(m, n) * 1024) = f4(acc);
                 } else if (m / 2 >= n / 2) {
                     // half (m & 1) of fragment (n, m / 2)
-                    Pair p = split2(acc, kZero4);
-                    unsigned char* at = dst + upper_frag(n, m / 2) * 2048 + (m & 1) * 8;
-                    *reinterpret_cast<uint2*>(at) = make_uint2(p.hi.w[0], p.hi.w[1]);
-                    *reinterpret_cast<uint2*>(at + 1024) = make_uint2(p.lo.w[0], p.lo.w[1]);
+                    const Pair p = split2(acc, kZero4);
+                    unsigned char* to = da + upper_frag(n, m / 2) * 2048 + (m & 1) * 8;
+                    *reinterpret_cast<uint2*>(to) = make_uint2(p.hi.w[0], p.hi.w[1]);
+                    *reinterpret_cast<uint2*>(to + 1024) = make_uint2(p.lo.w[0], p.lo.w[1]);
                 }
             }
         }
     }
-    lds_wait();
     {
         float* sc = o.scal + u * kScal * C;
         const float rk = tok[kRk][lane];
@@ -258,18 +282,21 @@ __global__ __launch_bounds__(256) void ssd_delta_prep_kernel(DeltaArgs a, PrepOu
         sc[kKout * C + lane] = out * rk;
         sc[kQin * C + lane] = into * tok[kRq][lane];
         sc[kBeta * C + lane] = beta;
+        if (PM == kPrepScaled) tok[kOut][lane] = out * rk;
         if (lane == 0) o.across[u] = last == 0 ? fast_exp2((float)Gc) : 0.0f;
     }
+    lds_wait();
 
     // ---- the inverse: lane group q takes diagonal block q, lane i its column i
     {
         float x[16];
+        const float* dg = lt + tile_id(q, q) * 16 * kLtRow;
 #pragma unroll
         for (int r = 15; r >= 0; --r) {
             float v = r == i ? 1.0f : 0.0f;
 #pragma unroll
             for (int s4 = (r + 1) / 4; s4 < 4; ++s4) {
-                const float4 l = *reinterpret_cast<const float4*>(&lt[16 * q + r][16 * q + 4 * s4]);
+                const float4 l = *reinterpret_cast<const float4*>(dg + r * kLtRow + 4 * s4);
                 if (4 * s4 + 0 > r) v = fmaf(-l.x, x[4 * s4 + 0], v);
                 if (4 * s4 + 1 > r) v = fmaf(-l.y, x[4 * s4 + 1], v);
                 if (4 * s4 + 2 > r) v = fmaf(-l.z, x[4 * s4 + 2], v);
@@ -278,18 +305,18 @@ __global__ __launch_bounds__(256) void ssd_delta_prep_kernel(DeltaArgs a, PrepOu
             x[r] = v;
         }
         lds_wait();
+        float* dw = lt + tile_id(q, q) * 16 * kLtRow + i;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) lt[16 * q + r][16 * q + i] = x[r];
+        for (int r = 0; r < 16; ++r) dw[r * kLtRow] = x[r];
     }
     lds_wait();
     f32x4 tt[4][4];                                  // [c][a]: rows j of block c, columns t of block a
-    auto lt4 = [&](int rb, int cb) { return *reinterpret_cast<const float4*>(&lt[16 * rb + i][16 * cb + 4 * q]); };
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) tt[n][m] = kZero4;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) tt[m][m][r] = lt[16 * m + 4 * q + r][16 * m + i];
+        for (int r = 0; r < 4; ++r) tt[m][m][r] = *ltp(m, m, 4 * q + r, i);
 #pragma unroll
         for (int n = m - 1; n >= 0; --n) {
             f32x4 y = kZero4;
@@ -298,31 +325,38 @@ __global__ __launch_bounds__(256) void ssd_delta_prep_kernel(DeltaArgs a, PrepOu
             tt[n][m] = -mma_f32(kZero4, lt4(n, n), f4(y));
         }
     }
-    unsigned char* dst = o.T + u * Bytes<F32>::split + lane * 16;
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        if constexpr (F32) {
-#pragma unroll
-            for (int n = 0; n <= m; ++n) *reinterpret_cast<float4*>(dst + tile_id(m, n) * 1024) = f4(tt[n][m]);
-        } else {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                    if (s > m / 2) continue;
-                const Pair p = split2(tt[2 * s][m], tt[2 * s + 1][m]);
-                *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 2048) = p.hi.u;
-                *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 2048 + 1024) = p.lo.u;
-            }
-        }
-    }
-    if constexpr (BWD) {
+    // T^T back to LDS, over L^T, where its transpose is wanted
+    if constexpr (PM != kPrepPlain) {
         lds_wait();
 #pragma unroll
         for (int m = 1; m < 4; ++m)
 #pragma unroll
             for (int n = 0; n < m; ++n)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) lt[16 * n + 4 * q + r][16 * m + i] = tt[n][m][r];
-        lds_wait();
+                for (int r = 0; r < 4; ++r) *ltp(n, m, 4 * q + r, i) = tt[n][m][r];
+    }
+    unsigned char* dst = o.T + u * Bytes<F32>::split + lane * 16;
+    lds_wait();
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        if constexpr (PM == kPrepScaled) {
+            const float ko = col1(kOut, m);
+#pragma unroll
+            for (int n = 0; n <= m; ++n) tt[n][m] *= row4(kB, n) * ko;
+        }
+        if constexpr (F32) {
+#pragma unroll
+            for (int n = 0; n <= m; ++n) *reinterpret_cast<float4*>(dst + tile_id(m, n) * 1024) = f4(tt[n][m]);
+        } else {
+#pragma unroll
+            for (int s = 0; s < m / 2 + 1; ++s) {
+                const Pair p = split2(tt[2 * s][m], tt[2 * s + 1][m]);
+                *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 2048) = p.hi.u;
+                *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 2048 + 1024) = p.lo.u;
+            }
+        }
+    }
+    if constexpr (PM == kPrepBwd) {
         unsigned char* dtt = o.TT + u * Bytes<F32>::split + lane * 16;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -339,43 +373,355 @@ __global__ __launch_bounds__(256) void ssd_delta_prep_kernel(DeltaArgs a, PrepOu
             }
         }
     }
+
+    // ---- Att
+    if constexpr (PM != kPrepBwd) {
+        unsigned char* da = o.att + u * Bytes<F32>::att + lane * 16;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if constexpr (F32) {
+#pragma unroll
+                for (int n = 0; n <= m; ++n) *reinterpret_cast<float4*>(da + tile_id(m, n) * 1024) = f4(at[n][m]);
+            } else {
+                // (Att T)^T, tile (n, m) = sum_k T^T(n, k) Att^T(k, m) over k = n .. m; on the fp32 MFMA, since the
+                // VALU, which would split the operands, is what this kernel is short of
+                f32x4 w[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    w[n] = kZero4;
+                    if (n > m) continue;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k >= n && k <= m) w[n] = mma_f32(w[n], lt4(n, k), f4(at[k][m]));
+                    w[n] *= row4(kB, n);
+                }
+#pragma unroll
+                for (int s = 0; s < m / 2 + 1; ++s)
+                    *reinterpret_cast<uint4*>(da + lower_frag(m, s) * 1024) = round2(w[2 * s], w[2 * s + 1]).u;
+            }
+        }
+    }
 }
 
 // ============================================================ scan
-// One workgroup of four waves holds 64 of a head's P columns, a wave 16 of
-// them: its part of the state, N x 16, stays in accumulator tiles from the
-// first chunk to the last, and since an accumulator tile is an operand
-// fragment as it stands, the chain K S -> X -> T X -> U -> K^T U -> S never
-// leaves the wave's registers.  What the waves share are the chunk's left
-// operands, staged in LDS: k (read by rows for K S and, transposed, for
-// K^T U), q, T, Att and v.  The next chunk's loads are in flight meanwhile.
-// Splits (bf16): S, X and U scaled are hi + lo pairs, T too: K S and K^T U
-// take two MFMAs a tile, T X three.  Y is rounded to bf16 in the end, so its
-// products take S and U rounded once (relative 2^-9 each before the output's
-// own 2^-9).
+// One workgroup holds 64 of a head's P columns, a wave 16 of them: its part of
+// the state, N x 16, stays in accumulator tiles from the first chunk to the
+// last, and since an accumulator tile is an operand fragment as it stands, the
+// chain K S -> X -> T X -> K^T U -> S never leaves the wave's registers.  The
+// chunks' left operands, which the waves share, are staged in LDS in two
+// buffers, the next chunk's while this one is computed.
 struct ScanIo {
     const unsigned char *T, *att;
     const float *scal, *across;
     int nc;
+    float *keepS, *keepU;          // kKeep: the state entering each chunk [u][N][P] and U [u][C][P]
+};
+enum { kY = 0, kKeep = 1 };        // forward: y; backward's recomputation: S and U, no y
+
+// ---- bf16 forward
+// With one sequence's head to a workgroup there is one chain to a SIMD, and
+// its latency a chunk is what bounds the kernel.  So four waves do nothing but
+// the chain, and four more everything that is not part of it, on the same
+// SIMDs: they bring the next chunk's k, v and T from memory to LDS, and compute
+// and store the last chunk's y from the S and X fragments that the chain left
+// in LDS.  A chunk costs one barrier.  The chain's LDS reads are issued ahead
+// of the products they feed (sched_barrier: left to itself the compiler reads
+// each fragment just before its use).
+// Splits: S, X, U and T are hi + lo pairs, k is bf16 as it is: K S and K^T U
+// take two MFMAs a tile, T X three; the state's error stays near 2^-18.  Y is
+// rounded to bf16 in the end, so its products take S and Att T rounded once,
+// 2^-9 each, as the output's own rounding, and X as a pair.
+template <int N>
+struct ChainLds {
+    static constexpr int kRow = N * 2;               // bytes of a k row, its 16-byte pieces permuted (piece())
+    static constexpr int vRow = 64 * 2 + 16;
+    static constexpr int KS = N / 32;
+    // The piece of row t that holds entries 8 x .. 8 x + 7.  Both reads of k hit every bank once: by rows (16
+    // consecutive rows, one x) and transposed (rows 4 q .. 4 q + 3, four consecutive x).
+    static __device__ __forceinline__ int piece(int t, int x) {
+        return x ^ (N == 128 ? (t & 3) << 2 | (t >> 2 & 3) : N == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 3) : t >> 2 & 3);
+    }
+    static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow, kin = t + Bytes<false>::split, across = kin + C * 4;
+    static constexpr int buffer = across + 256;
+    static constexpr int kept = (KS + 4) * 1024;     // a wave's S (rounded) and X (split) fragments
+    static constexpr int bytes = 2 * (buffer + 4 * kept);
 };
 
-template <typename T, int N>
+template <int N>
+__global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, ScanIo io) {
+    using LD = ChainLds<N>;
+    constexpr int NT = N / 16, KS = N / 32, nc16 = N / 8;
+    extern __shared__ __align__(16) unsigned char lds_all[];
+    const int tid = threadIdx.x % 256, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
+    const int pb = a.P / 64;
+    // heads of a group, which read the same q and k, on one XCD (workgroups go round the eight of them)
+    int unit = blockIdx.x;
+    const int share = a.H / a.G * pb;
+    if (a.B * a.G % 8 == 0) unit = (unit / 8 / share * 8 + unit % 8) * share + unit / 8 % share;
+    const int p0 = unit % pb * 64, bh = unit / pb, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+    const int len = row_len(a, b), nch = (len + C - 1) / C;
+    const size_t tok0 = (size_t)b * a.L;
+    unsigned char* const kept = lds_all + 2 * LD::buffer + wave * LD::kept + lane * 16;   // + 4 LD::kept a parity
+
+    if (threadIdx.x < 256) {
+        // ------------------------------------------------ the chain
+        // tile n of lane (q, i) holds the state's rows 32 (n / 2) + 8 q + 4 (n % 2) .. +3 of column p
+        const size_t sofs = ((size_t)bh * a.P + p0 + 16 * wave + i) * N + 8 * q;
+        f32x4 S[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            S[n] = a.init_state ? v4(*reinterpret_cast<const float4*>(a.init_state + sofs + 32 * (n / 2) + 4 * (n % 2))) : kZero4;
+        __builtin_amdgcn_s_setprio(3);               // before the other four waves wherever both can issue
+        lds_barrier();
+        for (int c = 0; c < nch; ++c) {
+            const unsigned char* const lds = lds_all + (c & 1) * LD::buffer;
+            unsigned char* const keep = kept + (c & 1) * 4 * LD::kept;
+            Frag kf[4][KS], th[6], tl[6], kt[NT][2];
+            FragBF vf[4];
+            f32x4 kin[4];
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    kf[m][s].u = *reinterpret_cast<const uint4*>(lds + LD::k + (16 * m + i) * LD::kRow + LD::piece(i, 4 * s + q) * 16);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                kin[m] = v4(*reinterpret_cast<const float4*>(lds + LD::kin + (16 * m + 4 * q) * 4));
+                vf[m] = tr_read(lds, LD::v + (16 * m + 4 * q + i / 4) * LD::vRow + (16 * wave + 4 * (i % 4)) * 2);
+            }
+            const float across = *reinterpret_cast<const float*>(lds + LD::across);
+            __builtin_amdgcn_sched_barrier(0);
+            Pair sp[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                sp[s] = split2(S[2 * s], S[2 * s + 1]);
+                *reinterpret_cast<uint4*>(keep + s * 1024) = sp[s].hi.u;
+            }
+            f32x4 R[4], U[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) R[m] = U[m] = kZero4;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) R[m] = mma(R[m], kf[m][s], sp[s].lo);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) R[m] = mma(R[m], kf[m][s], sp[s].hi);
+            }
+#pragma unroll
+            for (int f = 0; f < 6; ++f) {
+                th[f].u = *reinterpret_cast<const uint4*>(lds + LD::t + f * 2048 + lane * 16);
+                tl[f].u = *reinterpret_cast<const uint4*>(lds + LD::t + f * 2048 + 1024 + lane * 16);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // k^T: row i of the state tiles' numbering, K index t
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int r = 4 * q + i / 4, at = LD::piece(r, 4 * (n / 2) + i % 4) * 16 + 8 * (n % 2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const FragBF f = tr_read(lds, LD::k + (32 * s + 16 * e + r) * LD::kRow + at);
+                        kt[n][s].w[2 * e] = f.a;
+                        kt[n][s].w[2 * e + 1] = f.b;
+                    }
+                }
+            f32x4 X[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const f32x4 v = {bf16_lo(vf[m].a), bf16_hi(vf[m].a), bf16_lo(vf[m].b), bf16_hi(vf[m].b)};
+                X[m] = v - kin[m] * R[m];
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) S[n] *= across;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Pair xp = split2(X[2 * s], X[2 * s + 1]);
+                *reinterpret_cast<uint4*>(keep + (KS + 2 * s) * 1024) = xp.hi.u;
+                *reinterpret_cast<uint4*>(keep + (KS + 2 * s + 1) * 1024) = xp.lo.u;
+#pragma unroll
+                for (int x = 0; x < 3; ++x)
+#pragma unroll
+                    for (int m = 2 * s; m < 4; ++m) {
+                        const int f = lower_frag(m, s);
+                        U[m] = x == 0 ? mma(U[m], tl[f], xp.hi) : mma(U[m], th[f], x == 1 ? xp.lo : xp.hi);
+                    }
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Pair up = split2(U[2 * s], U[2 * s + 1]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) S[n] = mma(S[n], kt[n][s], up.lo);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) S[n] = mma(S[n], kt[n][s], up.hi);
+            }
+            lds_barrier();
+        }
+        if (a.final_state) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                *reinterpret_cast<float4*>(a.final_state + sofs + 32 * (n / 2) + 4 * (n % 2)) = f4(S[n]);
+        }
+        return;
+    }
+    // ---------------------------------------------------- staging and y
+    constexpr int NK = C * nc16 / 256, NV = 2, NTp = Bytes<false>::split / 4096;
+    // two chunks are on their way at any time, in register sets of their parity: one chunk's time is less than
+    // the memory's latency under this kernel's own load
+    u32x4_t rk[2][NK], rv[2][NV], rt[2][NTp];
+    float rs[2];
+    const unsigned char* kb = static_cast<const unsigned char*>(a.k) + (tok0 * a.k_stride + (size_t)g * N) * 2;
+    const unsigned char* qb = static_cast<const unsigned char*>(a.q) + (tok0 * a.q_stride + (size_t)g * N) * 2;
+    const unsigned char* vb = static_cast<const unsigned char*>(a.v) + (tok0 * a.v_stride + (size_t)h * a.P + p0) * 2;
+    unsigned char* yb = static_cast<unsigned char*>(a.y) + tok0 * a.y_stride * 2;
+    const uint32_t k_row = (uint32_t)a.k_stride * 2, q_row = (uint32_t)a.q_stride * 2, v_row = (uint32_t)a.v_stride * 2;
+    const uint32_t y_row = (uint32_t)a.y_stride * 2, y_col = (uint32_t)(h * a.P + p0 + 16 * (q & 1) + 8 * (q >> 1)) * 2;
+    // No branch stands between the loads, the stores and the waits for them, so
+    // that the waits can count: a chunk number past the end is the last one's,
+    // rows past the sequence read its last row (k and v of them become zeros on
+    // their way to LDS), and their y falls out of the buffer's range.
+    auto fetch = [&](int c, auto set) {
+        constexpr int Z = decltype(set)::value;
+        c = min(c, nch - 1);
+        const size_t u = (size_t)bh * io.nc + c;
+        const int n_on = min(C, len - c * C);
+        const unsigned char *kc = kb + (size_t)c * C * k_row, *vc = vb + (size_t)c * C * v_row;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int e = tid + 256 * j, t = min(e / nc16, n_on - 1), x = e % nc16;
+            rk[Z][j] = *reinterpret_cast<const u32x4_t*>(kc + ((uint32_t)t * k_row + x * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int e = tid + 256 * j, t = min(e / 8, n_on - 1), x = e % 8;
+            rv[Z][j] = *reinterpret_cast<const u32x4_t*>(vc + ((uint32_t)t * v_row + x * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < NTp; ++j) rt[Z][j] = *reinterpret_cast<const u32x4_t*>(io.T + u * Bytes<false>::split + (tid + 256 * j) * 16);
+        const float* sc = tid < C ? io.scal + (u * kScal + kKin) * C + tid : io.across + u;
+        rs[Z] = *sc;
+    };
+    auto stage = [&](int c, auto set) {
+        constexpr int Z = decltype(set)::value;
+        unsigned char* const lds = lds_all + (c & 1) * LD::buffer;
+        const int n_on = len - min(c, nch - 1) * C;
+        const u32x4_t zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int e = tid + 256 * j, t = e / nc16, x = e % nc16;
+            *reinterpret_cast<u32x4_t*>(lds + LD::k + t * LD::kRow + LD::piece(t, x) * 16) = t < n_on ? rk[Z][j] : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int e = tid + 256 * j, t = e / 8, x = e % 8;
+            *reinterpret_cast<u32x4_t*>(lds + LD::v + t * LD::vRow + x * 16) = t < n_on ? rv[Z][j] : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < NTp; ++j) *reinterpret_cast<u32x4_t*>(lds + LD::t + (tid + 256 * j) * 16) = rt[Z][j];
+        if (tid < 128) *reinterpret_cast<float*>(lds + LD::kin + min(tid, C) * 4) = rs[Z];
+    };
+    // y: this wave's 16 tokens of all 64 columns, so that each piece of q and Att T is read by one wave
+    Frag qf[2][KS], af[2][2];
+    float qin[2];
+    auto fetch_q = [&](int c, auto set) {
+        constexpr int Z = decltype(set)::value;
+        c = min(c, nch - 1);
+        const size_t u = (size_t)bh * io.nc + c;
+        const int t = min(16 * wave + i, min(C, len - c * C) - 1);
+        const unsigned char* qc = qb + ((size_t)c * C + t) * q_row + 16 * q;
+        qin[Z] = io.scal[(u * kScal + kQin) * C + 16 * wave + i];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[Z][s].u = *reinterpret_cast<const uint4*>(qc + 64 * s);
+        const unsigned char* ac = io.att + u * Bytes<false>::att + lane * 16;
+        af[Z][0].u = *reinterpret_cast<const uint4*>(ac + lower_frag(wave, 0) * 1024);
+        af[Z][1].u = *reinterpret_cast<const uint4*>(ac + lower_frag(wave, wave / 2) * 1024);   // waves 2 and 3: their second
+    };
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
+    if (nch > 0) {
+        fetch(0, even);
+        stage(0, even);
+        fetch(1, odd);
+        fetch(2, even);
+        fetch_q(0, even);
+        fetch_q(1, odd);
+    }
+    lds_barrier();
+    // while the chain is at chunk c (of parity Z): chunk c + 1 to LDS, c + 3 on its way; behind the barrier, beside
+    // chunk c + 1, y of c
+    auto body = [&](int c, auto set, auto other) {
+        constexpr int Z = decltype(set)::value;
+        stage(c + 1, other);
+        fetch(c + 3, other);
+        lds_barrier();
+        const unsigned char* const keep = lds_all + 2 * LD::buffer + (c & 1) * 4 * LD::kept + lane * 16;
+        f32x4 O[4];
+#pragma unroll
+        for (int w0 = 0; w0 < 4; w0 += 2) {          // the chain's waves, 16 columns each, two at a time
+            Frag f[2][KS + 4];
+#pragma unroll
+            for (int x = 0; x < KS + 4; ++x)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) f[w][x].u = *reinterpret_cast<const uint4*>(keep + (w0 + w) * LD::kept + x * 1024);
+            __builtin_amdgcn_sched_barrier(0);
+            O[w0] = O[w0 + 1] = kZero4;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) O[w0 + w] = mma(O[w0 + w], f[w][s], qf[Z][s]);   // [p][t]
+#pragma unroll
+            for (int w = 0; w < 2; ++w) O[w0 + w] *= qin[Z];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) O[w0 + w] = mma(O[w0 + w], f[w][KS + x], af[Z][0]);
+            if (wave >= 2) {
+#pragma unroll
+                for (int x = 2; x < 4; ++x)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) O[w0 + w] = mma(O[w0 + w], f[w][KS + x], af[Z][1]);
+            }
+        }
+        fetch_q(c + 2, set);
+        const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(yb + (size_t)c * C * y_row, 0, 0x7fffffff, 0x00020000);
+        const int t = 16 * wave + i;
+        const uint32_t at = c * C + t < len ? (uint32_t)t * y_row + y_col : 0x80000000u;
+#pragma unroll
+        for (int w = 0; w < 4; w += 2) {
+            // lanes of neighbouring rows of 16 exchange halves of two tiles: eight columns a lane, 64 bytes a token
+            const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(O[w][0], O[w][1]), pack_bf16x2(O[w + 1][0], O[w + 1][1]), false, false);
+            const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(O[w][2], O[w][3]), pack_bf16x2(O[w + 1][2], O[w + 1][3]), false, false);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{lo[0], hi[0], lo[1], hi[1]}, yr, at, 32 * w, 0);
+        }
+    };
+    for (int c = 0; c < nch;) {
+        body(c++, even, odd);
+        if (c == nch) break;
+        body(c++, odd, even);
+    }
+    // rows past the sequence are exactly 0
+    for (int t = len + i; t < a.L; t += 16) if (wave % 2 == 0) *reinterpret_cast<uint4*>(yb + (size_t)t * y_row + y_col + 32 * wave) = make_uint4(0, 0, 0, 0);
+}
+
+// ---- fp32 forward, and the backward's recomputation
+template <typename T, int N, int MODE>
 struct ScanLds {
     static constexpr bool F32 = std::is_same<T, float>::value;
     static constexpr int es = sizeof(T);
     static constexpr int kRow = N * es + 16;         // bytes of a k or q row: the odd 16 spreads rows over the banks
     static constexpr int vRow = 64 * es + 16;
-    static constexpr int k = 0, q = k + C * kRow, v = q + C * kRow, t = v + C * vRow;
-    static constexpr int att = t + Bytes<F32>::split, scal = att + Bytes<F32>::att;
-    static constexpr int bytes = scal + kScal * C * 4;
+    static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow, scal = t + Bytes<F32>::split;
+    static constexpr int q = scal + kScal * C * 4, att = q + (MODE == kY ? C * kRow : 0);
+    static constexpr int bytes = att + (MODE == kY ? Bytes<F32>::att : 0);
+    static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
 };
 
-template <typename T, int N>
+template <typename T, int N, int MODE>
 __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo io) {
-    using LD = ScanLds<T, N>;
+    using LD = ScanLds<T, N, MODE>;
     constexpr bool F32 = LD::F32;
-    constexpr int NT = N / 16, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
-    extern __shared__ __align__(16) unsigned char lds[];
+    constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
+    extern __shared__ __align__(16) unsigned char lds_all[];
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
     const int pb = a.P / 64;
     // heads of a group, which read the same q and k, on one XCD (workgroups go round the eight of them)
@@ -396,52 +742,64 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
         S[n] = a.init_state ? v4(*reinterpret_cast<const float4*>(a.init_state + sofs + state_n(n))) : kZero4;
 
     // ---- staging: 16-byte pieces, the next chunk's in registers
-    constexpr int NK = (C * nc16 + 255) / 256, NVp = (C * nv16 + 255) / 256;
+    constexpr int NK = C * nc16 / 256, NVp = C * nv16 / 256;
     constexpr int NTp = (Bytes<F32>::split / 16 + 255) / 256, NA = (Bytes<F32>::att / 16 + 255) / 256;
     u32x4_t rk[NK], rq[NK], rv[NVp], rt[NTp], ra[NA];
     float rs = 0.0f, r_across = 0.0f;
-    const unsigned char* kb = static_cast<const unsigned char*>(a.k) + (size_t)g * N * es;
-    const unsigned char* qb = static_cast<const unsigned char*>(a.q) + (size_t)g * N * es;
-    const unsigned char* vb = static_cast<const unsigned char*>(a.v) + ((size_t)h * a.P + p0) * es;
+    const unsigned char* kb = static_cast<const unsigned char*>(a.k) + (tok0 * a.k_stride + (size_t)g * N) * es;
+    const unsigned char* qb = static_cast<const unsigned char*>(a.q) + (tok0 * a.q_stride + (size_t)g * N) * es;
+    const unsigned char* vb = static_cast<const unsigned char*>(a.v) + (tok0 * a.v_stride + (size_t)h * a.P + p0) * es;
+    const uint32_t k_row = (uint32_t)a.k_stride * es, q_row = (uint32_t)a.q_stride * es, v_row = (uint32_t)a.v_stride * es;
+    // rows past the sequence read its last row here and become zeros on their way to LDS
     auto fetch = [&](int c) {
         const size_t u = (size_t)bh * io.nc + c;
-        const int t0 = c * C;
+        const int n_on = min(C, len - c * C);
+        const unsigned char *kc = kb + (size_t)c * C * k_row, *qc = qb + (size_t)c * C * q_row, *vc = vb + (size_t)c * C * v_row;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
-            const int e = tid + 256 * j, t = e / nc16, x = e % nc16;
-            const bool on = t0 + t < len;
-            const size_t row = tok0 + (on ? t0 + t : 0);
-            rk[j] = on ? *reinterpret_cast<const u32x4_t*>(kb + row * a.k_stride * es + x * 16) : u32x4_t{0, 0, 0, 0};
-            rq[j] = on ? *reinterpret_cast<const u32x4_t*>(qb + row * a.q_stride * es + x * 16) : u32x4_t{0, 0, 0, 0};
+            const int e = tid + 256 * j, t = min(e / nc16, n_on - 1), x = e % nc16;
+            rk[j] = *reinterpret_cast<const u32x4_t*>(kc + ((uint32_t)t * k_row + x * 16));
+            if (MODE == kY) rq[j] = *reinterpret_cast<const u32x4_t*>(qc + ((uint32_t)t * q_row + x * 16));
         }
 #pragma unroll
         for (int j = 0; j < NVp; ++j) {
-            const int e = tid + 256 * j, t = e / nv16, x = e % nv16;
-            const bool on = t0 + t < len;
-            const size_t row = tok0 + (on ? t0 + t : 0);
-            rv[j] = on ? *reinterpret_cast<const u32x4_t*>(vb + row * a.v_stride * es + x * 16) : u32x4_t{0, 0, 0, 0};
+            const int e = tid + 256 * j, t = min(e / nv16, n_on - 1), x = e % nv16;
+            rv[j] = *reinterpret_cast<const u32x4_t*>(vc + ((uint32_t)t * v_row + x * 16));
         }
 #pragma unroll
         for (int j = 0; j < NTp; ++j) {
             const int e = min(tid + 256 * j, Bytes<F32>::split / 16 - 1);
             rt[j] = *reinterpret_cast<const u32x4_t*>(io.T + u * Bytes<F32>::split + e * 16);
         }
+        if (MODE == kY) {
 #pragma unroll
-        for (int j = 0; j < NA; ++j) {
-            const int e = min(tid + 256 * j, Bytes<F32>::att / 16 - 1);
-            ra[j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<F32>::att + e * 16);
+            for (int j = 0; j < NA; ++j) {
+                const int e = min(tid + 256 * j, Bytes<F32>::att / 16 - 1);
+                ra[j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<F32>::att + e * 16);
+            }
         }
         rs = io.scal[u * kScal * C + tid];
         r_across = io.across[u];
     };
-    auto stage = [&]() {
+    auto stage = [&](unsigned char* lds, int c) {
+        const int n_on = len - c * C;
+        const u32x4_t zero = {0, 0, 0, 0};
+        if (n_on < C) {
+#pragma unroll
+            for (int j = 0; j < NK; ++j)
+                if ((tid + 256 * j) / nc16 >= n_on) {
+                    rk[j] = zero;
+                    if (MODE == kY) rq[j] = zero;
+                }
+#pragma unroll
+            for (int j = 0; j < NVp; ++j)
+                if ((tid + 256 * j) / nv16 >= n_on) rv[j] = zero;
+        }
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
             const int e = tid + 256 * j, t = e / nc16, x = e % nc16;
-            if (e < C * nc16) {
-                *reinterpret_cast<u32x4_t*>(lds + LD::k + t * LD::kRow + x * 16) = rk[j];
-                *reinterpret_cast<u32x4_t*>(lds + LD::q + t * LD::kRow + x * 16) = rq[j];
-            }
+            *reinterpret_cast<u32x4_t*>(lds + LD::k + t * LD::kRow + x * 16) = rk[j];
+            if (MODE == kY) *reinterpret_cast<u32x4_t*>(lds + LD::q + t * LD::kRow + x * 16) = rq[j];
         }
 #pragma unroll
         for (int j = 0; j < NVp; ++j) {
@@ -451,123 +809,178 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
 #pragma unroll
         for (int j = 0; j < NTp; ++j)
             if (tid + 256 * j < Bytes<F32>::split / 16) *reinterpret_cast<u32x4_t*>(lds + LD::t + (tid + 256 * j) * 16) = rt[j];
+        if (MODE == kY) {
 #pragma unroll
-        for (int j = 0; j < NA; ++j)
-            if (tid + 256 * j < Bytes<F32>::att / 16) *reinterpret_cast<u32x4_t*>(lds + LD::att + (tid + 256 * j) * 16) = ra[j];
+            for (int j = 0; j < NA; ++j)
+                if (tid + 256 * j < Bytes<F32>::att / 16) *reinterpret_cast<u32x4_t*>(lds + LD::att + (tid + 256 * j) * 16) = ra[j];
+        }
         *reinterpret_cast<float*>(lds + LD::scal + tid * 4) = rs;
     };
-    auto scal4 = [&](int what, int m) {
-        return *reinterpret_cast<const float4*>(lds + LD::scal + (what * C + 16 * m + 4 * q) * 4);
-    };
-    auto frag16 = [&](int ofs) { return *reinterpret_cast<const uint4*>(lds + ofs + lane * 16); };
 
-    T* yp = static_cast<T*>(a.y) + tok0 * a.y_stride + (size_t)h * a.P + p0 + 16 * wave + 4 * q;
-    if (nch > 0) fetch(0);
+    unsigned char* yb = static_cast<unsigned char*>(a.y) + tok0 * a.y_stride * es;
+    const uint32_t y_row = (uint32_t)a.y_stride * es, y_col = (uint32_t)(h * a.P + p0 + 16 * wave + 4 * q) * es;
+    float across = 0.0f;
+    if (nch > 0) {
+        fetch(0);
+        stage(lds_all, 0);
+        across = r_across;
+        if (nch > 1) fetch(1);
+        lds_barrier();
+    }
     for (int c = 0; c < nch; ++c) {
-        __syncthreads();                             // the last chunk's operands have been read
-        stage();
-        const float across = r_across;
-        __syncthreads();
-        if (c + 1 < nch) fetch(c + 1);
-
-        f32x4 U[4];
+        unsigned char* const lds = lds_all + (LD::buffers == 2 && c % 2 ? LD::bytes : 0);
+        auto scal4 = [&](int what, int m) {
+            return v4(*reinterpret_cast<const float4*>(lds + LD::scal + (what * C + 16 * m + 4 * q) * 4));
+        };
+        auto frag16 = [&](int ofs) { return *reinterpret_cast<const uint4*>(lds + ofs + lane * 16); };
+        auto next = [&]() {                          // the next chunk to the other buffer, the one after it on its way
+            if (c + 1 < nch) {
+                stage(lds_all + (LD::buffers == 2 && c % 2 == 0 ? LD::bytes : 0), c + 1);
+                across = r_across;
+                if (c + 2 < nch) fetch(c + 2);
+            }
+        };
+        const float keep = across;                   // of this chunk
+        if constexpr (MODE == kKeep) {
+            float* ks = io.keepS + ((size_t)bh * io.nc + c) * N * a.P + p;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) ks[(size_t)(state_n(n) + r) * a.P] = S[n][r];
+        }
+        f32x4 R[4], X[4], U[4], O[4];
         if constexpr (!F32) {
-            Pair sp[NT / 2];
+            Frag kf[4][KS], th[6], tl[6];
+            FragBF vf[4];
+            f32x4 kin[4], be[4];
 #pragma unroll
-            for (int s = 0; s < NT / 2; ++s) sp[s] = split2(S[2 * s], S[2 * s + 1]);
-            f32x4 X[4], O[4];
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 R = kZero4;
-                O[m] = kZero4;
-#pragma unroll
-                for (int s = 0; s < NT / 2; ++s) {
-                    Frag kf, qf;
-                    kf.u = *reinterpret_cast<const uint4*>(lds + LD::k + (16 * m + i) * LD::kRow + 64 * s + 16 * q);
-                    qf.u = *reinterpret_cast<const uint4*>(lds + LD::q + (16 * m + i) * LD::kRow + 64 * s + 16 * q);
-                    R = mma(R, kf, sp[s].lo);
-                    R = mma(R, kf, sp[s].hi);
-                    O[m] = mma(O[m], sp[s].hi, qf);   // [p][t]
-                }
-                const FragBF vf = tr_read(lds, LD::v + (16 * m + 4 * q + i / 4) * LD::vRow + (16 * wave + 4 * (i % 4)) * 2);
-                const float4 kin = scal4(kKin, m), be = scal4(kBeta, m);
-                X[m][0] = be.x * (bf16_lo(vf.a) - kin.x * R[0]);
-                X[m][1] = be.y * (bf16_hi(vf.a) - kin.y * R[1]);
-                X[m][2] = be.z * (bf16_lo(vf.b) - kin.z * R[2]);
-                X[m][3] = be.w * (bf16_hi(vf.b) - kin.w * R[3]);
-            }
-            const Pair xp[2] = {split2(X[0], X[1]), split2(X[2], X[3])};
+                for (int s = 0; s < KS; ++s)
+                    kf[m][s].u = *reinterpret_cast<const uint4*>(lds + LD::k + (16 * m + i) * LD::kRow + 64 * s + 16 * q);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                U[m] = kZero4;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (s > m / 2) continue;
-                    Frag th, tl;
-                    th.u = frag16(LD::t + lower_frag(m, s) * 2048);
-                    tl.u = frag16(LD::t + lower_frag(m, s) * 2048 + 1024);
-                    U[m] = mma(U[m], tl, xp[s].hi);
-                    U[m] = mma(U[m], th, xp[s].lo);
-                    U[m] = mma(U[m], th, xp[s].hi);
-                }
-            }
-            const Frag ub[2] = {round2(U[0], U[1]), round2(U[2], U[3])};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int t = c * C + 16 * m + i;
-                const float qin = *reinterpret_cast<const float*>(lds + LD::scal + (kQin * C + 16 * m + i) * 4);
-                O[m] *= qin;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (s > m / 2) continue;
-                    Frag af;
-                    af.u = frag16(LD::att + lower_frag(m, s) * 1024);
-                    O[m] = mma(O[m], ub[s], af);
-                }
-                if (t < len)
-                    *reinterpret_cast<uint2*>(yp + (size_t)t * a.y_stride) =
-                        make_uint2(pack_bf16x2(O[m][0], O[m][1]), pack_bf16x2(O[m][2], O[m][3]));
+                kin[m] = scal4(kKin, m);
+                be[m] = scal4(kBeta, m);
+                vf[m] = tr_read(lds, LD::v + (16 * m + 4 * q + i / 4) * LD::vRow + (16 * wave + 4 * (i % 4)) * 2);
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) U[m] *= v4(scal4(kKout, m));
-            const Pair up[2] = {split2(U[0], U[1]), split2(U[2], U[3])};
+            for (int f = 0; f < 6; ++f) {
+                th[f].u = frag16(LD::t + f * 2048);
+                tl[f].u = frag16(LD::t + f * 2048 + 1024);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            Pair sp[KS];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                S[n] *= across;
+            for (int s = 0; s < KS; ++s) sp[s] = split2(S[2 * s], S[2 * s + 1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) R[m] = kZero4;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) R[m] = mma(R[m], kf[m][s], sp[s].lo);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) R[m] = mma(R[m], kf[m][s], sp[s].hi);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // the second half's operands: k^T (row n of the tile pair's numbering, K index t), q, Att
+            Frag kt[NT][2], qf[4][KS], af[6];
+            f32x4 kout[4];
+            float qin[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) kout[m] = scal4(kKout, m);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    // k^T: row n of the tile pair's numbering, K index t
-                    Frag kt;
                     const int col = 32 * (n / 2) + 8 * (i % 4) + 4 * (n % 2);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const FragBF f = tr_read(lds, LD::k + (32 * s + 16 * e + 4 * q + i / 4) * LD::kRow + col * 2);
-                        kt.w[2 * e] = f.a;
-                        kt.w[2 * e + 1] = f.b;
+                        kt[n][s].w[2 * e] = f.a;
+                        kt[n][s].w[2 * e + 1] = f.b;
                     }
-                    S[n] = mma(S[n], kt, up[s].lo);
-                    S[n] = mma(S[n], kt, up[s].hi);
                 }
+            if constexpr (MODE == kY) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    qin[m] = *reinterpret_cast<const float*>(lds + LD::scal + (kQin * C + 16 * m + i) * 4);
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        qf[m][s].u = *reinterpret_cast<const uint4*>(lds + LD::q + (16 * m + i) * LD::kRow + 64 * s + 16 * q);
+                }
+#pragma unroll
+                for (int f = 0; f < 6; ++f) af[f].u = frag16(LD::att + f * 1024);
             }
-        } else {
-            f32x4 X[4], O[4];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                f32x4 R = kZero4;
-                O[m] = kZero4;
+                const f32x4 v = {bf16_lo(vf[m].a), bf16_hi(vf[m].a), bf16_lo(vf[m].b), bf16_hi(vf[m].b)};
+                X[m] = be[m] * (v - kin[m] * R[m]);
+            }
+            const Pair xp[2] = {split2(X[0], X[1]), split2(X[2], X[3])};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) U[m] = kZero4;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int x = 0; x < 3; ++x)
+#pragma unroll
+                    for (int m = 2 * s; m < 4; ++m) {
+                        const int f = lower_frag(m, s);
+                        U[m] = x == 0 ? mma(U[m], tl[f], xp[s].hi) : mma(U[m], th[f], x == 1 ? xp[s].lo : xp[s].hi);
+                    }
+            if constexpr (MODE == kY) {
+                const Pair ub[2] = {split2(U[0], U[1]), split2(U[2], U[3])};
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    O[m] = kZero4;
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) O[m] = mma(O[m], sp[s].hi, qf[m][s]);   // [p][t]
+                    O[m] *= qin[m];
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int m = 2 * s; m < 4; ++m) {
+                        O[m] = mma(O[m], ub[s].lo, af[lower_frag(m, s)]);
+                        O[m] = mma(O[m], ub[s].hi, af[lower_frag(m, s)]);
+                    }
+            }
+            Pair up[2];
+            {
+                f32x4 w[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) w[m] = U[m] * kout[m];
+                up[0] = split2(w[0], w[1]);
+                up[1] = split2(w[2], w[3]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) S[n] *= keep;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) S[n] = mma(S[n], kt[n][s], x ? up[s].hi : up[s].lo);
+        } else {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                R[m] = O[m] = kZero4;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const float4 kf = *reinterpret_cast<const float4*>(lds + LD::k + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4);
-                    const float4 qf = *reinterpret_cast<const float4*>(lds + LD::q + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4);
-                    R = mma_f32(R, kf, f4(S[n]));
-                    O[m] = mma_f32(O[m], f4(S[n]), qf);
+                    R[m] = mma_f32(R[m], kf, f4(S[n]));
+                    if constexpr (MODE == kY) {
+                        const float4 qf = *reinterpret_cast<const float4*>(lds + LD::q + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4);
+                        O[m] = mma_f32(O[m], f4(S[n]), qf);
+                    }
                 }
-                const float4 kin = scal4(kKin, m), be = scal4(kBeta, m);
-                const float k4[4] = {kin.x, kin.y, kin.z, kin.w}, b4[4] = {be.x, be.y, be.z, be.w};
+                const f32x4 kin = scal4(kKin, m), be = scal4(kBeta, m);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float v = *reinterpret_cast<const float*>(lds + LD::v + (16 * m + 4 * q + r) * LD::vRow + (16 * wave + i) * 4);
-                    X[m][r] = b4[r] * (v - k4[r] * R[r]);
+                    X[m][r] = be[r] * (v - kin[r] * R[m][r]);
                 }
             }
 #pragma unroll
@@ -577,21 +990,21 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
                 for (int n = 0; n <= m; ++n)
                     U[m] = mma_f32(U[m], __builtin_bit_cast(float4, frag16(LD::t + tile_id(m, n) * 1024)), f4(X[n]));
             }
+            if constexpr (MODE == kY) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int t = c * C + 16 * m + i;
-                const float qin = *reinterpret_cast<const float*>(lds + LD::scal + (kQin * C + 16 * m + i) * 4);
-                O[m] *= qin;
+                for (int m = 0; m < 4; ++m) {
+                    O[m] *= *reinterpret_cast<const float*>(lds + LD::scal + (kQin * C + 16 * m + i) * 4);
 #pragma unroll
-                for (int n = 0; n <= m; ++n)
-                    O[m] = mma_f32(O[m], f4(U[n]), __builtin_bit_cast(float4, frag16(LD::att + tile_id(m, n) * 1024)));
-                if (t < len) *reinterpret_cast<float4*>(yp + (size_t)t * a.y_stride) = f4(O[m]);
+                    for (int n = 0; n <= m; ++n)
+                        O[m] = mma_f32(O[m], f4(U[n]), __builtin_bit_cast(float4, frag16(LD::att + tile_id(m, n) * 1024)));
+                }
             }
+            f32x4 w[4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) U[m] *= v4(scal4(kKout, m));
+            for (int m = 0; m < 4; ++m) w[m] = U[m] * scal4(kKout, m);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                S[n] *= across;
+                S[n] *= keep;
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const unsigned char* kc = lds + LD::k + (16 * m + 4 * q) * LD::kRow + (16 * n + i) * 4;
@@ -600,19 +1013,46 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
                     kt.y = *reinterpret_cast<const float*>(kc + LD::kRow);
                     kt.z = *reinterpret_cast<const float*>(kc + 2 * LD::kRow);
                     kt.w = *reinterpret_cast<const float*>(kc + 3 * LD::kRow);
-                    S[n] = mma_f32(S[n], kt, f4(U[m]));
+                    S[n] = mma_f32(S[n], kt, f4(w[m]));
                 }
             }
         }
-    }
-    // rows past the sequence are exactly 0
-    for (int t = len + i; t < a.L; t += 16) {
-        if constexpr (F32) *reinterpret_cast<float4*>(yp + (size_t)t * a.y_stride) = make_float4(0, 0, 0, 0);
-        else *reinterpret_cast<uint2*>(yp + (size_t)t * a.y_stride) = make_uint2(0, 0);
-    }
-    if (a.final_state) {
+        if constexpr (LD::buffers == 1) lds_barrier();   // this chunk's operands have been read
+        next();
+        __builtin_amdgcn_sched_barrier(0);
+        // Stores come last and without a branch (rows past the sequence are out
+        // of the buffer's range and dropped): the next chunk's wait for its
+        // loads then counts past them instead of waiting for them.
+        if constexpr (MODE == kY) {
+            const __amdgpu_buffer_rsrc_t yr =
+                __builtin_amdgcn_make_buffer_rsrc(yb + (size_t)c * C * y_row, 0, 0x7fffffff, 0x00020000);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(a.final_state + sofs + state_n(n)) = f4(S[n]);
+            for (int m = 0; m < 4; ++m) {
+                const int t = 16 * m + i;
+                const uint32_t at = c * C + t < len ? (uint32_t)t * y_row + y_col : 0x80000000u;
+                if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, O[m]), yr, at, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{pack_bf16x2(O[m][0], O[m][1]), pack_bf16x2(O[m][2], O[m][3])}, yr, at, 0, 0);
+            }
+        } else {
+            float* ku = io.keepU + ((size_t)bh * io.nc + c) * C * a.P + p;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) ku[(size_t)(16 * m + 4 * q + r) * a.P] = U[m][r];
+        }
+        lds_barrier();
+    }
+    if constexpr (MODE == kY) {
+        // rows past the sequence are exactly 0
+        for (int t = len + i; t < a.L; t += 16) {
+            unsigned char* at = yb + (size_t)t * y_row + y_col;
+            if constexpr (F32) *reinterpret_cast<float4*>(at) = make_float4(0, 0, 0, 0);
+            else *reinterpret_cast<uint2*>(at) = make_uint2(0, 0);
+        }
+        if (a.final_state) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(a.final_state + sofs + state_n(n)) = f4(S[n]);
+        }
     }
 }
 
@@ -632,21 +1072,31 @@ FwdWs fwd_ws(int B, int L, int H, int dtype) {
 
 template <typename T, int N>
 hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
+    constexpr bool F32 = std::is_same<T, float>::value;
+    constexpr int PM = F32 ? kPrepPlain : kPrepScaled;
     const int nc = (a.L + C - 1) / C;
     const FwdWs w = fwd_ws(a.B, a.L, a.H, a.dtype);
     unsigned char* base = static_cast<unsigned char*>(ws);
     PrepOut o{base + w.T, nullptr, base + w.att, reinterpret_cast<float*>(base + w.scal),
               reinterpret_cast<float*>(base + w.across)};
     const int64_t units = (int64_t)a.B * a.H * nc;
-    hipLaunchKernelGGL((ssd_delta_prep_kernel<T, N, false>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0, stream, a,
-                       o, nc);
+    hipLaunchKernelGGL((ssd_delta_prep_kernel<T, N, PM>), dim3((unsigned)((units + kPrepWaves - 1) / kPrepWaves)),
+                       dim3(64 * kPrepWaves), 0, stream, a, o, nc);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    constexpr size_t lds = ScanLds<T, N>::bytes;
-    e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N>), lds);
-    if (e != hipSuccess) return e;
-    ScanIo io{o.T, o.att, o.scal, o.across, nc};
-    hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N>), dim3(a.B * a.H * (a.P / 64)), dim3(256), lds, stream, a, io);
+    ScanIo io{o.T, o.att, o.scal, o.across, nc, nullptr, nullptr};
+    const dim3 grid(a.B * a.H * (a.P / 64));
+    if constexpr (F32) {
+        constexpr size_t lds = (size_t)ScanLds<T, N, kY>::bytes * ScanLds<T, N, kY>::buffers;
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N, kY>), lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kY>), grid, dim3(256), lds, stream, a, io);
+    } else {
+        constexpr size_t lds = ChainLds<N>::bytes;
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N>), lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((ssd_delta_chain_kernel<N>), grid, dim3(512), lds, stream, a, io);
+    }
     return hipGetLastError();
 }
 

@@ -194,6 +194,7 @@ __device__ __forceinline__ f32x4 mma_split(f32x4 acc, const Split4& a0, const Sp
 // tile.
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 #define SSD_LDS __attribute__((address_space(3)))
 
 __device__ __forceinline__ FragBF tr_read(const unsigned char* lds_base, uint32_t byte_off) {
