@@ -641,6 +641,56 @@ int ssd_delta_step(int B, int H, int P, int N, int G, int dtype,
                    float *state, void *y, int64_t y_row_stride, void *stream);
 
 /*
+ * ssd_delta_scan_bwd -- backward (vector-Jacobian product) of
+ * ssd_delta_scan_fwd, for grad_y = dLoss/dy and, where given,
+ * grad_final_state = dLoss/d(final_state).
+ *
+ * The forward is recomputed from the inputs.  Documents and lengths cut
+ * gradients as they cut the forward; gradients behind a row's length are
+ * exactly 0, and grad_y there is not used.
+ *   q, k, v, dt, A, beta, doc_ids, lengths, init_state and the scalars as in
+ *               ssd_delta_scan_fwd
+ *   grad_y  T   [B][L][H*P]
+ *   grad_final_state  f32 [B][H][P][N] or NULL (zero)
+ *   dq, dk  T   [B][L][G*N] (the sums over a group's heads), dv T [B][L][H*P];
+ *               rounded once to T
+ *   ddt, dbeta  f32 [B][L][H]: with respect to the raw values where
+ *               dt_softplus / beta_sigmoid are 1
+ *   dA      f32 [H]: with respect to A (the caller chains A = -exp(A_log))
+ *   ddt_bias f32 [H] or NULL (written when dt_softplus = 1)
+ *   grad_init_state  f32 [B][H][P][N] or NULL; must not be grad_final_state's
+ *               or another input's memory
+ *   workspace, workspace_bytes: required, at least
+ *               ssd_delta_scan_bwd_workspace_size() bytes, 16-byte aligned,
+ *               caller-owned, not shared by concurrent calls
+ * Results are deterministic: a group's heads are summed in one workgroup, dA
+ * and ddt_bias through per-chunk partial sums added in a fixed order.  Outputs
+ * must not overlap the inputs or each other.  L = 0 writes zero dA and
+ * ddt_bias and copies grad_final_state through.
+ */
+int ssd_delta_scan_bwd(int B, int L, int H, int P, int N, int G, int chunk, int dtype,
+                       const void *q, int64_t q_row_stride,
+                       const void *k, int64_t k_row_stride,
+                       const void *v, int64_t v_row_stride,
+                       const float *dt, int64_t dt_row_stride, int dt_softplus, const float *dt_bias,
+                       const float *A,
+                       const float *beta, int64_t beta_row_stride, int beta_sigmoid,
+                       float scale, int qk_norm,
+                       const int32_t *doc_ids, const int32_t *lengths, const float *init_state,
+                       const void *grad_y, int64_t grad_y_row_stride, const float *grad_final_state,
+                       void *dq, int64_t dq_row_stride,
+                       void *dk, int64_t dk_row_stride,
+                       void *dv, int64_t dv_row_stride,
+                       float *ddt, int64_t ddt_row_stride,
+                       float *dbeta, int64_t dbeta_row_stride,
+                       float *dA, float *ddt_bias, float *grad_init_state,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of ssd_delta_scan_bwd: every chunk's T, its transpose and
+ * M o Q K^T, the state entering and the adjoint leaving it, U and Z. */
+size_t ssd_delta_scan_bwd_workspace_size(int B, int L, int H, int P, int N, int G, int dtype);
+
+/*
  * ssd_norm_fwd -- the norm of R rows of `groups` times W columns, every group
  * of W columns by itself (groups = 1: the whole row; groups = H, W = P: every
  * head of a token's row):

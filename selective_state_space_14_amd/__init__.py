@@ -35,7 +35,8 @@ __all__ = ["load", "ssd_conv_fwd", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_sta
            "ssd_s6_scan_fwd", "ssd_chunk_scan_workspace_size", "ssd_mixer_workspace_size", "ssd_s6_workspace_size",
            "ssd_chunk_scan_bwd", "ssd_conv_bwd", "ssd_mixer_bwd", "ssd_chunk_scan_bwd_workspace_size",
            "ssd_conv_bwd_workspace_size", "ssd_mixer_bwd_workspace_size",
-           "ssd_delta_scan_fwd", "ssd_delta_scan_workspace_size", "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
+           "ssd_delta_scan_fwd", "ssd_delta_scan_workspace_size", "ssd_delta_scan_bwd",
+           "ssd_delta_scan_bwd_workspace_size", "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
            "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_ACT_SILU", "SSD_ACT_NONE"]
 
 # SSD_LIBRARY names another build of the same library (the host-sanitized one the ABI checks use)
@@ -111,8 +112,12 @@ def load() -> ctypes.CDLL:
     delta = [P, I64, P, I64, P, I64, P, I64, I, P, P, P, I64, I, F, I]
     lib.ssd_delta_scan_fwd.restype = I
     lib.ssd_delta_scan_fwd.argtypes = [I, I, I, I, I, I, I, I, *delta, P, P, P, P, P, I64, P, SZ, P]
-    lib.ssd_delta_scan_workspace_size.restype = SZ
-    lib.ssd_delta_scan_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.ssd_delta_scan_bwd.restype = I
+    lib.ssd_delta_scan_bwd.argtypes = [I, I, I, I, I, I, I, I, *delta, P, P, P, P, I64, P, P, I64, P, I64, P, I64, P,
+                                       I64, P, I64, P, P, P, P, SZ, P]
+    for nm in ("ssd_delta_scan_workspace_size", "ssd_delta_scan_bwd_workspace_size"):
+        getattr(lib, nm).restype = SZ
+        getattr(lib, nm).argtypes = [I, I, I, I, I, I, I]
     lib.ssd_delta_step.restype = I
     lib.ssd_delta_step.argtypes = [I, I, I, I, I, I, *delta, P, P, I64, P]
     lib.ssd_norm_fwd.restype = I
@@ -710,6 +715,42 @@ def _norm_groups(c, shape, tensors):
     flat = shape[:-2] + (g * W,)
     return n // g, g, {name: c.rows(None if t is None else t.flatten(-2), name, dtype, flat)
                        for name, (t, dtype) in tensors.items()}
+
+
+def ssd_delta_scan_bwd_workspace_size(B, L, H, P, N, G, dtype=SSD_BF16) -> int:
+    return int(load().ssd_delta_scan_bwd_workspace_size(B, L, H, P, N, G, dtype))
+
+
+def ssd_delta_scan_bwd(q, k, v, dt, A, beta, grad_y, *, H, P, N, G, scale=None, qk_norm=False, dt_softplus=False,
+                       dt_bias=None, beta_sigmoid=False, doc_ids=None, lengths=None, init_state=None,
+                       grad_final_state=None, chunk=64, workspace=None, stream=None):
+    """Backward of ssd_delta_scan_fwd; grad_y [B, L, H*P] in q's dtype, grad_final_state [B, H, P, N] fp32 or None.
+    Returns a dict: q, k, v in q's dtype, dt, beta [B, L, H] and A [H] fp32, and where those inputs are given (dt_bias:
+    where dt_softplus is) dt_bias [H] and init_state [B, H, P, N] fp32.  A workspace is allocated here when none is
+    passed."""
+    lib = load()
+    c = _Call(q, "q")
+    dtype = _dtype_code(q, "q")
+    B, L, T = q.shape[0], q.shape[1], q.dtype
+    head = _delta_head(c, (B, L), T, q, k, v, dt, A, beta, H, P, N, G, scale, qk_norm, dt_softplus, dt_bias, beta_sigmoid)
+    gp, gs = c.rows(grad_y, "grad_y", T, (B, L, H * P))
+    f32, same, state = dict(dtype=torch.float32, device=c.dev), dict(dtype=T, device=c.dev), (B, H, P, N)
+    g = {"q": torch.empty(B, L, G * N, **same), "k": torch.empty(B, L, G * N, **same),
+         "v": torch.empty(B, L, H * P, **same), "dt": torch.empty(B, L, H, **f32), "beta": torch.empty(B, L, H, **f32),
+         "A": torch.empty(H, **f32)}
+    if dt_softplus:
+        g["dt_bias"] = torch.empty(H, **f32)
+    if init_state is not None:
+        g["init_state"] = torch.empty(state, **f32)
+    ws = _ws(workspace, ssd_delta_scan_bwd_workspace_size(B, L, H, P, N, G, dtype), c.dev)
+    out = lambda n: g[n].data_ptr() if n in g else None  # noqa: E731
+    c.run(lib.ssd_delta_scan_bwd,
+          (B, L, H, P, N, G, chunk, dtype, *head, c.vec(doc_ids, "doc_ids", torch.int32, (B, L)),
+           c.vec(lengths, "lengths", torch.int32, (B,)), c.vec(init_state, "init_state", torch.float32, state), gp, gs,
+           c.vec(grad_final_state, "grad_final_state", torch.float32, state), out("q"), G * N, out("k"), G * N, out("v"),
+           H * P, out("dt"), H, out("beta"), H, out("A"), out("dt_bias"), out("init_state"), c.ptr(ws, "workspace"),
+           ws.numel() * ws.element_size()), stream)
+    return g
 
 
 def ssd_norm_fwd(x, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, out_dtype=None, y=None, stream=None):

@@ -19,7 +19,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssd.so")
-SOURCES = ["api.cpp", "conv.hip", "scan.hip", "step.hip", "s6.hip", "bwd.hip", "norm.hip", "delta_step.hip", "delta.hip"]
+SOURCES = ["api.cpp", "conv.hip", "scan.hip", "step.hip", "s6.hip", "bwd.hip", "norm.hip", "delta_step.hip", "delta.hip", "delta_bwd.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -31,7 +31,7 @@ CFLAGS = [
 
 # accumulators in vector registers: the delta rule's kernels feed them to vector instructions and to the next product,
 # and copies from and to accumulation registers were a sixth of their instructions
-EXTRA_CFLAGS = {"delta.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA_CFLAGS = {s: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for s in ("delta.hip", "delta_bwd.hip")}
 
 
 def _compile(src: str, obj_dir: str) -> str:

@@ -1077,6 +1077,95 @@ int ssd_delta_scan_fwd(int B, int L, int H, int P, int N, int G, int chunk, int 
     return hip_status(fn, ssd::launch_delta_fwd(a, workspace, s));
 }
 
+size_t ssd_delta_scan_bwd_workspace_size(int B, int L, int H, int P, int N, int G, int dtype) {
+    if (B <= 0 || L <= 0 || H <= 0 || P <= 0 || N <= 0 || G <= 0) return 0;
+    return ssd::delta_bwd_workspace_bytes(B, L, H, P, N, dtype);
+}
+
+int ssd_delta_scan_bwd(int B, int L, int H, int P, int N, int G, int chunk, int dtype,
+                       const void* q, int64_t q_row_stride,
+                       const void* k, int64_t k_row_stride,
+                       const void* v, int64_t v_row_stride,
+                       const float* dt, int64_t dt_row_stride, int dt_softplus, const float* dt_bias,
+                       const float* A,
+                       const float* beta, int64_t beta_row_stride, int beta_sigmoid,
+                       float scale, int qk_norm,
+                       const int32_t* doc_ids, const int32_t* lengths, const float* init_state,
+                       const void* grad_y, int64_t grad_y_row_stride, const float* grad_final_state,
+                       void* dq, int64_t dq_row_stride,
+                       void* dk, int64_t dk_row_stride,
+                       void* dv, int64_t dv_row_stride,
+                       float* ddt, int64_t ddt_row_stride,
+                       float* dbeta, int64_t dbeta_row_stride,
+                       float* dA, float* ddt_bias, float* grad_init_state,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssd_delta_scan_bwd";
+    ssd::DeltaBwdArgs a{};
+    a.f = delta_args(B, L, H, P, N, G, dtype, q, q_row_stride, k, k_row_stride, v, v_row_stride, dt, dt_row_stride,
+                     dt_softplus, dt_bias, A, beta, beta_row_stride, beta_sigmoid, scale, qk_norm);
+    a.f.doc = doc_ids; a.f.lengths = lengths; a.f.init_state = init_state;
+    a.gy = grad_y; a.gy_stride = grad_y_row_stride;
+    a.g_final = grad_final_state; a.g_init = grad_init_state;
+    a.dq = dq; a.dq_stride = dq_row_stride;
+    a.dk = dk; a.dk_stride = dk_row_stride;
+    a.dv = dv; a.dv_stride = dv_row_stride;
+    a.ddt = ddt; a.ddt_stride = ddt_row_stride;
+    a.dbeta = dbeta; a.dbeta_stride = dbeta_row_stride;
+    a.dA = dA; a.ddt_bias = dt_softplus ? ddt_bias : nullptr;
+    const bool work = B > 0 && L > 0;
+    const int es = esize(dtype);
+    const int64_t HP = (int64_t)H * P, GN = (int64_t)G * N;
+    TRY(check_delta(fn, a.f, work));
+    if (chunk != 64) return fail(SSD_ERR_UNSUPPORTED, "%s: chunk=%d is not supported (must be 64)", fn, chunk);
+    TRY(check_tensor(fn, "grad_y", grad_y, grad_y_row_stride, HP, es, work));
+    TRY(check_tensor(fn, "dq", dq, dq_row_stride, GN, es, work));
+    TRY(check_tensor(fn, "dk", dk, dk_row_stride, GN, es, work));
+    TRY(check_tensor(fn, "dv", dv, dv_row_stride, HP, es, work));
+    if (work) {
+        if (!ddt) return fail(SSD_ERR_NULL_ARG, "%s: ddt is NULL", fn);
+        if (!dbeta) return fail(SSD_ERR_NULL_ARG, "%s: dbeta is NULL", fn);
+        if (ddt_row_stride < H || dbeta_row_stride < H)
+            return fail(SSD_ERR_BAD_SHAPE, "%s: ddt / dbeta row strides (%lld, %lld) are smaller than H=%d", fn,
+                        (long long)ddt_row_stride, (long long)dbeta_row_stride, H);
+        if (grad_y_row_stride > (1 << 22) || dq_row_stride > (1 << 22) || dk_row_stride > (1 << 22) ||
+            dv_row_stride > (1 << 22) || ddt_row_stride > (1 << 22) || dbeta_row_stride > (1 << 22))
+            return fail(SSD_ERR_BAD_SHAPE, "%s: row strides above 4194304 elements are not supported", fn);
+    }
+    TRY(check_ptr(fn, "ddt", ddt, false, false));
+    TRY(check_ptr(fn, "dbeta", dbeta, false, false));
+    TRY(check_ptr(fn, "dA", dA, B > 0, false));
+    TRY(check_ptr(fn, "ddt_bias", ddt_bias, false, false));
+    TRY(check_ptr(fn, "init_state", init_state, false, true));
+    TRY(check_ptr(fn, "grad_final_state", grad_final_state, false, true));
+    TRY(check_ptr(fn, "grad_init_state", grad_init_state, false, true));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!work) {
+        if (B > 0) {
+            TRY(hip_status(fn, ssd::launch_zero_f32(dA, (size_t)H, s)));
+            TRY(hip_status(fn, ssd::launch_zero_f32(a.ddt_bias, (size_t)H, s)));
+            if (grad_init_state)
+                return hip_status(fn, ssd::launch_copy16(grad_final_state, grad_init_state, (size_t)B * HP * N * 4 / 16, s));
+        }
+        return ok();
+    }
+    const void* outs[] = {dq, dk, dv, ddt, dbeta, dA, a.ddt_bias, grad_init_state};
+    const void* ins[] = {q, k, v, dt, beta, A, init_state, grad_y, grad_final_state};
+    for (int i = 0; i < 8; ++i) {
+        if (!outs[i]) continue;
+        for (const void* in : ins)
+            if (outs[i] == in) return fail(SSD_ERR_BAD_SHAPE, "%s: an output must not alias an input", fn);
+        for (int j = 0; j < i; ++j)
+            if (outs[i] == outs[j]) return fail(SSD_ERR_BAD_SHAPE, "%s: two outputs must not alias each other", fn);
+    }
+    const size_t need = ssd_delta_scan_bwd_workspace_size(B, L, H, P, N, G, dtype);
+    if (!workspace || workspace_bytes < need)
+        return fail(SSD_ERR_WORKSPACE, "%s: workspace_bytes=%zu is smaller than the required %zu", fn,
+                    workspace ? workspace_bytes : (size_t)0, need);
+    if (!aligned16(workspace))
+        return fail(SSD_ERR_ALIGNMENT, "%s: workspace=%p is not 16-byte aligned", fn, workspace);
+    return hip_status(fn, ssd::launch_delta_bwd(a, workspace, s));
+}
+
 int ssd_delta_step(int B, int H, int P, int N, int G, int dtype,
                    const void* q, int64_t q_row_stride,
                    const void* k, int64_t k_row_stride,

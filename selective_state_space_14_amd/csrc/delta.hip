@@ -46,45 +46,6 @@ enum Prep {
     kPrepBwd = 2,                  // backward: T, its transpose, Att's transposed product's operand (all split)
 };
 
-struct PrepOut {
-    unsigned char *T, *TT, *att;   // per unit, as above
-    float* scal;                   // [u][kScal][C]
-    float* across;                 // [u]
-};
-
-template <typename T>
-struct Rows;                       // 8 consecutive entries of a row
-template <>
-struct Rows<uint16_t> {
-    Frag f;
-    __device__ __forceinline__ void load(const uint16_t* p) { f.u = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void clear() { f.u = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ float sq() const {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float lo = bf16_lo(f.w[i]), hi = bf16_hi(f.w[i]);
-            s = fmaf(lo, lo, fmaf(hi, hi, s));
-        }
-        return s;
-    }
-    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Rows& a, const Rows& b) { return mma(acc, a.f, b.f); }
-};
-template <>
-struct Rows<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = *reinterpret_cast<const float4*>(p);
-        b = *reinterpret_cast<const float4*>(p + 4);
-    }
-    __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
-    __device__ __forceinline__ float sq() const {
-        return a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w + b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
-    }
-    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Rows& x, const Rows& y) {
-        return mma_f32(mma_f32(acc, x.a, y.a), x.b, y.b);
-    }
-};
 
 __device__ __forceinline__ double shfl_up_f64(double v, int d) {
     const long long b = __double_as_longlong(v);
@@ -276,8 +237,16 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
         }
     }
     {
-        float* sc = o.scal + u * kScal * C;
+        constexpr int NS = PM == kPrepBwd ? kScalBwd : kScal;
+        float* sc = o.scal + u * NS * C;
         const float rk = tok[kRk][lane];
+        if (PM == kPrepBwd) {
+            sc[kSGhi * C + lane] = ghi;
+            sc[kSGlo * C + lane] = tok[kGlo][lane];
+            sc[kSSeg * C + lane] = (float)seg;
+            sc[kSRk * C + lane] = rk;
+            sc[kSRq * C + lane] = tok[kRq][lane];
+        }
         sc[kKin * C + lane] = into * rk;
         sc[kKout * C + lane] = out * rk;
         sc[kQin * C + lane] = into * tok[kRq][lane];
@@ -721,6 +690,7 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
     using LD = ScanLds<T, N, MODE>;
     constexpr bool F32 = LD::F32;
     constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
+    constexpr int NS = MODE == kY ? kScal : kScalBwd;
     extern __shared__ __align__(16) unsigned char lds_all[];
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
     const int pb = a.P / 64;
@@ -778,7 +748,7 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
                 ra[j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<F32>::att + e * 16);
             }
         }
-        rs = io.scal[u * kScal * C + tid];
+        rs = io.scal[u * NS * C + tid];
         r_across = io.across[u];
     };
     auto stage = [&](unsigned char* lds, int c) {
@@ -1100,6 +1070,31 @@ hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <typename T, int N>
+hipError_t launch_keep_n(const DeltaArgs& a, const PrepOut& o, float* keepS, float* keepU, hipStream_t stream) {
+    const int nc = (a.L + C - 1) / C;
+    const int64_t units = (int64_t)a.B * a.H * nc;
+    hipLaunchKernelGGL((ssd_delta_prep_kernel<T, N, kPrepBwd>), dim3((unsigned)((units + kPrepWaves - 1) / kPrepWaves)),
+                       dim3(64 * kPrepWaves), 0, stream, a, o, nc);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    constexpr size_t lds = (size_t)ScanLds<T, N, kKeep>::bytes * ScanLds<T, N, kKeep>::buffers;
+    e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N, kKeep>), lds);
+    if (e != hipSuccess) return e;
+    ScanIo io{o.T, nullptr, o.scal, o.across, nc, keepS, keepU};
+    hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kKeep>), dim3(a.B * a.H * (a.P / 64)), dim3(256), lds, stream, a, io);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t launch_keep_t(const DeltaArgs& a, const PrepOut& o, float* keepS, float* keepU, hipStream_t stream) {
+    switch (a.N) {
+        case 32: return launch_keep_n<T, 32>(a, o, keepS, keepU, stream);
+        case 64: return launch_keep_n<T, 64>(a, o, keepS, keepU, stream);
+        case 128: return launch_keep_n<T, 128>(a, o, keepS, keepU, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
 template <typename T>
 hipError_t launch_fwd_t(const DeltaArgs& a, void* ws, hipStream_t stream) {
     switch (a.N) {
@@ -1111,6 +1106,12 @@ hipError_t launch_fwd_t(const DeltaArgs& a, void* ws, hipStream_t stream) {
 }
 
 }  // namespace
+
+namespace delta {
+hipError_t launch_keep(const DeltaArgs& a, const PrepOut& o, float* keepS, float* keepU, hipStream_t stream) {
+    return a.dtype == 0 ? launch_keep_t<float>(a, o, keepS, keepU, stream) : launch_keep_t<uint16_t>(a, o, keepS, keepU, stream);
+}
+}  // namespace delta
 
 size_t delta_fwd_workspace_bytes(int B, int L, int H, int dtype) { return fwd_ws(B, L, H, dtype).total; }
 

@@ -1,0 +1,770 @@
+// delta_bwd.hip -- backward of the gated delta rule.
+//
+// With dS the adjoint of the state leaving a chunk and the forward's T, U and
+// S0 (delta_device.hpp), x o y the row-wise products:
+//     dU = Att^T dY + e^{G_C - G} o K dS         Z = T^T dU         dV = beta o Z
+//     dS0 = e^{G_C} dS + (scale e^G o Q)^T dY - (beta e^G o K)^T Z
+// and from dAtt = dY U^T, dL = -Z U^T, W1 = dY S0^T, W2 = Z S0^T, W3 = U dS^T
+//     dQ = scale e^G o W1 + (scale M o dAtt) K
+//     dK = e^{G_C - G} o W3 - beta e^G o W2 + (scale M o dAtt)^T Q + (D + D^T) K,   D = beta M o dL
+//     dbeta_t = Z_t.V_t - e^{G_t} K_t.W2_t + sum_j dL_tj M_tj k_t.k_j
+//     dG_t = row sums - column sums of dAtt o Att + dL o L, + scale e^{G_t} Q_t.W1_t - beta_t e^{G_t} K_t.W2_t
+//            - e^{G_C - G_t} K_t.W3_t, and at the chunk's end + sum of the last + e^{G_C} <S0, dS>
+//     d(dt A)_t = sum of dG behind t in the chunk
+// Row and column sums are taken of the same fp32 entries, so pairs on one side
+// of t cancel to fp32 rounding whatever the products' own error.
+//
+// Launches: delta.hip's prep (T, T^T, Att, scalars) and forward chain (S0 and U
+// of every chunk), the reverse chain here (dS and Z of every chunk), then all
+// chunks at once (the gradients), then dA's and ddt_bias's sums.
+#include <hip/hip_runtime.h>
+#include <algorithm>
+#include <type_traits>
+
+#include "delta_device.hpp"
+
+namespace ssd {
+namespace {
+
+using namespace delta;
+
+struct BwdIo {
+    const unsigned char *TT, *att;
+    const float *scal, *across;    // [u][kScalBwd][C], [u]
+    const float *S, *U;            // [u][N][P], [u][C][P]
+    float *D, *Z;                  // as S and U: the adjoint leaving each chunk, Z
+    float* part;                   // [2][B * nc][H]
+    int nc;
+};
+
+// ============================================================ the reverse chain
+// As the forward's: a wave holds 16 columns of dS from the last chunk to the
+// first, the chunk's left operands (k and q both ways, Att^T, T^T, dY) staged
+// in LDS ahead of it.  Bound by the chain's latency, like the forward.
+template <typename T, int N>
+struct RevLds {
+    static constexpr bool F32 = std::is_same<T, float>::value;
+    static constexpr int es = sizeof(T);
+    static constexpr int kRow = N * es + 16, dRow = 64 * es + 16;
+    static constexpr int k = 0, q = k + C * kRow, d = q + C * kRow, tt = d + C * dRow;
+    static constexpr int att = tt + Bytes<F32>::split, scal = att + Bytes<F32>::split;
+    static constexpr int bytes = scal + kScal * C * 4;
+    static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
+};
+
+template <typename T, int N>
+__global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba, BwdIo io) {
+    using LD = RevLds<T, N>;
+    constexpr bool F32 = LD::F32;
+    constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
+    extern __shared__ __align__(16) unsigned char lds_all[];
+    const DeltaArgs& a = ba.f;
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
+    const int pb = a.P / 64;
+    int unit = blockIdx.x;
+    const int share = a.H / a.G * pb;                // heads of a group on one XCD
+    if (a.B * a.G % 8 == 0) unit = (unit / 8 / share * 8 + unit % 8) * share + unit / 8 % share;
+    const int p0 = unit % pb * 64, bh = unit / pb, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+    const int len = row_len(a, b), nch = (len + C - 1) / C;
+    const size_t tok0 = (size_t)b * a.L;
+    const int p = p0 + 16 * wave + i;
+    auto state_n = [&](int n) { return F32 ? 16 * n + 4 * q : 32 * (n / 2) + 8 * q + 4 * (n % 2); };
+    const size_t sofs = ((size_t)bh * a.P + p) * N;
+    f32x4 D[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        D[n] = ba.g_final ? v4(*reinterpret_cast<const float4*>(ba.g_final + sofs + state_n(n))) : kZero4;
+
+    constexpr int NK = C * nc16 / 256, NVp = C * nv16 / 256, NTp = (Bytes<F32>::split / 16 + 255) / 256;
+    u32x4_t rk[NK], rq[NK], rd[NVp], rt[NTp], ra[NTp];
+    float rs = 0.0f, r_across = 0.0f;
+    const unsigned char* kb = static_cast<const unsigned char*>(a.k) + (tok0 * a.k_stride + (size_t)g * N) * es;
+    const unsigned char* qb = static_cast<const unsigned char*>(a.q) + (tok0 * a.q_stride + (size_t)g * N) * es;
+    const unsigned char* db = static_cast<const unsigned char*>(ba.gy) + (tok0 * ba.gy_stride + (size_t)h * a.P + p0) * es;
+    const uint32_t k_row = (uint32_t)a.k_stride * es, q_row = (uint32_t)a.q_stride * es, d_row = (uint32_t)ba.gy_stride * es;
+    auto fetch = [&](int c) {
+        const size_t u = (size_t)bh * io.nc + c;
+        const int n_on = min(C, len - c * C);
+        const unsigned char *kc = kb + (size_t)c * C * k_row, *qc = qb + (size_t)c * C * q_row, *dc = db + (size_t)c * C * d_row;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int e = tid + 256 * j, t = min(e / nc16, n_on - 1), x = e % nc16;
+            rk[j] = *reinterpret_cast<const u32x4_t*>(kc + ((uint32_t)t * k_row + x * 16));
+            rq[j] = *reinterpret_cast<const u32x4_t*>(qc + ((uint32_t)t * q_row + x * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < NVp; ++j) {
+            const int e = tid + 256 * j, t = min(e / nv16, n_on - 1), x = e % nv16;
+            rd[j] = *reinterpret_cast<const u32x4_t*>(dc + ((uint32_t)t * d_row + x * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < NTp; ++j) {
+            const int e = min(tid + 256 * j, Bytes<F32>::split / 16 - 1);
+            rt[j] = *reinterpret_cast<const u32x4_t*>(io.TT + u * Bytes<F32>::split + e * 16);
+            ra[j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<F32>::split + e * 16);
+        }
+        rs = io.scal[u * kScalBwd * C + tid];
+        r_across = io.across[u];
+    };
+    auto stage = [&](unsigned char* lds, int c) {
+        const int n_on = len - c * C;
+        const u32x4_t zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int e = tid + 256 * j, t = e / nc16, x = e % nc16;
+            *reinterpret_cast<u32x4_t*>(lds + LD::k + t * LD::kRow + x * 16) = t < n_on ? rk[j] : zero;
+            *reinterpret_cast<u32x4_t*>(lds + LD::q + t * LD::kRow + x * 16) = t < n_on ? rq[j] : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < NVp; ++j) {
+            const int e = tid + 256 * j, t = e / nv16, x = e % nv16;
+            *reinterpret_cast<u32x4_t*>(lds + LD::d + t * LD::dRow + x * 16) = t < n_on ? rd[j] : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < NTp; ++j)
+            if (tid + 256 * j < Bytes<F32>::split / 16) {
+                *reinterpret_cast<u32x4_t*>(lds + LD::tt + (tid + 256 * j) * 16) = rt[j];
+                *reinterpret_cast<u32x4_t*>(lds + LD::att + (tid + 256 * j) * 16) = ra[j];
+            }
+        *reinterpret_cast<float*>(lds + LD::scal + tid * 4) = rs;
+    };
+    float across = 0.0f;
+    if (nch > 0) {
+        fetch(nch - 1);
+        stage(lds_all + (LD::buffers == 2 && (nch - 1) % 2 ? LD::bytes : 0), nch - 1);
+        across = r_across;
+        if (nch > 1) fetch(nch - 2);
+        lds_barrier();
+    }
+    for (int c = nch - 1; c >= 0; --c) {
+        unsigned char* const lds = lds_all + (LD::buffers == 2 && c % 2 ? LD::bytes : 0);
+        auto scal4 = [&](int what, int m) {
+            return v4(*reinterpret_cast<const float4*>(lds + LD::scal + (what * C + 16 * m + 4 * q) * 4));
+        };
+        auto frag16 = [&](int ofs) { return *reinterpret_cast<const uint4*>(lds + ofs + lane * 16); };
+        const float keep = across;
+        const size_t u = (size_t)bh * io.nc + c;
+        f32x4 Z[4], W[4], Y[4];                      // dU then Z; dY times qin, and -beta kin Z
+        {
+            float* kd = io.D + u * N * a.P + p;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) kd[(size_t)(state_n(n) + r) * a.P] = D[n][r];
+        }
+        if constexpr (!F32) {
+            Pair sp[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) sp[s] = split2(D[2 * s], D[2 * s + 1]);
+            Frag df[2];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const FragBF f = tr_read(lds, LD::d + (16 * m + 4 * q + i / 4) * LD::dRow + (16 * wave + 4 * (i % 4)) * 2);
+                df[m / 2].w[2 * (m % 2)] = f.a;
+                df[m / 2].w[2 * (m % 2) + 1] = f.b;
+                const f32x4 y = {bf16_lo(f.a), bf16_hi(f.a), bf16_lo(f.b), bf16_hi(f.b)};
+                Y[m] = y * scal4(kQin, m);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                W[m] = kZero4;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    Frag kf;
+                    kf.u = *reinterpret_cast<const uint4*>(lds + LD::k + (16 * m + i) * LD::kRow + 64 * s + 16 * q);
+                    W[m] = mma(W[m], kf, sp[s].lo);
+                    W[m] = mma(W[m], kf, sp[s].hi);
+                }
+                W[m] *= scal4(kKout, m);
+#pragma unroll
+                for (int s = m / 2; s < 2; ++s) {
+                    Frag ah, al;
+                    ah.u = frag16(LD::att + upper_frag(m, s) * 2048);
+                    al.u = frag16(LD::att + upper_frag(m, s) * 2048 + 1024);
+                    W[m] = mma(W[m], al, df[s]);
+                    W[m] = mma(W[m], ah, df[s]);
+                }
+            }
+            const Pair up[2] = {split2(W[0], W[1]), split2(W[2], W[3])};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                Z[m] = kZero4;
+#pragma unroll
+                for (int s = m / 2; s < 2; ++s) {
+                    Frag th, tl;
+                    th.u = frag16(LD::tt + upper_frag(m, s) * 2048);
+                    tl.u = frag16(LD::tt + upper_frag(m, s) * 2048 + 1024);
+                    Z[m] = mma(Z[m], tl, up[s].hi);
+                    Z[m] = mma(Z[m], th, up[s].lo);
+                    Z[m] = mma(Z[m], th, up[s].hi);
+                }
+                W[m] = -Z[m] * scal4(kKin, m) * scal4(kBeta, m);
+            }
+            const Pair yp[2] = {split2(Y[0], Y[1]), split2(Y[2], Y[3])}, zp[2] = {split2(W[0], W[1]), split2(W[2], W[3])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                D[n] *= keep;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int col = 32 * (n / 2) + 8 * (i % 4) + 4 * (n % 2);
+                    Frag kt, qt;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 32 * s + 16 * e + 4 * q + i / 4;
+                        const FragBF f = tr_read(lds, LD::k + row * LD::kRow + col * 2), z = tr_read(lds, LD::q + row * LD::kRow + col * 2);
+                        kt.w[2 * e] = f.a;
+                        kt.w[2 * e + 1] = f.b;
+                        qt.w[2 * e] = z.a;
+                        qt.w[2 * e + 1] = z.b;
+                    }
+                    D[n] = mma(D[n], qt, yp[s].lo);
+                    D[n] = mma(D[n], kt, zp[s].lo);
+                    D[n] = mma(D[n], qt, yp[s].hi);
+                    D[n] = mma(D[n], kt, zp[s].hi);
+                }
+            }
+        } else {
+            f32x4 d4[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    d4[m][r] = *reinterpret_cast<const float*>(lds + LD::d + (16 * m + 4 * q + r) * LD::dRow + (16 * wave + i) * 4);
+                Y[m] = d4[m] * scal4(kQin, m);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                W[m] = kZero4;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    W[m] = mma_f32(W[m], *reinterpret_cast<const float4*>(lds + LD::k + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4), f4(D[n]));
+                W[m] *= scal4(kKout, m);
+#pragma unroll
+                for (int t = m; t < 4; ++t)
+                    W[m] = mma_f32(W[m], __builtin_bit_cast(float4, frag16(LD::att + tile_id(t, m) * 1024)), f4(d4[t]));
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                Z[m] = kZero4;
+#pragma unroll
+                for (int t = m; t < 4; ++t)
+                    Z[m] = mma_f32(Z[m], __builtin_bit_cast(float4, frag16(LD::tt + tile_id(t, m) * 1024)), f4(W[t]));
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) W[m] = -Z[m] * scal4(kKin, m) * scal4(kBeta, m);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                D[n] *= keep;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    auto col = [&](int base) {
+                        const unsigned char* at = lds + base + (16 * m + 4 * q) * LD::kRow + (16 * n + i) * 4;
+                        return make_float4(*reinterpret_cast<const float*>(at), *reinterpret_cast<const float*>(at + LD::kRow),
+                                           *reinterpret_cast<const float*>(at + 2 * LD::kRow), *reinterpret_cast<const float*>(at + 3 * LD::kRow));
+                    };
+                    D[n] = mma_f32(D[n], col(LD::q), f4(Y[m]));
+                    D[n] = mma_f32(D[n], col(LD::k), f4(W[m]));
+                }
+            }
+        }
+        if constexpr (LD::buffers == 1) lds_barrier();
+        if (c > 0) {
+            stage(lds_all + (LD::buffers == 2 && c % 2 == 0 ? LD::bytes : 0), c - 1);
+            across = r_across;
+            if (c > 1) fetch(c - 2);
+        }
+        float* kz = io.Z + u * C * a.P + p;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) kz[(size_t)(16 * m + 4 * q + r) * a.P] = Z[m][r];
+        lds_barrier();
+    }
+    if (ba.g_init) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(ba.g_init + sofs + state_n(n)) = f4(D[n]);
+    }
+}
+
+// ============================================================ the gradients
+// One workgroup a chunk and group; its heads in turn, dQ and dK of the group
+// summed over them in registers, in order.  Wave w has the tokens 16 w .. +15
+// as the columns of its tiles, so every token's scalars are one a lane, and
+// products come out as [n][t] or [j][t]: W^T = S0 [n][p] x dY, Z, U [t][p], and
+// dAtt^T, dL^T [j][t], whose tiles are again operands for dQ^T and dK^T of the
+// wave's own tokens; the tiles that other waves' keys need go through LDS.
+// U and the state are read once from memory by 16-row tiles, one wave each,
+// and shared as fragments (P in halves of 64 columns, S0 and then dS in one
+// buffer).
+template <typename T, int N>
+struct GradLds {
+    static constexpr int es = sizeof(T);
+    static constexpr int kRow = N * es + 16, gRow = C * es + 16;
+    static constexpr int k = 0, q = k + C * kRow, s = q + C * kRow;
+    static constexpr int s_bytes = std::max(N * 256, 2 * C * gRow);   // a half of S0 or dS; then the two [j][t] matrices
+    static constexpr int u = s + s_bytes, scal = u + 16 * 1024;
+    static constexpr int col = scal + kScalBwd * C * 4;               // [4][C] column sums
+    static constexpr int row = col + 4 * C * 4;                       // [3][C]: dG's rows, its W3 part, dbeta
+    static constexpr int dot = row + 3 * C * 4;                       // [4] <S0, dS>
+    static constexpr int bytes = dot + 64;
+};
+
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
+
+// four consecutive entries of a row, and their store
+__device__ __forceinline__ f32x4 ld4t(const unsigned char* p, uint16_t) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return f32x4{bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+}
+__device__ __forceinline__ f32x4 ld4t(const unsigned char* p, float) { return v4(*reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ void st4t(uint16_t* p, f32x4 v) { *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])); }
+__device__ __forceinline__ void st4t(float* p, f32x4 v) { *reinterpret_cast<float4*>(p) = f4(v); }
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return fmaf(a[3], b[3], fmaf(a[2], b[2], fmaf(a[1], b[1], a[0] * b[0]))); }
+
+// the sum over 8 entries of z * v
+__device__ __forceinline__ float dot8(const float4& a, const float4& b, const Rows<float>& v) {
+    return a.x * v.a.x + a.y * v.a.y + a.z * v.a.z + a.w * v.a.w + b.x * v.b.x + b.y * v.b.y + b.z * v.b.z + b.w * v.b.w;
+}
+__device__ __forceinline__ float dot8(const float4& a, const float4& b, const Rows<uint16_t>& v) {
+    const uint32_t* w = v.f.w;
+    return a.x * bf16_lo(w[0]) + a.y * bf16_hi(w[0]) + a.z * bf16_lo(w[1]) + a.w * bf16_hi(w[1]) + b.x * bf16_lo(w[2]) +
+           b.y * bf16_hi(w[2]) + b.z * bf16_lo(w[3]) + b.w * bf16_hi(w[3]);
+}
+
+// two [j][t] tiles (K blocks of 16) as an operand of the last products, rounded to bf16 there: its outputs are bf16
+template <typename T>
+struct Last;
+template <>
+struct Last<uint16_t> {
+    Frag f;
+    __device__ __forceinline__ void set(f32x4 a, f32x4 b) { f = round2(a, b); }
+    // row j of a [j][t] matrix, K blocks 2 s and 2 s + 1
+    __device__ __forceinline__ void row(const unsigned char* p, int s, int q) {
+        const FragBF x = plain_read(p + (32 * s + 4 * q) * 2), y = plain_read(p + (32 * s + 16 + 4 * q) * 2);
+        f.w[0] = x.a; f.w[1] = x.b; f.w[2] = y.a; f.w[3] = y.b;
+    }
+    // column n of rows t of k or q: the transposed operand [n][t], 16-row tile at column n0
+    __device__ __forceinline__ void tr(const unsigned char* base, int ofs, int row_bytes, int s, int n0, int q, int i) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const FragBF x = tr_read(base, ofs + (32 * s + 16 * e + 4 * q + i / 4) * row_bytes + (n0 + 4 * (i % 4)) * 2);
+            f.w[2 * e] = x.a;
+            f.w[2 * e + 1] = x.b;
+        }
+    }
+    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Last& a, const Last& b) { return mma(acc, a.f, b.f); }
+};
+template <>
+struct Last<float> {
+    float4 a, b;
+    __device__ __forceinline__ void set(f32x4 x, f32x4 y) { a = f4(x); b = f4(y); }
+    __device__ __forceinline__ void row(const unsigned char* p, int s, int q) {
+        a = *reinterpret_cast<const float4*>(p + (32 * s + 4 * q) * 4);
+        b = *reinterpret_cast<const float4*>(p + (32 * s + 16 + 4 * q) * 4);
+    }
+    __device__ __forceinline__ void tr(const unsigned char* base, int ofs, int row_bytes, int s, int n0, int q, int i) {
+        const unsigned char* p = base + ofs + (32 * s + 4 * q) * row_bytes + (n0 + i) * 4;
+        auto at = [&](int t) { return *reinterpret_cast<const float*>(p + t * row_bytes); };
+        a = make_float4(at(0), at(1), at(2), at(3));
+        b = make_float4(at(16), at(17), at(18), at(19));
+    }
+    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Last& x, const Last& y) { return mma_f32(mma_f32(acc, x.a, y.a), x.b, y.b); }
+};
+
+template <typename T, int N>
+__global__ __launch_bounds__(256) void ssd_delta_grad_kernel(DeltaBwdArgs ba, BwdIo io) {
+    using LD = GradLds<T, N>;
+    constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16;
+    extern __shared__ __align__(16) unsigned char lds[];
+    const DeltaArgs& a = ba.f;
+    const int tid = threadIdx.x, lane = tid % 64, q = lane / 16, i = lane % 16;
+    const int w = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int g = blockIdx.x % a.G, c = blockIdx.x / a.G % io.nc, b = blockIdx.x / a.G / io.nc;
+    const int hg = a.H / a.G, t0 = c * C, n_on = min(C, row_len(a, b) - t0), n_rows = min(C, a.L - t0);
+    const size_t tok0 = (size_t)b * a.L + t0;
+    const size_t bc = (size_t)b * io.nc + c, parts = (size_t)a.B * io.nc * a.H;
+    T* dq = static_cast<T*>(ba.dq) + tok0 * ba.dq_stride + (size_t)g * N;
+    T* dk = static_cast<T*>(ba.dk) + tok0 * ba.dk_stride + (size_t)g * N;
+    T* dv = static_cast<T*>(ba.dv) + tok0 * ba.dv_stride + (size_t)g * hg * a.P;
+    if (n_on <= 0) {                                 // nothing real in the chunk: zero gradients
+        for (int e = tid; e < n_rows * N / 4; e += 256) {
+            st4t(dq + (size_t)(e / (N / 4)) * ba.dq_stride + e % (N / 4) * 4, kZero4);
+            st4t(dk + (size_t)(e / (N / 4)) * ba.dk_stride + e % (N / 4) * 4, kZero4);
+        }
+        const int wide = hg * a.P / 4;
+        for (int e = tid; e < n_rows * wide; e += 256) st4t(dv + (size_t)(e / wide) * ba.dv_stride + e % wide * 4, kZero4);
+        for (int e = tid; e < n_rows * hg; e += 256) {
+            ba.ddt[(tok0 + e / hg) * ba.ddt_stride + g * hg + e % hg] = 0.0f;
+            ba.dbeta[(tok0 + e / hg) * ba.dbeta_stride + g * hg + e % hg] = 0.0f;
+        }
+        for (int e = tid; e < hg; e += 256) io.part[bc * a.H + g * hg + e] = io.part[parts + bc * a.H + g * hg + e] = 0.0f;
+        return;
+    }
+    // ---- k and q of the chunk
+    {
+        const unsigned char* kc = static_cast<const unsigned char*>(a.k) + (tok0 * a.k_stride + (size_t)g * N) * es;
+        const unsigned char* qc = static_cast<const unsigned char*>(a.q) + (tok0 * a.q_stride + (size_t)g * N) * es;
+        const u32x4_t zero = {0, 0, 0, 0};
+        for (int e = tid; e < C * nc16; e += 256) {
+            const int t = e / nc16, x = e % nc16, r = min(t, n_on - 1);
+            const u32x4_t vk = *reinterpret_cast<const u32x4_t*>(kc + (size_t)r * a.k_stride * es + x * 16);
+            const u32x4_t vq = *reinterpret_cast<const u32x4_t*>(qc + (size_t)r * a.q_stride * es + x * 16);
+            *reinterpret_cast<u32x4_t*>(lds + LD::k + t * LD::kRow + x * 16) = t < n_on ? vk : zero;
+            *reinterpret_cast<u32x4_t*>(lds + LD::q + t * LD::kRow + x * 16) = t < n_on ? vq : zero;
+        }
+    }
+    const int t = 16 * w + i;                        // this lane's token
+    const bool on = t < n_on;
+    const size_t trow = tok0 + min(t, n_on - 1);
+    f32x4 dQ[NT], dK[NT];                            // [n][t]
+#pragma unroll
+    for (int n = 0; n < NT; ++n) dQ[n] = dK[n] = kZero4;
+    float* colp = reinterpret_cast<float*>(lds + LD::col);
+    float* rowp = reinterpret_cast<float*>(lds + LD::row);
+    float* dotp = reinterpret_cast<float*>(lds + LD::dot);
+
+    for (int hh = 0; hh < hg; ++hh) {
+        const int h = g * hg + hh;
+        const size_t u = ((size_t)b * a.H + h) * io.nc + c;
+        for (int e = tid; e < kScalBwd * C; e += 256) *reinterpret_cast<float*>(lds + LD::scal + e * 4) = io.scal[u * kScalBwd * C + e];
+        const float beta = io.scal[(u * kScalBwd + kBeta) * C + t];
+        f32x4 W1[NT], W2[NT], W3[NT], EA[4], EL[4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) W1[n] = W2[n] = W3[n] = kZero4;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) EA[n] = EL[n] = kZero4;
+        float zv = 0.0f, sd = 0.0f;
+        for (int p0 = 0; p0 < a.P; p0 += 64) {
+            // the wave's own rows t: dY, Z, U as operands; dV; U's tile for everyone
+            Rows<T> dy[2];
+            Wide<T> z[2], uw[2], ds[(NT + 3) / 4][2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int col = p0 + 32 * s + 8 * q;
+                Rows<T> v;
+                dy[s].load(static_cast<const T*>(ba.gy) + trow * ba.gy_stride + (size_t)h * a.P + col);
+                v.load(static_cast<const T*>(a.v) + trow * a.v_stride + (size_t)h * a.P + col);
+                if (!on) {
+                    dy[s].clear();
+                    v.clear();
+                }
+                const float* zp = io.Z + (u * C + t) * a.P + col;
+                const float* up = io.U + (u * C + t) * a.P + col;
+                const float4 z0 = *reinterpret_cast<const float4*>(zp), z1 = *reinterpret_cast<const float4*>(zp + 4);
+                z[s].set(z0, z1);
+                uw[s].set(*reinterpret_cast<const float4*>(up), *reinterpret_cast<const float4*>(up + 4));
+                uw[s].put(lds + LD::u + (w * 2 + s) * 2048 + lane * 16);
+                zv += dot8(z0, z1, v);
+                if (t < n_rows) {
+                    T* dst = dv + (size_t)t * ba.dv_stride + (size_t)hh * a.P + col;
+                    st4t(dst, v4(z0) * beta);
+                    st4t(dst + 4, v4(z1) * beta);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < (NT + 3) / 4; ++j) {
+                const int n = w + 4 * j;
+                if (n < NT) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const size_t at = (u * N + 16 * n + i) * a.P + p0 + 32 * s + 8 * q;
+                        const float4 s0 = *reinterpret_cast<const float4*>(io.S + at), s1 = *reinterpret_cast<const float4*>(io.S + at + 4);
+                        const float4 d0 = *reinterpret_cast<const float4*>(io.D + at), d1 = *reinterpret_cast<const float4*>(io.D + at + 4);
+                        sd += dot4(v4(s0), v4(d0)) + dot4(v4(s1), v4(d1));
+                        ds[j][s].set(d0, d1);
+                        Wide<T> f;
+                        f.set(s0, s1);
+                        f.put(lds + LD::s + (n * 2 + s) * 2048 + lane * 16);
+                    }
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                if (n > w) continue;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    Wide<T> f;
+                    f.get(lds + LD::u + (n * 2 + s) * 2048 + lane * 16);
+                    EA[n] = Wide<T>::mul(EA[n], f, dy[s]);
+                    EL[n] = Wide<T>::mul(EL[n], f, z[s]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    Wide<T> f;
+                    f.get(lds + LD::s + (n * 2 + s) * 2048 + lane * 16);
+                    W1[n] = Wide<T>::mul(W1[n], f, dy[s]);
+                    W2[n] = Wide<T>::mul(W2[n], f, z[s]);
+                }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < (NT + 3) / 4; ++j) {
+                const int n = w + 4 * j;
+                if (n < NT) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) ds[j][s].put(lds + LD::s + (n * 2 + s) * 2048 + lane * 16);
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    Wide<T> f;
+                    f.get(lds + LD::s + (n * 2 + s) * 2048 + lane * 16);
+                    W3[n] = Wide<T>::mul(W3[n], f, uw[s]);
+                }
+            __syncthreads();
+        }
+        auto sc1 = [&](int what) { return *reinterpret_cast<const float*>(lds + LD::scal + (what * C + t) * 4); };
+        auto sc4 = [&](int what, int n) { return v4(*reinterpret_cast<const float4*>(lds + LD::scal + (what * C + 16 * n + 4 * q) * 4)); };
+        const float kin = sc1(kKin), kout = sc1(kKout), qin = sc1(kQin), rk = sc1(kSRk), rq = sc1(kSRq);
+        const float th = sc1(kSGhi), tl = sc1(kSGlo), ts = sc1(kSSeg);
+        // ---- the state's parts, and their row products
+        float r1 = 0.0f, r2 = 0.0f, r3 = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const f32x4 k4 = ld4t(lds + LD::k + t * LD::kRow + (16 * n + 4 * q) * es, T()), q4 = ld4t(lds + LD::q + t * LD::kRow + (16 * n + 4 * q) * es, T());
+            W1[n] *= qin;
+            W2[n] *= kin;
+            W3[n] *= kout;
+            r1 += dot4(W1[n], q4);
+            r2 += dot4(W2[n], k4);
+            r3 += dot4(W3[n], k4);
+            dQ[n] += W1[n];
+            dK[n] += W3[n] - beta * W2[n];
+        }
+        // ---- the chunk's own pairs: [j][t], j = 16 n + 4 q + r <= t
+        Rows<T> ko[KS], qo[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            ko[s].load(reinterpret_cast<const T*>(lds + LD::k + t * LD::kRow) + 32 * s + 8 * q);
+            qo[s].load(reinterpret_cast<const T*>(lds + LD::q + t * LD::kRow) + 32 * s + 8 * q);
+        }
+        float rsum = 0.0f, bsum = 0.0f;
+        unsigned char *g1 = lds + LD::s, *g2 = g1 + C * LD::gRow;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            f32x4 x1 = kZero4, x2 = kZero4, cs = kZero4;
+            if (n <= w) {
+                f32x4 kk = kZero4, qk = kZero4;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    Rows<T> kf;
+                    kf.load(reinterpret_cast<const T*>(lds + LD::k + (16 * n + i) * LD::kRow) + 32 * s + 8 * q);
+                    kk = Rows<T>::mul(kk, kf, ko[s]);
+                    qk = Rows<T>::mul(qk, kf, qo[s]);
+                }
+                const f32x4 h4 = sc4(kSGhi, n), l4 = sc4(kSGlo, n), s4 = sc4(kSSeg, n), rk4 = sc4(kSRk, n);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = 16 * n + 4 * q + r;
+                    const float m = fast_exp2(s4[r] == ts && j <= t ? (th - h4[r]) + (tl - l4[r]) : -INFINITY) * rk4[r];
+                    const bool before = j < t;
+                    x1[r] = EA[n][r] * (m * rq);
+                    x2[r] = before ? -EL[n][r] * (m * rk) : 0.0f;   // without beta
+                    const float ea = before ? x1[r] * qk[r] : 0.0f, el = x2[r] * kk[r];
+                    bsum += el;
+                    cs[r] = fmaf(beta, el, ea);
+                    rsum += cs[r];
+                    x2[r] *= beta;
+                }
+            }
+            EA[n] = x1;
+            EL[n] = x2;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = 16 * n + 4 * q + r;
+                cs[r] = lanes_sum<16>(cs[r]);
+                if (i == 0) colp[w * C + j] = cs[r];
+                if constexpr (es == 2) {
+                    *reinterpret_cast<uint16_t*>(g1 + j * LD::gRow + t * 2) = (uint16_t)f32_to_bf16_bits(x1[r]);
+                    *reinterpret_cast<uint16_t*>(g2 + j * LD::gRow + t * 2) = (uint16_t)f32_to_bf16_bits(x2[r]);
+                } else {
+                    *reinterpret_cast<float*>(g1 + j * LD::gRow + t * 4) = x1[r];
+                    *reinterpret_cast<float*>(g2 + j * LD::gRow + t * 4) = x2[r];
+                }
+            }
+        }
+        {
+            float all[6] = {r1, r2, r3, rsum, bsum, zv};
+#pragma unroll
+            for (int x = 0; x < 6; ++x) all[x] = rows_sum(all[x]);
+            sd = wave_sum(sd);
+            if (q == 0) {
+                rowp[t] = all[3] + all[0] - beta * all[1] - all[2];
+                rowp[C + t] = all[2];
+                rowp[2 * C + t] = all[5] - all[1] + all[4];
+            }
+            if (lane == 0) dotp[w] = sd;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            Last<T> own1, own2, far1, far2;
+            own1.set(EA[2 * s], EA[2 * s + 1]);      // queries and keys of this wave's tokens: K index j
+            own2.set(EL[2 * s], EL[2 * s + 1]);
+            far1.row(g1 + t * LD::gRow, s, q);       // this wave's tokens as keys j: K index t
+            far2.row(g2 + t * LD::gRow, s, q);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                Last<T> kt, qt;
+                kt.tr(lds, LD::k, LD::kRow, s, 16 * n, q, i);
+                qt.tr(lds, LD::q, LD::kRow, s, 16 * n, q, i);
+                dQ[n] = Last<T>::mul(dQ[n], kt, own1);
+                dK[n] = Last<T>::mul(dK[n], kt, own2);
+                dK[n] = Last<T>::mul(dK[n], qt, far1);
+                dK[n] = Last<T>::mul(dK[n], kt, far2);
+            }
+        }
+        if (w == 0) {
+            // one token a lane: d(dt A) is the sum of dG behind it
+            float dG = rowp[lane] - ((colp[lane] + colp[C + lane]) + (colp[2 * C + lane] + colp[3 * C + lane]));
+            const float r3s = wave_sum(rowp[C + lane]), dot = (dotp[0] + dotp[1]) + (dotp[2] + dotp[3]);
+            if (lane == 63) dG += fmaf(io.across[u], dot, r3s);
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const float dn = __shfl_down(dG, d);
+                if (lane + d < 64) dG += dn;
+            }
+            const size_t at = tok0 + min(lane, n_on - 1);
+            float dt = a.dt[at * a.dt_stride + h], chain = 1.0f;
+            const float be = *reinterpret_cast<const float*>(lds + LD::scal + (kBeta * C + lane) * 4);
+            float db = rowp[2 * C + lane];
+            if (a.dt_softplus) {
+                dt += a.dt_bias ? a.dt_bias[h] : 0.0f;
+                chain = 1.0f / (1.0f + expf(-dt));
+                dt = softplus_f(dt);
+            }
+            if (a.beta_sigmoid) db *= be * (1.0f - be);
+            // Every pair across t carries the factor exp(dt A): below e^-30 the true sum is far under the rounding
+            // that the row and column sums leave behind (2^-24 of them), which a large dt would carry into dA.
+            if (dt * a.A[h] < -30.0f) dG = 0.0f;
+            const bool live = lane < n_on;
+            const float dd = live ? dG * a.A[h] * chain : 0.0f;
+            if (lane < n_rows) {
+                ba.ddt[(tok0 + lane) * ba.ddt_stride + h] = dd;
+                ba.dbeta[(tok0 + lane) * ba.dbeta_stride + h] = live ? db : 0.0f;
+            }
+            const float pa = wave_sum(live && dG != 0.0f ? dG * dt : 0.0f), pd = wave_sum(dd);   // dt may be infinite
+            if (lane == 0) {
+                io.part[bc * a.H + h] = pa;
+                io.part[parts + bc * a.H + h] = pd;
+            }
+        }
+        __syncthreads();
+    }
+    // ---- through the norms, and out
+    float sq = 0.0f, sk = 0.0f, dotq = 0.0f, dotk = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const f32x4 k4 = ld4t(lds + LD::k + t * LD::kRow + (16 * n + 4 * q) * es, T()), q4 = ld4t(lds + LD::q + t * LD::kRow + (16 * n + 4 * q) * es, T());
+        sq += dot4(q4, q4);
+        sk += dot4(k4, k4);
+        dotq += dot4(q4, dQ[n]);
+        dotk += dot4(k4, dK[n]);
+    }
+    const float fq = a.qk_norm ? rows_sum(dotq) / (rows_sum(sq) + kQkEps) : 0.0f;
+    const float fk = a.qk_norm ? rows_sum(dotk) / (rows_sum(sk) + kQkEps) : 0.0f;
+    if (t < n_rows) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const f32x4 k4 = ld4t(lds + LD::k + t * LD::kRow + (16 * n + 4 * q) * es, T()), q4 = ld4t(lds + LD::q + t * LD::kRow + (16 * n + 4 * q) * es, T());
+            st4t(dq + (size_t)t * ba.dq_stride + 16 * n + 4 * q, dQ[n] - fq * q4);
+            st4t(dk + (size_t)t * ba.dk_stride + 16 * n + 4 * q, dK[n] - fk * k4);
+        }
+    }
+}
+
+// dA and ddt_bias: the chunks' parts of a head, added in a fixed order
+__global__ __launch_bounds__(256) void ssd_delta_sum_kernel(const float* part, size_t rows, int H, float* dA, float* ddt_bias) {
+    __shared__ float s[256];
+    const int h = blockIdx.x % H, k = blockIdx.x / H;
+    float v = 0.0f;
+    for (size_t r = threadIdx.x; r < rows; r += 256) v += part[(k * rows + r) * H + h];
+    s[threadIdx.x] = v;
+    __syncthreads();
+#pragma unroll
+    for (int d = 128; d > 0; d /= 2) {
+        if (threadIdx.x < d) s[threadIdx.x] += s[threadIdx.x + d];
+        __syncthreads();
+    }
+    float* out = k ? ddt_bias : dA;
+    if (threadIdx.x == 0 && out) out[h] = s[0];
+}
+
+struct BwdWs {
+    size_t T, TT, att, scal, across, S, U, D, Z, part, total;
+};
+BwdWs bwd_ws(int B, int L, int H, int P, int N, int dtype) {
+    const size_t nc = (L + C - 1) / C, units = (size_t)B * H * nc;
+    const size_t split = dtype == 0 ? Bytes<true>::split : Bytes<false>::split;
+    BwdWs w;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at += (n + 255) / 256 * 256;
+        return o;
+    };
+    w.T = take(units * split);
+    w.TT = take(units * split);
+    w.att = take(units * split);
+    w.scal = take(units * kScalBwd * C * 4);
+    w.across = take(units * 4);
+    w.S = take(units * N * P * 4);
+    w.U = take(units * C * P * 4);
+    w.D = take(units * N * P * 4);
+    w.Z = take(units * C * P * 4);
+    w.part = take(2 * units * 4);
+    w.total = at;
+    return w;
+}
+
+template <typename T, int N>
+hipError_t launch_bwd_n(const DeltaBwdArgs& ba, void* ws, hipStream_t stream) {
+    const DeltaArgs& a = ba.f;
+    const int nc = (a.L + C - 1) / C;
+    const BwdWs w = bwd_ws(a.B, a.L, a.H, a.P, N, a.dtype);
+    unsigned char* base = static_cast<unsigned char*>(ws);
+    auto fp = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
+    PrepOut o{base + w.T, base + w.TT, base + w.att, fp(w.scal), fp(w.across)};
+    hipError_t e = launch_keep(a, o, fp(w.S), fp(w.U), stream);
+    if (e != hipSuccess) return e;
+    BwdIo io{o.TT, o.att, o.scal, o.across, fp(w.S), fp(w.U), fp(w.D), fp(w.Z), fp(w.part), nc};
+    constexpr size_t rev = (size_t)RevLds<T, N>::bytes * RevLds<T, N>::buffers, grad = GradLds<T, N>::bytes;
+    e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_reverse_kernel<T, N>), rev);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((ssd_delta_reverse_kernel<T, N>), dim3(a.B * a.H * (a.P / 64)), dim3(256), rev, stream, ba, io);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_grad_kernel<T, N>), grad);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((ssd_delta_grad_kernel<T, N>), dim3((unsigned)((size_t)a.B * nc * a.G)), dim3(256), grad, stream, ba, io);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(ssd_delta_sum_kernel, dim3(2 * a.H), dim3(256), 0, stream, io.part, (size_t)a.B * nc, a.H, ba.dA, ba.ddt_bias);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_bwd_t(const DeltaBwdArgs& a, void* ws, hipStream_t stream) {
+    switch (a.f.N) {
+        case 32: return launch_bwd_n<T, 32>(a, ws, stream);
+        case 64: return launch_bwd_n<T, 64>(a, ws, stream);
+        case 128: return launch_bwd_n<T, 128>(a, ws, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t delta_bwd_workspace_bytes(int B, int L, int H, int P, int N, int dtype) { return bwd_ws(B, L, H, P, N, dtype).total; }
+
+hipError_t launch_delta_bwd(const DeltaBwdArgs& a, void* ws, hipStream_t stream) {
+    return a.f.dtype == 0 ? launch_bwd_t<float>(a, ws, stream) : launch_bwd_t<uint16_t>(a, ws, stream);
+}
+
+}  // namespace ssd

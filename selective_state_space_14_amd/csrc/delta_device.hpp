@@ -39,6 +39,15 @@ struct Bytes {
 };
 // per-token scalars of a unit: four arrays of C
 enum { kKin = 0, kKout = 1, kQin = 2, kBeta = 3, kScal = 4 };
+// the backward's: also the running sum of dt A (log2) as two floats, the document's number within the chunk, and the
+// norms' factors of k and of q times the output's scale
+enum { kSGhi = 4, kSGlo = 5, kSSeg = 6, kSRk = 7, kSRq = 8, kScalBwd = 9 };
+struct PrepOut {
+    unsigned char *T, *TT, *att;   // per unit: T, its transpose, Att or Att T
+    float* scal;                   // [u][kScal][C]
+    float* across;                 // [u]
+};
+
 
 // ------------------------------------------------------------ sums over the four 16-lane rows
 __device__ __forceinline__ float rows_sum(float v) {
@@ -79,10 +88,89 @@ __device__ __forceinline__ float4 f4(const f32x4& a) { return make_float4(a[0], 
 __device__ __forceinline__ f32x4 v4(const float4& a) { return f32x4{a.x, a.y, a.z, a.w}; }
 constexpr f32x4 kZero4 = {0.0f, 0.0f, 0.0f, 0.0f};
 
+// ------------------------------------------------------------ operands read by rows, K contiguous: 32 of K a fragment
+// 8 consecutive entries of a row of the inputs; lane (q, i) holds row i, entries 8 q .. 8 q + 7
+template <typename T>
+struct Rows;
+template <>
+struct Rows<uint16_t> {
+    Frag f;
+    __device__ __forceinline__ void load(const uint16_t* p) { f.u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void clear() { f.u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float sq() const {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float lo = bf16_lo(f.w[i]), hi = bf16_hi(f.w[i]);
+            s = fmaf(lo, lo, fmaf(hi, hi, s));
+        }
+        return s;
+    }
+    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Rows& a, const Rows& b) { return mma(acc, a.f, b.f); }
+};
+template <>
+struct Rows<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ float sq() const {
+        return a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w + b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
+    }
+    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Rows& x, const Rows& y) {
+        return mma_f32(mma_f32(acc, x.a, y.a), x.b, y.b);
+    }
+};
+
+// 8 consecutive entries of a row of fp32 intermediates: two 16-byte words a lane either way
+template <typename T>
+struct Wide;
+template <>
+struct Wide<uint16_t> {
+    Pair p;
+    __device__ __forceinline__ void set(const float4& a, const float4& b) { p = split2(v4(a), v4(b)); }
+    __device__ __forceinline__ void put(unsigned char* at) const {
+        *reinterpret_cast<uint4*>(at) = p.hi.u;
+        *reinterpret_cast<uint4*>(at + 1024) = p.lo.u;
+    }
+    __device__ __forceinline__ void get(const unsigned char* at) {
+        p.hi.u = *reinterpret_cast<const uint4*>(at);
+        p.lo.u = *reinterpret_cast<const uint4*>(at + 1024);
+    }
+    // wide x input, wide x wide
+    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Wide& a, const Rows<uint16_t>& b) {
+        return mma(mma(acc, a.p.lo, b.f), a.p.hi, b.f);
+    }
+    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Wide& a, const Wide& b) {
+        return mma(mma(mma(acc, a.p.lo, b.p.hi), a.p.hi, b.p.lo), a.p.hi, b.p.hi);
+    }
+};
+template <>
+struct Wide<float> {
+    Rows<float> p;
+    __device__ __forceinline__ void set(const float4& a, const float4& b) { p.a = a; p.b = b; }
+    __device__ __forceinline__ void put(unsigned char* at) const {
+        *reinterpret_cast<float4*>(at) = p.a;
+        *reinterpret_cast<float4*>(at + 1024) = p.b;
+    }
+    __device__ __forceinline__ void get(const unsigned char* at) {
+        p.a = *reinterpret_cast<const float4*>(at);
+        p.b = *reinterpret_cast<const float4*>(at + 1024);
+    }
+    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Wide& a, const Rows<float>& b) { return Rows<float>::mul(acc, a.p, b); }
+    static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Wide& a, const Wide& b) { return Rows<float>::mul(acc, a.p, b.p); }
+};
+
 // the real tokens of batch row b
 __device__ __forceinline__ int row_len(const DeltaArgs& a, int b) {
     return a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
 }
+
+// the backward's first launches (delta.hip): every chunk's T, T^T, Att and scalars, then the states entering the
+// chunks [u][N][P] and U [u][C][P]
+hipError_t launch_keep(const DeltaArgs& a, const PrepOut& o, float* keepS, float* keepU, hipStream_t stream);
 
 }  // namespace delta
 }  // namespace ssd

@@ -169,6 +169,21 @@ struct DeltaArgs {
     const float* init_state; float* final_state;   // [B][H][P][N]; the step updates final_state in place
     void* y; int64_t y_stride;             // [B][L][H*P] (dtype)
 };
+// Its backward: gradients of q, k, v in dtype, of dt and beta (with respect to
+// the raw values where softplus / sigmoid are on), A, dt_bias and the states
+// in fp32.
+struct DeltaBwdArgs {
+    DeltaArgs f;                           // final_state and y unused
+    const void* gy; int64_t gy_stride;     // [B][L][H*P] (dtype)
+    const float* g_final;                  // [B][H][P][N] or null
+    void* dq; int64_t dq_stride;
+    void* dk; int64_t dk_stride;
+    void* dv; int64_t dv_stride;
+    float* ddt; int64_t ddt_stride;
+    float* dbeta; int64_t dbeta_stride;
+    float* dA; float* ddt_bias;            // [H]; ddt_bias or null
+    float* g_init;                         // [B][H][P][N] or null
+};
 
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_scan(const ScanArgs& a, hipStream_t stream);
@@ -208,6 +223,8 @@ hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t stream);
 hipError_t prepare_launch(const void* fn, size_t lds);
 size_t delta_fwd_workspace_bytes(int B, int L, int H, int dtype);
 hipError_t launch_delta_fwd(const DeltaArgs& a, void* ws, hipStream_t stream);
+size_t delta_bwd_workspace_bytes(int B, int L, int H, int P, int N, int dtype);
+hipError_t launch_delta_bwd(const DeltaBwdArgs& a, void* ws, hipStream_t stream);
 hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 size_t norm_bwd_workspace_bytes(int64_t R, int W);

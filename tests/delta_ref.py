@@ -16,7 +16,8 @@ def unit(x, norm):
 def gates(dt, beta, softplus, dt_bias, sigmoid):
     dt, beta = dt.to(F64), beta.to(F64)
     if softplus:
-        dt = torch.nn.functional.softplus(dt + (0.0 if dt_bias is None else dt_bias.to(F64)), threshold=1e9)
+        dt = dt + (0.0 if dt_bias is None else dt_bias.to(F64))
+        dt = torch.logaddexp(dt, torch.zeros_like(dt))
     if sigmoid:
         beta = torch.sigmoid(beta)
     return dt, beta
