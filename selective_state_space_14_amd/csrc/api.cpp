@@ -1032,7 +1032,7 @@ static ssd::DeltaArgs delta_args(int B, int L, int H, int P, int N, int G, int d
 
 size_t ssd_delta_scan_workspace_size(int B, int L, int H, int P, int N, int G, int dtype) {
     if (B <= 0 || L <= 0 || H <= 0 || P <= 0 || N <= 0 || G <= 0) return 0;
-    return ssd::delta_fwd_workspace_bytes(B, L, H, dtype);
+    return ssd::delta_fwd_workspace_bytes(B, L, H, P, N, dtype);
 }
 
 int ssd_delta_scan_fwd(int B, int L, int H, int P, int N, int G, int chunk, int dtype,

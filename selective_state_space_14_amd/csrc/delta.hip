@@ -61,9 +61,9 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
     enum { kGhi, kGlo, kSeg, kB, kRk, kRq, kF, kOut, kE, kTok = kE + 3 };
     __shared__ __align__(16) float tok_s[kPrepWaves][kTok][C];
 
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, q = lane / 16, i = lane % 16;
-    const int64_t id = (int64_t)blockIdx.x * kPrepWaves + wave;
-    if (id >= (int64_t)a.B * nc * a.H) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, q = lane / 16, i = lane % 16;
+    const uint32_t id = blockIdx.x * kPrepWaves + wave;   // below 2^31 (api)
+    if (id >= (uint32_t)a.B * nc * a.H) return;
     const int h = (int)(id % a.H), c = (int)(id / a.H % nc), b = (int)(id / a.H / nc);
     const int t0 = c * C, n_on = min(C, row_len(a, b) - t0);
     if (n_on <= 0) return;
@@ -140,28 +140,38 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
     float rq[4];                                     // of column t = 16 m + i, with the output's scale
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        float s = 0.0f, z = 0.0f;
+        // a row's square is the diagonal of its tile's product with itself: entry r = i % 4 of lane (i / 4, i)
+        float rk = 1.0f;
+        rq[m] = a.scale;
+        if (a.qk_norm) {
+            f32x4 kk = kZero4, qq = kZero4;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            s += kf[m][k].sq();
-            z += qf[m][k].sq();
+            for (int s = 0; s < KS; ++s) {
+                kk = Rows<T>::mul(kk, kf[m][s], kf[m][s]);
+                qq = Rows<T>::mul(qq, qf[m][s], qf[m][s]);
+            }
+            const bool odd = i & 1, high = i & 2, mine = q == i / 4;
+            const float k1 = high ? (odd ? kk[3] : kk[2]) : (odd ? kk[1] : kk[0]);
+            const float q1 = high ? (odd ? qq[3] : qq[2]) : (odd ? qq[1] : qq[0]);
+            rk = __builtin_amdgcn_rsqf(rows_sum(mine ? k1 : 0.0f) + kQkEps);
+            rq[m] *= __builtin_amdgcn_rsqf(rows_sum(mine ? q1 : 0.0f) + kQkEps);
         }
-        s = rows_sum(s);
-        z = rows_sum(z);
-        rq[m] = (a.qk_norm ? __builtin_amdgcn_rsqf(z + kQkEps) : 1.0f) * a.scale;
         if (q == 0) {
-            tok[kRk][16 * m + i] = a.qk_norm ? __builtin_amdgcn_rsqf(s + kQkEps) : 1.0f;
+            tok[kRk][16 * m + i] = rk;
             tok[kRq][16 * m + i] = rq[m];
         }
     }
     lds_wait();
     auto row4 = [&](int what, int n) { return v4(*reinterpret_cast<const float4*>(&tok[what][16 * n + 4 * q])); };
     auto col1 = [&](int what, int m) { return tok[what][16 * m + i]; };
-    // the table's decays with k_j's norm
+    // the table's decays with k_j's norm.  The bf16 forward wants T diag(beta) and Att T diag(beta): with beta on the
+    // columns of L instead of its rows, T' = (I + L')^-1 has T diag(beta) = diag(beta) T', and Att T diag(beta) =
+    // (Att diag(beta)) T', so there beta_j joins the table too
     f32x4 rk4[4];
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         rk4[n] = row4(kRk, n);
+        if (PM == kPrepScaled) rk4[n] *= row4(kB, n);
 #pragma unroll
         for (int m = n + 1; m < 4; ++m) {
             const f32x4 e = row4(kE + m - 1, n) * rk4[n];
@@ -175,7 +185,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
     f32x4 at[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        const float ct = col1(kF, m), cb = col1(kB, m) * col1(kRk, m);
+        const float ct = col1(kF, m), cb = PM == kPrepScaled ? col1(kRk, m) : col1(kB, m) * col1(kRk, m);
 #pragma unroll
         for (int n = 0; n <= m; ++n) {
             f32x4 l = kZero4, d;
@@ -251,7 +261,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
         sc[kKout * C + lane] = out * rk;
         sc[kQin * C + lane] = into * tok[kRq][lane];
         sc[kBeta * C + lane] = beta;
-        if (PM == kPrepScaled) tok[kOut][lane] = out * rk;
+        if (PM == kPrepScaled) tok[kOut][lane] = out * rk * beta;
         if (lane == 0) o.across[u] = last == 0 ? fast_exp2((float)Gc) : 0.0f;
     }
     lds_wait();
@@ -311,7 +321,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
         if constexpr (PM == kPrepScaled) {
             const float ko = col1(kOut, m);
 #pragma unroll
-            for (int n = 0; n <= m; ++n) tt[n][m] *= row4(kB, n) * ko;
+            for (int n = 0; n <= m; ++n) tt[n][m] *= ko;
         }
         if constexpr (F32) {
 #pragma unroll
@@ -362,7 +372,6 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (k >= n && k <= m) w[n] = mma_f32(w[n], lt4(n, k), f4(at[k][m]));
-                    w[n] *= row4(kB, n);
                 }
 #pragma unroll
                 for (int s = 0; s < m / 2 + 1; ++s)
@@ -384,6 +393,10 @@ struct ScanIo {
     const float *scal, *across;
     int nc;
     float *keepS, *keepU;          // kKeep: the state entering each chunk [u][N][P] and U [u][C][P]
+    // sequence split: K superchunks of S chunks (K = 1: none).  Of all but the last, the end state from a zero state
+    // [b h][K - 1][P][N] and the transition [b h][K - 1][N columns][N]; the state entering each [b h][K][P][N].
+    int K, S;
+    float *loc, *phi, *s0;
 };
 enum { kY = 0, kKeep = 1 };        // forward: y; backward's recomputation: S and U, no y
 
@@ -400,6 +413,15 @@ enum { kY = 0, kKeep = 1 };        // forward: y; backward's recomputation: S an
 // take two MFMAs a tile, T X three; the state's error stays near 2^-18.  Y is
 // rounded to bf16 in the end, so its products take S and Att T rounded once,
 // 2^-9 each, as the output's own rounding, and X as a pair.
+//
+// Few heads and a long sequence leave most CUs without a chain.  A chunk's
+// step is linear in the state, S' = Phi S + (a part from v), so the sequence
+// is cut into superchunks: one launch (kState) passes over all but the last
+// from a zero state, and with N columns more, which start as the identity and
+// see v = 0, computes their transitions; ssd_delta_join_kernel puts the states
+// entering the superchunks together; the full launch runs them side by side.
+enum { kFull = 0, kState = 1 };
+
 template <int N>
 struct ChainLds {
     static constexpr int kRow = N * 2;               // bytes of a k row, its 16-byte pieces permuted (piece())
@@ -416,19 +438,24 @@ struct ChainLds {
     static constexpr int bytes = 2 * (buffer + 4 * kept);
 };
 
-template <int N>
+template <int N, int MODE>
 __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, ScanIo io) {
     using LD = ChainLds<N>;
     constexpr int NT = N / 16, KS = N / 32, nc16 = N / 8;
     extern __shared__ __align__(16) unsigned char lds_all[];
     const int tid = threadIdx.x % 256, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
-    const int pb = a.P / 64;
+    // blocks of 64 columns of a head: P's, and in the state pass the transition's
+    const int pb = a.P / 64 + (MODE == kState ? (N + 63) / 64 : 0);
+    const int units = a.B * a.H * pb, sk = blockIdx.x / units;
     // heads of a group, which read the same q and k, on one XCD (workgroups go round the eight of them)
-    int unit = blockIdx.x;
+    int unit = blockIdx.x % units;
     const int share = a.H / a.G * pb;
     if (a.B * a.G % 8 == 0) unit = (unit / 8 / share * 8 + unit % 8) * share + unit / 8 % share;
-    const int p0 = unit % pb * 64, bh = unit / pb, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
-    const int len = row_len(a, b), nch = (len + C - 1) / C;
+    const int blk = unit % pb, bh = unit / pb, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+    const bool phi = MODE == kState && blk >= a.P / 64;
+    const int p0 = phi ? 0 : blk * 64;
+    const int len = row_len(a, b), c0 = sk * io.S;
+    const int nch = max(0, min(io.S, (len + C - 1) / C - c0));   // chunks here, counted from c0 below
     const size_t tok0 = (size_t)b * a.L;
     unsigned char* const kept = lds_all + 2 * LD::buffer + wave * LD::kept + lane * 16;   // + 4 LD::kept a parity
 
@@ -436,10 +463,20 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         // ------------------------------------------------ the chain
         // tile n of lane (q, i) holds the state's rows 32 (n / 2) + 8 q + 4 (n % 2) .. +3 of column p
         const size_t sofs = ((size_t)bh * a.P + p0 + 16 * wave + i) * N + 8 * q;
+        const int pc = (blk - a.P / 64) * 64 + 16 * wave + i;   // column of the transition
         f32x4 S[NT];
+        const float* first = MODE == kState ? nullptr
+                             : io.K > 1     ? io.s0 + ((size_t)bh * io.K + sk) * a.P * N + (sofs - (size_t)bh * a.P * N)
+                             : a.init_state ? a.init_state + sofs
+                                            : nullptr;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            S[n] = a.init_state ? v4(*reinterpret_cast<const float4*>(a.init_state + sofs + 32 * (n / 2) + 4 * (n % 2))) : kZero4;
+        for (int n = 0; n < NT; ++n) {
+            S[n] = first ? v4(*reinterpret_cast<const float4*>(first + 32 * (n / 2) + 4 * (n % 2))) : kZero4;
+            if (phi) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[n][r] = 32 * (n / 2) + 8 * q + 4 * (n % 2) + r == pc ? 1.0f : 0.0f;
+            }
+        }
         __builtin_amdgcn_s_setprio(3);               // before the other four waves wherever both can issue
         lds_barrier();
         for (int c = 0; c < nch; ++c) {
@@ -464,7 +501,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 sp[s] = split2(S[2 * s], S[2 * s + 1]);
-                *reinterpret_cast<uint4*>(keep + s * 1024) = sp[s].hi.u;
+                if (MODE == kFull) *reinterpret_cast<uint4*>(keep + s * 1024) = sp[s].hi.u;
             }
             f32x4 R[4], U[4];
 #pragma unroll
@@ -506,8 +543,10 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const Pair xp = split2(X[2 * s], X[2 * s + 1]);
-                *reinterpret_cast<uint4*>(keep + (KS + 2 * s) * 1024) = xp.hi.u;
-                *reinterpret_cast<uint4*>(keep + (KS + 2 * s + 1) * 1024) = xp.lo.u;
+                if (MODE == kFull) {
+                    *reinterpret_cast<uint4*>(keep + (KS + 2 * s) * 1024) = xp.hi.u;
+                    *reinterpret_cast<uint4*>(keep + (KS + 2 * s + 1) * 1024) = xp.lo.u;
+                }
 #pragma unroll
                 for (int x = 0; x < 3; ++x)
 #pragma unroll
@@ -526,10 +565,16 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             }
             lds_barrier();
         }
-        if (a.final_state) {
+        float* last;
+        if (MODE == kState) {
+            const size_t u = (size_t)bh * (io.K - 1) + sk;
+            last = phi ? (pc < N ? io.phi + (u * N + pc) * N + 8 * q : nullptr) : io.loc + (u * a.P + p0 + 16 * wave + i) * N + 8 * q;
+        } else {
+            last = a.final_state && sk == io.K - 1 ? a.final_state + sofs : nullptr;
+        }
+        if (last) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<float4*>(a.final_state + sofs + 32 * (n / 2) + 4 * (n % 2)) = f4(S[n]);
+            for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(last + 32 * (n / 2) + 4 * (n % 2)) = f4(S[n]);
         }
         return;
     }
@@ -551,7 +596,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
     // their way to LDS), and their y falls out of the buffer's range.
     auto fetch = [&](int c, auto set) {
         constexpr int Z = decltype(set)::value;
-        c = min(c, nch - 1);
+        c = c0 + min(c, nch - 1);
         const size_t u = (size_t)bh * io.nc + c;
         const int n_on = min(C, len - c * C);
         const unsigned char *kc = kb + (size_t)c * C * k_row, *vc = vb + (size_t)c * C * v_row;
@@ -573,7 +618,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
     auto stage = [&](int c, auto set) {
         constexpr int Z = decltype(set)::value;
         unsigned char* const lds = lds_all + (c & 1) * LD::buffer;
-        const int n_on = len - min(c, nch - 1) * C;
+        const int n_on = len - (c0 + min(c, nch - 1)) * C;
         const u32x4_t zero = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
@@ -583,7 +628,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int e = tid + 256 * j, t = e / 8, x = e % 8;
-            *reinterpret_cast<u32x4_t*>(lds + LD::v + t * LD::vRow + x * 16) = t < n_on ? rv[Z][j] : zero;
+            *reinterpret_cast<u32x4_t*>(lds + LD::v + t * LD::vRow + x * 16) = t < n_on && !phi ? rv[Z][j] : zero;
         }
 #pragma unroll
         for (int j = 0; j < NTp; ++j) *reinterpret_cast<u32x4_t*>(lds + LD::t + (tid + 256 * j) * 16) = rt[Z][j];
@@ -594,7 +639,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
     float qin[2];
     auto fetch_q = [&](int c, auto set) {
         constexpr int Z = decltype(set)::value;
-        c = min(c, nch - 1);
+        c = c0 + min(c, nch - 1);
         const size_t u = (size_t)bh * io.nc + c;
         const int t = min(16 * wave + i, min(C, len - c * C) - 1);
         const unsigned char* qc = qb + ((size_t)c * C + t) * q_row + 16 * q;
@@ -612,8 +657,10 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         stage(0, even);
         fetch(1, odd);
         fetch(2, even);
-        fetch_q(0, even);
-        fetch_q(1, odd);
+        if (MODE == kFull) {
+            fetch_q(0, even);
+            fetch_q(1, odd);
+        }
     }
     lds_barrier();
     // while the chain is at chunk c (of parity Z): chunk c + 1 to LDS, c + 3 on its way; behind the barrier, beside
@@ -623,6 +670,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         stage(c + 1, other);
         fetch(c + 3, other);
         lds_barrier();
+        if constexpr (MODE == kState) return;
         const unsigned char* const keep = lds_all + 2 * LD::buffer + (c & 1) * 4 * LD::kept + lane * 16;
         f32x4 O[4];
 #pragma unroll
@@ -652,9 +700,9 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             }
         }
         fetch_q(c + 2, set);
-        const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(yb + (size_t)c * C * y_row, 0, 0x7fffffff, 0x00020000);
+        const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(yb + (size_t)(c0 + c) * C * y_row, 0, 0x7fffffff, 0x00020000);
         const int t = 16 * wave + i;
-        const uint32_t at = c * C + t < len ? (uint32_t)t * y_row + y_col : 0x80000000u;
+        const uint32_t at = (c0 + c) * C + t < len ? (uint32_t)t * y_row + y_col : 0x80000000u;
 #pragma unroll
         for (int w = 0; w < 4; w += 2) {
             // lanes of neighbouring rows of 16 exchange halves of two tiles: eight columns a lane, 64 bytes a token
@@ -668,8 +716,55 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         if (c == nch) break;
         body(c++, odd, even);
     }
+    if (MODE == kState) return;
     // rows past the sequence are exactly 0
-    for (int t = len + i; t < a.L; t += 16) if (wave % 2 == 0) *reinterpret_cast<uint4*>(yb + (size_t)t * y_row + y_col + 32 * wave) = make_uint4(0, 0, 0, 0);
+    const int tend = sk == io.K - 1 ? a.L : min(a.L, (c0 + io.S) * C);
+    for (int t = max(len, c0 * C) + i; t < tend; t += 16) if (wave % 2 == 0) *reinterpret_cast<uint4*>(yb + (size_t)t * y_row + y_col + 32 * wave) = make_uint4(0, 0, 0, 0);
+}
+
+// The states entering the superchunks, S_{k+1} = Phi_k S_k + loc_k in turn, on the fp32 MFMA.  A workgroup has 16
+// columns, its waves every fourth row tile; all of S_k goes round through LDS, whose two halves take turns.
+template <int N>
+__global__ __launch_bounds__(256) void ssd_delta_join_kernel(DeltaArgs a, ScanIo io) {
+    constexpr int NT = N / 16, NW = (NT + 3) / 4;
+    __shared__ __align__(16) float4 s_all[2][NT][64];
+    const int lane = threadIdx.x % 64, q = lane / 16, i = lane % 16;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int pb = a.P / 16, bh = blockIdx.x / pb, p = blockIdx.x % pb * 16 + i;
+    f32x4 S[NW];
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+        const int n = w + 4 * j;
+        S[j] = a.init_state && n < NT ? v4(*reinterpret_cast<const float4*>(a.init_state + ((size_t)bh * a.P + p) * N + 16 * n + 4 * q)) : kZero4;
+    }
+    for (int k = 0; k < io.K; ++k) {
+        float* to = io.s0 + (((size_t)bh * io.K + k) * a.P + p) * N + 4 * q;
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            const int n = w + 4 * j;
+            if (n < NT) {
+                *reinterpret_cast<float4*>(to + 16 * n) = f4(S[j]);
+                s_all[k & 1][n][lane] = f4(S[j]);
+            }
+        }
+        if (k == io.K - 1) break;
+        __syncthreads();
+        const size_t u = (size_t)bh * (io.K - 1) + k;
+        const float* loc = io.loc + (u * a.P + p) * N + 4 * q;
+        const float* phi = io.phi + (u * N + 4 * q) * N + i;   // [column m][row n]
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            const int n = w + 4 * j;
+            if (n >= NT) continue;
+            f32x4 R = v4(*reinterpret_cast<const float4*>(loc + 16 * n));
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+                const float* f = phi + (size_t)16 * m * N + 16 * n;
+                R = mma_f32(R, make_float4(f[0], f[N], f[2 * N], f[3 * N]), s_all[k & 1][m][lane]);
+            }
+            S[j] = R;
+        }
+    }
 }
 
 // ---- fp32 forward, and the backward's recomputation
@@ -1026,17 +1121,45 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
     }
 }
 
+// Superchunks of a sequence, bf16: the K that takes the fewest chunk steps, with one workgroup a CU at a time.  Against
+// a step of the full pass the state pass's, without y, takes 0.75, and joining one superchunk about 3 (measured: 2.0,
+// 1.5 and 5 us at N = P = 128).  B=1 L=32768 H=16: 1.07 ms with K = 1, KMEASURED.
+void delta_split(int B, int L, int H, int P, int N, int dtype, int& K, int& S) {
+    const int nc = (L + C - 1) / C;
+    const int64_t units = (int64_t)B * H * (P / 64), wide = (int64_t)B * H * (P / 64 + (N + 63) / 64);
+    K = 1;
+    S = nc;
+    if (dtype == 0) return;
+    auto rounds = [](int64_t n) { return (double)((n + 255) / 256); };
+    double best = rounds(units) * nc;
+    for (int k = 2; k <= 32; ++k) {
+        const int s = (nc + k - 1) / k, used = (nc + s - 1) / s;
+        if (s < 8) break;
+        const double t = s * (rounds(units * used) + 0.75 * rounds(wide * (used - 1))) + 3.0 * (used - 1);
+        if (t < best) {
+            best = t;
+            K = used;
+            S = s;
+        }
+    }
+}
+
 struct FwdWs {                     // byte offsets
-    size_t T, att, scal, across, total;
+    size_t T, att, scal, across, loc, phi, s0, total;
+    int K, S;
 };
-FwdWs fwd_ws(int B, int L, int H, int dtype) {
-    const size_t units = (size_t)B * H * ((L + C - 1) / C);
+FwdWs fwd_ws(int B, int L, int H, int P, int N, int dtype) {
+    const size_t heads = (size_t)B * H, units = heads * ((L + C - 1) / C);
     FwdWs w;
+    delta_split(B, L, H, P, N, dtype, w.K, w.S);
     w.T = 0;
     w.att = w.T + units * (dtype == 0 ? Bytes<true>::split : Bytes<false>::split);
     w.scal = w.att + units * (dtype == 0 ? Bytes<true>::att : Bytes<false>::att);
     w.across = w.scal + units * kScal * C * 4;
-    w.total = w.across + (units * 4 + 255) / 256 * 256;
+    w.loc = w.across + (units * 4 + 255) / 256 * 256;
+    w.phi = w.loc + (w.K > 1 ? heads * (w.K - 1) * P * N * 4 : 0);
+    w.s0 = w.phi + (w.K > 1 ? heads * (w.K - 1) * N * N * 4 : 0);
+    w.total = w.s0 + (w.K > 1 ? heads * w.K * P * N * 4 : 0);
     return w;
 }
 
@@ -1045,7 +1168,7 @@ hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
     constexpr bool F32 = std::is_same<T, float>::value;
     constexpr int PM = F32 ? kPrepPlain : kPrepScaled;
     const int nc = (a.L + C - 1) / C;
-    const FwdWs w = fwd_ws(a.B, a.L, a.H, a.dtype);
+    const FwdWs w = fwd_ws(a.B, a.L, a.H, a.P, N, a.dtype);
     unsigned char* base = static_cast<unsigned char*>(ws);
     PrepOut o{base + w.T, nullptr, base + w.att, reinterpret_cast<float*>(base + w.scal),
               reinterpret_cast<float*>(base + w.across)};
@@ -1054,8 +1177,9 @@ hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
                        dim3(64 * kPrepWaves), 0, stream, a, o, nc);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    ScanIo io{o.T, o.att, o.scal, o.across, nc, nullptr, nullptr};
-    const dim3 grid(a.B * a.H * (a.P / 64));
+    auto fp = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
+    ScanIo io{o.T, o.att, o.scal, o.across, nc, nullptr, nullptr, w.K, w.S, fp(w.loc), fp(w.phi), fp(w.s0)};
+    const dim3 grid(a.B * a.H * (a.P / 64) * w.K);
     if constexpr (F32) {
         constexpr size_t lds = (size_t)ScanLds<T, N, kY>::bytes * ScanLds<T, N, kY>::buffers;
         e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N, kY>), lds);
@@ -1063,9 +1187,21 @@ hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
         hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kY>), grid, dim3(256), lds, stream, a, io);
     } else {
         constexpr size_t lds = ChainLds<N>::bytes;
-        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N>), lds);
+        if (w.K > 1) {
+            constexpr size_t state_lds = 2 * ChainLds<N>::buffer;   // nothing is kept for y
+            e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, kState>), state_lds);
+            if (e != hipSuccess) return e;
+            hipLaunchKernelGGL((ssd_delta_chain_kernel<N, kState>), dim3(a.B * a.H * (a.P / 64 + (N + 63) / 64) * (w.K - 1)),
+                               dim3(512), state_lds, stream, a, io);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            hipLaunchKernelGGL((ssd_delta_join_kernel<N>), dim3(a.B * a.H * (a.P / 16)), dim3(256), 0, stream, a, io);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, kFull>), lds);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((ssd_delta_chain_kernel<N>), grid, dim3(512), lds, stream, a, io);
+        hipLaunchKernelGGL((ssd_delta_chain_kernel<N, kFull>), grid, dim3(512), lds, stream, a, io);
     }
     return hipGetLastError();
 }
@@ -1081,7 +1217,7 @@ hipError_t launch_keep_n(const DeltaArgs& a, const PrepOut& o, float* keepS, flo
     constexpr size_t lds = (size_t)ScanLds<T, N, kKeep>::bytes * ScanLds<T, N, kKeep>::buffers;
     e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N, kKeep>), lds);
     if (e != hipSuccess) return e;
-    ScanIo io{o.T, nullptr, o.scal, o.across, nc, keepS, keepU};
+    ScanIo io{o.T, nullptr, o.scal, o.across, nc, keepS, keepU, 1, nc, nullptr, nullptr, nullptr};
     hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kKeep>), dim3(a.B * a.H * (a.P / 64)), dim3(256), lds, stream, a, io);
     return hipGetLastError();
 }
@@ -1113,7 +1249,7 @@ hipError_t launch_keep(const DeltaArgs& a, const PrepOut& o, float* keepS, float
 }
 }  // namespace delta
 
-size_t delta_fwd_workspace_bytes(int B, int L, int H, int dtype) { return fwd_ws(B, L, H, dtype).total; }
+size_t delta_fwd_workspace_bytes(int B, int L, int H, int P, int N, int dtype) { return fwd_ws(B, L, H, P, N, dtype).total; }
 
 hipError_t launch_delta_fwd(const DeltaArgs& a, void* ws, hipStream_t stream) {
     return a.dtype == 0 ? launch_fwd_t<float>(a, ws, stream) : launch_fwd_t<uint16_t>(a, ws, stream);

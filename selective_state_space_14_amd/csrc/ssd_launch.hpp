@@ -221,7 +221,7 @@ hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t stream);
 // Raises a kernel's dynamic-LDS cap to `lds` on the current device before its
 // first launch there; once per (kernel, device), thread-safe.
 hipError_t prepare_launch(const void* fn, size_t lds);
-size_t delta_fwd_workspace_bytes(int B, int L, int H, int dtype);
+size_t delta_fwd_workspace_bytes(int B, int L, int H, int P, int N, int dtype);
 hipError_t launch_delta_fwd(const DeltaArgs& a, void* ws, hipStream_t stream);
 size_t delta_bwd_workspace_bytes(int B, int L, int H, int P, int N, int dtype);
 hipError_t launch_delta_bwd(const DeltaBwdArgs& a, void* ws, hipStream_t stream);

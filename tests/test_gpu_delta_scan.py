@@ -270,3 +270,21 @@ def test_layer_prefill_and_decode(gpu_lib):
     bound = (2 * 4 + 3) * 2.0 ** -8
     assert (got - want).norm() <= bound * want.norm(), float((got - want).norm() / want.norm())
     assert (got[:, L:] - want[:, L:]).norm() <= bound * want[:, L:].norm()
+
+
+@pytest.mark.parametrize("B,L,H,P,N,docs,lengths", [(1, 2100, 2, 64, 64, 0.0, None), (1, 2048, 1, 128, 128, 0.002, None),
+                                                    (3, 2500, 1, 64, 32, 0.0, [0, 2500, 700]), (2, 2111, 2, 128, 64, 0.01, None)])
+def test_split_sequences(gpu_lib, B, L, H, P, N, docs, lengths):
+    """Few heads and a long row: the sequence is cut into superchunks (the workspace is larger than the chunks' own);
+    with a carried state in place, documents across the cuts, and rows that end before the last superchunk."""
+    ssd, dims, dtype = gpu_lib, (H, P, N, 1), torch.bfloat16
+    d, opt = make(B, L, *dims, dtype, state=True, docs=docs, lengths=lengths)
+    units = B * H * -(-L // 64)
+    assert ssd.ssd_delta_scan_workspace_size(B, L, H, P, N, 1) > units * (12288 + 6144 + 1024 + 4) + 256
+    y, fs = check(ssd, d, opt, dims)
+    st = opt["init_state"].to(DEV)
+    g, o = to_dev(d), to_dev({**opt, "init_state": None})
+    y2 = ssd.ssd_delta_scan_fwd(g["q"], g["k"], g["v"], g["dt"], g["A"], g["beta"], H=H, P=P, N=N, G=1, qk_norm=True,
+                                dt_softplus=True, beta_sigmoid=True, dt_bias=g["dt_bias"], doc_ids=o["doc_ids"],
+                                lengths=o["lengths"], init_state=st, final_state=st)
+    assert torch.equal(y, y2) and torch.equal(st, fs)
