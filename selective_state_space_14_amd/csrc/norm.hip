@@ -66,6 +66,44 @@ __device__ __forceinline__ void stv(uint16_t* p, const float (&v)[VEC]) {
     }
 }
 
+// A vector as it is in memory: loaded a row ahead, widened when its row comes.
+template <typename T, int VEC>
+struct Raw {
+    T v;
+    __device__ __forceinline__ void load(const T* p) { v = *p; }
+    __device__ __forceinline__ void clear() { v = 0; }
+    __device__ __forceinline__ void get(float (&o)[VEC]) const { ldv<VEC>(&v, o); }
+};
+template <>
+struct Raw<uint16_t, 8> {
+    u32x4_t v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
+    __device__ __forceinline__ void clear() { v = u32x4_t{0, 0, 0, 0}; }
+    __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = bf16_lo(v[i]);
+            o[2 * i + 1] = bf16_hi(v[i]);
+        }
+    }
+};
+template <>
+struct Raw<float, 8> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const f32x4*>(p);
+        b = *reinterpret_cast<const f32x4*>(p + 4);
+    }
+    __device__ __forceinline__ void clear() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+    __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[i] = a[i];
+            o[4 + i] = b[i];
+        }
+    }
+};
+
 // ------------------------------------------------------------ sums over a row's threads
 // two sums at once; over a workgroup they meet in `red`, whose two halves are
 // used in turn, so one barrier a call is enough: a wave reads its half before
@@ -236,23 +274,45 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
     X* dxp = static_cast<X*>(a.dx);
     T* dzp = static_cast<T*>(a.dz);
     const float inv = 1.0f / (float)a.W;
-    for (int64_t r0 = (int64_t)blockIdx.x * SH::rows; r0 < a.R; r0 += (int64_t)gridDim.x * SH::rows) {
-        const bool live = r0 + sub < a.R;
+    // the next row's operands are on their way while this row is computed
+    Raw<X, VEC> nx[NV];
+    Raw<T, VEC> nz[NV], ng[NV];
+    auto fetch = [&](int64_t at) {
+        const bool live = at < a.R;
         int64_t r;
         int col;
-        locate(a, r0 + sub, r, col);
-        float x[NV][VEC], z[NV][VEC], g[NV][VEC];
+        locate(a, at, r, col);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (lane + j * TPR) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[j][e] = z[j][e] = g[j][e] = 0.0f;
+            nx[j].clear();
+            nz[j].clear();
+            ng[j].clear();
             if (live && on[j]) {
-                ldv<VEC>(xp + r * a.x_stride + col + c, x[j]);
-                ldv<VEC>(gp + r * a.gy_stride + col + c, g[j]);
-                if (zp) ldv<VEC>(zp + r * a.z_stride + col + c, z[j]);
+                nx[j].load(xp + r * a.x_stride + col + c);
+                ng[j].load(gp + r * a.gy_stride + col + c);
+                if (zp) nz[j].load(zp + r * a.z_stride + col + c);
             }
         }
+    };
+    const int64_t step = (int64_t)gridDim.x * SH::rows;
+    int64_t at = (int64_t)blockIdx.x * SH::rows + sub;
+    constexpr bool kAhead = !kLds;                   // 1024 threads have no registers for it
+    if (kAhead) fetch(at);
+    for (; at - sub < a.R; at += step) {
+        if (!kAhead) fetch(at);
+        const bool live = at < a.R;
+        int64_t r;
+        int col;
+        locate(a, at, r, col);
+        float x[NV][VEC], z[NV][VEC], g[NV][VEC];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            nx[j].get(x[j]);
+            nz[j].get(z[j]);
+            ng[j].get(g[j]);
+        }
+        if (kAhead) fetch(at + step);
         const float rstd = to_hat<TPR, NV, VEC>(x, on, a.W, a.rms, a.eps, red, turn);
         if (!kHeld) load_params<TPR, NV, VEC>(a.w, a.b, on, lane, wv, bv);
         float m1 = 0.0f, m2 = 0.0f;
@@ -340,25 +400,34 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
     }
 }
 
-// dw and db: the sum of the workgroups' partial rows, 32 columns a workgroup,
-// eight threads of a column each adding every eighth row
-__global__ __launch_bounds__(256) void ssd_norm_sum_kernel(const float* part, int nblk, int W, float* dw, float* db) {
-    __shared__ float s[8][33];
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
-    float v = 0.0f;
+// dw and db: the sum of the workgroups' partial rows.  32 columns a workgroup,
+// 32 threads a column each adding every 32nd row, four loads at a time, then
+// the 32 sums in order.
+__global__ __launch_bounds__(1024) void ssd_norm_sum_kernel(const float* part, int nblk, int W, float* dw, float* db) {
+    __shared__ float s[32][33];
+    const int x = threadIdx.x % 32, k = threadIdx.x / 32, c = blockIdx.x * 32 + x;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < 2 * W) {
-        for (int i = k; i < nblk; i += 8) v += part[(size_t)i * 2 * W + c];
+        const float* p = part + c;
+        int i = k;
+        for (; i + 96 < nblk; i += 128) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += p[(size_t)(i + 32 * j) * 2 * W];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + 32 * j < nblk) v[j] += p[(size_t)(i + 32 * j) * 2 * W];
     }
-    s[k][threadIdx.x % 32] = v;
+    s[k][x] = (v[0] + v[1]) + (v[2] + v[3]);
     __syncthreads();
     if (k == 0 && c < 2 * W) {
-        v = 0.0f;
+        float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += s[i][threadIdx.x];
+        for (int i = 0; i < 32; ++i) t += s[i][x];
         if (c < W) {
-            if (dw) dw[c] = v;
+            if (dw) dw[c] = t;
         } else if (db) {
-            db[c - W] = v;
+            db[c - W] = t;
         }
     }
 }
@@ -377,7 +446,7 @@ hipError_t launch_bwd(const NormArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC>), dim3(n), dim3(SH::threads), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
-    hipLaunchKernelGGL(ssd_norm_sum_kernel, dim3((2 * a.W + 31) / 32), dim3(256), 0, stream, a.part, n, a.W, a.dw, a.db);
+    hipLaunchKernelGGL(ssd_norm_sum_kernel, dim3((2 * a.W + 31) / 32), dim3(1024), 0, stream, a.part, n, a.W, a.dw, a.db);
     return hipGetLastError();
 }
 
