@@ -64,7 +64,9 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, q = lane / 16, i = lane % 16;
     const uint32_t id = blockIdx.x * kPrepWaves + wave;   // below 2^31 (api)
     if (id >= (uint32_t)a.B * nc * a.H) return;
-    const int h = (int)(id % a.H), c = (int)(id / a.H % nc), b = (int)(id / a.H / nc);
+    // the last chunks of every row first: the scan starts with the first ones, which are then the latest written and
+    // mostly still in the last-level cache (256 MB)
+    const int h = (int)(id % a.H), b = (int)(id / a.H % a.B), c = nc - 1 - (int)(id / a.H / a.B);
     const int t0 = c * C, n_on = min(C, row_len(a, b) - t0);
     if (n_on <= 0) return;
     const size_t u = ((size_t)b * a.H + h) * nc + c;
@@ -565,6 +567,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             }
             lds_barrier();
         }
+        if (nch & 1) lds_barrier();                  // the other waves go in pairs
         float* last;
         if (MODE == kState) {
             const size_t u = (size_t)bh * (io.K - 1) + sk;
@@ -652,15 +655,32 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
     };
     const std::integral_constant<int, 0> even;
     const std::integral_constant<int, 1> odd;
+    // The loads before the loop stand in the loop's own order, stores (dropped, out of range) included: a wait in the
+    // loop can then count past as many younger operations on its first round as on the others, and waits for no more.
+    auto no_store = [&]() {
+        const __amdgpu_buffer_rsrc_t none = __builtin_amdgcn_make_buffer_rsrc(yb, 0, 0, 0x00020000);
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{0, 0, 0, 0}, none, 0x80000000u, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{0, 0, 0, 0}, none, 0x80000000u, 64, 0);
+    };
     if (nch > 0) {
         fetch(0, even);
         stage(0, even);
         fetch(1, odd);
-        fetch(2, even);
-        if (MODE == kFull) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE == kFull) {
             fetch_q(0, even);
-            fetch_q(1, odd);
+            __builtin_amdgcn_sched_barrier(0);
+            no_store();
         }
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(2, even);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE == kFull) {
+            fetch_q(1, odd);
+            __builtin_amdgcn_sched_barrier(0);
+            no_store();
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
     lds_barrier();
     // while the chain is at chunk c (of parity Z): chunk c + 1 to LDS, c + 3 on its way; behind the barrier, beside
@@ -702,7 +722,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         fetch_q(c + 2, set);
         const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(yb + (size_t)(c0 + c) * C * y_row, 0, 0x7fffffff, 0x00020000);
         const int t = 16 * wave + i;
-        const uint32_t at = (c0 + c) * C + t < len ? (uint32_t)t * y_row + y_col : 0x80000000u;
+        const uint32_t at = c < nch && (c0 + c) * C + t < len ? (uint32_t)t * y_row + y_col : 0x80000000u;
 #pragma unroll
         for (int w = 0; w < 4; w += 2) {
             // lanes of neighbouring rows of 16 exchange halves of two tiles: eight columns a lane, 64 bytes a token
@@ -711,10 +731,10 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{lo[0], hi[0], lo[1], hi[1]}, yr, at, 32 * w, 0);
         }
     };
-    for (int c = 0; c < nch;) {
-        body(c++, even, odd);
-        if (c == nch) break;
-        body(c++, odd, even);
+    // in pairs, so that the loop has one way round and the waits' counts hold; the chain passes as many barriers
+    for (int c = 0; c < nch; c += 2) {
+        body(c, even, odd);
+        body(c + 1, odd, even);
     }
     if (MODE == kState) return;
     // rows past the sequence are exactly 0
