@@ -316,7 +316,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
 #pragma unroll
                 for (int r = 0; r < 4; ++r) *ltp(n, m, 4 * q + r, i) = tt[n][m][r];
     }
-    unsigned char* dst = o.T + u * Bytes<F32>::split + lane * 16;
+    unsigned char* dst = o.T + u * (PM == kPrepScaled ? Bytes<F32>::packed : Bytes<F32>::split) + (PM == kPrepScaled ? 0 : lane * 16);
     lds_wait();
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -332,8 +332,14 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
 #pragma unroll
             for (int s = 0; s < m / 2 + 1; ++s) {
                 const Pair p = split2(tt[2 * s][m], tt[2 * s + 1][m]);
-                *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 2048) = p.hi.u;
-                *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 2048 + 1024) = p.lo.u;
+                if constexpr (PM == kPrepScaled) {
+                    unsigned char* at = dst + packed_at(m, s) * 1024;
+                    packed_write(at, packed_half(m, s), lane, p.hi.u);
+                    packed_write(at + (packed_half(m, s) ? 512 : 1024), packed_half(m, s), lane, p.lo.u);
+                } else {
+                    *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 2048) = p.hi.u;
+                    *reinterpret_cast<uint4*>(dst + lower_frag(m, s) * 2048 + 1024) = p.lo.u;
+                }
             }
         }
     }
@@ -434,7 +440,7 @@ struct ChainLds {
     static __device__ __forceinline__ int piece(int t, int x) {
         return x ^ (N == 128 ? (t & 3) << 2 | (t >> 2 & 3) : N == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 3) : t >> 2 & 3);
     }
-    static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow, kin = t + Bytes<false>::split, across = kin + C * 4;
+    static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow, kin = t + Bytes<false>::packed, across = kin + C * 4;
     static constexpr int buffer = across + 256;
     static constexpr int kept = (KS + 4) * 1024;     // a wave's S (rounded) and X (split) fragments
     static constexpr int bytes = 2 * (buffer + 4 * kept);
@@ -516,10 +522,14 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
                 for (int m = 0; m < 4; ++m) R[m] = mma(R[m], kf[m][s], sp[s].hi);
             }
 #pragma unroll
-            for (int f = 0; f < 6; ++f) {
-                th[f].u = *reinterpret_cast<const uint4*>(lds + LD::t + f * 2048 + lane * 16);
-                tl[f].u = *reinterpret_cast<const uint4*>(lds + LD::t + f * 2048 + 1024 + lane * 16);
-            }
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int s = 0; s < m / 2 + 1; ++s) {
+                    const unsigned char* at = lds + LD::t + packed_at(m, s) * 1024;
+                    const int f = lower_frag(m, s);
+                    th[f].u = packed_read(at, packed_half(m, s), lane);
+                    tl[f].u = packed_read(at + (packed_half(m, s) ? 512 : 1024), packed_half(m, s), lane);
+                }
             __builtin_amdgcn_sched_barrier(0);
             // k^T: row i of the state tiles' numbering, K index t
 #pragma unroll
@@ -582,7 +592,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         return;
     }
     // ---------------------------------------------------- staging and y
-    constexpr int NK = C * nc16 / 256, NV = 2, NTp = Bytes<false>::split / 4096;
+    constexpr int NK = C * nc16 / 256, NV = 2, NTp = (Bytes<false>::packed / 16 + 255) / 256;
     // two chunks are on their way at any time, in register sets of their parity: one chunk's time is less than
     // the memory's latency under this kernel's own load
     u32x4_t rk[2][NK], rv[2][NV], rt[2][NTp];
@@ -614,7 +624,10 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             rv[Z][j] = *reinterpret_cast<const u32x4_t*>(vc + ((uint32_t)t * v_row + x * 16));
         }
 #pragma unroll
-        for (int j = 0; j < NTp; ++j) rt[Z][j] = *reinterpret_cast<const u32x4_t*>(io.T + u * Bytes<false>::split + (tid + 256 * j) * 16);
+        for (int j = 0; j < NTp; ++j) {
+            const int e = min(tid + 256 * j, Bytes<false>::packed / 16 - 1);
+            rt[Z][j] = *reinterpret_cast<const u32x4_t*>(io.T + u * Bytes<false>::packed + e * 16);
+        }
         const float* sc = tid < C ? io.scal + (u * kScal + kKin) * C + tid : io.across + u;
         rs[Z] = *sc;
     };
@@ -634,7 +647,8 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             *reinterpret_cast<u32x4_t*>(lds + LD::v + t * LD::vRow + x * 16) = t < n_on && !phi ? rv[Z][j] : zero;
         }
 #pragma unroll
-        for (int j = 0; j < NTp; ++j) *reinterpret_cast<u32x4_t*>(lds + LD::t + (tid + 256 * j) * 16) = rt[Z][j];
+        for (int j = 0; j < NTp; ++j)                // past T's end the last piece again
+            *reinterpret_cast<u32x4_t*>(lds + LD::t + min(tid + 256 * j, Bytes<false>::packed / 16 - 1) * 16) = rt[Z][j];
         if (tid < 128) *reinterpret_cast<float*>(lds + LD::kin + min(tid, C) * 4) = rs[Z];
     };
     // y: this wave's 16 tokens of all 64 columns, so that each piece of q and Att T is read by one wave
@@ -1173,7 +1187,7 @@ FwdWs fwd_ws(int B, int L, int H, int P, int N, int dtype) {
     FwdWs w;
     delta_split(B, L, H, P, N, dtype, w.K, w.S);
     w.T = 0;
-    w.att = w.T + units * (dtype == 0 ? Bytes<true>::split : Bytes<false>::split);
+    w.att = w.T + units * (dtype == 0 ? Bytes<true>::split : Bytes<false>::packed);
     w.scal = w.att + units * (dtype == 0 ? Bytes<true>::att : Bytes<false>::att);
     w.across = w.scal + units * kScal * C * 4;
     w.loc = w.across + (units * 4 + 255) / 256 * 256;

@@ -32,11 +32,27 @@ __host__ __device__ constexpr int lower_frag(int m, int s) { return m < 2 ? m : 
 __host__ __device__ constexpr int upper_frag(int n, int s) { return n < 2 ? 2 * n + s : 2 + n; }
 __host__ __device__ constexpr int tile_id(int m, int n) { return m * (m + 1) / 2 + n; }   // n <= m
 
+// The bf16 forward's T is packed: of the two fragments whose second block lies
+// above the diagonal only the first halves are kept, 8 bytes a lane.
 template <bool F32>
 struct Bytes {
     static constexpr int split = F32 ? 10 * 1024 : 12 * 1024;   // T, its transpose, the backward's Att
+    static constexpr int packed = 10 * 1024;                    // the bf16 forward's T
     static constexpr int att = F32 ? 10 * 1024 : 6 * 1024;      // the forward's Att (one bf16 rounding)
 };
+__host__ __device__ constexpr bool packed_half(int m, int s) { return m == 2 * s; }
+// where fragment (m, s)'s high part starts, in KB; its low part follows
+__host__ __device__ constexpr int packed_at(int m, int s) { return m == 0 ? 0 : m == 1 ? 1 : m == 2 ? 3 + 2 * s : 6 + 2 * s; }
+// a fragment from its packed place, the second half 0 where it is not kept
+__device__ __forceinline__ uint4 packed_read(const unsigned char* at, bool half, int lane) {
+    if (!half) return *reinterpret_cast<const uint4*>(at + lane * 16);
+    const uint2 v = *reinterpret_cast<const uint2*>(at + lane * 8);
+    return make_uint4(v.x, v.y, 0, 0);
+}
+__device__ __forceinline__ void packed_write(unsigned char* at, bool half, int lane, const uint4& v) {
+    if (half) *reinterpret_cast<uint2*>(at + lane * 8) = make_uint2(v.x, v.y);
+    else *reinterpret_cast<uint4*>(at + lane * 16) = v;
+}
 // per-token scalars of a unit: four arrays of C
 enum { kKin = 0, kKout = 1, kQin = 2, kBeta = 3, kScal = 4 };
 // the backward's: also the running sum of dt A (log2) as two floats, the document's number within the chunk, and the

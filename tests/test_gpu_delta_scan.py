@@ -280,7 +280,7 @@ def test_split_sequences(gpu_lib, B, L, H, P, N, docs, lengths):
     ssd, dims, dtype = gpu_lib, (H, P, N, 1), torch.bfloat16
     d, opt = make(B, L, *dims, dtype, state=True, docs=docs, lengths=lengths)
     units = B * H * -(-L // 64)
-    assert ssd.ssd_delta_scan_workspace_size(B, L, H, P, N, 1) > units * (12288 + 6144 + 1024 + 4) + 256
+    assert ssd.ssd_delta_scan_workspace_size(B, L, H, P, N, 1) > units * (10240 + 6144 + 1024 + 4) + 256
     y, fs = check(ssd, d, opt, dims)
     st = opt["init_state"].to(DEV)
     g, o = to_dev(d), to_dev({**opt, "init_state": None})
