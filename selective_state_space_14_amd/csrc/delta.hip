@@ -428,9 +428,11 @@ enum { kY = 0, kKeep = 1 };        // forward: y; backward's recomputation: S an
 // from a zero state, and with N columns more, which start as the identity and
 // see v = 0, computes their transitions; ssd_delta_join_kernel puts the states
 // entering the superchunks together; the full launch runs them side by side.
-enum { kFull = 0, kState = 1 };
+// The backward's recomputation is the same chain (kStates) with T and beta apart, each chunk's entering state and U
+// going to memory from the chain's waves, and no y.
+enum { kFull = 0, kState = 1, kStates = 2 };
 
-template <int N>
+template <int N, int MODE>
 struct ChainLds {
     static constexpr int kRow = N * 2;               // bytes of a k row, its 16-byte pieces permuted (piece())
     static constexpr int vRow = 64 * 2 + 16;
@@ -440,15 +442,18 @@ struct ChainLds {
     static __device__ __forceinline__ int piece(int t, int x) {
         return x ^ (N == 128 ? (t & 3) << 2 | (t >> 2 & 3) : N == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 3) : t >> 2 & 3);
     }
-    static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow, kin = t + Bytes<false>::packed, across = kin + C * 4;
+    static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow;
+    static constexpr int t_bytes = MODE == kStates ? Bytes<false>::split : Bytes<false>::packed;
+    // kin (kStates: all four arrays of scalars), then the decay across the chunk
+    static constexpr int kin = t + t_bytes, across = kin + (MODE == kStates ? kScal : 1) * C * 4;
     static constexpr int buffer = across + 256;
     static constexpr int kept = (KS + 4) * 1024;     // a wave's S (rounded) and X (split) fragments
-    static constexpr int bytes = 2 * (buffer + 4 * kept);
+    static constexpr int bytes = 2 * (buffer + (MODE == kFull ? 4 * kept : 0));
 };
 
 template <int N, int MODE>
 __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, ScanIo io) {
-    using LD = ChainLds<N>;
+    using LD = ChainLds<N, MODE>;
     constexpr int NT = N / 16, KS = N / 32, nc16 = N / 8;
     extern __shared__ __align__(16) unsigned char lds_all[];
     const int tid = threadIdx.x % 256, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
@@ -505,6 +510,13 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             }
             const float across = *reinterpret_cast<const float*>(lds + LD::across);
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (MODE == kStates) {
+                float* to = io.keepS + ((size_t)bh * io.nc + c) * N * a.P + p0 + 16 * wave + i;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) to[(size_t)(32 * (n / 2) + 8 * q + 4 * (n % 2) + r) * a.P] = S[n][r];
+            }
             Pair sp[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
@@ -521,15 +533,27 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
 #pragma unroll
                 for (int m = 0; m < 4; ++m) R[m] = mma(R[m], kf[m][s], sp[s].hi);
             }
+            f32x4 be[4], kout[4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < 4; ++m) {
 #pragma unroll
                 for (int s = 0; s < m / 2 + 1; ++s) {
-                    const unsigned char* at = lds + LD::t + packed_at(m, s) * 1024;
                     const int f = lower_frag(m, s);
-                    th[f].u = packed_read(at, packed_half(m, s), lane);
-                    tl[f].u = packed_read(at + (packed_half(m, s) ? 512 : 1024), packed_half(m, s), lane);
+                    if constexpr (MODE == kStates) {
+                        const unsigned char* at = lds + LD::t + f * 2048 + lane * 16;
+                        th[f].u = *reinterpret_cast<const uint4*>(at);
+                        tl[f].u = *reinterpret_cast<const uint4*>(at + 1024);
+                    } else {
+                        const unsigned char* at = lds + LD::t + packed_at(m, s) * 1024;
+                        th[f].u = packed_read(at, packed_half(m, s), lane);
+                        tl[f].u = packed_read(at + (packed_half(m, s) ? 512 : 1024), packed_half(m, s), lane);
+                    }
                 }
+                if constexpr (MODE == kStates) {
+                    be[m] = v4(*reinterpret_cast<const float4*>(lds + LD::kin + (kBeta * C + 16 * m + 4 * q) * 4));
+                    kout[m] = v4(*reinterpret_cast<const float4*>(lds + LD::kin + (kKout * C + 16 * m + 4 * q) * 4));
+                }
+            }
             __builtin_amdgcn_sched_barrier(0);
             // k^T: row i of the state tiles' numbering, K index t
 #pragma unroll
@@ -549,6 +573,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             for (int m = 0; m < 4; ++m) {
                 const f32x4 v = {bf16_lo(vf[m].a), bf16_hi(vf[m].a), bf16_lo(vf[m].b), bf16_hi(vf[m].b)};
                 X[m] = v - kin[m] * R[m];
+                if constexpr (MODE == kStates) X[m] *= be[m];
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) S[n] *= across;
@@ -567,6 +592,15 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
                         U[m] = x == 0 ? mma(U[m], tl[f], xp.hi) : mma(U[m], th[f], x == 1 ? xp.lo : xp.hi);
                     }
             }
+            if constexpr (MODE == kStates) {
+                float* to = io.keepU + ((size_t)bh * io.nc + c) * C * a.P + p0 + 16 * wave + i;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) to[(size_t)(16 * m + 4 * q + r) * a.P] = U[m][r];
+                    U[m] *= kout[m];
+                }
+            }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const Pair up = split2(U[2 * s], U[2 * s + 1]);
@@ -579,7 +613,9 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         }
         if (nch & 1) lds_barrier();                  // the other waves go in pairs
         float* last;
-        if (MODE == kState) {
+        if (MODE == kStates) {
+            last = nullptr;
+        } else if (MODE == kState) {
             const size_t u = (size_t)bh * (io.K - 1) + sk;
             last = phi ? (pc < N ? io.phi + (u * N + pc) * N + 8 * q : nullptr) : io.loc + (u * a.P + p0 + 16 * wave + i) * N + 8 * q;
         } else {
@@ -592,11 +628,11 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         return;
     }
     // ---------------------------------------------------- staging and y
-    constexpr int NK = C * nc16 / 256, NV = 2, NTp = (Bytes<false>::packed / 16 + 255) / 256;
+    constexpr int NK = C * nc16 / 256, NV = 2, NTp = (LD::t_bytes / 16 + 255) / 256, NS = MODE == kStates ? kScalBwd : kScal;
     // two chunks are on their way at any time, in register sets of their parity: one chunk's time is less than
     // the memory's latency under this kernel's own load
     u32x4_t rk[2][NK], rv[2][NV], rt[2][NTp];
-    float rs[2];
+    float rs[2], ra[2];
     const unsigned char* kb = static_cast<const unsigned char*>(a.k) + (tok0 * a.k_stride + (size_t)g * N) * 2;
     const unsigned char* qb = static_cast<const unsigned char*>(a.q) + (tok0 * a.q_stride + (size_t)g * N) * 2;
     const unsigned char* vb = static_cast<const unsigned char*>(a.v) + (tok0 * a.v_stride + (size_t)h * a.P + p0) * 2;
@@ -625,11 +661,16 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         }
 #pragma unroll
         for (int j = 0; j < NTp; ++j) {
-            const int e = min(tid + 256 * j, Bytes<false>::packed / 16 - 1);
-            rt[Z][j] = *reinterpret_cast<const u32x4_t*>(io.T + u * Bytes<false>::packed + e * 16);
+            const int e = min(tid + 256 * j, LD::t_bytes / 16 - 1);
+            rt[Z][j] = *reinterpret_cast<const u32x4_t*>(io.T + u * LD::t_bytes + e * 16);
         }
-        const float* sc = tid < C ? io.scal + (u * kScal + kKin) * C + tid : io.across + u;
-        rs[Z] = *sc;
+        if constexpr (MODE == kStates) {
+            rs[Z] = io.scal[u * NS * C + tid];
+            ra[Z] = io.across[u];
+        } else {
+            const float* sc = tid < C ? io.scal + (u * NS + kKin) * C + tid : io.across + u;
+            rs[Z] = *sc;
+        }
     };
     auto stage = [&](int c, auto set) {
         constexpr int Z = decltype(set)::value;
@@ -648,8 +689,13 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         }
 #pragma unroll
         for (int j = 0; j < NTp; ++j)                // past T's end the last piece again
-            *reinterpret_cast<u32x4_t*>(lds + LD::t + min(tid + 256 * j, Bytes<false>::packed / 16 - 1) * 16) = rt[Z][j];
-        if (tid < 128) *reinterpret_cast<float*>(lds + LD::kin + min(tid, C) * 4) = rs[Z];
+            *reinterpret_cast<u32x4_t*>(lds + LD::t + min(tid + 256 * j, LD::t_bytes / 16 - 1) * 16) = rt[Z][j];
+        if constexpr (MODE == kStates) {
+            *reinterpret_cast<float*>(lds + LD::kin + tid * 4) = rs[Z];
+            if (tid == 0) *reinterpret_cast<float*>(lds + LD::across) = ra[Z];
+        } else {
+            if (tid < 128) *reinterpret_cast<float*>(lds + LD::kin + min(tid, C) * 4) = rs[Z];
+        }
     };
     // y: this wave's 16 tokens of all 64 columns, so that each piece of q and Att T is read by one wave
     Frag qf[2][KS], af[2][2];
@@ -704,7 +750,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         stage(c + 1, other);
         fetch(c + 3, other);
         lds_barrier();
-        if constexpr (MODE == kState) return;
+        if constexpr (MODE != kFull) return;
         const unsigned char* const keep = lds_all + 2 * LD::buffer + (c & 1) * 4 * LD::kept + lane * 16;
         f32x4 O[4];
 #pragma unroll
@@ -750,7 +796,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         body(c, even, odd);
         body(c + 1, odd, even);
     }
-    if (MODE == kState) return;
+    if (MODE != kFull) return;
     // rows past the sequence are exactly 0
     const int tend = sk == io.K - 1 ? a.L : min(a.L, (c0 + io.S) * C);
     for (int t = max(len, c0 * C) + i; t < tend; t += 16) if (wave % 2 == 0) *reinterpret_cast<uint4*>(yb + (size_t)t * y_row + y_col + 32 * wave) = make_uint4(0, 0, 0, 0);
@@ -1220,9 +1266,9 @@ hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kY>), grid, dim3(256), lds, stream, a, io);
     } else {
-        constexpr size_t lds = ChainLds<N>::bytes;
+        constexpr size_t lds = ChainLds<N, kFull>::bytes;
         if (w.K > 1) {
-            constexpr size_t state_lds = 2 * ChainLds<N>::buffer;   // nothing is kept for y
+            constexpr size_t state_lds = 2 * ChainLds<N, kState>::buffer;   // nothing is kept for y
             e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, kState>), state_lds);
             if (e != hipSuccess) return e;
             hipLaunchKernelGGL((ssd_delta_chain_kernel<N, kState>), dim3(a.B * a.H * (a.P / 64 + (N + 63) / 64) * (w.K - 1)),
@@ -1248,11 +1294,19 @@ hipError_t launch_keep_n(const DeltaArgs& a, const PrepOut& o, float* keepS, flo
                        dim3(64 * kPrepWaves), 0, stream, a, o, nc);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    constexpr size_t lds = (size_t)ScanLds<T, N, kKeep>::bytes * ScanLds<T, N, kKeep>::buffers;
-    e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N, kKeep>), lds);
-    if (e != hipSuccess) return e;
     ScanIo io{o.T, nullptr, o.scal, o.across, nc, keepS, keepU, 1, nc, nullptr, nullptr, nullptr};
-    hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kKeep>), dim3(a.B * a.H * (a.P / 64)), dim3(256), lds, stream, a, io);
+    const dim3 grid(a.B * a.H * (a.P / 64));
+    if constexpr (std::is_same<T, float>::value) {
+        constexpr size_t lds = (size_t)ScanLds<T, N, kKeep>::bytes * ScanLds<T, N, kKeep>::buffers;
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N, kKeep>), lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kKeep>), grid, dim3(256), lds, stream, a, io);
+    } else {
+        constexpr size_t lds = ChainLds<N, kStates>::bytes;
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, kStates>), lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((ssd_delta_chain_kernel<N, kStates>), grid, dim3(512), lds, stream, a, io);
+    }
     return hipGetLastError();
 }
 template <typename T>
