@@ -437,11 +437,7 @@ struct ChainLds {
     static constexpr int kRow = N * 2;               // bytes of a k row, its 16-byte pieces permuted (piece())
     static constexpr int vRow = 64 * 2 + 16;
     static constexpr int KS = N / 32;
-    // The piece of row t that holds entries 8 x .. 8 x + 7.  Both reads of k hit every bank once: by rows (16
-    // consecutive rows, one x) and transposed (rows 4 q .. 4 q + 3, four consecutive x).
-    static __device__ __forceinline__ int piece(int t, int x) {
-        return x ^ (N == 128 ? (t & 3) << 2 | (t >> 2 & 3) : N == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 3) : t >> 2 & 3);
-    }
+    static __device__ __forceinline__ int piece(int t, int x) { return row_piece<N>(t, x); }
     static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow;
     static constexpr int t_bytes = MODE == kStates ? Bytes<false>::split : Bytes<false>::packed;
     // kin (kStates: all four arrays of scalars), then the decay across the chunk

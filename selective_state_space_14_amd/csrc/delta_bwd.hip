@@ -41,10 +41,280 @@ struct BwdIo {
 // As the forward's: a wave holds 16 columns of dS from the last chunk to the
 // first, the chunk's left operands (k and q both ways, Att^T, T^T, dY) staged
 // in LDS ahead of it.  Bound by the chain's latency, like the forward.
-template <typename T, int N>
+
+// ---- bf16: four waves are the chain, four more bring the next chunks
+template <int N>
+struct BackLds {
+    static constexpr int kRow = N * 2, dRow = 64 * 2 + 16;
+    static constexpr int k = 0, q = k + C * kRow, d = q + C * kRow, tt = d + C * dRow;
+    static constexpr int att = tt + Bytes<false>::split, scal = att + Bytes<false>::split, across = scal + kScal * C * 4;
+    static constexpr int buffer = across + 256;
+};
+
+template <int N>
+__global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba, BwdIo io) {
+    using LD = BackLds<N>;
+    constexpr int NT = N / 16, KS = N / 32, nc16 = N / 8, QS = N == 128 ? 1 : 2;   // QS: half of Q^T and K^T at a time where registers run short
+    extern __shared__ __align__(16) unsigned char lds_all[];
+    const DeltaArgs& a = ba.f;
+    const int tid = threadIdx.x % 256, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
+    const int pb = a.P / 64;
+    int unit = blockIdx.x;
+    const int share = a.H / a.G * pb;                // heads of a group on one XCD
+    if (a.B * a.G % 8 == 0) unit = (unit / 8 / share * 8 + unit % 8) * share + unit / 8 % share;
+    const int p0 = unit % pb * 64, bh = unit / pb, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+    const int len = row_len(a, b), nch = (len + C - 1) / C;   // step e is chunk nch - 1 - e
+    const size_t tok0 = (size_t)b * a.L;
+
+    if (threadIdx.x < 256) {
+        const int p = p0 + 16 * wave + i;
+        const size_t sofs = ((size_t)bh * a.P + p) * N + 8 * q;
+        f32x4 D[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            D[n] = ba.g_final ? v4(*reinterpret_cast<const float4*>(ba.g_final + sofs + 32 * (n / 2) + 4 * (n % 2))) : kZero4;
+        lds_barrier();
+        for (int e = 0; e < nch; ++e) {
+            const unsigned char* const lds = lds_all + (e & 1) * LD::buffer;
+            const size_t u = (size_t)bh * io.nc + nch - 1 - e;
+            auto scal4 = [&](int what, int m) {
+                return v4(*reinterpret_cast<const float4*>(lds + LD::scal + (what * C + 16 * m + 4 * q) * 4));
+            };
+            auto frag = [&](int at) {
+                Frag f;
+                f.u = *reinterpret_cast<const uint4*>(lds + at + lane * 16);
+                return f;
+            };
+            auto trans = [&](int at, int s, int n) {   // the transposed operand: row i of the state tiles' numbering, K index t
+                Frag f;
+                const int r = 4 * q + i / 4, x = row_piece<N>(r, 4 * (n / 2) + i % 4) * 16 + 8 * (n % 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const FragBF z = tr_read(lds, at + (32 * s + 16 * e + r) * LD::kRow + x);
+                    f.w[2 * e] = z.a;
+                    f.w[2 * e + 1] = z.b;
+                }
+                return f;
+            };
+            Frag kf[4][KS], ah[6], al[6], df[2];
+            f32x4 qin[4], kout[4];
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    kf[m][s].u = *reinterpret_cast<const uint4*>(lds + LD::k + (16 * m + i) * LD::kRow + row_piece<N>(i, 4 * s + q) * 16);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const FragBF f = tr_read(lds, LD::d + (16 * m + 4 * q + i / 4) * LD::dRow + (16 * wave + 4 * (i % 4)) * 2);
+                df[m / 2].w[2 * (m % 2)] = f.a;
+                df[m / 2].w[2 * (m % 2) + 1] = f.b;
+            }
+            auto scals = [&]() {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    qin[m] = scal4(kQin, m);
+                    kout[m] = scal4(kKout, m);
+                }
+            };
+            if (QS == 2) scals();
+#pragma unroll
+            for (int f = 0; f < 6; ++f) {
+                ah[f] = frag(LD::att + f * 2048);
+                al[f] = frag(LD::att + f * 2048 + 1024);
+            }
+            const float across = *reinterpret_cast<const float*>(lds + LD::across);
+            __builtin_amdgcn_sched_barrier(0);
+            if (QS == 1) scals();
+            float* kd = io.D + u * N * a.P + p;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) kd[(size_t)(32 * (n / 2) + 8 * q + 4 * (n % 2) + r) * a.P] = D[n][r];
+            f32x4 W[4], Z[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) W[m] = Z[m] = kZero4;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const Pair sp = split2(D[2 * s], D[2 * s + 1]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) W[m] = mma(W[m], kf[m][s], sp.lo);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) W[m] = mma(W[m], kf[m][s], sp.hi);
+            }
+            Pair yp[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t* w = df[s].w;
+                const f32x4 y0 = {bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+                const f32x4 y1 = {bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3])};
+                yp[s] = split2(y0 * qin[2 * s], y1 * qin[2 * s + 1]);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) W[m] *= kout[m];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int s = m / 2; s < 2; ++s) {
+                    W[m] = mma(W[m], al[upper_frag(m, s)], df[s]);
+                    W[m] = mma(W[m], ah[upper_frag(m, s)], df[s]);
+                }
+            Frag th[6], tl[6];
+            f32x4 kb[4];
+#pragma unroll
+            for (int f = 0; f < 6; ++f) {
+                th[f] = frag(LD::tt + f * 2048);
+                tl[f] = frag(LD::tt + f * 2048 + 1024);
+            }
+            {
+                // the part of dS that does not wait for Z fills in while W is split
+#pragma unroll
+                for (int n = 0; n < NT; ++n) D[n] *= across;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) kb[m] = scal4(kKin, m) * scal4(kBeta, m);
+#pragma unroll
+                for (int s = 0; s < 2; s += QS) {
+                    Frag qt[QS][NT];
+#pragma unroll
+                    for (int x = 0; x < QS; ++x)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) qt[x][n] = trans(LD::q, s + x, n);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int x = 0; x < QS; ++x) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) D[n] = mma(D[n], qt[x][n], yp[s + x].lo);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) D[n] = mma(D[n], qt[x][n], yp[s + x].hi);
+                    }
+                }
+            }
+            const Pair up[2] = {split2(W[0], W[1]), split2(W[2], W[3])};
+            Frag kt[NT][2];
+            auto read_kt = [&](int s) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) kt[n][s] = trans(LD::k, s, n);
+            };
+            read_kt(0);
+            if (QS == 2) read_kt(1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 1; s >= 0; --s)
+#pragma unroll
+                for (int x = 0; x < 3; ++x)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        if (m / 2 > s) continue;
+                        const int f = upper_frag(m, s);
+                        Z[m] = x == 0 ? mma(Z[m], tl[f], up[s].hi) : mma(Z[m], th[f], x == 1 ? up[s].lo : up[s].hi);
+                    }
+            float* kz = io.Z + u * C * a.P + p;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) kz[(size_t)(16 * m + 4 * q + r) * a.P] = Z[m][r];
+                Z[m] *= -kb[m];
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Pair zp = split2(Z[2 * s], Z[2 * s + 1]);
+                if (QS == 1 && s == 1) read_kt(1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) D[n] = mma(D[n], kt[n][s], zp.lo);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) D[n] = mma(D[n], kt[n][s], zp.hi);
+            }
+            lds_barrier();
+        }
+        if (nch & 1) lds_barrier();                  // the other waves go in pairs
+        if (ba.g_init) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(ba.g_init + sofs + 32 * (n / 2) + 4 * (n % 2)) = f4(D[n]);
+        }
+        return;
+    }
+    // ---- staging: two chunks on their way; a step past the first chunk is that chunk again, rows past the sequence
+    // read its last row and become zeros
+    constexpr int NK = C * nc16 / 256, NTp = Bytes<false>::split / 4096;
+    u32x4_t rk[2][NK], rq[2][NK], rd[2][2], rt[2][NTp], ra[2][NTp];
+    float rs[2], rx[2];
+    const unsigned char* kb = static_cast<const unsigned char*>(a.k) + (tok0 * a.k_stride + (size_t)g * N) * 2;
+    const unsigned char* qb = static_cast<const unsigned char*>(a.q) + (tok0 * a.q_stride + (size_t)g * N) * 2;
+    const unsigned char* db = static_cast<const unsigned char*>(ba.gy) + (tok0 * ba.gy_stride + (size_t)h * a.P + p0) * 2;
+    const uint32_t k_row = (uint32_t)a.k_stride * 2, q_row = (uint32_t)a.q_stride * 2, d_row = (uint32_t)ba.gy_stride * 2;
+    auto fetch = [&](int e, auto set) {
+        constexpr int Z = decltype(set)::value;
+        const int c = max(nch - 1 - e, 0);
+        const size_t u = (size_t)bh * io.nc + c;
+        const int n_on = min(C, len - c * C);
+        const unsigned char *kc = kb + (size_t)c * C * k_row, *qc = qb + (size_t)c * C * q_row, *dc = db + (size_t)c * C * d_row;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int x = tid + 256 * j, t = min(x / nc16, n_on - 1);
+            rk[Z][j] = *reinterpret_cast<const u32x4_t*>(kc + ((uint32_t)t * k_row + x % nc16 * 16));
+            rq[Z][j] = *reinterpret_cast<const u32x4_t*>(qc + ((uint32_t)t * q_row + x % nc16 * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int x = tid + 256 * j, t = min(x / 8, n_on - 1);
+            rd[Z][j] = *reinterpret_cast<const u32x4_t*>(dc + ((uint32_t)t * d_row + x % 8 * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < NTp; ++j) {
+            rt[Z][j] = *reinterpret_cast<const u32x4_t*>(io.TT + u * Bytes<false>::split + (tid + 256 * j) * 16);
+            ra[Z][j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<false>::split + (tid + 256 * j) * 16);
+        }
+        rs[Z] = io.scal[u * kScalBwd * C + tid];
+        rx[Z] = io.across[u];
+    };
+    auto stage = [&](int e, auto set) {
+        constexpr int Z = decltype(set)::value;
+        unsigned char* const lds = lds_all + (e & 1) * LD::buffer;
+        const int n_on = len - max(nch - 1 - e, 0) * C;
+        const u32x4_t zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int x = tid + 256 * j, t = x / nc16, at = t * LD::kRow + row_piece<N>(t, x % nc16) * 16;
+            *reinterpret_cast<u32x4_t*>(lds + LD::k + at) = t < n_on ? rk[Z][j] : zero;
+            *reinterpret_cast<u32x4_t*>(lds + LD::q + at) = t < n_on ? rq[Z][j] : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int x = tid + 256 * j, t = x / 8;
+            *reinterpret_cast<u32x4_t*>(lds + LD::d + t * LD::dRow + x % 8 * 16) = t < n_on ? rd[Z][j] : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < NTp; ++j) {
+            *reinterpret_cast<u32x4_t*>(lds + LD::tt + (tid + 256 * j) * 16) = rt[Z][j];
+            *reinterpret_cast<u32x4_t*>(lds + LD::att + (tid + 256 * j) * 16) = ra[Z][j];
+        }
+        *reinterpret_cast<float*>(lds + LD::scal + tid * 4) = rs[Z];
+        if (tid == 0) *reinterpret_cast<float*>(lds + LD::across) = rx[Z];
+    };
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
+    if (nch > 0) {
+        fetch(0, even);
+        stage(0, even);
+        fetch(1, odd);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(2, even);
+    }
+    lds_barrier();
+    for (int e = 0; e < nch; e += 2) {
+        stage(e + 1, odd);
+        fetch(e + 3, odd);
+        lds_barrier();
+        stage(e + 2, even);
+        fetch(e + 4, even);
+        lds_barrier();
+    }
+}
+
+// ---- fp32
+template <int N>
 struct RevLds {
-    static constexpr bool F32 = std::is_same<T, float>::value;
-    static constexpr int es = sizeof(T);
+    static constexpr bool F32 = true;
+    static constexpr int es = 4;
     static constexpr int kRow = N * es + 16, dRow = 64 * es + 16;
     static constexpr int k = 0, q = k + C * kRow, d = q + C * kRow, tt = d + C * dRow;
     static constexpr int att = tt + Bytes<F32>::split, scal = att + Bytes<F32>::split;
@@ -52,11 +322,11 @@ struct RevLds {
     static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
 };
 
-template <typename T, int N>
+template <int N>
 __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba, BwdIo io) {
-    using LD = RevLds<T, N>;
+    using LD = RevLds<N>;
     constexpr bool F32 = LD::F32;
-    constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
+    constexpr int NT = N / 16, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
     extern __shared__ __align__(16) unsigned char lds_all[];
     const DeltaArgs& a = ba.f;
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
@@ -152,78 +422,7 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
 #pragma unroll
                 for (int r = 0; r < 4; ++r) kd[(size_t)(state_n(n) + r) * a.P] = D[n][r];
         }
-        if constexpr (!F32) {
-            Pair sp[KS];
-#pragma unroll
-            for (int s = 0; s < KS; ++s) sp[s] = split2(D[2 * s], D[2 * s + 1]);
-            Frag df[2];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const FragBF f = tr_read(lds, LD::d + (16 * m + 4 * q + i / 4) * LD::dRow + (16 * wave + 4 * (i % 4)) * 2);
-                df[m / 2].w[2 * (m % 2)] = f.a;
-                df[m / 2].w[2 * (m % 2) + 1] = f.b;
-                const f32x4 y = {bf16_lo(f.a), bf16_hi(f.a), bf16_lo(f.b), bf16_hi(f.b)};
-                Y[m] = y * scal4(kQin, m);
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                W[m] = kZero4;
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    Frag kf;
-                    kf.u = *reinterpret_cast<const uint4*>(lds + LD::k + (16 * m + i) * LD::kRow + 64 * s + 16 * q);
-                    W[m] = mma(W[m], kf, sp[s].lo);
-                    W[m] = mma(W[m], kf, sp[s].hi);
-                }
-                W[m] *= scal4(kKout, m);
-#pragma unroll
-                for (int s = m / 2; s < 2; ++s) {
-                    Frag ah, al;
-                    ah.u = frag16(LD::att + upper_frag(m, s) * 2048);
-                    al.u = frag16(LD::att + upper_frag(m, s) * 2048 + 1024);
-                    W[m] = mma(W[m], al, df[s]);
-                    W[m] = mma(W[m], ah, df[s]);
-                }
-            }
-            const Pair up[2] = {split2(W[0], W[1]), split2(W[2], W[3])};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                Z[m] = kZero4;
-#pragma unroll
-                for (int s = m / 2; s < 2; ++s) {
-                    Frag th, tl;
-                    th.u = frag16(LD::tt + upper_frag(m, s) * 2048);
-                    tl.u = frag16(LD::tt + upper_frag(m, s) * 2048 + 1024);
-                    Z[m] = mma(Z[m], tl, up[s].hi);
-                    Z[m] = mma(Z[m], th, up[s].lo);
-                    Z[m] = mma(Z[m], th, up[s].hi);
-                }
-                W[m] = -Z[m] * scal4(kKin, m) * scal4(kBeta, m);
-            }
-            const Pair yp[2] = {split2(Y[0], Y[1]), split2(Y[2], Y[3])}, zp[2] = {split2(W[0], W[1]), split2(W[2], W[3])};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                D[n] *= keep;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int col = 32 * (n / 2) + 8 * (i % 4) + 4 * (n % 2);
-                    Frag kt, qt;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = 32 * s + 16 * e + 4 * q + i / 4;
-                        const FragBF f = tr_read(lds, LD::k + row * LD::kRow + col * 2), z = tr_read(lds, LD::q + row * LD::kRow + col * 2);
-                        kt.w[2 * e] = f.a;
-                        kt.w[2 * e + 1] = f.b;
-                        qt.w[2 * e] = z.a;
-                        qt.w[2 * e + 1] = z.b;
-                    }
-                    D[n] = mma(D[n], qt, yp[s].lo);
-                    D[n] = mma(D[n], kt, zp[s].lo);
-                    D[n] = mma(D[n], qt, yp[s].hi);
-                    D[n] = mma(D[n], kt, zp[s].hi);
-                }
-            }
-        } else {
+        {
             f32x4 d4[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -734,10 +933,19 @@ hipError_t launch_bwd_n(const DeltaBwdArgs& ba, void* ws, hipStream_t stream) {
     hipError_t e = launch_keep(a, o, fp(w.S), fp(w.U), stream);
     if (e != hipSuccess) return e;
     BwdIo io{o.TT, o.att, o.scal, o.across, fp(w.S), fp(w.U), fp(w.D), fp(w.Z), fp(w.part), nc};
-    constexpr size_t rev = (size_t)RevLds<T, N>::bytes * RevLds<T, N>::buffers, grad = GradLds<T, N>::bytes;
-    e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_reverse_kernel<T, N>), rev);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((ssd_delta_reverse_kernel<T, N>), dim3(a.B * a.H * (a.P / 64)), dim3(256), rev, stream, ba, io);
+    constexpr size_t grad = GradLds<T, N>::bytes;
+    const dim3 chains(a.B * a.H * (a.P / 64));
+    if constexpr (std::is_same<T, float>::value) {
+        constexpr size_t rev = (size_t)RevLds<N>::bytes * RevLds<N>::buffers;
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_reverse_kernel<N>), rev);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((ssd_delta_reverse_kernel<N>), chains, dim3(256), rev, stream, ba, io);
+    } else {
+        constexpr size_t rev = 2 * BackLds<N>::buffer;
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_back_kernel<N>), rev);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((ssd_delta_back_kernel<N>), chains, dim3(512), rev, stream, ba, io);
+    }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_grad_kernel<T, N>), grad);

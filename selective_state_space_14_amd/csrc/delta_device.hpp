@@ -65,6 +65,15 @@ struct PrepOut {
 };
 
 
+// A 64 x N bf16 matrix in LDS, rows unpadded: the 16-byte piece of row t that
+// holds entries 8 x .. 8 x + 7.  Both kinds of read hit every bank once: by
+// rows (16 consecutive rows, one x) and transposed (rows 4 q .. 4 q + 3, four
+// consecutive x).
+template <int N>
+__device__ __forceinline__ int row_piece(int t, int x) {
+    return x ^ (N == 128 ? (t & 3) << 2 | (t >> 2 & 3) : N == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 3) : t >> 2 & 3);
+}
+
 // ------------------------------------------------------------ sums over the four 16-lane rows
 __device__ __forceinline__ float rows_sum(float v) {
     const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
