@@ -571,7 +571,7 @@ struct Last<float> {
 };
 
 template <typename T, int N>
-__global__ __launch_bounds__(256) void ssd_delta_grad_kernel(DeltaBwdArgs ba, BwdIo io) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_delta_grad_kernel(DeltaBwdArgs ba, BwdIo io) {
     using LD = GradLds<T, N>;
     constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16;
     extern __shared__ __align__(16) unsigned char lds[];
@@ -614,7 +614,7 @@ __global__ __launch_bounds__(256) void ssd_delta_grad_kernel(DeltaBwdArgs ba, Bw
     }
     const int t = 16 * w + i;                        // this lane's token
     const bool on = t < n_on;
-    const size_t trow = tok0 + min(t, n_on - 1);
+    const uint32_t row = min(t, n_on - 1);           // offsets within a chunk fit 32 bits
     f32x4 dQ[NT], dK[NT];                            // [n][t]
 #pragma unroll
     for (int n = 0; n < NT; ++n) dQ[n] = dK[n] = kZero4;
@@ -636,26 +636,27 @@ __global__ __launch_bounds__(256) void ssd_delta_grad_kernel(DeltaBwdArgs ba, Bw
         for (int p0 = 0; p0 < a.P; p0 += 64) {
             // the wave's own rows t: dY, Z, U as operands; dV; U's tile for everyone
             Rows<T> dy[2];
-            Wide<T> z[2], uw[2], ds[(NT + 3) / 4][2];
+            Wide<T> z[2], ds[(NT + 3) / 4][2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int col = p0 + 32 * s + 8 * q;
+                const uint32_t col = p0 + 32 * s + 8 * q;
                 Rows<T> v;
-                dy[s].load(static_cast<const T*>(ba.gy) + trow * ba.gy_stride + (size_t)h * a.P + col);
-                v.load(static_cast<const T*>(a.v) + trow * a.v_stride + (size_t)h * a.P + col);
+                dy[s].load(static_cast<const T*>(ba.gy) + tok0 * ba.gy_stride + (size_t)h * a.P + (row * (uint32_t)ba.gy_stride + col));
+                v.load(static_cast<const T*>(a.v) + tok0 * a.v_stride + (size_t)h * a.P + (row * (uint32_t)a.v_stride + col));
                 if (!on) {
                     dy[s].clear();
                     v.clear();
                 }
-                const float* zp = io.Z + (u * C + t) * a.P + col;
-                const float* up = io.U + (u * C + t) * a.P + col;
+                const float* zp = io.Z + u * C * a.P + ((uint32_t)t * a.P + col);
+                const float* up = io.U + u * C * a.P + ((uint32_t)t * a.P + col);
                 const float4 z0 = *reinterpret_cast<const float4*>(zp), z1 = *reinterpret_cast<const float4*>(zp + 4);
                 z[s].set(z0, z1);
-                uw[s].set(*reinterpret_cast<const float4*>(up), *reinterpret_cast<const float4*>(up + 4));
-                uw[s].put(lds + LD::u + (w * 2 + s) * 2048 + lane * 16);
+                Wide<T> f;
+                f.set(*reinterpret_cast<const float4*>(up), *reinterpret_cast<const float4*>(up + 4));
+                f.put(lds + LD::u + (w * 2 + s) * 2048 + lane * 16);
                 zv += dot8(z0, z1, v);
                 if (t < n_rows) {
-                    T* dst = dv + (size_t)t * ba.dv_stride + (size_t)hh * a.P + col;
+                    T* dst = dv + (size_t)hh * a.P + ((uint32_t)t * (uint32_t)ba.dv_stride + col);
                     st4t(dst, v4(z0) * beta);
                     st4t(dst + 4, v4(z1) * beta);
                 }
@@ -666,9 +667,10 @@ __global__ __launch_bounds__(256) void ssd_delta_grad_kernel(DeltaBwdArgs ba, Bw
                 if (n < NT) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const size_t at = (u * N + 16 * n + i) * a.P + p0 + 32 * s + 8 * q;
-                        const float4 s0 = *reinterpret_cast<const float4*>(io.S + at), s1 = *reinterpret_cast<const float4*>(io.S + at + 4);
-                        const float4 d0 = *reinterpret_cast<const float4*>(io.D + at), d1 = *reinterpret_cast<const float4*>(io.D + at + 4);
+                        const uint32_t at = (uint32_t)(16 * n + i) * a.P + p0 + 32 * s + 8 * q;
+                        const float *sp = io.S + u * N * a.P + at, *dp = io.D + u * N * a.P + at;
+                        const float4 s0 = *reinterpret_cast<const float4*>(sp), s1 = *reinterpret_cast<const float4*>(sp + 4);
+                        const float4 d0 = *reinterpret_cast<const float4*>(dp), d1 = *reinterpret_cast<const float4*>(dp + 4);
                         sd += dot4(v4(s0), v4(d0)) + dot4(v4(s1), v4(d1));
                         ds[j][s].set(d0, d1);
                         Wide<T> f;
@@ -709,13 +711,16 @@ __global__ __launch_bounds__(256) void ssd_delta_grad_kernel(DeltaBwdArgs ba, Bw
             }
             __syncthreads();
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int s = 0; s < 2; ++s) {
+                Wide<T> own;
+                own.get(lds + LD::u + (w * 2 + s) * 2048 + lane * 16);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
+                for (int n = 0; n < NT; ++n) {
                     Wide<T> f;
                     f.get(lds + LD::s + (n * 2 + s) * 2048 + lane * 16);
-                    W3[n] = Wide<T>::mul(W3[n], f, uw[s]);
+                    W3[n] = Wide<T>::mul(W3[n], f, own);
                 }
+            }
             __syncthreads();
         }
         auto sc1 = [&](int what) { return *reinterpret_cast<const float*>(lds + LD::scal + (what * C + t) * 4); };
