@@ -64,9 +64,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void ssd_delta_prep_kernel(DeltaAr
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, q = lane / 16, i = lane % 16;
     const uint32_t id = blockIdx.x * kPrepWaves + wave;   // below 2^31 (api)
     if (id >= (uint32_t)a.B * nc * a.H) return;
-    // the last chunks of every row first: the scan starts with the first ones, which are then the latest written and
-    // mostly still in the last-level cache (256 MB)
-    const int h = (int)(id % a.H), b = (int)(id / a.H % a.B), c = nc - 1 - (int)(id / a.H / a.B);
+    const int h = (int)(id % a.H), b = (int)(id / a.H % a.B), c = (int)(id / a.H / a.B);
     const int t0 = c * C, n_on = min(C, row_len(a, b) - t0);
     if (n_on <= 0) return;
     const size_t u = ((size_t)b * a.H + h) * nc + c;
@@ -406,7 +404,6 @@ struct ScanIo {
     int K, S;
     float *loc, *phi, *s0;
 };
-enum { kY = 0, kKeep = 1 };        // forward: y; backward's recomputation: S and U, no y
 
 // ---- bf16 forward
 // With one sequence's head to a workgroup there is one chain to a SIMD, and
@@ -843,24 +840,27 @@ __global__ __launch_bounds__(256) void ssd_delta_join_kernel(DeltaArgs a, ScanIo
     }
 }
 
-// ---- fp32 forward, and the backward's recomputation
-template <typename T, int N, int MODE>
+// ---- fp32: the forward (kY), and the backward's recomputation of S and U (kKeep)
+// The same chain on the fp32 MFMA (a 16 x 16 x 4 product takes 32 cycles), which is what bounds it: k, q, Att and T come
+// as they are, four waves stage their own chunks, and y is computed in the chain.  B=2 L=300 H=4 P=64 N=32 takes 15 us,
+// five chunks of 3 us.
+enum { kY = 0, kKeep = 1 };
+
+template <int N, int MODE>
 struct ScanLds {
-    static constexpr bool F32 = std::is_same<T, float>::value;
-    static constexpr int es = sizeof(T);
+    static constexpr int es = 4;
     static constexpr int kRow = N * es + 16;         // bytes of a k or q row: the odd 16 spreads rows over the banks
     static constexpr int vRow = 64 * es + 16;
-    static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow, scal = t + Bytes<F32>::split;
+    static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow, scal = t + Bytes<true>::split;
     static constexpr int q = scal + kScal * C * 4, att = q + (MODE == kY ? C * kRow : 0);
-    static constexpr int bytes = att + (MODE == kY ? Bytes<F32>::att : 0);
+    static constexpr int bytes = att + (MODE == kY ? Bytes<true>::att : 0);
     static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
 };
 
-template <typename T, int N, int MODE>
+template <int N, int MODE>
 __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo io) {
-    using LD = ScanLds<T, N, MODE>;
-    constexpr bool F32 = LD::F32;
-    constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
+    using LD = ScanLds<N, MODE>;
+    constexpr int NT = N / 16, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
     constexpr int NS = MODE == kY ? kScal : kScalBwd;
     extern __shared__ __align__(16) unsigned char lds_all[];
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
@@ -875,7 +875,7 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
 
     // the state: tile n of lane (q, i) holds rows state_n(n) .. +3 of column p
     const int p = p0 + 16 * wave + i;
-    auto state_n = [&](int n) { return F32 ? 16 * n + 4 * q : 32 * (n / 2) + 8 * q + 4 * (n % 2); };
+    auto state_n = [&](int n) { return 16 * n + 4 * q; };
     const size_t sofs = ((size_t)bh * a.P + p) * N;
     f32x4 S[NT];
 #pragma unroll
@@ -884,7 +884,7 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
 
     // ---- staging: 16-byte pieces, the next chunk's in registers
     constexpr int NK = C * nc16 / 256, NVp = C * nv16 / 256;
-    constexpr int NTp = (Bytes<F32>::split / 16 + 255) / 256, NA = (Bytes<F32>::att / 16 + 255) / 256;
+    constexpr int NTp = (Bytes<true>::split / 16 + 255) / 256, NA = (Bytes<true>::att / 16 + 255) / 256;
     u32x4_t rk[NK], rq[NK], rv[NVp], rt[NTp], ra[NA];
     float rs = 0.0f, r_across = 0.0f;
     const unsigned char* kb = static_cast<const unsigned char*>(a.k) + (tok0 * a.k_stride + (size_t)g * N) * es;
@@ -909,14 +909,14 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
         }
 #pragma unroll
         for (int j = 0; j < NTp; ++j) {
-            const int e = min(tid + 256 * j, Bytes<F32>::split / 16 - 1);
-            rt[j] = *reinterpret_cast<const u32x4_t*>(io.T + u * Bytes<F32>::split + e * 16);
+            const int e = min(tid + 256 * j, Bytes<true>::split / 16 - 1);
+            rt[j] = *reinterpret_cast<const u32x4_t*>(io.T + u * Bytes<true>::split + e * 16);
         }
         if (MODE == kY) {
 #pragma unroll
             for (int j = 0; j < NA; ++j) {
-                const int e = min(tid + 256 * j, Bytes<F32>::att / 16 - 1);
-                ra[j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<F32>::att + e * 16);
+                const int e = min(tid + 256 * j, Bytes<true>::att / 16 - 1);
+                ra[j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<true>::att + e * 16);
             }
         }
         rs = io.scal[u * NS * C + tid];
@@ -949,11 +949,11 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
         }
 #pragma unroll
         for (int j = 0; j < NTp; ++j)
-            if (tid + 256 * j < Bytes<F32>::split / 16) *reinterpret_cast<u32x4_t*>(lds + LD::t + (tid + 256 * j) * 16) = rt[j];
+            if (tid + 256 * j < Bytes<true>::split / 16) *reinterpret_cast<u32x4_t*>(lds + LD::t + (tid + 256 * j) * 16) = rt[j];
         if (MODE == kY) {
 #pragma unroll
             for (int j = 0; j < NA; ++j)
-                if (tid + 256 * j < Bytes<F32>::att / 16) *reinterpret_cast<u32x4_t*>(lds + LD::att + (tid + 256 * j) * 16) = ra[j];
+                if (tid + 256 * j < Bytes<true>::att / 16) *reinterpret_cast<u32x4_t*>(lds + LD::att + (tid + 256 * j) * 16) = ra[j];
         }
         *reinterpret_cast<float*>(lds + LD::scal + tid * 4) = rs;
     };
@@ -990,172 +990,56 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
                 for (int r = 0; r < 4; ++r) ks[(size_t)(state_n(n) + r) * a.P] = S[n][r];
         }
         f32x4 R[4], X[4], U[4], O[4];
-        if constexpr (!F32) {
-            Frag kf[4][KS], th[6], tl[6];
-            FragBF vf[4];
-            f32x4 kin[4], be[4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    kf[m][s].u = *reinterpret_cast<const uint4*>(lds + LD::k + (16 * m + i) * LD::kRow + 64 * s + 16 * q);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                kin[m] = scal4(kKin, m);
-                be[m] = scal4(kBeta, m);
-                vf[m] = tr_read(lds, LD::v + (16 * m + 4 * q + i / 4) * LD::vRow + (16 * wave + 4 * (i % 4)) * 2);
-            }
-#pragma unroll
-            for (int f = 0; f < 6; ++f) {
-                th[f].u = frag16(LD::t + f * 2048);
-                tl[f].u = frag16(LD::t + f * 2048 + 1024);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            Pair sp[KS];
-#pragma unroll
-            for (int s = 0; s < KS; ++s) sp[s] = split2(S[2 * s], S[2 * s + 1]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) R[m] = kZero4;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) R[m] = mma(R[m], kf[m][s], sp[s].lo);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) R[m] = mma(R[m], kf[m][s], sp[s].hi);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            // the second half's operands: k^T (row n of the tile pair's numbering, K index t), q, Att
-            Frag kt[NT][2], qf[4][KS], af[6];
-            f32x4 kout[4];
-            float qin[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) kout[m] = scal4(kKout, m);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int col = 32 * (n / 2) + 8 * (i % 4) + 4 * (n % 2);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const FragBF f = tr_read(lds, LD::k + (32 * s + 16 * e + 4 * q + i / 4) * LD::kRow + col * 2);
-                        kt[n][s].w[2 * e] = f.a;
-                        kt[n][s].w[2 * e + 1] = f.b;
-                    }
-                }
-            if constexpr (MODE == kY) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    qin[m] = *reinterpret_cast<const float*>(lds + LD::scal + (kQin * C + 16 * m + i) * 4);
-#pragma unroll
-                    for (int s = 0; s < KS; ++s)
-                        qf[m][s].u = *reinterpret_cast<const uint4*>(lds + LD::q + (16 * m + i) * LD::kRow + 64 * s + 16 * q);
-                }
-#pragma unroll
-                for (int f = 0; f < 6; ++f) af[f].u = frag16(LD::att + f * 1024);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const f32x4 v = {bf16_lo(vf[m].a), bf16_hi(vf[m].a), bf16_lo(vf[m].b), bf16_hi(vf[m].b)};
-                X[m] = be[m] * (v - kin[m] * R[m]);
-            }
-            const Pair xp[2] = {split2(X[0], X[1]), split2(X[2], X[3])};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) U[m] = kZero4;
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int x = 0; x < 3; ++x)
-#pragma unroll
-                    for (int m = 2 * s; m < 4; ++m) {
-                        const int f = lower_frag(m, s);
-                        U[m] = x == 0 ? mma(U[m], tl[f], xp[s].hi) : mma(U[m], th[f], x == 1 ? xp[s].lo : xp[s].hi);
-                    }
-            if constexpr (MODE == kY) {
-                const Pair ub[2] = {split2(U[0], U[1]), split2(U[2], U[3])};
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    O[m] = kZero4;
-#pragma unroll
-                    for (int s = 0; s < KS; ++s) O[m] = mma(O[m], sp[s].hi, qf[m][s]);   // [p][t]
-                    O[m] *= qin[m];
-                }
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int m = 2 * s; m < 4; ++m) {
-                        O[m] = mma(O[m], ub[s].lo, af[lower_frag(m, s)]);
-                        O[m] = mma(O[m], ub[s].hi, af[lower_frag(m, s)]);
-                    }
-            }
-            Pair up[2];
-            {
-                f32x4 w[4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) w[m] = U[m] * kout[m];
-                up[0] = split2(w[0], w[1]);
-                up[1] = split2(w[2], w[3]);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) S[n] *= keep;
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) S[n] = mma(S[n], kt[n][s], x ? up[s].hi : up[s].lo);
-        } else {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                R[m] = O[m] = kZero4;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float4 kf = *reinterpret_cast<const float4*>(lds + LD::k + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4);
-                    R[m] = mma_f32(R[m], kf, f4(S[n]));
-                    if constexpr (MODE == kY) {
-                        const float4 qf = *reinterpret_cast<const float4*>(lds + LD::q + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4);
-                        O[m] = mma_f32(O[m], f4(S[n]), qf);
-                    }
-                }
-                const f32x4 kin = scal4(kKin, m), be = scal4(kBeta, m);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float v = *reinterpret_cast<const float*>(lds + LD::v + (16 * m + 4 * q + r) * LD::vRow + (16 * wave + i) * 4);
-                    X[m][r] = be[r] * (v - kin[r] * R[m][r]);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                U[m] = kZero4;
-#pragma unroll
-                for (int n = 0; n <= m; ++n)
-                    U[m] = mma_f32(U[m], __builtin_bit_cast(float4, frag16(LD::t + tile_id(m, n) * 1024)), f4(X[n]));
-            }
-            if constexpr (MODE == kY) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    O[m] *= *reinterpret_cast<const float*>(lds + LD::scal + (kQin * C + 16 * m + i) * 4);
-#pragma unroll
-                    for (int n = 0; n <= m; ++n)
-                        O[m] = mma_f32(O[m], f4(U[n]), __builtin_bit_cast(float4, frag16(LD::att + tile_id(m, n) * 1024)));
-                }
-            }
-            f32x4 w[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) w[m] = U[m] * scal4(kKout, m);
+        for (int m = 0; m < 4; ++m) {
+            R[m] = O[m] = kZero4;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                S[n] *= keep;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const unsigned char* kc = lds + LD::k + (16 * m + 4 * q) * LD::kRow + (16 * n + i) * 4;
-                    float4 kt;
-                    kt.x = *reinterpret_cast<const float*>(kc);
-                    kt.y = *reinterpret_cast<const float*>(kc + LD::kRow);
-                    kt.z = *reinterpret_cast<const float*>(kc + 2 * LD::kRow);
-                    kt.w = *reinterpret_cast<const float*>(kc + 3 * LD::kRow);
-                    S[n] = mma_f32(S[n], kt, f4(w[m]));
+                const float4 kf = *reinterpret_cast<const float4*>(lds + LD::k + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4);
+                R[m] = mma_f32(R[m], kf, f4(S[n]));
+                if constexpr (MODE == kY) {
+                    const float4 qf = *reinterpret_cast<const float4*>(lds + LD::q + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4);
+                    O[m] = mma_f32(O[m], f4(S[n]), qf);
                 }
+            }
+            const f32x4 kin = scal4(kKin, m), be = scal4(kBeta, m);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float v = *reinterpret_cast<const float*>(lds + LD::v + (16 * m + 4 * q + r) * LD::vRow + (16 * wave + i) * 4);
+                X[m][r] = be[r] * (v - kin[r] * R[m][r]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            U[m] = kZero4;
+#pragma unroll
+            for (int n = 0; n <= m; ++n)
+                U[m] = mma_f32(U[m], __builtin_bit_cast(float4, frag16(LD::t + tile_id(m, n) * 1024)), f4(X[n]));
+        }
+        if constexpr (MODE == kY) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                O[m] *= *reinterpret_cast<const float*>(lds + LD::scal + (kQin * C + 16 * m + i) * 4);
+#pragma unroll
+                for (int n = 0; n <= m; ++n)
+                    O[m] = mma_f32(O[m], f4(U[n]), __builtin_bit_cast(float4, frag16(LD::att + tile_id(m, n) * 1024)));
+            }
+        }
+        f32x4 w[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) w[m] = U[m] * scal4(kKout, m);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            S[n] *= keep;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const unsigned char* kc = lds + LD::k + (16 * m + 4 * q) * LD::kRow + (16 * n + i) * 4;
+                float4 kt;
+                kt.x = *reinterpret_cast<const float*>(kc);
+                kt.y = *reinterpret_cast<const float*>(kc + LD::kRow);
+                kt.z = *reinterpret_cast<const float*>(kc + 2 * LD::kRow);
+                kt.w = *reinterpret_cast<const float*>(kc + 3 * LD::kRow);
+                S[n] = mma_f32(S[n], kt, f4(w[m]));
             }
         }
         if constexpr (LD::buffers == 1) lds_barrier();   // this chunk's operands have been read
@@ -1171,8 +1055,7 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
             for (int m = 0; m < 4; ++m) {
                 const int t = 16 * m + i;
                 const uint32_t at = c * C + t < len ? (uint32_t)t * y_row + y_col : 0x80000000u;
-                if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, O[m]), yr, at, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{pack_bf16x2(O[m][0], O[m][1]), pack_bf16x2(O[m][2], O[m][3])}, yr, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, O[m]), yr, at, 0, 0);
             }
         } else {
             float* ku = io.keepU + ((size_t)bh * io.nc + c) * C * a.P + p;
@@ -1185,11 +1068,7 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
     }
     if constexpr (MODE == kY) {
         // rows past the sequence are exactly 0
-        for (int t = len + i; t < a.L; t += 16) {
-            unsigned char* at = yb + (size_t)t * y_row + y_col;
-            if constexpr (F32) *reinterpret_cast<float4*>(at) = make_float4(0, 0, 0, 0);
-            else *reinterpret_cast<uint2*>(at) = make_uint2(0, 0);
-        }
+        for (int t = len + i; t < a.L; t += 16) *reinterpret_cast<float4*>(yb + (size_t)t * y_row + y_col) = make_float4(0, 0, 0, 0);
         if (a.final_state) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(a.final_state + sofs + state_n(n)) = f4(S[n]);
@@ -1199,7 +1078,8 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
 
 // Superchunks of a sequence, bf16: the K that takes the fewest chunk steps, with one workgroup a CU at a time.  Against
 // a step of the full pass the state pass's, without y, takes 0.75, and joining one superchunk about 3 (measured: 2.0,
-// 1.5 and 5 us at N = P = 128).  B=1 L=32768 H=16: 1.07 ms with K = 1, KMEASURED.
+// 1.5 and 5 us at N = P = 128).  B=1 L=32768 H=16 N=P=128 takes 1.07 ms
+// whole and 0.52 ms in the superchunks chosen.
 void delta_split(int B, int L, int H, int P, int N, int dtype, int& K, int& S) {
     const int nc = (L + C - 1) / C;
     const int64_t units = (int64_t)B * H * (P / 64), wide = (int64_t)B * H * (P / 64 + (N + 63) / 64);
@@ -1257,10 +1137,10 @@ hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
     ScanIo io{o.T, o.att, o.scal, o.across, nc, nullptr, nullptr, w.K, w.S, fp(w.loc), fp(w.phi), fp(w.s0)};
     const dim3 grid(a.B * a.H * (a.P / 64) * w.K);
     if constexpr (F32) {
-        constexpr size_t lds = (size_t)ScanLds<T, N, kY>::bytes * ScanLds<T, N, kY>::buffers;
-        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N, kY>), lds);
+        constexpr size_t lds = (size_t)ScanLds<N, kY>::bytes * ScanLds<N, kY>::buffers;
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<N, kY>), lds);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kY>), grid, dim3(256), lds, stream, a, io);
+        hipLaunchKernelGGL((ssd_delta_scan_kernel<N, kY>), grid, dim3(256), lds, stream, a, io);
     } else {
         constexpr size_t lds = ChainLds<N, kFull>::bytes;
         if (w.K > 1) {
@@ -1293,10 +1173,10 @@ hipError_t launch_keep_n(const DeltaArgs& a, const PrepOut& o, float* keepS, flo
     ScanIo io{o.T, nullptr, o.scal, o.across, nc, keepS, keepU, 1, nc, nullptr, nullptr, nullptr};
     const dim3 grid(a.B * a.H * (a.P / 64));
     if constexpr (std::is_same<T, float>::value) {
-        constexpr size_t lds = (size_t)ScanLds<T, N, kKeep>::bytes * ScanLds<T, N, kKeep>::buffers;
-        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<T, N, kKeep>), lds);
+        constexpr size_t lds = (size_t)ScanLds<N, kKeep>::bytes * ScanLds<N, kKeep>::buffers;
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<N, kKeep>), lds);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((ssd_delta_scan_kernel<T, N, kKeep>), grid, dim3(256), lds, stream, a, io);
+        hipLaunchKernelGGL((ssd_delta_scan_kernel<N, kKeep>), grid, dim3(256), lds, stream, a, io);
     } else {
         constexpr size_t lds = ChainLds<N, kStates>::bytes;
         e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, kStates>), lds);

@@ -313,11 +313,10 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba,
 // ---- fp32
 template <int N>
 struct RevLds {
-    static constexpr bool F32 = true;
     static constexpr int es = 4;
     static constexpr int kRow = N * es + 16, dRow = 64 * es + 16;
     static constexpr int k = 0, q = k + C * kRow, d = q + C * kRow, tt = d + C * dRow;
-    static constexpr int att = tt + Bytes<F32>::split, scal = att + Bytes<F32>::split;
+    static constexpr int att = tt + Bytes<true>::split, scal = att + Bytes<true>::split;
     static constexpr int bytes = scal + kScal * C * 4;
     static constexpr int buffers = 2 * bytes <= 160 * 1024 ? 2 : 1;
 };
@@ -325,7 +324,6 @@ struct RevLds {
 template <int N>
 __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba, BwdIo io) {
     using LD = RevLds<N>;
-    constexpr bool F32 = LD::F32;
     constexpr int NT = N / 16, es = LD::es, nc16 = N * es / 16, nv16 = 64 * es / 16;
     extern __shared__ __align__(16) unsigned char lds_all[];
     const DeltaArgs& a = ba.f;
@@ -338,14 +336,14 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
     const int len = row_len(a, b), nch = (len + C - 1) / C;
     const size_t tok0 = (size_t)b * a.L;
     const int p = p0 + 16 * wave + i;
-    auto state_n = [&](int n) { return F32 ? 16 * n + 4 * q : 32 * (n / 2) + 8 * q + 4 * (n % 2); };
+    auto state_n = [&](int n) { return 16 * n + 4 * q; };
     const size_t sofs = ((size_t)bh * a.P + p) * N;
     f32x4 D[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         D[n] = ba.g_final ? v4(*reinterpret_cast<const float4*>(ba.g_final + sofs + state_n(n))) : kZero4;
 
-    constexpr int NK = C * nc16 / 256, NVp = C * nv16 / 256, NTp = (Bytes<F32>::split / 16 + 255) / 256;
+    constexpr int NK = C * nc16 / 256, NVp = C * nv16 / 256, NTp = (Bytes<true>::split / 16 + 255) / 256;
     u32x4_t rk[NK], rq[NK], rd[NVp], rt[NTp], ra[NTp];
     float rs = 0.0f, r_across = 0.0f;
     const unsigned char* kb = static_cast<const unsigned char*>(a.k) + (tok0 * a.k_stride + (size_t)g * N) * es;
@@ -369,9 +367,9 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
         }
 #pragma unroll
         for (int j = 0; j < NTp; ++j) {
-            const int e = min(tid + 256 * j, Bytes<F32>::split / 16 - 1);
-            rt[j] = *reinterpret_cast<const u32x4_t*>(io.TT + u * Bytes<F32>::split + e * 16);
-            ra[j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<F32>::split + e * 16);
+            const int e = min(tid + 256 * j, Bytes<true>::split / 16 - 1);
+            rt[j] = *reinterpret_cast<const u32x4_t*>(io.TT + u * Bytes<true>::split + e * 16);
+            ra[j] = *reinterpret_cast<const u32x4_t*>(io.att + u * Bytes<true>::split + e * 16);
         }
         rs = io.scal[u * kScalBwd * C + tid];
         r_across = io.across[u];
@@ -392,7 +390,7 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
         }
 #pragma unroll
         for (int j = 0; j < NTp; ++j)
-            if (tid + 256 * j < Bytes<F32>::split / 16) {
+            if (tid + 256 * j < Bytes<true>::split / 16) {
                 *reinterpret_cast<u32x4_t*>(lds + LD::tt + (tid + 256 * j) * 16) = rt[j];
                 *reinterpret_cast<u32x4_t*>(lds + LD::att + (tid + 256 * j) * 16) = ra[j];
             }
@@ -422,48 +420,46 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
 #pragma unroll
                 for (int r = 0; r < 4; ++r) kd[(size_t)(state_n(n) + r) * a.P] = D[n][r];
         }
-        {
-            f32x4 d4[4];
+        f32x4 d4[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                d4[m][r] = *reinterpret_cast<const float*>(lds + LD::d + (16 * m + 4 * q + r) * LD::dRow + (16 * wave + i) * 4);
+            Y[m] = d4[m] * scal4(kQin, m);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            W[m] = kZero4;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                W[m] = mma_f32(W[m], *reinterpret_cast<const float4*>(lds + LD::k + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4), f4(D[n]));
+            W[m] *= scal4(kKout, m);
+#pragma unroll
+            for (int t = m; t < 4; ++t)
+                W[m] = mma_f32(W[m], __builtin_bit_cast(float4, frag16(LD::att + tile_id(t, m) * 1024)), f4(d4[t]));
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            Z[m] = kZero4;
+#pragma unroll
+            for (int t = m; t < 4; ++t)
+                Z[m] = mma_f32(Z[m], __builtin_bit_cast(float4, frag16(LD::tt + tile_id(t, m) * 1024)), f4(W[t]));
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) W[m] = -Z[m] * scal4(kKin, m) * scal4(kBeta, m);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            D[n] *= keep;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    d4[m][r] = *reinterpret_cast<const float*>(lds + LD::d + (16 * m + 4 * q + r) * LD::dRow + (16 * wave + i) * 4);
-                Y[m] = d4[m] * scal4(kQin, m);
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                W[m] = kZero4;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    W[m] = mma_f32(W[m], *reinterpret_cast<const float4*>(lds + LD::k + (16 * m + i) * LD::kRow + (16 * n + 4 * q) * 4), f4(D[n]));
-                W[m] *= scal4(kKout, m);
-#pragma unroll
-                for (int t = m; t < 4; ++t)
-                    W[m] = mma_f32(W[m], __builtin_bit_cast(float4, frag16(LD::att + tile_id(t, m) * 1024)), f4(d4[t]));
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                Z[m] = kZero4;
-#pragma unroll
-                for (int t = m; t < 4; ++t)
-                    Z[m] = mma_f32(Z[m], __builtin_bit_cast(float4, frag16(LD::tt + tile_id(t, m) * 1024)), f4(W[t]));
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) W[m] = -Z[m] * scal4(kKin, m) * scal4(kBeta, m);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                D[n] *= keep;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    auto col = [&](int base) {
-                        const unsigned char* at = lds + base + (16 * m + 4 * q) * LD::kRow + (16 * n + i) * 4;
-                        return make_float4(*reinterpret_cast<const float*>(at), *reinterpret_cast<const float*>(at + LD::kRow),
-                                           *reinterpret_cast<const float*>(at + 2 * LD::kRow), *reinterpret_cast<const float*>(at + 3 * LD::kRow));
-                    };
-                    D[n] = mma_f32(D[n], col(LD::q), f4(Y[m]));
-                    D[n] = mma_f32(D[n], col(LD::k), f4(W[m]));
-                }
+                auto col = [&](int base) {
+                    const unsigned char* at = lds + base + (16 * m + 4 * q) * LD::kRow + (16 * n + i) * 4;
+                    return make_float4(*reinterpret_cast<const float*>(at), *reinterpret_cast<const float*>(at + LD::kRow),
+                                       *reinterpret_cast<const float*>(at + 2 * LD::kRow), *reinterpret_cast<const float*>(at + 3 * LD::kRow));
+                };
+                D[n] = mma_f32(D[n], col(LD::q), f4(Y[m]));
+                D[n] = mma_f32(D[n], col(LD::k), f4(W[m]));
             }
         }
         if constexpr (LD::buffers == 1) lds_barrier();
