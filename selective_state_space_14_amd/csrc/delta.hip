@@ -398,9 +398,9 @@ struct ScanIo {
     const unsigned char *T, *att;
     const float *scal, *across;
     int nc;
-    float *keepS, *keepU;          // kKeep: the state entering each chunk [u][N][P] and U [u][C][P]
-    // sequence split: K superchunks of S chunks (K = 1: none).  Of all but the last, the end state from a zero state
-    // [b h][K - 1][P][N] and the transition [b h][K - 1][N columns][N]; the state entering each [b h][K][P][N].
+    float *keepS, *keepU;          // backward: the state entering each chunk [u][N][P] and U [u][C][P]
+    // sequence split: K superchunks of S chunks (K = 1: none).  Of each, the end state from a zero state [b h][K][P][N]
+    // and the transition [b h][K][N columns][N] (the forward's last has none); the state entering each [b h][K][P][N].
     int K, S;
     float *loc, *phi, *s0;
 };
@@ -427,7 +427,7 @@ struct ScanIo {
 // entering the superchunks together; the full launch runs them side by side.
 // The backward's recomputation is the same chain (kStates) with T and beta apart, each chunk's entering state and U
 // going to memory from the chain's waves, and no y.
-enum { kFull = 0, kState = 1, kStates = 2 };
+enum { kFull = 0, kState = 1, kStates = 2, kStateApart = 3 };   // kStateApart: kState for kStates
 
 template <int N, int MODE>
 struct ChainLds {
@@ -435,10 +435,11 @@ struct ChainLds {
     static constexpr int vRow = 64 * 2 + 16;
     static constexpr int KS = N / 32;
     static __device__ __forceinline__ int piece(int t, int x) { return row_piece<N>(t, x); }
+    static constexpr bool apart = MODE == kStates || MODE == kStateApart;   // T, beta and kout come by themselves
     static constexpr int k = 0, v = k + C * kRow, t = v + C * vRow;
-    static constexpr int t_bytes = MODE == kStates ? Bytes<false>::split : Bytes<false>::packed;
-    // kin (kStates: all four arrays of scalars), then the decay across the chunk
-    static constexpr int kin = t + t_bytes, across = kin + (MODE == kStates ? kScal : 1) * C * 4;
+    static constexpr int t_bytes = apart ? Bytes<false>::split : Bytes<false>::packed;
+    // kin (apart: all four arrays of scalars), then the decay across the chunk
+    static constexpr int kin = t + t_bytes, across = kin + (apart ? kScal : 1) * C * 4;
     static constexpr int buffer = across + 256;
     static constexpr int kept = (KS + 4) * 1024;     // a wave's S (rounded) and X (split) fragments
     static constexpr int bytes = 2 * (buffer + (MODE == kFull ? 4 * kept : 0));
@@ -448,17 +449,18 @@ template <int N, int MODE>
 __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, ScanIo io) {
     using LD = ChainLds<N, MODE>;
     constexpr int NT = N / 16, KS = N / 32, nc16 = N / 8;
+    constexpr bool kApart = LD::apart, kPass = MODE == kState || MODE == kStateApart;
     extern __shared__ __align__(16) unsigned char lds_all[];
     const int tid = threadIdx.x % 256, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
     // blocks of 64 columns of a head: P's, and in the state pass the transition's
-    const int pb = a.P / 64 + (MODE == kState ? (N + 63) / 64 : 0);
+    const int pb = a.P / 64 + (kPass ? (N + 63) / 64 : 0);
     const int units = a.B * a.H * pb, sk = blockIdx.x / units;
     // heads of a group, which read the same q and k, on one XCD (workgroups go round the eight of them)
     int unit = blockIdx.x % units;
     const int share = a.H / a.G * pb;
     if (a.B * a.G % 8 == 0) unit = (unit / 8 / share * 8 + unit % 8) * share + unit / 8 % share;
     const int blk = unit % pb, bh = unit / pb, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
-    const bool phi = MODE == kState && blk >= a.P / 64;
+    const bool phi = kPass && blk >= a.P / 64;
     const int p0 = phi ? 0 : blk * 64;
     const int len = row_len(a, b), c0 = sk * io.S;
     const int nch = max(0, min(io.S, (len + C - 1) / C - c0));   // chunks here, counted from c0 below
@@ -471,7 +473,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         const size_t sofs = ((size_t)bh * a.P + p0 + 16 * wave + i) * N + 8 * q;
         const int pc = (blk - a.P / 64) * 64 + 16 * wave + i;   // column of the transition
         f32x4 S[NT];
-        const float* first = MODE == kState ? nullptr
+        const float* first = kPass ? nullptr
                              : io.K > 1     ? io.s0 + ((size_t)bh * io.K + sk) * a.P * N + (sofs - (size_t)bh * a.P * N)
                              : a.init_state ? a.init_state + sofs
                                             : nullptr;
@@ -504,7 +506,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             const float across = *reinterpret_cast<const float*>(lds + LD::across);
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (MODE == kStates) {
-                float* to = io.keepS + ((size_t)bh * io.nc + c) * N * a.P + p0 + 16 * wave + i;
+                float* to = io.keepS + ((size_t)bh * io.nc + c0 + c) * N * a.P + p0 + 16 * wave + i;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -532,7 +534,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
 #pragma unroll
                 for (int s = 0; s < m / 2 + 1; ++s) {
                     const int f = lower_frag(m, s);
-                    if constexpr (MODE == kStates) {
+                    if constexpr (kApart) {
                         const unsigned char* at = lds + LD::t + f * 2048 + lane * 16;
                         th[f].u = *reinterpret_cast<const uint4*>(at);
                         tl[f].u = *reinterpret_cast<const uint4*>(at + 1024);
@@ -542,7 +544,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
                         tl[f].u = packed_read(at + (packed_half(m, s) ? 512 : 1024), packed_half(m, s), lane);
                     }
                 }
-                if constexpr (MODE == kStates) {
+                if constexpr (kApart) {
                     be[m] = v4(*reinterpret_cast<const float4*>(lds + LD::kin + (kBeta * C + 16 * m + 4 * q) * 4));
                     kout[m] = v4(*reinterpret_cast<const float4*>(lds + LD::kin + (kKout * C + 16 * m + 4 * q) * 4));
                 }
@@ -566,7 +568,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             for (int m = 0; m < 4; ++m) {
                 const f32x4 v = {bf16_lo(vf[m].a), bf16_hi(vf[m].a), bf16_lo(vf[m].b), bf16_hi(vf[m].b)};
                 X[m] = v - kin[m] * R[m];
-                if constexpr (MODE == kStates) X[m] *= be[m];
+                if constexpr (kApart) X[m] *= be[m];
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) S[n] *= across;
@@ -586,13 +588,15 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
                     }
             }
             if constexpr (MODE == kStates) {
-                float* to = io.keepU + ((size_t)bh * io.nc + c) * C * a.P + p0 + 16 * wave + i;
+                float* to = io.keepU + ((size_t)bh * io.nc + c0 + c) * C * a.P + p0 + 16 * wave + i;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
+                for (int m = 0; m < 4; ++m)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) to[(size_t)(16 * m + 4 * q + r) * a.P] = U[m][r];
-                    U[m] *= kout[m];
-                }
+            }
+            if constexpr (kApart) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) U[m] *= kout[m];
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -608,8 +612,8 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         float* last;
         if (MODE == kStates) {
             last = nullptr;
-        } else if (MODE == kState) {
-            const size_t u = (size_t)bh * (io.K - 1) + sk;
+        } else if (kPass) {
+            const size_t u = (size_t)bh * io.K + sk;
             last = phi ? (pc < N ? io.phi + (u * N + pc) * N + 8 * q : nullptr) : io.loc + (u * a.P + p0 + 16 * wave + i) * N + 8 * q;
         } else {
             last = a.final_state && sk == io.K - 1 ? a.final_state + sofs : nullptr;
@@ -621,7 +625,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
         return;
     }
     // ---------------------------------------------------- staging and y
-    constexpr int NK = C * nc16 / 256, NV = 2, NTp = (LD::t_bytes / 16 + 255) / 256, NS = MODE == kStates ? kScalBwd : kScal;
+    constexpr int NK = C * nc16 / 256, NV = 2, NTp = (LD::t_bytes / 16 + 255) / 256, NS = kApart ? kScalBwd : kScal;
     // two chunks are on their way at any time, in register sets of their parity: one chunk's time is less than
     // the memory's latency under this kernel's own load
     u32x4_t rk[2][NK], rv[2][NV], rt[2][NTp];
@@ -657,7 +661,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
             const int e = min(tid + 256 * j, LD::t_bytes / 16 - 1);
             rt[Z][j] = *reinterpret_cast<const u32x4_t*>(io.T + u * LD::t_bytes + e * 16);
         }
-        if constexpr (MODE == kStates) {
+        if constexpr (kApart) {
             rs[Z] = io.scal[u * NS * C + tid];
             ra[Z] = io.across[u];
         } else {
@@ -683,7 +687,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
 #pragma unroll
         for (int j = 0; j < NTp; ++j)                // past T's end the last piece again
             *reinterpret_cast<u32x4_t*>(lds + LD::t + min(tid + 256 * j, LD::t_bytes / 16 - 1) * 16) = rt[Z][j];
-        if constexpr (MODE == kStates) {
+        if constexpr (kApart) {
             *reinterpret_cast<float*>(lds + LD::kin + tid * 4) = rs[Z];
             if (tid == 0) *reinterpret_cast<float*>(lds + LD::across) = ra[Z];
         } else {
@@ -796,9 +800,10 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_chain_kernel(DeltaArgs a, Sc
 }
 
 // The states entering the superchunks, S_{k+1} = Phi_k S_k + loc_k in turn, on the fp32 MFMA.  A workgroup has 16
-// columns, its waves every fourth row tile; all of S_k goes round through LDS, whose two halves take turns.
-template <int N>
-__global__ __launch_bounds__(256) void ssd_delta_join_kernel(DeltaArgs a, ScanIo io) {
+// columns, its waves every fourth row tile; all of S_k goes round through LDS, whose two halves take turns.  The
+// backward's gradients of the states (REV) go the other way, D_{k-1} = Phi_k^T D_k + loc_k.
+template <int N, bool REV>
+__global__ __launch_bounds__(256) void ssd_delta_join_kernel(DeltaArgs a, ScanIo io, const float* first) {
     constexpr int NT = N / 16, NW = (NT + 3) / 4;
     __shared__ __align__(16) float4 s_all[2][NT][64];
     const int lane = threadIdx.x % 64, q = lane / 16, i = lane % 16;
@@ -808,23 +813,23 @@ __global__ __launch_bounds__(256) void ssd_delta_join_kernel(DeltaArgs a, ScanIo
 #pragma unroll
     for (int j = 0; j < NW; ++j) {
         const int n = w + 4 * j;
-        S[j] = a.init_state && n < NT ? v4(*reinterpret_cast<const float4*>(a.init_state + ((size_t)bh * a.P + p) * N + 16 * n + 4 * q)) : kZero4;
+        S[j] = first && n < NT ? v4(*reinterpret_cast<const float4*>(first + ((size_t)bh * a.P + p) * N + 16 * n + 4 * q)) : kZero4;
     }
-    for (int k = 0; k < io.K; ++k) {
-        float* to = io.s0 + (((size_t)bh * io.K + k) * a.P + p) * N + 4 * q;
+    for (int x = 0; x < io.K; ++x) {
+        const size_t u = (size_t)bh * io.K + (REV ? io.K - 1 - x : x);
+        float* to = io.s0 + (u * a.P + p) * N + 4 * q;
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
             const int n = w + 4 * j;
             if (n < NT) {
                 *reinterpret_cast<float4*>(to + 16 * n) = f4(S[j]);
-                s_all[k & 1][n][lane] = f4(S[j]);
+                s_all[x & 1][n][lane] = f4(S[j]);
             }
         }
-        if (k == io.K - 1) break;
+        if (x == io.K - 1) break;
         __syncthreads();
-        const size_t u = (size_t)bh * (io.K - 1) + k;
         const float* loc = io.loc + (u * a.P + p) * N + 4 * q;
-        const float* phi = io.phi + (u * N + 4 * q) * N + i;   // [column m][row n]
+        const float* phi = io.phi + u * N * N;                 // [column][row]
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
             const int n = w + 4 * j;
@@ -832,8 +837,14 @@ __global__ __launch_bounds__(256) void ssd_delta_join_kernel(DeltaArgs a, ScanIo
             f32x4 R = v4(*reinterpret_cast<const float4*>(loc + 16 * n));
 #pragma unroll
             for (int m = 0; m < NT; ++m) {
-                const float* f = phi + (size_t)16 * m * N + 16 * n;
-                R = mma_f32(R, make_float4(f[0], f[N], f[2 * N], f[3 * N]), s_all[k & 1][m][lane]);
+                float4 f;                                      // row 16 n + i of Phi or its transpose, columns 16 m + 4 q ..
+                if constexpr (REV) {
+                    f = *reinterpret_cast<const float4*>(phi + (16 * n + i) * N + 16 * m + 4 * q);
+                } else {
+                    const float* at = phi + (16 * m + 4 * q) * N + 16 * n + i;
+                    f = make_float4(at[0], at[N], at[2 * N], at[3 * N]);
+                }
+                R = mma_f32(R, f, s_all[x & 1][m][lane]);
             }
             S[j] = R;
         }
@@ -1078,20 +1089,23 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
 
 // Superchunks of a sequence, bf16: the K that takes the fewest chunk steps, with one workgroup a CU at a time.  Against
 // a step of the full pass the state pass's, without y, takes 0.75, and joining one superchunk about 3 (measured: 2.0,
-// 1.5 and 5 us at N = P = 128).  B=1 L=32768 H=16 N=P=128 takes 1.07 ms
-// whole and 0.52 ms in the superchunks chosen.
-void delta_split(int B, int L, int H, int P, int N, int dtype, int& K, int& S) {
+// 1.5 and 5 us at N = P = 128).  B=1 L=32768 H=16 N=P=128 takes 1.07 ms whole and 0.52 ms in the superchunks chosen.
+// The backward has two full passes (a step of both: 2.2) and two state passes, the transitions in the first only, and two
+// joins: B=2 L=8192 H=32 N=P=64 takes 553 us of chains whole and 382 us in four superchunks, joins and all.
+void delta_split(int B, int L, int H, int P, int N, int dtype, bool bwd, int& K, int& S) {
     const int nc = (L + C - 1) / C;
     const int64_t units = (int64_t)B * H * (P / 64), wide = (int64_t)B * H * (P / 64 + (N + 63) / 64);
     K = 1;
     S = nc;
     if (dtype == 0) return;
     auto rounds = [](int64_t n) { return (double)((n + 255) / 256); };
-    double best = rounds(units) * nc;
+    const double full = bwd ? 2.2 : 1.0;
+    double best = full * rounds(units) * nc;
     for (int k = 2; k <= 32; ++k) {
         const int s = (nc + k - 1) / k, used = (nc + s - 1) / s;
         if (s < 8) break;
-        const double t = s * (rounds(units * used) + 0.75 * rounds(wide * (used - 1))) + 3.0 * (used - 1);
+        const double ahead = bwd ? rounds(wide * used) + rounds(units * (used - 1)) : rounds(wide * (used - 1));
+        const double t = s * (full * rounds(units * used) + 0.75 * ahead) + (bwd ? 6.0 : 3.0) * (used - 1);
         if (t < best) {
             best = t;
             K = used;
@@ -1107,16 +1121,30 @@ struct FwdWs {                     // byte offsets
 FwdWs fwd_ws(int B, int L, int H, int P, int N, int dtype) {
     const size_t heads = (size_t)B * H, units = heads * ((L + C - 1) / C);
     FwdWs w;
-    delta_split(B, L, H, P, N, dtype, w.K, w.S);
+    delta_split(B, L, H, P, N, dtype, false, w.K, w.S);
+    const size_t split = w.K > 1 ? heads * w.K * N * 4 : 0;
     w.T = 0;
     w.att = w.T + units * (dtype == 0 ? Bytes<true>::split : Bytes<false>::packed);
     w.scal = w.att + units * (dtype == 0 ? Bytes<true>::att : Bytes<false>::att);
     w.across = w.scal + units * kScal * C * 4;
     w.loc = w.across + (units * 4 + 255) / 256 * 256;
-    w.phi = w.loc + (w.K > 1 ? heads * (w.K - 1) * P * N * 4 : 0);
-    w.s0 = w.phi + (w.K > 1 ? heads * (w.K - 1) * N * N * 4 : 0);
-    w.total = w.s0 + (w.K > 1 ? heads * w.K * P * N * 4 : 0);
+    w.phi = w.loc + split * P;
+    w.s0 = w.phi + split * N;
+    w.total = w.s0 + split * P;
     return w;
+}
+
+// the states entering the superchunks: the pass over all of them but, in the forward, the last, and the join
+template <int N, int MODE>
+hipError_t launch_ahead(const DeltaArgs& a, const ScanIo& io, int count, hipStream_t stream) {
+    constexpr size_t lds = 2 * ChainLds<N, MODE>::buffer;
+    hipError_t e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, MODE>), lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((ssd_delta_chain_kernel<N, MODE>), dim3(a.B * a.H * (a.P / 64 + (N + 63) / 64) * count), dim3(512), lds, stream, a, io);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((ssd_delta_join_kernel<N, false>), dim3(a.B * a.H * (a.P / 16)), dim3(256), 0, stream, a, io, a.init_state);
+    return hipGetLastError();
 }
 
 template <typename T, int N>
@@ -1144,15 +1172,7 @@ hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
     } else {
         constexpr size_t lds = ChainLds<N, kFull>::bytes;
         if (w.K > 1) {
-            constexpr size_t state_lds = 2 * ChainLds<N, kState>::buffer;   // nothing is kept for y
-            e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, kState>), state_lds);
-            if (e != hipSuccess) return e;
-            hipLaunchKernelGGL((ssd_delta_chain_kernel<N, kState>), dim3(a.B * a.H * (a.P / 64 + (N + 63) / 64) * (w.K - 1)),
-                               dim3(512), state_lds, stream, a, io);
-            e = hipGetLastError();
-            if (e != hipSuccess) return e;
-            hipLaunchKernelGGL((ssd_delta_join_kernel<N>), dim3(a.B * a.H * (a.P / 16)), dim3(256), 0, stream, a, io);
-            e = hipGetLastError();
+            e = launch_ahead<N, kState>(a, io, w.K - 1, stream);
             if (e != hipSuccess) return e;
         }
         e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, kFull>), lds);
@@ -1163,15 +1183,15 @@ hipError_t launch_fwd_n(const DeltaArgs& a, void* ws, hipStream_t stream) {
 }
 
 template <typename T, int N>
-hipError_t launch_keep_n(const DeltaArgs& a, const PrepOut& o, float* keepS, float* keepU, hipStream_t stream) {
+hipError_t launch_keep_n(const DeltaArgs& a, const PrepOut& o, const KeepOut& k, hipStream_t stream) {
     const int nc = (a.L + C - 1) / C;
     const int64_t units = (int64_t)a.B * a.H * nc;
     hipLaunchKernelGGL((ssd_delta_prep_kernel<T, N, kPrepBwd>), dim3((unsigned)((units + kPrepWaves - 1) / kPrepWaves)),
                        dim3(64 * kPrepWaves), 0, stream, a, o, nc);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    ScanIo io{o.T, nullptr, o.scal, o.across, nc, keepS, keepU, 1, nc, nullptr, nullptr, nullptr};
-    const dim3 grid(a.B * a.H * (a.P / 64));
+    ScanIo io{o.T, nullptr, o.scal, o.across, nc, k.S, k.U, k.split.K, k.split.S, k.split.loc, k.split.phi, k.split.s0};
+    const dim3 grid(a.B * a.H * (a.P / 64) * k.split.K);
     if constexpr (std::is_same<T, float>::value) {
         constexpr size_t lds = (size_t)ScanLds<N, kKeep>::bytes * ScanLds<N, kKeep>::buffers;
         e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_scan_kernel<N, kKeep>), lds);
@@ -1179,6 +1199,10 @@ hipError_t launch_keep_n(const DeltaArgs& a, const PrepOut& o, float* keepS, flo
         hipLaunchKernelGGL((ssd_delta_scan_kernel<N, kKeep>), grid, dim3(256), lds, stream, a, io);
     } else {
         constexpr size_t lds = ChainLds<N, kStates>::bytes;
+        if (k.split.K > 1) {                         // the last superchunk's transition is for the gradients
+            e = launch_ahead<N, kStateApart>(a, io, k.split.K, stream);
+            if (e != hipSuccess) return e;
+        }
         e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_chain_kernel<N, kStates>), lds);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((ssd_delta_chain_kernel<N, kStates>), grid, dim3(512), lds, stream, a, io);
@@ -1186,13 +1210,25 @@ hipError_t launch_keep_n(const DeltaArgs& a, const PrepOut& o, float* keepS, flo
     return hipGetLastError();
 }
 template <typename T>
-hipError_t launch_keep_t(const DeltaArgs& a, const PrepOut& o, float* keepS, float* keepU, hipStream_t stream) {
+hipError_t launch_keep_t(const DeltaArgs& a, const PrepOut& o, const KeepOut& k, hipStream_t stream) {
     switch (a.N) {
-        case 32: return launch_keep_n<T, 32>(a, o, keepS, keepU, stream);
-        case 64: return launch_keep_n<T, 64>(a, o, keepS, keepU, stream);
-        case 128: return launch_keep_n<T, 128>(a, o, keepS, keepU, stream);
+        case 32: return launch_keep_n<T, 32>(a, o, k, stream);
+        case 64: return launch_keep_n<T, 64>(a, o, k, stream);
+        case 128: return launch_keep_n<T, 128>(a, o, k, stream);
     }
     return hipErrorInvalidValue;
+}
+
+template <int N>
+hipError_t launch_join_back_n(const DeltaArgs& a, const Split& s, const float* g_final, hipStream_t stream) {
+    ScanIo io{};
+    io.K = s.K;
+    io.S = s.S;
+    io.loc = s.loc;
+    io.phi = s.phi;
+    io.s0 = s.s0;
+    hipLaunchKernelGGL((ssd_delta_join_kernel<N, true>), dim3(a.B * a.H * (a.P / 16)), dim3(256), 0, stream, a, io, g_final);
+    return hipGetLastError();
 }
 
 template <typename T>
@@ -1208,9 +1244,18 @@ hipError_t launch_fwd_t(const DeltaArgs& a, void* ws, hipStream_t stream) {
 }  // namespace
 
 namespace delta {
-hipError_t launch_keep(const DeltaArgs& a, const PrepOut& o, float* keepS, float* keepU, hipStream_t stream) {
-    return a.dtype == 0 ? launch_keep_t<float>(a, o, keepS, keepU, stream) : launch_keep_t<uint16_t>(a, o, keepS, keepU, stream);
+hipError_t launch_keep(const DeltaArgs& a, const PrepOut& o, const KeepOut& k, hipStream_t stream) {
+    return a.dtype == 0 ? launch_keep_t<float>(a, o, k, stream) : launch_keep_t<uint16_t>(a, o, k, stream);
 }
+hipError_t launch_join_back(const DeltaArgs& a, const Split& s, const float* g_final, hipStream_t stream) {
+    switch (a.N) {
+        case 32: return launch_join_back_n<32>(a, s, g_final, stream);
+        case 64: return launch_join_back_n<64>(a, s, g_final, stream);
+        case 128: return launch_join_back_n<128>(a, s, g_final, stream);
+    }
+    return hipErrorInvalidValue;
+}
+void split_bwd(int B, int L, int H, int P, int N, int dtype, Split& s) { delta_split(B, L, H, P, N, dtype, true, s.K, s.S); }
 }  // namespace delta
 
 size_t delta_fwd_workspace_bytes(int B, int L, int H, int P, int N, int dtype) { return fwd_ws(B, L, H, P, N, dtype).total; }

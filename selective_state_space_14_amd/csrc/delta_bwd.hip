@@ -35,6 +35,7 @@ struct BwdIo {
     float *D, *Z;                  // as S and U: the adjoint leaving each chunk, Z
     float* part;                   // [2][B * nc][H]
     int nc;
+    Split split;
 };
 
 // ============================================================ the reverse chain
@@ -51,7 +52,8 @@ struct BackLds {
     static constexpr int buffer = across + 256;
 };
 
-template <int N>
+// AHEAD: superchunks from a zero gradient, for launch_join_back.
+template <int N, bool AHEAD>
 __global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba, BwdIo io) {
     using LD = BackLds<N>;
     constexpr int NT = N / 16, KS = N / 32, nc16 = N / 8, QS = N == 128 ? 1 : 2;   // QS: half of Q^T and K^T at a time where registers run short
@@ -59,24 +61,27 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba,
     const DeltaArgs& a = ba.f;
     const int tid = threadIdx.x % 256, wave = tid / 64, lane = tid % 64, q = lane / 16, i = lane % 16;
     const int pb = a.P / 64;
-    int unit = blockIdx.x;
+    const int units = a.B * a.H * pb, sk = blockIdx.x / units + AHEAD;   // the first superchunk hands nothing on
+    int unit = blockIdx.x % units;
     const int share = a.H / a.G * pb;                // heads of a group on one XCD
     if (a.B * a.G % 8 == 0) unit = (unit / 8 / share * 8 + unit % 8) * share + unit / 8 % share;
     const int p0 = unit % pb * 64, bh = unit / pb, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
-    const int len = row_len(a, b), nch = (len + C - 1) / C;   // step e is chunk nch - 1 - e
+    const int len = row_len(a, b), c0 = sk * io.split.S;
+    const int nch = max(0, min(io.split.S, (len + C - 1) / C - c0)), last = c0 + nch - 1;   // step e is chunk last - e
     const size_t tok0 = (size_t)b * a.L;
 
     if (threadIdx.x < 256) {
         const int p = p0 + 16 * wave + i;
-        const size_t sofs = ((size_t)bh * a.P + p) * N + 8 * q;
+        const size_t sofs = ((size_t)bh * a.P + p) * N + 8 * q, kofs = (((size_t)bh * io.split.K + sk) * a.P + p) * N + 8 * q;
+        const float* from = AHEAD ? nullptr : io.split.K > 1 ? io.split.s0 + kofs : ba.g_final ? ba.g_final + sofs : nullptr;
         f32x4 D[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            D[n] = ba.g_final ? v4(*reinterpret_cast<const float4*>(ba.g_final + sofs + 32 * (n / 2) + 4 * (n % 2))) : kZero4;
+            D[n] = from ? v4(*reinterpret_cast<const float4*>(from + 32 * (n / 2) + 4 * (n % 2))) : kZero4;
         lds_barrier();
         for (int e = 0; e < nch; ++e) {
             const unsigned char* const lds = lds_all + (e & 1) * LD::buffer;
-            const size_t u = (size_t)bh * io.nc + nch - 1 - e;
+            const size_t u = (size_t)bh * io.nc + last - e;
             auto scal4 = [&](int what, int m) {
                 return v4(*reinterpret_cast<const float4*>(lds + LD::scal + (what * C + 16 * m + 4 * q) * 4));
             };
@@ -125,11 +130,13 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba,
             const float across = *reinterpret_cast<const float*>(lds + LD::across);
             __builtin_amdgcn_sched_barrier(0);
             if (QS == 1) scals();
-            float* kd = io.D + u * N * a.P + p;
+            if constexpr (!AHEAD) {
+                float* kd = io.D + u * N * a.P + p;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) kd[(size_t)(32 * (n / 2) + 8 * q + 4 * (n % 2) + r) * a.P] = D[n][r];
+                    for (int r = 0; r < 4; ++r) kd[(size_t)(32 * (n / 2) + 8 * q + 4 * (n % 2) + r) * a.P] = D[n][r];
+            }
             f32x4 W[4], Z[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) W[m] = Z[m] = kZero4;
@@ -211,7 +218,8 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba,
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) kz[(size_t)(16 * m + 4 * q + r) * a.P] = Z[m][r];
+                for (int r = 0; r < 4; ++r)
+                    if (!AHEAD) kz[(size_t)(16 * m + 4 * q + r) * a.P] = Z[m][r];
                 Z[m] *= -kb[m];
             }
 #pragma unroll
@@ -226,9 +234,10 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba,
             lds_barrier();
         }
         if (nch & 1) lds_barrier();                  // the other waves go in pairs
-        if (ba.g_init) {
+        float* to = AHEAD ? io.split.loc + kofs : ba.g_init && sk == 0 ? ba.g_init + sofs : nullptr;
+        if (to) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(ba.g_init + sofs + 32 * (n / 2) + 4 * (n % 2)) = f4(D[n]);
+            for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(to + 32 * (n / 2) + 4 * (n % 2)) = f4(D[n]);
         }
         return;
     }
@@ -243,7 +252,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba,
     const uint32_t k_row = (uint32_t)a.k_stride * 2, q_row = (uint32_t)a.q_stride * 2, d_row = (uint32_t)ba.gy_stride * 2;
     auto fetch = [&](int e, auto set) {
         constexpr int Z = decltype(set)::value;
-        const int c = max(nch - 1 - e, 0);
+        const int c = max(last - e, c0);
         const size_t u = (size_t)bh * io.nc + c;
         const int n_on = min(C, len - c * C);
         const unsigned char *kc = kb + (size_t)c * C * k_row, *qc = qb + (size_t)c * C * q_row, *dc = db + (size_t)c * C * d_row;
@@ -269,7 +278,7 @@ __global__ __launch_bounds__(512, 2) void ssd_delta_back_kernel(DeltaBwdArgs ba,
     auto stage = [&](int e, auto set) {
         constexpr int Z = decltype(set)::value;
         unsigned char* const lds = lds_all + (e & 1) * LD::buffer;
-        const int n_on = len - max(nch - 1 - e, 0) * C;
+        const int n_on = len - max(last - e, c0) * C;
         const u32x4_t zero = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
@@ -897,7 +906,8 @@ __global__ __launch_bounds__(256) void ssd_delta_sum_kernel(const float* part, s
 }
 
 struct BwdWs {
-    size_t T, TT, att, scal, across, S, U, D, Z, part, total;
+    size_t T, TT, att, scal, across, S, U, D, Z, part, loc, phi, s0, total;
+    Split split;
 };
 BwdWs bwd_ws(int B, int L, int H, int P, int N, int dtype) {
     const size_t nc = (L + C - 1) / C, units = (size_t)B * H * nc;
@@ -919,6 +929,11 @@ BwdWs bwd_ws(int B, int L, int H, int P, int N, int dtype) {
     w.D = take(units * N * P * 4);
     w.Z = take(units * C * P * 4);
     w.part = take(2 * units * 4);
+    split_bwd(B, L, H, P, N, dtype, w.split);
+    const size_t states = w.split.K > 1 ? (size_t)B * H * w.split.K * N * 4 : 0;
+    w.loc = take(states * P);
+    w.phi = take(states * N);
+    w.s0 = take(states * P);
     w.total = at;
     return w;
 }
@@ -931,9 +946,10 @@ hipError_t launch_bwd_n(const DeltaBwdArgs& ba, void* ws, hipStream_t stream) {
     unsigned char* base = static_cast<unsigned char*>(ws);
     auto fp = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
     PrepOut o{base + w.T, base + w.TT, base + w.att, fp(w.scal), fp(w.across)};
-    hipError_t e = launch_keep(a, o, fp(w.S), fp(w.U), stream);
+    const Split split{w.split.K, w.split.S, fp(w.loc), fp(w.phi), fp(w.s0)};
+    hipError_t e = launch_keep(a, o, KeepOut{fp(w.S), fp(w.U), split}, stream);
     if (e != hipSuccess) return e;
-    BwdIo io{o.TT, o.att, o.scal, o.across, fp(w.S), fp(w.U), fp(w.D), fp(w.Z), fp(w.part), nc};
+    BwdIo io{o.TT, o.att, o.scal, o.across, fp(w.S), fp(w.U), fp(w.D), fp(w.Z), fp(w.part), nc, split};
     constexpr size_t grad = GradLds<T, N>::bytes;
     const dim3 chains(a.B * a.H * (a.P / 64));
     if constexpr (std::is_same<T, float>::value) {
@@ -943,9 +959,18 @@ hipError_t launch_bwd_n(const DeltaBwdArgs& ba, void* ws, hipStream_t stream) {
         hipLaunchKernelGGL((ssd_delta_reverse_kernel<N>), chains, dim3(256), rev, stream, ba, io);
     } else {
         constexpr size_t rev = 2 * BackLds<N>::buffer;
-        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_back_kernel<N>), rev);
+        if (split.K > 1) {
+            e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_back_kernel<N, true>), rev);
+            if (e != hipSuccess) return e;
+            hipLaunchKernelGGL((ssd_delta_back_kernel<N, true>), dim3(chains.x * (split.K - 1)), dim3(512), rev, stream, ba, io);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            e = launch_join_back(a, split, ba.g_final, stream);
+            if (e != hipSuccess) return e;
+        }
+        e = prepare_launch(reinterpret_cast<const void*>(&ssd_delta_back_kernel<N, false>), rev);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((ssd_delta_back_kernel<N>), chains, dim3(512), rev, stream, ba, io);
+        hipLaunchKernelGGL((ssd_delta_back_kernel<N, false>), dim3(chains.x * split.K), dim3(512), rev, stream, ba, io);
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -193,9 +193,21 @@ __device__ __forceinline__ int row_len(const DeltaArgs& a, int b) {
     return a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
 }
 
-// the backward's first launches (delta.hip): every chunk's T, T^T, Att and scalars, then the states entering the
-// chunks [u][N][P] and U [u][C][P]
-hipError_t launch_keep(const DeltaArgs& a, const PrepOut& o, float* keepS, float* keepU, hipStream_t stream);
+// a long sequence's superchunks: K of S chunks (K = 1: none), and [b h][K] states from zero and entering, transitions
+struct Split {
+    int K, S;
+    float *loc, *phi, *s0;
+};
+struct KeepOut {
+    float *S, *U;                  // the states entering the chunks [u][N][P], U [u][C][P]
+    Split split;
+};
+
+// the backward's first launches (delta.hip): every chunk's T, T^T, Att and scalars, then the states and U
+hipError_t launch_keep(const DeltaArgs& a, const PrepOut& o, const KeepOut& k, hipStream_t stream);
+// the gradients of the states leaving the superchunks (to s0), from those that they have of their own (loc)
+hipError_t launch_join_back(const DeltaArgs& a, const Split& s, const float* g_final, hipStream_t stream);
+void split_bwd(int B, int L, int H, int P, int N, int dtype, Split& s);
 
 }  // namespace delta
 }  // namespace ssd

@@ -230,3 +230,20 @@ def test_layer_backward(gpu_lib):
     for name, g in got.items():
         err = (g.double().cpu() - want[name]).norm() / want[name].norm()
         assert err <= 2.0 ** -14 + 2.0 ** -13, (name, float(err))
+
+
+@pytest.mark.parametrize("B,L,H,P,N,docs,lengths", [(1, 1500, 2, 64, 64, 0.0, None), (1, 1472, 1, 128, 128, 0.003, None),
+                                                    (3, 1600, 1, 64, 32, 0.0, [0, 1600, 500])])
+def test_split_sequences(gpu_lib, monkeypatch, B, L, H, P, N, docs, lengths):
+    """Few heads and a long row: cut into superchunks both ways (the workspace is larger than the chunks' own).  A state
+    entering one passes the chain's products twice, its own part's and the transition's: the fp32 outputs' bound doubles."""
+    ssd, dims, dtype = gpu_lib, (H, P, N, 1), torch.bfloat16
+    d, opt = make(B, L, *dims, dtype, state=True, docs=docs, lengths=lengths)
+    units = B * H * -(-L // 64)
+    chunks = units * (3 * 12288 + 9 * 256 + 4 + 8 * P * (N + 64) + 8)
+    assert ssd.ssd_delta_scan_bwd_workspace_size(B, L, H, P, N, 1) > chunks + 12 * 256
+    monkeypatch.setitem(WIDE, dtype, 2.0 ** -11)
+    out = check(ssd, d, opt, dims)
+    gy, gS = cotangents(d, opt, dims)
+    again = grads(ssd, d, opt, dims, gy, gS)
+    assert all(torch.equal(out[n], again[n]) for n in out)
