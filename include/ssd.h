@@ -598,10 +598,16 @@ size_t ssd_mixer_bwd_workspace_size(int B, int L, int H, int P, int N, int G, in
  *     T = (I + strictly_lower(beta_t M_tj k_t.k_j))^-1
  *     U = T (beta (V - e^G K S)),  Y = scale (e^G Q S + (M o Q K^T) U),
  *     S' = e^{G_C} S + (e^{G_C - G} K)^T U
- * A first launch computes T and M o Q K^T of all chunks; a second passes the
- * state from chunk to chunk, held on chip.  Chunks are counted from t = 0, so
- * a prefill split at a multiple of 64 tokens with the state carried is
- * bitwise identical to one call.  L = 0 copies the state through.
+ * A first launch computes T and (M o Q K^T) of all chunks; a second passes the
+ * state from chunk to chunk, held on chip.  bf16 rows of many chunks and few
+ * heads (a rule on B, H, P, N and the chunks of L) are cut into superchunks
+ * that run side by side, with two launches before for the states entering
+ * them.  Chunks are counted from t = 0, so a prefill split at a multiple of 64
+ * tokens with the state carried is bitwise identical to one call wherever no
+ * call of them is cut (always in fp32); otherwise it agrees to the kernels'
+ * rounding.  Results are deterministic.  L = 0 copies the state through.
+ * A NaN or Inf among a row's real tokens reaches its whole chunk and what
+ * follows in that row and head.
  */
 int ssd_delta_scan_fwd(int B, int L, int H, int P, int N, int G, int chunk, int dtype,
                        const void *q, int64_t q_row_stride,
@@ -617,7 +623,7 @@ int ssd_delta_scan_fwd(int B, int L, int H, int P, int N, int G, int chunk, int 
                        void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace of ssd_delta_scan_fwd: T, M o Q K^T and the decays of
- * every chunk and head. */
+ * every chunk and head, and the superchunks' states and transitions. */
 size_t ssd_delta_scan_workspace_size(int B, int L, int H, int P, int N, int G, int dtype);
 
 /*
@@ -687,7 +693,8 @@ int ssd_delta_scan_bwd(int B, int L, int H, int P, int N, int G, int chunk, int 
                        void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace of ssd_delta_scan_bwd: every chunk's T, its transpose and
- * M o Q K^T, the state entering and the adjoint leaving it, U and Z. */
+ * M o Q K^T, the state entering and the adjoint leaving it, U and Z, and the
+ * superchunks' states and transitions. */
 size_t ssd_delta_scan_bwd_workspace_size(int B, int L, int H, int P, int N, int G, int dtype);
 
 /*
