@@ -1,6 +1,7 @@
 // delta.hip -- the gated delta rule over a sequence: what of a chunk does not
 // depend on the state (ssd_delta_prep_kernel, all chunks at once), then the
-// chunks in turn (ssd_delta_scan_kernel).
+// chunks in turn (ssd_delta_chain_kernel in bf16, ssd_delta_scan_kernel in
+// fp32).
 #include <hip/hip_runtime.h>
 #include <algorithm>
 #include <type_traits>
@@ -37,7 +38,15 @@ using namespace delta;
 // What the scan needs of T depends on it (Prep): the bf16 forward multiplies X
 // by T only to get U scaled for the state, diag(e^{G_C - G}) T diag(beta), and
 // Att T diag(beta) for y, so those two products are formed here, where all
-// chunks run at once, and not in the chain of the scan.
+// chunks run at once, and not in the chain of the scan.  (Forming only Att here
+// took 122 us in place of 156 at B=5 L=8192 H=32 N=64, but the scan 242 in
+// place of 225.)
+//
+// Measured, bf16: 154 us at B=5 L=8192 H=32 P=N=64 (20480 units, 17 KB written
+// each, 357 MB), 300 us at B=4 L=4096 H=128 N=128 (32768 units; 558 MB written,
+// 331 MB read: 175 us at a copy's rate, the matrix pipes busy for 85 us and the
+// vector units for 89, so what is left is the substitution's latency, of which
+// two waves a SIMD hide a part).
 constexpr int kLtRow = 20;                           // floats of an L^T tile's row: 16-byte reads of 16 rows hit all banks
 constexpr int kPrepWaves = 2;
 enum Prep {
@@ -411,7 +420,11 @@ struct ScanIo {
 // the chain, and four more everything that is not part of it, on the same
 // SIMDs: they bring the next chunk's k, v and T from memory to LDS, and compute
 // and store the last chunk's y from the S and X fragments that the chain left
-// in LDS.  A chunk costs one barrier.  The chain's LDS reads are issued ahead
+// in LDS.  A chunk costs one barrier.  Measured: 1.7 us a chunk at N = 64 (218
+// us at B=5 L=8192 H=32, 160 workgroups; 364 us with all of it in four waves),
+// 2.9 us at N = 128 (375 us at B=4 L=4096 H=128, two rounds of 64 chunks).  At
+// N = 128 a CU's reads in flight bound it (11 bytes a cycle and CU), at N = 64
+// the chain's latency.  The chain's LDS reads are issued ahead
 // of the products they feed (sched_barrier: left to itself the compiler reads
 // each fragment just before its use).
 // Splits: S, X, U and T are hi + lo pairs, k is bf16 as it is: K S and K^T U
@@ -853,8 +866,9 @@ __global__ __launch_bounds__(256) void ssd_delta_join_kernel(DeltaArgs a, ScanIo
 
 // ---- fp32: the forward (kY), and the backward's recomputation of S and U (kKeep)
 // The same chain on the fp32 MFMA (a 16 x 16 x 4 product takes 32 cycles), which is what bounds it: k, q, Att and T come
-// as they are, four waves stage their own chunks, and y is computed in the chain.  B=2 L=300 H=4 P=64 N=32 takes 15 us,
-// five chunks of 3 us.
+// as they are, four waves stage their own chunks, and y is computed in the chain.  Measured: B=3 L=77 H=8 P=N=64 in 14.5
+// us, two chunks of 272 products a wave (3.6 us each at 2.4 GHz) and the first chunk's loads; the backward's S and U of
+// B=2 L=150 H=4 P=64 N=32 in 11.4 us.
 enum { kY = 0, kKeep = 1 };
 
 template <int N, int MODE>

@@ -11,7 +11,7 @@
 //     dG_t = row sums - column sums of dAtt o Att + dL o L, + scale e^{G_t} Q_t.W1_t - beta_t e^{G_t} K_t.W2_t
 //            - e^{G_C - G_t} K_t.W3_t, and at the chunk's end + sum of the last + e^{G_C} <S0, dS>
 //     d(dt A)_t = sum of dG behind t in the chunk
-// Row and column sums are taken of the same fp32 entries, so pairs on one side
+// Row and column sums are taken of the same entries, so pairs on one side
 // of t cancel to fp32 rounding whatever the products' own error.
 //
 // Launches: delta.hip's prep (T, T^T, Att, scalars) and forward chain (S0 and U
@@ -44,6 +44,12 @@ struct BwdIo {
 // in LDS ahead of it.  Bound by the chain's latency, like the forward.
 
 // ---- bf16: four waves are the chain, four more bring the next chunks
+// LDS is read in three batches ahead of the products they feed.  2.4 us a chunk
+// at N = P = 64, against 4.1 with staging in the chain's own waves: B=2 L=8192
+// H=32 took 531 us so, 307 us this way, and in four superchunks side by side
+// (AHEAD and the join included) 193 us.
+// Splits: dS, dU and Z are hi + lo pairs like Att and T, dY and k, q bf16 as
+// they are.
 template <int N>
 struct BackLds {
     static constexpr int kRow = N * 2, dRow = 64 * 2 + 16;
@@ -500,6 +506,18 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
 // U and the state are read once from memory by 16-row tiles, one wave each,
 // and shared as fragments (P in halves of 64 columns, S0 and then dS in one
 // buffer).
+//
+// bf16: states, U and Z enter as pairs, and the last products (of dAtt and dL
+// with K and Q, whose results are rounded to bf16) with one rounding each.
+// Measured, B=2 L=8192 H=32 G=8 P=N=64: 250 to 285 us (0.74 GB of states, U, Z
+// and rows: 145 us at a copy's rate).  Loads are not ahead of their head (the
+// registers are full), so it takes two workgroups a CU to hide them: at one,
+// with 280 registers a wave, it took 415 us.
+// The sums behind d(dt A): fp32 inputs take them in fp64, where the row and column sums of an entry cancel exactly
+// (dA and ddt_bias at B=2 L=150 H=4: 2.3e-6 off in fp32, 8e-7 this way); the products of bf16 inputs are off by more than fp32 sums.
+template <typename T>
+using Sum = std::conditional_t<std::is_same<T, float>::value, double, float>;
+
 template <typename T, int N>
 struct GradLds {
     static constexpr int es = sizeof(T);
@@ -508,12 +526,29 @@ struct GradLds {
     static constexpr int s_bytes = std::max(N * 256, 2 * C * gRow);   // a half of S0 or dS; then the two [j][t] matrices
     static constexpr int u = s + s_bytes, scal = u + 16 * 1024;
     static constexpr int col = scal + kScalBwd * C * 4;               // [4][C] column sums
-    static constexpr int row = col + 4 * C * 4;                       // [3][C]: dG's rows, its W3 part, dbeta
-    static constexpr int dot = row + 3 * C * 4;                       // [4] <S0, dS>
+    static constexpr int row = col + 4 * C * sizeof(Sum<T>);          // [3][C]: dG's rows, its W3 part, dbeta
+    static constexpr int dot = row + 3 * C * sizeof(Sum<T>);          // [4] <S0, dS>
     static constexpr int bytes = dot + 64;
 };
 
 __device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
+__device__ __forceinline__ float shfl_down(float v, int d) { return __shfl_down(v, d); }
+__device__ __forceinline__ double shfl_down(double v, int d) {
+    const long long b = __double_as_longlong(v);
+    return __longlong_as_double(((long long)__shfl_down((int)(b >> 32), d) << 32) | (unsigned)__shfl_down((int)b, d));
+}
+// over 16 lanes (the first has it), and over the four rows of 16
+__device__ __forceinline__ float sum16(float v) { return lanes_sum<16>(v); }
+__device__ __forceinline__ double sum16(double v) {
+#pragma unroll
+    for (int d = 8; d > 0; d /= 2) v += shfl_down(v, d);
+    return v;
+}
+__device__ __forceinline__ float sum_rows(float v) { return rows_sum(v); }
+__device__ __forceinline__ double sum_rows(double v) {
+    v += shfl_down(v, 32);
+    return v + shfl_down(v, 16);     // the first row has it
+}
 
 // four consecutive entries of a row, and their store
 __device__ __forceinline__ f32x4 ld4t(const unsigned char* p, uint16_t) {
@@ -579,6 +614,7 @@ template <typename T, int N>
 __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_delta_grad_kernel(DeltaBwdArgs ba, BwdIo io) {
     using LD = GradLds<T, N>;
     constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16;
+    constexpr bool kLate = es == 4 && N == 128;      // dS only when S0 has been used: registers
     extern __shared__ __align__(16) unsigned char lds[];
     const DeltaArgs& a = ba.f;
     const int tid = threadIdx.x, lane = tid % 64, q = lane / 16, i = lane % 16;
@@ -623,8 +659,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
     f32x4 dQ[NT], dK[NT];                            // [n][t]
 #pragma unroll
     for (int n = 0; n < NT; ++n) dQ[n] = dK[n] = kZero4;
-    float* colp = reinterpret_cast<float*>(lds + LD::col);
-    float* rowp = reinterpret_cast<float*>(lds + LD::row);
+    using SumT = Sum<T>;
+    SumT* colp = reinterpret_cast<SumT*>(lds + LD::col);
+    SumT* rowp = reinterpret_cast<SumT*>(lds + LD::row);
     float* dotp = reinterpret_cast<float*>(lds + LD::dot);
 
     for (int hh = 0; hh < hg; ++hh) {
@@ -675,9 +712,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
                         const uint32_t at = (uint32_t)(16 * n + i) * a.P + p0 + 32 * s + 8 * q;
                         const float *sp = io.S + u * N * a.P + at, *dp = io.D + u * N * a.P + at;
                         const float4 s0 = *reinterpret_cast<const float4*>(sp), s1 = *reinterpret_cast<const float4*>(sp + 4);
-                        const float4 d0 = *reinterpret_cast<const float4*>(dp), d1 = *reinterpret_cast<const float4*>(dp + 4);
-                        sd += dot4(v4(s0), v4(d0)) + dot4(v4(s1), v4(d1));
-                        ds[j][s].set(d0, d1);
+                        if constexpr (!kLate) {
+                            const float4 d0 = *reinterpret_cast<const float4*>(dp), d1 = *reinterpret_cast<const float4*>(dp + 4);
+                            sd += dot4(v4(s0), v4(d0)) + dot4(v4(s1), v4(d1));
+                            ds[j][s].set(d0, d1);
+                        }
                         Wide<T> f;
                         f.set(s0, s1);
                         f.put(lds + LD::s + (n * 2 + s) * 2048 + lane * 16);
@@ -711,7 +750,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
                 const int n = w + 4 * j;
                 if (n < NT) {
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) ds[j][s].put(lds + LD::s + (n * 2 + s) * 2048 + lane * 16);
+                    for (int s = 0; s < 2; ++s) {
+                        unsigned char* to = lds + LD::s + (n * 2 + s) * 2048 + lane * 16;
+                        if constexpr (kLate) {
+                            const float* dp = io.D + u * N * a.P + (uint32_t)(16 * n + i) * a.P + p0 + 32 * s + 8 * q;
+                            const float4 d0 = *reinterpret_cast<const float4*>(dp), d1 = *reinterpret_cast<const float4*>(dp + 4);
+                            Wide<T> f;
+                            f.get(to);
+                            sd += dot4(v4(f.p.a), v4(d0)) + dot4(v4(f.p.b), v4(d1));
+                            ds[j][s].set(d0, d1);
+                        }
+                        ds[j][s].put(to);
+                    }
                 }
             }
             __syncthreads();
@@ -753,7 +803,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
             ko[s].load(reinterpret_cast<const T*>(lds + LD::k + t * LD::kRow) + 32 * s + 8 * q);
             qo[s].load(reinterpret_cast<const T*>(lds + LD::q + t * LD::kRow) + 32 * s + 8 * q);
         }
-        float rsum = 0.0f, bsum = 0.0f;
+        SumT rsum = 0.0f;
+        float bsum = 0.0f;
         unsigned char *g1 = lds + LD::s, *g2 = g1 + C * LD::gRow;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -787,8 +838,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int j = 16 * n + 4 * q + r;
-                cs[r] = lanes_sum<16>(cs[r]);
-                if (i == 0) colp[w * C + j] = cs[r];
+                const SumT all = sum16((SumT)cs[r]);
+                if (i == 0) colp[w * C + j] = all;
                 if constexpr (es == 2) {
                     *reinterpret_cast<uint16_t*>(g1 + j * LD::gRow + t * 2) = (uint16_t)f32_to_bf16_bits(x1[r]);
                     *reinterpret_cast<uint16_t*>(g2 + j * LD::gRow + t * 2) = (uint16_t)f32_to_bf16_bits(x2[r]);
@@ -799,14 +850,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
             }
         }
         {
-            float all[6] = {r1, r2, r3, rsum, bsum, zv};
+            float all[5] = {r1, r2, r3, bsum, zv};
 #pragma unroll
-            for (int x = 0; x < 6; ++x) all[x] = rows_sum(all[x]);
+            for (int x = 0; x < 5; ++x) all[x] = rows_sum(all[x]);
+            rsum = sum_rows(rsum);
             sd = wave_sum(sd);
             if (q == 0) {
-                rowp[t] = all[3] + all[0] - beta * all[1] - all[2];
+                rowp[t] = rsum + all[0] - (SumT)beta * all[1] - all[2];
                 rowp[C + t] = all[2];
-                rowp[2 * C + t] = all[5] - all[1] + all[4];
+                rowp[2 * C + t] = all[4] - all[1] + all[3];
             }
             if (lane == 0) dotp[w] = sd;
         }
@@ -831,18 +883,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
         }
         if (w == 0) {
             // one token a lane: d(dt A) is the sum of dG behind it
-            float dG = rowp[lane] - ((colp[lane] + colp[C + lane]) + (colp[2 * C + lane] + colp[3 * C + lane]));
-            const float r3s = wave_sum(rowp[C + lane]), dot = (dotp[0] + dotp[1]) + (dotp[2] + dotp[3]);
+            SumT dG = rowp[lane] - ((colp[lane] + colp[C + lane]) + (colp[2 * C + lane] + colp[3 * C + lane]));
+            const float r3s = wave_sum((float)rowp[C + lane]), dot = (dotp[0] + dotp[1]) + (dotp[2] + dotp[3]);
             if (lane == 63) dG += fmaf(io.across[u], dot, r3s);
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
-                const float dn = __shfl_down(dG, d);
+                const SumT dn = shfl_down(dG, d);
                 if (lane + d < 64) dG += dn;
             }
             const size_t at = tok0 + min(lane, n_on - 1);
             float dt = a.dt[at * a.dt_stride + h], chain = 1.0f;
             const float be = *reinterpret_cast<const float*>(lds + LD::scal + (kBeta * C + lane) * 4);
-            float db = rowp[2 * C + lane];
+            float db = (float)rowp[2 * C + lane];
             if (a.dt_softplus) {
                 dt += a.dt_bias ? a.dt_bias[h] : 0.0f;
                 chain = 1.0f / (1.0f + expf(-dt));
@@ -853,12 +905,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
             // that the row and column sums leave behind (2^-24 of them), which a large dt would carry into dA.
             if (dt * a.A[h] < -30.0f) dG = 0.0f;
             const bool live = lane < n_on;
-            const float dd = live ? dG * a.A[h] * chain : 0.0f;
+            const float dd = live ? (float)dG * a.A[h] * chain : 0.0f;
             if (lane < n_rows) {
                 ba.ddt[(tok0 + lane) * ba.ddt_stride + h] = dd;
                 ba.dbeta[(tok0 + lane) * ba.dbeta_stride + h] = live ? db : 0.0f;
             }
-            const float pa = wave_sum(live && dG != 0.0f ? dG * dt : 0.0f), pd = wave_sum(dd);   // dt may be infinite
+            const float pa = wave_sum(live && dG != 0.0f ? (float)dG * dt : 0.0f), pd = wave_sum(dd);   // dt may be infinite
             if (lane == 0) {
                 io.part[bc * a.H + h] = pa;
                 io.part[parts + bc * a.H + h] = pd;

