@@ -27,6 +27,7 @@ tensor is not on the GPU, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -635,10 +636,10 @@ class _Call:
         # a single row: any stride that holds it and keeps the alignment
         return p, (-(-shape[-1] // 8) * 8 if rs is None else rs)
 
-    def run(self, fn, args, stream):
-        """fn(*args, stream) on the tensors' device."""
+    def run(self, fn, args):
+        """fn(*args, stream) on the tensors' device and its current stream."""
         index = self.dev.index
-        stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+        stream = torch._C._cuda_getCurrentRawStream(index)
         if index == torch._C._cuda_getDevice():
             st = fn(*args, stream)
         else:
@@ -646,6 +647,23 @@ class _Call:
                 st = fn(*args, stream)
         if st:
             _check(st)
+
+
+def _on_stream(fn):
+    """A call with `stream`, a torch stream or a raw handle, makes it the current one, so that what the call allocates
+    (outputs, a workspace that is free again on return) belongs to the stream that uses it."""
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            at = next((t.device for t in (*args, *kw.values()) if isinstance(t, torch.Tensor) and t.is_cuda), None)
+            stream = torch.cuda.ExternalStream(_stream(stream), device=at)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    return call
 
 
 def _delta_head(c, lead, T, q, k, v, dt, A, beta, H, P, N, G, scale, qk_norm, dt_softplus, dt_bias, beta_sigmoid):
@@ -664,9 +682,10 @@ def ssd_delta_scan_workspace_size(B, L, H, P, N, G, dtype=SSD_BF16) -> int:
     return int(load().ssd_delta_scan_workspace_size(B, L, H, P, N, G, dtype))
 
 
+@_on_stream
 def ssd_delta_scan_fwd(q, k, v, dt, A, beta, *, H, P, N, G, scale=None, qk_norm=False, dt_softplus=False, dt_bias=None,
                        beta_sigmoid=False, doc_ids=None, lengths=None, init_state=None, final_state=None, y=None,
-                       chunk=64, workspace=None, stream=None):
+                       chunk=64, workspace=None):
     """The gated delta rule.  q, k [B, L, G*N], v [B, L, H*P] (one dtype), dt, beta [B, L, H] fp32, A [H] fp32.
     scale: N^-0.5 if None.  Returns y [B, L, H*P] in q's dtype (and writes final_state [B, H, P, N] if given).  A
     workspace is allocated here when none is passed."""
@@ -684,12 +703,13 @@ def ssd_delta_scan_fwd(q, k, v, dt, A, beta, *, H, P, N, G, scale=None, qk_norm=
           (B, L, H, P, N, G, chunk, dtype, *head, c.vec(doc_ids, "doc_ids", torch.int32, (B, L)),
            c.vec(lengths, "lengths", torch.int32, (B,)), c.vec(init_state, "init_state", torch.float32, state),
            c.vec(final_state, "final_state", torch.float32, state), yp, ys, c.ptr(ws, "workspace"),
-           ws.numel() * ws.element_size()), stream)
+           ws.numel() * ws.element_size()))
     return y
 
 
+@_on_stream
 def ssd_delta_step(q, k, v, dt, A, beta, state, *, H, P, N, G, scale=None, qk_norm=False, dt_softplus=False,
-                   dt_bias=None, beta_sigmoid=False, y=None, stream=None):
+                   dt_bias=None, beta_sigmoid=False, y=None):
     """One token of the gated delta rule.  q, k [B, G*N], v [B, H*P] (one dtype), dt, beta [B, H] fp32, A [H] fp32;
     state [B, H, P, N] fp32 is updated in place.  scale: N^-0.5 if None.  Returns y [B, H*P] in q's dtype."""
     lib = load()
@@ -700,8 +720,7 @@ def ssd_delta_step(q, k, v, dt, A, beta, state, *, H, P, N, G, scale=None, qk_no
     if y is None:
         y = torch.empty((B, H * P), dtype=T, device=c.dev)
     yp, ys = c.rows(y, "y", T, (B, H * P))
-    c.run(lib.ssd_delta_step, (B, H, P, N, G, dtype, *head, c.vec(state, "state", torch.float32, (B, H, P, N)), yp, ys),
-          stream)
+    c.run(lib.ssd_delta_step, (B, H, P, N, G, dtype, *head, c.vec(state, "state", torch.float32, (B, H, P, N)), yp, ys))
     return y
 
 
@@ -727,9 +746,10 @@ def ssd_delta_scan_bwd_workspace_size(B, L, H, P, N, G, dtype=SSD_BF16) -> int:
     return int(load().ssd_delta_scan_bwd_workspace_size(B, L, H, P, N, G, dtype))
 
 
+@_on_stream
 def ssd_delta_scan_bwd(q, k, v, dt, A, beta, grad_y, *, H, P, N, G, scale=None, qk_norm=False, dt_softplus=False,
                        dt_bias=None, beta_sigmoid=False, doc_ids=None, lengths=None, init_state=None,
-                       grad_final_state=None, chunk=64, workspace=None, stream=None):
+                       grad_final_state=None, chunk=64, workspace=None):
     """Backward of ssd_delta_scan_fwd; grad_y [B, L, H*P] in q's dtype, grad_final_state [B, H, P, N] fp32 or None.
     Returns a dict: q, k, v in q's dtype, dt, beta [B, L, H] and A [H] fp32, and where those inputs are given (dt_bias:
     where dt_softplus is) dt_bias [H] and init_state [B, H, P, N] fp32.  A workspace is allocated here when none is
@@ -755,11 +775,12 @@ def ssd_delta_scan_bwd(q, k, v, dt, A, beta, grad_y, *, H, P, N, G, scale=None, 
            c.vec(lengths, "lengths", torch.int32, (B,)), c.vec(init_state, "init_state", torch.float32, state), gp, gs,
            c.vec(grad_final_state, "grad_final_state", torch.float32, state), out("q"), G * N, out("k"), G * N, out("v"),
            H * P, out("dt"), H, out("beta"), H, out("A"), out("dt_bias"), out("init_state"), c.ptr(ws, "workspace"),
-           ws.numel() * ws.element_size()), stream)
+           ws.numel() * ws.element_size()))
     return g
 
 
-def ssd_norm_fwd(x, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, out_dtype=None, y=None, stream=None):
+@_on_stream
+def ssd_norm_fwd(x, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, out_dtype=None, y=None):
     """Norm of x's last dimension, times weight plus bias, times silu(z).  x [..., W] fp32 or bf16, its rows a uniform
     distance apart, or [..., heads, W] with the heads of a row side by side; weight, bias fp32 [W]; z in the output's
     dtype, which is y's, else out_dtype, else z's, else x's.  Returns y."""
@@ -774,7 +795,7 @@ def ssd_norm_fwd(x, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, out_
     R, groups, at = _norm_groups(c, shape, {"x": (x, None), "z": (z, T), "y": (y, T)})
     c.run(lib.ssd_norm_fwd, (R, groups, W, _dtype_code(x, "x"), _dtype_code(y, "y"), int(bool(rms)), float(eps), *at["x"],
                              c.vec(weight, "weight", torch.float32, (W,)), c.vec(bias, "bias", torch.float32, (W,)),
-                             *at["z"], *at["y"]), stream)
+                             *at["z"], *at["y"]))
     return y
 
 
@@ -782,7 +803,8 @@ def ssd_norm_bwd_workspace_size(R, groups, W) -> int:
     return int(load().ssd_norm_bwd_workspace_size(R, groups, W))
 
 
-def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, workspace=None, stream=None):
+@_on_stream
+def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, workspace=None):
     """Backward of ssd_norm_fwd; grad_y (and z) in the output's dtype.  Returns a dict: x in x's dtype, weight and
     bias fp32 [W] and z in z's dtype, where those inputs are given.  A workspace is allocated here when none is
     passed."""
@@ -807,5 +829,5 @@ def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e
     c.run(lib.ssd_norm_bwd, (R, groups, W, _dtype_code(x, "x"), _dtype_code(grad_y, "grad_y"), int(bool(rms)), float(eps),
                              *at["x"], c.vec(weight, "weight", torch.float32, (W,)),
                              c.vec(bias, "bias", torch.float32, (W,)), *at["z"], *at["grad_y"], *at["dx"], out("weight"),
-                             out("bias"), *at["dz"], c.ptr(ws, "workspace"), nb), stream)
+                             out("bias"), *at["dz"], c.ptr(ws, "workspace"), nb))
     return g
