@@ -10,8 +10,8 @@
 // 256-byte lines; each lane holds its four entries of k and q for every row.
 // A thread takes F rows' parts, all loaded before the first is used.
 //
-// Measured: B=256 H=64 N=128, 1.07 GB of state, 199 us (5.4 TB/s; a large copy
-// reaches 5.1).  B=1 H=32 N=64: 3.5 us on the GPU, the call's host time more.
+// Measured: B=256 H=64 N=128, 1.07 GB read and written, 178 us (6.0 TB/s; a
+// large copy reaches 5.1).  B=1 H=32 N=64: 3.5 us on the GPU, the call's host time more.
 #include <hip/hip_runtime.h>
 
 #include "ssd_device.hpp"
@@ -35,7 +35,7 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
     return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, a.x * b.x)));
 }
 
-template <typename T, int N, int F>
+template <typename T, int N, int F, bool STREAM>
 __global__ __launch_bounds__(kThreads) void ssd_delta_step_kernel(DeltaArgs a) {
     constexpr int NQ = N / 4;                       // lanes of a state row
     constexpr int kRows = kThreads / NQ;            // state rows of the workgroup at a time
@@ -52,7 +52,9 @@ __global__ __launch_bounds__(kThreads) void ssd_delta_step_kernel(DeltaArgs a) {
     const T* vrow = static_cast<const T*>(a.v) + (size_t)b * a.v_stride + (size_t)h * a.P + p0;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-        s[f] = *reinterpret_cast<const float4*>(S + (size_t)f * kRows * N);
+        const f32x4* at = reinterpret_cast<const f32x4*>(S + (size_t)f * kRows * N);
+        const f32x4 z = STREAM ? __builtin_nontemporal_load(at) : *at;
+        s[f] = make_float4(z[0], z[1], z[2], z[3]);
         vv[f] = ld1(vrow + f * kRows);
     }
     float4 q = ld4(static_cast<const T*>(a.q) + (size_t)b * a.q_stride + (size_t)g * N + n0);
@@ -74,12 +76,10 @@ __global__ __launch_bounds__(kThreads) void ssd_delta_step_kernel(DeltaArgs a) {
     for (int f = 0; f < F; ++f) {
         const float sk = lanes_sum<NQ>(dot4(s[f], k)), sq = lanes_sum<NQ>(dot4(s[f], q));
         const float u = beta * (vv[f] - dec * sk);
-        float4 o;
-        o.x = fmaf(dec, s[f].x, u * k.x);
-        o.y = fmaf(dec, s[f].y, u * k.y);
-        o.z = fmaf(dec, s[f].z, u * k.z);
-        o.w = fmaf(dec, s[f].w, u * k.w);
-        *reinterpret_cast<float4*>(S + (size_t)f * kRows * N) = o;
+        const f32x4 o = {fmaf(dec, s[f].x, u * k.x), fmaf(dec, s[f].y, u * k.y), fmaf(dec, s[f].z, u * k.z), fmaf(dec, s[f].w, u * k.w)};
+        f32x4* to = reinterpret_cast<f32x4*>(S + (size_t)f * kRows * N);
+        if (STREAM) __builtin_nontemporal_store(o, to);
+        else *to = o;
         if (n0 == 0) st1(yrow + f * kRows, qs * fmaf(dec, sq, u * kq));
     }
 }
@@ -87,17 +87,21 @@ __global__ __launch_bounds__(kThreads) void ssd_delta_step_kernel(DeltaArgs a) {
 template <typename T, int N>
 hipError_t launch_n(const DeltaArgs& a, hipStream_t stream) {
     // the most rows a thread that leave 1024 workgroups, four on every CU.  Measured: the 1.07 GB
-    // of B=256 H=64 N=128 take 195 to 199 us with F = 8 and 208 with F = 1; B=1 H=32 N=64 3.9 us with F = 1 and 4.1 with 4
+    // of B=256 H=64 N=128 took 195 to 199 us with F = 8 and 208 with F = 1; B=1 H=32 N=64 3.9 us with F = 1 and 4.1 with 4
     const int64_t work = (int64_t)a.B * a.H * a.P * N / (kThreads * 4);   // workgroups at F = 1
     const int most = a.P * N / (kThreads * 4);                            // F of a whole head: >= 2
     int f = 8;
     while (f > 1 && (f > most || work / f < 1024)) f /= 2;
     const dim3 grid((unsigned)(work / f));
     switch (f) {
-        case 1: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 1>), grid, dim3(kThreads), 0, stream, a); break;
-        case 2: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 2>), grid, dim3(kThreads), 0, stream, a); break;
-        case 4: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 4>), grid, dim3(kThreads), 0, stream, a); break;
-        default: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 8>), grid, dim3(kThreads), 0, stream, a);
+        case 1: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 1, false>), grid, dim3(kThreads), 0, stream, a); break;
+        case 2: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 2, false>), grid, dim3(kThreads), 0, stream, a); break;
+        case 4: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 4, false>), grid, dim3(kThreads), 0, stream, a); break;
+        default:
+            // A state that the last-level cache cannot hold until the next token goes past it: 512 MB take 178 us this way
+            // and 199 without, but 256 MB 87 and 83, 64 MB 22.3 and 21.0.
+            if (work * kThreads * 16 > (256LL << 20)) hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 8, true>), grid, dim3(kThreads), 0, stream, a);
+            else hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 8, false>), grid, dim3(kThreads), 0, stream, a);
     }
     return hipGetLastError();
 }
