@@ -18,14 +18,14 @@
 // workgroup's rows up in LDS, and a second launch adds the workgroups' sums
 // in their order, so results do not change from run to run.
 //
-// Measured: 40960 rows of 2048, fp32 to bf16, 84 us (6.0 TB/s; a large copy
-// reaches 5.1); 1.3 million gated rows of 64 in bf16, 84 us (6.0 TB/s); the
-// gated backward of 40960 rows of 2048 in bf16, 169 us and 5 us of sums
+// Measured: 40960 rows of 2048, fp32 to bf16, 91 us (5.5 TB/s; a large copy
+// reaches 5.1); 1.3 million gated rows of 64 in bf16, 98 us (5.1 TB/s); the
+// gated backward of 40960 rows of 2048 in bf16, 172 us and 5 us of sums
 // (4.9 TB/s), 200 us before it loaded the next row's operands a row ahead.
 // The threads of a row: at 2048 columns a wave of four vectors a thread takes
 // 91 us forward and 256 threads of one 99, while backward, with more live a
 // column, they take 201 and 172; rows of 64 take 98 us with eight threads each
-// and 428 with a wave each (forward: through the cache, see streams()).
+// and 428 with a wave each.
 #include <hip/hip_runtime.h>
 #include <algorithm>
 
@@ -36,11 +36,6 @@ namespace ssd {
 namespace {
 
 // ------------------------------------------------------------ vectors of a row
-// STREAM: inputs that the last-level cache cannot hold go past it.
-template <bool STREAM, typename V, typename E>
-__device__ __forceinline__ V ldg(const E* p) {
-    return STREAM ? __builtin_nontemporal_load(reinterpret_cast<const V*>(p)) : *reinterpret_cast<const V*>(p);
-}
 template <int VEC>
 __device__ __forceinline__ void ldv(const float* p, float (&v)[VEC]) {
     if constexpr (VEC == 8) {
@@ -84,7 +79,6 @@ __device__ __forceinline__ void stv(uint16_t* p, const float (&v)[VEC]) {
 template <typename T, int VEC>
 struct Raw {
     T v;
-    template <bool STREAM>
     __device__ __forceinline__ void load(const T* p) { v = *p; }
     __device__ __forceinline__ void clear() { v = 0; }
     __device__ __forceinline__ void get(float (&o)[VEC]) const { ldv<VEC>(&v, o); }
@@ -92,8 +86,7 @@ struct Raw {
 template <>
 struct Raw<uint16_t, 8> {
     u32x4_t v;
-    template <bool STREAM>
-    __device__ __forceinline__ void load(const uint16_t* p) { v = ldg<STREAM, u32x4_t>(p); }
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
     __device__ __forceinline__ void clear() { v = u32x4_t{0, 0, 0, 0}; }
     __device__ __forceinline__ void get(float (&o)[8]) const {
 #pragma unroll
@@ -106,10 +99,9 @@ struct Raw<uint16_t, 8> {
 template <>
 struct Raw<float, 8> {
     f32x4 a, b;
-    template <bool STREAM>
     __device__ __forceinline__ void load(const float* p) {
-        a = ldg<STREAM, f32x4>(p);
-        b = ldg<STREAM, f32x4>(p + 4);
+        a = *reinterpret_cast<const f32x4*>(p);
+        b = *reinterpret_cast<const f32x4*>(p + 4);
     }
     __device__ __forceinline__ void clear() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
     __device__ __forceinline__ void get(float (&o)[8]) const {
@@ -217,7 +209,7 @@ __device__ __forceinline__ void locate(const NormArgs& a, int64_t r, int64_t& ro
     }
 }
 
-template <typename X, typename T, int TPR, int NV, int VEC, bool STREAM>
+template <typename X, typename T, int TPR, int NV, int VEC>
 __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_kernel(NormArgs a) {
     using SH = Shape<TPR, NV, VEC>;
     __shared__ float red[2][2][16];
@@ -243,14 +235,8 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_k
 #pragma unroll
             for (int e = 0; e < VEC; ++e) x[j][e] = z[j][e] = 0.0f;
             if (live && on[j]) {
-                Raw<X, VEC> rx;
-                rx.template load<STREAM>(xp + r * a.x_stride + col + c);
-                rx.get(x[j]);
-                if (zp) {
-                    Raw<T, VEC> rz;
-                    rz.template load<STREAM>(zp + r * a.z_stride + col + c);
-                    rz.get(z[j]);
-                }
+                ldv<VEC>(xp + r * a.x_stride + col + c, x[j]);
+                if (zp) ldv<VEC>(zp + r * a.z_stride + col + c, z[j]);
             }
         }
         to_hat<TPR, NV, VEC>(x, on, a.W, a.rms, a.eps, red, turn);
@@ -312,9 +298,9 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             nz[j].clear();
             ng[j].clear();
             if (live && on[j]) {
-                nx[j].template load<false>(xp + r * a.x_stride + col + c);
-                ng[j].template load<false>(gp + r * a.gy_stride + col + c);
-                if (zp) nz[j].template load<false>(zp + r * a.z_stride + col + c);
+                nx[j].load(xp + r * a.x_stride + col + c);
+                ng[j].load(gp + r * a.gy_stride + col + c);
+                if (zp) nz[j].load(zp + r * a.z_stride + col + c);
             }
         }
     };
@@ -455,19 +441,11 @@ __global__ __launch_bounds__(1024) void ssd_norm_sum_kernel(const float* part, i
     }
 }
 
-// Whether the forward's inputs are more than the last-level cache: 336 MB of x and z take 84 us past it and 98 through
-// it, but 200 MB that the cache still holds from a call before 52 and 50 us, 64 MB 21 and 18.  (Backward: no difference.)
-bool streams(const NormArgs& a) {
-    const int bytes = (a.x_dtype == 0 ? 4 : 2) + (a.z ? (a.dtype == 0 ? 4 : 2) : 0);
-    return a.R * a.W * bytes > (256LL << 20);
-}
-
 template <typename X, typename T, int TPR, int NV, int VEC>
 hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
     using SH = Shape<TPR, NV, VEC>;
     const int64_t blocks = std::min<int64_t>((a.R + SH::rows - 1) / SH::rows, kNormGrid);
-    if (VEC == 8 && streams(a)) hipLaunchKernelGGL((ssd_norm_fwd_kernel<X, T, TPR, NV, VEC, VEC == 8>), dim3((unsigned)blocks), dim3(SH::threads), 0, stream, a);
-    else hipLaunchKernelGGL((ssd_norm_fwd_kernel<X, T, TPR, NV, VEC, false>), dim3((unsigned)blocks), dim3(SH::threads), 0, stream, a);
+    hipLaunchKernelGGL((ssd_norm_fwd_kernel<X, T, TPR, NV, VEC>), dim3((unsigned)blocks), dim3(SH::threads), 0, stream, a);
     return hipGetLastError();
 }
 template <typename X, typename T, int TPR, int NV, int VEC>
