@@ -509,7 +509,7 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
 //
 // bf16: states, U and Z enter as pairs, and the last products (of dAtt and dL
 // with K and Q, whose results are rounded to bf16) with one rounding each.
-// Measured, B=2 L=8192 H=32 G=8 P=N=64: 250 to 285 us (0.74 GB of states, U, Z
+// Measured, B=2 L=8192 H=32 G=8 P=N=64: 250 to 290 us (0.74 GB of states, U, Z
 // and rows: 145 us at a copy's rate).  Loads are not ahead of their head (the
 // registers are full), so it takes two workgroups a CU to hide them: at one,
 // with 280 registers a wave, it took 415 us.
