@@ -663,7 +663,7 @@ def _on_stream(fn):
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
 
-    call.__doc__ += "  stream: a torch stream or a raw handle to run on in place of the current one."
+    call.__doc__ = (fn.__doc__ or "") + "  stream: a torch stream or a raw handle to run on in place of the current one."
     return call
 
 
