@@ -430,7 +430,7 @@ struct ScanIo {
 // Splits: S, X, U and T are hi + lo pairs, k is bf16 as it is: K S and K^T U
 // take two MFMAs a tile, T X three; the state's error stays near 2^-18.  Y is
 // rounded to bf16 in the end, so its products take S and Att T rounded once,
-// 2^-9 each, as the output's own rounding, and X as a pair.
+// 2^-8 each at most, as the output's own rounding, and X as a pair.
 //
 // Few heads and a long sequence leave most CUs without a chain.  A chunk's
 // step is linear in the state, S' = Phi S + (a part from v), so the sequence
