@@ -146,9 +146,11 @@ struct Shape {
     static constexpr int rows = threads / TPR;      // rows of a workgroup at a time
 };
 
-// mean (0 for rms) and rstd of the row in x; x becomes xhat
+// mean (0 for rms) and rstd of the row in x; x becomes xhat.  Threads without a
+// row (not live) hold zeros: their rstd is 0, since with eps = 0 it would be
+// infinite and their xhat, which enters the weights' sums, NaN
 template <int TPR, int NV, int VEC>
-__device__ __forceinline__ float to_hat(float (&x)[NV][VEC], const bool (&on)[NV], int W, int rms, float eps,
+__device__ __forceinline__ float to_hat(float (&x)[NV][VEC], const bool (&on)[NV], bool live, int W, int rms, float eps,
                                         float (*red)[2][16], int& turn) {
     const float inv = 1.0f / (float)W;
     float s = 0.0f, unused = 0.0f;
@@ -170,7 +172,7 @@ __device__ __forceinline__ float to_hat(float (&x)[NV][VEC], const bool (&on)[NV
 #pragma unroll
         for (int e = 0; e < VEC; ++e) s = fmaf(x[j][e], x[j][e], s);
     row_sum2<TPR>(s, unused, red, turn);
-    const float rstd = 1.0f / sqrtf(s * inv + eps);
+    const float rstd = live ? 1.0f / sqrtf(s * inv + eps) : 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -241,7 +243,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_k
                 if (zp) ldv<VEC>(zp + r * a.z_stride + col + c, z[j]);
             }
         }
-        to_hat<TPR, NV, VEC>(x, on, a.W, a.rms, a.eps, red, turn);
+        to_hat<TPR, NV, VEC>(x, on, live, a.W, a.rms, a.eps, red, turn);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (lane + j * TPR) * VEC;
@@ -324,7 +326,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             ng[j].get(g[j]);
         }
         if (kAhead) fetch(at + step);
-        const float rstd = to_hat<TPR, NV, VEC>(x, on, a.W, a.rms, a.eps, red, turn);
+        const float rstd = to_hat<TPR, NV, VEC>(x, on, live, a.W, a.rms, a.eps, red, turn);
         if (!kHeld) load_params<TPR, NV, VEC>(a.w, a.b, on, lane, wv, bv);
         float m1 = 0.0f, m2 = 0.0f;
 #pragma unroll
