@@ -672,7 +672,8 @@ int ssd_delta_step(int B, int H, int P, int N, int G, int dtype,
  * Results are deterministic: a group's heads are summed in one workgroup, dA
  * and ddt_bias through per-chunk partial sums added in a fixed order.  Outputs
  * must not overlap the inputs or each other.  L = 0 writes zero dA and
- * ddt_bias and copies grad_final_state through.
+ * ddt_bias and copies grad_final_state through; B = 0 writes nothing, and dA
+ * and ddt_bias stay as the caller left them.
  */
 int ssd_delta_scan_bwd(int B, int L, int H, int P, int N, int G, int chunk, int dtype,
                        const void *q, int64_t q_row_stride,

@@ -473,6 +473,11 @@ def ssd_mixer_bwd_workspace_size(B, L, H, P, N, G, dtype=SSD_BF16) -> int:
     return int(load().ssd_mixer_bwd_workspace_size(B, L, H, P, N, G, dtype))
 
 
+def _params(batch):
+    """The allocator of parameter gradients: an empty batch, for which the library does nothing, leaves them zero."""
+    return torch.empty if batch else torch.zeros
+
+
 def _ws(workspace, nbytes, device):
     if workspace is None:
         return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
@@ -764,9 +769,9 @@ def ssd_delta_scan_bwd(q, k, v, dt, A, beta, grad_y, *, H, P, N, G, scale=None, 
     f32, same, state = dict(dtype=torch.float32, device=c.dev), dict(dtype=T, device=c.dev), (B, H, P, N)
     g = {"q": torch.empty(B, L, G * N, **same), "k": torch.empty(B, L, G * N, **same),
          "v": torch.empty(B, L, H * P, **same), "dt": torch.empty(B, L, H, **f32), "beta": torch.empty(B, L, H, **f32),
-         "A": torch.empty(H, **f32)}
+         "A": _params(B)(H, **f32)}
     if dt_softplus:
-        g["dt_bias"] = torch.empty(H, **f32)
+        g["dt_bias"] = _params(B)(H, **f32)
     if init_state is not None:
         g["init_state"] = torch.empty(state, **f32)
     ws = _ws(workspace, ssd_delta_scan_bwd_workspace_size(B, L, H, P, N, G, dtype), c.dev)
