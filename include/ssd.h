@@ -472,7 +472,7 @@ size_t ssd_s6_workspace_size(int B, int L, int D, int N, int dtype);
  *               caller-owned, not shared by concurrent calls
  * Outputs must not overlap the inputs or each other.  Supported: N in
  * {16, 32, 64, 128}, P = 64, chunk = 64.  L = 0 writes zero parameter
- * gradients.
+ * gradients; B = 0 leaves dA, dD and ddt_bias as the caller left them.
  */
 int ssd_chunk_scan_bwd(int B, int L, int H, int P, int N, int G, int chunk, int dtype,
                        const void *x, int64_t x_row_stride,

@@ -504,10 +504,10 @@ def ssd_chunk_scan_bwd(x, Bm, Cm, dt, A, grad_y, *, H, P, N, G, D=None, z=None, 
     _contig(doc_ids, "doc_ids", (B, L))
     f32 = dict(dtype=torch.float32, device=dev)
     g = {"x": torch.empty(B, L, H * P, **f32), "Bm": torch.empty(B, L, G * N, **f32),
-         "Cm": torch.empty(B, L, G * N, **f32), "dt": torch.empty(B, L, H, **f32), "A": torch.empty(H, **f32),
-         "D": torch.empty(H, **f32) if D is not None else None,
+         "Cm": torch.empty(B, L, G * N, **f32), "dt": torch.empty(B, L, H, **f32), "A": _params(B)(H, **f32),
+         "D": _params(B)(H, **f32) if D is not None else None,
          "z": torch.empty(B, L, H * P, **f32) if z is not None else None,
-         "dt_bias": torch.empty(H, **f32) if dt_softplus else None}
+         "dt_bias": _params(B)(H, **f32) if dt_softplus else None}
     ws = _ws(workspace, ssd_chunk_scan_bwd_workspace_size(B, L, H, P, N, G, dtype), dev)
     nb = ws.numel() * ws.element_size()
     st = lib.ssd_chunk_scan_bwd(
@@ -571,8 +571,8 @@ def ssd_mixer_bwd(xbc_raw, dt_raw, conv_w, A, grad_y, *, H, P, N, G, K=4, conv_b
     f32 = dict(dtype=torch.float32, device=dev)
     g = {"raw": torch.empty(B, L, C, **f32), "w": torch.empty(C, K, **f32),
          "bias": torch.empty(C, **f32) if conv_b is not None else None, "dt_raw": torch.empty(B, L, H, **f32),
-         "dt_bias": torch.empty(H, **f32) if dt_bias is not None else None, "A": torch.empty(H, **f32),
-         "D": torch.empty(H, **f32) if D is not None else None,
+         "dt_bias": _params(B)(H, **f32) if dt_bias is not None else None, "A": _params(B)(H, **f32),
+         "D": _params(B)(H, **f32) if D is not None else None,
          "z": torch.empty(B, L, H * P, **f32) if z is not None else None}
     ws = _ws(workspace, ssd_mixer_bwd_workspace_size(B, L, H, P, N, G, dtype), dev)
     st = lib.ssd_mixer_bwd(
