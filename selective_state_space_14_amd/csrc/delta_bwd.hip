@@ -33,7 +33,7 @@ struct BwdIo {
     const float *scal, *across;    // [u][kScalBwd][C], [u]
     const float *S, *U;            // [u][N][P], [u][C][P]
     float *D, *Z;                  // as S and U: the adjoint leaving each chunk, Z
-    float* part;                   // [2][B * nc][H]
+    void* part;                    // [2][B * nc][H] (Sum)
     int nc;
     Split split;
 };
@@ -513,8 +513,10 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
 // and rows: 145 us at a copy's rate).  Loads are not ahead of their head (the
 // registers are full), so it takes two workgroups a CU to hide them: at one,
 // with 280 registers a wave, it took 415 us.
-// The sums behind d(dt A): fp32 inputs take them in fp64, where the row and column sums of an entry cancel exactly
-// (dA and ddt_bias at B=2 L=150 H=4: 2.3e-6 off in fp32, 8e-7 this way); the products of bf16 inputs are off by more than fp32 sums.
+// The sums behind d(dt A), from a row's parts to dA and ddt_bias: fp32 inputs take all of them in fp64, where the terms on
+// one side of a token cancel to 2^-47 of their magnitudes (dA and ddt_bias of four seeds at B=2 L=150 H=4 P=64 N=32: up to
+// 1.3e-6 and 2.8e-6 off with the chunk's totals and the last sums in fp32, up to 3.5e-7 and 2.6e-7 this way); the products
+// of bf16 inputs are off by more than fp32 sums.
 template <typename T>
 using Sum = std::conditional_t<std::is_same<T, float>::value, double, float>;
 
@@ -531,7 +533,31 @@ struct GradLds {
     static constexpr int bytes = dot + 64;
 };
 
+// every lane has it
 __device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
+__device__ __forceinline__ double of_halves(unsigned lo, unsigned hi) {
+    return __longlong_as_double(((long long)(int)hi << 32) | lo);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_plus64(double v) {
+    const long long b = __double_as_longlong(v);
+    return v + of_halves(__builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xF, 0xF, true),
+                         __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ double wave_sum(double v) {   // the moves of lanes_sum, on both halves
+    v = dpp_plus64<0xB1>(v);
+    v = dpp_plus64<0x4E>(v);
+    v = dpp_plus64<0x141>(v);
+    v = dpp_plus64<0x140>(v);
+    long long b = __double_as_longlong(v);
+    auto lo = __builtin_amdgcn_permlane16_swap((unsigned)b, (unsigned)b, false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
+    v = of_halves(lo[0], hi[0]) + of_halves(lo[1], hi[1]);
+    b = __double_as_longlong(v);
+    lo = __builtin_amdgcn_permlane32_swap((unsigned)b, (unsigned)b, false, false);
+    hi = __builtin_amdgcn_permlane32_swap((unsigned)(b >> 32), (unsigned)(b >> 32), false, false);
+    return of_halves(lo[0], hi[0]) + of_halves(lo[1], hi[1]);
+}
 __device__ __forceinline__ float shfl_down(float v, int d) { return __shfl_down(v, d); }
 __device__ __forceinline__ double shfl_down(double v, int d) {
     const long long b = __double_as_longlong(v);
@@ -610,8 +636,9 @@ struct Last<float> {
     static __device__ __forceinline__ f32x4 mul(f32x4 acc, const Last& x, const Last& y) { return mma_f32(mma_f32(acc, x.a, y.a), x.b, y.b); }
 };
 
+// two workgroups a CU where a wave's registers allow it (fp32 N = 32: 242)
 template <typename T, int N>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_delta_grad_kernel(DeltaBwdArgs ba, BwdIo io) {
+__global__ __launch_bounds__(256, N <= (sizeof(T) == 2 ? 64 : 32) ? 2 : 1) void ssd_delta_grad_kernel(DeltaBwdArgs ba, BwdIo io) {
     using LD = GradLds<T, N>;
     constexpr int NT = N / 16, KS = N / 32, es = LD::es, nc16 = N * es / 16;
     constexpr bool kLate = es == 4 && N == 128;      // dS only when S0 has been used: registers
@@ -623,6 +650,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
     const int hg = a.H / a.G, t0 = c * C, n_on = min(C, row_len(a, b) - t0), n_rows = min(C, a.L - t0);
     const size_t tok0 = (size_t)b * a.L + t0;
     const size_t bc = (size_t)b * io.nc + c, parts = (size_t)a.B * io.nc * a.H;
+    using SumT = Sum<T>;
+    SumT* part = static_cast<SumT*>(io.part);
     T* dq = static_cast<T*>(ba.dq) + tok0 * ba.dq_stride + (size_t)g * N;
     T* dk = static_cast<T*>(ba.dk) + tok0 * ba.dk_stride + (size_t)g * N;
     T* dv = static_cast<T*>(ba.dv) + tok0 * ba.dv_stride + (size_t)g * hg * a.P;
@@ -637,7 +666,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
             ba.ddt[(tok0 + e / hg) * ba.ddt_stride + g * hg + e % hg] = 0.0f;
             ba.dbeta[(tok0 + e / hg) * ba.dbeta_stride + g * hg + e % hg] = 0.0f;
         }
-        for (int e = tid; e < hg; e += 256) io.part[bc * a.H + g * hg + e] = io.part[parts + bc * a.H + g * hg + e] = 0.0f;
+        for (int e = tid; e < hg; e += 256) part[bc * a.H + g * hg + e] = part[parts + bc * a.H + g * hg + e] = 0;
         return;
     }
     // ---- k and q of the chunk
@@ -659,10 +688,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
     f32x4 dQ[NT], dK[NT];                            // [n][t]
 #pragma unroll
     for (int n = 0; n < NT; ++n) dQ[n] = dK[n] = kZero4;
-    using SumT = Sum<T>;
     SumT* colp = reinterpret_cast<SumT*>(lds + LD::col);
     SumT* rowp = reinterpret_cast<SumT*>(lds + LD::row);
-    float* dotp = reinterpret_cast<float*>(lds + LD::dot);
+    SumT* dotp = reinterpret_cast<SumT*>(lds + LD::dot);
 
     for (int hh = 0; hh < hg; ++hh) {
         const int h = g * hg + hh;
@@ -674,7 +702,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
         for (int n = 0; n < NT; ++n) W1[n] = W2[n] = W3[n] = kZero4;
 #pragma unroll
         for (int n = 0; n < 4; ++n) EA[n] = EL[n] = kZero4;
-        float zv = 0.0f, sd = 0.0f;
+        float zv = 0.0f;
+        SumT sd = 0.0f;
         for (int p0 = 0; p0 < a.P; p0 += 64) {
             // the wave's own rows t: dY, Z, U as operands; dV; U's tile for everyone
             Rows<T> dy[2];
@@ -745,6 +774,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
                     W2[n] = Wide<T>::mul(W2[n], f, z[s]);
                 }
             __syncthreads();
+            float late = 0.0f;                       // kLate: 32 products of <S0, dS>
 #pragma unroll
             for (int j = 0; j < (NT + 3) / 4; ++j) {
                 const int n = w + 4 * j;
@@ -757,12 +787,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
                             const float4 d0 = *reinterpret_cast<const float4*>(dp), d1 = *reinterpret_cast<const float4*>(dp + 4);
                             Wide<T> f;
                             f.get(to);
-                            sd += dot4(v4(f.p.a), v4(d0)) + dot4(v4(f.p.b), v4(d1));
+                            late += dot4(v4(f.p.a), v4(d0)) + dot4(v4(f.p.b), v4(d1));
                             ds[j][s].set(d0, d1);
                         }
                         ds[j][s].put(to);
                     }
                 }
+            }
+            if constexpr (kLate) {                   // not held over the products, for the registers' sake
+                const SumT all = wave_sum((SumT)late);
+                if (lane == 0) dotp[w] = p0 == 0 ? all : dotp[w] + all;
             }
             __syncthreads();
 #pragma unroll
@@ -854,13 +888,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
 #pragma unroll
             for (int x = 0; x < 5; ++x) all[x] = rows_sum(all[x]);
             rsum = sum_rows(rsum);
-            sd = wave_sum(sd);
+            if constexpr (!kLate) sd = wave_sum(sd);
             if (q == 0) {
                 rowp[t] = rsum + all[0] - (SumT)beta * all[1] - all[2];
                 rowp[C + t] = all[2];
                 rowp[2 * C + t] = all[4] - all[1] + all[3];
             }
-            if (lane == 0) dotp[w] = sd;
+            if (!kLate && lane == 0) dotp[w] = sd;
         }
         __syncthreads();
 #pragma unroll
@@ -884,8 +918,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
         if (w == 0) {
             // one token a lane: d(dt A) is the sum of dG behind it
             SumT dG = rowp[lane] - ((colp[lane] + colp[C + lane]) + (colp[2 * C + lane] + colp[3 * C + lane]));
-            const float r3s = wave_sum((float)rowp[C + lane]), dot = (dotp[0] + dotp[1]) + (dotp[2] + dotp[3]);
-            if (lane == 63) dG += fmaf(io.across[u], dot, r3s);
+            const SumT r3s = wave_sum(rowp[C + lane]), dot = (dotp[0] + dotp[1]) + (dotp[2] + dotp[3]);
+            if (lane == 63) dG += fma((SumT)io.across[u], dot, r3s);
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
                 const SumT dn = shfl_down(dG, d);
@@ -910,10 +944,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
                 ba.ddt[(tok0 + lane) * ba.ddt_stride + h] = dd;
                 ba.dbeta[(tok0 + lane) * ba.dbeta_stride + h] = live ? db : 0.0f;
             }
-            const float pa = wave_sum(live && dG != 0.0f ? (float)dG * dt : 0.0f), pd = wave_sum(dd);   // dt may be infinite
+            const SumT pa = wave_sum(live && dG != 0.0f ? dG * dt : SumT(0)), pd = wave_sum((SumT)dd);   // dt may be infinite
             if (lane == 0) {
-                io.part[bc * a.H + h] = pa;
-                io.part[parts + bc * a.H + h] = pd;
+                part[bc * a.H + h] = pa;
+                part[parts + bc * a.H + h] = pd;
             }
         }
         __syncthreads();
@@ -941,10 +975,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && N <= 64 ? 2 : 1) void ssd_de
 }
 
 // dA and ddt_bias: the chunks' parts of a head, added in a fixed order
-__global__ __launch_bounds__(256) void ssd_delta_sum_kernel(const float* part, size_t rows, int H, float* dA, float* ddt_bias) {
-    __shared__ float s[256];
+template <typename S>
+__global__ __launch_bounds__(256) void ssd_delta_sum_kernel(const S* part, size_t rows, int H, float* dA, float* ddt_bias) {
+    __shared__ S s[256];
     const int h = blockIdx.x % H, k = blockIdx.x / H;
-    float v = 0.0f;
+    S v = 0.0f;
     for (size_t r = threadIdx.x; r < rows; r += 256) v += part[(k * rows + r) * H + h];
     s[threadIdx.x] = v;
     __syncthreads();
@@ -954,7 +989,7 @@ __global__ __launch_bounds__(256) void ssd_delta_sum_kernel(const float* part, s
         __syncthreads();
     }
     float* out = k ? ddt_bias : dA;
-    if (threadIdx.x == 0 && out) out[h] = s[0];
+    if (threadIdx.x == 0 && out) out[h] = (float)s[0];
 }
 
 struct BwdWs {
@@ -980,7 +1015,7 @@ BwdWs bwd_ws(int B, int L, int H, int P, int N, int dtype) {
     w.U = take(units * C * P * 4);
     w.D = take(units * N * P * 4);
     w.Z = take(units * C * P * 4);
-    w.part = take(2 * units * 4);
+    w.part = take(2 * units * (dtype == 0 ? sizeof(Sum<float>) : sizeof(Sum<uint16_t>)));
     split_bwd(B, L, H, P, N, dtype, w.split);
     const size_t states = w.split.K > 1 ? (size_t)B * H * w.split.K * N * 4 : 0;
     w.loc = take(states * P);
@@ -1001,7 +1036,7 @@ hipError_t launch_bwd_n(const DeltaBwdArgs& ba, void* ws, hipStream_t stream) {
     const Split split{w.split.K, w.split.S, fp(w.loc), fp(w.phi), fp(w.s0)};
     hipError_t e = launch_keep(a, o, KeepOut{fp(w.S), fp(w.U), split}, stream);
     if (e != hipSuccess) return e;
-    BwdIo io{o.TT, o.att, o.scal, o.across, fp(w.S), fp(w.U), fp(w.D), fp(w.Z), fp(w.part), nc, split};
+    BwdIo io{o.TT, o.att, o.scal, o.across, fp(w.S), fp(w.U), fp(w.D), fp(w.Z), base + w.part, nc, split};
     constexpr size_t grad = GradLds<T, N>::bytes;
     const dim3 chains(a.B * a.H * (a.P / 64));
     if constexpr (std::is_same<T, float>::value) {
@@ -1031,7 +1066,7 @@ hipError_t launch_bwd_n(const DeltaBwdArgs& ba, void* ws, hipStream_t stream) {
     hipLaunchKernelGGL((ssd_delta_grad_kernel<T, N>), dim3((unsigned)((size_t)a.B * nc * a.G)), dim3(256), grad, stream, ba, io);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(ssd_delta_sum_kernel, dim3(2 * a.H), dim3(256), 0, stream, io.part, (size_t)a.B * nc, a.H, ba.dA, ba.ddt_bias);
+    hipLaunchKernelGGL((ssd_delta_sum_kernel<Sum<T>>), dim3(2 * a.H), dim3(256), 0, stream, static_cast<const Sum<T>*>(io.part), (size_t)a.B * nc, a.H, ba.dA, ba.ddt_bias);
     return hipGetLastError();
 }
 
