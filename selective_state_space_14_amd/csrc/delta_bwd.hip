@@ -938,6 +938,10 @@ __global__ __launch_bounds__(256, N <= (sizeof(T) == 2 ? 64 : 32) ? 2 : 1) void 
             // Every pair across t carries the factor exp(dt A): below e^-30 the true sum is far under the rounding
             // that the row and column sums leave behind (2^-24 of them), which a large dt would carry into dA.
             if (dt * a.A[h] < -30.0f) dG = 0.0f;
+            // Nothing passes into a document's first token, nor into a row's that has no state before it: exactly 0.
+            const float* seg = reinterpret_cast<const float*>(lds + LD::scal) + kSSeg * C;
+            const bool none = seg[lane] != (lane ? seg[lane - 1] : 0.0f) || (t0 + lane == 0 && !a.init_state);
+            if (none) dG = 0.0f;
             const bool live = lane < n_on;
             const float dd = live ? (float)dG * a.A[h] * chain : 0.0f;
             if (lane < n_rows) {

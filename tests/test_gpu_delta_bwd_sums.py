@@ -76,3 +76,26 @@ def test_dt_bias_is_the_sum_of_dt(gpu_lib):
     err = (out["dt_bias"].double() - dt.sum(0)).abs()
     tol = 2.0 ** -24 * dt.sum(0).abs() + 2.0 ** -43 * dt.abs().sum(0)
     assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("lengths", [None, [0, 1, 150]])
+def test_nothing_passes_into_a_first_token(gpu_lib, dtype, state, lengths):
+    """The gradient of dt at a document's first token, and at a row's where no state enters it, is exactly 0.  Of the
+    other tokens it is not, a row's first with a state among them, where dt A > -5: the pairs across such a token carry 2^-8
+    or more.  (Below dt A = -30 the kernel returns 0, and in between what pairs are left can round away.)"""
+    dims = (2, 64, 64, 1)
+    d, opt = make(3, 150, *dims, dtype, state=state, lengths=lengths, docs=0.05)
+    opt["doc_ids"][:, 63:] += 1
+    opt["doc_ids"][:, 64:] += 1                      # a document of one token at a chunk's end, one that starts a chunk
+    gy, gS = cotangents(d, opt, dims)
+    out = grads(gpu_lib, d, opt, dims, gy, gS)["dt"].cpu()
+    first = torch.zeros(3, 150, dtype=torch.bool)
+    first[:, 1:] = opt["doc_ids"][:, 1:] != opt["doc_ids"][:, :-1]
+    first[:, 0] = not state
+    assert (out[first] == 0).all(), out[first].abs().max()
+    live = torch.arange(150)[None] < torch.tensor([150] * 3 if lengths is None else lengths)[:, None]
+    dt, _ = ref.gates(d["dt"], d["beta"], True, d["dt_bias"], True)
+    seen = (live & ~first)[..., None] & (dt * d["A"].double() > -5.0)
+    assert seen[:, 0].any() == state and (out[seen] != 0).all()
