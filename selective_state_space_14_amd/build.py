@@ -34,9 +34,14 @@ CFLAGS = [
 EXTRA_CFLAGS = {s: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for s in ("delta.hip", "delta_bwd.hip")}
 
 
+def cflags(src: str) -> list:
+    """The flags that a source is compiled with."""
+    return [*CFLAGS, *EXTRA_CFLAGS.get(src, [])]
+
+
 def _compile(src: str, obj_dir: str) -> str:
     obj = os.path.join(obj_dir, os.path.basename(src) + ".o")
-    cmd = [HIPCC, *CFLAGS, *EXTRA_CFLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *cflags(src), "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
