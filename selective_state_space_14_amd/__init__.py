@@ -656,19 +656,22 @@ class _Call:
 
 def _on_stream(fn):
     """A call with `stream`, a torch stream or a raw handle, makes it the current one, so that what the call allocates
-    (outputs, a workspace that is free again on return) belongs to the stream that uses it."""
+    (outputs, a workspace that is free again on return) belongs to the stream that uses it.  A torch stream of another
+    GPU than the tensors' is refused; a raw handle, which does not tell, is taken as one of theirs."""
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
+        at = next((t.device for t in (*args, *kw.values()) if isinstance(t, torch.Tensor) and t.is_cuda), None)
+        if at is not None and getattr(stream, "device", at) != at:
+            raise ValueError(f"stream: on {stream.device}, expected {at} as the tensors")
         if not isinstance(stream, torch.cuda.Stream):
-            at = next((t.device for t in (*args, *kw.values()) if isinstance(t, torch.Tensor) and t.is_cuda), None)
             stream = torch.cuda.ExternalStream(_stream(stream), device=at)
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
 
-    call.__doc__ = (fn.__doc__ or "") + "  stream: a torch stream or a raw handle to run on in place of the current one."
+    call.__doc__ = (fn.__doc__ or "") + "  stream: a torch stream or a raw handle, on the tensors' GPU, to run on in place of the current one."
     return call
 
 
