@@ -623,7 +623,8 @@ int ssd_delta_scan_fwd(int B, int L, int H, int P, int N, int G, int chunk, int 
                        void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace of ssd_delta_scan_fwd: T, M o Q K^T and the decays of
- * every chunk and head, and the superchunks' states and transitions. */
+ * every chunk and head, and the superchunks' states and transitions.  0 for
+ * sizes of no work and for more tokens or heads than the call accepts. */
 size_t ssd_delta_scan_workspace_size(int B, int L, int H, int P, int N, int G, int dtype);
 
 /*
@@ -695,7 +696,7 @@ int ssd_delta_scan_bwd(int B, int L, int H, int P, int N, int G, int chunk, int 
 
 /* Bytes of workspace of ssd_delta_scan_bwd: every chunk's T, its transpose and
  * M o Q K^T, the state entering and the adjoint leaving it, U and Z, and the
- * superchunks' states and transitions. */
+ * superchunks' states and transitions.  0 as above. */
 size_t ssd_delta_scan_bwd_workspace_size(int B, int L, int H, int P, int N, int G, int dtype);
 
 /*

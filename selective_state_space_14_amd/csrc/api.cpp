@@ -965,6 +965,16 @@ int ssd_step(int B, int H, int P, int N, int G, int K, int dtype,
 }
 
 // ---- the gated delta rule: sizes and arguments that its three calls share
+// the grids: a workgroup for every chunk of every head, and up to 16 for a head's step
+static bool delta_units_fit(int B, int L, int H) {
+    const long long heads = (long long)B * H;
+    return heads <= 0x7fffffffLL && heads * std::max(16LL, ((long long)L + 63) / 64) <= 0x7fffffffLL;
+}
+
+static bool delta_has_work(int B, int L, int H, int P, int N, int G) {
+    return B > 0 && L > 0 && H > 0 && P > 0 && N > 0 && G > 0 && L <= kMaxL && delta_units_fit(B, L, H);
+}
+
 static int check_delta(const char* fn, ssd::DeltaArgs& a, bool work) {
     if (a.dtype != SSD_F32 && a.dtype != SSD_BF16)
         return fail(SSD_ERR_UNSUPPORTED, "%s: dtype=%d is not supported (only SSD_F32=0 and SSD_BF16=1; "
@@ -979,10 +989,8 @@ static int check_delta(const char* fn, ssd::DeltaArgs& a, bool work) {
         return fail(SSD_ERR_UNSUPPORTED, "%s: P=%d is not supported (head dim must be 64 or 128)", fn, a.P);
     if (a.N != 32 && a.N != 64 && a.N != 128)
         return fail(SSD_ERR_UNSUPPORTED, "%s: N=%d is not supported (state dim must be 32, 64 or 128)", fn, a.N);
-    // the grids: a workgroup for every chunk of every head, and up to 16 for a head's step
-    const long long units = (long long)a.B * a.H * std::max(16LL, ((long long)a.L + 63) / 64);
-    if (units > 0x7fffffffLL)
-        return fail(SSD_ERR_BAD_SHAPE, "%s: B*H*max(16, L/64)=%lld is too large", fn, units);
+    if (!delta_units_fit(a.B, a.L, a.H))
+        return fail(SSD_ERR_BAD_SHAPE, "%s: B*H*max(16, L/64) of B=%d, H=%d, L=%d is too large", fn, a.B, a.H, a.L);
     if (a.dt_softplus != 0 && a.dt_softplus != 1)
         return fail(SSD_ERR_UNSUPPORTED, "%s: dt_softplus=%d must be 0 or 1", fn, a.dt_softplus);
     if (a.beta_sigmoid != 0 && a.beta_sigmoid != 1)
@@ -1031,7 +1039,7 @@ static ssd::DeltaArgs delta_args(int B, int L, int H, int P, int N, int G, int d
 }
 
 size_t ssd_delta_scan_workspace_size(int B, int L, int H, int P, int N, int G, int dtype) {
-    if (B <= 0 || L <= 0 || H <= 0 || P <= 0 || N <= 0 || G <= 0) return 0;
+    if (!delta_has_work(B, L, H, P, N, G)) return 0;
     return ssd::delta_fwd_workspace_bytes(B, L, H, P, N, dtype);
 }
 
@@ -1078,7 +1086,7 @@ int ssd_delta_scan_fwd(int B, int L, int H, int P, int N, int G, int chunk, int 
 }
 
 size_t ssd_delta_scan_bwd_workspace_size(int B, int L, int H, int P, int N, int G, int dtype) {
-    if (B <= 0 || L <= 0 || H <= 0 || P <= 0 || N <= 0 || G <= 0) return 0;
+    if (!delta_has_work(B, L, H, P, N, G)) return 0;
     return ssd::delta_bwd_workspace_bytes(B, L, H, P, N, dtype);
 }
 
@@ -1255,7 +1263,7 @@ int ssd_norm_fwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, 
 
 size_t ssd_norm_bwd_workspace_size(int64_t R, int groups, int W) {
     if (R <= 0 || groups <= 0 || W <= 0) return 0;
-    return ssd::norm_bwd_workspace_bytes(R * groups, W);
+    return ssd::norm_bwd_workspace_bytes(std::min<int64_t>(R, ssd::kNormBwdGrid) * groups, W);   // a workgroup a row at most
 }
 
 int ssd_norm_bwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, float eps,
