@@ -743,7 +743,9 @@ def _norm_groups(c, shape, tensors):
     try:
         return n, 1, {name: c.rows(t, name, dtype, shape) for name, (t, dtype) in tensors.items()}
     except ValueError:
-        if len(shape) < 3 or any(t is not None and (t.shape != shape or t.stride(-2) != W) for t, _ in tensors.values()):
+        # heads side by side: else flatten() below would hand the library a copy
+        if len(shape) < 3 or any(t is not None and (t.shape != shape or t.stride(-2) != W or (W > 1 and t.stride(-1) != 1))
+                                 for t, _ in tensors.values()):
             raise
     g = shape[-2]
     flat = shape[:-2] + (g * W,)
