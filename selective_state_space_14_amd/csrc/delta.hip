@@ -40,13 +40,13 @@ using namespace delta;
 // Att T diag(beta) for y, so those two products are formed here, where all
 // chunks run at once, and not in the chain of the scan.  (Forming only Att here
 // took 122 us in place of 156 at B=5 L=8192 H=32 N=64, but the scan 242 in
-// place of 225.)
+// place of 225, both from an idle GPU's lower clocks.)
 //
-// Measured, bf16: 154 us at B=5 L=8192 H=32 P=N=64 (20480 units, 17 KB written
-// each, 357 MB), 300 us at B=4 L=4096 H=128 N=128 (32768 units; 558 MB written,
-// 331 MB read: 175 us at a copy's rate, the matrix pipes busy for 85 us and the
-// vector units for 89, so what is left is the substitution's latency, of which
-// two waves a SIMD hide a part).
+// Measured, bf16: 144 us at B=5 L=8192 H=32 P=N=64 (20480 units, 17 KB written
+// each, 357 MB, and 255 MB read: 120 us at a copy's rate), 262 us at B=4 L=4096
+// H=128 N=128 (32768 units; 571 MB written and 681 MB read, since a group's 16
+// heads are on all eight XCDs: 245 us at a copy's rate, with the matrix pipes
+// busy for 85 us and the vector units for 89).
 constexpr int kLtRow = 20;                           // floats of an L^T tile's row: 16-byte reads of 16 rows hit all banks
 constexpr int kPrepWaves = 2;
 enum Prep {
@@ -420,9 +420,9 @@ struct ScanIo {
 // the chain, and four more everything that is not part of it, on the same
 // SIMDs: they bring the next chunk's k, v and T from memory to LDS, and compute
 // and store the last chunk's y from the S and X fragments that the chain left
-// in LDS.  A chunk costs one barrier.  Measured: 1.7 us a chunk at N = 64 (218
+// in LDS.  A chunk costs one barrier.  Measured: 1.7 us a chunk at N = 64 (213
 // us at B=5 L=8192 H=32, 160 workgroups; 364 us with all of it in four waves),
-// 2.9 us at N = 128 (375 us at B=4 L=4096 H=128, two rounds of 64 chunks).  At
+// 2.6 us at N = 128 (331 us at B=4 L=4096 H=128, two rounds of 64 chunks).  At
 // N = 128 a CU's reads in flight bound it (11 bytes a cycle and CU), at N = 64
 // the chain's latency.  The chain's LDS reads are issued ahead
 // of the products they feed (sched_barrier: left to itself the compiler reads
@@ -1102,10 +1102,10 @@ __global__ __launch_bounds__(256) void ssd_delta_scan_kernel(DeltaArgs a, ScanIo
 }
 
 // Superchunks of a sequence, bf16: the K that takes the fewest chunk steps, with one workgroup a CU at a time.  Against
-// a step of the full pass the state pass's, without y, takes 0.75, and joining one superchunk about 3 (measured: 2.0,
-// 1.5 and 5 us at N = P = 128).  B=1 L=32768 H=16 N=P=128 takes 1.07 ms whole and 0.52 ms in the superchunks chosen.
+// a step of the full pass the state pass's, without y, is counted as 0.75, and joining one superchunk as 3 (measured: 2.4,
+// 1.6 and 3 us at N = P = 128).  B=1 L=32768 H=16 N=P=128 takes 1.07 ms whole and 0.47 ms in the superchunks chosen.
 // The backward has two full passes (a step of both: 2.2) and two state passes, the transitions in the first only, and two
-// joins: B=2 L=8192 H=32 N=P=64 takes 553 us of chains whole and 382 us in four superchunks, joins and all.
+// joins: B=2 L=8192 H=32 N=P=64 takes 902 us whole and 722 us in four superchunks.
 void delta_split(int B, int L, int H, int P, int N, int dtype, bool bwd, int& K, int& S) {
     const int nc = (L + C - 1) / C;
     const int64_t units = (int64_t)B * H * (P / 64), wide = (int64_t)B * H * (P / 64 + (N + 63) / 64);

@@ -47,7 +47,7 @@ struct BwdIo {
 // LDS is read in three batches ahead of the products they feed.  2.4 us a chunk
 // at N = P = 64, against 4.1 with staging in the chain's own waves: B=2 L=8192
 // H=32 took 531 us so, 307 us this way, and in four superchunks side by side
-// (AHEAD and the join included) 193 us.
+// (AHEAD and the join included) 195 us.
 // Splits: dS, dU and Z are hi + lo pairs like Att and T, dY and k, q bf16 as
 // they are.
 template <int N>
@@ -509,8 +509,8 @@ __global__ __launch_bounds__(256) void ssd_delta_reverse_kernel(DeltaBwdArgs ba,
 //
 // bf16: states, U and Z enter as pairs, and the last products (of dAtt and dL
 // with K and Q, whose results are rounded to bf16) with one rounding each.
-// Measured, B=2 L=8192 H=32 G=8 P=N=64: 250 to 290 us (0.74 GB of states, U, Z
-// and rows: 145 us at a copy's rate).  Loads are not ahead of their head (the
+// Measured, B=2 L=8192 H=32 G=8 P=N=64: 256 us (0.79 GB read and 0.14 GB
+// written: 181 us at a copy's rate).  Loads are not ahead of their head (the
 // registers are full), so it takes two workgroups a CU to hide them: at one,
 // with 280 registers a wave, it took 415 us.
 // The sums behind d(dt A), from a row's parts to dA and ddt_bias: fp32 inputs take all of them in fp64, where the terms on

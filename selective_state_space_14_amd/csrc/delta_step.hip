@@ -11,7 +11,7 @@
 // A thread takes F rows' parts, all loaded before the first is used.
 //
 // Measured: B=256 H=64 N=128, 1.07 GB read and written, 178 us (6.0 TB/s; a
-// large copy reaches 5.1).  B=1 H=32 N=64: 3.5 us on the GPU, the call's host time more.
+// large copy reaches 5.1).  B=1 H=32 N=64: 3.6 us on the GPU, the call's host time more.
 #include <hip/hip_runtime.h>
 
 #include "ssd_device.hpp"
@@ -86,8 +86,9 @@ __global__ __launch_bounds__(kThreads) void ssd_delta_step_kernel(DeltaArgs a) {
 
 template <typename T, int N>
 hipError_t launch_n(const DeltaArgs& a, hipStream_t stream) {
-    // the most rows a thread that leave 1024 workgroups, four on every CU.  Measured: the 1.07 GB
-    // of B=256 H=64 N=128 took 195 to 199 us with F = 8 and 208 with F = 1; B=1 H=32 N=64 3.9 us with F = 1 and 4.1 with 4
+    // the most rows a thread that leave 1024 workgroups, four on every CU.  Measured: the 1.07 GB of B=256 H=64 N=128,
+    // past the last-level cache, take 179 us with F = 8, 178 with 4 and 214 to 218 with 1; B=1 H=32 N=64 3.9 us with F = 1
+    // and 4.1 with 4
     const int64_t work = (int64_t)a.B * a.H * a.P * N / (kThreads * 4);   // workgroups at F = 1
     const int most = a.P * N / (kThreads * 4);                            // F of a whole head: >= 2
     int f = 8;
@@ -98,7 +99,7 @@ hipError_t launch_n(const DeltaArgs& a, hipStream_t stream) {
         case 2: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 2, false>), grid, dim3(kThreads), 0, stream, a); break;
         case 4: hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 4, false>), grid, dim3(kThreads), 0, stream, a); break;
         default:
-            // A state that the last-level cache cannot hold until the next token goes past it: 512 MB take 178 us this way
+            // A state that the last-level cache cannot hold until the next token goes past it: 512 MB take 179 us this way
             // and 199 without, but 256 MB 87 and 83, 64 MB 22.3 and 21.0.
             if (work * kThreads * 16 > (256LL << 20)) hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 8, true>), grid, dim3(kThreads), 0, stream, a);
             else hipLaunchKernelGGL((ssd_delta_step_kernel<T, N, 8, false>), grid, dim3(kThreads), 0, stream, a);
