@@ -662,7 +662,9 @@ int ssd_delta_step(int B, int H, int P, int N, int G, int dtype,
  *   dq, dk  T   [B][L][G*N] (the sums over a group's heads), dv T [B][L][H*P];
  *               rounded once to T
  *   ddt, dbeta  f32 [B][L][H]: with respect to the raw values where
- *               dt_softplus / beta_sigmoid are 1
+ *               dt_softplus / beta_sigmoid are 1.  ddt is exactly 0 at a
+ *               document's first token, at a row's where init_state is NULL,
+ *               and where dt A is below -30
  *   dA      f32 [H]: with respect to A (the caller chains A = -exp(A_log))
  *   ddt_bias f32 [H] or NULL (written when dt_softplus = 1)
  *   grad_init_state  f32 [B][H][P][N] or NULL; must not be grad_final_state's
@@ -714,7 +716,8 @@ size_t ssd_delta_scan_bwd_workspace_size(int B, int L, int H, int P, int N, int 
  * 1 <= W <= 16384; a W above 8192 needs 16-byte aligned bases and row strides
  * and W % 8 == 0 (SSD_ERR_ALIGNMENT).  Otherwise any alignment of the element
  * type will do; rows that meet those conditions are read in 16-byte pieces.
- * Statistics are fp32, the variance from the centred row.
+ * Statistics are fp32, the variance from the centred row.  eps >= 0; with
+ * eps = 0 a row of nothing but its mean (rms: of zeros) gives NaN.
  */
 int ssd_norm_fwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, float eps,
                  const void *x, int64_t x_row_stride, const float *weight, const float *bias,
