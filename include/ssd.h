@@ -1,7 +1,7 @@
 /*
  * ssd.h -- C ABI of libssd.so, the gfx950 (MI355X) Mamba-2 SSD mixer core.
  *
- * Fourteen operations, each a few HIP kernel launches on the caller's stream:
+ * Seventeen operations, each a few HIP kernel launches on the caller's stream:
  *
  *   ssd_conv_fwd        causal depthwise conv (k = 4) + SiLU over the
  *                       [x | B | C] columns, and dt = softplus(dt_raw + dt_bias)
@@ -25,6 +25,9 @@
  *   ssd_delta_scan_bwd  backward (VJP) of ssd_delta_scan_fwd
  *   ssd_norm_fwd        layer or RMS norm of rows, with weight, bias and gate
  *   ssd_norm_bwd        backward of ssd_norm_fwd, with the weights' reductions
+ *   ssd_glr_scan_fwd    the gated linear recurrence (a state a channel)
+ *   ssd_glr_step        one decode token of it per sequence
+ *   ssd_glr_scan_bwd    backward (VJP) of ssd_glr_scan_fwd
  *
  * The operation (per batch row b and head h, token t, head h in group
  * g = h / (H/G)):
@@ -747,6 +750,106 @@ int ssd_norm_bwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, 
 
 /* Bytes of workspace of ssd_norm_bwd: one fp32 row pair for every workgroup. */
 size_t ssd_norm_bwd_workspace_size(int64_t R, int groups, int W);
+
+/*
+ * The gated linear recurrence (ssd_glr_scan_fwd, ssd_glr_step,
+ * ssd_glr_scan_bwd) -- one number of state for every channel, with a gate on
+ * the decay and one on the input.  Per batch row b, token t and channel d:
+ *     a_t = exp(sigmoid(r_t + r_bias) * A)
+ *     h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * sigmoid(i_t + i_bias) * x_t
+ *     y_t = h_t
+ * The inputs are three columns of one projection, the gate behind it is the
+ * norm's (ssd_norm_fwd, ssd_add_norm_fwd with z).
+ *
+ *   x, r, i  T   [B][L][D]  row strides in elements, >= D and <= 4194304; any
+ *               alignment of the element type (rows on pairs of elements with
+ *               an even D are read in pairs)
+ *   r_bias, i_bias  f32 [D] or NULL (0)
+ *   A       f32 [D], A <= 0 (the caller computes it, for instance
+ *               A = -c softplus(lambda)); A > 0 gives NaN
+ *   doc_ids i32 [B][L] or NULL: a new document starts from a zero state, its
+ *               first input scaled like any other
+ *   lengths i32 [B] or NULL: row b is real at t < lengths[b] (read on the
+ *               device, clamped to [0, L]).  y is exactly 0 behind it, the
+ *               state stops there, and inputs behind it are not used
+ *   state   f32 [B][D], 16-byte aligned bases
+ *   y       T   [B][L][D], rounded once; must not overlap the inputs
+ * Any D >= 1 with B * D < 2^31.  Gates, decays and states are fp32; decays
+ * near 1 and 1 - a^2 are taken from the series of 1 - a, to a few 2^-24.
+ */
+
+/*
+ * ssd_glr_scan_fwd -- the recurrence over [B][L] tokens.
+ *   init_state    f32 [B][D] or NULL (zero)
+ *   final_state   f32 [B][D] or NULL; may equal init_state (in place)
+ *   chunk_states  f32 [B][ceil(L / 64)][D] or NULL: the state that enters
+ *               every 64 tokens, written for ssd_glr_scan_bwd
+ *   workspace, workspace_bytes: at least ssd_glr_scan_workspace_size() bytes
+ *               (0 for short rows: then NULL will do), 16-byte aligned,
+ *               caller-owned, not shared by concurrent calls
+ * Deterministic.  L = 0 copies the state through.
+ */
+int ssd_glr_scan_fwd(int B, int L, int D, int dtype,
+                     const void *x, int64_t x_row_stride,
+                     const void *r, int64_t r_row_stride,
+                     const void *i, int64_t i_row_stride,
+                     const float *r_bias, const float *i_bias, const float *A,
+                     const int32_t *doc_ids, const int32_t *lengths,
+                     const float *init_state, float *final_state, float *chunk_states,
+                     void *y, int64_t y_row_stride,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of ssd_glr_scan_fwd; 0 for sizes of no work and for
+ * sizes that the call does not accept. */
+size_t ssd_glr_scan_workspace_size(int B, int L, int D, int dtype);
+
+/*
+ * ssd_glr_step -- one token for each of B sequences: x, r, i, y T [B][D],
+ * state f32 [B][D] read and updated in place.  It continues
+ * ssd_glr_scan_fwd's final_state as it is.  Batch-invariant.
+ */
+int ssd_glr_step(int B, int D, int dtype,
+                 const void *x, int64_t x_row_stride,
+                 const void *r, int64_t r_row_stride,
+                 const void *i, int64_t i_row_stride,
+                 const float *r_bias, const float *i_bias, const float *A,
+                 float *state, void *y, int64_t y_row_stride, void *stream);
+
+/*
+ * ssd_glr_scan_bwd -- backward (vector-Jacobian product) of ssd_glr_scan_fwd,
+ * for grad_y = dLoss/dy and, where given, grad_final_state.
+ *   x, r, i, r_bias, i_bias, A, doc_ids, lengths, init_state   as there
+ *   chunk_states  f32 as the forward wrote them for these inputs, or NULL:
+ *               then they are computed again (init_state is read only then)
+ *   grad_y  T   [B][L][D]; grad_final_state f32 [B][D] or NULL (zero)
+ *   dx, dr, di  T   [B][L][D] (r and i before their biases); exactly 0
+ *               behind a row's length, where grad_y is not used
+ *   dA      f32 [D]; dr_bias, di_bias f32 [D] or NULL
+ *   grad_init_state  f32 [B][D] or NULL
+ *   workspace, workspace_bytes: required, at least
+ *               ssd_glr_scan_bwd_workspace_size() bytes, as above
+ * Where sqrt(1 - a^2) is 0 (A = 0, or a gate that underflows) its derivative,
+ * infinite there, is taken as 0.  Deterministic: dA, dr_bias and di_bias are
+ * sums of 64 tokens in fp32, added in a fixed order in 64 bits.  Outputs must
+ * not overlap the inputs or each other.  L = 0 writes zero dA, dr_bias and
+ * di_bias and copies grad_final_state through; B = 0 writes nothing.
+ */
+int ssd_glr_scan_bwd(int B, int L, int D, int dtype,
+                     const void *x, int64_t x_row_stride,
+                     const void *r, int64_t r_row_stride,
+                     const void *i, int64_t i_row_stride,
+                     const float *r_bias, const float *i_bias, const float *A,
+                     const int32_t *doc_ids, const int32_t *lengths,
+                     const float *init_state, const float *chunk_states,
+                     const void *grad_y, int64_t grad_y_row_stride, const float *grad_final_state,
+                     void *dx, int64_t dx_row_stride,
+                     void *dr, int64_t dr_row_stride,
+                     void *di, int64_t di_row_stride,
+                     float *dA, float *dr_bias, float *di_bias, float *grad_init_state,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of ssd_glr_scan_bwd, with the states' recomputation. */
+size_t ssd_glr_scan_bwd_workspace_size(int B, int L, int D, int dtype);
 
 #ifdef __cplusplus
 }

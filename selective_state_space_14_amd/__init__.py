@@ -18,6 +18,9 @@ The entry points mirror the C ABI in include/ssd.h one to one:
     ssd_delta_scan_bwd  backward (VJP) of the gated delta rule
     ssd_norm_fwd        layer or RMS norm of rows, with weight, bias and a silu gate
     ssd_norm_bwd        its backward, with the weights' reductions
+    ssd_glr_scan_fwd    the gated linear recurrence (one number of state a channel)
+    ssd_glr_step        one decode token of it per sequence
+    ssd_glr_scan_bwd    its backward (VJP)
 
 This module only marshals torch tensors (device pointers, row strides, the
 current HIP stream) into the library; every step of the computation runs in
@@ -38,6 +41,8 @@ __all__ = ["load", "ssd_conv_fwd", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_sta
            "ssd_conv_bwd_workspace_size", "ssd_mixer_bwd_workspace_size",
            "ssd_delta_scan_fwd", "ssd_delta_scan_workspace_size", "ssd_delta_scan_bwd",
            "ssd_delta_scan_bwd_workspace_size", "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
+           "ssd_glr_scan_fwd", "ssd_glr_scan_workspace_size", "ssd_glr_step", "ssd_glr_scan_bwd",
+           "ssd_glr_scan_bwd_workspace_size",
            "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_ACT_SILU", "SSD_ACT_NONE"]
 
 # SSD_LIBRARY names another build of the same library (the host-sanitized one the ABI checks use)
@@ -129,6 +134,17 @@ def load() -> ctypes.CDLL:
     lib.ssd_norm_bwd_workspace_size.argtypes = [I64, I, I]
     lib.ssd_s6_workspace_size.restype = SZ
     lib.ssd_s6_workspace_size.argtypes = [I, I, I, I, I]
+    # x, r, i, r_bias, i_bias, A: the shared head of the recurrence's calls
+    glr = [P, I64, P, I64, P, I64, P, P, P]
+    lib.ssd_glr_scan_fwd.restype = I
+    lib.ssd_glr_scan_fwd.argtypes = [I, I, I, I, *glr, P, P, P, P, P, P, I64, P, SZ, P]
+    lib.ssd_glr_step.restype = I
+    lib.ssd_glr_step.argtypes = [I, I, I, *glr, P, P, I64, P]
+    lib.ssd_glr_scan_bwd.restype = I
+    lib.ssd_glr_scan_bwd.argtypes = [I, I, I, I, *glr, P, P, P, P, P, I64, P, P, I64, P, I64, P, I64, P, P, P, P, P, SZ, P]
+    for nm in ("ssd_glr_scan_workspace_size", "ssd_glr_scan_bwd_workspace_size"):
+        getattr(lib, nm).restype = SZ
+        getattr(lib, nm).argtypes = [I, I, I, I]
     _lib = lib
     return lib
 
@@ -841,4 +857,95 @@ def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e
                              *at["x"], c.vec(weight, "weight", torch.float32, (W,)),
                              c.vec(bias, "bias", torch.float32, (W,)), *at["z"], *at["grad_y"], *at["dx"], out("weight"),
                              out("bias"), *at["dz"], c.ptr(ws, "workspace"), nb))
+    return g
+
+
+# ---- the gated linear recurrence
+def _glr_head(c, lead, T, D, x, r, i, A, r_bias, i_bias):
+    """The arguments that the recurrence's calls share; lead: the dimensions before the channels, (B, L) or (B,)."""
+    return [*c.rows(x, "x", T, lead + (D,)), *c.rows(r, "r", T, lead + (D,)), *c.rows(i, "i", T, lead + (D,)),
+            c.vec(r_bias, "r_bias", torch.float32, (D,)), c.vec(i_bias, "i_bias", torch.float32, (D,)),
+            c.vec(A, "A", torch.float32, (D,))]
+
+
+def ssd_glr_scan_workspace_size(B, L, D, dtype=SSD_BF16) -> int:
+    return int(load().ssd_glr_scan_workspace_size(B, L, D, dtype))
+
+
+@_on_stream
+def ssd_glr_scan_fwd(x, r, i, A, *, r_bias=None, i_bias=None, doc_ids=None, lengths=None, init_state=None,
+                     final_state=None, chunk_states=None, y=None, workspace=None):
+    """The gated linear recurrence h <- a h + sqrt(1 - a^2) sigmoid(i + i_bias) x, a = exp(sigmoid(r + r_bias) A).
+    x, r, i [B, L, D] (one dtype), A, r_bias, i_bias [D] fp32.  Returns y [B, L, D] in x's dtype (and writes final_state
+    [B, D] and chunk_states [B, ceil(L / 64), D], fp32, if given).  A workspace is allocated here when none is passed."""
+    lib = load()
+    c = _Call(x, "x")
+    dtype, T = _dtype_code(x, "x"), x.dtype
+    B, L, D = x.shape
+    head = _glr_head(c, (B, L), T, D, x, r, i, A, r_bias, i_bias)
+    if y is None:
+        y = torch.empty((B, L, D), dtype=T, device=c.dev)
+    yp, ys = c.rows(y, "y", T, (B, L, D))
+    need = ssd_glr_scan_workspace_size(B, L, D, dtype)
+    ws = _ws(workspace, need, c.dev) if need or workspace is not None else None
+    c.run(lib.ssd_glr_scan_fwd,
+          (B, L, D, dtype, *head, c.vec(doc_ids, "doc_ids", torch.int32, (B, L)),
+           c.vec(lengths, "lengths", torch.int32, (B,)), c.vec(init_state, "init_state", torch.float32, (B, D)),
+           c.vec(final_state, "final_state", torch.float32, (B, D)),
+           c.vec(chunk_states, "chunk_states", torch.float32, (B, -(-L // 64), D)), yp, ys, c.ptr(ws, "workspace"),
+           0 if ws is None else ws.numel() * ws.element_size()))
+    return y
+
+
+@_on_stream
+def ssd_glr_step(x, r, i, A, state, *, r_bias=None, i_bias=None, y=None):
+    """One token of the gated linear recurrence.  x, r, i [B, D] (one dtype), A, r_bias, i_bias [D] fp32; state [B, D]
+    fp32 is updated in place.  Returns y [B, D] in x's dtype."""
+    lib = load()
+    c = _Call(x, "x")
+    dtype, T = _dtype_code(x, "x"), x.dtype
+    B, D = x.shape
+    head = _glr_head(c, (B,), T, D, x, r, i, A, r_bias, i_bias)
+    if y is None:
+        y = torch.empty((B, D), dtype=T, device=c.dev)
+    yp, ys = c.rows(y, "y", T, (B, D))
+    c.run(lib.ssd_glr_step, (B, D, dtype, *head, c.vec(state, "state", torch.float32, (B, D)), yp, ys))
+    return y
+
+
+def ssd_glr_scan_bwd_workspace_size(B, L, D, dtype=SSD_BF16) -> int:
+    return int(load().ssd_glr_scan_bwd_workspace_size(B, L, D, dtype))
+
+
+@_on_stream
+def ssd_glr_scan_bwd(x, r, i, A, grad_y, *, r_bias=None, i_bias=None, doc_ids=None, lengths=None, init_state=None,
+                     grad_final_state=None, chunk_states=None, workspace=None):
+    """Backward of ssd_glr_scan_fwd; grad_y [B, L, D] in x's dtype, grad_final_state [B, D] fp32 or None, chunk_states as
+    the forward wrote them for these inputs (None: computed again).  Returns a dict: x, r, i in x's dtype, A [D] fp32, and
+    where those inputs are given r_bias, i_bias [D] and init_state [B, D] fp32.  A workspace is allocated here when none
+    is passed."""
+    lib = load()
+    c = _Call(x, "x")
+    dtype, T = _dtype_code(x, "x"), x.dtype
+    B, L, D = x.shape
+    head = _glr_head(c, (B, L), T, D, x, r, i, A, r_bias, i_bias)
+    gp, gs = c.rows(grad_y, "grad_y", T, (B, L, D))
+    f32, same = dict(dtype=torch.float32, device=c.dev), dict(dtype=T, device=c.dev)
+    g = {n: torch.empty(B, L, D, **same) for n in ("x", "r", "i")}
+    g["A"] = _params(B)(D, **f32)
+    if r_bias is not None:
+        g["r_bias"] = _params(B)(D, **f32)
+    if i_bias is not None:
+        g["i_bias"] = _params(B)(D, **f32)
+    if init_state is not None:
+        g["init_state"] = torch.empty(B, D, **f32)
+    ws = _ws(workspace, ssd_glr_scan_bwd_workspace_size(B, L, D, dtype), c.dev)
+    out = lambda n: g[n].data_ptr() if n in g else None  # noqa: E731
+    c.run(lib.ssd_glr_scan_bwd,
+          (B, L, D, dtype, *head, c.vec(doc_ids, "doc_ids", torch.int32, (B, L)),
+           c.vec(lengths, "lengths", torch.int32, (B,)), c.vec(init_state, "init_state", torch.float32, (B, D)),
+           c.vec(chunk_states, "chunk_states", torch.float32, (B, -(-L // 64), D)), gp, gs,
+           c.vec(grad_final_state, "grad_final_state", torch.float32, (B, D)), out("x"), D, out("r"), D, out("i"), D,
+           out("A"), out("r_bias"), out("i_bias"), out("init_state"), c.ptr(ws, "workspace"),
+           ws.numel() * ws.element_size()))
     return g

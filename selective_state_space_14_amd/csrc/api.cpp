@@ -1308,4 +1308,198 @@ int ssd_norm_bwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, 
     return hip_status(fn, ssd::launch_norm(a, s));
 }
 
+// ---- the gated linear recurrence
+// the grids: a workgroup for every chunk of 64 tokens and 128 channels, a thread for every state
+static bool glr_units_fit(int B, int L, int D) {
+    return (long long)B * D <= 0x7fffffffLL && (long long)B * (((long long)D + 127) / 128) <= 0x7fffffffLL / std::max(1LL, ((long long)L + 63) / 64);
+}
+
+static bool glr_has_work(int B, int L, int D) { return B > 0 && L > 0 && L <= kMaxL && D > 0 && glr_units_fit(B, L, D); }
+
+// `rows`: the activations of a call, the first three its inputs
+struct GlrRow { const char* name; const void* p; int64_t stride; };
+static int check_glr(const char* fn, ssd::GlrArgs& a, const GlrRow* rows, int n, bool work) {
+    if (a.dtype != SSD_F32 && a.dtype != SSD_BF16)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: dtype=%d is not supported (only SSD_F32=0 and SSD_BF16=1; "
+                    "fp16, fp64 and other types are refused, not converted)", fn, a.dtype);
+    if (a.B < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: B=%d must be >= 0", fn, a.B);
+    if (a.L < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: L=%d must be >= 0", fn, a.L);
+    if (a.L > kMaxL) return fail(SSD_ERR_BAD_SHAPE, "%s: L=%d is above the %d tokens a row may hold", fn, a.L, kMaxL);
+    if (a.D <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: D=%d must be > 0", fn, a.D);
+    if (!glr_units_fit(a.B, a.L, a.D))
+        return fail(SSD_ERR_BAD_SHAPE, "%s: B=%d rows of L=%d tokens and D=%d channels are too many", fn, a.B, a.L, a.D);
+    const int es = esize(a.dtype);
+    a.pair = a.D % 2 == 0;
+    a.vec = a.D % 8 == 0;
+    for (int i = 0; i < n; ++i) {
+        const GlrRow& r = rows[i];
+        if (!r.p) {
+            if (work) return fail(SSD_ERR_NULL_ARG, "%s: %s is NULL", fn, r.name);
+            continue;
+        }
+        if (r.stride < a.D)
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is smaller than the row width %d", fn, r.name,
+                        (long long)r.stride, a.D);
+        if (r.stride > (1 << 22))
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is above 4194304 elements", fn, r.name, (long long)r.stride);
+        if (reinterpret_cast<uintptr_t>(r.p) % es)
+            return fail(SSD_ERR_ALIGNMENT, "%s: %s=%p is not aligned to its elements", fn, r.name, r.p);
+        if (r.stride % 2 || reinterpret_cast<uintptr_t>(r.p) % (2 * es)) a.pair = 0;
+        if (!aligned16(r.p) || r.stride * es % 16) a.vec = 0;
+    }
+    TRY(check_ptr(fn, "A", a.A, a.B > 0, false));
+    TRY(check_ptr(fn, "r_bias", a.r_bias, false, false));
+    TRY(check_ptr(fn, "i_bias", a.i_bias, false, false));
+    TRY(check_ptr(fn, "doc_ids", a.doc, false, false));
+    TRY(check_ptr(fn, "lengths", a.lengths, false, false));
+    TRY(check_ptr(fn, "init_state", a.init_state, false, true));
+    TRY(check_ptr(fn, "chunk_states", a.states, false, true));
+    return SSD_OK;
+}
+
+static int check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+    if (need && (!workspace || bytes < need))
+        return fail(SSD_ERR_WORKSPACE, "%s: workspace_bytes=%zu is smaller than the required %zu", fn,
+                    workspace ? bytes : (size_t)0, need);
+    if (need && !aligned16(workspace))
+        return fail(SSD_ERR_ALIGNMENT, "%s: workspace=%p is not 16-byte aligned", fn, workspace);
+    return SSD_OK;
+}
+
+// no output is an input or another output
+static int check_apart(const char* fn, const void* const* outs, int no, const void* const* ins, int ni) {
+    for (int i = 0; i < no; ++i) {
+        if (!outs[i]) continue;
+        for (int k = 0; k < ni; ++k)
+            if (outs[i] == ins[k]) return fail(SSD_ERR_BAD_SHAPE, "%s: an output must not alias an input", fn);
+        for (int j = 0; j < i; ++j)
+            if (outs[i] == outs[j]) return fail(SSD_ERR_BAD_SHAPE, "%s: two outputs must not alias each other", fn);
+    }
+    return SSD_OK;
+}
+
+static ssd::GlrArgs glr_args(int B, int L, int D, int dtype, const void* x, int64_t x_stride, const void* r, int64_t r_stride,
+                             const void* i, int64_t i_stride, const float* r_bias, const float* i_bias, const float* A) {
+    ssd::GlrArgs a{};
+    a.B = B; a.L = L; a.D = D; a.dtype = dtype;
+    a.x = x; a.x_stride = x_stride;
+    a.r = r; a.r_stride = r_stride;
+    a.i = i; a.i_stride = i_stride;
+    a.r_bias = r_bias; a.i_bias = i_bias; a.A = A;
+    return a;
+}
+
+size_t ssd_glr_scan_workspace_size(int B, int L, int D, int dtype) {
+    if (!glr_has_work(B, L, D)) return 0;
+    return ssd::glr_fwd_workspace_bytes(B, L, D, dtype);
+}
+
+int ssd_glr_scan_fwd(int B, int L, int D, int dtype,
+                     const void* x, int64_t x_row_stride,
+                     const void* r, int64_t r_row_stride,
+                     const void* i, int64_t i_row_stride,
+                     const float* r_bias, const float* i_bias, const float* A,
+                     const int32_t* doc_ids, const int32_t* lengths,
+                     const float* init_state, float* final_state, float* chunk_states,
+                     void* y, int64_t y_row_stride,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssd_glr_scan_fwd";
+    ssd::GlrArgs a = glr_args(B, L, D, dtype, x, x_row_stride, r, r_row_stride, i, i_row_stride, r_bias, i_bias, A);
+    a.doc = doc_ids; a.lengths = lengths;
+    a.init_state = init_state; a.final_state = final_state; a.states = chunk_states;
+    a.y = y; a.y_stride = y_row_stride;
+    const bool work = B > 0 && L > 0;
+    const GlrRow rows[] = {{"x", x, x_row_stride}, {"r", r, r_row_stride}, {"i", i, i_row_stride}, {"y", y, y_row_stride}};
+    TRY(check_glr(fn, a, rows, 4, work));
+    TRY(check_ptr(fn, "final_state", final_state, false, true));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!work) {
+        if (final_state && final_state != init_state)
+            return hip_status(fn, ssd::launch_glr_copy(init_state, final_state, (int64_t)B * D, s));
+        return ok();
+    }
+    const void* outs[] = {y, chunk_states};
+    const void* ins[] = {x, r, i, A, r_bias, i_bias, init_state, final_state};
+    TRY(check_apart(fn, outs, 2, ins, 8));
+    TRY(check_workspace(fn, workspace, workspace_bytes, ssd_glr_scan_workspace_size(B, L, D, dtype)));
+    return hip_status(fn, ssd::launch_glr_fwd(a, workspace, s));
+}
+
+int ssd_glr_step(int B, int D, int dtype,
+                 const void* x, int64_t x_row_stride,
+                 const void* r, int64_t r_row_stride,
+                 const void* i, int64_t i_row_stride,
+                 const float* r_bias, const float* i_bias, const float* A,
+                 float* state, void* y, int64_t y_row_stride, void* stream) {
+    const char* fn = "ssd_glr_step";
+    ssd::GlrArgs a = glr_args(B, 1, D, dtype, x, x_row_stride, r, r_row_stride, i, i_row_stride, r_bias, i_bias, A);
+    a.final_state = state;
+    a.y = y; a.y_stride = y_row_stride;
+    const bool work = B > 0;
+    const GlrRow rows[] = {{"x", x, x_row_stride}, {"r", r, r_row_stride}, {"i", i, i_row_stride}, {"y", y, y_row_stride}};
+    TRY(check_glr(fn, a, rows, 4, work));
+    TRY(check_ptr(fn, "state", state, work, true));
+    if (!work) return ok();
+    const void* outs[] = {y, state};
+    const void* ins[] = {x, r, i, A, r_bias, i_bias};
+    TRY(check_apart(fn, outs, 2, ins, 6));
+    return hip_status(fn, ssd::launch_glr_step(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_glr_scan_bwd_workspace_size(int B, int L, int D, int dtype) {
+    if (!glr_has_work(B, L, D)) return 0;
+    return ssd::glr_bwd_workspace_bytes(B, L, D, dtype);
+}
+
+int ssd_glr_scan_bwd(int B, int L, int D, int dtype,
+                     const void* x, int64_t x_row_stride,
+                     const void* r, int64_t r_row_stride,
+                     const void* i, int64_t i_row_stride,
+                     const float* r_bias, const float* i_bias, const float* A,
+                     const int32_t* doc_ids, const int32_t* lengths,
+                     const float* init_state, const float* chunk_states,
+                     const void* grad_y, int64_t grad_y_row_stride, const float* grad_final_state,
+                     void* dx, int64_t dx_row_stride,
+                     void* dr, int64_t dr_row_stride,
+                     void* di, int64_t di_row_stride,
+                     float* dA, float* dr_bias, float* di_bias, float* grad_init_state,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssd_glr_scan_bwd";
+    ssd::GlrArgs a = glr_args(B, L, D, dtype, x, x_row_stride, r, r_row_stride, i, i_row_stride, r_bias, i_bias, A);
+    a.doc = doc_ids; a.lengths = lengths;
+    a.init_state = init_state; a.states = const_cast<float*>(chunk_states);
+    a.gy = grad_y; a.gy_stride = grad_y_row_stride; a.g_final = grad_final_state;
+    a.dx = dx; a.dx_stride = dx_row_stride;
+    a.dr = dr; a.dr_stride = dr_row_stride;
+    a.di = di; a.di_stride = di_row_stride;
+    a.dA = dA; a.dr_bias = dr_bias; a.di_bias = di_bias; a.g_init = grad_init_state;
+    const bool work = B > 0 && L > 0;
+    const GlrRow rows[] = {{"x", x, x_row_stride}, {"r", r, r_row_stride}, {"i", i, i_row_stride},
+                           {"grad_y", grad_y, grad_y_row_stride}, {"dx", dx, dx_row_stride}, {"dr", dr, dr_row_stride},
+                           {"di", di, di_row_stride}};
+    TRY(check_glr(fn, a, rows, 7, work));
+    TRY(check_ptr(fn, "dA", dA, B > 0, false));
+    TRY(check_ptr(fn, "dr_bias", dr_bias, false, false));
+    TRY(check_ptr(fn, "di_bias", di_bias, false, false));
+    TRY(check_ptr(fn, "grad_final_state", grad_final_state, false, true));
+    TRY(check_ptr(fn, "grad_init_state", grad_init_state, false, true));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const void* outs[] = {dx, dr, di, dA, dr_bias, di_bias, grad_init_state};
+    const void* ins[] = {x, r, i, A, r_bias, i_bias, init_state, chunk_states, grad_y, grad_final_state};
+    if (!work) {
+        if (B > 0) {
+            TRY(check_apart(fn, outs + 3, 4, ins + 3, 7));
+            TRY(hip_status(fn, ssd::launch_zero_f32(dA, (size_t)D, s)));
+            TRY(hip_status(fn, ssd::launch_zero_f32(dr_bias, (size_t)D, s)));
+            TRY(hip_status(fn, ssd::launch_zero_f32(di_bias, (size_t)D, s)));
+            if (grad_init_state)
+                return hip_status(fn, ssd::launch_glr_copy(grad_final_state, grad_init_state, (int64_t)B * D, s));
+        }
+        return ok();
+    }
+    TRY(check_apart(fn, outs, 7, ins, 10));
+    TRY(check_workspace(fn, workspace, workspace_bytes, ssd_glr_scan_bwd_workspace_size(B, L, D, dtype)));
+    return hip_status(fn, ssd::launch_glr_bwd(a, workspace, s));
+}
+
 }  // extern "C"

@@ -1,0 +1,601 @@
+// glr.hip -- the gated linear recurrence: one number of state per channel, with a gate on the decay and one on
+// the input.
+//
+//   s = sigmoid(r + r_bias),  g = sigmoid(i + i_bias),  a = exp(s A)          (A <= 0)
+//   h_t = a_t h_{t-1} + m_t g_t x_t,  m = sqrt(1 - a^2),  y_t = h_t
+//
+// and backward, from gy and the state after the row's last token:
+//   lam_t = gy_t + a_{t+1} lam_{t+1}
+//   dx = lam m g,  di = lam m x g (1 - g),  dl = lam (a h_{t-1} - g x a^2 / m),  dr = dl A s (1 - s)
+//   dA = sum dl s,  dr_bias = sum dr,  di_bias = sum di
+// (where m is 0 the second part of dl is taken as 0).
+//
+// A stretch of tokens maps the state that enters it to A h + H (A the product of its decays, H what it gathers from a
+// zero state), and two stretches after one another compose: A = A2 A1, H = A2 H1 + H2.  A tile is kWaves stretches, one a
+// wave, of Tw tokens by 128 channels; every lane keeps the decays and inputs of its two channels in registers, so that the
+// tokens are read once.  A tile's waves join in LDS.  Document starts and tokens behind a row's length are decays of 0 and
+// 1: chosen, not multiplied, so what stands there is not used.
+#include <algorithm>
+
+#include "ssd_device.hpp"
+#include "ssd_launch.hpp"
+
+namespace ssd {
+namespace {
+
+constexpr int kWaves = 8, kThreads = 64 * kWaves, kCols = 128;
+template <typename T> constexpr int kTw = sizeof(T) == 2 ? 16 : 8;      // tokens of a wave, forward
+template <typename T> constexpr int kTile = kTw<T> * kWaves;
+
+// ------------------------------------------------------------ a lane's two channels
+// PAIR: neighbours, read together (even widths and strides, bases on pairs); else 64 apart
+template <typename T, bool PAIR> struct Two;
+template <> struct Two<float, true> {
+    float2 v;
+    __device__ __forceinline__ void load(const float* p, int c, int) { v = *reinterpret_cast<const float2*>(p + c); }
+    __device__ __forceinline__ float get(int j) const { return j ? v.y : v.x; }
+    __device__ __forceinline__ static void store(float* p, int c, int, int, float a, float b) {
+        *reinterpret_cast<float2*>(p + c) = make_float2(a, b);
+    }
+};
+template <> struct Two<uint16_t, true> {
+    uint32_t v;
+    __device__ __forceinline__ void load(const uint16_t* p, int c, int) { v = *reinterpret_cast<const uint32_t*>(p + c); }
+    __device__ __forceinline__ float get(int j) const { return j ? bf16_hi(v) : bf16_lo(v); }
+    __device__ __forceinline__ static void store(uint16_t* p, int c, int, int, float a, float b) {
+        *reinterpret_cast<uint32_t*>(p + c) = pack_bf16x2(a, b);
+    }
+};
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
+__device__ __forceinline__ void narrow(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
+template <typename T> struct Two<T, false> {
+    T v[2];
+    // channels past the last are read from it
+    __device__ __forceinline__ void load(const T* p, int c, int last) {
+        v[0] = p[min(c, last)];
+        v[1] = p[min(c + 64, last)];
+    }
+    __device__ __forceinline__ float get(int j) const { return widen(v[j]); }
+    __device__ __forceinline__ static void store(T* p, int c, int, int D, float a, float b) {
+        if (c < D) narrow(p + c, a);
+        if (c + 64 < D) narrow(p + c + 64, b);
+    }
+};
+// the first of a lane's channels; a lane whose channels are all past D is off (PAIR: it reads the last pair)
+template <bool PAIR>
+struct Lane {
+    int c, last;
+    bool on;
+    __device__ __forceinline__ Lane(int blk, int D) {
+        const int l = threadIdx.x % 64;
+        c = blk * kCols + (PAIR ? 2 * l : l);
+        on = c < D;
+        last = D - 1;
+        if (PAIR) c = min(c, D - 2);
+    }
+};
+
+// ------------------------------------------------------------ the gates
+__device__ __forceinline__ float sigmoid_f(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
+
+// decay a = e^-n and 1 - a.  A decay near 1 is what a long memory rests on: there 1 - a comes from its series (7 terms,
+// off by n^7 / 8! of itself, 2e-8 at the border) and a from 1 - a by one rounding, so that neither the hardware exp2's
+// error nor the difference's shows: over thousands of tokens a decay that is off by one step the same way each time
+// would move the state by some 1e-5.  From the border on the hardware's exp2 and the difference are within 2^-22.
+__device__ __forceinline__ void decay(float n, float& a, float& om) {
+    float q = fmaf(n, -1.0f / 5040.0f, 1.0f / 720.0f);
+    q = fmaf(n, -q, 1.0f / 120.0f);
+    q = fmaf(n, -q, 1.0f / 24.0f);
+    q = fmaf(n, -q, 1.0f / 6.0f);
+    q = fmaf(n, -q, 0.5f);
+    q = fmaf(n, -q, 1.0f);
+    q *= n;
+    const float e = fast_exp2(-n * kLog2e);
+    a = n < 0.35f ? 1.0f - q : e;
+    om = n < 0.35f ? q : 1.0f - e;
+}
+
+// bit t set: a document starts at token t0 + t (t < n <= 64)
+__device__ __forceinline__ uint64_t starts_in(const int32_t* doc, int t0, int n, int L) {
+    if (!doc) return 0;
+    const int l = threadIdx.x % 64, t = t0 + l;
+    return __ballot(l < n && t > 0 && t < L && doc[max(min(t, L - 1), 0)] != doc[max(min(t, L - 1) - 1, 0)]);
+}
+
+struct Params {
+    float nA[2], rb[2], ib[2];
+    template <bool PAIR>
+    __device__ __forceinline__ void load(const GlrArgs& a, const Lane<PAIR>& ln) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = min(PAIR ? ln.c + j : ln.c + 64 * j, ln.last);
+            nA[j] = -a.A[c];
+            rb[j] = a.r_bias ? a.r_bias[c] : 0.0f;
+            ib[j] = a.i_bias ? a.i_bias[c] : 0.0f;
+        }
+    }
+};
+
+// the wave's number, known to the compiler to be the same for its lanes: rows are then addressed by scalars
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+
+// What a wave knows of its place: batch row, tile, first token, tokens that are real
+struct Place {
+    int b, c, blk, t0, len;
+    __device__ __forceinline__ Place(const GlrArgs& a, int id, int tile, int Tw) {
+        const int nblk = (a.D + kCols - 1) / kCols;
+        blk = id % nblk;
+        b = id / nblk % a.B;
+        c = id / nblk / a.B;
+        t0 = c * tile + wave_id() * Tw;
+        len = a.lengths ? max(0, min(a.lengths[b], a.L)) : a.L;
+    }
+};
+
+// decays and inputs of a wave's tokens, and their composition
+template <typename T, bool PAIR, int Tw>
+struct Stretch {
+    float a[Tw][2], v[Tw][2];
+    float A[2], H[2];
+    __device__ __forceinline__ void compute(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Params& w) {
+        Two<T, PAIR> x[Tw], r[Tw], i[Tw];
+        const T* xp = static_cast<const T*>(g.x);
+        const T* rp = static_cast<const T*>(g.r);
+        const T* ip = static_cast<const T*>(g.i);
+#pragma unroll
+        for (int t = 0; t < Tw; ++t) {
+            const int64_t row = (int64_t)p.b * g.L + min(p.t0 + t, g.L - 1);
+            x[t].load(xp + row * g.x_stride, ln.c, ln.last);
+            r[t].load(rp + row * g.r_stride, ln.c, ln.last);
+            i[t].load(ip + row * g.i_stride, ln.c, ln.last);
+        }
+        const uint64_t starts = starts_in(g.doc ? g.doc + (size_t)p.b * g.L : nullptr, p.t0, Tw, g.L);
+        A[0] = A[1] = 1.0f;
+        H[0] = H[1] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < Tw; ++t) {
+            const bool live = p.t0 + t < p.len, start = (starts >> t) & 1;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float d, om;
+                decay(sigmoid_f(r[t].get(j) + w.rb[j]) * w.nA[j], d, om);
+                const float in = __builtin_amdgcn_sqrtf(om * (1.0f + d)) * sigmoid_f(i[t].get(j) + w.ib[j]) * x[t].get(j);
+                a[t][j] = live ? (start ? 0.0f : d) : 1.0f;
+                v[t][j] = live ? in : 0.0f;
+                A[j] *= a[t][j];
+                H[j] = fmaf(a[t][j], H[j], v[t][j]);
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------ forward
+// agg: [tile][2][D] for every batch row, what a tile's tokens do to the state
+template <typename T, bool PAIR>
+__global__ __launch_bounds__(kThreads, 4) void ssd_glr_tiles_kernel(GlrArgs g, float* agg) {
+    constexpr int Tw = kTw<T>;
+    __shared__ float2 sA[kWaves][64], sH[kWaves][64];
+    const Place p(g, blockIdx.x, kTile<T>, Tw);
+    const Lane<PAIR> ln(p.blk, g.D);
+    Params w;
+    w.load(g, ln);
+    Stretch<T, PAIR, Tw> s;
+    s.compute(g, p, ln, w);
+    const int wave = wave_id(), l = threadIdx.x % 64;
+    sA[wave][l] = make_float2(s.A[0], s.A[1]);
+    sH[wave][l] = make_float2(s.H[0], s.H[1]);
+    __syncthreads();
+    if (wave || !ln.on) return;
+    float A[2] = {1.0f, 1.0f}, H[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) {
+        const float2 a = sA[k][l], h = sH[k][l];
+        A[0] *= a.x; A[1] *= a.y;
+        H[0] = fmaf(a.x, H[0], h.x);
+        H[1] = fmaf(a.y, H[1], h.y);
+    }
+    float* out = agg + ((size_t)p.b * g.tiles + p.c) * 2 * g.D;
+    Two<float, PAIR>::store(out, ln.c, 0, g.D, A[0], A[1]);
+    Two<float, PAIR>::store(out + g.D, ln.c, 0, g.D, H[0], H[1]);
+}
+
+// enter: [tile][D] for every batch row, the state that enters a tile (rev: the adjoint that enters it from behind)
+__global__ __launch_bounds__(256) void ssd_glr_fold_kernel(const float* agg, const float* first, float* enter, int B, int D, int tiles,
+                                                           int rev) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)B * D) return;
+    const int b = (int)(i / D), d = (int)(i % D);
+    float h = first ? first[i] : 0.0f;
+    for (int k = 0; k < tiles; ++k) {
+        const size_t c = (size_t)b * tiles + (rev ? tiles - 1 - k : k);
+        enter[c * D + d] = h;
+        h = fmaf(agg[c * 2 * D + d], h, agg[c * 2 * D + D + d]);
+    }
+}
+
+template <typename T, bool PAIR>
+__global__ __launch_bounds__(kThreads, 4) void ssd_glr_scan_kernel(GlrArgs g, const float* enter) {
+    constexpr int Tw = kTw<T>;
+    __shared__ float2 sA[kWaves][64], sH[kWaves][64];
+    const Place p(g, blockIdx.x, kTile<T>, Tw);
+    const Lane<PAIR> ln(p.blk, g.D);
+    Params w;
+    w.load(g, ln);
+    Stretch<T, PAIR, Tw> s;
+    s.compute(g, p, ln, w);
+    float h[2] = {0.0f, 0.0f};
+    if (enter || g.init_state) {
+        Two<float, PAIR> e;
+        e.load(enter ? enter + ((size_t)p.b * g.tiles + p.c) * g.D : g.init_state + (size_t)p.b * g.D, ln.c, ln.last);
+        h[0] = e.get(0);
+        h[1] = e.get(1);
+    }
+    const int wave = wave_id(), l = threadIdx.x % 64;
+    sA[wave][l] = make_float2(s.A[0], s.A[1]);
+    sH[wave][l] = make_float2(s.H[0], s.H[1]);
+    __syncthreads();                                 // init_state has been read: final_state may be it
+    for (int k = 0; k < wave; ++k) {
+        const float2 a = sA[k][l], v = sH[k][l];
+        h[0] = fmaf(a.x, h[0], v.x);
+        h[1] = fmaf(a.y, h[1], v.y);
+    }
+    if (!ln.on || p.t0 >= g.L) return;
+    if (g.states && p.t0 % 64 == 0)
+        Two<float, PAIR>::store(g.states + ((size_t)p.b * ((g.L + 63) / 64) + p.t0 / 64) * g.D, ln.c, 0, g.D, h[0], h[1]);
+    T* yp = static_cast<T*>(g.y);
+#pragma unroll
+    for (int t = 0; t < Tw; ++t) {
+        h[0] = fmaf(s.a[t][0], h[0], s.v[t][0]);
+        h[1] = fmaf(s.a[t][1], h[1], s.v[t][1]);
+        const bool live = p.t0 + t < p.len;
+        if (yp && p.t0 + t < g.L)
+            Two<T, PAIR>::store(yp + ((int64_t)p.b * g.L + p.t0 + t) * g.y_stride, ln.c, 0, g.D, live ? h[0] : 0.0f,
+                                live ? h[1] : 0.0f);
+    }
+    if (g.final_state && p.t0 + Tw >= g.L)
+        Two<float, PAIR>::store(g.final_state + (size_t)p.b * g.D, ln.c, 0, g.D, h[0], h[1]);
+}
+
+// ------------------------------------------------------------ backward
+constexpr int kTb = 8, kTileB = kTb * kWaves;         // tokens of a wave and of a tile: a chunk of 64
+static_assert(kTileB == 64, "a tile starts at a chunk's state");
+
+// What a wave needs of its tokens in both directions
+template <typename T, bool PAIR>
+struct Back {
+    Two<T, PAIR> x[kTb], gy[kTb];
+    float a[kTb][2], v[kTb][2], s[kTb][2], gi[kTb][2];    // carry decay, input (later a h_{t-1}), gates
+    float A[2], H[2], N[2];                               // compositions: of the state, and of the adjoint from behind
+    __device__ __forceinline__ void compute(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Params& w) {
+        Two<T, PAIR> r[kTb], i[kTb];
+        const T* xp = static_cast<const T*>(g.x);
+        const T* rp = static_cast<const T*>(g.r);
+        const T* ip = static_cast<const T*>(g.i);
+        const T* gp = static_cast<const T*>(g.gy);
+#pragma unroll
+        for (int t = 0; t < kTb; ++t) {
+            const int64_t row = (int64_t)p.b * g.L + min(p.t0 + t, g.L - 1);
+            x[t].load(xp + row * g.x_stride, ln.c, ln.last);
+            r[t].load(rp + row * g.r_stride, ln.c, ln.last);
+            i[t].load(ip + row * g.i_stride, ln.c, ln.last);
+            gy[t].load(gp + row * g.gy_stride, ln.c, ln.last);
+        }
+        const uint64_t starts = starts_in(g.doc ? g.doc + (size_t)p.b * g.L : nullptr, p.t0, kTb, g.L);
+        A[0] = A[1] = 1.0f;
+        H[0] = H[1] = N[0] = N[1] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < kTb; ++t) {
+            if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);  // not all tokens' gates at once: the registers again
+            const bool live = p.t0 + t < p.len, start = (starts >> t) & 1;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float d, om;
+                s[t][j] = sigmoid_f(r[t].get(j) + w.rb[j]);
+                gi[t][j] = sigmoid_f(i[t].get(j) + w.ib[j]);
+                decay(s[t][j] * w.nA[j], d, om);
+                const float in = __builtin_amdgcn_sqrtf(om * (1.0f + d)) * gi[t][j] * x[t].get(j);
+                a[t][j] = live ? (start ? 0.0f : d) : 1.0f;
+                v[t][j] = live ? in : 0.0f;
+                A[j] *= a[t][j];
+                H[j] = fmaf(a[t][j], H[j], v[t][j]);
+            }
+        }
+#pragma unroll
+        for (int t = kTb - 1; t >= 0; --t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) N[j] = a[t][j] * ((p.t0 + t < p.len ? gy[t].get(j) : 0.0f) + N[j]);
+    }
+};
+
+template <typename T, bool PAIR>
+__global__ __launch_bounds__(kThreads, 4) void ssd_glr_back_tiles_kernel(GlrArgs g, float* agg) {
+    __shared__ float2 sA[kWaves][64], sN[kWaves][64];
+    const Place p(g, blockIdx.x, kTileB, kTb);
+    const Lane<PAIR> ln(p.blk, g.D);
+    Params w;
+    w.load(g, ln);
+    Back<T, PAIR> s;
+    s.compute(g, p, ln, w);
+    const int wave = wave_id(), l = threadIdx.x % 64;
+    sA[wave][l] = make_float2(s.A[0], s.A[1]);
+    sN[wave][l] = make_float2(s.N[0], s.N[1]);
+    __syncthreads();
+    if (wave || !ln.on) return;
+    float A[2] = {1.0f, 1.0f}, N[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = kWaves - 1; k >= 0; --k) {
+        const float2 a = sA[k][l], n = sN[k][l];
+        A[0] *= a.x; A[1] *= a.y;
+        N[0] = fmaf(a.x, N[0], n.x);
+        N[1] = fmaf(a.y, N[1], n.y);
+    }
+    float* out = agg + ((size_t)p.b * g.tiles + p.c) * 2 * g.D;
+    Two<float, PAIR>::store(out, ln.c, 0, g.D, A[0], A[1]);
+    Two<float, PAIR>::store(out + g.D, ln.c, 0, g.D, N[0], N[1]);
+}
+
+// enter: the adjoint that enters every tile from behind.  part: [tile of all rows][3][D], a tile's sums of dA, dr_bias
+// and di_bias.
+template <typename T, bool PAIR>
+__global__ __launch_bounds__(kThreads, 4) void ssd_glr_back_kernel(GlrArgs g, const float* enter, float* part) {
+    __shared__ float2 sA[kWaves][64], sH[kWaves][64], sN[kWaves][64];
+    const Place p(g, blockIdx.x, kTileB, kTb);
+    const Lane<PAIR> ln(p.blk, g.D);
+    Params w;
+    w.load(g, ln);
+    Back<T, PAIR> s;
+    s.compute(g, p, ln, w);
+    const size_t tile = (size_t)p.b * g.tiles + p.c;
+    Two<float, PAIR> e, n;
+    e.load(g.states + tile * g.D, ln.c, ln.last);
+    n.load(enter + tile * g.D, ln.c, ln.last);
+    float h[2] = {e.get(0), e.get(1)}, nu[2] = {n.get(0), n.get(1)};
+    const int wave = wave_id(), l = threadIdx.x % 64;
+    sA[wave][l] = make_float2(s.A[0], s.A[1]);
+    sH[wave][l] = make_float2(s.H[0], s.H[1]);
+    sN[wave][l] = make_float2(s.N[0], s.N[1]);
+    __syncthreads();
+    for (int k = 0; k < wave; ++k) {
+        const float2 a = sA[k][l], v = sH[k][l];
+        h[0] = fmaf(a.x, h[0], v.x);
+        h[1] = fmaf(a.y, h[1], v.y);
+    }
+    for (int k = kWaves - 1; k > wave; --k) {
+        const float2 a = sA[k][l], v = sN[k][l];
+        nu[0] = fmaf(a.x, nu[0], v.x);
+        nu[1] = fmaf(a.y, nu[1], v.y);
+    }
+#pragma unroll
+    for (int t = 0; t < kTb; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float held = s.a[t][j] * h[j];
+            h[j] = held + s.v[t][j];
+            s.v[t][j] = held;
+            // the decays below are computed again from s: kept from above, they would not fit the registers
+            asm volatile("" : "+v"(s.s[t][j]));
+        }
+    T* dxp = static_cast<T*>(g.dx);
+    T* drp = static_cast<T*>(g.dr);
+    T* dip = static_cast<T*>(g.di);
+    float sum[3][2] = {};
+#pragma unroll
+    for (int t = kTb - 1; t >= 0; --t) {
+        const bool live = p.t0 + t < p.len;
+        float dx[2], dr[2], di[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float lam = (live ? s.gy[t].get(j) : 0.0f) + nu[j];
+            nu[j] = s.a[t][j] * lam;
+            float d, om;
+            decay(s.s[t][j] * w.nA[j], d, om);
+            const float m2 = om * (1.0f + d), inv = m2 > 0.0f ? __builtin_amdgcn_rsqf(m2) : 0.0f;
+            const float x = s.x[t].get(j), gi = s.gi[t][j], lm = lam * m2 * inv;
+            dx[j] = live ? lm * gi : 0.0f;
+            di[j] = live ? lm * x * gi * (1.0f - gi) : 0.0f;
+            const float dl = live ? lam * (s.v[t][j] - gi * x * d * d * inv) : 0.0f;
+            dr[j] = live ? -dl * w.nA[j] * s.s[t][j] * (1.0f - s.s[t][j]) : 0.0f;
+            sum[0][j] = live ? fmaf(dl, s.s[t][j], sum[0][j]) : sum[0][j];
+            sum[1][j] += dr[j];
+            sum[2][j] += di[j];
+        }
+        if (ln.on && p.t0 + t < g.L) {
+            const int64_t row = (int64_t)p.b * g.L + p.t0 + t;
+            Two<T, PAIR>::store(dxp + row * g.dx_stride, ln.c, 0, g.D, dx[0], dx[1]);
+            Two<T, PAIR>::store(drp + row * g.dr_stride, ln.c, 0, g.D, dr[0], dr[1]);
+            Two<T, PAIR>::store(dip + row * g.di_stride, ln.c, 0, g.D, di[0], di[1]);
+        }
+    }
+    if (g.g_init && p.t0 == 0 && ln.on)
+        Two<float, PAIR>::store(g.g_init + (size_t)p.b * g.D, ln.c, 0, g.D, nu[0], nu[1]);
+    // the waves' sums in their order
+    __syncthreads();
+    sA[wave][l] = make_float2(sum[0][0], sum[0][1]);
+    sH[wave][l] = make_float2(sum[1][0], sum[1][1]);
+    sN[wave][l] = make_float2(sum[2][0], sum[2][1]);
+    __syncthreads();
+    if (wave >= 3 || !ln.on) return;
+    const float2(*from)[64] = wave == 0 ? sA : wave == 1 ? sH : sN;
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) {
+        a += from[k][l].x;
+        b += from[k][l].y;
+    }
+    Two<float, PAIR>::store(part + (tile * 3 + wave) * g.D, ln.c, 0, g.D, a, b);
+}
+
+// dA, dr_bias and di_bias: the tiles' sums in a fixed order, in 64 bits.  32 columns a workgroup, 32 threads a column.
+__global__ __launch_bounds__(1024) void ssd_glr_sum_kernel(const float* part, int64_t rows, int D, float* dA, float* dr_bias,
+                                                           float* di_bias) {
+    __shared__ double s[32][33];
+    const int x = threadIdx.x % 32, k = threadIdx.x / 32, c = blockIdx.x * 32 + x;
+    double v = 0.0;
+    if (c < 3 * D)
+        for (int64_t r = k; r < rows; r += 32) v += part[r * 3 * D + c];
+    s[k][x] = v;
+    __syncthreads();
+    if (k || c >= 3 * D) return;
+    double t = 0.0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += s[i][x];
+    if (c < D) dA[c] = (float)t;
+    else if (c < 2 * D) {
+        if (dr_bias) dr_bias[c - D] = (float)t;
+    } else if (di_bias) di_bias[c - 2 * D] = (float)t;
+}
+
+// to = from, or 0 where there is none: a state through a row of no tokens
+__global__ __launch_bounds__(256) void ssd_glr_copy_kernel(const float* from, float* to, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) to[i] = from ? from[i] : 0.0f;
+}
+
+// ------------------------------------------------------------ one token
+// V channels a thread: 8 where every row and state starts on a 16-byte boundary and D % 8 == 0, else 1.  Bound by HBM:
+// 8 bytes of state and four activations a channel.
+template <typename T, int V> __device__ __forceinline__ void step_ld(const T* p, float (&o)[V]) {
+    if constexpr (V == 1) {
+        o[0] = widen(*p);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        o[0] = bf16_lo(v.x); o[1] = bf16_hi(v.x); o[2] = bf16_lo(v.y); o[3] = bf16_hi(v.y);
+        o[4] = bf16_lo(v.z); o[5] = bf16_hi(v.z); o[6] = bf16_lo(v.w); o[7] = bf16_hi(v.w);
+    } else {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    }
+}
+template <typename T, int V> __device__ __forceinline__ void step_st(T* p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        narrow(p, v[0]);
+    } else if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+template <typename T, int V>
+__global__ __launch_bounds__(256) void ssd_glr_step_kernel(GlrArgs g) {
+    const int n = g.D / V;                           // V > 1: D % 8 == 0
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= (int64_t)g.B * n) return;
+    const int b = (int)(at / n), c = (int)(at % n) * V;
+    float x[V], r[V], i[V], A[V], rb[V], ib[V], h[V];
+    step_ld<T, V>(static_cast<const T*>(g.x) + b * g.x_stride + c, x);
+    step_ld<T, V>(static_cast<const T*>(g.r) + b * g.r_stride + c, r);
+    step_ld<T, V>(static_cast<const T*>(g.i) + b * g.i_stride + c, i);
+    float* state = g.final_state + (int64_t)b * g.D + c;
+    step_ld<float, V>(state, h);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        A[j] = g.A[c + j];
+        rb[j] = g.r_bias ? g.r_bias[c + j] : 0.0f;
+        ib[j] = g.i_bias ? g.i_bias[c + j] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float d, om;
+        decay(-sigmoid_f(r[j] + rb[j]) * A[j], d, om);
+        h[j] = fmaf(d, h[j], __builtin_amdgcn_sqrtf(om * (1.0f + d)) * sigmoid_f(i[j] + ib[j]) * x[j]);
+    }
+    step_st<float, V>(state, h);
+    step_st<T, V>(static_cast<T*>(g.y) + b * g.y_stride + c, h);
+}
+
+int cols(int D) { return (D + kCols - 1) / kCols; }
+int tiles_of(int L, int tile) { return (int)(((int64_t)L + tile - 1) / tile); }
+size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
+
+template <typename T, bool PAIR>
+hipError_t fwd_t(GlrArgs a, void* ws, hipStream_t s) {
+    a.tiles = tiles_of(a.L, kTile<T>);
+    const dim3 grid((unsigned)(a.tiles * (int64_t)a.B * cols(a.D)));
+    float *agg = static_cast<float*>(ws), *enter = nullptr;
+    if (a.tiles > 1) {
+        enter = agg + (size_t)a.B * a.tiles * 2 * a.D;
+        hipLaunchKernelGGL((ssd_glr_tiles_kernel<T, PAIR>), grid, dim3(kThreads), 0, s, a, agg);
+        if (hipError_t e = hipGetLastError()) return e;
+        hipLaunchKernelGGL(ssd_glr_fold_kernel, dim3((unsigned)(((int64_t)a.B * a.D + 255) / 256)), dim3(256), 0, s, agg,
+                           a.init_state, enter, a.B, a.D, a.tiles, 0);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    hipLaunchKernelGGL((ssd_glr_scan_kernel<T, PAIR>), grid, dim3(kThreads), 0, s, a, enter);
+    return hipGetLastError();
+}
+
+size_t fwd_bytes(int B, int L, int D, int dtype) {
+    const int tiles = tiles_of(L, dtype == 0 ? kTile<float> : kTile<uint16_t>);
+    return tiles > 1 ? pad16((size_t)B * tiles * 3 * D * sizeof(float)) : 0;
+}
+size_t states_bytes(int B, int L, int D) { return pad16((size_t)B * tiles_of(L, kTileB) * D * sizeof(float)); }
+
+template <typename T, bool PAIR>
+hipError_t bwd_t(GlrArgs a, void* ws, hipStream_t s) {
+    char* at = static_cast<char*>(ws);
+    if (!a.states) {
+        a.states = reinterpret_cast<float*>(at);
+        at += states_bytes(a.B, a.L, a.D);
+        GlrArgs f = a;
+        f.y = nullptr;
+        f.final_state = nullptr;
+        if (hipError_t e = fwd_t<T, PAIR>(f, at, s)) return e;
+        at += fwd_bytes(a.B, a.L, a.D, a.dtype);
+    }
+    a.tiles = tiles_of(a.L, kTileB);
+    const size_t n = (size_t)a.B * a.tiles * a.D;
+    float* agg = reinterpret_cast<float*>(at);
+    float *enter = agg + 2 * n, *part = enter + n;
+    const dim3 grid((unsigned)(a.tiles * (int64_t)a.B * cols(a.D)));
+    hipLaunchKernelGGL((ssd_glr_back_tiles_kernel<T, PAIR>), grid, dim3(kThreads), 0, s, a, agg);
+    if (hipError_t e = hipGetLastError()) return e;
+    hipLaunchKernelGGL(ssd_glr_fold_kernel, dim3((unsigned)(((int64_t)a.B * a.D + 255) / 256)), dim3(256), 0, s, agg, a.g_final,
+                       enter, a.B, a.D, a.tiles, 1);
+    if (hipError_t e = hipGetLastError()) return e;
+    hipLaunchKernelGGL((ssd_glr_back_kernel<T, PAIR>), grid, dim3(kThreads), 0, s, a, enter, part);
+    if (hipError_t e = hipGetLastError()) return e;
+    hipLaunchKernelGGL(ssd_glr_sum_kernel, dim3((unsigned)((3LL * a.D + 31) / 32)), dim3(1024), 0, s, part,
+                       (int64_t)a.B * a.tiles, a.D, a.dA, a.dr_bias, a.di_bias);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t glr_fwd_workspace_bytes(int B, int L, int D, int dtype) { return fwd_bytes(B, L, D, dtype); }
+size_t glr_bwd_workspace_bytes(int B, int L, int D, int dtype) {
+    const size_t n = (size_t)B * tiles_of(L, kTileB) * D * sizeof(float);
+    return states_bytes(B, L, D) + fwd_bytes(B, L, D, dtype) + 6 * n;
+}
+
+hipError_t launch_glr_fwd(const GlrArgs& a, void* ws, hipStream_t s) {
+    if (a.dtype == 0) return a.pair ? fwd_t<float, true>(a, ws, s) : fwd_t<float, false>(a, ws, s);
+    return a.pair ? fwd_t<uint16_t, true>(a, ws, s) : fwd_t<uint16_t, false>(a, ws, s);
+}
+hipError_t launch_glr_bwd(const GlrArgs& a, void* ws, hipStream_t s) {
+    if (a.dtype == 0) return a.pair ? bwd_t<float, true>(a, ws, s) : bwd_t<float, false>(a, ws, s);
+    return a.pair ? bwd_t<uint16_t, true>(a, ws, s) : bwd_t<uint16_t, false>(a, ws, s);
+}
+hipError_t launch_glr_copy(const float* from, float* to, int64_t n, hipStream_t s) {
+    if (n == 0) return hipSuccess;
+    hipLaunchKernelGGL(ssd_glr_copy_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, from, to, n);
+    return hipGetLastError();
+}
+hipError_t launch_glr_step(const GlrArgs& a, hipStream_t s) {
+    const int64_t n = (int64_t)a.B * (a.vec ? a.D / 8 : a.D);
+    const dim3 grid((unsigned)((n + 255) / 256));
+    if (a.dtype == 0) {
+        if (a.vec) hipLaunchKernelGGL((ssd_glr_step_kernel<float, 8>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((ssd_glr_step_kernel<float, 1>), grid, dim3(256), 0, s, a);
+    } else {
+        if (a.vec) hipLaunchKernelGGL((ssd_glr_step_kernel<uint16_t, 8>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((ssd_glr_step_kernel<uint16_t, 1>), grid, dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace ssd

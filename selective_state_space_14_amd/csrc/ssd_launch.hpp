@@ -185,6 +185,31 @@ struct DeltaBwdArgs {
     float* g_init;                         // [B][H][P][N] or null
 };
 
+// Gated linear recurrence: forward (gy = null), one token (final_state in place) and backward.
+struct GlrArgs {
+    int B, L, D, dtype;
+    int pair;                              // even widths and strides, bases on pairs: two channels a load
+    int vec;                               // the step: 16-byte rows and D % 8 == 0
+    int tiles;                             // set by the launchers
+    const void* x; int64_t x_stride;       // [B][L][D] (dtype)
+    const void* r; int64_t r_stride;
+    const void* i; int64_t i_stride;
+    const float* A;                        // [D]
+    const float* r_bias; const float* i_bias;      // [D] or null
+    const int32_t* doc; const int32_t* lengths;
+    const float* init_state; float* final_state;   // [B][D]
+    float* states;                         // [B][chunks of 64][D]: the states entering them, or null
+    void* y; int64_t y_stride;             // null in the backward's own forward pass
+    // backward
+    const void* gy; int64_t gy_stride;
+    const float* g_final;                  // [B][D] or null
+    void* dx; int64_t dx_stride;
+    void* dr; int64_t dr_stride;
+    void* di; int64_t di_stride;
+    float* dA; float* dr_bias; float* di_bias;     // [D]; the biases' or null
+    float* g_init;                         // [B][D] or null
+};
+
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_scan(const ScanArgs& a, hipStream_t stream);
 // Sequence split chosen for these sizes (1 = none) and its superchunk length.
@@ -228,6 +253,13 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, void* ws, hipStream_t stream)
 hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 size_t norm_bwd_workspace_bytes(int64_t R, int W);
+size_t glr_fwd_workspace_bytes(int B, int L, int D, int dtype);
+hipError_t launch_glr_fwd(const GlrArgs& a, void* ws, hipStream_t stream);
+size_t glr_bwd_workspace_bytes(int B, int L, int D, int dtype);
+hipError_t launch_glr_bwd(const GlrArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_glr_step(const GlrArgs& a, hipStream_t stream);
+// n floats from `from` (null: zeros)
+hipError_t launch_glr_copy(const float* from, float* to, int64_t n, hipStream_t stream);
 void s6_split(int B, int L, int D, int& K, int& S);
 size_t s6_workspace_bytes(int B, int L, int D, int N);
 
