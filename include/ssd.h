@@ -1,7 +1,7 @@
 /*
  * ssd.h -- C ABI of libssd.so, the gfx950 (MI355X) Mamba-2 SSD mixer core.
  *
- * Seventeen operations, each a few HIP kernel launches on the caller's stream:
+ * Nineteen operations, each a few HIP kernel launches on the caller's stream:
  *
  *   ssd_conv_fwd        causal depthwise conv (k = 4) + SiLU over the
  *                       [x | B | C] columns, and dt = softplus(dt_raw + dt_bias)
@@ -28,6 +28,8 @@
  *   ssd_glr_scan_fwd    the gated linear recurrence (a state a channel)
  *   ssd_glr_step        one decode token of it per sequence
  *   ssd_glr_scan_bwd    backward (VJP) of ssd_glr_scan_fwd
+ *   ssd_add_norm_fwd    the norm with a residual's addition and an 8-bit output
+ *   ssd_add_norm_bwd    backward of ssd_add_norm_fwd
  *
  * The operation (per batch row b and head h, token t, head h in group
  * g = h / (H/G)):
@@ -850,6 +852,60 @@ int ssd_glr_scan_bwd(int B, int L, int D, int dtype,
 
 /* Bytes of workspace of ssd_glr_scan_bwd, with the states' recomputation. */
 size_t ssd_glr_scan_bwd_workspace_size(int B, int L, int D, int dtype);
+
+/*
+ * ssd_add_norm_fwd -- the norm at a layer's entry and end: a residual added
+ * before it, an 8-bit output with scales behind it, for R rows of W columns.
+ *     s = x + residual  (rounded to the residual's type), or x without one
+ *     n = norm(s) as in ssd_norm_fwd
+ *     y = (n * weight + bias) * silu(z)
+ *     q = e4m3(y / scale),  scale = max|y| / 448 over every 128 columns
+ *   x       f32 or bf16 (x_dtype) [R][W]
+ *   residual, sum  f32 or bf16 (residual_dtype) [R][W] or NULL; sum = s is
+ *               written where given, and may be the residual itself, or x of
+ *               the same type (with its row stride): in place
+ *   weight, bias  f32 [W] or NULL; z T [R][W] or NULL
+ *   y       T   [R][W] or NULL
+ *   q       OCP e4m3 [R][W] or NULL; q_scale f32 [R][ceil(W / 128)], given
+ *               with q: y stands for q * q_scale of its block, the last block
+ *               of a row the rest of its columns
+ * At least one of y and q is given.  q is rounded (to nearest even) from
+ * fp32, not from y.  A block of zeros has scale 1; max|y| counts at least
+ * 2^-100 and at most the largest fp32, so an infinity saturates; a NaN
+ * becomes NaN and does not choose the scale.  Rows, W, alignment and eps as
+ * in ssd_norm_fwd; rows whose bases and strides are multiples of 16 bytes (q:
+ * 8) and W % 8 == 0 are read and written in pieces.
+ */
+int ssd_add_norm_fwd(int64_t R, int W, int x_dtype, int residual_dtype, int dtype, int rms, float eps,
+                     const void *x, int64_t x_row_stride,
+                     const void *residual, int64_t residual_row_stride,
+                     const float *weight, const float *bias,
+                     const void *z, int64_t z_row_stride,
+                     void *sum, int64_t sum_row_stride,
+                     void *y, int64_t y_row_stride,
+                     void *q, int64_t q_row_stride, float *q_scale, int64_t q_scale_row_stride, void *stream);
+
+/*
+ * ssd_add_norm_bwd -- backward of ssd_add_norm_fwd (of y; for the 8-bit
+ * output its rounding counts as the identity), from the stored sum:
+ *     dsum = the gradient of ssd_norm_bwd's dx for sum + grad_sum
+ * and dweight, dbias, dz as there.  dsum is the gradient of x and of the
+ * residual alike.
+ *   sum, grad_sum, dsum  f32 or bf16 (sum_dtype) [R][W]; grad_sum, what
+ *               reaches the sum past the norm, or NULL (zero); dsum may be
+ *               grad_sum itself (with its row stride)
+ *   grad_y  T   [R][W];  dz T, NULL or given with z
+ *   workspace   ssd_norm_bwd_workspace_size(R, 1, W) bytes, required where
+ *               dweight or dbias is given
+ */
+int ssd_add_norm_bwd(int64_t R, int W, int sum_dtype, int dtype, int rms, float eps,
+                     const void *sum, int64_t sum_row_stride, const float *weight, const float *bias,
+                     const void *z, int64_t z_row_stride,
+                     const void *grad_y, int64_t grad_y_row_stride,
+                     const void *grad_sum, int64_t grad_sum_row_stride,
+                     void *dsum, int64_t dsum_row_stride, float *dweight, float *dbias,
+                     void *dz, int64_t dz_row_stride,
+                     void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,8 @@ The entry points mirror the C ABI in include/ssd.h one to one:
     ssd_glr_scan_fwd    the gated linear recurrence (one number of state a channel)
     ssd_glr_step        one decode token of it per sequence
     ssd_glr_scan_bwd    its backward (VJP)
+    ssd_add_norm_fwd    layer or RMS norm with a residual's addition and an 8-bit output with scales
+    ssd_add_norm_bwd    its backward
 
 This module only marshals torch tensors (device pointers, row strides, the
 current HIP stream) into the library; every step of the computation runs in
@@ -42,7 +44,7 @@ __all__ = ["load", "ssd_conv_fwd", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_sta
            "ssd_delta_scan_fwd", "ssd_delta_scan_workspace_size", "ssd_delta_scan_bwd",
            "ssd_delta_scan_bwd_workspace_size", "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
            "ssd_glr_scan_fwd", "ssd_glr_scan_workspace_size", "ssd_glr_step", "ssd_glr_scan_bwd",
-           "ssd_glr_scan_bwd_workspace_size",
+           "ssd_glr_scan_bwd_workspace_size", "ssd_add_norm_fwd", "ssd_add_norm_bwd",
            "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_ACT_SILU", "SSD_ACT_NONE"]
 
 # SSD_LIBRARY names another build of the same library (the host-sanitized one the ABI checks use)
@@ -145,6 +147,10 @@ def load() -> ctypes.CDLL:
     for nm in ("ssd_glr_scan_workspace_size", "ssd_glr_scan_bwd_workspace_size"):
         getattr(lib, nm).restype = SZ
         getattr(lib, nm).argtypes = [I, I, I, I]
+    lib.ssd_add_norm_fwd.restype = I
+    lib.ssd_add_norm_fwd.argtypes = [I64, I, I, I, I, I, F, P, I64, P, I64, P, P, P, I64, P, I64, P, I64, P, I64, P, I64, P]
+    lib.ssd_add_norm_bwd.restype = I
+    lib.ssd_add_norm_bwd.argtypes = [I64, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P, I64, P, I64, P, P, P, I64, P, SZ, P]
     _lib = lib
     return lib
 
@@ -948,4 +954,77 @@ def ssd_glr_scan_bwd(x, r, i, A, grad_y, *, r_bias=None, i_bias=None, doc_ids=No
            c.vec(grad_final_state, "grad_final_state", torch.float32, (B, D)), out("x"), D, out("r"), D, out("i"), D,
            out("A"), out("r_bias"), out("i_bias"), out("init_state"), c.ptr(ws, "workspace"),
            ws.numel() * ws.element_size()))
+    return g
+
+
+# ---- the norm with the residual's addition and 8-bit output
+def _lead_rows(shape):
+    n = 1
+    for s in shape[:-1]:
+        n *= s
+    return n
+
+
+@_on_stream
+def ssd_add_norm_fwd(x, residual=None, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, out_dtype=None, want_y=True,
+                     want_q=False, sum=None, y=None, q=None, q_scale=None):
+    """Norm of x + residual, times weight plus bias, times silu(z), in the output's type and in 8 bits.  x, residual
+    [..., W] fp32 or bf16, weight, bias fp32 [W], z in the output's dtype, which is y's, else out_dtype, else z's, else
+    x's.  Returns a dict: "sum" in the residual's dtype where there is one, "y" unless want_y is false, and with want_q
+    "q" (float8_e4m3fn) and "scale" (fp32 [..., ceil(W / 128)]).  Outputs may be given: sum (the residual itself: in
+    place), y, q, q_scale."""
+    lib = load()
+    c = _Call(x, "x")
+    shape, W = x.shape, x.shape[-1]
+    T = y.dtype if y is not None else out_dtype or (x.dtype if z is None else z.dtype)
+    if (want_y or y is not None) and y is None:
+        y = torch.empty(shape, dtype=T, device=c.dev)
+    blocks = shape[:-1] + (-(-W // 128),)
+    if want_q or q is not None or q_scale is not None:
+        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=c.dev) if q is None else q
+        q_scale = torch.empty(blocks, dtype=torch.float32, device=c.dev) if q_scale is None else q_scale
+    RT = x.dtype if residual is None else residual.dtype
+    if residual is not None and sum is None:
+        sum = torch.empty(shape, dtype=RT, device=c.dev)
+    out = {n: t for n, t in (("sum", sum), ("y", y), ("q", q), ("scale", q_scale)) if t is not None}
+    if x.numel() == 0:
+        return out
+    code = SSD_F32 if T == torch.float32 else SSD_BF16 if T == torch.bfloat16 else -1
+    c.run(lib.ssd_add_norm_fwd,
+          (_lead_rows(shape), W, _dtype_code(x, "x"), _dtype_code(x if residual is None else residual, "residual"), code,
+           int(bool(rms)), float(eps), *c.rows(x, "x", None, shape), *c.rows(residual, "residual", None, shape),
+           c.vec(weight, "weight", torch.float32, (W,)), c.vec(bias, "bias", torch.float32, (W,)), *c.rows(z, "z", T, shape),
+           *c.rows(sum, "sum", RT, shape), *c.rows(y, "y", T, shape), *c.rows(q, "q", torch.float8_e4m3fn, shape),
+           *c.rows(q_scale, "q_scale", torch.float32, blocks)))
+    return out
+
+
+@_on_stream
+def ssd_add_norm_bwd(sum, grad_y, grad_sum=None, weight=None, *, bias=None, z=None, rms=False, eps=1e-5, workspace=None):
+    """Backward of ssd_add_norm_fwd from its sum; grad_y (and z) in the output's dtype, grad_sum, what reaches the sum past
+    the norm, in sum's.  Returns a dict: sum (the gradient of x and of the residual alike) in sum's dtype, weight and bias
+    fp32 [W] and z in z's dtype, where those inputs are given.  A workspace is allocated here when none is passed."""
+    lib = load()
+    c = _Call(sum, "sum")
+    shape, W, T = sum.shape, sum.shape[-1], grad_y.dtype
+    R = _lead_rows(shape)
+    f32 = dict(dtype=torch.float32, device=c.dev)
+    g = {"sum": torch.empty(shape, dtype=sum.dtype, device=c.dev)}
+    if weight is not None:
+        g["weight"] = torch.empty(W, **f32)
+    if bias is not None:
+        g["bias"] = torch.empty(W, **f32)
+    if z is not None:
+        g["z"] = torch.empty(shape, dtype=T, device=c.dev)
+    ws, nb = None, 0
+    if weight is not None or bias is not None:
+        ws = _ws(workspace, ssd_norm_bwd_workspace_size(R, 1, W), c.dev)
+        nb = ws.numel() * ws.element_size()
+    out = lambda n: g[n].data_ptr() if n in g else None  # noqa: E731
+    c.run(lib.ssd_add_norm_bwd,
+          (R, W, _dtype_code(sum, "sum"), _dtype_code(grad_y, "grad_y"), int(bool(rms)), float(eps),
+           *c.rows(sum, "sum", None, shape), c.vec(weight, "weight", torch.float32, (W,)),
+           c.vec(bias, "bias", torch.float32, (W,)), *c.rows(z, "z", T, shape), *c.rows(grad_y, "grad_y", T, shape),
+           *c.rows(grad_sum, "grad_sum", sum.dtype, shape), out("sum"), W, out("weight"), out("bias"), out("z"), W,
+           c.ptr(ws, "workspace"), nb))
     return g

@@ -1502,4 +1502,150 @@ int ssd_glr_scan_bwd(int B, int L, int D, int dtype,
     return hip_status(fn, ssd::launch_glr_bwd(a, workspace, s));
 }
 
+// ---- the norm with the residual's addition and 8-bit output
+// a row operand: es = 1 for 8-bit values, whose rows in vectors are 8 bytes
+struct NormRow { const char* name; const void* p; int64_t stride; int es; bool required; };
+static int check_norm_rows(const char* fn, const NormRow* rows, int n, int64_t width, int& vec) {
+    for (int i = 0; i < n; ++i) {
+        const NormRow& r = rows[i];
+        if (!r.p) {
+            if (r.required) return fail(SSD_ERR_NULL_ARG, "%s: %s is NULL", fn, r.name);
+            continue;
+        }
+        if (r.stride < width)
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is smaller than the row width %lld", fn, r.name,
+                        (long long)r.stride, (long long)width);
+        if (r.stride > (1 << 22))
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is above 4194304 elements", fn, r.name,
+                        (long long)r.stride);
+        if (reinterpret_cast<uintptr_t>(r.p) % r.es)
+            return fail(SSD_ERR_ALIGNMENT, "%s: %s=%p is not aligned to its elements", fn, r.name, r.p);
+        const int piece = r.es == 1 ? 8 : 16;
+        if (reinterpret_cast<uintptr_t>(r.p) % piece || r.stride * r.es % piece) vec = 0;
+    }
+    return SSD_OK;
+}
+static int check_norm_dims(const char* fn, int64_t R, int W, int rms, float eps, const int* dtypes, int nd) {
+    for (int i = 0; i < nd; ++i)
+        if (dtypes[i] != SSD_F32 && dtypes[i] != SSD_BF16)
+            return fail(SSD_ERR_UNSUPPORTED, "%s: dtype=%d is not supported (only SSD_F32=0 and SSD_BF16=1; "
+                        "fp16, fp64 and other types are refused, not converted)", fn, dtypes[i]);
+    if (R < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: R=%lld must be >= 0", fn, (long long)R);
+    if (R > 0x7fffffffLL) return fail(SSD_ERR_BAD_SHAPE, "%s: R=%lld rows are too many", fn, (long long)R);
+    if (W <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: W=%d must be > 0", fn, W);
+    if (W > 16384) return fail(SSD_ERR_UNSUPPORTED, "%s: W=%d is not supported (at most 16384 columns)", fn, W);
+    if (rms != 0 && rms != 1) return fail(SSD_ERR_UNSUPPORTED, "%s: rms=%d must be 0 or 1", fn, rms);
+    if (!(eps >= 0.0f)) return fail(SSD_ERR_UNSUPPORTED, "%s: eps=%g must be >= 0", fn, (double)eps);
+    return SSD_OK;
+}
+
+int ssd_add_norm_fwd(int64_t R, int W, int x_dtype, int residual_dtype, int dtype, int rms, float eps,
+                     const void* x, int64_t x_row_stride,
+                     const void* residual, int64_t residual_row_stride,
+                     const float* weight, const float* bias,
+                     const void* z, int64_t z_row_stride,
+                     void* sum, int64_t sum_row_stride,
+                     void* y, int64_t y_row_stride,
+                     void* q, int64_t q_row_stride, float* q_scale, int64_t q_scale_row_stride, void* stream) {
+    const char* fn = "ssd_add_norm_fwd";
+    const int dtypes[] = {x_dtype, residual_dtype, dtype};
+    TRY(check_norm_dims(fn, R, W, rms, eps, dtypes, 3));
+    ssd::AddNormArgs a{};
+    a.R = R; a.W = W; a.x_dtype = x_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
+    a.s_dtype = residual ? residual_dtype : x_dtype;
+    a.x = x; a.x_stride = x_row_stride;
+    a.residual = residual; a.residual_stride = residual_row_stride;
+    a.w = weight; a.b = bias;
+    a.z = z; a.z_stride = z_row_stride;
+    a.sum = sum; a.sum_stride = sum_row_stride;
+    a.y = y; a.y_stride = y_row_stride;
+    a.q = static_cast<uint8_t*>(q); a.q_stride = q_row_stride;
+    a.scale = q_scale; a.scale_stride = q_scale_row_stride;
+    a.vec = W % 8 == 0;
+    const bool work = R > 0;
+    const int xe = esize(x_dtype), re = esize(residual_dtype), te = esize(dtype);
+    const NormRow rows[] = {{"x", x, x_row_stride, xe, work}, {"residual", residual, residual_row_stride, re, false},
+                            {"z", z, z_row_stride, te, false}, {"sum", sum, sum_row_stride, re, false},
+                            {"y", y, y_row_stride, te, false}, {"q", q, q_row_stride, 1, false}};
+    TRY(check_norm_rows(fn, rows, 6, W, a.vec));
+    if (!a.vec && W > 8192)
+        return fail(SSD_ERR_ALIGNMENT, "%s: W=%d above 8192 needs W %% 8 == 0 and 16-byte aligned rows", fn, W);
+    TRY(check_ptr(fn, "weight", weight, false, false));
+    TRY(check_ptr(fn, "bias", bias, false, false));
+    TRY(check_ptr(fn, "q_scale", q_scale, q != nullptr, false));
+    if (q && q_scale_row_stride < (W + 127) / 128)
+        return fail(SSD_ERR_BAD_SHAPE, "%s: q_scale row stride %lld is smaller than the %d blocks of a row", fn,
+                    (long long)q_scale_row_stride, (W + 127) / 128);
+    if (q_scale && !q) return fail(SSD_ERR_NULL_ARG, "%s: q_scale is given but q is NULL", fn);
+    if (sum && !residual) return fail(SSD_ERR_NULL_ARG, "%s: sum is given but residual is NULL", fn);
+    if (!work) return ok();
+    if (!y && !q) return fail(SSD_ERR_NULL_ARG, "%s: y and q are both NULL", fn);
+    // the sum may replace the residual, or x of its type: a row is read before it is written
+    if (sum && ((sum == residual && sum_row_stride != residual_row_stride) ||
+                (sum == x && (sum_row_stride != x_row_stride || x_dtype != residual_dtype))))
+        return fail(SSD_ERR_BAD_SHAPE, "%s: a sum in place of an input needs its row stride and type", fn);
+    const void* outs[] = {y, q, q_scale};
+    const void* ins[] = {x, residual, z, weight, bias, sum};
+    TRY(check_apart(fn, outs, 3, ins, 6));
+    if (sum && (sum == z || sum == weight || sum == bias))
+        return fail(SSD_ERR_BAD_SHAPE, "%s: sum must not alias z, weight or bias", fn);
+    return hip_status(fn, ssd::launch_add_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+int ssd_add_norm_bwd(int64_t R, int W, int sum_dtype, int dtype, int rms, float eps,
+                     const void* sum, int64_t sum_row_stride, const float* weight, const float* bias,
+                     const void* z, int64_t z_row_stride,
+                     const void* grad_y, int64_t grad_y_row_stride,
+                     const void* grad_sum, int64_t grad_sum_row_stride,
+                     void* dsum, int64_t dsum_row_stride, float* dweight, float* dbias,
+                     void* dz, int64_t dz_row_stride,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssd_add_norm_bwd";
+    const int dtypes[] = {sum_dtype, dtype};
+    TRY(check_norm_dims(fn, R, W, rms, eps, dtypes, 2));
+    ssd::NormArgs a{};
+    a.R = R; a.groups = 1; a.W = W; a.x_dtype = sum_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
+    a.x = sum; a.x_stride = sum_row_stride;
+    a.w = weight; a.b = bias;
+    a.z = z; a.z_stride = z_row_stride;
+    a.gy = grad_y; a.gy_stride = grad_y_row_stride;
+    a.gs = grad_sum; a.gs_stride = grad_sum_row_stride;
+    a.dx = dsum; a.dx_stride = dsum_row_stride;
+    a.dz = dz; a.dz_stride = dz_row_stride;
+    a.dw = dweight; a.db = dbias;
+    a.vec = W % 8 == 0;
+    const bool work = R > 0;
+    const int se = esize(sum_dtype), te = esize(dtype);
+    const NormRow rows[] = {{"sum", sum, sum_row_stride, se, work}, {"z", z, z_row_stride, te, false},
+                            {"grad_y", grad_y, grad_y_row_stride, te, work},
+                            {"grad_sum", grad_sum, grad_sum_row_stride, se, false},
+                            {"dsum", dsum, dsum_row_stride, se, work}, {"dz", dz, dz_row_stride, te, false}};
+    TRY(check_norm_rows(fn, rows, 6, W, a.vec));
+    if (!a.vec && W > 8192)
+        return fail(SSD_ERR_ALIGNMENT, "%s: W=%d above 8192 needs W %% 8 == 0 and 16-byte aligned rows", fn, W);
+    if (dz && !z) return fail(SSD_ERR_NULL_ARG, "%s: dz is given but z is NULL", fn);
+    TRY(check_ptr(fn, "weight", weight, false, false));
+    TRY(check_ptr(fn, "bias", bias, false, false));
+    TRY(check_ptr(fn, "dweight", dweight, false, false));
+    TRY(check_ptr(fn, "dbias", dbias, false, false));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!work) {
+        TRY(hip_status(fn, ssd::launch_zero_f32(dweight, (size_t)W, s)));
+        TRY(hip_status(fn, ssd::launch_zero_f32(dbias, (size_t)W, s)));
+        return ok();
+    }
+    // dsum may replace grad_sum: a row is read before it is written
+    if (dsum == grad_sum && dsum_row_stride != grad_sum_row_stride)
+        return fail(SSD_ERR_BAD_SHAPE, "%s: a dsum in place of grad_sum needs its row stride", fn);
+    const void* outs[] = {dsum, dz, dweight, dbias};
+    const void* ins[] = {sum, z, grad_y, weight, bias, dsum == grad_sum ? nullptr : grad_sum};
+    TRY(check_apart(fn, outs, 4, ins, 6));
+    if (grad_sum && (dz == grad_sum)) return fail(SSD_ERR_BAD_SHAPE, "%s: an output must not alias an input", fn);
+    if (dweight || dbias) {
+        TRY(check_workspace(fn, workspace, workspace_bytes, ssd_norm_bwd_workspace_size(R, 1, W)));
+        a.part = static_cast<float*>(workspace);
+    }
+    return hip_status(fn, ssd::launch_norm(a, s));
+}
+
 }  // extern "C"

@@ -31,176 +31,11 @@
 #include <hip/hip_runtime.h>
 #include <algorithm>
 
-#include "ssd_device.hpp"
+#include "norm_device.hpp"
 #include "ssd_launch.hpp"
 
 namespace ssd {
 namespace {
-
-// ------------------------------------------------------------ vectors of a row
-template <int VEC>
-__device__ __forceinline__ void ldv(const float* p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        v[0] = *p;
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void ldv(const uint16_t* p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p);
-        v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
-        v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
-    } else {
-        v[0] = bf16_to_f32(*p);
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void stv(float* p, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        *p = v[0];
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void stv(uint16_t* p, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    } else {
-        *p = (uint16_t)f32_to_bf16_bits(v[0]);
-    }
-}
-
-// A vector as it is in memory: loaded a row ahead, widened when its row comes.
-template <typename T, int VEC>
-struct Raw {
-    T v;
-    __device__ __forceinline__ void load(const T* p) { v = *p; }
-    __device__ __forceinline__ void clear() { v = 0; }
-    __device__ __forceinline__ void get(float (&o)[VEC]) const { ldv<VEC>(&v, o); }
-};
-template <>
-struct Raw<uint16_t, 8> {
-    u32x4_t v;
-    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
-    __device__ __forceinline__ void clear() { v = u32x4_t{0, 0, 0, 0}; }
-    __device__ __forceinline__ void get(float (&o)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = bf16_lo(v[i]);
-            o[2 * i + 1] = bf16_hi(v[i]);
-        }
-    }
-};
-template <>
-struct Raw<float, 8> {
-    f32x4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = *reinterpret_cast<const f32x4*>(p);
-        b = *reinterpret_cast<const f32x4*>(p + 4);
-    }
-    __device__ __forceinline__ void clear() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
-    __device__ __forceinline__ void get(float (&o)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[i] = a[i];
-            o[4 + i] = b[i];
-        }
-    }
-};
-
-// ------------------------------------------------------------ sums over a row's threads
-// two sums at once; over a workgroup they meet in `red`, whose two halves are
-// used in turn, so one barrier a call is enough: a wave reads its half before
-// it comes to the next call's barrier, behind which the half is written again
-template <int TPR>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float (*red)[2][16], int& turn) {
-    a = lanes_sum<(TPR > 64 ? 64 : TPR)>(a);
-    b = lanes_sum<(TPR > 64 ? 64 : TPR)>(b);
-    if constexpr (TPR > 64) {
-        const int wave = threadIdx.x / 64;
-        if (threadIdx.x % 64 == 0) {
-            red[turn][0][wave] = a;
-            red[turn][1][wave] = b;
-        }
-        __syncthreads();
-        a = b = 0.0f;
-#pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) {
-            a += red[turn][0][i];
-            b += red[turn][1][i];
-        }
-        turn ^= 1;
-    }
-}
-
-template <int TPR, int NV, int VEC>
-struct Shape {
-    static constexpr int threads = TPR > 256 ? TPR : 256;
-    static constexpr int rows = threads / TPR;      // rows of a workgroup at a time
-};
-
-// mean (0 for rms) and rstd of the row in x; x becomes xhat.  Threads without a
-// row (not live) hold zeros: their rstd is 0, since with eps = 0 it would be
-// infinite and their xhat, which enters the weights' sums, NaN
-template <int TPR, int NV, int VEC>
-__device__ __forceinline__ float to_hat(float (&x)[NV][VEC], const bool (&on)[NV], bool live, int W, int rms, float eps,
-                                        float (*red)[2][16], int& turn) {
-    const float inv = 1.0f / (float)W;
-    float s = 0.0f, unused = 0.0f;
-    if (!rms) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s += x[j][e];
-        row_sum2<TPR>(s, unused, red, turn);
-        const float mean = s * inv;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[j][e] = on[j] ? x[j][e] - mean : 0.0f;
-    }
-    s = unused = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s = fmaf(x[j][e], x[j][e], s);
-    row_sum2<TPR>(s, unused, red, turn);
-    const float rstd = live ? 1.0f / sqrtf(s * inv + eps) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[j][e] *= rstd;
-    return rstd;
-}
-
-template <int TPR, int NV, int VEC>
-__device__ __forceinline__ void load_params(const float* w, const float* b, const bool (&on)[NV], int lane,
-                                            float (&wv)[NV][VEC], float (&bv)[NV][VEC]) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            wv[j][e] = 1.0f;
-            bv[j][e] = 0.0f;
-        }
-        const int c = (lane + j * TPR) * VEC;
-        if (on[j] && w) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) wv[j][e] = w[c + e];
-        }
-        if (on[j] && b) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) bv[j][e] = b[c + e];
-        }
-    }
-}
 
 // group r as row `row` of memory and the columns before it; r < 2^31
 __device__ __forceinline__ void locate(const NormArgs& a, int64_t r, int64_t& row, int& col) {
@@ -258,7 +93,8 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_k
     }
 }
 
-template <typename X, typename T, int TPR, int NV, int VEC>
+// ADD: dx also takes gs, the gradient that reaches the norm's input past it (a residual stream's)
+template <typename X, typename T, int TPR, int NV, int VEC, bool ADD>
 __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_kernel(NormArgs a) {
     using SH = Shape<TPR, NV, VEC>;
     __shared__ float red[2][2][16];
@@ -271,6 +107,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
     // 1024 threads have 128 registers each: there the sums stand in LDS, every
     // thread's own column of it, so that nothing spills
     constexpr bool kLds = TPR == 1024;
+    constexpr bool kAddAhead = ADD && !kLds;         // and gs is read where it is used
     __shared__ float sums[2][kLds ? NV * VEC : 1][kLds ? TPR : 1];
     float wv[NV][VEC], bv[NV][VEC], dw[kLds ? 1 : NV][VEC], db[kLds ? 1 : NV][VEC];
     if (kHeld) load_params<TPR, NV, VEC>(a.w, a.b, on, lane, wv, bv);
@@ -284,11 +121,12 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
     const X* xp = static_cast<const X*>(a.x);
     const T* zp = static_cast<const T*>(a.z);
     const T* gp = static_cast<const T*>(a.gy);
+    const X* sp = static_cast<const X*>(a.gs);
     X* dxp = static_cast<X*>(a.dx);
     T* dzp = static_cast<T*>(a.dz);
     const float inv = 1.0f / (float)a.W;
     // the next row's operands are on their way while this row is computed
-    Raw<X, VEC> nx[NV];
+    Raw<X, VEC> nx[NV], ns[kAddAhead ? NV : 1];
     Raw<T, VEC> nz[NV], ng[NV];
     auto fetch = [&](int64_t at) {
         const bool live = at < a.R;
@@ -301,7 +139,9 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             nx[j].clear();
             nz[j].clear();
             ng[j].clear();
+            if constexpr (kAddAhead) ns[j].clear();
             if (live && on[j]) {
+                if constexpr (kAddAhead) ns[j].load(sp + r * a.gs_stride + col + c);
                 nx[j].load(xp + r * a.x_stride + col + c);
                 ng[j].load(gp + r * a.gy_stride + col + c);
                 if (zp) nz[j].load(zp + r * a.z_stride + col + c);
@@ -318,12 +158,13 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
         int64_t r;
         int col;
         locate(a, at, r, col);
-        float x[NV][VEC], z[NV][VEC], g[NV][VEC];
+        float x[NV][VEC], z[NV][VEC], g[NV][VEC], past[kAddAhead ? NV : 1][VEC];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             nx[j].get(x[j]);
             nz[j].get(z[j]);
             ng[j].get(g[j]);
+            if constexpr (kAddAhead) ns[j].get(past[j]);
         }
         if (kAhead) fetch(at + step);
         const float rstd = to_hat<TPR, NV, VEC>(x, on, live, a.W, a.rms, a.eps, red, turn);
@@ -365,7 +206,18 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             const int c = (lane + j * TPR) * VEC;
             float d[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) d[e] = rstd * (g[j][e] - m1 - x[j][e] * m2);
+            for (int e = 0; e < VEC; ++e) {
+                d[e] = rstd * (g[j][e] - m1 - x[j][e] * m2);
+                if constexpr (kAddAhead) d[e] += past[j][e];
+            }
+            if constexpr (ADD && !kAddAhead) {
+                float p[VEC];
+                if (live && on[j]) {
+                    ldv<VEC>(sp + r * a.gs_stride + col + c, p);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) d[e] += p[e];
+                }
+            }
             if (live && on[j]) stv<VEC>(dxp + r * a.dx_stride + col + c, d);
         }
     }
@@ -456,7 +308,8 @@ template <typename X, typename T, int TPR, int NV, int VEC>
 hipError_t launch_bwd(const NormArgs& a, hipStream_t stream) {
     using SH = Shape<TPR, NV, VEC>;
     const int n = (int)std::min<int64_t>((a.R + SH::rows - 1) / SH::rows, kNormBwdGrid);
-    hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC>), dim3(n), dim3(SH::threads), 0, stream, a);
+    if (a.gs) hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC, true>), dim3(n), dim3(SH::threads), 0, stream, a);
+    else hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC, false>), dim3(n), dim3(SH::threads), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
     hipLaunchKernelGGL(ssd_norm_sum_kernel, dim3((2 * a.W + 31) / 32), dim3(1024), 0, stream, a.part, n, a.W, a.dw, a.db);

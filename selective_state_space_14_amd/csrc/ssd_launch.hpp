@@ -145,10 +145,26 @@ struct NormArgs {
     void* y; int64_t y_stride;             // dtype
     // backward
     const void* gy; int64_t gy_stride;     // dtype
+    const void* gs; int64_t gs_stride;     // x_dtype, added to dx, or null
     void* dx; int64_t dx_stride;           // x_dtype
     void* dz; int64_t dz_stride;           // dtype, or null
     float* dw; float* db;                  // [W] or null
     float* part;                           // [workgroups][2][W], null when neither dw nor db is asked for
+};
+// The norm with the residual's addition and 8-bit output.
+struct AddNormArgs {
+    int64_t R;
+    int W, x_dtype, s_dtype, dtype, rms;   // s_dtype: residual's and sum's, x's without a residual
+    int vec;
+    float eps;
+    const void* x; int64_t x_stride;
+    const void* residual; int64_t residual_stride;     // or null
+    const float* w; const float* b;        // [W] or null
+    const void* z; int64_t z_stride;       // dtype, or null
+    void* sum; int64_t sum_stride;         // s_dtype, or null
+    void* y; int64_t y_stride;             // dtype, or null
+    uint8_t* q; int64_t q_stride;          // e4m3, or null
+    float* scale; int64_t scale_stride;    // [R][ceil(W / 128)], with q
 };
 // workgroups of the two passes at most: 8 and 4 of 256 threads on every CU
 constexpr int kNormGrid = 2048, kNormBwdGrid = 1024;
@@ -253,6 +269,7 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, void* ws, hipStream_t stream)
 hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 size_t norm_bwd_workspace_bytes(int64_t R, int W);
+hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t stream);
 size_t glr_fwd_workspace_bytes(int B, int L, int D, int dtype);
 hipError_t launch_glr_fwd(const GlrArgs& a, void* ws, hipStream_t stream);
 size_t glr_bwd_workspace_bytes(int B, int L, int D, int dtype);
