@@ -1,7 +1,7 @@
 /*
  * ssd.h -- C ABI of libssd.so, the gfx950 (MI355X) Mamba-2 SSD mixer core.
  *
- * Nineteen operations, each a few HIP kernel launches on the caller's stream:
+ * Twenty operations, each a few HIP kernel launches on the caller's stream:
  *
  *   ssd_conv_fwd        causal depthwise conv (k = 4) + SiLU over the
  *                       [x | B | C] columns, and dt = softplus(dt_raw + dt_bias)
@@ -30,6 +30,7 @@
  *   ssd_glr_scan_bwd    backward (VJP) of ssd_glr_scan_fwd
  *   ssd_add_norm_fwd    the norm with a residual's addition and an 8-bit output
  *   ssd_add_norm_bwd    backward of ssd_add_norm_fwd
+ *   ssd_proj_fp8_fwd    a projection in 8-bit floating point with block scales
  *
  * The operation (per batch row b and head h, token t, head h in group
  * g = h / (H/G)):
@@ -906,6 +907,28 @@ int ssd_add_norm_bwd(int64_t R, int W, int sum_dtype, int dtype, int rms, float 
                      void *dsum, int64_t dsum_row_stride, float *dweight, float *dbias,
                      void *dz, int64_t dz_row_stride,
                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ssd_proj_fp8_fwd -- a layer's projection (in_proj, out_proj) in 8-bit
+ * floating point, with a scale for every block of 128:
+ *     y[m][n] = sum over blocks b of  a_scale[m][b] w_scale[n / 128][b]
+ *               * sum over k in block b of  a[m][k] w[n][k]
+ *   a       OCP e4m3 [M][K] with a_scale f32 [M][ceil(K / 128)]: rows as
+ *               ssd_add_norm_fwd leaves them (q, q_scale)
+ *   w       OCP e4m3 [N][K] with w_scale f32 [ceil(N / 128)][ceil(K / 128)],
+ *               a scale for every 128 rows by 128 columns: the caller
+ *               quantises a weight once, largest magnitude / 448 a block
+ *   y       T   [M][N], rounded once; row stride y_row_stride: the columns of
+ *               a wider row (z | x | B | C | dt) are fine
+ * K a multiple of 16; a and w with 16-byte aligned bases and row strides (in
+ * elements, >= K and <= 4194304); scales 4-byte aligned; y aligned to its
+ * elements.  Products are exact, sums fp32, scales fp32.  A NaN reaches its
+ * own row (a) or column (w) of y.  Deterministic.  M = 0 writes nothing.
+ */
+int ssd_proj_fp8_fwd(int M, int N, int K, int dtype,
+                     const void *a, int64_t a_row_stride, const float *a_scale, int64_t a_scale_row_stride,
+                     const void *w, int64_t w_row_stride, const float *w_scale, int64_t w_scale_row_stride,
+                     void *y, int64_t y_row_stride, void *stream);
 
 #ifdef __cplusplus
 }

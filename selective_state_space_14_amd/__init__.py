@@ -23,6 +23,7 @@ The entry points mirror the C ABI in include/ssd.h one to one:
     ssd_glr_scan_bwd    its backward (VJP)
     ssd_add_norm_fwd    layer or RMS norm with a residual's addition and an 8-bit output with scales
     ssd_add_norm_bwd    its backward
+    ssd_proj_fp8_fwd    a projection in 8-bit floating point with block scales
 
 This module only marshals torch tensors (device pointers, row strides, the
 current HIP stream) into the library; every step of the computation runs in
@@ -45,6 +46,7 @@ __all__ = ["load", "ssd_conv_fwd", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_sta
            "ssd_delta_scan_bwd_workspace_size", "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
            "ssd_glr_scan_fwd", "ssd_glr_scan_workspace_size", "ssd_glr_step", "ssd_glr_scan_bwd",
            "ssd_glr_scan_bwd_workspace_size", "ssd_add_norm_fwd", "ssd_add_norm_bwd",
+           "ssd_proj_fp8_fwd",
            "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_ACT_SILU", "SSD_ACT_NONE"]
 
 # SSD_LIBRARY names another build of the same library (the host-sanitized one the ABI checks use)
@@ -151,6 +153,8 @@ def load() -> ctypes.CDLL:
     lib.ssd_add_norm_fwd.argtypes = [I64, I, I, I, I, I, F, P, I64, P, I64, P, P, P, I64, P, I64, P, I64, P, I64, P, I64, P]
     lib.ssd_add_norm_bwd.restype = I
     lib.ssd_add_norm_bwd.argtypes = [I64, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P, I64, P, I64, P, P, P, I64, P, SZ, P]
+    lib.ssd_proj_fp8_fwd.restype = I
+    lib.ssd_proj_fp8_fwd.argtypes = [I, I, I, I, P, I64, P, I64, P, I64, P, I64, P, I64, P]
     _lib = lib
     return lib
 
@@ -1028,3 +1032,23 @@ def ssd_add_norm_bwd(sum, grad_y, grad_sum=None, weight=None, *, bias=None, z=No
            *c.rows(grad_sum, "grad_sum", sum.dtype, shape), out("sum"), W, out("weight"), out("bias"), out("z"), W,
            c.ptr(ws, "workspace"), nb))
     return g
+
+
+# ---- the 8-bit projection
+@_on_stream
+def ssd_proj_fp8_fwd(a, a_scale, w, w_scale, *, out_dtype=torch.bfloat16, y=None):
+    """a times w transposed in float8_e4m3fn with a scale for every block of 128.  a [..., K] with a_scale fp32
+    [..., ceil(K / 128)] (ssd_add_norm_fwd's "q" and "scale"), w [N, K] with w_scale fp32 [ceil(N / 128), ceil(K / 128)].
+    Returns y [..., N] in y's dtype, else out_dtype."""
+    lib = load()
+    c = _Call(a, "a")
+    lead, K, N = a.shape[:-1], a.shape[-1], w.shape[0]
+    blocks = -(-K // 128)
+    T = out_dtype if y is None else y.dtype
+    if y is None:
+        y = torch.empty(lead + (N,), dtype=T, device=c.dev)
+    c.run(lib.ssd_proj_fp8_fwd,
+          (_lead_rows(a.shape), N, K, _dtype_code(y, "y"), *c.rows(a, "a", torch.float8_e4m3fn, a.shape),
+           *c.rows(a_scale, "a_scale", torch.float32, lead + (blocks,)), *c.rows(w, "w", torch.float8_e4m3fn, (N, K)),
+           *c.rows(w_scale, "w_scale", torch.float32, (-(-N // 128), blocks)), *c.rows(y, "y", T, lead + (N,))))
+    return y

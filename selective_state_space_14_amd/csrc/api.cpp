@@ -1648,4 +1648,65 @@ int ssd_add_norm_bwd(int64_t R, int W, int sum_dtype, int dtype, int rms, float 
     return hip_status(fn, ssd::launch_norm(a, s));
 }
 
+// ---- the 8-bit projection
+int ssd_proj_fp8_fwd(int M, int N, int K, int dtype,
+                     const void* a, int64_t a_row_stride, const float* a_scale, int64_t a_scale_row_stride,
+                     const void* w, int64_t w_row_stride, const float* w_scale, int64_t w_scale_row_stride,
+                     void* y, int64_t y_row_stride, void* stream) {
+    const char* fn = "ssd_proj_fp8_fwd";
+    if (dtype != SSD_F32 && dtype != SSD_BF16)
+        return fail(SSD_ERR_UNSUPPORTED, "%s: dtype=%d is not supported (only SSD_F32=0 and SSD_BF16=1; "
+                    "fp16, fp64 and other types are refused, not converted)", fn, dtype);
+    if (M < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: M=%d must be >= 0", fn, M);
+    if (N <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: N=%d must be > 0", fn, N);
+    if (K <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: K=%d must be > 0", fn, K);
+    if (K % 16 != 0) return fail(SSD_ERR_UNSUPPORTED, "%s: K=%d is not supported (must be a multiple of 16)", fn, K);
+    // the grids: a workgroup for every 128 x 128 of y
+    if (((int64_t)M + 127) / 128 * (((int64_t)N + 127) / 128) > 0x7fffffffLL)
+        return fail(SSD_ERR_BAD_SHAPE, "%s: M=%d rows of N=%d columns are too many", fn, M, N);
+    const int blocks = (K + 127) / 128, es = esize(dtype);
+    const bool work = M > 0;
+    struct Operand { const char* name; const void* p; int64_t stride, width; };
+    const Operand bytes[] = {{"a", a, a_row_stride, K}, {"w", w, w_row_stride, K}};
+    const Operand scales[] = {{"a_scale", a_scale, a_scale_row_stride, blocks}, {"w_scale", w_scale, w_scale_row_stride, blocks}};
+    for (const Operand* o : {&bytes[0], &bytes[1], &scales[0], &scales[1]}) {
+        const bool eight = o == &bytes[0] || o == &bytes[1];
+        if (!o->p) {
+            if (work) return fail(SSD_ERR_NULL_ARG, "%s: %s is NULL", fn, o->name);
+            continue;
+        }
+        if (o->stride < o->width)
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is smaller than the row width %lld", fn, o->name,
+                        (long long)o->stride, (long long)o->width);
+        if (o->stride > (1 << 22))
+            return fail(SSD_ERR_BAD_SHAPE, "%s: %s row stride %lld is above 4194304 elements", fn, o->name, (long long)o->stride);
+        TRY(check_ptr(fn, o->name, o->p, false, eight));
+        if (eight && o->stride % 16)
+            return fail(SSD_ERR_ALIGNMENT, "%s: %s row stride %lld is not a multiple of 16 bytes", fn, o->name, (long long)o->stride);
+    }
+    if (!y) {
+        if (work) return fail(SSD_ERR_NULL_ARG, "%s: y is NULL", fn);
+        return ok();
+    }
+    if (y_row_stride < N)
+        return fail(SSD_ERR_BAD_SHAPE, "%s: y row stride %lld is smaller than the row width %d", fn, (long long)y_row_stride, N);
+    if (y_row_stride > (1 << 22))
+        return fail(SSD_ERR_BAD_SHAPE, "%s: y row stride %lld is above 4194304 elements", fn, (long long)y_row_stride);
+    if (reinterpret_cast<uintptr_t>(y) % es)
+        return fail(SSD_ERR_ALIGNMENT, "%s: y=%p is not aligned to its elements", fn, y);
+    const void* outs[] = {y};
+    const void* ins[] = {a, a_scale, w, w_scale};
+    TRY(check_apart(fn, outs, 1, ins, 4));
+    if (!work) return ok();
+    ssd::ProjArgs p{};
+    p.M = M; p.N = N; p.K = K; p.dtype = dtype;
+    p.wide = y_row_stride % 4 == 0 && reinterpret_cast<uintptr_t>(y) % (4 * es) == 0;
+    p.a = static_cast<const uint8_t*>(a); p.a_stride = a_row_stride;
+    p.a_scale = a_scale; p.a_scale_stride = a_scale_row_stride;
+    p.w = static_cast<const uint8_t*>(w); p.w_stride = w_row_stride;
+    p.w_scale = w_scale; p.w_scale_stride = w_scale_row_stride;
+    p.y = y; p.y_stride = y_row_stride;
+    return hip_status(fn, ssd::launch_proj(p, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

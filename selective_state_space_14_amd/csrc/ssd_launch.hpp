@@ -226,6 +226,17 @@ struct GlrArgs {
     float* g_init;                         // [B][D] or null
 };
 
+// The 8-bit projection: y [M][N] from a [M][K] and w [N][K], a scale for every 128 columns of K (and rows of w).
+struct ProjArgs {
+    int M, N, K, dtype;
+    int wide;                              // y's base and rows on four elements
+    const uint8_t* a; int64_t a_stride;
+    const float* a_scale; int64_t a_scale_stride;      // [M][ceil(K / 128)]
+    const uint8_t* w; int64_t w_stride;
+    const float* w_scale; int64_t w_scale_stride;      // [ceil(N / 128)][ceil(K / 128)]
+    void* y; int64_t y_stride;             // dtype
+};
+
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_scan(const ScanArgs& a, hipStream_t stream);
 // Sequence split chosen for these sizes (1 = none) and its superchunk length.
@@ -270,6 +281,7 @@ hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 size_t norm_bwd_workspace_bytes(int64_t R, int W);
 hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t stream);
+hipError_t launch_proj(const ProjArgs& a, hipStream_t stream);
 size_t glr_fwd_workspace_bytes(int B, int L, int D, int dtype);
 hipError_t launch_glr_fwd(const GlrArgs& a, void* ws, hipStream_t stream);
 size_t glr_bwd_workspace_bytes(int B, int L, int D, int dtype);
