@@ -10,11 +10,18 @@
 //   dA = sum dl s,  dr_bias = sum dr,  di_bias = sum di
 // (where m is 0 the second part of dl is taken as 0).
 //
-// A stretch of tokens maps the state that enters it to A h + H (A the product of its decays, H what it gathers from a
-// zero state), and two stretches after one another compose: A = A2 A1, H = A2 H1 + H2.  A tile is kWaves stretches, one a
-// wave, of Tw tokens by 128 channels; every lane keeps the decays and inputs of its two channels in registers, so that the
-// tokens are read once.  A tile's waves join in LDS.  Document starts and tokens behind a row's length are decays of 0 and
-// 1: chosen, not multiplied, so what stands there is not used.
+// A stretch of tokens maps the state h that enters it to A h + H (A the product of its decays, H what it gathers from a
+// zero state), and two stretches after one another compose: A = A1 A2, H = A2 H1 + H2.  A tile is kWaves stretches, one a
+// wave, of some tokens by 128 channels; every lane keeps the decays and inputs of its two channels in registers, so that
+// the tokens are read once.  A tile's waves join in LDS; tiles join through the workspace in the same launch: each
+// publishes its (A, H), composes those before it in its group of 16 with the state that enters the group, and the group's
+// last tile publishes the state that leaves it.  A document's start cuts: what was before is dropped, NaN included.  Tokens
+// behind a row's length are decays of 1.  Both are chosen, not multiplied, so what stands there is not used.
+//
+// Every wait ends: a workgroup takes its place in the chain from a counter when it starts, so all places before its own
+// belong to workgroups that have started, and these wait only for places before theirs.  A published pair is one 64-bit
+// word with its own mark of validity, written and read by single relaxed atomics of device scope: no other memory is
+// ordered by it.  What is composed, and in which order, does not depend on the timing: results are deterministic.
 #include <algorithm>
 
 #include "ssd_device.hpp"
@@ -29,11 +36,14 @@ template <typename T> constexpr int kTile = kTw<T> * kWaves;
 
 // ------------------------------------------------------------ a lane's two channels
 // PAIR: neighbours, read together (even widths and strides, bases on pairs); else 64 apart
+// hide(): the compiler forgets what it knows of the values, so that it does not keep what it has made of them
 template <typename T, bool PAIR> struct Two;
 template <> struct Two<float, true> {
     float2 v;
     __device__ __forceinline__ void load(const float* p, int c, int) { v = *reinterpret_cast<const float2*>(p + c); }
     __device__ __forceinline__ float get(int j) const { return j ? v.y : v.x; }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v.x), "+v"(v.y)); }
+    __device__ __forceinline__ void keep(bool on) { v = make_float2(on ? v.x : 0.0f, on ? v.y : 0.0f); }
     __device__ __forceinline__ static void store(float* p, int c, int, int, float a, float b) {
         *reinterpret_cast<float2*>(p + c) = make_float2(a, b);
     }
@@ -42,6 +52,8 @@ template <> struct Two<uint16_t, true> {
     uint32_t v;
     __device__ __forceinline__ void load(const uint16_t* p, int c, int) { v = *reinterpret_cast<const uint32_t*>(p + c); }
     __device__ __forceinline__ float get(int j) const { return j ? bf16_hi(v) : bf16_lo(v); }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
+    __device__ __forceinline__ void keep(bool on) { v = on ? v : 0; }
     __device__ __forceinline__ static void store(uint16_t* p, int c, int, int, float a, float b) {
         *reinterpret_cast<uint32_t*>(p + c) = pack_bf16x2(a, b);
     }
@@ -50,15 +62,27 @@ __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(uint16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
 __device__ __forceinline__ void narrow(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
-template <typename T> struct Two<T, false> {
-    T v[2];
+template <> struct Two<float, false> {
+    float2 v;
     // channels past the last are read from it
-    __device__ __forceinline__ void load(const T* p, int c, int last) {
-        v[0] = p[min(c, last)];
-        v[1] = p[min(c + 64, last)];
+    __device__ __forceinline__ void load(const float* p, int c, int last) { v = make_float2(p[min(c, last)], p[min(c + 64, last)]); }
+    __device__ __forceinline__ float get(int j) const { return j ? v.y : v.x; }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v.x), "+v"(v.y)); }
+    __device__ __forceinline__ void keep(bool on) { v = make_float2(on ? v.x : 0.0f, on ? v.y : 0.0f); }
+    __device__ __forceinline__ static void store(float* p, int c, int, int D, float a, float b) {
+        if (c < D) p[c] = a;
+        if (c + 64 < D) p[c + 64] = b;
     }
-    __device__ __forceinline__ float get(int j) const { return widen(v[j]); }
-    __device__ __forceinline__ static void store(T* p, int c, int, int D, float a, float b) {
+};
+template <> struct Two<uint16_t, false> {
+    uint32_t v;
+    __device__ __forceinline__ void load(const uint16_t* p, int c, int last) {
+        v = p[min(c, last)] | (uint32_t)p[min(c + 64, last)] << 16;
+    }
+    __device__ __forceinline__ float get(int j) const { return j ? bf16_hi(v) : bf16_lo(v); }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
+    __device__ __forceinline__ void keep(bool on) { v = on ? v : 0; }
+    __device__ __forceinline__ static void store(uint16_t* p, int c, int, int D, float a, float b) {
         if (c < D) narrow(p + c, a);
         if (c + 64 < D) narrow(p + c + 64, b);
     }
@@ -84,17 +108,20 @@ __device__ __forceinline__ float sigmoid_f(float v) { return fast_rcp(1.0f + fas
 // off by n^7 / 8! of itself, 2e-8 at the border) and a from 1 - a by one rounding, so that neither the hardware exp2's
 // error nor the difference's shows: over thousands of tokens a decay that is off by one step the same way each time
 // would move the state by some 1e-5.  From the border on the hardware's exp2 and the difference are within 2^-22.
-__device__ __forceinline__ void decay(float n, float& a, float& om) {
+__device__ __forceinline__ float one_minus(float n) {
     float q = fmaf(n, -1.0f / 5040.0f, 1.0f / 720.0f);
     q = fmaf(n, -q, 1.0f / 120.0f);
     q = fmaf(n, -q, 1.0f / 24.0f);
     q = fmaf(n, -q, 1.0f / 6.0f);
     q = fmaf(n, -q, 0.5f);
     q = fmaf(n, -q, 1.0f);
-    q *= n;
-    const float e = fast_exp2(-n * kLog2e);
-    a = n < 0.35f ? 1.0f - q : e;
-    om = n < 0.35f ? q : 1.0f - e;
+    return q * n;
+}
+constexpr float kSeries = 0.35f;
+__device__ __forceinline__ void decay(float n, float& a, float& om) {
+    const float q = one_minus(n), e = fast_exp2(-n * kLog2e);
+    a = n < kSeries ? 1.0f - q : e;
+    om = n < kSeries ? q : 1.0f - e;
 }
 
 // bit t set: a document starts at token t0 + t (t < n <= 64)
@@ -102,6 +129,16 @@ __device__ __forceinline__ uint64_t starts_in(const int32_t* doc, int t0, int n,
     if (!doc) return 0;
     const int l = threadIdx.x % 64, t = t0 + l;
     return __ballot(l < n && t > 0 && t < L && doc[max(min(t, L - 1), 0)] != doc[max(min(t, L - 1) - 1, 0)]);
+}
+
+// A of a stretch that a document starts in: nothing passes through
+constexpr uint32_t kCut = 0x80000000u;              // -0.0
+__device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) == kCut; }
+__device__ __forceinline__ float through(float A, float H, float h) { return is_cut(A) ? H : fmaf(A, h, H); }
+// (A, H) and then (A2, H2); a product of -0.0 and a decay is -0.0
+__device__ __forceinline__ void then(float& A, float& H, float A2, float H2) {
+    H = through(A2, H2, H);
+    A = is_cut(A2) ? A2 : A * A2;
 }
 
 struct Params {
@@ -134,11 +171,22 @@ struct Place {
     }
 };
 
+// bits of a wave's n tokens: those that start a document, those that are real.  In vector registers, though the same in
+// every lane: of scalars the compiler makes a branch a token.
+__device__ __forceinline__ void masks(const GlrArgs& g, const Place& p, int n, uint32_t& starts, uint32_t& lives) {
+    const int k = max(0, min(p.len - p.t0, n));
+    lives = (1u << k) - 1;                          // n <= 16
+    starts = (uint32_t)starts_in(g.doc ? g.doc + (size_t)p.b * g.L : nullptr, p.t0, n, g.L) & lives;
+    asm volatile("" : "+v"(starts), "+v"(lives));
+}
+__device__ __forceinline__ bool bit(uint32_t mask, int t) { return (mask >> t) & 1; }
+
 // decays and inputs of a wave's tokens, and their composition
 template <typename T, bool PAIR, int Tw>
 struct Stretch {
     float a[Tw][2], v[Tw][2];
     float A[2], H[2];
+    uint32_t starts, lives;                               // bits of the tokens
     __device__ __forceinline__ void compute(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Params& w) {
         Two<T, PAIR> x[Tw], r[Tw], i[Tw];
         const T* xp = static_cast<const T*>(g.x);
@@ -151,84 +199,126 @@ struct Stretch {
             r[t].load(rp + row * g.r_stride, ln.c, ln.last);
             i[t].load(ip + row * g.i_stride, ln.c, ln.last);
         }
-        const uint64_t starts = starts_in(g.doc ? g.doc + (size_t)p.b * g.L : nullptr, p.t0, Tw, g.L);
+        masks(g, p, Tw, starts, lives);
         A[0] = A[1] = 1.0f;
         H[0] = H[1] = 0.0f;
 #pragma unroll
         for (int t = 0; t < Tw; ++t) {
-            const bool live = p.t0 + t < p.len, start = (starts >> t) & 1;
+            const bool live = bit(lives, t), start = bit(starts, t);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float d, om;
                 decay(sigmoid_f(r[t].get(j) + w.rb[j]) * w.nA[j], d, om);
                 const float in = __builtin_amdgcn_sqrtf(om * (1.0f + d)) * sigmoid_f(i[t].get(j) + w.ib[j]) * x[t].get(j);
-                a[t][j] = live ? (start ? 0.0f : d) : 1.0f;
+                a[t][j] = live ? d : 1.0f;
                 v[t][j] = live ? in : 0.0f;
-                A[j] *= a[t][j];
-                H[j] = fmaf(a[t][j], H[j], v[t][j]);
+                A[j] = start ? __uint_as_float(kCut) : A[j] * a[t][j];
+                H[j] = start ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
             }
         }
     }
 };
 
-// ------------------------------------------------------------ forward
-// agg: [tile][2][D] for every batch row, what a tile's tokens do to the state
-template <typename T, bool PAIR>
-__global__ __launch_bounds__(kThreads, 4) void ssd_glr_tiles_kernel(GlrArgs g, float* agg) {
-    constexpr int Tw = kTw<T>;
-    __shared__ float2 sA[kWaves][64], sH[kWaves][64];
-    const Place p(g, blockIdx.x, kTile<T>, Tw);
-    const Lane<PAIR> ln(p.blk, g.D);
-    Params w;
-    w.load(g, ln);
-    Stretch<T, PAIR, Tw> s;
-    s.compute(g, p, ln, w);
-    const int wave = wave_id(), l = threadIdx.x % 64;
-    sA[wave][l] = make_float2(s.A[0], s.A[1]);
-    sH[wave][l] = make_float2(s.H[0], s.H[1]);
+// ------------------------------------------------------------ tiles in a chain
+// Places 0, 1, ... along each row of the batch (forward: its tiles in order, backward: from the last).  All bits set: not
+// written yet.  A's own NaNs have other bits.
+constexpr int kGroup = 16;
+constexpr uint32_t kUnset = 0xffffffffu;
+struct Chain {
+    uint32_t* ticket;                               // kUnset at the start
+    uint64_t* pairs;                                // [B][tiles][D]
+    uint64_t* enter;                                // [B][groups - 1][D]: the state that leaves a group
+    int groups;
+};
+__device__ __forceinline__ uint64_t pack_pair(float A, float H) {
+    return (uint64_t)__float_as_uint(H) << 32 | (A == A ? __float_as_uint(A) : 0x7fc00000u);
+}
+__device__ __forceinline__ float pair_A(uint64_t w) { return __uint_as_float((uint32_t)w); }
+__device__ __forceinline__ float pair_H(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32)); }
+__device__ __forceinline__ bool is_set(uint64_t w) { return (uint32_t)w != kUnset; }
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <bool PAIR>
+__device__ __forceinline__ void publish(uint64_t* row, const Lane<PAIR>& ln, int D, float2 A, float2 H) {
+    const int c1 = PAIR ? ln.c + 1 : ln.c + 64;
+    if (ln.on) __hip_atomic_store(row + ln.c, pack_pair(A.x, H.x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (ln.on && c1 < D) __hip_atomic_store(row + c1, pack_pair(A.y, H.y), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <bool PAIR>
+__device__ __forceinline__ void await(const uint64_t* row, const Lane<PAIR>& ln, uint64_t (&w)[2]) {
+    const int c0 = min(ln.c, ln.last), c1 = min(PAIR ? ln.c + 1 : ln.c + 64, ln.last);
+    for (;;) {
+        w[0] = peek(row + c0);
+        w[1] = peek(row + c1);
+        if (__all(is_set(w[0]) && is_set(w[1]))) return;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+__device__ __forceinline__ int chain_place(const Chain& ch) {
+    __shared__ uint32_t place;
+    if (threadIdx.x == 0) place = atomicAdd(ch.ticket, 1u) + 1u;
     __syncthreads();
-    if (wave || !ln.on) return;
-    float A[2] = {1.0f, 1.0f}, H[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-        const float2 a = sA[k][l], h = sH[k][l];
-        A[0] *= a.x; A[1] *= a.y;
-        H[0] = fmaf(a.x, H[0], h.x);
-        H[1] = fmaf(a.y, H[1], h.y);
+    return (int)__builtin_amdgcn_readfirstlane(place);
+}
+// What stands before place k of a row: each wave composes two places of k's group into pA, pH, wave 0 also fetches the
+// state that enters the group.  Followed by a barrier and chain_enter().
+template <bool PAIR>
+__device__ __forceinline__ void chain_gather(const Chain& ch, int b, int k, int tiles, int D, const Lane<PAIR>& ln, float2 (*pA)[64],
+                                             float2 (*pH)[64], float2* in) {
+    const int wave = wave_id(), l = threadIdx.x % 64, group = k / kGroup, first = group * kGroup + 2 * wave;
+    uint64_t w[2], w2[2];
+    if (first < k) {
+        const uint64_t* row = ch.pairs + ((size_t)b * tiles + first) * D;
+        await(row, ln, w);
+        float2 A = make_float2(pair_A(w[0]), pair_A(w[1])), H = make_float2(pair_H(w[0]), pair_H(w[1]));
+        if (first + 1 < k) {
+            await(row + D, ln, w2);
+            then(A.x, H.x, pair_A(w2[0]), pair_H(w2[0]));
+            then(A.y, H.y, pair_A(w2[1]), pair_H(w2[1]));
+        }
+        pA[wave][l] = A;
+        pH[wave][l] = H;
     }
-    float* out = agg + ((size_t)p.b * g.tiles + p.c) * 2 * g.D;
-    Two<float, PAIR>::store(out, ln.c, 0, g.D, A[0], A[1]);
-    Two<float, PAIR>::store(out + g.D, ln.c, 0, g.D, H[0], H[1]);
+    if (wave == 0 && group > 0) {
+        await(ch.enter + ((size_t)b * (ch.groups - 1) + group - 1) * D, ln, w);
+        in[l] = make_float2(pair_H(w[0]), pair_H(w[1]));
+    }
+}
+__device__ __forceinline__ void chain_enter(int k, const float2 (*pA)[64], const float2 (*pH)[64], const float2* in, float (&h)[2]) {
+    const int l = threadIdx.x % 64, n = k % kGroup;
+    if (k >= kGroup) {
+        h[0] = in[l].x;
+        h[1] = in[l].y;
+    }
+    for (int w = 0; 2 * w < n; ++w) {
+        const float2 A = pA[w][l], H = pH[w][l];
+        h[0] = through(A.x, H.x, h[0]);
+        h[1] = through(A.y, H.y, h[1]);
+    }
+}
+// the chain's memory to all bits set, 16 bytes a thread
+__global__ __launch_bounds__(256) void ssd_glr_unset_kernel(uint4* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        p[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
 }
 
-// enter: [tile][D] for every batch row, the state that enters a tile (rev: the adjoint that enters it from behind)
-__global__ __launch_bounds__(256) void ssd_glr_fold_kernel(const float* agg, const float* first, float* enter, int B, int D, int tiles,
-                                                           int rev) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)B * D) return;
-    const int b = (int)(i / D), d = (int)(i % D);
-    float h = first ? first[i] : 0.0f;
-    for (int k = 0; k < tiles; ++k) {
-        const size_t c = (size_t)b * tiles + (rev ? tiles - 1 - k : k);
-        enter[c * D + d] = h;
-        h = fmaf(agg[c * 2 * D + d], h, agg[c * 2 * D + D + d]);
-    }
-}
-
-template <typename T, bool PAIR>
-__global__ __launch_bounds__(kThreads, 4) void ssd_glr_scan_kernel(GlrArgs g, const float* enter) {
+// ------------------------------------------------------------ forward
+// CHAIN: rows of more than one tile
+template <typename T, bool PAIR, bool CHAIN>
+__global__ __launch_bounds__(kThreads, 4) void ssd_glr_scan_kernel(GlrArgs g, Chain ch) {
     constexpr int Tw = kTw<T>;
-    __shared__ float2 sA[kWaves][64], sH[kWaves][64];
-    const Place p(g, blockIdx.x, kTile<T>, Tw);
+    __shared__ float2 sA[kWaves][64], sH[kWaves][64], pA[CHAIN ? kWaves : 1][64], pH[CHAIN ? kWaves : 1][64], in[64];
+    const Place p(g, CHAIN ? chain_place(ch) : blockIdx.x, kTile<T>, Tw);
     const Lane<PAIR> ln(p.blk, g.D);
     Params w;
     w.load(g, ln);
     Stretch<T, PAIR, Tw> s;
     s.compute(g, p, ln, w);
     float h[2] = {0.0f, 0.0f};
-    if (enter || g.init_state) {
+    if (p.c == 0 && g.init_state) {
         Two<float, PAIR> e;
-        e.load(enter ? enter + ((size_t)p.b * g.tiles + p.c) * g.D : g.init_state + (size_t)p.b * g.D, ln.c, ln.last);
+        e.load(g.init_state + (size_t)p.b * g.D, ln.c, ln.last);
         h[0] = e.get(0);
         h[1] = e.get(1);
     }
@@ -236,10 +326,31 @@ __global__ __launch_bounds__(kThreads, 4) void ssd_glr_scan_kernel(GlrArgs g, co
     sA[wave][l] = make_float2(s.A[0], s.A[1]);
     sH[wave][l] = make_float2(s.H[0], s.H[1]);
     __syncthreads();                                 // init_state has been read: final_state may be it
+    if constexpr (CHAIN) {
+        if (wave == kWaves - 1) {                    // the first tile starts from the row's own state: a cut
+            float2 A = p.c == 0 ? make_float2(__uint_as_float(kCut), __uint_as_float(kCut)) : make_float2(1.0f, 1.0f);
+            float2 H = make_float2(h[0], h[1]);
+#pragma unroll
+            for (int k = 0; k < kWaves; ++k) {
+                const float2 a = sA[k][l], v = sH[k][l];
+                then(A.x, H.x, a.x, v.x);
+                then(A.y, H.y, a.y, v.y);
+            }
+            publish(ch.pairs + ((size_t)p.b * g.tiles + p.c) * g.D, ln, g.D, A, H);
+        }
+        chain_gather(ch, p.b, p.c, g.tiles, g.D, ln, pA, pH, in);
+        __syncthreads();
+        chain_enter(p.c, pA, pH, in, h);
+    }
     for (int k = 0; k < wave; ++k) {
         const float2 a = sA[k][l], v = sH[k][l];
-        h[0] = fmaf(a.x, h[0], v.x);
-        h[1] = fmaf(a.y, h[1], v.y);
+        h[0] = through(a.x, v.x, h[0]);
+        h[1] = through(a.y, v.y, h[1]);
+    }
+    if constexpr (CHAIN) {
+        if (wave == kWaves - 1 && p.c % kGroup == kGroup - 1 && p.c + 1 < g.tiles)
+            publish(ch.enter + ((size_t)p.b * (ch.groups - 1) + p.c / kGroup) * g.D, ln, g.D, make_float2(0.0f, 0.0f),
+                    make_float2(through(s.A[0], s.H[0], h[0]), through(s.A[1], s.H[1], h[1])));
     }
     if (!ln.on || p.t0 >= g.L) return;
     if (g.states && p.t0 % 64 == 0)
@@ -247,9 +358,9 @@ __global__ __launch_bounds__(kThreads, 4) void ssd_glr_scan_kernel(GlrArgs g, co
     T* yp = static_cast<T*>(g.y);
 #pragma unroll
     for (int t = 0; t < Tw; ++t) {
-        h[0] = fmaf(s.a[t][0], h[0], s.v[t][0]);
-        h[1] = fmaf(s.a[t][1], h[1], s.v[t][1]);
-        const bool live = p.t0 + t < p.len;
+        const bool live = bit(s.lives, t), start = bit(s.starts, t);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) h[j] = start ? s.v[t][j] : fmaf(s.a[t][j], h[j], s.v[t][j]);
         if (yp && p.t0 + t < g.L)
             Two<T, PAIR>::store(yp + ((int64_t)p.b * g.L + p.t0 + t) * g.y_stride, ln.c, 0, g.D, live ? h[0] : 0.0f,
                                 live ? h[1] : 0.0f);
@@ -268,6 +379,7 @@ struct Back {
     Two<T, PAIR> x[kTb], gy[kTb];
     float a[kTb][2], v[kTb][2], s[kTb][2], gi[kTb][2];    // carry decay, input (later a h_{t-1}), gates
     float A[2], H[2], N[2];                               // compositions: of the state, and of the adjoint from behind
+    uint32_t starts, lives;                               // bits of the tokens
     __device__ __forceinline__ void compute(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Params& w) {
         Two<T, PAIR> r[kTb], i[kTb];
         const T* xp = static_cast<const T*>(g.x);
@@ -282,13 +394,16 @@ struct Back {
             i[t].load(ip + row * g.i_stride, ln.c, ln.last);
             gy[t].load(gp + row * g.gy_stride, ln.c, ln.last);
         }
-        const uint64_t starts = starts_in(g.doc ? g.doc + (size_t)p.b * g.L : nullptr, p.t0, kTb, g.L);
+        masks(g, p, kTb, starts, lives);
         A[0] = A[1] = 1.0f;
         H[0] = H[1] = N[0] = N[1] = 0.0f;
 #pragma unroll
         for (int t = 0; t < kTb; ++t) {
-            if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);  // not all tokens' gates at once: the registers again
-            const bool live = p.t0 + t < p.len, start = (starts >> t) & 1;
+            const bool live = bit(lives, t), start = bit(starts, t);
+            x[t].keep(live);
+            r[t].keep(live);
+            i[t].keep(live);
+            gy[t].keep(live);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float d, om;
@@ -296,108 +411,115 @@ struct Back {
                 gi[t][j] = sigmoid_f(i[t].get(j) + w.ib[j]);
                 decay(s[t][j] * w.nA[j], d, om);
                 const float in = __builtin_amdgcn_sqrtf(om * (1.0f + d)) * gi[t][j] * x[t].get(j);
-                a[t][j] = live ? (start ? 0.0f : d) : 1.0f;
-                v[t][j] = live ? in : 0.0f;
-                A[j] *= a[t][j];
-                H[j] = fmaf(a[t][j], H[j], v[t][j]);
+                a[t][j] = live ? d : 1.0f;
+                v[t][j] = in;
+                // here and now: the compiler would put part of every token off, and hold what that part needs
+                asm volatile("" : "+v"(a[t][j]), "+v"(v[t][j]), "+v"(s[t][j]), "+v"(gi[t][j]));
+                A[j] = start ? __uint_as_float(kCut) : A[j] * a[t][j];
+                H[j] = start ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
             }
         }
 #pragma unroll
         for (int t = kTb - 1; t >= 0; --t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) N[j] = a[t][j] * ((p.t0 + t < p.len ? gy[t].get(j) : 0.0f) + N[j]);
+            for (int j = 0; j < 2; ++j)
+                N[j] = bit(starts, t) ? 0.0f : a[t][j] * (gy[t].get(j) + N[j]);
     }
 };
 
-template <typename T, bool PAIR>
-__global__ __launch_bounds__(kThreads, 4) void ssd_glr_back_tiles_kernel(GlrArgs g, float* agg) {
-    __shared__ float2 sA[kWaves][64], sN[kWaves][64];
-    const Place p(g, blockIdx.x, kTileB, kTb);
-    const Lane<PAIR> ln(p.blk, g.D);
-    Params w;
-    w.load(g, ln);
-    Back<T, PAIR> s;
-    s.compute(g, p, ln, w);
-    const int wave = wave_id(), l = threadIdx.x % 64;
-    sA[wave][l] = make_float2(s.A[0], s.A[1]);
-    sN[wave][l] = make_float2(s.N[0], s.N[1]);
-    __syncthreads();
-    if (wave || !ln.on) return;
-    float A[2] = {1.0f, 1.0f}, N[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int k = kWaves - 1; k >= 0; --k) {
-        const float2 a = sA[k][l], n = sN[k][l];
-        A[0] *= a.x; A[1] *= a.y;
-        N[0] = fmaf(a.x, N[0], n.x);
-        N[1] = fmaf(a.y, N[1], n.y);
-    }
-    float* out = agg + ((size_t)p.b * g.tiles + p.c) * 2 * g.D;
-    Two<float, PAIR>::store(out, ln.c, 0, g.D, A[0], A[1]);
-    Two<float, PAIR>::store(out + g.D, ln.c, 0, g.D, N[0], N[1]);
-}
-
-// enter: the adjoint that enters every tile from behind.  part: [tile of all rows][3][D], a tile's sums of dA, dr_bias
-// and di_bias.
-template <typename T, bool PAIR>
-__global__ __launch_bounds__(kThreads, 4) void ssd_glr_back_kernel(GlrArgs g, const float* enter, float* part) {
-    __shared__ float2 sA[kWaves][64], sH[kWaves][64], sN[kWaves][64];
-    const Place p(g, blockIdx.x, kTileB, kTb);
+// The chain runs from a row's last tile.  part: [tile of all rows][3][D], a tile's sums of dA, dr_bias and di_bias.
+// fp32 operands take the registers of one workgroup a CU; as many bytes are on their way then as with two in bf16.
+template <typename T, bool PAIR, bool CHAIN>
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 4 : 2)) void ssd_glr_back_kernel(GlrArgs g, Chain ch, float* part) {
+    __shared__ float2 sA[kWaves][64], sH[kWaves][64], sN[kWaves][64], pA[CHAIN ? kWaves : 1][64], pN[CHAIN ? kWaves : 1][64], in[64];
+    Place p(g, CHAIN ? chain_place(ch) : blockIdx.x, kTileB, kTb);
+    const int place = p.c;
+    p.c = g.tiles - 1 - place;
+    p.t0 = p.c * kTileB + wave_id() * kTb;
     const Lane<PAIR> ln(p.blk, g.D);
     Params w;
     w.load(g, ln);
     Back<T, PAIR> s;
     s.compute(g, p, ln, w);
     const size_t tile = (size_t)p.b * g.tiles + p.c;
-    Two<float, PAIR> e, n;
+    Two<float, PAIR> e;
     e.load(g.states + tile * g.D, ln.c, ln.last);
-    n.load(enter + tile * g.D, ln.c, ln.last);
-    float h[2] = {e.get(0), e.get(1)}, nu[2] = {n.get(0), n.get(1)};
+    float h[2] = {e.get(0), e.get(1)}, nu[2] = {0.0f, 0.0f};
+    if (place == 0 && g.g_final) {
+        e.load(g.g_final + (size_t)p.b * g.D, ln.c, ln.last);
+        nu[0] = e.get(0);
+        nu[1] = e.get(1);
+    }
     const int wave = wave_id(), l = threadIdx.x % 64;
     sA[wave][l] = make_float2(s.A[0], s.A[1]);
     sH[wave][l] = make_float2(s.H[0], s.H[1]);
     sN[wave][l] = make_float2(s.N[0], s.N[1]);
     __syncthreads();
+    if constexpr (CHAIN) {
+        if (wave == kWaves - 1) {
+            float2 A = place == 0 ? make_float2(__uint_as_float(kCut), __uint_as_float(kCut)) : make_float2(1.0f, 1.0f);
+            float2 N = make_float2(nu[0], nu[1]);
+#pragma unroll 2
+            for (int k = kWaves - 1; k >= 0; --k) {
+                const float2 a = sA[k][l], n = sN[k][l];
+                then(A.x, N.x, a.x, n.x);
+                then(A.y, N.y, a.y, n.y);
+            }
+            publish(ch.pairs + ((size_t)p.b * g.tiles + place) * g.D, ln, g.D, A, N);
+        }
+        chain_gather(ch, p.b, place, g.tiles, g.D, ln, pA, pN, in);
+        __syncthreads();
+        chain_enter(place, pA, pN, in, nu);
+    }
     for (int k = 0; k < wave; ++k) {
         const float2 a = sA[k][l], v = sH[k][l];
-        h[0] = fmaf(a.x, h[0], v.x);
-        h[1] = fmaf(a.y, h[1], v.y);
+        h[0] = through(a.x, v.x, h[0]);
+        h[1] = through(a.y, v.y, h[1]);
     }
     for (int k = kWaves - 1; k > wave; --k) {
         const float2 a = sA[k][l], v = sN[k][l];
-        nu[0] = fmaf(a.x, nu[0], v.x);
-        nu[1] = fmaf(a.y, nu[1], v.y);
+        nu[0] = through(a.x, v.x, nu[0]);
+        nu[1] = through(a.y, v.y, nu[1]);
+    }
+    if constexpr (CHAIN) {
+        if (wave == 0 && place % kGroup == kGroup - 1 && place + 1 < g.tiles)
+            publish(ch.enter + ((size_t)p.b * (ch.groups - 1) + place / kGroup) * g.D, ln, g.D, make_float2(0.0f, 0.0f),
+                    make_float2(through(s.A[0], s.N[0], nu[0]), through(s.A[1], s.N[1], nu[1])));
     }
 #pragma unroll
     for (int t = 0; t < kTb; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float held = s.a[t][j] * h[j];
+            const float held = bit(s.starts, t) ? 0.0f : s.a[t][j] * h[j];
             h[j] = held + s.v[t][j];
-            s.v[t][j] = held;
-            // the decays below are computed again from s: kept from above, they would not fit the registers
-            asm volatile("" : "+v"(s.s[t][j]));
+            s.v[t][j] = bit(s.lives, t) ? held : 0.0f;
         }
+#pragma unroll
+    for (int t = 0; t < kTb; ++t) {
+        s.x[t].hide();
+        s.gy[t].hide();
+    }
     T* dxp = static_cast<T*>(g.dx);
     T* drp = static_cast<T*>(g.dr);
     T* dip = static_cast<T*>(g.di);
     float sum[3][2] = {};
 #pragma unroll
     for (int t = kTb - 1; t >= 0; --t) {
-        const bool live = p.t0 + t < p.len;
+        const bool live = bit(s.lives, t);
         float dx[2], dr[2], di[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float lam = (live ? s.gy[t].get(j) : 0.0f) + nu[j];
-            nu[j] = s.a[t][j] * lam;
-            float d, om;
-            decay(s.s[t][j] * w.nA[j], d, om);
-            const float m2 = om * (1.0f + d), inv = m2 > 0.0f ? __builtin_amdgcn_rsqf(m2) : 0.0f;
+            const float all = s.gy[t].get(j) + nu[j], lam = live ? all : 0.0f;
+            nu[j] = bit(s.starts, t) ? 0.0f : s.a[t][j] * all;
+            const float d = s.a[t][j], n = s.s[t][j] * w.nA[j], om = n < kSeries ? one_minus(n) : 1.0f - d;
+            const float m2 = om * (1.0f + d);
+            const float inv = __uint_as_float(__float_as_uint(__builtin_amdgcn_rsqf(m2)) & (m2 > 0.0f ? ~0u : 0u));
             const float x = s.x[t].get(j), gi = s.gi[t][j], lm = lam * m2 * inv;
-            dx[j] = live ? lm * gi : 0.0f;
-            di[j] = live ? lm * x * gi * (1.0f - gi) : 0.0f;
-            const float dl = live ? lam * (s.v[t][j] - gi * x * d * d * inv) : 0.0f;
-            dr[j] = live ? -dl * w.nA[j] * s.s[t][j] * (1.0f - s.s[t][j]) : 0.0f;
-            sum[0][j] = live ? fmaf(dl, s.s[t][j], sum[0][j]) : sum[0][j];
+            dx[j] = lm * gi;
+            di[j] = lm * x * gi * (1.0f - gi);
+            const float dl = lam * (s.v[t][j] - gi * x * d * d * inv);
+            dr[j] = -dl * w.nA[j] * s.s[t][j] * (1.0f - s.s[t][j]);
+            sum[0][j] = fmaf(dl, s.s[t][j], sum[0][j]);
             sum[1][j] += dr[j];
             sum[2][j] += di[j];
         }
@@ -512,52 +634,63 @@ int cols(int D) { return (D + kCols - 1) / kCols; }
 int tiles_of(int L, int tile) { return (int)(((int64_t)L + tile - 1) / tile); }
 size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
 
+// the chain of a launch over `tiles` tiles a row, in n bytes at `ws`
+size_t chain_bytes(int B, int D, int tiles) {
+    if (tiles <= 1) return 0;
+    return 256 + pad16((size_t)B * D * (tiles + (tiles + kGroup - 1) / kGroup - 1) * sizeof(uint64_t));
+}
+hipError_t make_chain(Chain& ch, int B, int D, int tiles, char* ws, hipStream_t s) {
+    ch.groups = (tiles + kGroup - 1) / kGroup;
+    ch.ticket = reinterpret_cast<uint32_t*>(ws);
+    ch.pairs = reinterpret_cast<uint64_t*>(ws + 256);
+    ch.enter = ch.pairs + (size_t)B * tiles * D;
+    const int64_t n = (int64_t)(chain_bytes(B, D, tiles) / 16);
+    hipLaunchKernelGGL(ssd_glr_unset_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), 0, s,
+                       reinterpret_cast<uint4*>(ws), n);
+    return hipGetLastError();
+}
+
 template <typename T, bool PAIR>
-hipError_t fwd_t(GlrArgs a, void* ws, hipStream_t s) {
+hipError_t fwd_t(GlrArgs a, char* ws, hipStream_t s) {
     a.tiles = tiles_of(a.L, kTile<T>);
     const dim3 grid((unsigned)(a.tiles * (int64_t)a.B * cols(a.D)));
-    float *agg = static_cast<float*>(ws), *enter = nullptr;
+    Chain ch{};
     if (a.tiles > 1) {
-        enter = agg + (size_t)a.B * a.tiles * 2 * a.D;
-        hipLaunchKernelGGL((ssd_glr_tiles_kernel<T, PAIR>), grid, dim3(kThreads), 0, s, a, agg);
-        if (hipError_t e = hipGetLastError()) return e;
-        hipLaunchKernelGGL(ssd_glr_fold_kernel, dim3((unsigned)(((int64_t)a.B * a.D + 255) / 256)), dim3(256), 0, s, agg,
-                           a.init_state, enter, a.B, a.D, a.tiles, 0);
-        if (hipError_t e = hipGetLastError()) return e;
+        if (hipError_t e = make_chain(ch, a.B, a.D, a.tiles, ws, s)) return e;
+        hipLaunchKernelGGL((ssd_glr_scan_kernel<T, PAIR, true>), grid, dim3(kThreads), 0, s, a, ch);
+    } else {
+        hipLaunchKernelGGL((ssd_glr_scan_kernel<T, PAIR, false>), grid, dim3(kThreads), 0, s, a, ch);
     }
-    hipLaunchKernelGGL((ssd_glr_scan_kernel<T, PAIR>), grid, dim3(kThreads), 0, s, a, enter);
     return hipGetLastError();
 }
 
 size_t fwd_bytes(int B, int L, int D, int dtype) {
-    const int tiles = tiles_of(L, dtype == 0 ? kTile<float> : kTile<uint16_t>);
-    return tiles > 1 ? pad16((size_t)B * tiles * 3 * D * sizeof(float)) : 0;
+    return chain_bytes(B, D, tiles_of(L, dtype == 0 ? kTile<float> : kTile<uint16_t>));
 }
 size_t states_bytes(int B, int L, int D) { return pad16((size_t)B * tiles_of(L, kTileB) * D * sizeof(float)); }
 
 template <typename T, bool PAIR>
-hipError_t bwd_t(GlrArgs a, void* ws, hipStream_t s) {
-    char* at = static_cast<char*>(ws);
+hipError_t bwd_t(GlrArgs a, char* ws, hipStream_t s) {
     if (!a.states) {
-        a.states = reinterpret_cast<float*>(at);
-        at += states_bytes(a.B, a.L, a.D);
+        a.states = reinterpret_cast<float*>(ws);
+        ws += states_bytes(a.B, a.L, a.D);
         GlrArgs f = a;
         f.y = nullptr;
         f.final_state = nullptr;
-        if (hipError_t e = fwd_t<T, PAIR>(f, at, s)) return e;
-        at += fwd_bytes(a.B, a.L, a.D, a.dtype);
+        if (hipError_t e = fwd_t<T, PAIR>(f, ws, s)) return e;
+        ws += fwd_bytes(a.B, a.L, a.D, a.dtype);
     }
     a.tiles = tiles_of(a.L, kTileB);
-    const size_t n = (size_t)a.B * a.tiles * a.D;
-    float* agg = reinterpret_cast<float*>(at);
-    float *enter = agg + 2 * n, *part = enter + n;
+    float* part = reinterpret_cast<float*>(ws);
+    ws += pad16((size_t)a.B * a.tiles * 3 * a.D * sizeof(float));
     const dim3 grid((unsigned)(a.tiles * (int64_t)a.B * cols(a.D)));
-    hipLaunchKernelGGL((ssd_glr_back_tiles_kernel<T, PAIR>), grid, dim3(kThreads), 0, s, a, agg);
-    if (hipError_t e = hipGetLastError()) return e;
-    hipLaunchKernelGGL(ssd_glr_fold_kernel, dim3((unsigned)(((int64_t)a.B * a.D + 255) / 256)), dim3(256), 0, s, agg, a.g_final,
-                       enter, a.B, a.D, a.tiles, 1);
-    if (hipError_t e = hipGetLastError()) return e;
-    hipLaunchKernelGGL((ssd_glr_back_kernel<T, PAIR>), grid, dim3(kThreads), 0, s, a, enter, part);
+    Chain ch{};
+    if (a.tiles > 1) {
+        if (hipError_t e = make_chain(ch, a.B, a.D, a.tiles, ws, s)) return e;
+        hipLaunchKernelGGL((ssd_glr_back_kernel<T, PAIR, true>), grid, dim3(kThreads), 0, s, a, ch, part);
+    } else {
+        hipLaunchKernelGGL((ssd_glr_back_kernel<T, PAIR, false>), grid, dim3(kThreads), 0, s, a, ch, part);
+    }
     if (hipError_t e = hipGetLastError()) return e;
     hipLaunchKernelGGL(ssd_glr_sum_kernel, dim3((unsigned)((3LL * a.D + 31) / 32)), dim3(1024), 0, s, part,
                        (int64_t)a.B * a.tiles, a.D, a.dA, a.dr_bias, a.di_bias);
@@ -568,15 +701,18 @@ hipError_t bwd_t(GlrArgs a, void* ws, hipStream_t s) {
 
 size_t glr_fwd_workspace_bytes(int B, int L, int D, int dtype) { return fwd_bytes(B, L, D, dtype); }
 size_t glr_bwd_workspace_bytes(int B, int L, int D, int dtype) {
-    const size_t n = (size_t)B * tiles_of(L, kTileB) * D * sizeof(float);
-    return states_bytes(B, L, D) + fwd_bytes(B, L, D, dtype) + 6 * n;
+    const int tiles = tiles_of(L, kTileB);
+    return states_bytes(B, L, D) + fwd_bytes(B, L, D, dtype) + pad16((size_t)B * tiles * 3 * D * sizeof(float)) +
+           chain_bytes(B, D, tiles);
 }
 
-hipError_t launch_glr_fwd(const GlrArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_glr_fwd(const GlrArgs& a, void* workspace, hipStream_t s) {
+    char* ws = static_cast<char*>(workspace);
     if (a.dtype == 0) return a.pair ? fwd_t<float, true>(a, ws, s) : fwd_t<float, false>(a, ws, s);
     return a.pair ? fwd_t<uint16_t, true>(a, ws, s) : fwd_t<uint16_t, false>(a, ws, s);
 }
-hipError_t launch_glr_bwd(const GlrArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_glr_bwd(const GlrArgs& a, void* workspace, hipStream_t s) {
+    char* ws = static_cast<char*>(workspace);
     if (a.dtype == 0) return a.pair ? bwd_t<float, true>(a, ws, s) : bwd_t<float, false>(a, ws, s);
     return a.pair ? bwd_t<uint16_t, true>(a, ws, s) : bwd_t<uint16_t, false>(a, ws, s);
 }

@@ -330,3 +330,36 @@ def test_glr_empty(gpu_lib):
     g = ssd.ssd_glr_scan_bwd(e, e, e, A, e, r_bias=A)
     assert (g["A"] == 0).all() and (g["r_bias"] == 0).all() and g["x"].shape == (0, 9, 6)
     assert ssd.ssd_glr_step(e[:, 0], e[:, 0], e[:, 0], A, torch.zeros(0, 6, device=DEV)).shape == (0, 6)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_glr_documents_keep_nan_to_themselves(gpu_lib, t):
+    """NaN and infinities in a document reach no other: the state of later ones (within a stretch, a tile and across
+    tiles), and the gradients of earlier ones.  Behind a row's length gradients are 0 whatever the row holds."""
+    ssd, (B, L, D) = gpu_lib, (2, 2500, 34)
+    d = make(B, L, D, t, state=True)
+    cuts = [0, 3, 70, 400, 1500, 2400]
+    ids = torch.zeros(L, dtype=torch.int32)
+    for c in cuts:
+        ids[c:] += 1
+    d["doc_ids"], d["lengths"] = ids.repeat(B, 1), torch.tensor([L, 2450], dtype=torch.int32)
+    g = to_dev(d)
+    clean, cleanb = fwd(ssd, g), bwd(ssd, g)
+    for lo, hi in zip(cuts, cuts[1:] + [L]):
+        e = {n: None if v is None else v.clone() for n, v in g.items()}
+        e["x"][:, lo, ::2], e["r"][:, lo, 1::2] = float("inf"), float("nan")
+        if lo == 0:
+            e["init_state"].fill_(float("nan"))
+        y = fwd(ssd, e)["y"]
+        out = [k for k in range(L) if not lo <= k < hi]
+        assert torch.equal(y[:, out], clean["y"][:, out]) and not torch.isfinite(y[0, hi - 1]).any()
+        e = {n: None if v is None else v.clone() for n, v in g.items()}
+        e["grad_y"][:, hi - 1] = float("nan")
+        if hi == L:
+            e["grad_final_state"].fill_(float("inf"))
+        back = bwd(ssd, e)
+        for n in ("x", "r", "i"):
+            assert torch.equal(back[n][:, out], cleanb[n][:, out]) and (back[n][1, 2450:] == 0).all()
+    e = {n: None if v is None else v.clone() for n, v in g.items()}
+    e["x"][1, 2449] = float("inf")
+    assert all((bwd(ssd, e)[n][1, 2450:] == 0).all() for n in ("x", "r", "i"))
