@@ -35,91 +35,99 @@ template <typename T> constexpr int kTw = sizeof(T) == 2 ? 16 : 8;      // token
 template <typename T> constexpr int kTile = kTw<T> * kWaves;
 
 // ------------------------------------------------------------ a lane's two channels
-// PAIR: neighbours, read together (even widths and strides, bases on pairs); else 64 apart
-// hide(): the compiler forgets what it knows of the values, so that it does not keep what it has made of them
-template <typename T, bool PAIR> struct Two;
-template <> struct Two<float, true> {
-    float2 v;
-    __device__ __forceinline__ void load(const float* p, int c, int) { v = *reinterpret_cast<const float2*>(p + c); }
-    __device__ __forceinline__ float get(int j) const { return j ? v.y : v.x; }
-    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v.x), "+v"(v.y)); }
-    __device__ __forceinline__ void keep(bool on) { v = make_float2(on ? v.x : 0.0f, on ? v.y : 0.0f); }
-    __device__ __forceinline__ static void store(float* p, int c, int, int, float a, float b) {
-        *reinterpret_cast<float2*>(p + c) = make_float2(a, b);
-    }
-};
-template <> struct Two<uint16_t, true> {
-    uint32_t v;
-    __device__ __forceinline__ void load(const uint16_t* p, int c, int) { v = *reinterpret_cast<const uint32_t*>(p + c); }
-    __device__ __forceinline__ float get(int j) const { return j ? bf16_hi(v) : bf16_lo(v); }
-    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
-    __device__ __forceinline__ void keep(bool on) { v = on ? v : 0; }
-    __device__ __forceinline__ static void store(uint16_t* p, int c, int, int, float a, float b) {
-        *reinterpret_cast<uint32_t*>(p + c) = pack_bf16x2(a, b);
-    }
-};
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(uint16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
 __device__ __forceinline__ void narrow(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
-template <> struct Two<float, false> {
-    float2 v;
-    // channels past the last are read from it
-    __device__ __forceinline__ void load(const float* p, int c, int last) { v = make_float2(p[min(c, last)], p[min(c + 64, last)]); }
-    __device__ __forceinline__ float get(int j) const { return j ? v.y : v.x; }
-    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v.x), "+v"(v.y)); }
-    __device__ __forceinline__ void keep(bool on) { v = make_float2(on ? v.x : 0.0f, on ? v.y : 0.0f); }
-    __device__ __forceinline__ static void store(float* p, int c, int, int D, float a, float b) {
-        if (c < D) p[c] = a;
-        if (c + 64 < D) p[c + 64] = b;
-    }
-};
-template <> struct Two<uint16_t, false> {
-    uint32_t v;
-    __device__ __forceinline__ void load(const uint16_t* p, int c, int last) {
-        v = p[min(c, last)] | (uint32_t)p[min(c + 64, last)] << 16;
-    }
-    __device__ __forceinline__ float get(int j) const { return j ? bf16_hi(v) : bf16_lo(v); }
-    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
-    __device__ __forceinline__ void keep(bool on) { v = on ? v : 0; }
-    __device__ __forceinline__ static void store(uint16_t* p, int c, int, int D, float a, float b) {
-        if (c < D) narrow(p + c, a);
-        if (c + 64 < D) narrow(p + c + 64, b);
-    }
-};
-// the first of a lane's channels; a lane whose channels are all past D is off (PAIR: it reads the last pair)
+
+// Column c of a row whose address is the wave's: an unsigned offset of 32 bits keeps that address in scalars.
+template <typename V, typename T>
+__device__ __forceinline__ const V* column(const T* row, uint32_t c) {
+    return reinterpret_cast<const V*>(reinterpret_cast<const char*>(row) + c * (uint32_t)sizeof(T));
+}
+template <typename V, typename T>
+__device__ __forceinline__ V* column(T* row, uint32_t c) {
+    return reinterpret_cast<V*>(reinterpret_cast<char*>(row) + c * (uint32_t)sizeof(T));
+}
+
+// PAIR: neighbours, read together (even widths and strides, bases on pairs); else 64 apart.  Channels past the last are
+// read from it and not written.
 template <bool PAIR>
 struct Lane {
-    int c, last;
-    bool on;
+    uint32_t c[2];
+    bool on, on1;
     __device__ __forceinline__ Lane(int blk, int D) {
-        const int l = threadIdx.x % 64;
-        c = blk * kCols + (PAIR ? 2 * l : l);
-        on = c < D;
-        last = D - 1;
-        if (PAIR) c = min(c, D - 2);
+        const int l = threadIdx.x % 64, c0 = blk * kCols + (PAIR ? 2 * l : l), c1 = PAIR ? c0 + 1 : c0 + 64;
+        on = c0 < D;
+        on1 = c1 < D;                               // PAIR: D is even
+        c[0] = (uint32_t)min(c0, PAIR ? D - 2 : D - 1);
+        c[1] = (uint32_t)min(c1, D - 1);
     }
 };
+
+// two channels of a row as they are in memory
+// hide(): the compiler forgets what it knows of the values, so that it does not keep what it has made of them
+template <typename T> struct Two;
+template <> struct Two<float> {
+    float2 v;
+    __device__ __forceinline__ float get(int j) const { return j ? v.y : v.x; }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v.x), "+v"(v.y)); }
+    __device__ __forceinline__ void keep(bool on, float off) { v = make_float2(on ? v.x : off, on ? v.y : off); }
+};
+template <> struct Two<uint16_t> {
+    uint32_t v;
+    __device__ __forceinline__ float get(int j) const { return j ? bf16_hi(v) : bf16_lo(v); }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
+    __device__ __forceinline__ void keep(bool on, float off) { v = on ? v : (__float_as_uint(off) >> 16) * 0x10001u; }
+};
+template <bool PAIR>
+__device__ __forceinline__ Two<float> load2(const float* row, const Lane<PAIR>& ln) {
+    if (PAIR) return {*column<float2>(row, ln.c[0])};
+    return {make_float2(*column<float>(row, ln.c[0]), *column<float>(row, ln.c[1]))};
+}
+template <bool PAIR>
+__device__ __forceinline__ Two<uint16_t> load2(const uint16_t* row, const Lane<PAIR>& ln) {
+    if (PAIR) return {*column<uint32_t>(row, ln.c[0])};
+    return {*column<uint16_t>(row, ln.c[0]) | (uint32_t)*column<uint16_t>(row, ln.c[1]) << 16};
+}
+template <bool PAIR>
+__device__ __forceinline__ void store2(float* row, const Lane<PAIR>& ln, float a, float b) {
+    if (PAIR) {
+        if (ln.on) *column<float2>(row, ln.c[0]) = make_float2(a, b);
+    } else {
+        if (ln.on) *column<float>(row, ln.c[0]) = a;
+        if (ln.on1) *column<float>(row, ln.c[1]) = b;
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void store2(uint16_t* row, const Lane<PAIR>& ln, float a, float b) {
+    if (PAIR) {
+        if (ln.on) *column<uint32_t>(row, ln.c[0]) = pack_bf16x2(a, b);
+    } else {
+        if (ln.on) narrow(column<uint16_t>(row, ln.c[0]), a);
+        if (ln.on1) narrow(column<uint16_t>(row, ln.c[1]), b);
+    }
+}
 
 // ------------------------------------------------------------ the gates
 __device__ __forceinline__ float sigmoid_f(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
 
-// decay a = e^-n and 1 - a.  A decay near 1 is what a long memory rests on: there 1 - a comes from its series (7 terms,
-// off by n^7 / 8! of itself, 2e-8 at the border) and a from 1 - a by one rounding, so that neither the hardware exp2's
+// decay a = e^-n and 1 - a.  A decay near 1 is what a long memory rests on: there 1 - a comes from its series (6 terms,
+// off by n^6 / 7! of itself, 5e-8 at the border) and a from 1 - a by one rounding, so that neither the hardware exp2's
 // error nor the difference's shows: over thousands of tokens a decay that is off by one step the same way each time
-// would move the state by some 1e-5.  From the border on the hardware's exp2 and the difference are within 2^-22.
+// would move the state by some 1e-5.  From the border on the hardware's exp2 and the difference are within 2^-21.
+constexpr float kSeries = 0.25f;
 __device__ __forceinline__ float one_minus(float n) {
-    float q = fmaf(n, -1.0f / 5040.0f, 1.0f / 720.0f);
-    q = fmaf(n, -q, 1.0f / 120.0f);
+    float q = fmaf(n, -1.0f / 720.0f, 1.0f / 120.0f);
     q = fmaf(n, -q, 1.0f / 24.0f);
     q = fmaf(n, -q, 1.0f / 6.0f);
     q = fmaf(n, -q, 0.5f);
     q = fmaf(n, -q, 1.0f);
     return q * n;
 }
-constexpr float kSeries = 0.35f;
-__device__ __forceinline__ void decay(float n, float& a, float& om) {
-    const float q = one_minus(n), e = fast_exp2(-n * kLog2e);
+// e: the hardware's e^-n
+__device__ __forceinline__ void decay(float n, float e, float& a, float& om) {
+    const float q = one_minus(n);
     a = n < kSeries ? 1.0f - q : e;
     om = n < kSeries ? q : 1.0f - e;
 }
@@ -141,22 +149,26 @@ __device__ __forceinline__ void then(float& A, float& H, float A2, float H2) {
     A = is_cut(A2) ? A2 : A * A2;
 }
 
+// the wave's number, known to the compiler to be the same for its lanes: rows are then addressed by scalars
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+
+// a lane's parameters: -A, A log2 e and the biases times -log2 e, for sigmoid(v + bias) = 1 / (1 + 2^(-v log2 e - bias log2 e))
 struct Params {
-    float nA[2], rb[2], ib[2];
+    float nA[2], A2[2], rb[2], ib[2];
     template <bool PAIR>
     __device__ __forceinline__ void load(const GlrArgs& a, const Lane<PAIR>& ln) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int c = min(PAIR ? ln.c + j : ln.c + 64 * j, ln.last);
-            nA[j] = -a.A[c];
-            rb[j] = a.r_bias ? a.r_bias[c] : 0.0f;
-            ib[j] = a.i_bias ? a.i_bias[c] : 0.0f;
+            const float A = *column<float>(a.A, ln.c[j]);
+            nA[j] = -A;
+            A2[j] = A * kLog2e;
+            rb[j] = a.r_bias ? -kLog2e * *column<float>(a.r_bias, ln.c[j]) : 0.0f;
+            ib[j] = a.i_bias ? -kLog2e * *column<float>(a.i_bias, ln.c[j]) : 0.0f;
         }
     }
+    __device__ __forceinline__ float r_gate(float v, int j) const { return fast_rcp(1.0f + fast_exp2(fmaf(v, -kLog2e, rb[j]))); }
+    __device__ __forceinline__ float i_gate(float v, int j) const { return fast_rcp(1.0f + fast_exp2(fmaf(v, -kLog2e, ib[j]))); }
 };
-
-// the wave's number, known to the compiler to be the same for its lanes: rows are then addressed by scalars
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
 // What a wave knows of its place: batch row, tile, first token, tokens that are real
 struct Place {
@@ -171,50 +183,78 @@ struct Place {
     }
 };
 
-// bits of a wave's n tokens: those that start a document, those that are real.  In vector registers, though the same in
-// every lane: of scalars the compiler makes a branch a token.
-__device__ __forceinline__ void masks(const GlrArgs& g, const Place& p, int n, uint32_t& starts, uint32_t& lives) {
-    const int k = max(0, min(p.len - p.t0, n));
-    lives = (1u << k) - 1;                          // n <= 16
-    starts = (uint32_t)starts_in(g.doc ? g.doc + (size_t)p.b * g.L : nullptr, p.t0, n, g.L) & lives;
-    asm volatile("" : "+v"(starts), "+v"(lives));
-}
+// Bits of a wave's n <= 16 tokens: those that start a document, those that are real.  In vector registers, though the same
+// in every lane: of scalars the compiler makes a branch a token.  plain: none starts and all are real.
+struct Masks {
+    uint32_t starts, lives;
+    bool plain;
+    __device__ __forceinline__ Masks(const GlrArgs& g, const Place& p, int n) {
+        lives = (1u << max(0, min(p.len - p.t0, n))) - 1;
+        starts = (uint32_t)starts_in(g.doc ? g.doc + (size_t)p.b * g.L : nullptr, p.t0, n, g.L) & lives;
+        plain = starts == 0 && lives == (1u << n) - 1;
+        asm volatile("" : "+v"(starts), "+v"(lives));
+    }
+};
 __device__ __forceinline__ bool bit(uint32_t mask, int t) { return (mask >> t) & 1; }
+
+// rows of a wave's tokens: the address of its first (past the row's end its last stands in), and of those after it
+template <typename T>
+struct Rows {
+    T* first;
+    int stride, most;                               // elements; tokens after the first
+    __device__ __forceinline__ Rows(T* p, int64_t s, const GlrArgs& g, const Place& p0) {
+        const int t = min(p0.t0, g.L - 1);
+        first = p + ((int64_t)p0.b * g.L + t) * s;
+        stride = (int)s;
+        most = g.L - 1 - t;
+    }
+    __device__ __forceinline__ T* at(int t) const { return first + (int64_t)(min(t, most) * stride); }
+};
+
+// A token that is not real decays by 1 and takes nothing in: its decay gate is that of -inf, its inputs are 0.
+template <typename T>
+__device__ __forceinline__ void blank(Two<T>& x, Two<T>& r, Two<T>& i, bool live) {
+    x.keep(live, 0.0f);
+    r.keep(live, -INFINITY);
+    i.keep(live, 0.0f);
+}
 
 // decays and inputs of a wave's tokens, and their composition
 template <typename T, bool PAIR, int Tw>
 struct Stretch {
     float a[Tw][2], v[Tw][2];
     float A[2], H[2];
-    uint32_t starts, lives;                               // bits of the tokens
-    __device__ __forceinline__ void compute(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Params& w) {
-        Two<T, PAIR> x[Tw], r[Tw], i[Tw];
-        const T* xp = static_cast<const T*>(g.x);
-        const T* rp = static_cast<const T*>(g.r);
-        const T* ip = static_cast<const T*>(g.i);
+    __device__ __forceinline__ void gates(const Two<T> (&x)[Tw], const Two<T> (&r)[Tw], const Two<T> (&i)[Tw], const Params& w,
+                                          const Masks& m) {
 #pragma unroll
-        for (int t = 0; t < Tw; ++t) {
-            const int64_t row = (int64_t)p.b * g.L + min(p.t0 + t, g.L - 1);
-            x[t].load(xp + row * g.x_stride, ln.c, ln.last);
-            r[t].load(rp + row * g.r_stride, ln.c, ln.last);
-            i[t].load(ip + row * g.i_stride, ln.c, ln.last);
-        }
-        masks(g, p, Tw, starts, lives);
-        A[0] = A[1] = 1.0f;
-        H[0] = H[1] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < Tw; ++t) {
-            const bool live = bit(lives, t), start = bit(starts, t);
+        for (int t = 0; t < Tw; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float d, om;
-                decay(sigmoid_f(r[t].get(j) + w.rb[j]) * w.nA[j], d, om);
-                const float in = __builtin_amdgcn_sqrtf(om * (1.0f + d)) * sigmoid_f(i[t].get(j) + w.ib[j]) * x[t].get(j);
-                a[t][j] = live ? d : 1.0f;
-                v[t][j] = live ? in : 0.0f;
-                A[j] = start ? __uint_as_float(kCut) : A[j] * a[t][j];
-                H[j] = start ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
+                const float s = w.r_gate(r[t].get(j), j);
+                float om;
+                decay(s * w.nA[j], fast_exp2(s * w.A2[j]), a[t][j], om);
+                v[t][j] = __builtin_amdgcn_sqrtf(om * (1.0f + a[t][j])) * w.i_gate(i[t].get(j), j) * x[t].get(j);
+                // here and now: the compiler would put part of every token off, and hold what that part needs
+                asm volatile("" : "+v"(a[t][j]), "+v"(v[t][j]));
             }
+        A[0] = A[1] = 1.0f;
+        H[0] = H[1] = 0.0f;
+        if (m.plain) {
+#pragma unroll
+            for (int t = 0; t < Tw; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    A[j] *= a[t][j];
+                    H[j] = fmaf(a[t][j], H[j], v[t][j]);
+                }
+        } else {
+#pragma unroll
+            for (int t = 0; t < Tw; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    A[j] = bit(m.starts, t) ? __uint_as_float(kCut) : A[j] * a[t][j];
+                    H[j] = bit(m.starts, t) ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
+                }
         }
     }
 };
@@ -240,17 +280,15 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 template <bool PAIR>
-__device__ __forceinline__ void publish(uint64_t* row, const Lane<PAIR>& ln, int D, float2 A, float2 H) {
-    const int c1 = PAIR ? ln.c + 1 : ln.c + 64;
-    if (ln.on) __hip_atomic_store(row + ln.c, pack_pair(A.x, H.x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (ln.on && c1 < D) __hip_atomic_store(row + c1, pack_pair(A.y, H.y), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void publish(uint64_t* row, const Lane<PAIR>& ln, float2 A, float2 H) {
+    if (ln.on) __hip_atomic_store(column<uint64_t>(row, ln.c[0]), pack_pair(A.x, H.x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (ln.on1) __hip_atomic_store(column<uint64_t>(row, ln.c[1]), pack_pair(A.y, H.y), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 template <bool PAIR>
 __device__ __forceinline__ void await(const uint64_t* row, const Lane<PAIR>& ln, uint64_t (&w)[2]) {
-    const int c0 = min(ln.c, ln.last), c1 = min(PAIR ? ln.c + 1 : ln.c + 64, ln.last);
     for (;;) {
-        w[0] = peek(row + c0);
-        w[1] = peek(row + c1);
+        w[0] = peek(column<uint64_t>(row, ln.c[0]));
+        w[1] = peek(column<uint64_t>(row, ln.c[1]));
         if (__all(is_set(w[0]) && is_set(w[1]))) return;
         __builtin_amdgcn_s_sleep(1);
     }
@@ -304,69 +342,106 @@ __global__ __launch_bounds__(256) void ssd_glr_unset_kernel(uint4* p, int64_t n)
 }
 
 // ------------------------------------------------------------ forward
-// CHAIN: rows of more than one tile
+// CHAIN: one tile a workgroup, rows of many; else a workgroup walks a row's tiles
+// Two workgroups a CU, except where 16-bit channels are read one by one (twice the registers on their way) or walked.
 template <typename T, bool PAIR, bool CHAIN>
-__global__ __launch_bounds__(kThreads, 4) void ssd_glr_scan_kernel(GlrArgs g, Chain ch) {
+__global__ __launch_bounds__(kThreads, (CHAIN && (PAIR || sizeof(T) == 4) ? 4 : 2)) void ssd_glr_scan_kernel(GlrArgs g, Chain ch) {
     constexpr int Tw = kTw<T>;
-    __shared__ float2 sA[kWaves][64], sH[kWaves][64], pA[CHAIN ? kWaves : 1][64], pH[CHAIN ? kWaves : 1][64], in[64];
-    const Place p(g, CHAIN ? chain_place(ch) : blockIdx.x, kTile<T>, Tw);
+    __shared__ float2 sA[2][kWaves][64], sH[2][kWaves][64], pA[CHAIN ? kWaves : 1][64], pH[CHAIN ? kWaves : 1][64], in[64];
+    Place p(g, CHAIN ? chain_place(ch) : blockIdx.x, kTile<T>, Tw);
     const Lane<PAIR> ln(p.blk, g.D);
+    const int wave = wave_id(), l = threadIdx.x % 64;
     Params w;
     w.load(g, ln);
-    Stretch<T, PAIR, Tw> s;
-    s.compute(g, p, ln, w);
     float h[2] = {0.0f, 0.0f};
     if (p.c == 0 && g.init_state) {
-        Two<float, PAIR> e;
-        e.load(g.init_state + (size_t)p.b * g.D, ln.c, ln.last);
+        const Two<float> e = load2(g.init_state + (size_t)p.b * g.D, ln);
         h[0] = e.get(0);
         h[1] = e.get(1);
     }
-    const int wave = wave_id(), l = threadIdx.x % 64;
-    sA[wave][l] = make_float2(s.A[0], s.A[1]);
-    sH[wave][l] = make_float2(s.H[0], s.H[1]);
-    __syncthreads();                                 // init_state has been read: final_state may be it
-    if constexpr (CHAIN) {
-        if (wave == kWaves - 1) {                    // the first tile starts from the row's own state: a cut
-            float2 A = p.c == 0 ? make_float2(__uint_as_float(kCut), __uint_as_float(kCut)) : make_float2(1.0f, 1.0f);
-            float2 H = make_float2(h[0], h[1]);
+    for (;;) {
+        Stretch<T, PAIR, Tw> s;
+        Two<T> x[Tw], r[Tw], i[Tw];
+        {
+            const Rows<const T> xr(static_cast<const T*>(g.x), g.x_stride, g, p), rr(static_cast<const T*>(g.r), g.r_stride, g, p),
+                ir(static_cast<const T*>(g.i), g.i_stride, g, p);
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) {
-                const float2 a = sA[k][l], v = sH[k][l];
-                then(A.x, H.x, a.x, v.x);
-                then(A.y, H.y, a.y, v.y);
+            for (int t = 0; t < Tw; ++t) {
+                x[t] = load2(xr.at(t), ln);
+                r[t] = load2(rr.at(t), ln);
+                i[t] = load2(ir.at(t), ln);
             }
-            publish(ch.pairs + ((size_t)p.b * g.tiles + p.c) * g.D, ln, g.D, A, H);
         }
-        chain_gather(ch, p.b, p.c, g.tiles, g.D, ln, pA, pH, in);
-        __syncthreads();
-        chain_enter(p.c, pA, pH, in, h);
-    }
-    for (int k = 0; k < wave; ++k) {
-        const float2 a = sA[k][l], v = sH[k][l];
-        h[0] = through(a.x, v.x, h[0]);
-        h[1] = through(a.y, v.y, h[1]);
-    }
-    if constexpr (CHAIN) {
-        if (wave == kWaves - 1 && p.c % kGroup == kGroup - 1 && p.c + 1 < g.tiles)
-            publish(ch.enter + ((size_t)p.b * (ch.groups - 1) + p.c / kGroup) * g.D, ln, g.D, make_float2(0.0f, 0.0f),
-                    make_float2(through(s.A[0], s.H[0], h[0]), through(s.A[1], s.H[1], h[1])));
-    }
-    if (!ln.on || p.t0 >= g.L) return;
-    if (g.states && p.t0 % 64 == 0)
-        Two<float, PAIR>::store(g.states + ((size_t)p.b * ((g.L + 63) / 64) + p.t0 / 64) * g.D, ln.c, 0, g.D, h[0], h[1]);
-    T* yp = static_cast<T*>(g.y);
+        const Masks m(g, p, Tw);
+        if (!m.plain) {
 #pragma unroll
-    for (int t = 0; t < Tw; ++t) {
-        const bool live = bit(s.lives, t), start = bit(s.starts, t);
+            for (int t = 0; t < Tw; ++t) blank(x[t], r[t], i[t], bit(m.lives, t));
+        }
+        s.gates(x, r, i, w, m);
+        const int turn = CHAIN ? 0 : p.c & 1;        // a walk's next tile leaves these alone
+        sA[turn][wave][l] = make_float2(s.A[0], s.A[1]);
+        sH[turn][wave][l] = make_float2(s.H[0], s.H[1]);
+        __syncthreads();                             // init_state has been read: final_state may be it
+        if constexpr (CHAIN) {
+            if (wave == kWaves - 1) {                // the first tile starts from the row's own state: a cut
+                float2 A = p.c == 0 ? make_float2(__uint_as_float(kCut), __uint_as_float(kCut)) : make_float2(1.0f, 1.0f);
+                float2 H = make_float2(h[0], h[1]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) h[j] = start ? s.v[t][j] : fmaf(s.a[t][j], h[j], s.v[t][j]);
-        if (yp && p.t0 + t < g.L)
-            Two<T, PAIR>::store(yp + ((int64_t)p.b * g.L + p.t0 + t) * g.y_stride, ln.c, 0, g.D, live ? h[0] : 0.0f,
-                                live ? h[1] : 0.0f);
+                for (int k = 0; k < kWaves; ++k) {
+                    const float2 a = sA[0][k][l], v = sH[0][k][l];
+                    then(A.x, H.x, a.x, v.x);
+                    then(A.y, H.y, a.y, v.y);
+                }
+                publish(ch.pairs + ((size_t)p.b * g.tiles + p.c) * g.D, ln, A, H);
+            }
+            chain_gather(ch, p.b, p.c, g.tiles, g.D, ln, pA, pH, in);
+            __syncthreads();
+            chain_enter(p.c, pA, pH, in, h);
+        }
+        const float enter[2] = {h[0], h[1]};
+        for (int k = 0; k < wave; ++k) {
+            const float2 a = sA[turn][k][l], v = sH[turn][k][l];
+            h[0] = through(a.x, v.x, h[0]);
+            h[1] = through(a.y, v.y, h[1]);
+        }
+        if constexpr (CHAIN) {
+            if (wave == kWaves - 1 && p.c % kGroup == kGroup - 1 && p.c + 1 < g.tiles)
+                publish(ch.enter + ((size_t)p.b * (ch.groups - 1) + p.c / kGroup) * g.D, ln, make_float2(0.0f, 0.0f),
+                        make_float2(through(s.A[0], s.H[0], h[0]), through(s.A[1], s.H[1], h[1])));
+        }
+        if (p.t0 < g.L) {
+            if (g.states && p.t0 % 64 == 0)
+                store2(g.states + ((size_t)p.b * ((g.L + 63) / 64) + p.t0 / 64) * g.D, ln, h[0], h[1]);
+            const Rows<T> yr(static_cast<T*>(g.y), g.y_stride, g, p);
+            if (m.plain && g.y) {
+#pragma unroll
+                for (int t = 0; t < Tw; ++t) {
+                    h[0] = fmaf(s.a[t][0], h[0], s.v[t][0]);
+                    h[1] = fmaf(s.a[t][1], h[1], s.v[t][1]);
+                    store2(yr.at(t), ln, h[0], h[1]);
+                }
+            } else if (g.y || g.final_state) {
+#pragma unroll
+                for (int t = 0; t < Tw; ++t) {
+                    const bool live = bit(m.lives, t), start = bit(m.starts, t);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) h[j] = start ? s.v[t][j] : fmaf(s.a[t][j], h[j], s.v[t][j]);
+                    if (g.y && p.t0 + t < g.L) store2(yr.at(t), ln, live ? h[0] : 0.0f, live ? h[1] : 0.0f);
+                }
+            }
+            if (g.final_state && p.t0 + Tw >= g.L) store2(g.final_state + (size_t)p.b * g.D, ln, h[0], h[1]);
+        }
+        if (CHAIN || p.c + 1 == g.tiles) break;
+        h[0] = enter[0];
+        h[1] = enter[1];
+        for (int k = 0; k < kWaves; ++k) {
+            const float2 a = sA[turn][k][l], v = sH[turn][k][l];
+            h[0] = through(a.x, v.x, h[0]);
+            h[1] = through(a.y, v.y, h[1]);
+        }
+        ++p.c;
+        p.t0 += kTile<T>;
     }
-    if (g.final_state && p.t0 + Tw >= g.L)
-        Two<float, PAIR>::store(g.final_state + (size_t)p.b * g.D, ln.c, 0, g.D, h[0], h[1]);
 }
 
 // ------------------------------------------------------------ backward
@@ -376,177 +451,203 @@ static_assert(kTileB == 64, "a tile starts at a chunk's state");
 // What a wave needs of its tokens in both directions
 template <typename T, bool PAIR>
 struct Back {
-    Two<T, PAIR> x[kTb], gy[kTb];
-    float a[kTb][2], v[kTb][2], s[kTb][2], gi[kTb][2];    // carry decay, input (later a h_{t-1}), gates
+    Two<T> x[kTb], gy[kTb];
+    float a[kTb][2], v[kTb][2], s[kTb][2], gi[kTb][2];    // decay, input (later a h_{t-1}), gates
     float A[2], H[2], N[2];                               // compositions: of the state, and of the adjoint from behind
-    uint32_t starts, lives;                               // bits of the tokens
-    __device__ __forceinline__ void compute(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Params& w) {
-        Two<T, PAIR> r[kTb], i[kTb];
-        const T* xp = static_cast<const T*>(g.x);
-        const T* rp = static_cast<const T*>(g.r);
-        const T* ip = static_cast<const T*>(g.i);
-        const T* gp = static_cast<const T*>(g.gy);
+    __device__ __forceinline__ void gates(const Two<T> (&r)[kTb], const Two<T> (&i)[kTb], const Params& w, const Masks& m) {
 #pragma unroll
-        for (int t = 0; t < kTb; ++t) {
-            const int64_t row = (int64_t)p.b * g.L + min(p.t0 + t, g.L - 1);
-            x[t].load(xp + row * g.x_stride, ln.c, ln.last);
-            r[t].load(rp + row * g.r_stride, ln.c, ln.last);
-            i[t].load(ip + row * g.i_stride, ln.c, ln.last);
-            gy[t].load(gp + row * g.gy_stride, ln.c, ln.last);
-        }
-        masks(g, p, kTb, starts, lives);
+        for (int t = 0; t < kTb; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float om;
+                s[t][j] = w.r_gate(r[t].get(j), j);
+                gi[t][j] = w.i_gate(i[t].get(j), j);
+                decay(s[t][j] * w.nA[j], fast_exp2(s[t][j] * w.A2[j]), a[t][j], om);
+                v[t][j] = __builtin_amdgcn_sqrtf(om * (1.0f + a[t][j])) * gi[t][j] * x[t].get(j);
+                // here and now: the compiler would put part of every token off, and hold what that part needs
+                asm volatile("" : "+v"(a[t][j]), "+v"(v[t][j]), "+v"(s[t][j]), "+v"(gi[t][j]));
+            }
         A[0] = A[1] = 1.0f;
         H[0] = H[1] = N[0] = N[1] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < kTb; ++t) {
-            const bool live = bit(lives, t), start = bit(starts, t);
-            x[t].keep(live);
-            r[t].keep(live);
-            i[t].keep(live);
-            gy[t].keep(live);
+        for (int t = 0; t < kTb; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float d, om;
-                s[t][j] = sigmoid_f(r[t].get(j) + w.rb[j]);
-                gi[t][j] = sigmoid_f(i[t].get(j) + w.ib[j]);
-                decay(s[t][j] * w.nA[j], d, om);
-                const float in = __builtin_amdgcn_sqrtf(om * (1.0f + d)) * gi[t][j] * x[t].get(j);
-                a[t][j] = live ? d : 1.0f;
-                v[t][j] = in;
-                // here and now: the compiler would put part of every token off, and hold what that part needs
-                asm volatile("" : "+v"(a[t][j]), "+v"(v[t][j]), "+v"(s[t][j]), "+v"(gi[t][j]));
-                A[j] = start ? __uint_as_float(kCut) : A[j] * a[t][j];
-                H[j] = start ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
+                A[j] = bit(m.starts, t) ? __uint_as_float(kCut) : A[j] * a[t][j];
+                H[j] = bit(m.starts, t) ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
             }
-        }
 #pragma unroll
         for (int t = kTb - 1; t >= 0; --t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                N[j] = bit(starts, t) ? 0.0f : a[t][j] * (gy[t].get(j) + N[j]);
+            for (int j = 0; j < 2; ++j) N[j] = bit(m.starts, t) ? 0.0f : a[t][j] * (gy[t].get(j) + N[j]);
+    }
+    // a h_{t-1} in the inputs' place; h: the state that enters
+    __device__ __forceinline__ void hold(float (&h)[2], const Masks& m) {
+#pragma unroll
+        for (int t = 0; t < kTb; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float held = bit(m.starts, t) ? 0.0f : a[t][j] * h[j];
+                h[j] = held + v[t][j];
+                v[t][j] = bit(m.lives, t) ? held : 0.0f;
+                asm volatile("" : "+v"(s[t][j]), "+v"(gi[t][j]));
+            }
+#pragma unroll
+        for (int t = 0; t < kTb; ++t) {
+            x[t].hide();
+            gy[t].hide();
+        }
+    }
+    // the gradients; nu: the adjoint that enters from behind, then the one that leaves
+    __device__ __forceinline__ void grads(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Params& w, const Masks& m,
+                                          float (&nu)[2], float (&sum)[3][2]) {
+        const Rows<T> xr(static_cast<T*>(g.dx), g.dx_stride, g, p), rr(static_cast<T*>(g.dr), g.dr_stride, g, p),
+            ir(static_cast<T*>(g.di), g.di_stride, g, p);
+#pragma unroll
+        for (int t = kTb - 1; t >= 0; --t) {
+            float dx[2], dr[2], di[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float all = gy[t].get(j) + nu[j], lam = bit(m.lives, t) ? all : 0.0f;
+                nu[j] = bit(m.starts, t) ? 0.0f : a[t][j] * all;
+                const float d = a[t][j], n = s[t][j] * w.nA[j], om = n < kSeries ? one_minus(n) : 1.0f - d;
+                const float m2 = om * (1.0f + d);
+                // 1 / m, 0 where m is: no branch around the root
+                const float inv = __uint_as_float(__float_as_uint(__builtin_amdgcn_rsqf(m2)) & (m2 > 0.0f ? ~0u : 0u));
+                const float gx = gi[t][j] * x[t].get(j), lm = lam * (m2 * inv);
+                dx[j] = lm * gi[t][j];
+                di[j] = lm * gx * (1.0f - gi[t][j]);
+                const float dl = lam * (v[t][j] - gx * (d * d) * inv), ds = dl * s[t][j];
+                dr[j] = -w.nA[j] * ds * (1.0f - s[t][j]);
+                sum[0][j] += ds;
+                sum[1][j] += dr[j];
+                sum[2][j] += di[j];
+            }
+            if (p.t0 + t < g.L) {
+                store2(xr.at(t), ln, dx[0], dx[1]);
+                store2(rr.at(t), ln, dr[0], dr[1]);
+                store2(ir.at(t), ln, di[0], di[1]);
+            }
+        }
     }
 };
 
 // The chain runs from a row's last tile.  part: [tile of all rows][3][D], a tile's sums of dA, dr_bias and di_bias.
 // fp32 operands take the registers of one workgroup a CU; as many bytes are on their way then as with two in bf16.
 template <typename T, bool PAIR, bool CHAIN>
-__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 ? 4 : 2)) void ssd_glr_back_kernel(GlrArgs g, Chain ch, float* part) {
+__global__ __launch_bounds__(kThreads, (CHAIN && sizeof(T) == 2 ? 4 : 2)) void ssd_glr_back_kernel(GlrArgs g, Chain ch, float* part) {
     __shared__ float2 sA[kWaves][64], sH[kWaves][64], sN[kWaves][64], pA[CHAIN ? kWaves : 1][64], pN[CHAIN ? kWaves : 1][64], in[64];
     Place p(g, CHAIN ? chain_place(ch) : blockIdx.x, kTileB, kTb);
-    const int place = p.c;
-    p.c = g.tiles - 1 - place;
-    p.t0 = p.c * kTileB + wave_id() * kTb;
     const Lane<PAIR> ln(p.blk, g.D);
+    const int wave = wave_id(), l = threadIdx.x % 64;
     Params w;
     w.load(g, ln);
-    Back<T, PAIR> s;
-    s.compute(g, p, ln, w);
-    const size_t tile = (size_t)p.b * g.tiles + p.c;
-    Two<float, PAIR> e;
-    e.load(g.states + tile * g.D, ln.c, ln.last);
-    float h[2] = {e.get(0), e.get(1)}, nu[2] = {0.0f, 0.0f};
+    float nu[2] = {0.0f, 0.0f};
+    int place = p.c;
     if (place == 0 && g.g_final) {
-        e.load(g.g_final + (size_t)p.b * g.D, ln.c, ln.last);
+        const Two<float> e = load2(g.g_final + (size_t)p.b * g.D, ln);
         nu[0] = e.get(0);
         nu[1] = e.get(1);
     }
-    const int wave = wave_id(), l = threadIdx.x % 64;
-    sA[wave][l] = make_float2(s.A[0], s.A[1]);
-    sH[wave][l] = make_float2(s.H[0], s.H[1]);
-    sN[wave][l] = make_float2(s.N[0], s.N[1]);
-    __syncthreads();
-    if constexpr (CHAIN) {
-        if (wave == kWaves - 1) {
-            float2 A = place == 0 ? make_float2(__uint_as_float(kCut), __uint_as_float(kCut)) : make_float2(1.0f, 1.0f);
-            float2 N = make_float2(nu[0], nu[1]);
-#pragma unroll 2
-            for (int k = kWaves - 1; k >= 0; --k) {
-                const float2 a = sA[k][l], n = sN[k][l];
-                then(A.x, N.x, a.x, n.x);
-                then(A.y, N.y, a.y, n.y);
+    for (;;) {
+        p.c = g.tiles - 1 - place;
+        p.t0 = p.c * kTileB + wave * kTb;
+        const size_t tile = (size_t)p.b * g.tiles + p.c;
+        Back<T, PAIR> s;
+        const Two<float> e = load2(g.states + tile * g.D, ln);
+        Two<T> r[kTb], i[kTb];
+        {
+            const Rows<const T> xr(static_cast<const T*>(g.x), g.x_stride, g, p), rr(static_cast<const T*>(g.r), g.r_stride, g, p),
+                ir(static_cast<const T*>(g.i), g.i_stride, g, p), yr(static_cast<const T*>(g.gy), g.gy_stride, g, p);
+#pragma unroll
+            for (int t = 0; t < kTb; ++t) {
+                s.x[t] = load2(xr.at(t), ln);
+                r[t] = load2(rr.at(t), ln);
+                i[t] = load2(ir.at(t), ln);
+                s.gy[t] = load2(yr.at(t), ln);
             }
-            publish(ch.pairs + ((size_t)p.b * g.tiles + place) * g.D, ln, g.D, A, N);
         }
-        chain_gather(ch, p.b, place, g.tiles, g.D, ln, pA, pN, in);
+        const Masks m(g, p, kTb);
+        if (!m.plain) {
+#pragma unroll
+            for (int t = 0; t < kTb; ++t) {
+                blank(s.x[t], r[t], i[t], bit(m.lives, t));
+                s.gy[t].keep(bit(m.lives, t), 0.0f);
+            }
+        }
+        s.gates(r, i, w, m);
+        float h[2] = {e.get(0), e.get(1)};
+        sA[wave][l] = make_float2(s.A[0], s.A[1]);
+        sH[wave][l] = make_float2(s.H[0], s.H[1]);
+        sN[wave][l] = make_float2(s.N[0], s.N[1]);
         __syncthreads();
-        chain_enter(place, pA, pN, in, nu);
-    }
-    for (int k = 0; k < wave; ++k) {
-        const float2 a = sA[k][l], v = sH[k][l];
-        h[0] = through(a.x, v.x, h[0]);
-        h[1] = through(a.y, v.y, h[1]);
-    }
-    for (int k = kWaves - 1; k > wave; --k) {
-        const float2 a = sA[k][l], v = sN[k][l];
-        nu[0] = through(a.x, v.x, nu[0]);
-        nu[1] = through(a.y, v.y, nu[1]);
-    }
-    if constexpr (CHAIN) {
-        if (wave == 0 && place % kGroup == kGroup - 1 && place + 1 < g.tiles)
-            publish(ch.enter + ((size_t)p.b * (ch.groups - 1) + place / kGroup) * g.D, ln, g.D, make_float2(0.0f, 0.0f),
-                    make_float2(through(s.A[0], s.N[0], nu[0]), through(s.A[1], s.N[1], nu[1])));
-    }
-#pragma unroll
-    for (int t = 0; t < kTb; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float held = bit(s.starts, t) ? 0.0f : s.a[t][j] * h[j];
-            h[j] = held + s.v[t][j];
-            s.v[t][j] = bit(s.lives, t) ? held : 0.0f;
+        if constexpr (CHAIN) {
+            if (wave == kWaves - 1) {
+                float2 A = place == 0 ? make_float2(__uint_as_float(kCut), __uint_as_float(kCut)) : make_float2(1.0f, 1.0f);
+                float2 N = make_float2(nu[0], nu[1]);
+#pragma unroll 2
+                for (int k = kWaves - 1; k >= 0; --k) {
+                    const float2 a = sA[k][l], n = sN[k][l];
+                    then(A.x, N.x, a.x, n.x);
+                    then(A.y, N.y, a.y, n.y);
+                }
+                publish(ch.pairs + ((size_t)p.b * g.tiles + place) * g.D, ln, A, N);
+            }
+            chain_gather(ch, p.b, place, g.tiles, g.D, ln, pA, pN, in);
+            __syncthreads();
+            chain_enter(place, pA, pN, in, nu);
         }
-#pragma unroll
-    for (int t = 0; t < kTb; ++t) {
-        s.x[t].hide();
-        s.gy[t].hide();
-    }
-    T* dxp = static_cast<T*>(g.dx);
-    T* drp = static_cast<T*>(g.dr);
-    T* dip = static_cast<T*>(g.di);
-    float sum[3][2] = {};
-#pragma unroll
-    for (int t = kTb - 1; t >= 0; --t) {
-        const bool live = bit(s.lives, t);
-        float dx[2], dr[2], di[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float all = s.gy[t].get(j) + nu[j], lam = live ? all : 0.0f;
-            nu[j] = bit(s.starts, t) ? 0.0f : s.a[t][j] * all;
-            const float d = s.a[t][j], n = s.s[t][j] * w.nA[j], om = n < kSeries ? one_minus(n) : 1.0f - d;
-            const float m2 = om * (1.0f + d);
-            const float inv = __uint_as_float(__float_as_uint(__builtin_amdgcn_rsqf(m2)) & (m2 > 0.0f ? ~0u : 0u));
-            const float x = s.x[t].get(j), gi = s.gi[t][j], lm = lam * m2 * inv;
-            dx[j] = lm * gi;
-            di[j] = lm * x * gi * (1.0f - gi);
-            const float dl = lam * (s.v[t][j] - gi * x * d * d * inv);
-            dr[j] = -dl * w.nA[j] * s.s[t][j] * (1.0f - s.s[t][j]);
-            sum[0][j] = fmaf(dl, s.s[t][j], sum[0][j]);
-            sum[1][j] += dr[j];
-            sum[2][j] += di[j];
+        const float enter[2] = {nu[0], nu[1]};
+        for (int k = 0; k < wave; ++k) {
+            const float2 a = sA[k][l], v = sH[k][l];
+            h[0] = through(a.x, v.x, h[0]);
+            h[1] = through(a.y, v.y, h[1]);
         }
-        if (ln.on && p.t0 + t < g.L) {
-            const int64_t row = (int64_t)p.b * g.L + p.t0 + t;
-            Two<T, PAIR>::store(dxp + row * g.dx_stride, ln.c, 0, g.D, dx[0], dx[1]);
-            Two<T, PAIR>::store(drp + row * g.dr_stride, ln.c, 0, g.D, dr[0], dr[1]);
-            Two<T, PAIR>::store(dip + row * g.di_stride, ln.c, 0, g.D, di[0], di[1]);
+        for (int k = kWaves - 1; k > wave; --k) {
+            const float2 a = sA[k][l], v = sN[k][l];
+            nu[0] = through(a.x, v.x, nu[0]);
+            nu[1] = through(a.y, v.y, nu[1]);
         }
-    }
-    if (g.g_init && p.t0 == 0 && ln.on)
-        Two<float, PAIR>::store(g.g_init + (size_t)p.b * g.D, ln.c, 0, g.D, nu[0], nu[1]);
-    // the waves' sums in their order
-    __syncthreads();
-    sA[wave][l] = make_float2(sum[0][0], sum[0][1]);
-    sH[wave][l] = make_float2(sum[1][0], sum[1][1]);
-    sN[wave][l] = make_float2(sum[2][0], sum[2][1]);
-    __syncthreads();
-    if (wave >= 3 || !ln.on) return;
-    const float2(*from)[64] = wave == 0 ? sA : wave == 1 ? sH : sN;
-    float a = 0.0f, b = 0.0f;
+        float next[2] = {nu[0], nu[1]};
+        if constexpr (CHAIN) {
+            if (wave == 0 && place % kGroup == kGroup - 1 && place + 1 < g.tiles)
+                publish(ch.enter + ((size_t)p.b * (ch.groups - 1) + place / kGroup) * g.D, ln, make_float2(0.0f, 0.0f),
+                        make_float2(through(s.A[0], s.N[0], nu[0]), through(s.A[1], s.N[1], nu[1])));
+        } else {
+            next[0] = enter[0];
+            next[1] = enter[1];
+            for (int k = kWaves - 1; k >= 0; --k) {
+                const float2 a = sA[k][l], v = sN[k][l];
+                next[0] = through(a.x, v.x, next[0]);
+                next[1] = through(a.y, v.y, next[1]);
+            }
+        }
+        float sum[3][2] = {};
+        s.hold(h, m);
+        s.grads(g, p, ln, w, m, nu, sum);
+        if (g.g_init && p.t0 == 0) store2(g.g_init + (size_t)p.b * g.D, ln, nu[0], nu[1]);
+        // the waves' sums in their order
+        __syncthreads();
+        sA[wave][l] = make_float2(sum[0][0], sum[0][1]);
+        sH[wave][l] = make_float2(sum[1][0], sum[1][1]);
+        sN[wave][l] = make_float2(sum[2][0], sum[2][1]);
+        __syncthreads();
+        if (wave < 3) {
+            const float2(*from)[64] = wave == 0 ? sA : wave == 1 ? sH : sN;
+            float a = 0.0f, b = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-        a += from[k][l].x;
-        b += from[k][l].y;
+            for (int k = 0; k < kWaves; ++k) {
+                a += from[k][l].x;
+                b += from[k][l].y;
+            }
+            store2(part + (tile * 3 + wave) * g.D, ln, a, b);
+        }
+        if (CHAIN || p.c == 0) break;
+        nu[0] = next[0];
+        nu[1] = next[1];
+        ++place;
+        __syncthreads();                             // the sums have been read
     }
-    Two<float, PAIR>::store(part + (tile * 3 + wave) * g.D, ln.c, 0, g.D, a, b);
 }
 
 // dA, dr_bias and di_bias: the tiles' sums in a fixed order, in 64 bits.  32 columns a workgroup, 32 threads a column.
@@ -604,9 +705,8 @@ template <typename T, int V> __device__ __forceinline__ void step_st(T* p, const
 }
 template <typename T, int V>
 __global__ __launch_bounds__(256) void ssd_glr_step_kernel(GlrArgs g) {
-    const int n = g.D / V;                           // V > 1: D % 8 == 0
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (at >= (int64_t)g.B * n) return;
+    const uint32_t n = g.D / V, at = blockIdx.x * 256u + threadIdx.x;      // V > 1: D % 8 == 0; B * D < 2^31
+    if (at >= g.B * n) return;
     const int b = (int)(at / n), c = (int)(at % n) * V;
     float x[V], r[V], i[V], A[V], rb[V], ib[V], h[V];
     step_ld<T, V>(static_cast<const T*>(g.x) + b * g.x_stride + c, x);
@@ -623,7 +723,8 @@ __global__ __launch_bounds__(256) void ssd_glr_step_kernel(GlrArgs g) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         float d, om;
-        decay(-sigmoid_f(r[j] + rb[j]) * A[j], d, om);
+        const float n = -sigmoid_f(r[j] + rb[j]) * A[j];
+        decay(n, fast_exp2(-n * kLog2e), d, om);
         h[j] = fmaf(d, h[j], __builtin_amdgcn_sqrtf(om * (1.0f + d)) * sigmoid_f(i[j] + ib[j]) * x[j]);
     }
     step_st<float, V>(state, h);
@@ -634,9 +735,12 @@ int cols(int D) { return (D + kCols - 1) / kCols; }
 int tiles_of(int L, int tile) { return (int)(((int64_t)L + tile - 1) / tile); }
 size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
 
+// rows of at most this many tiles are walked by one workgroup: the chain's memory is another launch
+constexpr int kWalk = 2;
+
 // the chain of a launch over `tiles` tiles a row, in n bytes at `ws`
 size_t chain_bytes(int B, int D, int tiles) {
-    if (tiles <= 1) return 0;
+    if (tiles <= kWalk) return 0;
     return 256 + pad16((size_t)B * D * (tiles + (tiles + kGroup - 1) / kGroup - 1) * sizeof(uint64_t));
 }
 hipError_t make_chain(Chain& ch, int B, int D, int tiles, char* ws, hipStream_t s) {
@@ -653,13 +757,13 @@ hipError_t make_chain(Chain& ch, int B, int D, int tiles, char* ws, hipStream_t 
 template <typename T, bool PAIR>
 hipError_t fwd_t(GlrArgs a, char* ws, hipStream_t s) {
     a.tiles = tiles_of(a.L, kTile<T>);
-    const dim3 grid((unsigned)(a.tiles * (int64_t)a.B * cols(a.D)));
+    const int64_t rows = (int64_t)a.B * cols(a.D);
     Chain ch{};
-    if (a.tiles > 1) {
+    if (a.tiles > kWalk) {
         if (hipError_t e = make_chain(ch, a.B, a.D, a.tiles, ws, s)) return e;
-        hipLaunchKernelGGL((ssd_glr_scan_kernel<T, PAIR, true>), grid, dim3(kThreads), 0, s, a, ch);
+        hipLaunchKernelGGL((ssd_glr_scan_kernel<T, PAIR, true>), dim3((unsigned)(a.tiles * rows)), dim3(kThreads), 0, s, a, ch);
     } else {
-        hipLaunchKernelGGL((ssd_glr_scan_kernel<T, PAIR, false>), grid, dim3(kThreads), 0, s, a, ch);
+        hipLaunchKernelGGL((ssd_glr_scan_kernel<T, PAIR, false>), dim3((unsigned)rows), dim3(kThreads), 0, s, a, ch);
     }
     return hipGetLastError();
 }
@@ -683,13 +787,13 @@ hipError_t bwd_t(GlrArgs a, char* ws, hipStream_t s) {
     a.tiles = tiles_of(a.L, kTileB);
     float* part = reinterpret_cast<float*>(ws);
     ws += pad16((size_t)a.B * a.tiles * 3 * a.D * sizeof(float));
-    const dim3 grid((unsigned)(a.tiles * (int64_t)a.B * cols(a.D)));
+    const int64_t rows = (int64_t)a.B * cols(a.D);
     Chain ch{};
-    if (a.tiles > 1) {
+    if (a.tiles > kWalk) {
         if (hipError_t e = make_chain(ch, a.B, a.D, a.tiles, ws, s)) return e;
-        hipLaunchKernelGGL((ssd_glr_back_kernel<T, PAIR, true>), grid, dim3(kThreads), 0, s, a, ch, part);
+        hipLaunchKernelGGL((ssd_glr_back_kernel<T, PAIR, true>), dim3((unsigned)(a.tiles * rows)), dim3(kThreads), 0, s, a, ch, part);
     } else {
-        hipLaunchKernelGGL((ssd_glr_back_kernel<T, PAIR, false>), grid, dim3(kThreads), 0, s, a, ch, part);
+        hipLaunchKernelGGL((ssd_glr_back_kernel<T, PAIR, false>), dim3((unsigned)rows), dim3(kThreads), 0, s, a, ch, part);
     }
     if (hipError_t e = hipGetLastError()) return e;
     hipLaunchKernelGGL(ssd_glr_sum_kernel, dim3((unsigned)((3LL * a.D + 31) / 32)), dim3(1024), 0, s, part,
