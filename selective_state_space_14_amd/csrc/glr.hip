@@ -40,7 +40,7 @@ __device__ __forceinline__ float widen(uint16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
 __device__ __forceinline__ void narrow(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
 
-// Column c of a row whose address is the wave's: an unsigned offset of 32 bits keeps that address in scalars.
+// Column c of a row whose address is the wave's.
 template <typename V, typename T>
 __device__ __forceinline__ const V* column(const T* row, uint32_t c) {
     return reinterpret_cast<const V*>(reinterpret_cast<const char*>(row) + c * (uint32_t)sizeof(T));
@@ -80,15 +80,63 @@ template <> struct Two<uint16_t> {
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
     __device__ __forceinline__ void keep(bool on, float off) { v = on ? v : (__float_as_uint(off) >> 16) * 0x10001u; }
 };
+// The rows of a wave's tokens as one buffer: a row is a scalar offset, a lane's channels a vector offset that all rows share,
+// so that no address is computed per row and lane.  Rows past the batch row's end are its last one.
+template <typename T>
+struct Rows {
+    __amdgpu_buffer_rsrc_t rsrc;
+    int stride, most;                               // bytes; tokens after the first
+    __device__ __forceinline__ Rows(const T* p, int64_t s, int b, int t0, int L) {
+        const int t = min(t0, L - 1);
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p) + ((int64_t)b * L + t) * s, 0, 0x7fffffff, 0x00020000);
+        stride = (int)(s * (int)sizeof(T));          // 16 rows of at most 2^24 bytes
+        most = L - 1 - t;
+    }
+    __device__ __forceinline__ int at(int t) const { return min(t, most) * stride; }
+};
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <bool PAIR>
+__device__ __forceinline__ Two<float> load2(const Rows<float>& r, int t, const Lane<PAIR>& ln) {
+    if constexpr (PAIR) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r.rsrc, ln.c[0] * 4, r.at(t), 0));
+        return {make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]))};
+    } else {
+        return {make_float2(__uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r.rsrc, ln.c[0] * 4, r.at(t), 0)),
+                            __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r.rsrc, ln.c[1] * 4, r.at(t), 0)))};
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ Two<uint16_t> load2(const Rows<uint16_t>& r, int t, const Lane<PAIR>& ln) {
+    if constexpr (PAIR) return {(uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r.rsrc, ln.c[0] * 2, r.at(t), 0)};
+    else
+        return {(uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r.rsrc, ln.c[0] * 2, r.at(t), 0) |
+                (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r.rsrc, ln.c[1] * 2, r.at(t), 0) << 16};
+}
+template <bool PAIR>
+__device__ __forceinline__ void store2(const Rows<float>& r, int t, const Lane<PAIR>& ln, float a, float b) {
+    if constexpr (PAIR) {
+        const u32x2 v = {__float_as_uint(a), __float_as_uint(b)};
+        if (ln.on) __builtin_amdgcn_raw_buffer_store_b64(v, r.rsrc, ln.c[0] * 4, r.at(t), 0);
+    } else {
+        if (ln.on) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a), r.rsrc, ln.c[0] * 4, r.at(t), 0);
+        if (ln.on1) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(b), r.rsrc, ln.c[1] * 4, r.at(t), 0);
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void store2(const Rows<uint16_t>& r, int t, const Lane<PAIR>& ln, float a, float b) {
+    const uint32_t v = pack_bf16x2(a, b);
+    if constexpr (PAIR) {
+        if (ln.on) __builtin_amdgcn_raw_buffer_store_b32(v, r.rsrc, ln.c[0] * 2, r.at(t), 0);
+    } else {
+        if (ln.on) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, r.rsrc, ln.c[0] * 2, r.at(t), 0);
+        if (ln.on1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v >> 16), r.rsrc, ln.c[1] * 2, r.at(t), 0);
+    }
+}
+// of a row of states
 template <bool PAIR>
 __device__ __forceinline__ Two<float> load2(const float* row, const Lane<PAIR>& ln) {
     if (PAIR) return {*column<float2>(row, ln.c[0])};
     return {make_float2(*column<float>(row, ln.c[0]), *column<float>(row, ln.c[1]))};
-}
-template <bool PAIR>
-__device__ __forceinline__ Two<uint16_t> load2(const uint16_t* row, const Lane<PAIR>& ln) {
-    if (PAIR) return {*column<uint32_t>(row, ln.c[0])};
-    return {*column<uint16_t>(row, ln.c[0]) | (uint32_t)*column<uint16_t>(row, ln.c[1]) << 16};
 }
 template <bool PAIR>
 __device__ __forceinline__ void store2(float* row, const Lane<PAIR>& ln, float a, float b) {
@@ -99,37 +147,27 @@ __device__ __forceinline__ void store2(float* row, const Lane<PAIR>& ln, float a
         if (ln.on1) *column<float>(row, ln.c[1]) = b;
     }
 }
-template <bool PAIR>
-__device__ __forceinline__ void store2(uint16_t* row, const Lane<PAIR>& ln, float a, float b) {
-    if (PAIR) {
-        if (ln.on) *column<uint32_t>(row, ln.c[0]) = pack_bf16x2(a, b);
-    } else {
-        if (ln.on) narrow(column<uint16_t>(row, ln.c[0]), a);
-        if (ln.on1) narrow(column<uint16_t>(row, ln.c[1]), b);
-    }
-}
-
 // ------------------------------------------------------------ the gates
 __device__ __forceinline__ float sigmoid_f(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
 
-// decay a = e^-n and 1 - a.  A decay near 1 is what a long memory rests on: there 1 - a comes from its series (6 terms,
-// off by n^6 / 7! of itself, 5e-8 at the border) and a from 1 - a by one rounding, so that neither the hardware exp2's
-// error nor the difference's shows: over thousands of tokens a decay that is off by one step the same way each time
-// would move the state by some 1e-5.  From the border on the hardware's exp2 and the difference are within 2^-21.
-constexpr float kSeries = 0.25f;
-__device__ __forceinline__ float one_minus(float n) {
-    float q = fmaf(n, -1.0f / 720.0f, 1.0f / 120.0f);
-    q = fmaf(n, -q, 1.0f / 24.0f);
-    q = fmaf(n, -q, 1.0f / 6.0f);
-    q = fmaf(n, -q, 0.5f);
-    q = fmaf(n, -q, 1.0f);
-    return q * n;
+// decay a = e^-n = 2^-z and 1 - a, z = n log2 e.  A decay near 1 is what a long memory rests on: there 1 - a comes from its
+// series (5 terms in z, off by n^5 / 6! of itself, 4e-8 at the border) and a from 1 - a by one rounding, so that neither
+// the hardware exp2's error nor the difference's shows: over thousands of tokens a decay that is off by one step the same
+// way each time would move the state by some 1e-5.  From the border on the hardware's exp2 and the difference are within
+// 2^-20 of 1 - a.
+constexpr float kNear = 0.18f;                       // n < 0.125
+__device__ __forceinline__ float one_minus(float z) {
+    float q = fmaf(z, -0.0013333558146428443f, 0.009618129107628477f);
+    q = fmaf(z, -q, 0.05550410866482158f);
+    q = fmaf(z, -q, 0.2402265069591007f);
+    q = fmaf(z, -q, 0.6931471805599453f);
+    return q * z;
 }
-// e: the hardware's e^-n
-__device__ __forceinline__ void decay(float n, float e, float& a, float& om) {
-    const float q = one_minus(n);
-    a = n < kSeries ? 1.0f - q : e;
-    om = n < kSeries ? q : 1.0f - e;
+__device__ __forceinline__ void decay(float z, float& a, float& om) {
+    const float q = one_minus(z), e = fast_exp2(-z);
+    const bool near = z < kNear;
+    a = near ? 1.0f - q : e;
+    om = near ? q : 1.0f - e;
 }
 
 // bit t set: a document starts at token t0 + t (t < n <= 64)
@@ -152,16 +190,14 @@ __device__ __forceinline__ void then(float& A, float& H, float A2, float H2) {
 // the wave's number, known to the compiler to be the same for its lanes: rows are then addressed by scalars
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
-// a lane's parameters: -A, A log2 e and the biases times -log2 e, for sigmoid(v + bias) = 1 / (1 + 2^(-v log2 e - bias log2 e))
+// a lane's parameters: -A log2 e and the biases times -log2 e, for sigmoid(v + bias) = 1 / (1 + 2^(-v log2 e - bias log2 e))
 struct Params {
-    float nA[2], A2[2], rb[2], ib[2];
+    float zA[2], rb[2], ib[2];
     template <bool PAIR>
     __device__ __forceinline__ void load(const GlrArgs& a, const Lane<PAIR>& ln) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float A = *column<float>(a.A, ln.c[j]);
-            nA[j] = -A;
-            A2[j] = A * kLog2e;
+            zA[j] = *column<float>(a.A, ln.c[j]) * -kLog2e;
             rb[j] = a.r_bias ? -kLog2e * *column<float>(a.r_bias, ln.c[j]) : 0.0f;
             ib[j] = a.i_bias ? -kLog2e * *column<float>(a.i_bias, ln.c[j]) : 0.0f;
         }
@@ -197,20 +233,6 @@ struct Masks {
 };
 __device__ __forceinline__ bool bit(uint32_t mask, int t) { return (mask >> t) & 1; }
 
-// rows of a wave's tokens: the address of its first (past the row's end its last stands in), and of those after it
-template <typename T>
-struct Rows {
-    T* first;
-    int stride, most;                               // elements; tokens after the first
-    __device__ __forceinline__ Rows(T* p, int64_t s, const GlrArgs& g, const Place& p0) {
-        const int t = min(p0.t0, g.L - 1);
-        first = p + ((int64_t)p0.b * g.L + t) * s;
-        stride = (int)s;
-        most = g.L - 1 - t;
-    }
-    __device__ __forceinline__ T* at(int t) const { return first + (int64_t)(min(t, most) * stride); }
-};
-
 // A token that is not real decays by 1 and takes nothing in: its decay gate is that of -inf, its inputs are 0.
 template <typename T>
 __device__ __forceinline__ void blank(Two<T>& x, Two<T>& r, Two<T>& i, bool live) {
@@ -232,7 +254,7 @@ struct Stretch {
             for (int j = 0; j < 2; ++j) {
                 const float s = w.r_gate(r[t].get(j), j);
                 float om;
-                decay(s * w.nA[j], fast_exp2(s * w.A2[j]), a[t][j], om);
+                decay(s * w.zA[j], a[t][j], om);
                 v[t][j] = __builtin_amdgcn_sqrtf(om * (1.0f + a[t][j])) * w.i_gate(i[t].get(j), j) * x[t].get(j);
                 // here and now: the compiler would put part of every token off, and hold what that part needs
                 asm volatile("" : "+v"(a[t][j]), "+v"(v[t][j]));
@@ -363,13 +385,14 @@ __global__ __launch_bounds__(kThreads, (CHAIN && (PAIR || sizeof(T) == 4) ? 4 : 
         Stretch<T, PAIR, Tw> s;
         Two<T> x[Tw], r[Tw], i[Tw];
         {
-            const Rows<const T> xr(static_cast<const T*>(g.x), g.x_stride, g, p), rr(static_cast<const T*>(g.r), g.r_stride, g, p),
-                ir(static_cast<const T*>(g.i), g.i_stride, g, p);
+            const Rows<T> xr(static_cast<const T*>(g.x), g.x_stride, p.b, p.t0, g.L),
+                rr(static_cast<const T*>(g.r), g.r_stride, p.b, p.t0, g.L),
+                ir(static_cast<const T*>(g.i), g.i_stride, p.b, p.t0, g.L);
 #pragma unroll
             for (int t = 0; t < Tw; ++t) {
-                x[t] = load2(xr.at(t), ln);
-                r[t] = load2(rr.at(t), ln);
-                i[t] = load2(ir.at(t), ln);
+                x[t] = load2(xr, t, ln);
+                r[t] = load2(rr, t, ln);
+                i[t] = load2(ir, t, ln);
             }
         }
         const Masks m(g, p, Tw);
@@ -412,13 +435,13 @@ __global__ __launch_bounds__(kThreads, (CHAIN && (PAIR || sizeof(T) == 4) ? 4 : 
         if (p.t0 < g.L) {
             if (g.states && p.t0 % 64 == 0)
                 store2(g.states + ((size_t)p.b * ((g.L + 63) / 64) + p.t0 / 64) * g.D, ln, h[0], h[1]);
-            const Rows<T> yr(static_cast<T*>(g.y), g.y_stride, g, p);
+            const Rows<T> yr(static_cast<const T*>(g.y), g.y_stride, p.b, p.t0, g.L);
             if (m.plain && g.y) {
 #pragma unroll
                 for (int t = 0; t < Tw; ++t) {
                     h[0] = fmaf(s.a[t][0], h[0], s.v[t][0]);
                     h[1] = fmaf(s.a[t][1], h[1], s.v[t][1]);
-                    store2(yr.at(t), ln, h[0], h[1]);
+                    store2(yr, t, ln, h[0], h[1]);
                 }
             } else if (g.y || g.final_state) {
 #pragma unroll
@@ -426,7 +449,7 @@ __global__ __launch_bounds__(kThreads, (CHAIN && (PAIR || sizeof(T) == 4) ? 4 : 
                     const bool live = bit(m.lives, t), start = bit(m.starts, t);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) h[j] = start ? s.v[t][j] : fmaf(s.a[t][j], h[j], s.v[t][j]);
-                    if (g.y && p.t0 + t < g.L) store2(yr.at(t), ln, live ? h[0] : 0.0f, live ? h[1] : 0.0f);
+                    if (g.y && p.t0 + t < g.L) store2(yr, t, ln, live ? h[0] : 0.0f, live ? h[1] : 0.0f);
                 }
             }
             if (g.final_state && p.t0 + Tw >= g.L) store2(g.final_state + (size_t)p.b * g.D, ln, h[0], h[1]);
@@ -454,7 +477,7 @@ struct Back {
     Two<T> x[kTb], gy[kTb];
     float a[kTb][2], v[kTb][2], s[kTb][2], gi[kTb][2];    // decay, input (later a h_{t-1}), gates
     float A[2], H[2], N[2];                               // compositions: of the state, and of the adjoint from behind
-    __device__ __forceinline__ void gates(const Two<T> (&r)[kTb], const Two<T> (&i)[kTb], const Params& w, const Masks& m) {
+    __device__ __forceinline__ void gates(const Two<T> (&r)[kTb], const Two<T> (&i)[kTb], const Params& w, const Masks& k) {
 #pragma unroll
         for (int t = 0; t < kTb; ++t)
 #pragma unroll
@@ -462,71 +485,89 @@ struct Back {
                 float om;
                 s[t][j] = w.r_gate(r[t].get(j), j);
                 gi[t][j] = w.i_gate(i[t].get(j), j);
-                decay(s[t][j] * w.nA[j], fast_exp2(s[t][j] * w.A2[j]), a[t][j], om);
+                decay(s[t][j] * w.zA[j], a[t][j], om);
                 v[t][j] = __builtin_amdgcn_sqrtf(om * (1.0f + a[t][j])) * gi[t][j] * x[t].get(j);
                 // here and now: the compiler would put part of every token off, and hold what that part needs
                 asm volatile("" : "+v"(a[t][j]), "+v"(v[t][j]), "+v"(s[t][j]), "+v"(gi[t][j]));
             }
         A[0] = A[1] = 1.0f;
         H[0] = H[1] = N[0] = N[1] = 0.0f;
+        if (k.plain) {
 #pragma unroll
-        for (int t = 0; t < kTb; ++t)
+            for (int t = 0; t < kTb; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                A[j] = bit(m.starts, t) ? __uint_as_float(kCut) : A[j] * a[t][j];
-                H[j] = bit(m.starts, t) ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
-            }
+                for (int j = 0; j < 2; ++j) {
+                    A[j] *= a[t][j];
+                    H[j] = fmaf(a[t][j], H[j], v[t][j]);
+                }
 #pragma unroll
-        for (int t = kTb - 1; t >= 0; --t)
+            for (int t = kTb - 1; t >= 0; --t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) N[j] = bit(m.starts, t) ? 0.0f : a[t][j] * (gy[t].get(j) + N[j]);
+                for (int j = 0; j < 2; ++j) N[j] = a[t][j] * (gy[t].get(j) + N[j]);
+        } else {
+#pragma unroll
+            for (int t = 0; t < kTb; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    A[j] = bit(k.starts, t) ? __uint_as_float(kCut) : A[j] * a[t][j];
+                    H[j] = bit(k.starts, t) ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
+                }
+#pragma unroll
+            for (int t = kTb - 1; t >= 0; --t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) N[j] = bit(k.starts, t) ? 0.0f : a[t][j] * (gy[t].get(j) + N[j]);
+        }
     }
     // a h_{t-1} in the inputs' place; h: the state that enters
-    __device__ __forceinline__ void hold(float (&h)[2], const Masks& m) {
+    __device__ __forceinline__ void hold(float (&h)[2], const Masks& k) {
 #pragma unroll
         for (int t = 0; t < kTb; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float held = bit(m.starts, t) ? 0.0f : a[t][j] * h[j];
-                h[j] = held + v[t][j];
-                v[t][j] = bit(m.lives, t) ? held : 0.0f;
-                asm volatile("" : "+v"(s[t][j]), "+v"(gi[t][j]));
+                const float was = bit(k.starts, t) ? 0.0f : a[t][j] * h[j];
+                h[j] = was + v[t][j];
+                v[t][j] = bit(k.lives, t) ? was : 0.0f;
             }
+        // so that nothing made of these above is kept for below
 #pragma unroll
         for (int t = 0; t < kTb; ++t) {
             x[t].hide();
             gy[t].hide();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(s[t][j]), "+v"(gi[t][j]));
         }
     }
     // the gradients; nu: the adjoint that enters from behind, then the one that leaves
-    __device__ __forceinline__ void grads(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Params& w, const Masks& m,
-                                          float (&nu)[2], float (&sum)[3][2]) {
-        const Rows<T> xr(static_cast<T*>(g.dx), g.dx_stride, g, p), rr(static_cast<T*>(g.dr), g.dr_stride, g, p),
-            ir(static_cast<T*>(g.di), g.di_stride, g, p);
+    __device__ __forceinline__ void grads(const GlrArgs& g, const Place& p, const Lane<PAIR>& ln, const Masks& k, float (&nu)[2],
+                                          float (&sum)[3][2]) {
+        const Rows<T> xr(static_cast<const T*>(g.dx), g.dx_stride, p.b, p.t0, g.L),
+            rr(static_cast<const T*>(g.dr), g.dr_stride, p.b, p.t0, g.L),
+            ir(static_cast<const T*>(g.di), g.di_stride, p.b, p.t0, g.L);
+        float A2[2] = {*column<float>(g.A, ln.c[0]), *column<float>(g.A, ln.c[1])};   // not held from above
 #pragma unroll
         for (int t = kTb - 1; t >= 0; --t) {
             float dx[2], dr[2], di[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float all = gy[t].get(j) + nu[j], lam = bit(m.lives, t) ? all : 0.0f;
-                nu[j] = bit(m.starts, t) ? 0.0f : a[t][j] * all;
-                const float d = a[t][j], n = s[t][j] * w.nA[j], om = n < kSeries ? one_minus(n) : 1.0f - d;
-                const float m2 = om * (1.0f + d);
-                // 1 / m, 0 where m is: no branch around the root
+                const float all = gy[t].get(j) + nu[j], lam = bit(k.lives, t) ? all : 0.0f;
+                nu[j] = bit(k.starts, t) ? 0.0f : a[t][j] * all;
+                const float z = s[t][j] * (A2[j] * -kLog2e), om = z < kNear ? one_minus(z) : 1.0f - a[t][j];
+                const float m2 = om * (1.0f + a[t][j]);
+                // 1 / m, 0 where m is: no branch around it
                 const float inv = __uint_as_float(__float_as_uint(__builtin_amdgcn_rsqf(m2)) & (m2 > 0.0f ? ~0u : 0u));
                 const float gx = gi[t][j] * x[t].get(j), lm = lam * (m2 * inv);
                 dx[j] = lm * gi[t][j];
                 di[j] = lm * gx * (1.0f - gi[t][j]);
-                const float dl = lam * (v[t][j] - gx * (d * d) * inv), ds = dl * s[t][j];
-                dr[j] = -w.nA[j] * ds * (1.0f - s[t][j]);
+                const float ds = lam * (v[t][j] - gx * (a[t][j] * a[t][j]) * inv) * s[t][j];
+                dr[j] = A2[j] * ds * (1.0f - s[t][j]);
                 sum[0][j] += ds;
                 sum[1][j] += dr[j];
                 sum[2][j] += di[j];
             }
             if (p.t0 + t < g.L) {
-                store2(xr.at(t), ln, dx[0], dx[1]);
-                store2(rr.at(t), ln, dr[0], dr[1]);
-                store2(ir.at(t), ln, di[0], di[1]);
+                store2(xr, t, ln, dx[0], dx[1]);
+                store2(rr, t, ln, dr[0], dr[1]);
+                store2(ir, t, ln, di[0], di[1]);
             }
         }
     }
@@ -557,14 +598,16 @@ __global__ __launch_bounds__(kThreads, (CHAIN && sizeof(T) == 2 ? 4 : 2)) void s
         const Two<float> e = load2(g.states + tile * g.D, ln);
         Two<T> r[kTb], i[kTb];
         {
-            const Rows<const T> xr(static_cast<const T*>(g.x), g.x_stride, g, p), rr(static_cast<const T*>(g.r), g.r_stride, g, p),
-                ir(static_cast<const T*>(g.i), g.i_stride, g, p), yr(static_cast<const T*>(g.gy), g.gy_stride, g, p);
+            const Rows<T> xr(static_cast<const T*>(g.x), g.x_stride, p.b, p.t0, g.L),
+                rr(static_cast<const T*>(g.r), g.r_stride, p.b, p.t0, g.L),
+                ir(static_cast<const T*>(g.i), g.i_stride, p.b, p.t0, g.L),
+                yr(static_cast<const T*>(g.gy), g.gy_stride, p.b, p.t0, g.L);
 #pragma unroll
             for (int t = 0; t < kTb; ++t) {
-                s.x[t] = load2(xr.at(t), ln);
-                r[t] = load2(rr.at(t), ln);
-                i[t] = load2(ir.at(t), ln);
-                s.gy[t] = load2(yr.at(t), ln);
+                s.x[t] = load2(xr, t, ln);
+                r[t] = load2(rr, t, ln);
+                i[t] = load2(ir, t, ln);
+                s.gy[t] = load2(yr, t, ln);
             }
         }
         const Masks m(g, p, kTb);
@@ -624,7 +667,7 @@ __global__ __launch_bounds__(kThreads, (CHAIN && sizeof(T) == 2 ? 4 : 2)) void s
         }
         float sum[3][2] = {};
         s.hold(h, m);
-        s.grads(g, p, ln, w, m, nu, sum);
+        s.grads(g, p, ln, m, nu, sum);
         if (g.g_init && p.t0 == 0) store2(g.g_init + (size_t)p.b * g.D, ln, nu[0], nu[1]);
         // the waves' sums in their order
         __syncthreads();
@@ -723,8 +766,7 @@ __global__ __launch_bounds__(256) void ssd_glr_step_kernel(GlrArgs g) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         float d, om;
-        const float n = -sigmoid_f(r[j] + rb[j]) * A[j];
-        decay(n, fast_exp2(-n * kLog2e), d, om);
+        decay(sigmoid_f(r[j] + rb[j]) * (A[j] * -kLog2e), d, om);
         h[j] = fmaf(d, h[j], __builtin_amdgcn_sqrtf(om * (1.0f + d)) * sigmoid_f(i[j] + ib[j]) * x[j]);
     }
     step_st<float, V>(state, h);
