@@ -1347,6 +1347,7 @@ static int check_glr(const char* fn, ssd::GlrArgs& a, const GlrRow* rows, int n,
         if (r.stride % 2 || reinterpret_cast<uintptr_t>(r.p) % (2 * es)) a.pair = 0;
         if (!aligned16(r.p) || r.stride * es % 16) a.vec = 0;
     }
+    if (!aligned16(a.A) || !aligned16(a.r_bias) || !aligned16(a.i_bias)) a.vec = 0;
     TRY(check_ptr(fn, "A", a.A, a.B > 0, false));
     TRY(check_ptr(fn, "r_bias", a.r_bias, false, false));
     TRY(check_ptr(fn, "i_bias", a.i_bias, false, false));

@@ -720,7 +720,7 @@ __global__ __launch_bounds__(256) void ssd_glr_copy_kernel(const float* from, fl
 }
 
 // ------------------------------------------------------------ one token
-// V channels a thread: 8 where every row and state starts on a 16-byte boundary and D % 8 == 0, else 1.  Bound by HBM:
+// V channels a thread: 8 where every row, state and parameter starts on a 16-byte boundary and D % 8 == 0, else 1.  Bound by HBM:
 // 8 bytes of state and four activations a channel.
 template <typename T, int V> __device__ __forceinline__ void step_ld(const T* p, float (&o)[V]) {
     if constexpr (V == 1) {
@@ -758,11 +758,10 @@ __global__ __launch_bounds__(256) void ssd_glr_step_kernel(GlrArgs g) {
     float* state = g.final_state + (int64_t)b * g.D + c;
     step_ld<float, V>(state, h);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        A[j] = g.A[c + j];
-        rb[j] = g.r_bias ? g.r_bias[c + j] : 0.0f;
-        ib[j] = g.i_bias ? g.i_bias[c + j] : 0.0f;
-    }
+    for (int j = 0; j < V; ++j) rb[j] = ib[j] = 0.0f;
+    step_ld<float, V>(g.A + c, A);
+    if (g.r_bias) step_ld<float, V>(g.r_bias + c, rb);
+    if (g.i_bias) step_ld<float, V>(g.i_bias + c, ib);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         float d, om;

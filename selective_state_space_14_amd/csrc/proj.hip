@@ -16,6 +16,7 @@
 // products take the same bytes eight at a time: only that both operands agree matters.
 #include <hip/hip_runtime.h>
 #include <algorithm>
+#include <type_traits>
 
 #include "ssd_device.hpp"
 #include "ssd_launch.hpp"
@@ -110,7 +111,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void ssd_proj_rows_kernel(ProjAr
         float s[U][MT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int b = min(b0 + u * kSkinnyWaves, blocks - 1);
+            const int b = b0 + u * kSkinnyWaves;
+            if (b >= blocks) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 // past K the row's last bytes stand in, against activations of 0
@@ -196,13 +198,13 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
 
     const int blocks = (p.K + 127) / 128;
     // what a lane copies: piece c of row 8 j + l / 8 for the wave's j-th copy, weights first
+    static_assert(kCopies % 2 == 0, "the place of a lane's piece goes by j's parity");
     uint32_t row_off[kCopies];
     const uint8_t* base[kCopies];
-    int piece[kCopies];
+    const int piece0 = 16 * ((l % 8) ^ (l >> 4));   // at(): (r >> 1) & 7 = 4 (j & 1) + l / 16
 #pragma unroll
     for (int j = 0; j < kCopies; ++j) {
         const int first = 8 * (wave * kCopies + j), r = first + l / 8;
-        piece[j] = 16 * ((l % 8) ^ ((r >> 1) & 7));
         if (first < BN) {
             base[j] = p.w + (int64_t)n0 * p.w_stride;
             row_off[j] = (uint32_t)min(r, p.N - 1 - n0) * (uint32_t)p.w_stride;
@@ -212,46 +214,65 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
         }
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
-    auto issue = [&](int b) {
-        const uint32_t to = lds0 + (b & 1) * kStage + wave * kCopies * 1024;
-#pragma unroll
-        for (int j = 0; j < kCopies; ++j)
-            dma16(base[j], row_off[j] + (uint32_t)min(b * 128 + piece[j], p.K - 16), to + j * 1024);
+    // the wave's j-th copy of block b
+    auto copy = [&](int b, int j) {
+        dma16(base[j], row_off[j] + (uint32_t)min(b * 128 + (j & 1 ? piece0 ^ 64 : piece0), p.K - 16),
+              lds0 + (b & 1) * kStage + wave * kCopies * 1024 + j * 1024);
     };
-    const float* as[WM];
+    // rows of the activations' scales: 255 of at most 2^24 bytes each fit 32 bits
+    uint32_t as_off[WM];
 #pragma unroll
-    for (int t = 0; t < WM; ++t) as[t] = p.a_scale + (int64_t)min(m0 + 16 * (wm * WM + t) + i, p.M - 1) * p.a_scale_stride;
+    for (int t = 0; t < WM; ++t)
+        as_off[t] = (uint32_t)min(16 * (wm * WM + t) + i, p.M - 1 - m0) * (uint32_t)(p.a_scale_stride * 4);
+    const char* as = reinterpret_cast<const char*>(p.a_scale + (int64_t)m0 * p.a_scale_stride);
+    auto a_scale = [&](int b, int t) { return *reinterpret_cast<const float*>(as + (size_t)b * 4 + as_off[t]); };
     const float* ws = p.w_scale + (int64_t)(min(n0 + 16 * wn * WN, p.N - 1) / 128) * p.w_scale_stride;
 
-    f32x4 acc[WN][WM];
+    f32x4 acc[WN][WM], d[2][WM];                    // d: inner sums, one row of products behind its addition to acc
 #pragma unroll
-    for (int u = 0; u < WN; ++u)
+    for (int t = 0; t < WM; ++t) {
+        d[1][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int t = 0; t < WM; ++t) acc[u][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float next[WM], nw = ws[0];
+        for (int u = 0; u < WN; ++u) acc[u][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    static_assert(WN % 2 == 0, "the last row of products is d[1]");
+    float next[WM], s[WM], last[WM], nw = ws[0];
 #pragma unroll
-    for (int t = 0; t < WM; ++t) next[t] = as[t][0];
-    issue(0);
-    for (int b = 0; b < blocks; ++b) {
-        float s[WM];
+    for (int t = 0; t < WM; ++t) {
+        next[t] = a_scale(0, t);
+        s[t] = 0.0f;
+    }
 #pragma unroll
-        for (int t = 0; t < WM; ++t) s[t] = next[t] * nw;
+    for (int j = 0; j < kCopies; ++j) copy(0, j);
+    auto block = [&](int b, auto more) {
+        constexpr bool MORE = decltype(more)::value;
+#pragma unroll
+        for (int t = 0; t < WM; ++t) {
+            last[t] = s[t];
+            s[t] = next[t] * nw;
+        }
         // this wave's copies of block b have landed, and then everyone's; the other stage has been read by all
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (b + 1 < blocks) {
+        if (MORE) {
             nw = ws[b + 1];
 #pragma unroll
-            for (int t = 0; t < WM; ++t) next[t] = as[t][b + 1];
-            issue(b + 1);
+            for (int t = 0; t < WM; ++t) next[t] = a_scale(b + 1, t);
         }
         const uint8_t* stage = lds + (b & 1) * kStage;
-        Bytes ba[WM];
+        auto weights = [&](int u) {
+            Bytes w;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w.h[h] = *reinterpret_cast<const u32x4_t*>(stage + at(16 * (wn * WN + u) + i, 2 * g + h));
+            return w;
+        };
+        Bytes bw = weights(0), ba[WM];
 #pragma unroll
         for (int t = 0; t < WM; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 ba[t].h[h] = *reinterpret_cast<const u32x4_t*>(stage + BN * 128 + at(16 * (wm * WM + t) + i, 2 * g + h));
-        if (b * 128 + 128 > p.K) {                  // past K the row's last bytes stand in, against activations of 0
+        if (!MORE && b * 128 + 128 > p.K) {          // past K the row's last bytes stand in, against activations of 0
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (b * 128 + g * 32 + h * 16 >= p.K) {
@@ -262,19 +283,35 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
         Frag<T> fa[WM] = {Frag<T>(ba[0]), Frag<T>(ba[1]), Frag<T>(ba[2]), Frag<T>(ba[3])};
 #pragma unroll
         for (int u = 0; u < WN; ++u) {
-            Bytes bw;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                bw.h[h] = *reinterpret_cast<const u32x4_t*>(stage + at(16 * (wn * WN + u) + i, 2 * g + h));
             const Frag<T> fw(bw);
+            if (u + 1 < WN) bw = weights(u + 1);
+            if (MORE) {
+#pragma unroll
+                for (int j = u * kCopies / WN; j < (u + 1) * kCopies / WN; ++j) copy(b + 1, j);
+            }
+            // the products of this row while the last row's are scaled and added
 #pragma unroll
             for (int t = 0; t < WM; ++t) {
-                const f32x4 d = inner(fw, fa[t]);
+                d[u & 1][t] = inner(fw, fa[t]);
+                const f32x4 v = d[1 - (u & 1)][t];
+                f32x4& to = acc[u ? u - 1 : WN - 1][t];
+                const float f = u ? s[t] : last[t];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[u][t][e] = fmaf(d[e], s[t], acc[u][t][e]);
+                for (int e = 0; e < 4; ++e) to[e] = fmaf(v[e], f, to[e]);
+                if (!MORE) asm volatile("" : "+v"(to));      // here: the compiler would hold d for additions at the stores
+                __builtin_amdgcn_sched_group_barrier(0x008, sizeof(T) == 2 ? 1 : 4, 0);      // matrix
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                           // vector
             }
         }
-    }
+    };
+    for (int b = 0; b + 1 < blocks; ++b) block(b, std::true_type{});
+    block(blocks - 1, std::false_type{});
+#pragma unroll
+    for (int t = 0; t < WM; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[WN - 1][t][e] = fmaf(d[1][t][e], s[t], acc[WN - 1][t][e]);
+#pragma unroll
+    for (int t = 0; t < WM; ++t) asm volatile("" : "+v"(acc[WN - 1][t]));
     T* y = static_cast<T*>(p.y);
 #pragma unroll
     for (int t = 0; t < WM; ++t) {
@@ -313,7 +350,8 @@ hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
         if constexpr (sizeof(T) == 2) return tiles<T, 8, 4, 2, 4>(p, s);
         else return tiles<T, 4, 4, 2, 4>(p, s);     // widened operands take twice the registers
     }
-    return tiles<T, 4, 4, 2, 2>(p, s);
+    if constexpr (sizeof(T) == 2) return tiles<T, 4, 4, 2, 2>(p, s);
+    else return tiles<T, 2, 4, 4, 2>(p, s);
 }
 
 }  // namespace
