@@ -12,8 +12,8 @@
 // 2^-9 by which y is rounded.  For y in fp32 that would show, so the bytes are widened to bf16, which holds them exactly,
 // and the sum taken on v_mfma_f32_16x16x32_bf16 (6e-8 of y), whose rate is half.
 //
-// Operand layout of the 16x16x128 product, for lane l: row l % 16, bytes 32 (l / 16) .. + 32 of the block.  The bf16
-// products take the same bytes eight at a time: only that both operands agree matters.
+// Operand layout of the 16x16x128 product, for lane l: row l % 16 and 32 bytes of the block, the same ones of both operands.
+// The bf16 products take them eight at a time.
 #include <hip/hip_runtime.h>
 #include <algorithm>
 #include <type_traits>
@@ -91,7 +91,7 @@ template <typename T, int MT, int U>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void ssd_proj_rows_kernel(ProjArgs p) {
     __shared__ f32x4 part[kSkinnyWaves][MT][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, i = l % 16, g = l / 16;
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
+    const int tn = (p.N + 15) / 16, n0 = blockIdx.x % tn * 16, m0 = blockIdx.x / tn * 16 * MT;
     const int blocks = (p.K + 127) / 128;
     const uint8_t* w = p.w + (int64_t)min(n0 + i, p.N - 1) * p.w_stride;
     const uint8_t* a[MT];
@@ -158,31 +158,36 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void ssd_proj_rows_kernel(ProjAr
 }
 
 // ------------------------------------------------------------ many rows: tiles through LDS
-// LDS DMA, 16 bytes a lane to lds + 16 l, written so that the compiler does not model it (it would wait for every copy in
-// flight before each LDS read); base and lds are the wave's.
-__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t voff, uint32_t lds) {
-    uint32_t m0_saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %3\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %1, %2\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(m0_saved)
-        : "v"(voff), "s"(base), "s"(lds)
-        : "memory");
-}
+// LDS DMA, 16 bytes a lane to lds + 16 l (4 bytes to lds + 4 l), written so that the compiler does not model it (it would
+// wait for every copy in flight before each LDS read); base and lds are the wave's.
+#define SSD_DMA(width)                                                                                           \
+    uint32_t m0_saved;                                                                                           \
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_" width " %1, %2\n\ts_mov_b32 m0, %0" \
+                 : "=&s"(m0_saved)                                                                               \
+                 : "v"(voff), "s"(base), "s"(lds)                                                                \
+                 : "memory")
+__device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t lds) { SSD_DMA("dwordx4"); }
+__device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t lds) { SSD_DMA("dword"); }
+#undef SSD_DMA
 
 // Byte of piece c (16 bytes) of row r in a tile of 128-byte rows: sixteen rows at one piece fall on sixteen different
 // sixteenths of the LDS banks.
 __device__ __forceinline__ uint32_t at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ ((r >> 1) & 7)) << 4)); }
+// The h-th piece of a block that lane group g holds (the same of both operands, so that any assignment will do).  A 16-byte
+// LDS read takes sixteen lanes a clock, and not sixteen neighbours: eight rows of one group go with the other eight rows
+// of the next, whose piece differs in the last bit only, which at() keeps apart.  (With pieces 2 g and 2 g + 1 every read
+// took twice as long.)
+__device__ __forceinline__ int piece_of(int g, int h) { return (g & 1) | h << 1 | (g >> 1) << 2; }
 
 // A workgroup of NWN x NWM waves owns a tile of y; a wave's part of it is WN x WM products of 16 x 16.  The two operands'
-// block of 128 bytes a row goes through one of two LDS stages while the other is computed.
+// block of 128 bytes a row goes through one of two LDS stages while the other is computed, and so do the activations'
+// scales of 16 blocks at a time: read by the lanes that need them, they would be as many requests as the operands.
+template <int BN, int BM> constexpr int kTileLds = 2 * (BN + BM) * 128 + 2 * BM * 16 * 4;
 template <typename T, int WN, int WM, int NWN, int NWM>
 __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjArgs p) {
     constexpr int NW = NWN * NWM, BN = 16 * WN * NWN, BM = 16 * WM * NWM, kStage = (BN + BM) * 128;
     constexpr int kCopies = (BN + BM) / 8 / NW;     // of a wave: 8 rows each
+    constexpr int kPerRow = (2 * kCopies + WN - 1) / WN;      // copies beside a row of products: all in a block's first half
     static_assert(kCopies * 8 * NW == BN + BM && 128 % (16 * WN) == 0 && WM == 4, "tile");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, i = l % 16, g = l / 16;
@@ -197,73 +202,78 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
     const int n0 = in / rows * BN, m0 = (panel * 8 + in % rows) * BM;
 
     const int blocks = (p.K + 127) / 128;
-    // what a lane copies: piece c of row 8 j + l / 8 for the wave's j-th copy, weights first
-    static_assert(kCopies % 2 == 0, "the place of a lane's piece goes by j's parity");
-    uint32_t row_off[kCopies];
-    const uint8_t* base[kCopies];
+    // What a wave copies: kCopies times 8 rows, of the weights or (the later waves) the activations; lane l the piece at
+    // place l % 8 of the l / 8-th.  Rows past the operand's last are that one; where there are none, an 8-row step is a
+    // scalar's and a lane's offset is one register.
+    static_assert(kCopies % 2 == 0 && BN % (8 * kCopies) == 0, "a wave copies rows of one operand");
     const int piece0 = 16 * ((l % 8) ^ (l >> 4));   // at(): (r >> 1) & 7 = 4 (j & 1) + l / 16
-#pragma unroll
-    for (int j = 0; j < kCopies; ++j) {
-        const int first = 8 * (wave * kCopies + j), r = first + l / 8;
-        if (first < BN) {
-            base[j] = p.w + (int64_t)n0 * p.w_stride;
-            row_off[j] = (uint32_t)min(r, p.N - 1 - n0) * (uint32_t)p.w_stride;
-        } else {
-            base[j] = p.a + (int64_t)m0 * p.a_stride;
-            row_off[j] = (uint32_t)min(r - BN, p.M - 1 - m0) * (uint32_t)p.a_stride;
-        }
-    }
+    const int row0 = 8 * wave * kCopies;
+    const bool of_w = row0 < BN;
+    const uint8_t* base = of_w ? p.w + (int64_t)(n0 + row0) * p.w_stride : p.a + (int64_t)(m0 + row0 - BN) * p.a_stride;
+    const int most = of_w ? p.N - 1 - n0 - row0 : p.M - 1 - m0 - (row0 - BN);     // rows of the operand after row0
+    const uint32_t row_bytes = (uint32_t)(of_w ? p.w_stride : p.a_stride);
+    const bool whole = most >= 8 * kCopies - 1;
+    if (most < 0) base += (int64_t)most * row_bytes;                              // row0 itself is past the last
+    const uint32_t lane_off = (uint32_t)(l / 8) * row_bytes;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
     // the wave's j-th copy of block b
-    auto copy = [&](int b, int j) {
-        dma16(base[j], row_off[j] + (uint32_t)min(b * 128 + (j & 1 ? piece0 ^ 64 : piece0), p.K - 16),
-              lds0 + (b & 1) * kStage + wave * kCopies * 1024 + j * 1024);
+    auto copy = [&](int b, int j, auto full) {
+        const uint32_t k = (uint32_t)min(b * 128 + (j & 1 ? piece0 ^ 64 : piece0), p.K - 16);
+        const uint32_t to = lds0 + (b & 1) * kStage + wave * kCopies * 1024 + j * 1024;
+        if constexpr (decltype(full)::value) dma16(base + (size_t)(8 * j) * row_bytes, lane_off + k, to);
+        else dma16(base, (uint32_t)min(8 * j + l / 8, max(most, 0)) * row_bytes + k, to);
     };
-    // rows of the activations' scales: 255 of at most 2^24 bytes each fit 32 bits
-    uint32_t as_off[WM];
-#pragma unroll
-    for (int t = 0; t < WM; ++t)
-        as_off[t] = (uint32_t)min(16 * (wm * WM + t) + i, p.M - 1 - m0) * (uint32_t)(p.a_scale_stride * 4);
+    // the scales of blocks 16 q .. + 15 go to rows of 16, block c of row r at place c ^ (r % 16): sixteen rows' scales of one
+    // block are in sixteen banks.  Rows of at most 2^24 bytes, 255 of them: offsets fit 32 bits.
+    constexpr int kScales = 2 * kStage, kScaleCopies = BM / 4 / NW;       // of a wave: 4 rows each
+    static_assert(kScaleCopies * 4 * NW == BM, "scales");
     const char* as = reinterpret_cast<const char*>(p.a_scale + (int64_t)m0 * p.a_scale_stride);
-    auto a_scale = [&](int b, int t) { return *reinterpret_cast<const float*>(as + (size_t)b * 4 + as_off[t]); };
+    auto copy_scales = [&](int q) {
+#pragma unroll
+        for (int j = 0; j < kScaleCopies; ++j) {
+            const int first = 4 * (wave * kScaleCopies + j), r = first + g;
+            const uint32_t row = (uint32_t)min(r, p.M - 1 - m0) * (uint32_t)(p.a_scale_stride * 4);
+            dma4(as, row + 4 * (uint32_t)min(16 * q + (i ^ (r & 15)), blocks - 1), lds0 + kScales + (q & 1) * BM * 64 + first * 64);
+        }
+    };
+    // of the wave's rows, block b
+    auto a_scale = [&](int b, int t) {
+        return *reinterpret_cast<const float*>(lds + kScales + (b >> 4 & 1) * BM * 64 + (16 * (wm * WM + t) + i) * 64 + ((b & 15) ^ i) * 4);
+    };
     const float* ws = p.w_scale + (int64_t)(min(n0 + 16 * wn * WN, p.N - 1) / 128) * p.w_scale_stride;
 
-    f32x4 acc[WN][WM], d[2][WM];                    // d: inner sums, one row of products behind its addition to acc
+    f32x4 acc[WN][WM], d[WM];                       // d: inner sums of a row of products, until the next row's take their place
 #pragma unroll
     for (int t = 0; t < WM; ++t) {
-        d[1][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        d[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int u = 0; u < WN; ++u) acc[u][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    static_assert(WN % 2 == 0, "the last row of products is d[1]");
-    float next[WM], s[WM], last[WM], nw = ws[0];
+    float s[WM], last[WM], nw = ws[0];
 #pragma unroll
-    for (int t = 0; t < WM; ++t) {
-        next[t] = a_scale(0, t);
-        s[t] = 0.0f;
-    }
+    for (int t = 0; t < WM; ++t) s[t] = 0.0f;
+    copy_scales(0);
 #pragma unroll
-    for (int j = 0; j < kCopies; ++j) copy(0, j);
-    auto block = [&](int b, auto more) {
+    for (int j = 0; j < kCopies; ++j) copy(0, j, std::false_type{});
+    auto block = [&](int b, auto more, auto full) {
         constexpr bool MORE = decltype(more)::value;
+        // this wave's copies of block b have landed, and then everyone's; the other stage has been read by all
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
         for (int t = 0; t < WM; ++t) {
             last[t] = s[t];
-            s[t] = next[t] * nw;
+            s[t] = a_scale(b, t) * nw;
         }
-        // this wave's copies of block b have landed, and then everyone's; the other stage has been read by all
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (MORE) {
             nw = ws[b + 1];
-#pragma unroll
-            for (int t = 0; t < WM; ++t) next[t] = a_scale(b + 1, t);
+            if (b % 16 == 0) copy_scales(b / 16 + 1);
         }
         const uint8_t* stage = lds + (b & 1) * kStage;
         auto weights = [&](int u) {
             Bytes w;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                w.h[h] = *reinterpret_cast<const u32x4_t*>(stage + at(16 * (wn * WN + u) + i, 2 * g + h));
+                w.h[h] = *reinterpret_cast<const u32x4_t*>(stage + at(16 * (wn * WN + u) + i, piece_of(g, h)));
             return w;
         };
         Bytes bw = weights(0), ba[WM];
@@ -271,11 +281,11 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
         for (int t = 0; t < WM; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                ba[t].h[h] = *reinterpret_cast<const u32x4_t*>(stage + BN * 128 + at(16 * (wm * WM + t) + i, 2 * g + h));
+                ba[t].h[h] = *reinterpret_cast<const u32x4_t*>(stage + BN * 128 + at(16 * (wm * WM + t) + i, piece_of(g, h)));
         if (!MORE && b * 128 + 128 > p.K) {          // past K the row's last bytes stand in, against activations of 0
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (b * 128 + g * 32 + h * 16 >= p.K) {
+                if (b * 128 + piece_of(g, h) * 16 >= p.K) {
 #pragma unroll
                     for (int t = 0; t < WM; ++t) ba[t].h[h] = u32x4_t{0, 0, 0, 0};
                 }
@@ -283,33 +293,36 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
         Frag<T> fa[WM] = {Frag<T>(ba[0]), Frag<T>(ba[1]), Frag<T>(ba[2]), Frag<T>(ba[3])};
 #pragma unroll
         for (int u = 0; u < WN; ++u) {
+            if (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);      // a row at a time: the registers
             const Frag<T> fw(bw);
             if (u + 1 < WN) bw = weights(u + 1);
             if (MORE) {
 #pragma unroll
-                for (int j = u * kCopies / WN; j < (u + 1) * kCopies / WN; ++j) copy(b + 1, j);
+                for (int j = u * kPerRow; j < min((u + 1) * kPerRow, kCopies); ++j) copy(b + 1, j, full);
             }
             // the products of this row while the last row's are scaled and added
 #pragma unroll
             for (int t = 0; t < WM; ++t) {
-                d[u & 1][t] = inner(fw, fa[t]);
-                const f32x4 v = d[1 - (u & 1)][t];
                 f32x4& to = acc[u ? u - 1 : WN - 1][t];
                 const float f = u ? s[t] : last[t];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) to[e] = fmaf(v[e], f, to[e]);
+                for (int e = 0; e < 4; ++e) to[e] = fmaf(d[t][e], f, to[e]);
+                d[t] = inner(fw, fa[t]);
                 if (!MORE) asm volatile("" : "+v"(to));      // here: the compiler would hold d for additions at the stores
-                __builtin_amdgcn_sched_group_barrier(0x008, sizeof(T) == 2 ? 1 : 4, 0);      // matrix
                 __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                           // vector
+                __builtin_amdgcn_sched_group_barrier(0x008, sizeof(T) == 2 ? 1 : 4, 0);      // matrix
             }
         }
     };
-    for (int b = 0; b + 1 < blocks; ++b) block(b, std::true_type{});
-    block(blocks - 1, std::false_type{});
+    if (whole)
+        for (int b = 0; b + 1 < blocks; ++b) block(b, std::true_type{}, std::true_type{});
+    else
+        for (int b = 0; b + 1 < blocks; ++b) block(b, std::true_type{}, std::false_type{});
+    block(blocks - 1, std::false_type{}, std::false_type{});
 #pragma unroll
     for (int t = 0; t < WM; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[WN - 1][t][e] = fmaf(d[1][t][e], s[t], acc[WN - 1][t][e]);
+        for (int e = 0; e < 4; ++e) acc[WN - 1][t][e] = fmaf(d[t][e], s[t], acc[WN - 1][t][e]);
 #pragma unroll
     for (int t = 0; t < WM; ++t) asm volatile("" : "+v"(acc[WN - 1][t]));
     T* y = static_cast<T*>(p.y);
@@ -327,13 +340,14 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
 
 template <typename T, int MT, int U>
 hipError_t rows(const ProjArgs& p, hipStream_t s) {
-    const dim3 grid((p.N + 15) / 16, (p.M + 16 * MT - 1) / (16 * MT));
+    const int64_t n = (int64_t)((p.N + 15) / 16), m = (int64_t)((p.M + 16 * MT - 1) / (16 * MT));
+    const dim3 grid((unsigned)(n * m));
     hipLaunchKernelGGL((ssd_proj_rows_kernel<T, MT, U>), grid, dim3(64 * kSkinnyWaves), 0, s, p);
     return hipGetLastError();
 }
 template <typename T, int WN, int WM, int NWN, int NWM>
 hipError_t tiles(const ProjArgs& p, hipStream_t s) {
-    constexpr int BN = 16 * WN * NWN, BM = 16 * WM * NWM, lds = 2 * (BN + BM) * 128;
+    constexpr int BN = 16 * WN * NWN, BM = 16 * WM * NWM, lds = kTileLds<BN, BM>;
     const auto kernel = &ssd_proj_tiles_kernel<T, WN, WM, NWN, NWM>;
     if (hipError_t e = prepare_launch(reinterpret_cast<const void*>(kernel), lds)) return e;
     const int64_t n = (int64_t)((p.N + BN - 1) / BN) * ((p.M + BM - 1) / BM);
@@ -341,17 +355,34 @@ hipError_t tiles(const ProjArgs& p, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The kernel by its estimated time in us, from sweeps of M, N and K (256 CUs):
+//  - rows: a workgroup reads 16 rows of w and 16 MT of a, 2 KB a block each, at some 28 bytes a ns and CU from one workgroup
+//    or more, 40 where an XCD's 4 MB of L2 hold the weights; 3 us around it.
+//  - tiles of 128 x 128: 0.45 us a block (1 us with widened operands) for one a CU, 0.75 for every further one; 5 us.
+//  - tiles of 256 x 256, one a CU: 1.85 us a block, against 0.7 a 128 x 128 tile when there are many.
+// Measured, bf16, N = 5152, K = 2048: M = 32 rows 9.4, tiles 11.7; M = 64 rows 12.9, tiles 12.2; M = 256 rows 41, tiles 13.3;
+// N = 1024, K = 8192, M = 64: rows 11 (MT = 1; 16 with 2), tiles 37.  M = 777, N = 1000, K = 1040, fp32: rows 10.9, tiles
+// 15.7.  M = 4096, N = 5152, K = 2048: tiles of 128 60, of 256 64; M = N = K = 4096: 95 and 66.
 template <typename T>
 hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
-    if (p.M <= 16) return rows<T, 1, 4>(p, s);
-    if (p.M <= 32) return rows<T, 2, 2>(p, s);
-    if (p.M <= 256) return rows<T, 4, 2>(p, s);
-    if ((int64_t)((p.N + 255) / 256) * ((p.M + 255) / 256) >= 192) {
-        if constexpr (sizeof(T) == 2) return tiles<T, 8, 4, 2, 4>(p, s);
-        else return tiles<T, 4, 4, 2, 4>(p, s);     // widened operands take twice the registers
+    const auto over = [](double n, int d) { return (double)(((int64_t)n + d - 1) / d); };
+    const double blocks = over(p.K, 128), n16 = over(p.N, 16), small = over(p.N, 128) * over(p.M, 128);
+    const double piece = (int64_t)p.N * p.K <= 4 << 20 ? 0.05 : 0.073;
+    double best = 0.0;
+    int mt = 0;
+    for (int k : {1, 2}) {
+        const double wgs = n16 * over(p.M, 16 * k), t = 3.0 + blocks * piece * (1 + k) * std::max(1.0, wgs / 256);
+        if (!mt || t < best) {
+            mt = k;
+            best = t;
+        }
     }
-    if constexpr (sizeof(T) == 2) return tiles<T, 4, 4, 2, 2>(p, s);
-    else return tiles<T, 2, 4, 4, 2>(p, s);
+    const double one = sizeof(T) == 2 ? 0.45 : 1.0;
+    if (best < 5.0 + blocks * (one + 0.75 * std::max(0.0, small / 256 - 1.0))) return mt == 1 ? rows<T, 1, 4>(p, s) : rows<T, 2, 2>(p, s);
+    if constexpr (sizeof(T) == 2) {                  // widened operands take too many registers for the larger tile
+        if (over(over(p.N, 256) * over(p.M, 256), 256) * 1.85 < 0.7 * small / 256) return tiles<T, 8, 4, 2, 4>(p, s);
+    }
+    return tiles<T, 4, 4, 2, 2>(p, s);
 }
 
 }  // namespace

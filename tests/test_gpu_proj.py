@@ -48,7 +48,8 @@ def verify(ssd, d, t, **kw):
 
 
 SIZES = [(1, 1, 16), (1, 16, 128), (3, 17, 144), (16, 128, 256), (17, 129, 1040), (32, 100, 512), (33, 300, 400), (64, 64, 4096),
-         (65, 130, 2064), (100, 5, 16), (257, 128, 128), (300, 260, 1040), (513, 1000, 272), (129, 2000, 640)]
+         (65, 130, 2064), (100, 5, 16), (257, 128, 128), (300, 260, 1040), (513, 1000, 272), (129, 2000, 640),
+         (260, 140, 4368), (300, 129, 2048), (257, 40, 2064), (520, 256, 6000)]
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
@@ -58,7 +59,7 @@ def test_proj(gpu_lib, M, N, K, t):
     verify(gpu_lib, make(M, N, K), t)
 
 
-@pytest.mark.parametrize("M,N,K", [(3600, 3500, 272), (3585, 3600, 128), (4096, 4096, 144)])
+@pytest.mark.parametrize("M,N,K", [(3600, 3500, 272), (3585, 3600, 128), (4096, 4096, 144), (3600, 3500, 4384), (3585, 3600, 2064)])
 def test_proj_of_many_tiles(gpu_lib, M, N, K):
     """Sizes at which the largest tiles are taken, full and cut, in every place of the launch order."""
     d = make(M, N, K)
