@@ -1,0 +1,307 @@
+"""The gated linear recurrence, the norm with the residual's addition and the 8-bit projection without a GPU: what the C ABI
+and the torch binding refuse on the host, before any HIP call, with the documented status and a message naming the
+argument; and the workspace sizes."""
+import os
+
+import pytest
+import torch
+
+FAKE = 0x10000          # 16-byte aligned, never dereferenced: every call below fails validation
+MIS = 0x10008           # 8-byte aligned only
+INT_MAX = 0x7fffffff
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import selective_state_space_14_amd as ssd
+    if not os.path.exists(ssd.LIB_PATH):
+        from selective_state_space_14_amd import build
+        build.build(verbose=False)
+    return ssd.load()
+
+
+def at(i):
+    return FAKE + 0x1000 * i
+
+
+def refused(lib, st, status, needle):
+    assert st == status, (st, lib.ssd_last_error())
+    assert needle in lib.ssd_last_error().decode(), lib.ssd_last_error()
+
+
+GLR = dict(B=2, L=1000, D=130, dtype=1, x=at(1), xs=130, r=at(2), rs=390, i=at(3), is_=131, rb=at(4), ib=None, A=at(5), doc=None,
+           len=None, h0=None, hf=None, cs=None, y=at(6), ys=130, ws=at(7), wsb=1 << 40, state=at(8), gy=at(9), gys=130, gS=None,
+           dx=at(10), dxs=130, dr=at(11), drs=130, di=at(12), dis=130, dA=at(13), drb=at(14), dib=None, dh0=None)
+HEAD = ("x", "xs", "r", "rs", "i", "is_", "rb", "ib", "A")
+
+
+def glr(lib, kind, over):
+    a = {**GLR, **over}
+    v = lambda *names: [a[n] for n in names]  # noqa: E731
+    if kind == "fwd":
+        return lib.ssd_glr_scan_fwd(*v("B", "L", "D", "dtype", *HEAD, "doc", "len", "h0", "hf", "cs", "y", "ys", "ws", "wsb"), None)
+    if kind == "step":
+        return lib.ssd_glr_step(*v("B", "D", "dtype", *HEAD, "state", "y", "ys"), None)
+    return lib.ssd_glr_scan_bwd(*v("B", "L", "D", "dtype", *HEAD, "doc", "len", "h0", "cs", "gy", "gys", "gS", "dx", "dxs", "dr", "drs",
+                                   "di", "dis", "dA", "drb", "dib", "dh0", "ws", "wsb"), None)
+
+
+COMMON = [
+    (dict(dtype=2), 3, "dtype=2"),
+    (dict(B=-1), 2, "B=-1"),
+    (dict(D=0), 2, "D=0"),
+    (dict(B=INT_MAX, D=130), 2, "are too many"),
+    (dict(x=None), 1, "x is NULL"),
+    (dict(r=None), 1, "r is NULL"),
+    (dict(i=None), 1, "i is NULL"),
+    (dict(A=None), 1, "A is NULL"),
+    (dict(xs=129), 2, "x row stride 129 is smaller"),
+    (dict(is_=0), 2, "i row stride 0 is smaller"),
+    (dict(rs=(1 << 22) + 1), 2, "r row stride 4194305 is above"),
+    (dict(x=FAKE + 1), 4, "x="),
+    (dict(A=FAKE + 2), 4, "A="),
+    (dict(rb=FAKE + 1), 4, "r_bias"),
+    (dict(ib=FAKE + 3), 4, "i_bias"),
+]
+SCAN = [
+    (dict(L=-1), 2, "L=-1"),
+    (dict(L=(1 << 30) + 1), 2, "L=1073741825 is above"),
+    (dict(B=1 << 20, L=1 << 20), 2, "are too many"),
+    (dict(doc=FAKE + 1), 4, "doc_ids"),
+    (dict(len=FAKE + 2), 4, "lengths"),
+    (dict(h0=MIS), 4, "init_state"),
+    (dict(cs=MIS), 4, "chunk_states"),
+    (dict(ws=None), 5, "smaller than the required"),
+    (dict(wsb=1000), 5, "workspace_bytes=1000"),
+    (dict(ws=MIS), 4, "workspace="),
+]
+
+
+@pytest.mark.parametrize("over,status,needle", COMMON + SCAN + [
+    (dict(y=None), 1, "y is NULL"),
+    (dict(ys=100), 2, "y row stride 100"),
+    (dict(hf=MIS), 4, "final_state"),
+    (dict(y=at(1)), 2, "an output must not alias an input"),
+    (dict(y=at(20), hf=at(20)), 2, "must not alias"),
+    (dict(cs=at(20), hf=at(20)), 2, "must not alias"),
+    (dict(cs=at(20), h0=at(20)), 2, "must not alias"),
+    (dict(cs=at(6)), 2, "two outputs must not alias"),
+])
+def test_glr_scan_refusals(lib, over, status, needle):
+    refused(lib, glr(lib, "fwd", over), status, needle)
+
+
+@pytest.mark.parametrize("over,status,needle", COMMON + [
+    (dict(y=None), 1, "y is NULL"),
+    (dict(state=None), 1, "state is NULL"),
+    (dict(state=MIS), 4, "state="),
+    (dict(state=at(6)), 2, "two outputs must not alias"),
+    (dict(y=at(2)), 2, "an output must not alias an input"),
+])
+def test_glr_step_refusals(lib, over, status, needle):
+    refused(lib, glr(lib, "step", over), status, needle)
+
+
+@pytest.mark.parametrize("over,status,needle", COMMON + SCAN + [
+    (dict(gy=None), 1, "grad_y is NULL"),
+    (dict(dx=None), 1, "dx is NULL"),
+    (dict(dr=None), 1, "dr is NULL"),
+    (dict(di=FAKE + 1), 4, "di="),
+    (dict(drs=129), 2, "dr row stride 129"),
+    (dict(dA=None), 1, "dA is NULL"),
+    (dict(dib=FAKE + 2), 4, "di_bias"),
+    (dict(gS=MIS), 4, "grad_final_state"),
+    (dict(dh0=MIS), 4, "grad_init_state"),
+    (dict(dx=at(9)), 2, "an output must not alias an input"),
+    (dict(gS=at(20), dh0=at(20)), 2, "an output must not alias an input"),
+    (dict(cs=at(20), dh0=at(20)), 2, "an output must not alias an input"),
+    (dict(dr=at(10)), 2, "two outputs must not alias"),
+])
+def test_glr_bwd_refusals(lib, over, status, needle):
+    refused(lib, glr(lib, "bwd", over), status, needle)
+
+
+NORM = dict(R=10, W=64, xd=1, rd=1, d=1, rms=1, eps=1e-5, x=at(1), xs=64, res=at(2), rs=64, w=at(3), b=None, z=None, zs=0, s=at(4),
+            ss=64, y=at(5), ys=64, q=at(6), qs=64, sc=at(7), scs=1, gy=at(8), gys=64, gs=at(9), gss=64, ds=at(10), dss=64, dw=at(11),
+            db=None, dz=None, dzs=0, ws=at(12), wsb=1 << 30)
+
+
+def add_norm(lib, bwd, over):
+    a = {**NORM, **over}
+    v = lambda *names: [a[n] for n in names]  # noqa: E731
+    if bwd:
+        return lib.ssd_add_norm_bwd(*v("R", "W", "rd", "d", "rms", "eps", "s", "ss", "w", "b", "z", "zs", "gy", "gys", "gs", "gss", "ds",
+                                       "dss", "dw", "db", "dz", "dzs", "ws", "wsb"), None)
+    return lib.ssd_add_norm_fwd(*v("R", "W", "xd", "rd", "d", "rms", "eps", "x", "xs", "res", "rs", "w", "b", "z", "zs", "s", "ss", "y",
+                                   "ys", "q", "qs", "sc", "scs"), None)
+
+
+ROWS = [
+    (dict(rd=2), 3, "dtype=2"),
+    (dict(d=-1), 3, "dtype=-1"),
+    (dict(R=-1), 2, "R=-1"),
+    (dict(R=1 << 31), 2, "too many"),
+    (dict(W=0), 2, "W=0"),
+    (dict(W=16385), 3, "W=16385"),
+    (dict(rms=2), 3, "rms=2"),
+    (dict(eps=-1.0), 3, "eps=-1"),
+    (dict(eps=float("nan")), 3, "eps=nan"),
+    (dict(z=at(20), zs=32), 2, "z row stride 32"),
+    (dict(ss=63), 2, "sum row stride 63"),
+    (dict(ss=(1 << 22) + 1), 2, "above 4194304"),
+    (dict(s=FAKE + 1), 4, "sum="),
+    (dict(w=FAKE + 2), 4, "weight"),
+    (dict(b=FAKE + 1), 4, "bias"),
+]
+
+
+@pytest.mark.parametrize("over,status,needle", ROWS + [
+    (dict(xd=3), 3, "dtype=3"),
+    (dict(x=None), 1, "x is NULL"),
+    (dict(W=8193, xs=8193, rs=8193, ss=8193, ys=8193, qs=8193, scs=65), 4, "W=8193 above 8192"),
+    (dict(W=16384, xs=16386, rs=16384, ss=16384, ys=16384, qs=16384, scs=128), 4, "W=16384 above 8192"),
+    (dict(W=16384, xs=16384, rs=16384, ss=16384, ys=16384, qs=16385, scs=128), 4, "W=16384 above 8192"),
+    (dict(sc=None), 1, "q_scale is NULL"),
+    (dict(q=None), 1, "q_scale is given but q is NULL"),
+    (dict(q=None, sc=None, y=None), 1, "y and q are both NULL"),
+    (dict(W=200, xs=200, rs=200, ss=200, ys=200, qs=200), 2, "q_scale row stride 1 is smaller than the 2 blocks"),
+    (dict(sc=FAKE + 2), 4, "q_scale"),
+    (dict(qs=63), 2, "q row stride 63"),
+    (dict(res=None), 1, "sum is given but residual is NULL"),
+    (dict(s=at(2), ss=72), 2, "needs its row stride and type"),
+    (dict(s=at(1), xd=0), 2, "needs its row stride and type"),
+    (dict(y=at(1)), 2, "an output must not alias an input"),
+    (dict(y=at(2)), 2, "an output must not alias an input"),
+    (dict(y=at(4)), 2, "an output must not alias an input"),
+    (dict(y=at(6)), 2, "two outputs must not alias"),
+    (dict(z=at(4), zs=64), 2, "sum must not alias z"),
+])
+def test_add_norm_fwd_refusals(lib, over, status, needle):
+    refused(lib, add_norm(lib, False, over), status, needle)
+
+
+@pytest.mark.parametrize("over,status,needle", ROWS + [
+    (dict(s=None), 1, "sum is NULL"),
+    (dict(gy=None), 1, "grad_y is NULL"),
+    (dict(ds=None), 1, "dsum is NULL"),
+    (dict(W=8193, ss=8193, gys=8193, gss=8193, dss=8193), 4, "W=8193 above 8192"),
+    (dict(dz=at(20), dzs=64), 1, "dz is given but z is NULL"),
+    (dict(ds=at(9), dss=72), 2, "needs its row stride"),
+    (dict(ds=at(8)), 2, "an output must not alias an input"),
+    (dict(ds=at(4)), 2, "an output must not alias an input"),
+    (dict(z=at(20), zs=64, dz=at(9), dzs=64), 2, "an output must not alias an input"),
+    (dict(z=at(20), zs=64, dz=at(9), dzs=64, ds=at(9)), 2, "must not alias"),
+    (dict(dw=FAKE + 2), 4, "dweight"),
+    (dict(ws=None), 5, "smaller than the required"),
+    (dict(wsb=16), 5, "workspace_bytes=16"),
+    (dict(ws=MIS), 4, "workspace="),
+])
+def test_add_norm_bwd_refusals(lib, over, status, needle):
+    refused(lib, add_norm(lib, True, over), status, needle)
+
+
+PROJ = dict(M=10, N=200, K=272, dtype=1, a=at(1), as_=272, sa=at(2), sas=3, w=at(3), ws=288, sw=at(4), sws=3, y=at(5), ys=200)
+
+
+def proj(lib, over):
+    a = {**PROJ, **over}
+    return lib.ssd_proj_fp8_fwd(*(a[n] for n in ("M", "N", "K", "dtype", "a", "as_", "sa", "sas", "w", "ws", "sw", "sws", "y", "ys")), None)
+
+
+@pytest.mark.parametrize("over,status,needle", [
+    (dict(dtype=2), 3, "dtype=2"),
+    (dict(M=-1), 2, "M=-1"),
+    (dict(N=0), 2, "N=0"),
+    (dict(K=0), 2, "K=0"),
+    (dict(K=264), 3, "K=264"),
+    (dict(M=INT_MAX, N=INT_MAX), 2, "are too many"),
+    (dict(a=None), 1, "a is NULL"),
+    (dict(w=None), 1, "w is NULL"),
+    (dict(sa=None), 1, "a_scale is NULL"),
+    (dict(sw=None), 1, "w_scale is NULL"),
+    (dict(y=None), 1, "y is NULL"),
+    (dict(as_=256), 2, "a row stride 256 is smaller"),
+    (dict(ws=256), 2, "w row stride 256 is smaller"),
+    (dict(sas=2), 2, "a_scale row stride 2 is smaller"),
+    (dict(sws=2), 2, "w_scale row stride 2 is smaller"),
+    (dict(ys=199), 2, "y row stride 199"),
+    (dict(as_=(1 << 22) + 16), 2, "above 4194304"),
+    (dict(sas=(1 << 22) + 1), 2, "above 4194304"),
+    (dict(ys=(1 << 22) + 1), 2, "above 4194304"),
+    (dict(as_=280), 4, "a row stride 280 is not a multiple"),
+    (dict(a=MIS), 4, "a="),
+    (dict(w=MIS), 4, "w="),
+    (dict(sa=FAKE + 2), 4, "a_scale"),
+    (dict(y=FAKE + 1), 4, "y="),
+    (dict(y=at(1)), 2, "must not alias"),
+])
+def test_proj_refusals(lib, over, status, needle):
+    refused(lib, proj(lib, over), status, needle)
+
+
+def test_nothing_to_do_needs_no_gpu(lib):
+    for kind in ("fwd", "step", "bwd"):
+        assert glr(lib, kind, dict(B=0, A=None, dA=None)) == 0
+    assert glr(lib, "fwd", dict(L=0)) == 0 and glr(lib, "fwd", dict(L=0, h0=at(20), hf=at(20))) == 0
+    assert add_norm(lib, False, dict(R=0)) == 0 and add_norm(lib, True, dict(R=0, dw=None)) == 0
+    assert proj(lib, dict(M=0)) == 0 and proj(lib, dict(M=0, a=None, sa=None, y=None)) == 0
+
+
+def test_workspace_sizes(lib):
+    for size in (lib.ssd_glr_scan_workspace_size, lib.ssd_glr_scan_bwd_workspace_size):
+        for none in ((0, 10, 8, 1), (2, 0, 8, 1), (2, 10, 0, 1), (-1, 10, 8, 1), (2, (1 << 30) + 1, 8, 1), (INT_MAX, 10, 8, 1),
+                     (1 << 20, 1 << 20, 130, 1)):
+            assert size(*none) == 0, none
+        assert size(2, 9000, 200, 1) % 16 == 0 and size(3, 9000, 7, 0) % 16 == 0
+    # short rows need none; a chain's pairs are 8 bytes for every tile (128 tokens in bf16, 64 in fp32) and channel
+    assert lib.ssd_glr_scan_workspace_size(4, 100, 64, 0) == 0 and lib.ssd_glr_scan_workspace_size(4, 256, 64, 1) == 0
+    assert lib.ssd_glr_scan_workspace_size(4, 1280, 64, 1) >= 4 * 10 * 64 * 8
+    assert lib.ssd_glr_scan_workspace_size(4, 1280, 64, 0) >= 4 * 20 * 64 * 8
+    # backward: the states that enter the chunks, three sums of each, its own chain and the forward's
+    assert lib.ssd_glr_scan_bwd_workspace_size(4, 1280, 64, 1) >= 4 * 20 * 64 * (4 + 12 + 8) + 4 * 10 * 64 * 8
+
+
+class TestBinding:
+    """The torch binding refuses tensors that the library could not read, naming them (no GPU: every call fails before)."""
+
+    def test_host_tensors(self):
+        import selective_state_space_14_amd as ssd
+        x, A, q = torch.zeros(2, 10, 64), torch.zeros(64), torch.zeros(4, 64).to(torch.float8_e4m3fn)
+        for call, name in ((lambda: ssd.ssd_glr_scan_fwd(x, x, x, A), "x"), (lambda: ssd.ssd_glr_scan_bwd(x, x, x, A, x), "x"),
+                           (lambda: ssd.ssd_glr_step(x[0], x[0], x[0], A, x[0]), "x"), (lambda: ssd.ssd_add_norm_fwd(x, x), "x"),
+                           (lambda: ssd.ssd_add_norm_bwd(x, x, x), "sum"), (lambda: ssd.ssd_proj_fp8_fwd(q, x, q, x), "a")):
+            with pytest.raises((ValueError, TypeError), match=name):
+                call()
+
+    def test_shapes_and_types(self):
+        import selective_state_space_14_amd as ssd
+        from tests.test_binding_streams import OnGpu
+        gpu = lambda *s, t=torch.float32: torch.zeros(*s).to(t).as_subclass(OnGpu)  # noqa: E731
+        bf, e4 = torch.bfloat16, torch.float8_e4m3fn
+        x, A = gpu(2, 10, 6, t=bf), gpu(6)
+        for call, name in (
+                (lambda: ssd.ssd_glr_scan_fwd(x, gpu(2, 10, 6), x, A), "r: expected torch.bfloat16"),
+                (lambda: ssd.ssd_glr_scan_fwd(x, x, gpu(2, 10, 5, t=bf), A), "i: expected shape"),
+                (lambda: ssd.ssd_glr_scan_fwd(x, x, x, gpu(5)), "A: expected a contiguous tensor of shape"),
+                (lambda: ssd.ssd_glr_scan_fwd(x, x, x, A, lengths=gpu(2, t=torch.int64), y=x), "lengths: expected torch.int32"),
+                (lambda: ssd.ssd_glr_scan_fwd(x, x, x, A, chunk_states=gpu(2, 2, 6), y=x), "chunk_states: expected"),
+                (lambda: ssd.ssd_glr_scan_fwd(gpu(2, 10, 6, t=torch.float16), x, x, A), "float16"),
+                (lambda: ssd.ssd_glr_step(x[:, 0], x[:, 0], x[:, 0], A, gpu(2, 6, t=bf), y=x[:, 0]), "state: expected torch.float32"),
+                (lambda: ssd.ssd_add_norm_fwd(x, gpu(2, 10, 5), y=x, sum=x), "residual: expected shape"),
+                (lambda: ssd.ssd_add_norm_fwd(x, x, gpu(5), y=x, sum=x), "weight: expected"),
+                (lambda: ssd.ssd_add_norm_fwd(x, x, y=x, sum=x, z=gpu(2, 10, 6)), "z: expected torch.bfloat16"),
+                (lambda: ssd.ssd_proj_fp8_fwd(gpu(4, 32, t=e4), gpu(4, 1), gpu(8, 32, t=bf), gpu(1, 1), y=gpu(4, 8)), "w: expected torch.float8_e4m3fn"),
+                (lambda: ssd.ssd_proj_fp8_fwd(gpu(4, 32, t=e4), gpu(4, 2), gpu(8, 32, t=e4), gpu(1, 1), y=gpu(4, 8)), "a_scale: expected shape"),
+                (lambda: ssd.ssd_proj_fp8_fwd(gpu(4, 32, t=e4), gpu(4, 1), gpu(8, 48, t=e4), gpu(1, 1), y=gpu(4, 8)), "w: expected shape")):
+            with pytest.raises((ValueError, TypeError), match=name):
+                call()
+
+    def test_streams_of_another_device(self, monkeypatch):
+        import selective_state_space_14_amd as ssd
+        from tests.test_binding_streams import OnGpu, Stream
+        x = torch.zeros(1, 1, 64).as_subclass(OnGpu)
+        for call in (lambda **kw: ssd.ssd_glr_scan_fwd(x, x, x, x, **kw), lambda **kw: ssd.ssd_glr_step(x, x, x, x, x, **kw),
+                     lambda **kw: ssd.ssd_glr_scan_bwd(x, x, x, x, x, **kw), lambda **kw: ssd.ssd_add_norm_fwd(x, **kw),
+                     lambda **kw: ssd.ssd_add_norm_bwd(x, x, **kw), lambda **kw: ssd.ssd_proj_fp8_fwd(x, x, x, x, **kw)):
+            with pytest.raises(ValueError, match="stream: on cuda:1, expected cuda:0"):
+                call(stream=Stream(1))
