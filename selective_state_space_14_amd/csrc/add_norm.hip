@@ -13,8 +13,8 @@
 #include <hip/hip_runtime.h>
 #include <algorithm>
 
+#include "layer_launch.hpp"
 #include "norm_device.hpp"
-#include "ssd_launch.hpp"
 
 namespace ssd {
 namespace {

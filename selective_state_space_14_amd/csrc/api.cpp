@@ -8,7 +8,7 @@
 #include <string.h>
 
 #include "../../include/ssd.h"
-#include "ssd_launch.hpp"
+#include "layer_launch.hpp"
 
 namespace {
 
@@ -1604,7 +1604,7 @@ int ssd_add_norm_bwd(int64_t R, int W, int sum_dtype, int dtype, int rms, float 
     const char* fn = "ssd_add_norm_bwd";
     const int dtypes[] = {sum_dtype, dtype};
     TRY(check_norm_dims(fn, R, W, rms, eps, dtypes, 2));
-    ssd::NormArgs a{};
+    ssd::AddNormBwdArgs a{};
     a.R = R; a.groups = 1; a.W = W; a.x_dtype = sum_dtype; a.dtype = dtype; a.rms = rms; a.eps = eps;
     a.x = sum; a.x_stride = sum_row_stride;
     a.w = weight; a.b = bias;
@@ -1646,7 +1646,7 @@ int ssd_add_norm_bwd(int64_t R, int W, int sum_dtype, int dtype, int rms, float 
         TRY(check_workspace(fn, workspace, workspace_bytes, ssd_norm_bwd_workspace_size(R, 1, W)));
         a.part = static_cast<float*>(workspace);
     }
-    return hip_status(fn, ssd::launch_norm(a, s));
+    return hip_status(fn, ssd::launch_add_norm_bwd(a, s));
 }
 
 // ---- the 8-bit projection

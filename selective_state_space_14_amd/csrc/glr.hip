@@ -24,8 +24,8 @@
 // ordered by it.  What is composed, and in which order, does not depend on the timing: results are deterministic.
 #include <algorithm>
 
+#include "layer_launch.hpp"
 #include "ssd_device.hpp"
-#include "ssd_launch.hpp"
 
 namespace ssd {
 namespace {

@@ -31,8 +31,10 @@
 #include <hip/hip_runtime.h>
 #include <algorithm>
 
+#include <type_traits>
+
+#include "layer_launch.hpp"
 #include "norm_device.hpp"
-#include "ssd_launch.hpp"
 
 namespace ssd {
 namespace {
@@ -95,7 +97,8 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_k
 
 // ADD: dx also takes gs, the gradient that reaches the norm's input past it (a residual stream's)
 template <typename X, typename T, int TPR, int NV, int VEC, bool ADD>
-__global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_kernel(NormArgs a) {
+__global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_kernel(
+    std::conditional_t<ADD, AddNormBwdArgs, NormArgs> a) {
     using SH = Shape<TPR, NV, VEC>;
     __shared__ float red[2][2][16];
     int turn = 0;
@@ -121,7 +124,12 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
     const X* xp = static_cast<const X*>(a.x);
     const T* zp = static_cast<const T*>(a.z);
     const T* gp = static_cast<const T*>(a.gy);
-    const X* sp = static_cast<const X*>(a.gs);
+    const X* sp = nullptr;
+    int64_t sp_stride = 0;
+    if constexpr (ADD) {
+        sp = static_cast<const X*>(a.gs);
+        sp_stride = a.gs_stride;
+    }
     X* dxp = static_cast<X*>(a.dx);
     T* dzp = static_cast<T*>(a.dz);
     const float inv = 1.0f / (float)a.W;
@@ -141,7 +149,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             ng[j].clear();
             if constexpr (kAddAhead) ns[j].clear();
             if (live && on[j]) {
-                if constexpr (kAddAhead) ns[j].load(sp + r * a.gs_stride + col + c);
+                if constexpr (kAddAhead) ns[j].load(sp + r * sp_stride + col + c);
                 nx[j].load(xp + r * a.x_stride + col + c);
                 ng[j].load(gp + r * a.gy_stride + col + c);
                 if (zp) nz[j].load(zp + r * a.z_stride + col + c);
@@ -213,7 +221,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             if constexpr (ADD && !kAddAhead) {
                 float p[VEC];
                 if (live && on[j]) {
-                    ldv<VEC>(sp + r * a.gs_stride + col + c, p);
+                    ldv<VEC>(sp + r * sp_stride + col + c, p);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) d[e] += p[e];
                 }
@@ -304,12 +312,12 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((ssd_norm_fwd_kernel<X, T, TPR, NV, VEC>), dim3((unsigned)blocks), dim3(SH::threads), 0, stream, a);
     return hipGetLastError();
 }
-template <typename X, typename T, int TPR, int NV, int VEC>
-hipError_t launch_bwd(const NormArgs& a, hipStream_t stream) {
+template <typename X, typename T, int TPR, int NV, int VEC, typename Args>
+hipError_t launch_bwd(const Args& a, hipStream_t stream) {
     using SH = Shape<TPR, NV, VEC>;
     const int n = (int)std::min<int64_t>((a.R + SH::rows - 1) / SH::rows, kNormBwdGrid);
-    if (a.gs) hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC, true>), dim3(n), dim3(SH::threads), 0, stream, a);
-    else hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC, false>), dim3(n), dim3(SH::threads), 0, stream, a);
+    constexpr bool kAdd = std::is_same_v<Args, AddNormBwdArgs>;
+    hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC, kAdd>), dim3(n), dim3(SH::threads), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
     hipLaunchKernelGGL(ssd_norm_sum_kernel, dim3((2 * a.W + 31) / 32), dim3(1024), 0, stream, a.part, n, a.W, a.dw, a.db);
@@ -339,8 +347,8 @@ hipError_t launch_fwd_t(const NormArgs& a, hipStream_t s) {
     if (a.W <= 4096) return launch_fwd<X, T, 256, 16, 1>(a, s);
     return launch_fwd<X, T, 512, 16, 1>(a, s);
 }
-template <typename X, typename T>
-hipError_t launch_bwd_t(const NormArgs& a, hipStream_t s) {
+template <typename X, typename T, typename Args>
+hipError_t launch_bwd_t(const Args& a, hipStream_t s) {
     if (a.vec) {
         const int n = a.W / 8;
         if (n <= 8) return launch_bwd<X, T, 8, 1, 8>(a, s);
@@ -374,6 +382,12 @@ size_t norm_bwd_workspace_bytes(int64_t R, int W) {
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     if (a.x_dtype == 0) return a.dtype == 0 ? launch_norm_t<float, float>(a, s) : launch_norm_t<float, uint16_t>(a, s);
     return a.dtype == 0 ? launch_norm_t<uint16_t, float>(a, s) : launch_norm_t<uint16_t, uint16_t>(a, s);
+}
+
+hipError_t launch_add_norm_bwd(const AddNormBwdArgs& a, hipStream_t s) {
+    if (!a.gs) return launch_norm(a, s);
+    if (a.x_dtype == 0) return a.dtype == 0 ? launch_bwd_t<float, float>(a, s) : launch_bwd_t<float, uint16_t>(a, s);
+    return a.dtype == 0 ? launch_bwd_t<uint16_t, float>(a, s) : launch_bwd_t<uint16_t, uint16_t>(a, s);
 }
 
 }  // namespace ssd

@@ -18,8 +18,8 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "layer_launch.hpp"
 #include "ssd_device.hpp"
-#include "ssd_launch.hpp"
 
 namespace ssd {
 namespace {
