@@ -871,6 +871,11 @@ def ssd_norm_bwd(x, grad_y, weight=None, *, bias=None, z=None, rms=False, eps=1e
 
 
 # ---- the gated linear recurrence
+def _like(t, dtype):
+    """A contiguous output of t's shape: half the host's time of a shape spelt out, and small calls' time is the host's."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _glr_head(c, lead, T, D, x, r, i, A, r_bias, i_bias):
     """The arguments that the recurrence's calls share; lead: the dimensions before the channels, (B, L) or (B,)."""
     return [*c.rows(x, "x", T, lead + (D,)), *c.rows(r, "r", T, lead + (D,)), *c.rows(i, "i", T, lead + (D,)),
@@ -894,7 +899,7 @@ def ssd_glr_scan_fwd(x, r, i, A, *, r_bias=None, i_bias=None, doc_ids=None, leng
     B, L, D = x.shape
     head = _glr_head(c, (B, L), T, D, x, r, i, A, r_bias, i_bias)
     if y is None:
-        y = torch.empty((B, L, D), dtype=T, device=c.dev)
+        y = _like(x, T)
     yp, ys = c.rows(y, "y", T, (B, L, D))
     need = ssd_glr_scan_workspace_size(B, L, D, dtype)
     ws = _ws(workspace, need, c.dev) if need or workspace is not None else None
@@ -917,7 +922,7 @@ def ssd_glr_step(x, r, i, A, state, *, r_bias=None, i_bias=None, y=None):
     B, D = x.shape
     head = _glr_head(c, (B,), T, D, x, r, i, A, r_bias, i_bias)
     if y is None:
-        y = torch.empty((B, D), dtype=T, device=c.dev)
+        y = _like(x, T)
     yp, ys = c.rows(y, "y", T, (B, D))
     c.run(lib.ssd_glr_step, (B, D, dtype, *head, c.vec(state, "state", torch.float32, (B, D)), yp, ys))
     return y
@@ -940,15 +945,13 @@ def ssd_glr_scan_bwd(x, r, i, A, grad_y, *, r_bias=None, i_bias=None, doc_ids=No
     B, L, D = x.shape
     head = _glr_head(c, (B, L), T, D, x, r, i, A, r_bias, i_bias)
     gp, gs = c.rows(grad_y, "grad_y", T, (B, L, D))
-    f32, same = dict(dtype=torch.float32, device=c.dev), dict(dtype=T, device=c.dev)
-    g = {n: torch.empty(B, L, D, **same) for n in ("x", "r", "i")}
-    g["A"] = _params(B)(D, **f32)
-    if r_bias is not None:
-        g["r_bias"] = _params(B)(D, **f32)
-    if i_bias is not None:
-        g["i_bias"] = _params(B)(D, **f32)
+    f32 = torch.float32
+    g = {"x": _like(x, T), "r": _like(x, T), "i": _like(x, T)}
+    for n, v in (("A", A), ("r_bias", r_bias), ("i_bias", i_bias)):
+        if v is not None:
+            g[n] = _like(v, f32) if B else torch.zeros(D, dtype=f32, device=c.dev)
     if init_state is not None:
-        g["init_state"] = torch.empty(B, D, **f32)
+        g["init_state"] = _like(init_state, f32)
     ws = _ws(workspace, ssd_glr_scan_bwd_workspace_size(B, L, D, dtype), c.dev)
     out = lambda n: g[n].data_ptr() if n in g else None  # noqa: E731
     c.run(lib.ssd_glr_scan_bwd,
@@ -982,14 +985,14 @@ def ssd_add_norm_fwd(x, residual=None, weight=None, *, bias=None, z=None, rms=Fa
     shape, W = x.shape, x.shape[-1]
     T = y.dtype if y is not None else out_dtype or (x.dtype if z is None else z.dtype)
     if (want_y or y is not None) and y is None:
-        y = torch.empty(shape, dtype=T, device=c.dev)
+        y = _like(x, T)
     blocks = shape[:-1] + (-(-W // 128),)
     if want_q or q is not None or q_scale is not None:
-        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=c.dev) if q is None else q
-        q_scale = torch.empty(blocks, dtype=torch.float32, device=c.dev) if q_scale is None else q_scale
+        q = _like(x, torch.float8_e4m3fn) if q is None else q
+        q_scale = x.new_empty(blocks, dtype=torch.float32) if q_scale is None else q_scale
     RT = x.dtype if residual is None else residual.dtype
     if residual is not None and sum is None:
-        sum = torch.empty(shape, dtype=RT, device=c.dev)
+        sum = _like(x, RT)
     out = {n: t for n, t in (("sum", sum), ("y", y), ("q", q), ("scale", q_scale)) if t is not None}
     if x.numel() == 0:
         return out
@@ -1012,14 +1015,13 @@ def ssd_add_norm_bwd(sum, grad_y, grad_sum=None, weight=None, *, bias=None, z=No
     c = _Call(sum, "sum")
     shape, W, T = sum.shape, sum.shape[-1], grad_y.dtype
     R = _lead_rows(shape)
-    f32 = dict(dtype=torch.float32, device=c.dev)
-    g = {"sum": torch.empty(shape, dtype=sum.dtype, device=c.dev)}
+    g = {"sum": _like(sum, sum.dtype)}
     if weight is not None:
-        g["weight"] = torch.empty(W, **f32)
+        g["weight"] = _like(weight, torch.float32)
     if bias is not None:
-        g["bias"] = torch.empty(W, **f32)
+        g["bias"] = _like(bias, torch.float32)
     if z is not None:
-        g["z"] = torch.empty(shape, dtype=T, device=c.dev)
+        g["z"] = _like(sum, T)
     ws, nb = None, 0
     if weight is not None or bias is not None:
         ws = _ws(workspace, ssd_norm_bwd_workspace_size(R, 1, W), c.dev)
