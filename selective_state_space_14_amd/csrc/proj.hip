@@ -85,7 +85,8 @@ __device__ __forceinline__ void store4(uint16_t* p, int left, bool wide, f32x4 v
 // ------------------------------------------------------------ few rows: weights streamed from HBM into registers
 // A workgroup owns 16 columns of y and 16 MT rows; its eight waves take every eighth block of K and their sums meet in
 // LDS, in order.  The weights' bytes are the work: nothing is staged, a lane's 32 bytes of a block are two loads, and U
-// blocks are on their way at once.
+// blocks are on their way at once.  M = 4, N = 5152, K = 2048 to bf16: 5.7 us (10.6 MB; a copy of as much 2.0 us and a launch
+// 2 to 3).
 constexpr int kSkinnyWaves = 8;
 template <typename T, int MT, int U>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void ssd_proj_rows_kernel(ProjArgs p) {
@@ -182,6 +183,10 @@ __device__ __forceinline__ int piece_of(int g, int h) { return (g & 1) | h << 1 
 // A workgroup of NWN x NWM waves owns a tile of y; a wave's part of it is WN x WM products of 16 x 16.  The two operands'
 // block of 128 bytes a row goes through one of two LDS stages while the other is computed, and so do the activations'
 // scales of 16 blocks at a time: read by the lanes that need them, they would be as many requests as the operands.
+// M = 16384, N = 4096, K = 8192 to bf16: 471 to 490 us, 2.33 to 2.24 PFLOP/s; a library's 8-bit product without block scales
+// takes 412 us there.  Matrix instructions alone would take 300 us at the clock they leave, with their LDS reads and barriers 405;
+// copies and scales add the rest, and the scales' fmas nothing.  A row of products is scaled while the next one's run (one
+// after the other: 666 us).
 template <int BN, int BM> constexpr int kTileLds = 2 * (BN + BM) * 128 + 2 * BM * 16 * 4;
 template <typename T, int WN, int WM, int NWN, int NWM>
 __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjArgs p) {
