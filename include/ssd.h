@@ -777,7 +777,8 @@ size_t ssd_norm_bwd_workspace_size(int64_t R, int groups, int W);
  *               state stops there, and inputs behind it are not used
  *   state   f32 [B][D], 16-byte aligned bases
  *   y       T   [B][L][D], rounded once; must not overlap the inputs
- * Any D >= 1 with B * D < 2^31.  Gates, decays and states are fp32; decays
+ * Any D >= 1 with B * D < 2^31 and, but for the step,
+ * B * ceil(L / 64) * ceil(D / 128) < 2^23.  Gates, decays and states are fp32; decays
  * near 1 and 1 - a^2 are taken from the series of 1 - a, to a few 2^-24.
  */
 

@@ -1309,16 +1309,18 @@ int ssd_norm_bwd(int64_t R, int groups, int W, int x_dtype, int dtype, int rms, 
 }
 
 // ---- the gated linear recurrence
-// the grids: a workgroup for every chunk of 64 tokens and 128 channels, a thread for every state
-static bool glr_units_fit(int B, int L, int D) {
-    return (long long)B * D <= 0x7fffffffLL && (long long)B * (((long long)D + 127) / 128) <= 0x7fffffffLL / std::max(1LL, ((long long)L + 63) / 64);
+// the grids, whose threads a launch counts in 32 bits: 512 for every chunk of 64 tokens and 128 channels (no chunk: one
+// token), one for every state
+static bool glr_units_fit(int B, int L, int D, bool chunks = true) {
+    return (long long)B * D <= 0x7fffffffLL &&
+           (!chunks || (long long)B * (((long long)D + 127) / 128) <= (0xffffffffLL / 512) / std::max(1LL, ((long long)L + 63) / 64));
 }
 
 static bool glr_has_work(int B, int L, int D) { return B > 0 && L > 0 && L <= kMaxL && D > 0 && glr_units_fit(B, L, D); }
 
 // `rows`: the activations of a call, the first three its inputs
 struct GlrRow { const char* name; const void* p; int64_t stride; };
-static int check_glr(const char* fn, ssd::GlrArgs& a, const GlrRow* rows, int n, bool work) {
+static int check_glr(const char* fn, ssd::GlrArgs& a, const GlrRow* rows, int n, bool work, bool chunks = true) {
     if (a.dtype != SSD_F32 && a.dtype != SSD_BF16)
         return fail(SSD_ERR_UNSUPPORTED, "%s: dtype=%d is not supported (only SSD_F32=0 and SSD_BF16=1; "
                     "fp16, fp64 and other types are refused, not converted)", fn, a.dtype);
@@ -1326,7 +1328,7 @@ static int check_glr(const char* fn, ssd::GlrArgs& a, const GlrRow* rows, int n,
     if (a.L < 0) return fail(SSD_ERR_BAD_SHAPE, "%s: L=%d must be >= 0", fn, a.L);
     if (a.L > kMaxL) return fail(SSD_ERR_BAD_SHAPE, "%s: L=%d is above the %d tokens a row may hold", fn, a.L, kMaxL);
     if (a.D <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: D=%d must be > 0", fn, a.D);
-    if (!glr_units_fit(a.B, a.L, a.D))
+    if (!glr_units_fit(a.B, a.L, a.D, chunks))
         return fail(SSD_ERR_BAD_SHAPE, "%s: B=%d rows of L=%d tokens and D=%d channels are too many", fn, a.B, a.L, a.D);
     const int es = esize(a.dtype);
     a.pair = a.D % 2 == 0;
@@ -1419,9 +1421,11 @@ int ssd_glr_scan_fwd(int B, int L, int D, int dtype,
             return hip_status(fn, ssd::launch_glr_copy(init_state, final_state, (int64_t)B * D, s));
         return ok();
     }
-    const void* outs[] = {y, chunk_states};
-    const void* ins[] = {x, r, i, A, r_bias, i_bias, init_state, final_state};
-    TRY(check_apart(fn, outs, 2, ins, 8));
+    // final_state may be init_state: that is read before the row's last tile is entered
+    const void* outs[] = {y, chunk_states, final_state};
+    const void* ins[] = {x, r, i, A, r_bias, i_bias, doc_ids, lengths, init_state};
+    TRY(check_apart(fn, outs, 3, ins, 8));
+    TRY(check_apart(fn, outs, 2, ins + 8, 1));
     TRY(check_workspace(fn, workspace, workspace_bytes, ssd_glr_scan_workspace_size(B, L, D, dtype)));
     return hip_status(fn, ssd::launch_glr_fwd(a, workspace, s));
 }
@@ -1438,7 +1442,7 @@ int ssd_glr_step(int B, int D, int dtype,
     a.y = y; a.y_stride = y_row_stride;
     const bool work = B > 0;
     const GlrRow rows[] = {{"x", x, x_row_stride}, {"r", r, r_row_stride}, {"i", i, i_row_stride}, {"y", y, y_row_stride}};
-    TRY(check_glr(fn, a, rows, 4, work));
+    TRY(check_glr(fn, a, rows, 4, work, false));
     TRY(check_ptr(fn, "state", state, work, true));
     if (!work) return ok();
     const void* outs[] = {y, state};
@@ -1662,8 +1666,8 @@ int ssd_proj_fp8_fwd(int M, int N, int K, int dtype,
     if (N <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: N=%d must be > 0", fn, N);
     if (K <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: K=%d must be > 0", fn, K);
     if (K % 16 != 0) return fail(SSD_ERR_UNSUPPORTED, "%s: K=%d is not supported (must be a multiple of 16)", fn, K);
-    // the grids: a workgroup for every 128 x 128 of y
-    if (((int64_t)M + 127) / 128 * (((int64_t)N + 127) / 128) > 0x7fffffffLL)
+    // the grid, whose threads a launch counts in 32 bits: 256 for every 128 x 128 of y
+    if (((int64_t)M + 127) / 128 * (((int64_t)N + 127) / 128) > 0xffffffffLL / 256)
         return fail(SSD_ERR_BAD_SHAPE, "%s: M=%d rows of N=%d columns are too many", fn, M, N);
     const int blocks = (K + 127) / 128, es = esize(dtype);
     const bool work = M > 0;

@@ -408,7 +408,9 @@ __global__ __launch_bounds__(kThreads, (CHAIN && (PAIR || sizeof(T) == 4) ? 4 : 
         const int turn = CHAIN ? 0 : p.c & 1;        // a walk's next tile leaves these alone
         sA[turn][wave][l] = make_float2(s.A[0], s.A[1]);
         sH[turn][wave][l] = make_float2(s.H[0], s.H[1]);
-        __syncthreads();                             // init_state has been read: final_state may be it
+        // init_state has been read by all, for final_state may be it: h itself, not a load of it, passes the barrier
+        asm volatile("" : "+v"(h[0]), "+v"(h[1]));
+        __syncthreads();
         if constexpr (CHAIN) {
             if (wave == kWaves - 1) {                // the first tile starts from the row's own state: a cut
                 float2 A = p.c == 0 ? make_float2(__uint_as_float(kCut), __uint_as_float(kCut)) : make_float2(1.0f, 1.0f);

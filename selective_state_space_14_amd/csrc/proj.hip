@@ -376,14 +376,16 @@ hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
     double best = 0.0;
     int mt = 0;
     for (int k : {1, 2}) {
-        const double wgs = n16 * over(p.M, 16 * k), t = 3.0 + blocks * piece * (1 + k) * std::max(1.0, wgs / 256);
+        const double wgs = n16 * over(p.M, 16 * k);
+        if (wgs * 64 * kSkinnyWaves > 0xffffffffu) continue;      // a launch counts its threads in 32 bits
+        const double t = 3.0 + blocks * piece * (1 + k) * std::max(1.0, wgs / 256);
         if (!mt || t < best) {
             mt = k;
             best = t;
         }
     }
     const double one = sizeof(T) == 2 ? 0.45 : 1.0;
-    if (best < 5.0 + blocks * (one + 0.75 * std::max(0.0, small / 256 - 1.0))) return mt == 1 ? rows<T, 1, 4>(p, s) : rows<T, 2, 2>(p, s);
+    if (mt && best < 5.0 + blocks * (one + 0.75 * std::max(0.0, small / 256 - 1.0))) return mt == 1 ? rows<T, 1, 4>(p, s) : rows<T, 2, 2>(p, s);
     if constexpr (sizeof(T) == 2) {                  // widened operands take too many registers for the larger tile
         if (over(over(p.N, 256) * over(p.M, 256), 256) * 1.85 < 0.7 * small / 256) return tiles<T, 8, 4, 2, 4>(p, s);
     }

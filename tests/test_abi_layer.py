@@ -67,6 +67,8 @@ SCAN = [
     (dict(L=-1), 2, "L=-1"),
     (dict(L=(1 << 30) + 1), 2, "L=1073741825 is above"),
     (dict(B=1 << 20, L=1 << 20), 2, "are too many"),
+    (dict(B=1, L=1 << 30, D=1, A=at(30)), 2, "are too many"),
+    (dict(B=1 << 23, L=64, D=1), 2, "are too many"),
     (dict(doc=FAKE + 1), 4, "doc_ids"),
     (dict(len=FAKE + 2), 4, "lengths"),
     (dict(h0=MIS), 4, "init_state"),
@@ -86,6 +88,9 @@ SCAN = [
     (dict(cs=at(20), hf=at(20)), 2, "must not alias"),
     (dict(cs=at(20), h0=at(20)), 2, "must not alias"),
     (dict(cs=at(6)), 2, "two outputs must not alias"),
+    (dict(hf=at(5)), 2, "an output must not alias an input"),
+    (dict(len=at(20), hf=at(20)), 2, "an output must not alias an input"),
+    (dict(h0=at(20), hf=at(20), ws=None), 5, "smaller than the required"),        # in place: nothing else is wrong
 ])
 def test_glr_scan_refusals(lib, over, status, needle):
     refused(lib, glr(lib, "fwd", over), status, needle)
@@ -215,6 +220,7 @@ def proj(lib, over):
     (dict(K=0), 2, "K=0"),
     (dict(K=264), 3, "K=264"),
     (dict(M=INT_MAX, N=INT_MAX), 2, "are too many"),
+    (dict(M=INT_MAX, N=16, K=16), 2, "are too many"),
     (dict(a=None), 1, "a is NULL"),
     (dict(w=None), 1, "w is NULL"),
     (dict(sa=None), 1, "a_scale is NULL"),

@@ -228,7 +228,7 @@ def test_training(gpu_lib):
     h = Recurrence.apply(ssd, v, rr, i, dev[4], dev[5], dev[6], docs.to(DEV))
     mine = h @ dev[7] + s
     got = torch.autograd.grad((mine * gout.to(DEV)).sum(), dev)
-    close = lambda a, b: float((a.double().cpu() - b).norm() / b.norm())  # noqa: E731
+    close = lambda a, b: float((a.detach().double().cpu() - b).norm() / b.norm())  # noqa: E731
     assert close(mine, out.detach()) < 2.0 ** -8
     for k, (a, b) in enumerate(zip(got, want)):
         assert close(a, b) < 2.0 ** -8, (k, close(a, b))
