@@ -264,7 +264,7 @@ struct Stretch {
                 const float s = w.r_gate(r[t].get(j), j);
                 float om;
                 decay(s * w.zA[j], a[t][j], om);
-                v[t][j] = __builtin_amdgcn_sqrtf(om * (1.0f + a[t][j])) * w.i_gate(i[t].get(j), j) * x[t].get(j);
+                v[t][j] = __builtin_amdgcn_sqrtf(fmaf(om, a[t][j], om)) * w.i_gate(i[t].get(j), j) * x[t].get(j);
                 // here and now: the compiler would put part of every token off, and hold what that part needs
                 asm volatile("" : "+v"(a[t][j]), "+v"(v[t][j]));
             }
@@ -492,7 +492,7 @@ struct Back {
                 s[t][j] = w.r_gate(r[t].get(j), j);
                 gi[t][j] = w.i_gate(i[t].get(j), j);
                 decay(s[t][j] * w.zA[j], a[t][j], om);
-                v[t][j] = __builtin_amdgcn_sqrtf(om * (1.0f + a[t][j])) * gi[t][j] * x[t].get(j);
+                v[t][j] = __builtin_amdgcn_sqrtf(fmaf(om, a[t][j], om)) * gi[t][j] * x[t].get(j);
                 // here and now: the compiler would put part of every token off, and hold what that part needs
                 asm volatile("" : "+v"(a[t][j]), "+v"(v[t][j]), "+v"(s[t][j]), "+v"(gi[t][j]));
             }
@@ -558,14 +558,15 @@ struct Back {
                 const float all = gy[t].get(j) + nu[j], lam = bit(k.lives, t) ? all : 0.0f;
                 nu[j] = bit(k.starts, t) ? 0.0f : a[t][j] * all;
                 const float z = s[t][j] * (A2[j] * -kLog2e), om = z < kNear ? one_minus(z) : 1.0f - a[t][j];
-                const float m2 = om * (1.0f + a[t][j]);
-                // 1 / m, 0 where m is: no branch around it
-                const float inv = __uint_as_float(__float_as_uint(__builtin_amdgcn_rsqf(m2)) & (m2 > 0.0f ? ~0u : 0u));
+                const float m2 = fmaf(om, a[t][j], om);
+                float inv = __builtin_amdgcn_rsqf(m2);
+                asm volatile("" : "+v"(inv));            // no branch around it
+                inv = m2 > 0.0f ? inv : 0.0f;            // 1 / m, 0 where m is
                 const float gx = gi[t][j] * x[t].get(j), lm = lam * (m2 * inv);
                 dx[j] = lm * gi[t][j];
-                di[j] = lm * gx * (1.0f - gi[t][j]);
+                di[j] = lm * fmaf(-gx, gi[t][j], gx);
                 const float ds = lam * (v[t][j] - gx * (a[t][j] * a[t][j]) * inv) * s[t][j];
-                dr[j] = A2[j] * ds * (1.0f - s[t][j]);
+                dr[j] = ds * fmaf(-A2[j], s[t][j], A2[j]);
                 sum[0][j] += ds;
                 sum[1][j] += dr[j];
                 sum[2][j] += di[j];
@@ -787,7 +788,7 @@ __global__ __launch_bounds__(256) void ssd_glr_step_kernel(GlrArgs g) {
     for (int j = 0; j < V; ++j) {
         float d, om;
         decay(sigmoid_f(r[j] + rb[j]) * (A[j] * -kLog2e), d, om);
-        h[j] = fmaf(d, h[j], __builtin_amdgcn_sqrtf(om * (1.0f + d)) * sigmoid_f(i[j] + ib[j]) * x[j]);
+        h[j] = fmaf(d, h[j], __builtin_amdgcn_sqrtf(fmaf(om, d, om)) * sigmoid_f(i[j] + ib[j]) * x[j]);
     }
     step_st<float, V>(state, h);
     step_st<T, V>(static_cast<T*>(g.y) + b * g.y_stride + c, h);
