@@ -557,10 +557,12 @@ struct Back {
             for (int j = 0; j < 2; ++j) {
                 const float all = gy[t].get(j) + nu[j], lam = bit(k.lives, t) ? all : 0.0f;
                 nu[j] = bit(k.starts, t) ? 0.0f : a[t][j] * all;
-                const float z = s[t][j] * (A2[j] * -kLog2e), om = z < kNear ? one_minus(z) : 1.0f - a[t][j];
-                const float m2 = fmaf(om, a[t][j], om);
+                const float z = s[t][j] * (A2[j] * -kLog2e);
+                float q = one_minus(z);
+                asm volatile("" : "+v"(q));              // no branch around it, nor below
+                const float om = z < kNear ? q : 1.0f - a[t][j], m2 = fmaf(om, a[t][j], om);
                 float inv = __builtin_amdgcn_rsqf(m2);
-                asm volatile("" : "+v"(inv));            // no branch around it
+                asm volatile("" : "+v"(inv));
                 inv = m2 > 0.0f ? inv : 0.0f;            // 1 / m, 0 where m is
                 const float gx = gi[t][j] * x[t].get(j), lm = lam * (m2 * inv);
                 dx[j] = lm * gi[t][j];
