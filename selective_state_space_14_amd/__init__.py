@@ -645,8 +645,15 @@ class _Call:
         """(pointer, row stride) of a tensor of `shape`, its rows a uniform number of elements apart; dtype None: any."""
         if t is None:
             return None, 0
-        if t.shape == shape and t.device == self.dev and (t.dtype is dtype or dtype is None) and t.is_contiguous():
-            return t.data_ptr(), shape[-1]
+        if t.shape == shape and t.device == self.dev and (t.dtype is dtype or dtype is None):
+            if t.is_contiguous():
+                return t.data_ptr(), shape[-1]
+            st = t.stride()
+            if st[-1] == 1:                           # columns of wider rows
+                if len(st) == 2 and shape[0] > 1:
+                    return t.data_ptr(), st[0]
+                if len(st) == 3 and shape[1] > 1 and (shape[0] == 1 or st[0] == shape[1] * st[1]):
+                    return t.data_ptr(), st[1]
         p = self.ptr(t, name, dtype)
         if t.shape != shape:
             raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
@@ -876,6 +883,13 @@ def _like(t, dtype):
     return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
+def _new(dev, lead, width, dtype):
+    """A contiguous output of another width; two dimensions with their strides, which is the faster form too."""
+    if len(lead) == 1:
+        return torch.empty_strided((lead[0], width), (width, 1), dtype=dtype, device=dev)
+    return torch.empty(lead + (width,), dtype=dtype, device=dev)
+
+
 def _glr_head(c, lead, T, D, x, r, i, A, r_bias, i_bias):
     """The arguments that the recurrence's calls share; lead: the dimensions before the channels, (B, L) or (B,)."""
     return [*c.rows(x, "x", T, lead + (D,)), *c.rows(r, "r", T, lead + (D,)), *c.rows(i, "i", T, lead + (D,)),
@@ -989,7 +1003,7 @@ def ssd_add_norm_fwd(x, residual=None, weight=None, *, bias=None, z=None, rms=Fa
     blocks = shape[:-1] + (-(-W // 128),)
     if want_q or q is not None or q_scale is not None:
         q = _like(x, torch.float8_e4m3fn) if q is None else q
-        q_scale = x.new_empty(blocks, dtype=torch.float32) if q_scale is None else q_scale
+        q_scale = _new(c.dev, shape[:-1], blocks[-1], torch.float32) if q_scale is None else q_scale
     RT = x.dtype if residual is None else residual.dtype
     if residual is not None and sum is None:
         sum = _like(x, RT)
@@ -1048,7 +1062,7 @@ def ssd_proj_fp8_fwd(a, a_scale, w, w_scale, *, out_dtype=torch.bfloat16, y=None
     blocks = -(-K // 128)
     T = out_dtype if y is None else y.dtype
     if y is None:
-        y = torch.empty(lead + (N,), dtype=T, device=c.dev)
+        y = _new(c.dev, lead, N, T)
     c.run(lib.ssd_proj_fp8_fwd,
           (_lead_rows(a.shape), N, K, _dtype_code(y, "y"), *c.rows(a, "a", torch.float8_e4m3fn, a.shape),
            *c.rows(a_scale, "a_scale", torch.float32, lead + (blocks,)), *c.rows(w, "w", torch.float8_e4m3fn, (N, K)),
