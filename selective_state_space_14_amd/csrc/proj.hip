@@ -83,11 +83,12 @@ __device__ __forceinline__ void store4(uint16_t* p, int left, bool wide, f32x4 v
 }
 
 // ------------------------------------------------------------ few rows: weights streamed from HBM into registers
-// A workgroup owns 16 columns of y and 16 MT rows; its eight waves take every eighth block of K and their sums meet in
+// A workgroup owns 16 columns of y and 16 MT rows; its four waves take every fourth block of K and their sums meet in
 // LDS, in order.  The weights' bytes are the work: nothing is staged, a lane's 32 bytes of a block are two loads, and U
 // blocks are on their way at once.  M = 4, N = 5152, K = 2048 to bf16: 5.7 us (10.6 MB; a copy of as much 2.0 us and a launch
-// 2 to 3).
-constexpr int kSkinnyWaves = 8;
+// 2 to 3).  Eight waves: the same there, M = 777, N = 1000, K = 1040 to fp32 11.6 us in place of 10.4, M = 16, N = 1024, K = 8192 11.4
+// in place of 11.7.
+constexpr int kSkinnyWaves = 4;
 template <typename T, int MT, int U>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void ssd_proj_rows_kernel(ProjArgs p) {
     __shared__ f32x4 part[kSkinnyWaves][MT][64];
@@ -366,7 +367,7 @@ hipError_t tiles(const ProjArgs& p, hipStream_t s) {
 //  - tiles of 128 x 128: 0.45 us a block (1 us with widened operands) for one a CU, 0.75 for every further one; 5 us.
 //  - tiles of 256 x 256, one a CU: 1.85 us a block, against 0.7 a 128 x 128 tile when there are many.
 // Measured, bf16, N = 5152, K = 2048: M = 32 rows 9.4, tiles 11.7; M = 64 rows 12.9, tiles 12.2; M = 256 rows 41, tiles 13.3;
-// N = 1024, K = 8192, M = 64: rows 11 (MT = 1; 16 with 2), tiles 37.  M = 777, N = 1000, K = 1040, fp32: rows 10.9, tiles
+// N = 1024, K = 8192, M = 64: rows 11 (MT = 1; 16 with 2), tiles 37.  M = 777, N = 1000, K = 1040, fp32: rows 10.4, tiles
 // 15.7.  M = 4096, N = 5152, K = 2048: tiles of 128 60, of 256 64; M = N = K = 4096: 95 and 66.
 template <typename T>
 hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
