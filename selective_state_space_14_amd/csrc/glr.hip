@@ -27,10 +27,10 @@
 // the gates' arithmetic (six transcendentals and some 27 other instructions an element and pass) and a tile's latencies (its
 // place, its loads, the tiles before it) take about as long as the bytes, and two workgroups a CU overlap them.
 // Measured (B x L x D):
-//   forward, bf16, 1 x 65536 x 2048: 237 us, 4.5 TB/s (209 us with the arithmetic left out, 220 with operands from the
+//   forward, bf16, 1 x 65536 x 2048: 236 us, 4.6 TB/s (209 us with the arithmetic left out, 220 with operands from the
 //   cache); tiles of 64 tokens in place of 128: 318 us; tiles, their composition and the scan as three launches: 603 us
-//   forward, fp32, 2 x 16384 x 2048: 216 us, 5.0 TB/s
-//   forward and backward, bf16, 4 x 8192 x 2048, packed documents: 124 and 240 us, 374 with the chains' memory and the sums
+//   forward, fp32, 2 x 16384 x 2048: 215 us, 5.0 TB/s
+//   forward and backward, bf16, 4 x 8192 x 2048, packed documents: 124 and 230 us, 367 with the chains' memory and the sums
 #include <algorithm>
 
 #include "layer_launch.hpp"
@@ -584,8 +584,8 @@ struct Back {
 
 // The chain runs from a row's last tile.  part: [tile of all rows][3][D], a tile's sums of dA, dr_bias and di_bias.
 // fp32 operands take the registers of one workgroup a CU; as many bytes are on their way then as with two in bf16.
-// 8 tokens of a wave, so that a tile starts at a state that the forward kept: 4 x 8192 x 2048 in bf16 takes 240 us (1.0 GB with
-// the kept states and the partial sums, 4.3 TB/s).  Decays are formed again where the gradients need them: held, they would
+// 8 tokens of a wave, so that a tile starts at a state that the forward kept: 4 x 8192 x 2048 in bf16 takes 230 us (1.0 GB with
+// the kept states and the partial sums, 4.4 TB/s).  Decays are formed again where the gradients need them: held, they would
 // spill.
 template <typename T, bool PAIR, bool CHAIN>
 __global__ __launch_bounds__(kThreads, (CHAIN && sizeof(T) == 2 ? 4 : 2)) void ssd_glr_back_kernel(GlrArgs g, Chain ch, float* part) {
