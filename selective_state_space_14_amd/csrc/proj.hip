@@ -182,19 +182,19 @@ __device__ __forceinline__ uint32_t at(int r, int c) { return (uint32_t)(r * 128
 __device__ __forceinline__ int piece_of(int g, int h) { return (g & 1) | h << 1 | (g >> 1) << 2; }
 
 // A workgroup of NWN x NWM waves owns a tile of y; a wave's part of it is WN x WM products of 16 x 16.  The two operands'
-// block of 128 bytes a row goes through one of two LDS stages while the other is computed, and so do the activations'
+// block of 128 bytes a row goes through one of S LDS stages while another is computed, and so do the activations'
 // scales of 16 blocks at a time: read by the lanes that need them, they would be as many requests as the operands.
 // M = 16384, N = 4096, K = 8192 to bf16: 471 to 490 us, 2.33 to 2.24 PFLOP/s; a library's 8-bit product without block scales
 // takes 412 us there.  Matrix instructions alone would take 300 us at the clock they leave, with their LDS reads and barriers 405;
 // copies and scales add the rest, and the scales' fmas nothing.  A row of products is scaled while the next one's run (one
 // after the other: 666 us).
-template <int BN, int BM> constexpr int kTileLds = 2 * (BN + BM) * 128 + 2 * BM * 16 * 4;
-template <typename T, int WN, int WM, int NWN, int NWM>
+template <int BN, int BM, int S> constexpr int kTileLds = S * (BN + BM) * 128 + 2 * BM * 16 * 4;
+template <typename T, int WN, int WM, int NWN, int NWM, int S>
 __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjArgs p) {
     constexpr int NW = NWN * NWM, BN = 16 * WN * NWN, BM = 16 * WM * NWM, kStage = (BN + BM) * 128;
     constexpr int kCopies = (BN + BM) / 8 / NW;     // of a wave: 8 rows each
     constexpr int kPerRow = (2 * kCopies + WN - 1) / WN;      // copies beside a row of products: all in a block's first half
-    static_assert(kCopies * 8 * NW == BN + BM && 128 % (16 * WN) == 0 && WM == 4, "tile");
+    static_assert(kCopies * 8 * NW == BN + BM && 128 % (16 * WN) == 0 && WM == 4 && (S == 2 || S == 4), "tile");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, i = l % 16, g = l / 16;
     const int wn = wave % NWN, wm = wave / NWN;
@@ -225,13 +225,13 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
     // the wave's j-th copy of block b
     auto copy = [&](int b, int j, auto full) {
         const uint32_t k = (uint32_t)min(b * 128 + (j & 1 ? piece0 ^ 64 : piece0), p.K - 16);
-        const uint32_t to = lds0 + (b & 1) * kStage + wave * kCopies * 1024 + j * 1024;
+        const uint32_t to = lds0 + (b & (S - 1)) * kStage + wave * kCopies * 1024 + j * 1024;
         if constexpr (decltype(full)::value) dma16(base + (size_t)(8 * j) * row_bytes, lane_off + k, to);
         else dma16(base, (uint32_t)min(8 * j + l / 8, max(most, 0)) * row_bytes + k, to);
     };
     // the scales of blocks 16 q .. + 15 go to rows of 16, block c of row r at place c ^ (r % 16): sixteen rows' scales of one
     // block are in sixteen banks.  Rows of at most 2^24 bytes, 255 of them: offsets fit 32 bits.
-    constexpr int kScales = 2 * kStage, kScaleCopies = BM / 4 / NW;       // of a wave: 4 rows each
+    constexpr int kScales = S * kStage, kScaleCopies = BM / 4 / NW;       // of a wave: 4 rows each
     static_assert(kScaleCopies * 4 * NW == BM, "scales");
     const char* as = reinterpret_cast<const char*>(p.a_scale + (int64_t)m0 * p.a_scale_stride);
     auto copy_scales = [&](int q) {
@@ -260,11 +260,17 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
     for (int t = 0; t < WM; ++t) s[t] = 0.0f;
     copy_scales(0);
 #pragma unroll
-    for (int j = 0; j < kCopies; ++j) copy(0, j, std::false_type{});
-    auto block = [&](int b, auto more, auto full) {
-        constexpr bool MORE = decltype(more)::value;
-        // this wave's copies of block b have landed, and then everyone's; the other stage has been read by all
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    for (int k = 0; k < S - 1; ++k) {
+        if (k && k >= blocks) break;
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) copy(k, j, std::false_type{});
+    }
+    // MORE: another block follows, AHEAD: so does the one that is to be copied now
+    auto block = [&](int b, auto more, auto ahead, auto full) {
+        constexpr bool MORE = decltype(more)::value, AHEAD = decltype(ahead)::value;
+        // this wave's copies of block b have landed (those of S - 2 later blocks may not have: copies land in their order), and
+        // then everyone's; the stage of block b - 1 has been read by all
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(AHEAD ? (S - 2) * kCopies : 0) : "memory");
 #pragma unroll
         for (int t = 0; t < WM; ++t) {
             last[t] = s[t];
@@ -274,7 +280,7 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
             nw = ws[b + 1];
             if (b % 16 == 0) copy_scales(b / 16 + 1);
         }
-        const uint8_t* stage = lds + (b & 1) * kStage;
+        const uint8_t* stage = lds + (b & (S - 1)) * kStage;
         auto weights = [&](int u) {
             Bytes w;
 #pragma unroll
@@ -302,9 +308,9 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
             if (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);      // a row at a time: the registers
             const Frag<T> fw(bw);
             if (u + 1 < WN) bw = weights(u + 1);
-            if (MORE) {
+            if (AHEAD) {
 #pragma unroll
-                for (int j = u * kPerRow; j < min((u + 1) * kPerRow, kCopies); ++j) copy(b + 1, j, full);
+                for (int j = u * kPerRow; j < min((u + 1) * kPerRow, kCopies); ++j) copy(b + S - 1, j, full);
             }
             // the products of this row while the last row's are scaled and added
 #pragma unroll
@@ -320,11 +326,14 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
             }
         }
     };
+    int b = 0;
     if (whole)
-        for (int b = 0; b + 1 < blocks; ++b) block(b, std::true_type{}, std::true_type{});
+        for (; b + S - 1 < blocks; ++b) block(b, std::true_type{}, std::true_type{}, std::true_type{});
     else
-        for (int b = 0; b + 1 < blocks; ++b) block(b, std::true_type{}, std::false_type{});
-    block(blocks - 1, std::false_type{}, std::false_type{});
+        for (; b + S - 1 < blocks; ++b) block(b, std::true_type{}, std::true_type{}, std::false_type{});
+    if constexpr (S > 2)
+        for (; b + 1 < blocks; ++b) block(b, std::true_type{}, std::false_type{}, std::false_type{});
+    block(blocks - 1, std::false_type{}, std::false_type{}, std::false_type{});
 #pragma unroll
     for (int t = 0; t < WM; ++t)
 #pragma unroll
@@ -351,46 +360,55 @@ hipError_t rows(const ProjArgs& p, hipStream_t s) {
     hipLaunchKernelGGL((ssd_proj_rows_kernel<T, MT, U>), grid, dim3(64 * kSkinnyWaves), 0, s, p);
     return hipGetLastError();
 }
-template <typename T, int WN, int WM, int NWN, int NWM>
+template <typename T, int WN, int WM, int NWN, int NWM, int S>
 hipError_t tiles(const ProjArgs& p, hipStream_t s) {
-    constexpr int BN = 16 * WN * NWN, BM = 16 * WM * NWM, lds = kTileLds<BN, BM>;
-    const auto kernel = &ssd_proj_tiles_kernel<T, WN, WM, NWN, NWM>;
+    constexpr int BN = 16 * WN * NWN, BM = 16 * WM * NWM, lds = kTileLds<BN, BM, S>;
+    const auto kernel = &ssd_proj_tiles_kernel<T, WN, WM, NWN, NWM, S>;
     if (hipError_t e = prepare_launch(reinterpret_cast<const void*>(kernel), lds)) return e;
     const int64_t n = (int64_t)((p.N + BN - 1) / BN) * ((p.M + BM - 1) / BM);
     hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(64 * NWN * NWM), lds, s, p);
     return hipGetLastError();
 }
 
-// The kernel by its estimated time in us, from sweeps of M, N and K (256 CUs):
-//  - rows: a workgroup reads 16 rows of w and 16 MT of a, 2 KB a block each, at some 28 bytes a ns and CU from one workgroup
-//    or more, 40 where an XCD's 4 MB of L2 hold the weights; 3 us around it.
-//  - tiles of 128 x 128: 0.45 us a block (1 us with widened operands) for one a CU, 0.75 for every further one; 5 us.
+// The kernel by its estimated time in us, from sweeps of M, N and K (256 CUs, one workgroup each before any has two):
+//  - rows: a workgroup reads 16 rows of w and 16 MT of a, 2 KB a block each, at some 28 bytes a ns and CU (a CU's lines on
+//    their way), 40 where an XCD's 4 MB of L2 hold the weights; 3 us around it.
+//  - tiles of 64 x 64, four stages: 0.35 us a block (0.62 with widened operands), the chain of one block's steps; 3.5 us.
+//  - tiles of 128 x 128: 0.5 to 0.8 us a block (1.1 to 1.25) as the CUs fill; 5 us.
 //  - tiles of 256 x 256, one a CU: 1.85 us a block, against 0.7 a 128 x 128 tile when there are many.
-// Measured, bf16, N = 5152, K = 2048: M = 32 rows 9.4, tiles 11.7; M = 64 rows 12.9, tiles 12.2; M = 256 rows 41, tiles 13.3;
-// N = 1024, K = 8192, M = 64: rows 11 (MT = 1; 16 with 2), tiles 37.  M = 777, N = 1000, K = 1040, fp32: rows 10.4, tiles
-// 15.7.  M = 4096, N = 5152, K = 2048: tiles of 128 60, of 256 64; M = N = K = 4096: 95 and 66.
+// Measured, us, in that order (rows: the better MT; -: not built):
+//   bf16  M = 32, N = K = 4096        9.8  14.7  20    42      fp32  M = 777, N = 1000, K = 1040  10.2   8.9  15.9   -
+//         M = 64, N = 5152, K = 2048   13   8.6  12.3  24            M = 300, N = K = 2048        20.6  12.9  23.3   -
+//         M = 16, N = 1024, K = 8192   11    27    37  78            M = 1024, N = K = 4096        227  61.7  45.1   -
+//         M = 512, N = K = 4096       115    22    28  49      bf16  M = 4096, N = 5152, K = 2048    -     -    60  64
+//         M = 1024, N = K = 4096      227    43    30  51            M = N = K = 4096                -     -    95  66
 template <typename T>
 hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
+    constexpr bool kWide = sizeof(T) == 4;           // widened operands
     const auto over = [](double n, int d) { return (double)(((int64_t)n + d - 1) / d); };
-    const double blocks = over(p.K, 128), n16 = over(p.N, 16), small = over(p.N, 128) * over(p.M, 128);
-    const double piece = (int64_t)p.N * p.K <= 4 << 20 ? 0.05 : 0.073;
-    double best = 0.0;
-    int mt = 0;
+    const auto more = [](double n) { return std::max(0.0, n / 256 - 1.0); };      // workgroups a CU after the first
+    const double blocks = over(p.K, 128), n16 = over(p.N, 16), t64 = over(p.N, 64) * over(p.M, 64), t128 = over(p.N, 128) * over(p.M, 128);
+    const double piece = (int64_t)p.N * p.K <= 4 << 20 ? 0.05 : 0.073, most = 0xffffffffu;      // threads that a launch counts
+    double best = 5.0 + blocks * (kWide ? 1.1 + 0.15 * std::min(1.0, t128 / 256) + 0.9 * more(t128)
+                                        : 0.5 + 0.3 * std::min(1.0, t128 / 256) + 0.6 * more(t128));
+    enum { kRows1, kRows2, kTiles64, kTiles128 } kind = kTiles128;
+    const auto consider = [&](auto k, double t, double threads) {
+        if (t >= best || threads > most) return;
+        kind = k;
+        best = t;
+    };
+    consider(kTiles64, 3.5 + blocks * (kWide ? 0.62 + 0.38 * more(t64) : 0.35 + 0.27 * more(t64)), t64 * 256);
     for (int k : {1, 2}) {
         const double wgs = n16 * over(p.M, 16 * k);
-        if (wgs * 64 * kSkinnyWaves > 0xffffffffu) continue;      // a launch counts its threads in 32 bits
-        const double t = 3.0 + blocks * piece * (1 + k) * std::max(1.0, wgs / 256);
-        if (!mt || t < best) {
-            mt = k;
-            best = t;
-        }
+        consider(k == 1 ? kRows1 : kRows2, 3.0 + blocks * piece * (1 + k) * (1.0 + more(wgs)), wgs * 64 * kSkinnyWaves);
     }
-    const double one = sizeof(T) == 2 ? 0.45 : 1.0;
-    if (mt && best < 5.0 + blocks * (one + 0.75 * std::max(0.0, small / 256 - 1.0))) return mt == 1 ? rows<T, 1, 4>(p, s) : rows<T, 2, 2>(p, s);
-    if constexpr (sizeof(T) == 2) {                  // widened operands take too many registers for the larger tile
-        if (over(over(p.N, 256) * over(p.M, 256), 256) * 1.85 < 0.7 * small / 256) return tiles<T, 8, 4, 2, 4>(p, s);
+    if (kind == kRows1) return rows<T, 1, 4>(p, s);
+    if (kind == kRows2) return rows<T, 2, 2>(p, s);
+    if (kind == kTiles64) return tiles<T, 1, 4, 4, 1, 4>(p, s);
+    if constexpr (!kWide) {                          // widened operands take too many registers for the larger tile
+        if (over(over(p.N, 256) * over(p.M, 256), 256) * 1.85 < 0.7 * t128 / 256) return tiles<T, 8, 4, 2, 4, 2>(p, s);
     }
-    return tiles<T, 4, 4, 2, 2>(p, s);
+    return tiles<T, 4, 4, 2, 2, 2>(p, s);
 }
 
 }  // namespace

@@ -66,10 +66,28 @@ def test_proj_of_many_tiles(gpu_lib, M, N, K):
     verify(gpu_lib, d, "bf16")
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [128, 144, 256, 384, 400, 528, 656, 2048, 2064, 2192, 4368])
+def test_proj_of_middling_sizes(gpu_lib, K, t):
+    """Sizes at which the smallest tiles are taken, from one block to more than two sets of 16 scales, full and cut; the same
+    from wider rows full of NaN."""
+    for M, N in ((1000, 1000), (1024, 960)):
+        d = make(M, N, K)
+        want = verify(gpu_lib, d, t)
+        g = {}
+        for n in ("a", "w"):
+            wide = torch.full((d[n].shape[0], K + 32), float("nan"), device=DEV).to(E4M3)
+            wide.view(torch.uint8)[:, 16:16 + K] = d[n].to(DEV).view(torch.uint8)
+            g[n] = wide[:, 16:16 + K]
+        out = torch.full((M, N + 7), 7.0, dtype=T[t], device=DEV)
+        y = gpu_lib.ssd_proj_fp8_fwd(g["a"], d["a_scale"].to(DEV), g["w"], d["w_scale"].to(DEV), y=out[:, 3:3 + N])
+        assert torch.equal(y, want) and (out[:, :3] == 7).all() and (out[:, 3 + N:] == 7).all()
+
+
 def test_proj_exact_sums(gpu_lib):
     """Small whole numbers and scales that are powers of two: every sum is exact, so is y."""
     g = torch.Generator().manual_seed(3)
-    for M, N, K in ((5, 40, 384), (40, 200, 272), (300, 300, 656), (3600, 3600, 176)):
+    for M, N, K in ((5, 40, 384), (40, 200, 272), (300, 300, 656), (1000, 1000, 2064), (3600, 3600, 176)):
         kb = -(-K // 128)
         a, w = (torch.randint(-4, 5, (n, K), generator=g).float() for n in (M, N))
         sa, sw = 2.0 ** torch.randint(-2, 3, (M, kb), generator=g), 2.0 ** torch.randint(-2, 3, (-(-N // 128), kb), generator=g)
@@ -101,7 +119,7 @@ def test_proj_strides(gpu_lib):
 
 
 def test_proj_nan_stays_in_its_row_and_column(gpu_lib):
-    for M, N, K in ((5, 40, 272), (300, 300, 272), (3600, 3600, 272)):
+    for M, N, K in ((5, 40, 272), (300, 300, 272), (1000, 1000, 272), (3600, 3600, 272)):
         d = {n: v.to(DEV) for n, v in make(M, N, K).items()}
         clean = gpu_lib.ssd_proj_fp8_fwd(d["a"], d["a_scale"], d["w"], d["w_scale"])
         d["a"].view(torch.uint8)[2, K - 1] = 0x7f
