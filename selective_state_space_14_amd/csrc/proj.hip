@@ -182,21 +182,25 @@ __device__ __forceinline__ uint32_t at(int r, int c) { return (uint32_t)(r * 128
 __device__ __forceinline__ int piece_of(int g, int h) { return (g & 1) | h << 1 | (g >> 1) << 2; }
 
 // A workgroup of NWN x NWM waves owns a tile of y; a wave's part of it is WN x WM products of 16 x 16.  The two operands'
-// block of 128 bytes a row goes through one of S LDS stages while another is computed, and so do the activations'
+// block of 128 bytes a row goes through one of two LDS stages while the other is computed, and so do the activations'
 // scales of 16 blocks at a time: read by the lanes that need them, they would be as many requests as the operands.
 // M = 16384, N = 4096, K = 8192 to bf16: 471 to 490 us, 2.33 to 2.24 PFLOP/s; a library's 8-bit product without block scales
 // takes 412 us there.  Matrix instructions alone would take 300 us at the clock they leave, with their LDS reads and barriers 405;
 // copies and scales add the rest, and the scales' fmas nothing.  A row of products is scaled while the next one's run (one
 // after the other: 666 us).
-template <int BN, int BM, int S> constexpr int kTileLds = S * (BN + BM) * 128 + 2 * BM * 16 * 4;
-template <typename T, int WN, int WM, int NWN, int NWM, int S>
-__global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjArgs p) {
+// KG groups of waves take every KG-th block each, in stages of their own, and their sums meet in LDS: in a small tile a wave's
+// steps of a block are a chain that nothing else covers (64 x 64 of K = 4096: 14.2 us with one group and four stages, 11.0
+// with two groups of two; 256 x 4096 x 4096 16.0 and 13.3).
+template <int BN, int BM, int KG> constexpr int kTileLds = KG * 2 * (BN + BM) * 128 + 2 * BM * 16 * 4;
+template <typename T, int WN, int WM, int NWN, int NWM, int KG>
+__global__ __launch_bounds__(64 * NWN * NWM * KG, 2) void ssd_proj_tiles_kernel(ProjArgs p) {
     constexpr int NW = NWN * NWM, BN = 16 * WN * NWN, BM = 16 * WM * NWM, kStage = (BN + BM) * 128;
     constexpr int kCopies = (BN + BM) / 8 / NW;     // of a wave: 8 rows each
     constexpr int kPerRow = (2 * kCopies + WN - 1) / WN;      // copies beside a row of products: all in a block's first half
-    static_assert(kCopies * 8 * NW == BN + BM && 128 % (16 * WN) == 0 && WM == 4 && (S == 2 || S == 4), "tile");
+    static_assert(kCopies * 8 * NW == BN + BM && 128 % (16 * WN) == 0 && WM == 4 && 16 % KG == 0, "tile");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, i = l % 16, g = l / 16;
+    const int l = threadIdx.x % 64, i = l % 16, g = l / 16, any = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wave = any % NW, group = any / NW;
     const int wn = wave % NWN, wm = wave / NWN;
     // tiles of y in an order that keeps an XCD's workgroups (every eighth of the launch) on neighbouring tiles: panels of
     // 8 tiles of rows, column by column
@@ -222,16 +226,17 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
     if (most < 0) base += (int64_t)most * row_bytes;                              // row0 itself is past the last
     const uint32_t lane_off = (uint32_t)(l / 8) * row_bytes;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    auto stage_of = [&](int b) { return (group * 2 + (b / KG & 1)) * kStage; };
     // the wave's j-th copy of block b
     auto copy = [&](int b, int j, auto full) {
         const uint32_t k = (uint32_t)min(b * 128 + (j & 1 ? piece0 ^ 64 : piece0), p.K - 16);
-        const uint32_t to = lds0 + (b & (S - 1)) * kStage + wave * kCopies * 1024 + j * 1024;
+        const uint32_t to = lds0 + stage_of(b) + wave * kCopies * 1024 + j * 1024;
         if constexpr (decltype(full)::value) dma16(base + (size_t)(8 * j) * row_bytes, lane_off + k, to);
         else dma16(base, (uint32_t)min(8 * j + l / 8, max(most, 0)) * row_bytes + k, to);
     };
     // the scales of blocks 16 q .. + 15 go to rows of 16, block c of row r at place c ^ (r % 16): sixteen rows' scales of one
     // block are in sixteen banks.  Rows of at most 2^24 bytes, 255 of them: offsets fit 32 bits.
-    constexpr int kScales = S * kStage, kScaleCopies = BM / 4 / NW;       // of a wave: 4 rows each
+    constexpr int kScales = KG * 2 * kStage, kScaleCopies = BM / 4 / NW;       // of a wave: 4 rows each
     static_assert(kScaleCopies * 4 * NW == BM, "scales");
     const char* as = reinterpret_cast<const char*>(p.a_scale + (int64_t)m0 * p.a_scale_stride);
     auto copy_scales = [&](int q) {
@@ -255,32 +260,28 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
 #pragma unroll
         for (int u = 0; u < WN; ++u) acc[u][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    float s[WM], last[WM], nw = ws[0];
+    float s[WM], last[WM], nw = ws[min(group, blocks - 1)];
 #pragma unroll
     for (int t = 0; t < WM; ++t) s[t] = 0.0f;
-    copy_scales(0);
+    if (group == 0) copy_scales(0);
+    const int steps = (blocks + KG - 1) / KG;        // of every group; a last one past the last block adds 0
 #pragma unroll
-    for (int k = 0; k < S - 1; ++k) {
-        if (k && k >= blocks) break;
-#pragma unroll
-        for (int j = 0; j < kCopies; ++j) copy(k, j, std::false_type{});
-    }
-    // MORE: another block follows, AHEAD: so does the one that is to be copied now
-    auto block = [&](int b, auto more, auto ahead, auto full) {
-        constexpr bool MORE = decltype(more)::value, AHEAD = decltype(ahead)::value;
-        // this wave's copies of block b have landed (those of S - 2 later blocks may not have: copies land in their order), and
-        // then everyone's; the stage of block b - 1 has been read by all
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(AHEAD ? (S - 2) * kCopies : 0) : "memory");
+    for (int j = 0; j < kCopies; ++j) copy(group, j, std::false_type{});
+    auto block = [&](int b, auto more, auto full) {
+        constexpr bool MORE = decltype(more)::value;
+        // this wave's copies of block b have landed, and then everyone's; the other stage has been read by all
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
         for (int t = 0; t < WM; ++t) {
             last[t] = s[t];
             s[t] = a_scale(b, t) * nw;
+            if (!MORE && KG > 1 && b >= blocks) s[t] = 0.0f;
         }
         if (MORE) {
-            nw = ws[b + 1];
-            if (b % 16 == 0) copy_scales(b / 16 + 1);
+            nw = ws[KG == 1 ? b + 1 : min(b + KG, blocks - 1)];
+            if (b % 16 == 0) copy_scales(b / 16 + 1);            // group 0's: KG divides 16
         }
-        const uint8_t* stage = lds + (b & (S - 1)) * kStage;
+        const uint8_t* stage = lds + stage_of(b);
         auto weights = [&](int u) {
             Bytes w;
 #pragma unroll
@@ -308,9 +309,9 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
             if (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);      // a row at a time: the registers
             const Frag<T> fw(bw);
             if (u + 1 < WN) bw = weights(u + 1);
-            if (AHEAD) {
+            if (MORE) {
 #pragma unroll
-                for (int j = u * kPerRow; j < min((u + 1) * kPerRow, kCopies); ++j) copy(b + S - 1, j, full);
+                for (int j = u * kPerRow; j < min((u + 1) * kPerRow, kCopies); ++j) copy(b + KG, j, full);
             }
             // the products of this row while the last row's are scaled and added
 #pragma unroll
@@ -326,20 +327,36 @@ __global__ __launch_bounds__(64 * NWN * NWM, 2) void ssd_proj_tiles_kernel(ProjA
             }
         }
     };
-    int b = 0;
+    const int end = (steps - 1) * KG + group;
     if (whole)
-        for (; b + S - 1 < blocks; ++b) block(b, std::true_type{}, std::true_type{}, std::true_type{});
+        for (int b = group; b < end; b += KG) block(b, std::true_type{}, std::true_type{});
     else
-        for (; b + S - 1 < blocks; ++b) block(b, std::true_type{}, std::true_type{}, std::false_type{});
-    if constexpr (S > 2)
-        for (; b + 1 < blocks; ++b) block(b, std::true_type{}, std::false_type{}, std::false_type{});
-    block(blocks - 1, std::false_type{}, std::false_type{}, std::false_type{});
+        for (int b = group; b < end; b += KG) block(b, std::true_type{}, std::false_type{});
+    block(end, std::false_type{}, std::false_type{});
 #pragma unroll
     for (int t = 0; t < WM; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[WN - 1][t][e] = fmaf(d[t][e], s[t], acc[WN - 1][t][e]);
 #pragma unroll
     for (int t = 0; t < WM; ++t) asm volatile("" : "+v"(acc[WN - 1][t]));
+    if constexpr (KG > 1) {                          // the groups' sums, in order; the stages have been read by all
+        f32x4* sums = reinterpret_cast<f32x4*>(lds);
+        __syncthreads();
+        if (group) {
+#pragma unroll
+            for (int t = 0; t < WM; ++t)
+#pragma unroll
+                for (int u = 0; u < WN; ++u) sums[(((group - 1) * NW + wave) * WN * WM + t * WN + u) * 64 + l] = acc[u][t];
+        }
+        __syncthreads();
+        if (group) return;
+#pragma unroll
+        for (int k = 0; k < KG - 1; ++k)
+#pragma unroll
+            for (int t = 0; t < WM; ++t)
+#pragma unroll
+                for (int u = 0; u < WN; ++u) acc[u][t] += sums[((k * NW + wave) * WN * WM + t * WN + u) * 64 + l];
+    }
     T* y = static_cast<T*>(p.y);
 #pragma unroll
     for (int t = 0; t < WM; ++t) {
@@ -360,28 +377,30 @@ hipError_t rows(const ProjArgs& p, hipStream_t s) {
     hipLaunchKernelGGL((ssd_proj_rows_kernel<T, MT, U>), grid, dim3(64 * kSkinnyWaves), 0, s, p);
     return hipGetLastError();
 }
-template <typename T, int WN, int WM, int NWN, int NWM, int S>
+template <typename T, int WN, int WM, int NWN, int NWM, int KG>
 hipError_t tiles(const ProjArgs& p, hipStream_t s) {
-    constexpr int BN = 16 * WN * NWN, BM = 16 * WM * NWM, lds = kTileLds<BN, BM, S>;
-    const auto kernel = &ssd_proj_tiles_kernel<T, WN, WM, NWN, NWM, S>;
+    constexpr int BN = 16 * WN * NWN, BM = 16 * WM * NWM, lds = kTileLds<BN, BM, KG>;
+    const auto kernel = &ssd_proj_tiles_kernel<T, WN, WM, NWN, NWM, KG>;
     if (hipError_t e = prepare_launch(reinterpret_cast<const void*>(kernel), lds)) return e;
     const int64_t n = (int64_t)((p.N + BN - 1) / BN) * ((p.M + BM - 1) / BM);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(64 * NWN * NWM), lds, s, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(64 * NWN * NWM * KG), lds, s, p);
     return hipGetLastError();
 }
 
 // The kernel by its estimated time in us, from sweeps of M, N and K (256 CUs, one workgroup each before any has two):
 //  - rows: a workgroup reads 16 rows of w and 16 MT of a, 2 KB a block each, at some 28 bytes a ns and CU (a CU's lines on
 //    their way), 40 where an XCD's 4 MB of L2 hold the weights; 3 us around it.
-//  - tiles of 64 x 64, four stages: 0.35 us a block (0.62 with widened operands), the chain of one block's steps; 3.5 us.
+//  - tiles of 64 x 64, K in two groups: 0.24 to 0.31 us a block (0.4 to 0.5 with widened operands), the chain of a block's
+//    steps; 3.5 us.
 //  - tiles of 128 x 128: 0.5 to 0.8 us a block (1.1 to 1.25) as the CUs fill; 5 us.
 //  - tiles of 256 x 256, one a CU: 1.85 us a block, against 0.7 a 128 x 128 tile when there are many.
 // Measured, us, in that order (rows: the better MT; -: not built):
-//   bf16  M = 32, N = K = 4096        9.8  14.7  20    42      fp32  M = 777, N = 1000, K = 1040  10.2   8.9  15.9   -
-//         M = 64, N = 5152, K = 2048   13   8.6  12.3  24            M = 300, N = K = 2048        20.6  12.9  23.3   -
-//         M = 16, N = 1024, K = 8192   11    27    37  78            M = 1024, N = K = 4096        227  61.7  45.1   -
-//         M = 512, N = K = 4096       115    22    28  49      bf16  M = 4096, N = 5152, K = 2048    -     -    60  64
-//         M = 1024, N = K = 4096      227    43    30  51            M = N = K = 4096                -     -    95  66
+//   bf16  M = 32, N = K = 4096        9.8  11.4  20    42      fp32  M = 777, N = 1000, K = 1040  10.2   8.5  15.9   -
+//         M = 64, N = 5152, K = 2048   13   8.5  12.3  24            M = 300, N = K = 2048        20.6  10.7  23.3   -
+//         M = 16, N = 1024, K = 8192   11    19    37  78            M = 512, N = K = 4096         115  31.3  41.6   -
+//         M = 256, N = K = 4096        59  13.3  21.7  48      bf16  M = 4096, N = 5152, K = 2048    -     -    60  64
+//         M = 512, N = K = 4096       115    19    28  49            M = N = K = 4096                -     -    95  66
+//         M = 800, N = K = 4096         -    35    29  50            M = 2000, N = 8192, K = 256     53    29    18  17
 template <typename T>
 hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
     constexpr bool kWide = sizeof(T) == 4;           // widened operands
@@ -397,18 +416,19 @@ hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
         kind = k;
         best = t;
     };
-    consider(kTiles64, 3.5 + blocks * (kWide ? 0.62 + 0.38 * more(t64) : 0.35 + 0.27 * more(t64)), t64 * 256);
+    consider(kTiles64, 3.5 + blocks * (kWide ? 0.4 + 0.09 * std::min(1.0, t64 / 256) + 0.5 * more(t64)
+                                            : 0.24 + 0.07 * std::min(1.0, t64 / 256) + 0.3 * more(t64)), t64 * 512);
     for (int k : {1, 2}) {
         const double wgs = n16 * over(p.M, 16 * k);
         consider(k == 1 ? kRows1 : kRows2, 3.0 + blocks * piece * (1 + k) * (1.0 + more(wgs)), wgs * 64 * kSkinnyWaves);
     }
     if (kind == kRows1) return rows<T, 1, 4>(p, s);
     if (kind == kRows2) return rows<T, 2, 2>(p, s);
-    if (kind == kTiles64) return tiles<T, 1, 4, 4, 1, 4>(p, s);
+    if (kind == kTiles64) return tiles<T, 1, 4, 4, 1, 2>(p, s);
     if constexpr (!kWide) {                          // widened operands take too many registers for the larger tile
-        if (over(over(p.N, 256) * over(p.M, 256), 256) * 1.85 < 0.7 * t128 / 256) return tiles<T, 8, 4, 2, 4, 2>(p, s);
+        if (over(over(p.N, 256) * over(p.M, 256), 256) * 1.85 < 0.7 * t128 / 256) return tiles<T, 8, 4, 2, 4, 1>(p, s);
     }
-    return tiles<T, 4, 4, 2, 2, 2>(p, s);
+    return tiles<T, 4, 4, 2, 2, 1>(p, s);
 }
 
 }  // namespace
