@@ -8,8 +8,8 @@
 // and a second forward see the same row.  q is rounded from fp32, not from a y that was rounded before.
 //
 // One pass over HBM: a row stays in its threads' registers from the sum to the last output.  Threads and vectors of a row
-// are norm.hip's.  Where rows are read in vectors of 8, 128 columns are 16 neighbouring lanes and their maximum is four
-// lane exchanges; else the columns' maxima meet in LDS.
+// are norm.hip's, but that every row is read in vectors of 8: one that does not start on 16 bytes, or ends inside a vector, at
+// the alignment of its elements.  128 columns are 16 neighbouring lanes, so their maximum is four lane exchanges.
 //
 // Bound by HBM.  Measured: 32768 rows of 4096, bf16 plus bf16 to e4m3, 182 us (944 MB, 5.2 TB/s, the rate of a large copy);
 // 16 rows of 2048 6 us, a launch and a row's latency.  The backward, 40960 rows of 2048 in bf16 with the stream's gradient:
@@ -52,18 +52,19 @@ __device__ __forceinline__ float round_to(const float*, float v) { return v; }
 __device__ __forceinline__ float round_to(const uint16_t*, float v) { return __uint_as_float(f32_to_bf16_bits(v) << 16); }
 
 // S: the type of the row that is normalised (the residual's, or x's where there is none); T: y's and z's
-template <typename S, typename T, int TPR, int NV, int VEC>
-__global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_add_norm_kernel(AddNormArgs a) {
+// ODD: rows off the 16-byte grid, or cut inside a thread's eight columns
+template <typename S, typename T, int TPR, int NV, bool ODD>
+__global__ __launch_bounds__((Shape<TPR, NV, 8>::threads)) void ssd_add_norm_kernel(AddNormArgs a) {
+    constexpr int VEC = 8;
     using SH = Shape<TPR, NV, VEC>;
     __shared__ float red[2][2][16];
-    __shared__ uint32_t tops[VEC == 8 ? 1 : SH::rows][VEC == 8 ? 1 : (TPR * NV + 127) / 128];
     int turn = 0;
     const int lane = threadIdx.x % TPR, sub = SH::rows == 1 ? 0 : threadIdx.x / TPR;
     bool on[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) on[j] = (lane + j * TPR) * VEC < a.W;
     float wv[NV][VEC], bv[NV][VEC];
-    load_params<TPR, NV, VEC>(a.w, a.b, on, lane, wv, bv);
+    load_params<TPR, NV, VEC, ODD>(a.w, a.b, on, lane, wv, bv, a.W);
     const S* rp = static_cast<const S*>(a.residual);
     S* sp = static_cast<S*>(a.sum);
     const T* zp = static_cast<const T*>(a.z);
@@ -80,23 +81,25 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_add_norm_k
             if (live && on[j]) {
                 if (rp) {
                     float f[VEC];
-                    ldv<VEC>(rp + r * a.residual_stride + c, f);
-                    if (a.x_dtype == 0) ldv<VEC>(static_cast<const float*>(a.x) + r * a.x_stride + c, x[j]);
-                    else ldv<VEC>(static_cast<const uint16_t*>(a.x) + r * a.x_stride + c, x[j]);
+                    ld_row<VEC, ODD>(rp + r * a.residual_stride + c, a.W - c, f);
+                    if (a.x_dtype == 0) ld_row<VEC, ODD>(static_cast<const float*>(a.x) + r * a.x_stride + c, a.W - c, x[j]);
+                    else ld_row<VEC, ODD>(static_cast<const uint16_t*>(a.x) + r * a.x_stride + c, a.W - c, x[j]);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) x[j][e] = round_to(rp, x[j][e] + f[e]);
                 } else {
-                    ldv<VEC>(static_cast<const S*>(a.x) + r * a.x_stride + c, x[j]);
+                    ld_row<VEC, ODD>(static_cast<const S*>(a.x) + r * a.x_stride + c, a.W - c, x[j]);
                 }
-                if (zp) ldv<VEC>(zp + r * a.z_stride + c, z[j]);
+                if (zp) ld_row<VEC, ODD>(zp + r * a.z_stride + c, a.W - c, z[j]);
             }
         }
         if (sp) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (live && on[j]) stv<VEC>(sp + r * a.sum_stride + (lane + j * TPR) * VEC, x[j]);
+            for (int j = 0; j < NV; ++j) {
+                const int c = (lane + j * TPR) * VEC;
+                if (live && on[j]) st_row<VEC, ODD>(sp + r * a.sum_stride + c, a.W - c, x[j]);
+            }
         }
-        to_hat<TPR, NV, VEC>(x, on, live, a.W, a.rms, a.eps, red, turn);
+        to_hat<TPR, NV, VEC, ODD>(x, on, live, a.W, a.rms, a.eps, red, turn, lane);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -106,89 +109,76 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_add_norm_k
             }
         if (yp) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (live && on[j]) stv<VEC>(yp + r * a.y_stride + (lane + j * TPR) * VEC, x[j]);
+            for (int j = 0; j < NV; ++j) {
+                const int c = (lane + j * TPR) * VEC;
+                if (live && on[j]) st_row<VEC, ODD>(yp + r * a.y_stride + c, a.W - c, x[j]);
+            }
         }
         if (!a.q) continue;
-        if constexpr (VEC == 8) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                float top = 0.0f;
+        for (int j = 0; j < NV; ++j) {
+            float top = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, size_of(on[j] ? x[j][e] : 0.0f));
-                const float scale = scale_of(lanes_max<(TPR < 16 ? TPR : 16)>(top)), inv = 1.0f / scale;
-                float v[8];
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, size_of(on[j] ? x[j][e] : 0.0f));
+            const float scale = scale_of(lanes_max<(TPR < 16 ? TPR : 16)>(top)), inv = 1.0f / scale;
+            float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = into_range(x[j][e] * inv);
-                uint2 o;
-                int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-                o.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], p, true);
-                p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
-                o.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], p, true);
-                const int c = lane + j * TPR;
-                if (live && on[j]) {
-                    *reinterpret_cast<uint2*>(a.q + r * a.q_stride + c * 8) = o;
-                    if (c % 16 == 0) a.scale[r * a.scale_stride + c / 16] = scale;
+            for (int e = 0; e < 8; ++e) v[e] = into_range(x[j][e] * inv);
+            uint2 o;
+            int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+            o.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], p, true);
+            p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+            o.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], p, true);
+            const int c = lane + j * TPR;
+            if (live && on[j]) {
+                uint8_t* q = a.q + r * a.q_stride + c * 8;
+                if (!ODD) {
+                    *reinterpret_cast<uint2*>(q) = o;
+                } else if (a.W - c * 8 >= 8) {
+                    __builtin_memcpy(q, &o, 8);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (e < a.W - c * 8) q[e] = (uint8_t)((e < 4 ? o.x : o.y) >> 8 * (e % 4));
                 }
-            }
-        } else {
-            // block k of the row: columns c = lane + j * TPR with c / 128 = k
-            __syncthreads();                        // the last row's maxima have been read
-            for (int k = lane; k < (TPR * NV + 127) / 128; k += TPR) tops[sub][k] = 0;
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (on[j]) atomicMax(&tops[sub][(lane + j * TPR) / 128], __float_as_uint(size_of(x[j][0])));
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = lane + j * TPR;
-                if (!live || !on[j]) continue;
-                const float scale = scale_of(__uint_as_float(tops[sub][c / 128]));
-                const int p = __builtin_amdgcn_cvt_pk_fp8_f32(into_range(x[j][0] * (1.0f / scale)), 0.0f, 0, false);
-                a.q[r * a.q_stride + c] = (uint8_t)p;
-                if (c % 128 == 0) a.scale[r * a.scale_stride + c / 128] = scale;
+                if (c % 16 == 0) a.scale[r * a.scale_stride + c / 16] = scale;
             }
         }
     }
 }
 
-template <typename S, typename T, int TPR, int NV, int VEC>
+template <typename S, typename T, int TPR, int NV, bool ODD>
 hipError_t launch(const AddNormArgs& a, hipStream_t stream) {
-    using SH = Shape<TPR, NV, VEC>;
+    using SH = Shape<TPR, NV, 8>;
     const int64_t blocks = std::min<int64_t>((a.R + SH::rows - 1) / SH::rows, kNormGrid);
-    hipLaunchKernelGGL((ssd_add_norm_kernel<S, T, TPR, NV, VEC>), dim3((unsigned)blocks), dim3(SH::threads), 0, stream, a);
+    hipLaunchKernelGGL((ssd_add_norm_kernel<S, T, TPR, NV, ODD>), dim3((unsigned)blocks), dim3(SH::threads), 0, stream, a);
     return hipGetLastError();
 }
 
 // Threads and vectors of a row: norm.hip's up to 32 columns a thread, where they are measured.
-template <typename S, typename T>
+template <typename S, typename T, bool ODD>
 hipError_t launch_t(const AddNormArgs& a, hipStream_t s) {
-    if (a.vec) {
-        const int n = a.W / 8;
-        if (n <= 8) return launch<S, T, 8, 1, 8>(a, s);
-        if (n <= 16) return launch<S, T, 16, 1, 8>(a, s);
-        if (n <= 32) return launch<S, T, 32, 1, 8>(a, s);
-        if (n <= 64) return launch<S, T, 64, 1, 8>(a, s);
-        if (n <= 128) return launch<S, T, 64, 2, 8>(a, s);
-        if (n <= 256) return launch<S, T, 64, 4, 8>(a, s);
-        if (n <= 512) return launch<S, T, 256, 2, 8>(a, s);
-        if (n <= 1024) return launch<S, T, 256, 4, 8>(a, s);
-        return launch<S, T, 512, 4, 8>(a, s);
-    }
-    if (a.W <= 16) return launch<S, T, 16, 1, 1>(a, s);
-    if (a.W <= 64) return launch<S, T, 64, 1, 1>(a, s);
-    if (a.W <= 256) return launch<S, T, 64, 4, 1>(a, s);
-    if (a.W <= 1024) return launch<S, T, 64, 16, 1>(a, s);
-    if (a.W <= 4096) return launch<S, T, 256, 16, 1>(a, s);
-    return launch<S, T, 512, 16, 1>(a, s);
+    const int n = (a.W + 7) / 8;
+    if (n <= 8) return launch<S, T, 8, 1, ODD>(a, s);
+    if (n <= 16) return launch<S, T, 16, 1, ODD>(a, s);
+    if (n <= 32) return launch<S, T, 32, 1, ODD>(a, s);
+    if (n <= 64) return launch<S, T, 64, 1, ODD>(a, s);
+    if (n <= 128) return launch<S, T, 64, 2, ODD>(a, s);
+    if (n <= 256) return launch<S, T, 64, 4, ODD>(a, s);
+    if (n <= 512) return launch<S, T, 256, 2, ODD>(a, s);
+    if (n <= 1024) return launch<S, T, 256, 4, ODD>(a, s);
+    return launch<S, T, 512, 4, false>(a, s);        // rows of more than 8192 are on the grid
+}
+template <typename S, typename T>
+hipError_t launch_s(const AddNormArgs& a, hipStream_t s) {
+    return a.vec ? launch_t<S, T, false>(a, s) : launch_t<S, T, true>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t s) {
-    if (a.s_dtype == 0) return a.dtype == 0 ? launch_t<float, float>(a, s) : launch_t<float, uint16_t>(a, s);
-    return a.dtype == 0 ? launch_t<uint16_t, float>(a, s) : launch_t<uint16_t, uint16_t>(a, s);
+    if (a.s_dtype == 0) return a.dtype == 0 ? launch_s<float, float>(a, s) : launch_s<float, uint16_t>(a, s);
+    return a.dtype == 0 ? launch_s<uint16_t, float>(a, s) : launch_s<uint16_t, uint16_t>(a, s);
 }
 
 }  // namespace ssd

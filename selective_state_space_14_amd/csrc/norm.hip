@@ -95,8 +95,9 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_fwd_k
     }
 }
 
-// ADD: dx also takes gs, the gradient that reaches the norm's input past it (a residual stream's)
-template <typename X, typename T, int TPR, int NV, int VEC, bool ADD>
+// ADD: dx also takes gs, the gradient that reaches the norm's input past it (a residual stream's), or null with ODD: rows off
+// the 16-byte grid, or cut inside a thread's eight columns
+template <typename X, typename T, int TPR, int NV, int VEC, bool ADD, bool ODD>
 __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_kernel(
     std::conditional_t<ADD, AddNormBwdArgs, NormArgs> a) {
     using SH = Shape<TPR, NV, VEC>;
@@ -113,7 +114,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
     constexpr bool kAddAhead = ADD && !kLds;         // and gs is read where it is used
     __shared__ float sums[2][kLds ? NV * VEC : 1][kLds ? TPR : 1];
     float wv[NV][VEC], bv[NV][VEC], dw[kLds ? 1 : NV][VEC], db[kLds ? 1 : NV][VEC];
-    if (kHeld) load_params<TPR, NV, VEC>(a.w, a.b, on, lane, wv, bv);
+    if (kHeld) load_params<TPR, NV, VEC, ODD>(a.w, a.b, on, lane, wv, bv, a.W);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -149,10 +150,19 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             ng[j].clear();
             if constexpr (kAddAhead) ns[j].clear();
             if (live && on[j]) {
-                if constexpr (kAddAhead) ns[j].load(sp + r * sp_stride + col + c);
-                nx[j].load(xp + r * a.x_stride + col + c);
-                ng[j].load(gp + r * a.gy_stride + col + c);
-                if (zp) nz[j].load(zp + r * a.z_stride + col + c);
+                if constexpr (ODD) {
+                    if constexpr (kAddAhead) {
+                        if (sp) ns[j].load_odd(sp + r * sp_stride + c, a.W - c);
+                    }
+                    nx[j].load_odd(xp + r * a.x_stride + c, a.W - c);
+                    ng[j].load_odd(gp + r * a.gy_stride + c, a.W - c);
+                    if (zp) nz[j].load_odd(zp + r * a.z_stride + c, a.W - c);
+                } else {
+                    if constexpr (kAddAhead) ns[j].load(sp + r * sp_stride + col + c);
+                    nx[j].load(xp + r * a.x_stride + col + c);
+                    ng[j].load(gp + r * a.gy_stride + col + c);
+                    if (zp) nz[j].load(zp + r * a.z_stride + col + c);
+                }
             }
         }
     };
@@ -175,8 +185,8 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             if constexpr (kAddAhead) ns[j].get(past[j]);
         }
         if (kAhead) fetch(at + step);
-        const float rstd = to_hat<TPR, NV, VEC>(x, on, live, a.W, a.rms, a.eps, red, turn);
-        if (!kHeld) load_params<TPR, NV, VEC>(a.w, a.b, on, lane, wv, bv);
+        const float rstd = to_hat<TPR, NV, VEC, ODD>(x, on, live, a.W, a.rms, a.eps, red, turn, lane);
+        if (!kHeld) load_params<TPR, NV, VEC, ODD>(a.w, a.b, on, lane, wv, bv, a.W);
         float m1 = 0.0f, m2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -190,7 +200,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
                     d[e] = g[j][e] * n * s * fmaf(z[j][e], 1.0f - s, 1.0f);
                     g[j][e] *= z[j][e] * s;
                 }
-                if (dzp && live && on[j]) stv<VEC>(dzp + r * a.dz_stride + col + c, d);
+                if (dzp && live && on[j]) st_row<VEC, ODD>(dzp + r * a.dz_stride + col + c, a.W - c, d);
             }
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
@@ -226,7 +236,7 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
                     for (int e = 0; e < VEC; ++e) d[e] += p[e];
                 }
             }
-            if (live && on[j]) stv<VEC>(dxp + r * a.dx_stride + col + c, d);
+            if (live && on[j]) st_row<VEC, ODD>(dxp + r * a.dx_stride + col + c, a.W - c, d);
         }
     }
     // the workgroup's sums: [block][2][W], rows of the workgroup added in order
@@ -249,8 +259,8 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
         for (int j = 0; j < NV; ++j) {
             const int c = (lane + j * TPR) * VEC;
             if (on[j]) {
-                stv<VEC>(out + c, dw[j]);
-                stv<VEC>(out + a.W + c, db[j]);
+                st_row<VEC, ODD>(out + c, a.W - c, dw[j]);
+                st_row<VEC, ODD>(out + a.W + c, a.W - c, db[j]);
             }
         }
     } else {
@@ -312,12 +322,11 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((ssd_norm_fwd_kernel<X, T, TPR, NV, VEC>), dim3((unsigned)blocks), dim3(SH::threads), 0, stream, a);
     return hipGetLastError();
 }
-template <typename X, typename T, int TPR, int NV, int VEC, typename Args>
+template <typename X, typename T, int TPR, int NV, int VEC, bool ODD = false, typename Args>
 hipError_t launch_bwd(const Args& a, hipStream_t stream) {
     using SH = Shape<TPR, NV, VEC>;
     const int n = (int)std::min<int64_t>((a.R + SH::rows - 1) / SH::rows, kNormBwdGrid);
-    constexpr bool kAdd = std::is_same_v<Args, AddNormBwdArgs>;
-    hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC, kAdd>), dim3(n), dim3(SH::threads), 0, stream, a);
+    hipLaunchKernelGGL((ssd_norm_bwd_kernel<X, T, TPR, NV, VEC, std::is_same_v<Args, AddNormBwdArgs>, ODD>), dim3(n), dim3(SH::threads), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
     hipLaunchKernelGGL(ssd_norm_sum_kernel, dim3((2 * a.W + 31) / 32), dim3(1024), 0, stream, a.part, n, a.W, a.dw, a.db);
@@ -347,26 +356,33 @@ hipError_t launch_fwd_t(const NormArgs& a, hipStream_t s) {
     if (a.W <= 4096) return launch_fwd<X, T, 256, 16, 1>(a, s);
     return launch_fwd<X, T, 512, 16, 1>(a, s);
 }
-template <typename X, typename T, typename Args>
-hipError_t launch_bwd_t(const Args& a, hipStream_t s) {
-    if (a.vec) {
-        const int n = a.W / 8;
-        if (n <= 8) return launch_bwd<X, T, 8, 1, 8>(a, s);
-        if (n <= 16) return launch_bwd<X, T, 16, 1, 8>(a, s);
-        if (n <= 32) return launch_bwd<X, T, 32, 1, 8>(a, s);
-        if (n <= 64) return launch_bwd<X, T, 64, 1, 8>(a, s);
-        if (n <= 128) return launch_bwd<X, T, 64, 2, 8>(a, s);
-        if (n <= 256) return launch_bwd<X, T, 256, 1, 8>(a, s);
-        if (n <= 512) return launch_bwd<X, T, 256, 2, 8>(a, s);
-        if (n <= 1024) return launch_bwd<X, T, 512, 2, 8>(a, s);
-        return launch_bwd<X, T, 1024, 2, 8>(a, s);
-    }
+// every row in vectors, ODD: at the alignment of their elements
+template <typename X, typename T, bool ODD, typename Args>
+hipError_t launch_bwd_vec(const Args& a, hipStream_t s) {
+    const int n = (a.W + 7) / 8;
+    if (n <= 8) return launch_bwd<X, T, 8, 1, 8, ODD>(a, s);
+    if (n <= 16) return launch_bwd<X, T, 16, 1, 8, ODD>(a, s);
+    if (n <= 32) return launch_bwd<X, T, 32, 1, 8, ODD>(a, s);
+    if (n <= 64) return launch_bwd<X, T, 64, 1, 8, ODD>(a, s);
+    if (n <= 128) return launch_bwd<X, T, 64, 2, 8, ODD>(a, s);
+    if (n <= 256) return launch_bwd<X, T, 256, 1, 8, ODD>(a, s);
+    if (n <= 512) return launch_bwd<X, T, 256, 2, 8, ODD>(a, s);
+    if (n <= 1024) return launch_bwd<X, T, 512, 2, 8, ODD>(a, s);
+    return launch_bwd<X, T, 1024, 2, 8>(a, s);       // rows of more than 8192 are on the grid
+}
+template <typename X, typename T>
+hipError_t launch_bwd_t(const NormArgs& a, hipStream_t s) {
+    if (a.vec) return launch_bwd_vec<X, T, false>(a, s);
     if (a.W <= 16) return launch_bwd<X, T, 16, 1, 1>(a, s);
     if (a.W <= 64) return launch_bwd<X, T, 64, 1, 1>(a, s);
     if (a.W <= 256) return launch_bwd<X, T, 64, 4, 1>(a, s);
     if (a.W <= 1024) return launch_bwd<X, T, 256, 4, 1>(a, s);
     if (a.W <= 4096) return launch_bwd<X, T, 512, 8, 1>(a, s);
     return launch_bwd<X, T, 1024, 8, 1>(a, s);
+}
+template <typename X, typename T>
+hipError_t launch_bwd_t(const AddNormBwdArgs& a, hipStream_t s) {
+    return a.vec ? launch_bwd_vec<X, T, false>(a, s) : launch_bwd_vec<X, T, true>(a, s);
 }
 template <typename X, typename T>
 hipError_t launch_norm_t(const NormArgs& a, hipStream_t s) {
@@ -385,7 +401,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_add_norm_bwd(const AddNormBwdArgs& a, hipStream_t s) {
-    if (!a.gs) return launch_norm(a, s);
+    if (a.vec && !a.gs) return launch_norm(a, s);
     if (a.x_dtype == 0) return a.dtype == 0 ? launch_bwd_t<float, float>(a, s) : launch_bwd_t<float, uint16_t>(a, s);
     return a.dtype == 0 ? launch_bwd_t<uint16_t, float>(a, s) : launch_bwd_t<uint16_t, uint16_t>(a, s);
 }

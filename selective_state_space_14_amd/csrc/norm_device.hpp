@@ -46,6 +46,73 @@ __device__ __forceinline__ void stv(uint16_t* p, const float (&v)[VEC]) {
     }
 }
 
+// Eight elements at any alignment of theirs, which the hardware reads and writes in one instruction too; of a row's last ones
+// only the `left` that it has (the others read as 0).
+template <typename V>
+__device__ __forceinline__ V load_any(const void* p) {
+    V v;
+    __builtin_memcpy(&v, p, sizeof(V));
+    return v;
+}
+__device__ __forceinline__ void ld_odd(const float* p, int left, float (&v)[8]) {
+    if (left >= 8) {
+        const f32x4 a = load_any<f32x4>(p), b = load_any<f32x4>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : 0.0f;
+    }
+}
+__device__ __forceinline__ void ld_odd(const uint16_t* p, int left, float (&v)[8]) {
+    if (left >= 8) {
+        const u32x4_t a = load_any<u32x4_t>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_lo(a[i]);
+            v[2 * i + 1] = bf16_hi(a[i]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < left ? bf16_to_f32(p[e]) : 0.0f;
+    }
+}
+__device__ __forceinline__ void st_odd(float* p, int left, const float (&v)[8]) {
+    if (left >= 8) {
+        const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        __builtin_memcpy(static_cast<void*>(p), &a, 16);
+        __builtin_memcpy(static_cast<void*>(p + 4), &b, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) p[e] = v[e];
+    }
+}
+__device__ __forceinline__ void st_odd(uint16_t* p, int left, const float (&v)[8]) {
+    if (left >= 8) {
+        const u32x4_t a = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+        __builtin_memcpy(static_cast<void*>(p), &a, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) p[e] = (uint16_t)f32_to_bf16_bits(v[e]);
+    }
+}
+// a thread's vector, ODD: as above
+template <int VEC, bool ODD, typename T>
+__device__ __forceinline__ void ld_row(const T* p, int left, float (&v)[VEC]) {
+    if constexpr (ODD) ld_odd(p, left, v);
+    else ldv<VEC>(p, v);
+}
+template <int VEC, bool ODD, typename T>
+__device__ __forceinline__ void st_row(T* p, int left, const float (&v)[VEC]) {
+    if constexpr (ODD) st_odd(p, left, v);
+    else stv<VEC>(p, v);
+}
+
 // A vector as it is in memory: loaded a row ahead, widened when its row comes.
 template <typename T, int VEC>
 struct Raw {
@@ -58,6 +125,15 @@ template <>
 struct Raw<uint16_t, 8> {
     u32x4_t v;
     __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
+    __device__ __forceinline__ void load_odd(const uint16_t* p, int left) {
+        if (left >= 8) {
+            v = load_any<u32x4_t>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = (2 * i < left ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < left ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+        }
+    }
     __device__ __forceinline__ void clear() { v = u32x4_t{0, 0, 0, 0}; }
     __device__ __forceinline__ void get(float (&o)[8]) const {
 #pragma unroll
@@ -73,6 +149,18 @@ struct Raw<float, 8> {
     __device__ __forceinline__ void load(const float* p) {
         a = *reinterpret_cast<const f32x4*>(p);
         b = *reinterpret_cast<const f32x4*>(p + 4);
+    }
+    __device__ __forceinline__ void load_odd(const float* p, int left) {
+        if (left >= 8) {
+            a = load_any<f32x4>(p);
+            b = load_any<f32x4>(p + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = i < left ? p[i] : 0.0f;
+                b[i] = 4 + i < left ? p[4 + i] : 0.0f;
+            }
+        }
     }
     __device__ __forceinline__ void clear() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
     __device__ __forceinline__ void get(float (&o)[8]) const {
@@ -118,9 +206,9 @@ struct Shape {
 // mean (0 for rms) and rstd of the row in x; x becomes xhat.  Threads without a
 // row (not live) hold zeros: their rstd is 0, since with eps = 0 it would be
 // infinite and their xhat, which enters the weights' sums, NaN
-template <int TPR, int NV, int VEC>
+template <int TPR, int NV, int VEC, bool ODD = false>
 __device__ __forceinline__ float to_hat(float (&x)[NV][VEC], const bool (&on)[NV], bool live, int W, int rms, float eps,
-                                        float (*red)[2][16], int& turn) {
+                                        float (*red)[2][16], int& turn, int lane = 0) {
     const float inv = 1.0f / (float)W;
     float s = 0.0f, unused = 0.0f;
     if (!rms) {
@@ -133,7 +221,8 @@ __device__ __forceinline__ float to_hat(float (&x)[NV][VEC], const bool (&on)[NV
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) x[j][e] = on[j] ? x[j][e] - mean : 0.0f;
+            for (int e = 0; e < VEC; ++e)
+                x[j][e] = (ODD ? (lane + j * TPR) * VEC + e < W : on[j]) ? x[j][e] - mean : 0.0f;
     }
     s = unused = 0.0f;
 #pragma unroll
@@ -149,9 +238,9 @@ __device__ __forceinline__ float to_hat(float (&x)[NV][VEC], const bool (&on)[NV
     return rstd;
 }
 
-template <int TPR, int NV, int VEC>
+template <int TPR, int NV, int VEC, bool ODD = false>
 __device__ __forceinline__ void load_params(const float* w, const float* b, const bool (&on)[NV], int lane,
-                                            float (&wv)[NV][VEC], float (&bv)[NV][VEC]) {
+                                            float (&wv)[NV][VEC], float (&bv)[NV][VEC], int W = 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -160,13 +249,18 @@ __device__ __forceinline__ void load_params(const float* w, const float* b, cons
             bv[j][e] = 0.0f;
         }
         const int c = (lane + j * TPR) * VEC;
-        if (on[j] && w) {
+        if constexpr (ODD) {
+            if (on[j] && w) ld_odd(w + c, W - c, wv[j]);
+            if (on[j] && b) ld_odd(b + c, W - c, bv[j]);
+        } else {
+            if (on[j] && w) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) wv[j][e] = w[c + e];
-        }
-        if (on[j] && b) {
+                for (int e = 0; e < VEC; ++e) wv[j][e] = w[c + e];
+            }
+            if (on[j] && b) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) bv[j][e] = b[c + e];
+                for (int e = 0; e < VEC; ++e) bv[j][e] = b[c + e];
+            }
         }
     }
 }

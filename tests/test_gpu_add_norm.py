@@ -267,3 +267,38 @@ def test_add_norm_on_a_stream_captured_and_empty(gpu_lib):
     assert out["q"].shape == (0, 48) and out["scale"].shape == (0, 1) and out["sum"].shape == (0, 48)
     back = ssd.ssd_add_norm_bwd(e, e, e, torch.ones(48, device=DEV), bias=torch.ones(48, device=DEV))
     assert (back["weight"] == 0).all() and (back["bias"] == 0).all()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_add_norm_ends_of_rows(gpu_lib, t):
+    """Rows that end at every place of a vector and start at every alignment: nothing past a row's end is read (it is NaN) or
+    written, forward and backward."""
+    ssd, e4 = gpu_lib, torch.float8_e4m3fn
+    for W in list(range(1, 20)) + [63, 65, 127, 129, 255, 257, 1023, 1031, 2079]:
+        for lead, pad in ((0, 1), (1, 2), (3, 4), (8, 8)):
+            d = make(9, W, t, t, t, gate=True)
+            g = up(d)
+
+            def wide(v, fill=float("nan")):
+                out = torch.full((9, lead + W + pad), fill, dtype=v.dtype, device=DEV)
+                out[:, lead:lead + W] = v
+                return out[:, lead:lead + W], out
+
+            def clean(out):
+                edge = out.float()
+                return bool((edge[:, :lead] == 7).all() and (edge[:, lead + W:] == 7).all())
+            ins = {n: wide(g[n])[0] for n in ("x", "residual", "z", "gy", "gs")}
+            outs = {n: wide(torch.zeros(9, W, dtype=T[t], device=DEV), 7.0) for n in ("sum", "y")}
+            outs["q"] = wide(torch.zeros(9, W, device=DEV), 7.0)[1].to(e4)
+            q = outs["q"][:, lead:lead + W]
+            got = ssd.ssd_add_norm_fwd(ins["x"], ins["residual"], g["weight"], bias=g["bias"], z=ins["z"], rms=False, sum=outs["sum"][0],
+                                       y=outs["y"][0], q=q)
+            want = run(ssd, g, t, False, want_q=True)
+            for n in ("sum", "y", "scale"):
+                assert torch.equal(got[n], want[n]), (W, lead, n)
+            assert torch.equal(q.contiguous().view(torch.uint8), want["q"].view(torch.uint8)) and clean(outs["q"])
+            assert clean(outs["sum"][1]) and clean(outs["y"][1])
+            for gs in (None, "gs"):
+                a = ssd.ssd_add_norm_bwd(outs["sum"][0], ins["gy"], gs and ins[gs], g["weight"], bias=g["bias"], z=ins["z"])
+                b = ssd.ssd_add_norm_bwd(want["sum"], g["gy"], gs and g[gs], g["weight"], bias=g["bias"], z=g["z"])
+                assert set(a) == {"sum", "z", "weight", "bias"} and all(torch.equal(a[n], b[n]) for n in a), (W, lead, gs)
