@@ -876,7 +876,8 @@ size_t ssd_glr_scan_bwd_workspace_size(int B, int L, int D, int dtype);
  * 2^-100 and at most the largest fp32, so an infinity saturates; a NaN
  * becomes NaN and does not choose the scale.  Rows, W, alignment and eps as
  * in ssd_norm_fwd; rows whose bases and strides are multiples of 16 bytes (q:
- * 8) and W % 8 == 0 are read and written in pieces.
+ * 8) with W % 8 == 0 are the fastest, others are read and written in vectors
+ * at their elements' alignment.
  */
 int ssd_add_norm_fwd(int64_t R, int W, int x_dtype, int residual_dtype, int dtype, int rms, float eps,
                      const void *x, int64_t x_row_stride,

@@ -12,7 +12,8 @@
 // the alignment of its elements.  128 columns are 16 neighbouring lanes, so their maximum is four lane exchanges.
 //
 // Bound by HBM.  Measured: 32768 rows of 4096, bf16 plus bf16 to e4m3, 182 us (944 MB, 5.2 TB/s, the rate of a large copy);
-// 16 rows of 2048 6 us, a launch and a row's latency.  The backward, 40960 rows of 2048 in bf16 with the stream's gradient:
+// 16 rows of 2048 6 us, a launch and a row's latency.  Odd rows, in vectors and (in brackets) element by element: 16228 rows of
+// 3646 in bf16 to e4m3 117 us (436; 80 at a copy's rate), 20000 of 1001 in fp32 47 (122; 50).  The backward, 40960 rows of 2048 in bf16 with the stream's gradient:
 // 124 us and 5 us of sums (671 MB, 5.2 TB/s).
 #include <hip/hip_runtime.h>
 #include <algorithm>
@@ -81,15 +82,15 @@ __global__ __launch_bounds__((Shape<TPR, NV, 8>::threads)) void ssd_add_norm_ker
             if (live && on[j]) {
                 if (rp) {
                     float f[VEC];
-                    ld_row<VEC, ODD>(rp + r * a.residual_stride + c, a.W - c, f);
-                    if (a.x_dtype == 0) ld_row<VEC, ODD>(static_cast<const float*>(a.x) + r * a.x_stride + c, a.W - c, x[j]);
-                    else ld_row<VEC, ODD>(static_cast<const uint16_t*>(a.x) + r * a.x_stride + c, a.W - c, x[j]);
+                    ld_row<VEC, ODD>(rp + r * a.residual_stride + c, a.W - c, a.W < 8, f);
+                    if (a.x_dtype == 0) ld_row<VEC, ODD>(static_cast<const float*>(a.x) + r * a.x_stride + c, a.W - c, a.W < 8, x[j]);
+                    else ld_row<VEC, ODD>(static_cast<const uint16_t*>(a.x) + r * a.x_stride + c, a.W - c, a.W < 8, x[j]);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) x[j][e] = round_to(rp, x[j][e] + f[e]);
                 } else {
-                    ld_row<VEC, ODD>(static_cast<const S*>(a.x) + r * a.x_stride + c, a.W - c, x[j]);
+                    ld_row<VEC, ODD>(static_cast<const S*>(a.x) + r * a.x_stride + c, a.W - c, a.W < 8, x[j]);
                 }
-                if (zp) ld_row<VEC, ODD>(zp + r * a.z_stride + c, a.W - c, z[j]);
+                if (zp) ld_row<VEC, ODD>(zp + r * a.z_stride + c, a.W - c, a.W < 8, z[j]);
             }
         }
         if (sp) {

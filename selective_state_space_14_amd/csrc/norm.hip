@@ -152,11 +152,11 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             if (live && on[j]) {
                 if constexpr (ODD) {
                     if constexpr (kAddAhead) {
-                        if (sp) ns[j].load_odd(sp + r * sp_stride + c, a.W - c);
+                        if (sp) ns[j].load_odd(sp + r * sp_stride + c, a.W - c, a.W < 8);
                     }
-                    nx[j].load_odd(xp + r * a.x_stride + c, a.W - c);
-                    ng[j].load_odd(gp + r * a.gy_stride + c, a.W - c);
-                    if (zp) nz[j].load_odd(zp + r * a.z_stride + c, a.W - c);
+                    nx[j].load_odd(xp + r * a.x_stride + c, a.W - c, a.W < 8);
+                    ng[j].load_odd(gp + r * a.gy_stride + c, a.W - c, a.W < 8);
+                    if (zp) nz[j].load_odd(zp + r * a.z_stride + c, a.W - c, a.W < 8);
                 } else {
                     if constexpr (kAddAhead) ns[j].load(sp + r * sp_stride + col + c);
                     nx[j].load(xp + r * a.x_stride + col + c);
@@ -168,7 +168,8 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
     };
     const int64_t step = (int64_t)gridDim.x * SH::rows;
     int64_t at = (int64_t)blockIdx.x * SH::rows + sub;
-    constexpr bool kAhead = !kLds;                   // 1024 threads have no registers for it
+    // 1024 threads have no registers for it, nor have 512 with what the ends of rows take
+    constexpr bool kAhead = !kLds && !(ODD && TPR == 512);
     if (kAhead) fetch(at);
     for (; at - sub < a.R; at += step) {
         if (!kAhead) fetch(at);
@@ -183,6 +184,13 @@ __global__ __launch_bounds__((Shape<TPR, NV, VEC>::threads)) void ssd_norm_bwd_k
             nz[j].get(z[j]);
             ng[j].get(g[j]);
             if constexpr (kAddAhead) ns[j].get(past[j]);
+            if constexpr (ODD) {
+                const int k = on[j] && a.W >= 8 ? before(a.W - (lane + j * TPR) * VEC) : 0;
+                shift_out(x[j], k);
+                shift_out(z[j], k);
+                shift_out(g[j], k);
+                if constexpr (kAddAhead) shift_out(past[j], k);
+            }
         }
         if (kAhead) fetch(at + step);
         const float rstd = to_hat<TPR, NV, VEC, ODD>(x, on, live, a.W, a.rms, a.eps, red, turn, lane);

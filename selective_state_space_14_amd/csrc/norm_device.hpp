@@ -46,39 +46,55 @@ __device__ __forceinline__ void stv(uint16_t* p, const float (&v)[VEC]) {
     }
 }
 
-// Eight elements at any alignment of theirs, which the hardware reads and writes in one instruction too; of a row's last ones
-// only the `left` that it has (the others read as 0).
+// Eight elements at any alignment of theirs, which the hardware reads and writes in one instruction too.  Of a row's last ones
+// only `left` are the thread's: the vector that ends with the row is read, and what stands before the thread's own shifted
+// out (so no thread waits for single elements; what a neighbour may be writing there is not used).  Rows of fewer than eight
+// columns (few) are read one by one.  Elements that the row does not have read as 0.
 template <typename V>
 __device__ __forceinline__ V load_any(const void* p) {
     V v;
     __builtin_memcpy(&v, p, sizeof(V));
     return v;
 }
-__device__ __forceinline__ void ld_odd(const float* p, int left, float (&v)[8]) {
-    if (left >= 8) {
-        const f32x4 a = load_any<f32x4>(p), b = load_any<f32x4>(p + 4);
+__device__ __forceinline__ int before(int left) { return left < 8 ? 8 - left : 0; }
+__device__ __forceinline__ void shift_out(float (&v)[8], int k) {
+    if (!k) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    } else {
+    for (int s = 4; s; s >>= 1) {
+        const bool by = k & s;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = by ? (e + s < 8 ? v[e + s < 8 ? e + s : 0] : 0.0f) : v[e];
     }
 }
-__device__ __forceinline__ void ld_odd(const uint16_t* p, int left, float (&v)[8]) {
-    if (left >= 8) {
-        const u32x4_t a = load_any<u32x4_t>(p);
+__device__ __forceinline__ void ld_odd(const float* p, int left, bool few, float (&v)[8]) {
+    if (few) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16_lo(a[i]);
-            v[2 * i + 1] = bf16_hi(a[i]);
-        }
-    } else {
+        for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : 0.0f;
+        return;
+    }
+    const int k = before(left);
+    const f32x4 a = load_any<f32x4>(p - k), b = load_any<f32x4>(p - k + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+    }
+    shift_out(v, k);
+}
+__device__ __forceinline__ void ld_odd(const uint16_t* p, int left, bool few, float (&v)[8]) {
+    if (few) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = e < left ? bf16_to_f32(p[e]) : 0.0f;
+        return;
     }
+    const int k = before(left);
+    const u32x4_t a = load_any<u32x4_t>(p - k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(a[i]);
+        v[2 * i + 1] = bf16_hi(a[i]);
+    }
+    shift_out(v, k);
 }
 __device__ __forceinline__ void st_odd(float* p, int left, const float (&v)[8]) {
     if (left >= 8) {
@@ -103,8 +119,8 @@ __device__ __forceinline__ void st_odd(uint16_t* p, int left, const float (&v)[8
 }
 // a thread's vector, ODD: as above
 template <int VEC, bool ODD, typename T>
-__device__ __forceinline__ void ld_row(const T* p, int left, float (&v)[VEC]) {
-    if constexpr (ODD) ld_odd(p, left, v);
+__device__ __forceinline__ void ld_row(const T* p, int left, bool few, float (&v)[VEC]) {
+    if constexpr (ODD) ld_odd(p, left, few, v);
     else ldv<VEC>(p, v);
 }
 template <int VEC, bool ODD, typename T>
@@ -125,9 +141,9 @@ template <>
 struct Raw<uint16_t, 8> {
     u32x4_t v;
     __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
-    __device__ __forceinline__ void load_odd(const uint16_t* p, int left) {
-        if (left >= 8) {
-            v = load_any<u32x4_t>(p);
+    __device__ __forceinline__ void load_odd(const uint16_t* p, int left, bool few) {
+        if (!few) {
+            v = load_any<u32x4_t>(p - before(left));
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -150,8 +166,9 @@ struct Raw<float, 8> {
         a = *reinterpret_cast<const f32x4*>(p);
         b = *reinterpret_cast<const f32x4*>(p + 4);
     }
-    __device__ __forceinline__ void load_odd(const float* p, int left) {
-        if (left >= 8) {
+    __device__ __forceinline__ void load_odd(const float* p, int left, bool few) {
+        if (!few) {
+            p -= before(left);
             a = load_any<f32x4>(p);
             b = load_any<f32x4>(p + 4);
         } else {
@@ -250,8 +267,8 @@ __device__ __forceinline__ void load_params(const float* w, const float* b, cons
         }
         const int c = (lane + j * TPR) * VEC;
         if constexpr (ODD) {
-            if (on[j] && w) ld_odd(w + c, W - c, wv[j]);
-            if (on[j] && b) ld_odd(b + c, W - c, bv[j]);
+            if (on[j] && w) ld_odd(w + c, W - c, W < 8, wv[j]);
+            if (on[j] && b) ld_odd(b + c, W - c, W < 8, bv[j]);
         } else {
             if (on[j] && w) {
 #pragma unroll
