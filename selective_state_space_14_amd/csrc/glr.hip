@@ -186,7 +186,9 @@ __device__ __forceinline__ uint64_t starts_in(const int32_t* doc, int t0, int n,
     return __ballot(l < n && t > 0 && t < L && doc[max(min(t, L - 1), 0)] != doc[max(min(t, L - 1) - 1, 0)]);
 }
 
-// A of a stretch that a document starts in: nothing passes through
+// A of a stretch that a document starts in: nothing passes through, in either direction, whatever the stretch's decays are.  It is
+// set after their product: a NaN decay behind the start belongs to the state (H is NaN then, too), but would undo the cut for
+// the adjoint, which comes from behind.
 constexpr uint32_t kCut = 0x80000000u;              // -0.0
 __device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) == kCut; }
 __device__ __forceinline__ float through(float A, float H, float h) { return is_cut(A) ? H : fmaf(A, h, H); }
@@ -283,9 +285,10 @@ struct Stretch {
             for (int t = 0; t < Tw; ++t)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    A[j] = bit(m.starts, t) ? __uint_as_float(kCut) : A[j] * a[t][j];
+                    A[j] *= a[t][j];
                     H[j] = bit(m.starts, t) ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
                 }
+            if (m.starts) A[0] = A[1] = __uint_as_float(kCut);
         }
     }
 };
@@ -515,9 +518,10 @@ struct Back {
             for (int t = 0; t < kTb; ++t)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    A[j] = bit(k.starts, t) ? __uint_as_float(kCut) : A[j] * a[t][j];
+                    A[j] *= a[t][j];
                     H[j] = bit(k.starts, t) ? v[t][j] : fmaf(a[t][j], H[j], v[t][j]);
                 }
+            if (k.starts) A[0] = A[1] = __uint_as_float(kCut);
 #pragma unroll
             for (int t = kTb - 1; t >= 0; --t)
 #pragma unroll
