@@ -832,8 +832,9 @@ int ssd_glr_step(int B, int D, int dtype,
  *   grad_init_state  f32 [B][D] or NULL
  *   workspace, workspace_bytes: required, at least
  *               ssd_glr_scan_bwd_workspace_size() bytes, as above
- * Where sqrt(1 - a^2) is 0 (A = 0, or a gate that underflows) its derivative,
- * infinite there, is taken as 0.  Deterministic: dA, dr_bias and di_bias are
+ * Where sqrt(1 - a^2) is 0 (A = 0, or a gate that underflows: 1 - a^2 below
+ * 2^-126, the smallest normal number, counts as 0) its derivative, infinite at
+ * 0, is taken as 0.  Deterministic: dA, dr_bias and di_bias are
  * sums of 64 tokens in fp32, added in a fixed order in 64 bits.  Outputs must
  * not overlap the inputs or each other.  L = 0 writes zero dA, dr_bias and
  * di_bias and copies grad_final_state through; B = 0 writes nothing.

@@ -8,7 +8,7 @@
 //   lam_t = gy_t + a_{t+1} lam_{t+1}
 //   dx = lam m g,  di = lam m x g (1 - g),  dl = lam (a h_{t-1} - g x a^2 / m),  dr = dl A s (1 - s)
 //   dA = sum dl s,  dr_bias = sum dr,  di_bias = sum di
-// (where m is 0 the second part of dl is taken as 0).
+// (where m is 0 the second part of dl is taken as 0; a subnormal 1 - a^2, below 2^-126, counts as 0 for both).
 //
 // A stretch of tokens maps the state h that enters it to A h + H (A the product of its decays, H what it gathers from a
 // zero state), and two stretches after one another compose: A = A1 A2, H = A2 H1 + H2.  A tile is kWaves stretches, one a
@@ -567,7 +567,7 @@ struct Back {
                 const float om = z < kNear ? q : 1.0f - a[t][j], m2 = fmaf(om, a[t][j], om);
                 float inv = __builtin_amdgcn_rsqf(m2);
                 asm volatile("" : "+v"(inv));
-                inv = m2 > 0.0f ? inv : 0.0f;            // 1 / m, 0 where m is
+                inv = m2 >= 0x1p-126f ? inv : 0.0f;      // 1 / m, 0 where m is: the units take a subnormal m2 as 0
                 const float gx = gi[t][j] * x[t].get(j), lm = lam * (m2 * inv);
                 dx[j] = lm * gi[t][j];
                 di[j] = lm * fmaf(-gx, gi[t][j], gx);
