@@ -769,7 +769,7 @@ size_t ssd_norm_bwd_workspace_size(int64_t R, int groups, int W);
  *               an even D are read in pairs)
  *   r_bias, i_bias  f32 [D] or NULL (0)
  *   A       f32 [D], A <= 0 (the caller computes it, for instance
- *               A = -c softplus(lambda)); A > 0 gives NaN
+ *               A = -c softplus(lambda)); A > 0 gives NaN, -inf is a decay of 0
  *   doc_ids i32 [B][L] or NULL: a new document starts from a zero state, its
  *               first input scaled like any other
  *   lengths i32 [B] or NULL: row b is real at t < lengths[b] (read on the

@@ -32,6 +32,7 @@
 //   forward, fp32, 2 x 16384 x 2048: 215 us, 5.0 TB/s
 //   forward and backward, bf16, 4 x 8192 x 2048, packed documents: 124 and 230 us, 367 with the chains' memory and the sums
 #include <algorithm>
+#include <cfloat>
 
 #include "layer_launch.hpp"
 #include "ssd_device.hpp"
@@ -198,6 +199,11 @@ __device__ __forceinline__ void then(float& A, float& H, float A2, float H2) {
     A = is_cut(A2) ? A2 : A * A2;
 }
 
+// -A log2 e and a bias times -log2 e, infinite ones as the largest finite numbers: a decay of 0 and a gate of 0 or 1 all the same,
+// but no 0 * inf or inf - inf where a token that is not real has a gate of -inf.  NaN stays.
+__device__ __forceinline__ float finite(float v) { return v > FLT_MAX ? FLT_MAX : v < -FLT_MAX ? -FLT_MAX : v; }
+__device__ __forceinline__ float rate(float A) { return finite(A * -kLog2e); }
+
 // the wave's number, known to the compiler to be the same for its lanes: rows are then addressed by scalars
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
@@ -208,9 +214,9 @@ struct Params {
     __device__ __forceinline__ void load(const GlrArgs& a, const Lane<PAIR>& ln) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            zA[j] = *column<float>(a.A, ln.c[j]) * -kLog2e;
-            rb[j] = a.r_bias ? -kLog2e * *column<float>(a.r_bias, ln.c[j]) : 0.0f;
-            ib[j] = a.i_bias ? -kLog2e * *column<float>(a.i_bias, ln.c[j]) : 0.0f;
+            zA[j] = rate(*column<float>(a.A, ln.c[j]));
+            rb[j] = a.r_bias ? finite(-kLog2e * *column<float>(a.r_bias, ln.c[j])) : 0.0f;
+            ib[j] = a.i_bias ? finite(-kLog2e * *column<float>(a.i_bias, ln.c[j])) : 0.0f;
         }
     }
     __device__ __forceinline__ float r_gate(float v, int j) const { return fast_rcp(1.0f + fast_exp2(fmaf(v, -kLog2e, rb[j]))); }
@@ -553,7 +559,7 @@ struct Back {
         const Rows<T> xr(static_cast<const T*>(g.dx), g.dx_stride, p.b, p.t0, g.L),
             rr(static_cast<const T*>(g.dr), g.dr_stride, p.b, p.t0, g.L),
             ir(static_cast<const T*>(g.di), g.di_stride, p.b, p.t0, g.L);
-        float A2[2] = {*column<float>(g.A, ln.c[0]), *column<float>(g.A, ln.c[1])};   // not held from above
+        float A2[2] = {finite(*column<float>(g.A, ln.c[0])), finite(*column<float>(g.A, ln.c[1]))};   // not held from above
 #pragma unroll
         for (int t = kTb - 1; t >= 0; --t) {
             float dx[2], dr[2], di[2];
@@ -561,7 +567,7 @@ struct Back {
             for (int j = 0; j < 2; ++j) {
                 const float all = gy[t].get(j) + nu[j], lam = bit(k.lives, t) ? all : 0.0f;
                 nu[j] = bit(k.starts, t) ? 0.0f : a[t][j] * all;
-                const float z = s[t][j] * (A2[j] * -kLog2e);
+                const float z = s[t][j] * rate(A2[j]);
                 float q = one_minus(z);
                 asm volatile("" : "+v"(q));              // no branch around it, nor below
                 const float om = z < kNear ? q : 1.0f - a[t][j], m2 = fmaf(om, a[t][j], om);
@@ -793,7 +799,7 @@ __global__ __launch_bounds__(256) void ssd_glr_step_kernel(GlrArgs g) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         float d, om;
-        decay(sigmoid_f(r[j] + rb[j]) * (A[j] * -kLog2e), d, om);
+        decay(sigmoid_f(r[j] + rb[j]) * rate(A[j]), d, om);
         h[j] = fmaf(d, h[j], __builtin_amdgcn_sqrtf(fmaf(om, d, om)) * sigmoid_f(i[j] + ib[j]) * x[j]);
     }
     step_st<float, V>(state, h);

@@ -1,11 +1,13 @@
-"""GPU: the gated linear recurrence where numbers are not ordinary: NaN gates behind a document's start, and decays so near
-1 that 1 - a^2 is subnormal."""
+"""GPU: the gated linear recurrence where numbers are not ordinary: NaN gates behind a document's start, decays so near 1 that
+1 - a^2 is subnormal, and infinite parameters."""
 import pytest
 import torch
 
 from tests.test_gpu_glr import DEV, bwd, fwd, make, to_dev
 
 pytestmark = pytest.mark.gpu
+
+PARAMS = ("A", "r_bias", "i_bias")
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
@@ -94,3 +96,30 @@ def test_glr_subnormal_one_minus_square(gpu_lib):
     assert whole.sum() >= 2
     lim = (rel * dmag * s).sum((0, 1)) + 2.0 ** -120
     assert ((back["A"] - (dl * s).sum((0, 1))).abs() <= lim)[whole].all()
+
+
+def test_glr_infinite_parameters(gpu_lib):
+    """A of -inf (or so large that A log2 e is) forgets everything at each token, and biases of +-inf hold a gate open or shut:
+    the same as large finite values give, behind a row's length too, where the state stops and gradients are 0."""
+    inf = float("inf")
+    for t, L in (("f32", 150), ("bf16", 150), ("bf16", 1500), ("f32", 900)):
+        d = make(4, L, 14, t, state=True)
+        d["lengths"] = torch.tensor([L, 0, L // 2, 3], dtype=torch.int32)
+        live = torch.arange(L)[None] < d["lengths"][:, None]
+        large = {n: d[n].clone() for n in PARAMS}
+        for c, (n, v, w) in enumerate((("A", -inf, -1e30), ("A", -3e38, -1e30), ("r_bias", inf, 1e4), ("r_bias", -inf, -1e4), ("i_bias", inf, 1e4),
+                                       ("i_bias", -inf, -1e4), ("r_bias", inf, 1e4))):
+            d[n][2 * c], large[n][2 * c] = v, w
+        d["A"][12] = large["A"][12] = -0.5
+        e, f = to_dev(d), to_dev({**d, **large})
+        for got, want in ((fwd(gpu_lib, e), fwd(gpu_lib, f)), (bwd(gpu_lib, e), bwd(gpu_lib, f))):
+            for n in want:
+                assert torch.isfinite(want[n]).all() and (got[n] == want[n]).all(), (t, L, n)
+        back = bwd(gpu_lib, e)
+        assert all((back[n].cpu()[~live] == 0).all() for n in ("x", "r", "i"))
+        assert torch.equal(fwd(gpu_lib, e)["state"][1], e["init_state"][1])
+        rows = [e[n][:, 0].contiguous() for n in ("x", "r", "i")]
+        one, two = e["init_state"].clone(), e["init_state"].clone()
+        kw = lambda p: dict(r_bias=p["r_bias"], i_bias=p["i_bias"])  # noqa: E731
+        assert (gpu_lib.ssd_glr_step(*rows, e["A"], one, **kw(e)) == gpu_lib.ssd_glr_step(*rows, f["A"], two, **kw(f))).all()
+        assert torch.isfinite(one).all() and (one == two).all()
