@@ -939,6 +939,12 @@ int ssd_proj_fp8_fwd(int M, int N, int K, int dtype,
                      const void *w, int64_t w_row_stride, const float *w_scale, int64_t w_scale_row_stride,
                      void *y, int64_t y_row_stride, void *stream);
 
+/* Rows of y that a workgroup of the kernel for these sizes computes (16, 32,
+ * 64, 128 or 256: a kernel each); 0 for sizes of no work and for sizes that
+ * the call does not accept.  Calls of equal N, K and dtype that have the same
+ * answer sum in the same order: a row's bits do not depend on M. */
+int ssd_proj_fp8_tile_rows(int M, int N, int K, int dtype);
+
 #ifdef __cplusplus
 }
 #endif

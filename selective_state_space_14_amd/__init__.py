@@ -46,7 +46,7 @@ __all__ = ["load", "ssd_conv_fwd", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_sta
            "ssd_delta_scan_bwd_workspace_size", "ssd_delta_step", "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_size",
            "ssd_glr_scan_fwd", "ssd_glr_scan_workspace_size", "ssd_glr_step", "ssd_glr_scan_bwd",
            "ssd_glr_scan_bwd_workspace_size", "ssd_add_norm_fwd", "ssd_add_norm_bwd",
-           "ssd_proj_fp8_fwd",
+           "ssd_proj_fp8_fwd", "ssd_proj_fp8_tile_rows",
            "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_ACT_SILU", "SSD_ACT_NONE"]
 
 # SSD_LIBRARY names another build of the same library (the host-sanitized one the ABI checks use)
@@ -153,6 +153,8 @@ def load() -> ctypes.CDLL:
     lib.ssd_add_norm_fwd.argtypes = [I64, I, I, I, I, I, F, P, I64, P, I64, P, P, P, I64, P, I64, P, I64, P, I64, P, I64, P]
     lib.ssd_add_norm_bwd.restype = I
     lib.ssd_add_norm_bwd.argtypes = [I64, I, I, I, I, F, P, I64, P, P, P, I64, P, I64, P, I64, P, I64, P, P, P, I64, P, SZ, P]
+    lib.ssd_proj_fp8_tile_rows.restype = I
+    lib.ssd_proj_fp8_tile_rows.argtypes = [I, I, I, I]
     lib.ssd_proj_fp8_fwd.restype = I
     lib.ssd_proj_fp8_fwd.argtypes = [I, I, I, I, P, I64, P, I64, P, I64, P, I64, P, I64, P]
     _lib = lib
@@ -1051,6 +1053,11 @@ def ssd_add_norm_bwd(sum, grad_y, grad_sum=None, weight=None, *, bias=None, z=No
 
 
 # ---- the 8-bit projection
+def ssd_proj_fp8_tile_rows(M, N, K, dtype=SSD_BF16) -> int:
+    """Rows of y of a workgroup of the kernel for these sizes (16, 32, 64, 128 or 256), 0 where there is none; dtype: y's."""
+    return int(load().ssd_proj_fp8_tile_rows(M, N, K, dtype))
+
+
 @_on_stream
 def ssd_proj_fp8_fwd(a, a_scale, w, w_scale, *, out_dtype=torch.bfloat16, y=None):
     """a times w transposed in float8_e4m3fn with a scale for every block of 128.  a [..., K] with a_scale fp32

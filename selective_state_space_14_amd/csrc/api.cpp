@@ -1654,6 +1654,16 @@ int ssd_add_norm_bwd(int64_t R, int W, int sum_dtype, int dtype, int rms, float 
 }
 
 // ---- the 8-bit projection
+// the grid, whose threads a launch counts in 32 bits: 256 for every 128 x 128 of y
+static bool proj_units_fit(int M, int N) {
+    return ((int64_t)M + 127) / 128 * (((int64_t)N + 127) / 128) <= 0xffffffffLL / 256;
+}
+
+int ssd_proj_fp8_tile_rows(int M, int N, int K, int dtype) {
+    if ((dtype != SSD_F32 && dtype != SSD_BF16) || M <= 0 || N <= 0 || K <= 0 || K % 16 != 0 || !proj_units_fit(M, N)) return 0;
+    return ssd::proj_tile_rows(M, N, K, dtype);
+}
+
 int ssd_proj_fp8_fwd(int M, int N, int K, int dtype,
                      const void* a, int64_t a_row_stride, const float* a_scale, int64_t a_scale_row_stride,
                      const void* w, int64_t w_row_stride, const float* w_scale, int64_t w_scale_row_stride,
@@ -1666,8 +1676,7 @@ int ssd_proj_fp8_fwd(int M, int N, int K, int dtype,
     if (N <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: N=%d must be > 0", fn, N);
     if (K <= 0) return fail(SSD_ERR_BAD_SHAPE, "%s: K=%d must be > 0", fn, K);
     if (K % 16 != 0) return fail(SSD_ERR_UNSUPPORTED, "%s: K=%d is not supported (must be a multiple of 16)", fn, K);
-    // the grid, whose threads a launch counts in 32 bits: 256 for every 128 x 128 of y
-    if (((int64_t)M + 127) / 128 * (((int64_t)N + 127) / 128) > 0xffffffffLL / 256)
+    if (!proj_units_fit(M, N))
         return fail(SSD_ERR_BAD_SHAPE, "%s: M=%d rows of N=%d columns are too many", fn, M, N);
     const int blocks = (K + 127) / 128, es = esize(dtype);
     const bool work = M > 0;

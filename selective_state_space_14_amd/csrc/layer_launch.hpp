@@ -65,6 +65,7 @@ struct ProjArgs {
 hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t stream);
 hipError_t launch_add_norm_bwd(const AddNormBwdArgs& a, hipStream_t stream);
 hipError_t launch_proj(const ProjArgs& a, hipStream_t stream);
+int proj_tile_rows(int M, int N, int K, int dtype);    // rows of y of a workgroup of the kernel for these sizes
 size_t glr_fwd_workspace_bytes(int B, int L, int D, int dtype);
 hipError_t launch_glr_fwd(const GlrArgs& a, void* ws, hipStream_t stream);
 size_t glr_bwd_workspace_bytes(int B, int L, int D, int dtype);

@@ -401,38 +401,47 @@ hipError_t tiles(const ProjArgs& p, hipStream_t s) {
 //         M = 256, N = K = 4096        59  13.3  21.7  48      bf16  M = 4096, N = 5152, K = 2048    -     -    60  64
 //         M = 512, N = K = 4096       115    19    28  49            M = N = K = 4096                -     -    95  66
 //         M = 800, N = K = 4096         -    35    29  50            M = 2000, N = 8192, K = 256     53    29    18  17
-template <typename T>
-hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
-    constexpr bool kWide = sizeof(T) == 4;           // widened operands
+// The answer is the rows of y that a workgroup computes; each number is one kernel.
+enum : int { kRows16 = 16, kRows32 = 32, kTiles64 = 64, kTiles128 = 128, kTiles256 = 256 };
+int choose(int M, int N, int K, bool wide) {         // wide: widened operands
     const auto over = [](double n, int d) { return (double)(((int64_t)n + d - 1) / d); };
     const auto more = [](double n) { return std::max(0.0, n / 256 - 1.0); };      // workgroups a CU after the first
-    const double blocks = over(p.K, 128), n16 = over(p.N, 16), t64 = over(p.N, 64) * over(p.M, 64), t128 = over(p.N, 128) * over(p.M, 128);
-    const double piece = (int64_t)p.N * p.K <= 4 << 20 ? 0.05 : 0.073, most = 0xffffffffu;      // threads that a launch counts
-    double best = 5.0 + blocks * (kWide ? 1.1 + 0.15 * std::min(1.0, t128 / 256) + 0.9 * more(t128)
-                                        : 0.5 + 0.3 * std::min(1.0, t128 / 256) + 0.6 * more(t128));
-    enum { kRows1, kRows2, kTiles64, kTiles128 } kind = kTiles128;
-    const auto consider = [&](auto k, double t, double threads) {
+    const double blocks = over(K, 128), n16 = over(N, 16), t64 = over(N, 64) * over(M, 64), t128 = over(N, 128) * over(M, 128);
+    const double piece = (int64_t)N * K <= 4 << 20 ? 0.05 : 0.073, most = 0xffffffffu;          // threads that a launch counts
+    double best = 5.0 + blocks * (wide ? 1.1 + 0.15 * std::min(1.0, t128 / 256) + 0.9 * more(t128)
+                                       : 0.5 + 0.3 * std::min(1.0, t128 / 256) + 0.6 * more(t128));
+    int kind = kTiles128;
+    const auto consider = [&](int k, double t, double threads) {
         if (t >= best || threads > most) return;
         kind = k;
         best = t;
     };
-    consider(kTiles64, 3.5 + blocks * (kWide ? 0.4 + 0.09 * std::min(1.0, t64 / 256) + 0.5 * more(t64)
-                                            : 0.24 + 0.07 * std::min(1.0, t64 / 256) + 0.3 * more(t64)), t64 * 512);
+    consider(kTiles64, 3.5 + blocks * (wide ? 0.4 + 0.09 * std::min(1.0, t64 / 256) + 0.5 * more(t64)
+                                           : 0.24 + 0.07 * std::min(1.0, t64 / 256) + 0.3 * more(t64)), t64 * 512);
     for (int k : {1, 2}) {
-        const double wgs = n16 * over(p.M, 16 * k);
-        consider(k == 1 ? kRows1 : kRows2, 3.0 + blocks * piece * (1 + k) * (1.0 + more(wgs)), wgs * 64 * kSkinnyWaves);
+        const double wgs = n16 * over(M, 16 * k);
+        consider(k == 1 ? kRows16 : kRows32, 3.0 + blocks * piece * (1 + k) * (1.0 + more(wgs)), wgs * 64 * kSkinnyWaves);
     }
-    if (kind == kRows1) return rows<T, 1, 4>(p, s);
-    if (kind == kRows2) return rows<T, 2, 2>(p, s);
+    // widened operands take too many registers for the largest tile
+    if (kind == kTiles128 && !wide && over(over(N, 256) * over(M, 256), 256) * 1.85 < 0.7 * t128 / 256) return kTiles256;
+    return kind;
+}
+template <typename T>
+hipError_t proj_t(const ProjArgs& p, hipStream_t s) {
+    constexpr bool kWide = sizeof(T) == 4;
+    const int kind = choose(p.M, p.N, p.K, kWide);
+    if (kind == kRows16) return rows<T, 1, 4>(p, s);
+    if (kind == kRows32) return rows<T, 2, 2>(p, s);
     if (kind == kTiles64) return tiles<T, 1, 4, 4, 1, 2>(p, s);
-    if constexpr (!kWide) {                          // widened operands take too many registers for the larger tile
-        if (over(over(p.N, 256) * over(p.M, 256), 256) * 1.85 < 0.7 * t128 / 256) return tiles<T, 8, 4, 2, 4, 1>(p, s);
+    if constexpr (!kWide) {
+        if (kind == kTiles256) return tiles<T, 8, 4, 2, 4, 1>(p, s);
     }
     return tiles<T, 4, 4, 2, 2, 1>(p, s);
 }
 
 }  // namespace
 
+int proj_tile_rows(int M, int N, int K, int dtype) { return choose(M, N, K, dtype == 0); }
 hipError_t launch_proj(const ProjArgs& p, hipStream_t s) { return p.dtype == 0 ? proj_t<float>(p, s) : proj_t<uint16_t>(p, s); }
 
 }  // namespace ssd
