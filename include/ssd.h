@@ -873,7 +873,7 @@ size_t ssd_glr_scan_bwd_workspace_size(int B, int L, int D, int dtype);
  *               with q: y stands for q * q_scale of its block, the last block
  *               of a row the rest of its columns
  * At least one of y and q is given.  q is rounded (to nearest even) from
- * fp32, not from y.  A block of zeros has scale 1; max|y| counts at least
+ * fp32's y * (1 / scale), not from y in T.  A block of zeros has scale 1; max|y| counts at least
  * 2^-100 and at most the largest fp32, so an infinity saturates; a NaN
  * becomes NaN and does not choose the scale.  Rows, W, alignment and eps as
  * in ssd_norm_fwd; rows whose bases and strides are multiples of 16 bytes (q:
@@ -929,7 +929,10 @@ int ssd_add_norm_bwd(int64_t R, int W, int sum_dtype, int dtype, int rms, float 
  * product of two scales has to fit).  For y in f32 a block's products are
  * exact and their sum fp32; for y in bf16 the 8-bit matrix unit cuts each of
  * eight products that it adds at 2^-13 of the largest one's exponent before
- * an fp32 sum, 1.5e-5 of y on normal inputs against the 2^-9 of its rounding.
+ * an fp32 sum: an error of at most 7 * 2^-13 of the largest product of every
+ * eight.  Where the terms are of like size (normal inputs) that is 1.5e-5 of
+ * y, against the 2^-9 of its rounding; where large products cancel, it is
+ * relative to them and not to what they leave: then take y in f32.
  * A NaN reaches its own row (a) or column (w) of y.  Deterministic; the
  * kernel, and with it the order of a sum, is chosen by M, N and K.  M = 0
  * writes nothing.

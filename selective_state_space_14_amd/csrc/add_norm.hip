@@ -12,9 +12,10 @@
 // the alignment of its elements.  128 columns are 16 neighbouring lanes, so their maximum is four lane exchanges.
 //
 // Bound by HBM.  Measured: 32768 rows of 4096, bf16 plus bf16 to e4m3, 182 us (944 MB, 5.2 TB/s, the rate of a large copy);
-// 16 rows of 2048 6 us, a launch and a row's latency.  Odd rows, in vectors and (in brackets) element by element: 16228 rows of
-// 3646 in bf16 to e4m3 117 us (436; 80 at a copy's rate), 20000 of 1001 in fp32 47 (122; 50).  The backward, 40960 rows of 2048 in bf16 with the stream's gradient:
-// 124 us and 5 us of sums (671 MB, 5.2 TB/s).
+// 16 rows of 2048 6 us, a launch and a row's latency.  Odd rows to e4m3: 16228 of 3646 in bf16 113 us (a copy of as much 80), 20000
+// of 1001 in fp32 54 (50); read element by element the first took 436.  The backward, 40960 rows of 2048 in bf16 with the stream's
+// gradient: 124 us and 5 us of sums (671 MB, 5.2 TB/s).  The large ones with inputs that the last-level cache does not hold: 20000 x 1001 over
+// the same 160 MB of inputs takes 47.
 #include <hip/hip_runtime.h>
 #include <algorithm>
 

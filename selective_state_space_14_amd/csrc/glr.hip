@@ -29,8 +29,11 @@
 // Measured (B x L x D):
 //   forward, bf16, 1 x 65536 x 2048: 236 us, 4.6 TB/s (209 us with the arithmetic left out, 220 with operands from the
 //   cache); tiles of 64 tokens in place of 128: 318 us; tiles, their composition and the scan as three launches: 603 us
-//   forward, fp32, 2 x 16384 x 2048: 215 us, 5.0 TB/s
-//   forward and backward, bf16, 4 x 8192 x 2048, packed documents: 124 and 230 us, 367 with the chains' memory and the sums
+//   forward, fp32, 2 x 16384 x 2048 or 4 x 8192 x 2048: 215 us, 5.0 TB/s; with its backward 624 (567 at a copy's rate)
+//   off pairs, 4 x 8192 x 2047, forward and both passes: bf16 152 and 438 us (122 and 357 for 2048 channels), fp32 233 and 686
+//   few channels, bf16, 1 x 65536 x 256: 120 us, with its backward 355 (the chain of groups, whatever the channels; 26 and 71 at
+//   a copy's rate)
+//   forward and backward, bf16, 4 x 8192 x 2048, packed documents: 124 and 230 us, 368 with the chains' memory and the sums
 #include <algorithm>
 #include <cfloat>
 
@@ -759,7 +762,7 @@ __global__ __launch_bounds__(256) void ssd_glr_copy_kernel(const float* from, fl
 
 // ------------------------------------------------------------ one token
 // V channels a thread: 8 where every row, state and parameter starts on a 16-byte boundary and D % 8 == 0, else 1.  Bound by HBM:
-// 8 bytes of state and four activations a channel.  256 x 8192 in bf16: 8.3 us (33.6 MB; 7.8 in a graph, where an
+// 8 bytes of state and four activations a channel.  256 x 8192 in fp32: 10.8 us (50 MB, 9.7 at a copy's rate); in bf16: 8.3 us (33.6 MB; 7.8 in a graph, where an
 // empty step takes 2.4), 15.8 with the parameters read one by one, 8.9 in a graph with four rows a thread.
 template <typename T, int V> __device__ __forceinline__ void step_ld(const T* p, float (&o)[V]) {
     if constexpr (V == 1) {

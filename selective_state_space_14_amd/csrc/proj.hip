@@ -86,8 +86,7 @@ __device__ __forceinline__ void store4(uint16_t* p, int left, bool wide, f32x4 v
 // A workgroup owns 16 columns of y and 16 MT rows; its four waves take every fourth block of K and their sums meet in
 // LDS, in order.  The weights' bytes are the work: nothing is staged, a lane's 32 bytes of a block are two loads, and U
 // blocks are on their way at once.  M = 4, N = 5152, K = 2048 to bf16: 5.7 us (10.6 MB; a copy of as much 2.0 us and a launch
-// 2 to 3).  Eight waves: the same there, M = 777, N = 1000, K = 1040 to fp32 11.6 us in place of 10.4, M = 16, N = 1024, K = 8192 11.4
-// in place of 11.7.
+// 2 to 3).  Eight waves: the same there, M = 16, N = 1024, K = 8192 11.4 in place of 11.7.
 constexpr int kSkinnyWaves = 4;
 template <typename T, int MT, int U>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void ssd_proj_rows_kernel(ProjArgs p) {
@@ -184,13 +183,14 @@ __device__ __forceinline__ int piece_of(int g, int h) { return (g & 1) | h << 1 
 // A workgroup of NWN x NWM waves owns a tile of y; a wave's part of it is WN x WM products of 16 x 16.  The two operands'
 // block of 128 bytes a row goes through one of two LDS stages while the other is computed, and so do the activations'
 // scales of 16 blocks at a time: read by the lanes that need them, they would be as many requests as the operands.
-// M = 16384, N = 4096, K = 8192 to bf16: 471 to 490 us, 2.33 to 2.24 PFLOP/s; a library's 8-bit product without block scales
+// M = 16384, N = 4096, K = 8192 to bf16: 472 to 493 us, 2.33 to 2.23 PFLOP/s (to fp32, tiles of 128 x 128: 943); a library's 8-bit product without block scales
 // takes 412 us there.  Matrix instructions alone would take 300 us at the clock they leave, with their LDS reads and barriers 405;
 // copies and scales add the rest, and the scales' fmas nothing.  A row of products is scaled while the next one's run (one
 // after the other: 666 us).
 // KG groups of waves take every KG-th block each, in stages of their own, and their sums meet in LDS: in a small tile a wave's
 // steps of a block are a chain that nothing else covers (64 x 64 of K = 4096: 14.2 us with one group and four stages, 11.0
-// with two groups of two; 256 x 4096 x 4096 16.0 and 13.3).
+// with two groups of two; 256 x 4096 x 4096 16.0 and 13.3).  Four groups: 9.9 and 12.5, 128 x 8192 x 8192 23.7 in place of 29.4,
+// but 512 x 4096 x 4096, where a CU has two workgroups, 24.4 in place of 19.5.
 template <int BN, int BM, int KG> constexpr int kTileLds = KG * 2 * (BN + BM) * 128 + 2 * BM * 16 * 4;
 template <typename T, int WN, int WM, int NWN, int NWM, int KG>
 __global__ __launch_bounds__(64 * NWN * NWM * KG, 2) void ssd_proj_tiles_kernel(ProjArgs p) {
