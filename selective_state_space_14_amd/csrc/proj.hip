@@ -183,7 +183,7 @@ __device__ __forceinline__ int piece_of(int g, int h) { return (g & 1) | h << 1 
 // A workgroup of NWN x NWM waves owns a tile of y; a wave's part of it is WN x WM products of 16 x 16.  The two operands'
 // block of 128 bytes a row goes through one of two LDS stages while the other is computed, and so do the activations'
 // scales of 16 blocks at a time: read by the lanes that need them, they would be as many requests as the operands.
-// M = 16384, N = 4096, K = 8192 to bf16: 472 to 493 us, 2.33 to 2.23 PFLOP/s (to fp32, tiles of 128 x 128: 943); a library's 8-bit product without block scales
+// M = 16384, N = 4096, K = 8192 to bf16: 472 to 495 us, 2.33 to 2.22 PFLOP/s (to fp32, tiles of 128 x 128: 943); a library's 8-bit product without block scales
 // takes 412 us there.  Matrix instructions alone would take 300 us at the clock they leave, with their LDS reads and barriers 405;
 // copies and scales add the rest, and the scales' fmas nothing.  A row of products is scaled while the next one's run (one
 // after the other: 666 us).
